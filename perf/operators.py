@@ -111,7 +111,7 @@ def prepare(case, seed):
         return s
     V = case["V"]
     # head weights of 1/sqrt(D) scale; normalised hidden states that point, by a part of their
-    # own, at the row's target, so that its probability runs from 1/V to nearly 1
+    # own, at the row's target, so that its probability runs from 1/V to about a third
     W = _randn(g, V, D) * D ** -0.5
     x = _randn(g, N, D)
     kept = torch.rand(N, generator=g, device="cuda") >= case["ignored"]
@@ -128,7 +128,7 @@ def prepare(case, seed):
         index = torch.where(absent | ~kept[:, None], torch.full_like(index, -1), index)
         s["t_index"], s["t_logit"] = index.int(), logit
     Wt = W[target]
-    pull = 14.0 * torch.rand(N, 1, generator=g, device="cuda")
+    pull = math.log(V) * torch.rand(N, 1, generator=g, device="cuda")
     x = x + pull * Wt / (Wt * Wt).sum(1, keepdim=True)
     s["x"], s["W"] = x.to(dt), W.to(dt)
     if case["op"] == "ce":
