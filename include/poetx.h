@@ -69,7 +69,7 @@ poetx_status poetx_get_device_error(cudaStream_t stream);
 /* Where the first expired bounded wait seen by poetx_get_device_error happened: a site id,
  * (source file id) x 10000 + (source line) of the waiting call (file ids: 1 the tensor-core
  * GEMM engine, 2 the CNP products, 3 the index kernels, 4 the self-test, 5 the fused
- * backward block-diagonal product), or 0 if none was
+ * backward block-diagonal product, 6 the linear head's products), or 0 if none was
  * recorded.  Host-only (no synchronisation); for diagnosis. */
 int poetx_timeout_site(void);
 
@@ -460,6 +460,76 @@ poetx_status poetx_layer_bwd_adam(const poetx_layer* L, const void* x, const voi
                                   int accumulate, const poetx_adam* hp, float* m_R, float* v_R,
                                   float* m_P, float* v_P, void* ws, size_t ws_bytes,
                                   cudaStream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Layer norm (the norm in front of a transformer's linears), forward and backward
+ * ------------------------------------------------------------------------------------- */
+
+/* y = (x - mu) rstd gamma + beta per row of x [N, D], mu = mean(x), rstd = 1 / sqrt(mean((x -
+ * mu)^2) + eps), statistics and arithmetic in fp32, y rounded once to dt.
+ *   dt      POETX_BF16 or POETX_F32 (x, y); any N >= 0, D >= 1 (rows of a multiple of 16 bytes take
+ *           the 16-byte loads)
+ *   gamma, beta [D] fp32 (nullable: 1, 0);  mean, rstd [N] fp32 outputs (nullable), the backward's
+ *           inputs;  eps >= 0.  y must not alias x. */
+poetx_status poetx_layernorm_fwd(poetx_dtype dt, const void* x, int N, int D, const float* gamma,
+                                 const float* beta, float eps, void* y, float* mean, float* rstd,
+                                 cudaStream_t stream);
+
+/* Backward from dy [N, D], with x, mean and rstd of the forward: with h = (x - mean) rstd and
+ * u = dy gamma,
+ *   dx = rstd (u - mean(u) - h mean(u h))            [N, D] of dtype dt (must not alias x or dy)
+ *   dgamma = sum over rows of dy h, dbeta = sum of dy   [D] fp32 (nullable; accumulate != 0 adds
+ *            to them), summed in a fixed order
+ *   ws      scratch of poetx_layernorm_bwd_workspace_bytes(dt, N, D) bytes; may be NULL when
+ *           neither dgamma nor dbeta is wanted. */
+size_t poetx_layernorm_bwd_workspace_bytes(poetx_dtype dt, int N, int D);
+poetx_status poetx_layernorm_bwd(poetx_dtype dt, const void* x, const void* dy, int N, int D,
+                                 const float* gamma, const float* mean, const float* rstd, void* dx,
+                                 float* dgamma, float* dbeta, int accumulate, void* ws,
+                                 size_t ws_bytes, cudaStream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * The linear head's loss over a vocabulary of V, from the hidden states x [N, D] and the head's
+ * weight W [V, D], without keeping the logits x W^T; loss alone, or loss and gradients in one call
+ * ------------------------------------------------------------------------------------- */
+
+/* Softmax cross entropy.  With z = x W^T and lse = ln sum_v exp z_v (z in fp32):
+ *   loss[r] = lse - z_t + z_loss lse^2,  t = target[r];  0 where target[r] < 0 (an ignored row)
+ *   dz      = dloss[r] ((1 + 2 z_loss lse) softmax(z) - onehot_t), 0 in ignored rows
+ *   dx = dz W,  dW = dz^T x
+ *   dt      POETX_BF16 or POETX_F32: x, W, dx, dW.  D a multiple of 8, 8 <= D <= 131072,
+ *           1 <= V <= 4194304, N >= 0 (POETX_ERR_SHAPE otherwise).
+ *   target  [N] int32.  A target >= V is the caller's error: that row's loss is NaN, its gradient 0.
+ *   dloss   [N] fp32: the upstream gradient of each row's loss (for a mean over the kept rows,
+ *           1 / their number); required where dx or dW is wanted, else unused
+ *   loss, lse [N] fp32 outputs (lse nullable; written for ignored rows too)
+ *   dx [N, D], dW [V, D] outputs of dtype dt (each nullable; both NULL: the loss alone).
+ *           accumulate != 0 adds dW to its contents (dx is always overwritten).
+ *   ws      scratch of poetx_head_workspace_bytes(dt, N, D, V, 1, dx != NULL, dW != NULL) bytes
+ * bf16: products of bf16 operands summed in fp32; dz is rounded to bf16 for the gradients'
+ * products, dx and dW are rounded once (over all rows).  fp32: about fp32 accuracy throughout.
+ * With gradients, rows are taken in pieces, so that at most about 1 GB of 16-bit exponentials is
+ * held at a time.  Outputs must not alias inputs.  z_loss >= 0. */
+size_t poetx_head_workspace_bytes(poetx_dtype dt, int N, int D, int V, int K, int want_dx,
+                                  int want_dW);
+poetx_status poetx_head_ce(poetx_dtype dt, const void* x, int N, int D, const void* W, int V,
+                           const int32_t* target, float z_loss, const float* dloss, float* loss,
+                           float* lse, void* dx, void* dW, int accumulate, void* ws,
+                           size_t ws_bytes, cudaStream_t stream);
+
+/* Distillation from a teacher's K top logits.  t_index [N, K] int32, t_logit [N, K] fp32: the
+ * vocabulary entries the teacher kept and its logits; an entry with a negative index is absent (its
+ * logit is not read) and a row without entries (or with all of them -inf) is ignored.  With
+ * T = temperature > 0, z = x W^T / T and q = softmax over the row's entries of t_logit / T:
+ *   loss[r] = T^2 sum_k q_k (ln q_k - z_{i_k} + lse),  lse = ln sum over all V of exp z_v
+ *   d(x W^T) = dloss[r] T (softmax(z) - sum_k q_k onehot_{i_k})
+ * An index named twice counts twice.  1 <= K <= 1024; ws of poetx_head_workspace_bytes(dt, N, D, V,
+ * K, ...) bytes; everything else as for poetx_head_ce (an index >= V: loss NaN, gradient 0). */
+poetx_status poetx_head_distill(poetx_dtype dt, const void* x, int N, int D, const void* W, int V,
+                                const int32_t* t_index, const float* t_logit, int K,
+                                float temperature, const float* dloss, float* loss, float* lse,
+                                void* dx, void* dW, int accumulate, void* ws, size_t ws_bytes,
+                                cudaStream_t stream);
 
 #ifdef __cplusplus
 }

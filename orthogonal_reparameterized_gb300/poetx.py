@@ -100,6 +100,15 @@ _SIGS = {
     "poetx_group_step_host": (_i, [ctypes.POINTER(LayerDesc), _i] +
                               [ctypes.POINTER(ctypes.c_void_p)] * 2 + [_i] +
                               [ctypes.POINTER(ctypes.c_void_p)] * 4 + [_vp, _sz, _vp]),
+    "poetx_layernorm_fwd": (_i, [_i, _vp, _i, _i, _vp, _vp, _f, _vp, _vp, _vp, _vp]),
+    "poetx_layernorm_bwd_workspace_bytes": (_sz, [_i, _i, _i]),
+    "poetx_layernorm_bwd": (_i, [_i, _vp, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _i, _vp, _sz,
+                                 _vp]),
+    "poetx_head_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "poetx_head_ce": (_i, [_i, _vp, _i, _i, _vp, _i, _vp, _f, _vp, _vp, _vp, _vp, _vp, _i, _vp,
+                           _sz, _vp]),
+    "poetx_head_distill": (_i, [_i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _f, _vp, _vp, _vp, _vp,
+                                _vp, _i, _vp, _sz, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -471,3 +480,104 @@ def poetx_group_step_host(G, xs, dys, ys, dxs, dq_R, dq_P, dev, stream=None):
     _check("poetx_group_step_host", lib().poetx_group_step_host(
         G, k, arr(xs), arr(dys), N, arr(ys), arr(dxs), arr(dq_R), arr(dq_P), _p(dev),
         dev.numel() * dev.element_size(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- layer norm
+def _want(fn: str, what: str, t, shape, dtype):
+    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+        raise ValueError(f"{fn}: {what} must be {tuple(shape)} of {dtype}, "
+                         f"got {tuple(t.shape)} of {t.dtype}")
+
+
+def _scratch(nbytes: int, device, stream):
+    """Scratch for one call, from the allocator pool of the stream that will use it."""
+    if stream is None:
+        return workspace(nbytes, device)
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, device)
+
+
+def poetx_layernorm_fwd(x, y, gamma=None, beta=None, mean=None, rstd=None, eps=1e-5, stream=None):
+    """y = layer norm of the rows of x [N, D] (bf16 or fp32); gamma, beta [D] fp32; mean, rstd [N]
+    fp32 outputs, kept for the backward."""
+    fn, f32 = "poetx_layernorm_fwd", torch.float32
+    N, D = x.shape
+    _want(fn, "y", y, (N, D), x.dtype)
+    _want(fn, "gamma", gamma, (D,), f32)
+    _want(fn, "beta", beta, (D,), f32)
+    _want(fn, "mean", mean, (N,), f32)
+    _want(fn, "rstd", rstd, (N,), f32)
+    _check(fn, lib().poetx_layernorm_fwd(dtype_code(x), _p(x), N, D, _p(gamma), _p(beta), eps,
+                                         _p(y), _p(mean), _p(rstd), _stream(stream)))
+
+
+def poetx_layernorm_bwd_workspace_bytes(dt: int, N: int, D: int) -> int:
+    return lib().poetx_layernorm_bwd_workspace_bytes(dt, N, D)
+
+
+def poetx_layernorm_bwd(x, dy, mean, rstd, dx, gamma=None, dgamma=None, dbeta=None,
+                        accumulate=False, ws=None, stream=None):
+    """dx [N, D] and (where given) dgamma, dbeta [D] fp32 from dy and the forward's x, mean and
+    rstd."""
+    fn, f32 = "poetx_layernorm_bwd", torch.float32
+    N, D = x.shape
+    _want(fn, "dy", dy, (N, D), x.dtype)
+    _want(fn, "dx", dx, (N, D), x.dtype)
+    for what, t in (("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta)):
+        _want(fn, what, t, (D,), f32)
+    for what, t in (("mean", mean), ("rstd", rstd)):
+        _want(fn, what, t, (N,), f32)
+    dt = dtype_code(x)
+    if ws is None:
+        ws = _scratch(poetx_layernorm_bwd_workspace_bytes(dt, N, D), x.device, stream)
+    _check(fn, lib().poetx_layernorm_bwd(dt, _p(x), _p(dy), N, D, _p(gamma), _p(mean), _p(rstd),
+                                         _p(dx), _p(dgamma), _p(dbeta), int(bool(accumulate)),
+                                         _p(ws), ws.numel(), _stream(stream)))
+
+
+# ---------------------------------------------------------------- the linear head's loss
+def poetx_head_workspace_bytes(dt: int, N: int, D: int, V: int, K: int = 1, want_dx: bool = True,
+                               want_dW: bool = True) -> int:
+    return lib().poetx_head_workspace_bytes(dt, N, D, V, K, int(want_dx), int(want_dW))
+
+
+def _head_args(fn, x, W, K, loss, dloss, dx, dW, lse, ws, stream):
+    f32 = torch.float32
+    (N, D), V = x.shape, W.shape[0]
+    _want(fn, "W", W, (V, D), x.dtype)
+    _want(fn, "dx", dx, (N, D), x.dtype)
+    _want(fn, "dW", dW, (V, D), x.dtype)
+    for what, t in (("loss", loss), ("lse", lse), ("dloss", dloss)):
+        _want(fn, what, t, (N,), f32)
+    dt = dtype_code(x)
+    if ws is None:
+        ws = _scratch(poetx_head_workspace_bytes(dt, N, D, V, K, dx is not None, dW is not None),
+                      x.device, stream)
+    return dt, N, D, V, ws
+
+
+def poetx_head_ce(x, W, target, loss, dloss=None, dx=None, dW=None, lse=None, z_loss=0.0,
+                  accumulate=False, ws=None, stream=None):
+    """loss [N] fp32 of the softmax cross entropy of x W^T against target [N] int32 (negative:
+    ignored), and with dloss [N] fp32 (the upstream gradients) dx and / or dW."""
+    fn = "poetx_head_ce"
+    _want(fn, "target", target, (x.shape[0],), torch.int32)
+    dt, N, D, V, ws = _head_args(fn, x, W, 1, loss, dloss, dx, dW, lse, ws, stream)
+    _check(fn, lib().poetx_head_ce(dt, _p(x), N, D, _p(W), V, _p(target), z_loss, _p(dloss),
+                                   _p(loss), _p(lse), _p(dx), _p(dW), int(bool(accumulate)),
+                                   _p(ws), ws.numel(), _stream(stream)))
+
+
+def poetx_head_distill(x, W, t_index, t_logit, loss, dloss=None, dx=None, dW=None, lse=None,
+                       temperature=1.0, accumulate=False, ws=None, stream=None):
+    """loss [N] fp32 of T^2 KL(teacher || student) from the teacher's top logits t_logit [N, K]
+    fp32 at the entries t_index [N, K] int32 (negative: absent), and with dloss the gradients."""
+    fn = "poetx_head_distill"
+    N, K = t_index.shape
+    _want(fn, "t_index", t_index, (x.shape[0], K), torch.int32)
+    _want(fn, "t_logit", t_logit, (N, K), torch.float32)
+    dt, N, D, V, ws = _head_args(fn, x, W, K, loss, dloss, dx, dW, lse, ws, stream)
+    _check(fn, lib().poetx_head_distill(dt, _p(x), N, D, _p(W), V, _p(t_index), _p(t_logit), K,
+                                        temperature, _p(dloss), _p(loss), _p(lse), _p(dx), _p(dW),
+                                        int(bool(accumulate)), _p(ws), ws.numel(),
+                                        _stream(stream)))

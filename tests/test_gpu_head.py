@@ -1,0 +1,256 @@
+"""The linear head's cross entropy and distillation against the fp64 definition.
+
+Tolerances, relative Frobenius error.  loss and lse (fp32): logits of bf16 operands are exact
+products summed in fp32 (the tensor core's adds are handed over every 512 of K: about 32 x 2^-24 of
+a partial sum), so TOL_F32.  bf16 dx and dW: dz is rounded to bf16 for its products and the result
+once more, two roundings of at most 2^-9 (RMS 1.1e-3 each), TOL_BF16_STEP.  fp32 heads: TOL_F32
+throughout."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from gpu_util import DEV, P, TOL_BF16_STEP, TOL_F32, dev, host  # noqa: F401
+from oracle import head_oracle as H
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+
+
+def _inputs(N, V, D, dt, seed):
+    r = np.random.default_rng(seed)
+    W = r.standard_normal((V, D)) / np.sqrt(D)
+    t = r.integers(0, V, N)
+    x = r.standard_normal((N, D)) + r.uniform(0, 12, (N, 1)) * W[t] / (W[t] ** 2).sum(1)[:, None]
+    x, W = torch.tensor(x).to(DT[dt]), torch.tensor(W).to(DT[dt])
+    dloss = (r.uniform(0.5, 1.5, N) / N).astype(np.float32)
+    return x, W, t.astype(np.int32), dloss
+
+
+def _ce(P, x, W, t, dloss, z_loss=0.0, dx=True, dW=True, acc=None, **kw):
+    xd, Wd = x.to(DEV), W.to(DEV)
+    N = x.shape[0]
+    o = {k: torch.full((N,), float("nan"), device=DEV) for k in ("loss", "lse")}
+    if dx:
+        o["dx"] = torch.full_like(xd, float("nan"))
+    if dW:
+        o["dW"] = torch.full_like(Wd, float("nan") if acc is None else acc)
+    P.poetx_head_ce(xd, Wd, dev(t, torch.int32), o["loss"], lse=o["lse"], z_loss=z_loss,
+                    dloss=dev(dloss, torch.float32) if dx or dW else None, dx=o.get("dx"),
+                    dW=o.get("dW"), accumulate=acc is not None, **kw)
+    torch.cuda.synchronize()
+    assert P.poetx_get_device_error() == 0
+    return o
+
+
+def _distill(P, x, W, idx, u, dloss, T=1.0, grads=True):
+    xd, Wd = x.to(DEV), W.to(DEV)
+    N = x.shape[0]
+    o = {k: torch.full((N,), float("nan"), device=DEV) for k in ("loss", "lse")}
+    if grads:
+        o["dx"], o["dW"] = torch.full_like(xd, float("nan")), torch.full_like(Wd, float("nan"))
+    P.poetx_head_distill(xd, Wd, dev(idx, torch.int32), dev(u, torch.float32), o["loss"],
+                         lse=o["lse"], dloss=dev(dloss, torch.float32) if grads else None,
+                         dx=o.get("dx"), dW=o.get("dW"), temperature=T)
+    torch.cuda.synchronize()
+    assert P.poetx_get_device_error() == 0
+    return o
+
+
+def _near(got, ref, dt):
+    for k in got:
+        tol = TOL_BF16_STEP if dt == "bf16" and k in ("dx", "dW") else TOL_F32
+        assert O.rel_fro(host(got[k]), ref[k]) <= tol, k
+
+
+# one row, one class, less than a tile, tile and group edges, odd vocabularies, K tails
+SHAPES = [(1, 1, 8), (1, 2, 64), (3, 33, 72), (5, 127, 8), (127, 129, 128), (128, 256, 64),
+          (129, 257, 200), (256, 128, 520), (300, 1000, 1024), (257, 5003, 136), (700, 3001, 264)]
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,D", SHAPES)
+def test_ce(P, N, V, D, dt):
+    x, W, t, g = _inputs(N, V, D, dt, N + V + D)
+    got = _ce(P, x, W, t, g)
+    ref = H.head_ce(host(x), host(W), t, g)
+    if V == 1:  # p = 1: nothing to learn
+        assert np.abs(host(got["loss"])).max() <= 1e-5 * np.abs(ref["lse"]).max()
+        assert np.abs(host(got["dx"])).max() <= 1e-5 * np.abs(g).max() * np.abs(host(W)).max()
+        return
+    _near(got, ref, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("z_loss", [0.0, 0.02])
+def test_ce_ignored_rows(P, dt, z_loss):
+    x, W, t, g = _inputs(301, 777, 96, dt, 5)
+    t[::3] = -100
+    t[1] = -1
+    got = _ce(P, x, W, t, g, z_loss)
+    _near(got, H.head_ce(host(x), host(W), t, g, z_loss), dt)
+    assert not host(got["loss"])[t < 0].any() and not host(got["dx"])[t < 0].any()
+    t[:] = -100  # nothing left
+    got = _ce(P, x, W, t, g, z_loss)
+    assert not host(got["loss"]).any() and not host(got["dx"]).any() and not host(got["dW"]).any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ce_parts_agree(P, dt):
+    """Loss alone, dx alone, dW alone and all at once give the same bits, every time."""
+    x, W, t, g = _inputs(290, 1100, 192, dt, 6)
+    full = _ce(P, x, W, t, g)
+    for dx, dW in ((True, True), (True, False), (False, True), (False, False)):
+        got = _ce(P, x, W, t, g, dx=dx, dW=dW)
+        for k in got:
+            assert torch.equal(got[k], full[k]), (k, dx, dW)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ce_accumulates_dW(P, dt):
+    x, W, t, g = _inputs(150, 500, 128, dt, 7)
+    ref = H.head_ce(host(x), host(W), t, g)
+    got = _ce(P, x, W, t, g, acc=0.25)
+    assert O.rel_fro(host(got["dW"]), ref["dW"] + 0.25) <= \
+        (TOL_BF16_STEP if dt == "bf16" else TOL_F32)
+
+
+def test_ce_far_logits(P):
+    """Logits in the hundreds: probabilities of exactly 0 and 1 in fp32, no overflow."""
+    x, W, t, g = _inputs(64, 600, 64, "bf16", 8)
+    x = x * 40
+    t[::2] = (t[::2] + 1) % 600
+    _near(_ce(P, x, W, t, g), H.head_ce(host(x), host(W), t, g), "bf16")
+
+
+def test_ce_infinite_weights(P):
+    """A vocabulary entry whose logit is -inf gets probability 0 (also where a whole group of 128
+    has it); a NaN stays in its row."""
+    x, W, t, g = _inputs(40, 700, 64, "bf16", 9)
+    x = x.abs() + 0.1
+    W[128:256] = float("-inf")
+    W[300] = float("-inf")
+    t[(t >= 128) & (t < 256) | (t == 300)] = 5
+    got = _ce(P, x, W, t, g, dx=False, dW=False)
+    keep = np.ones(700, bool)
+    keep[128:256] = keep[300] = False
+    place = np.cumsum(keep) - 1
+    ref = H.head_ce(host(x), host(W)[keep], place[t])
+    _near(got, ref, "bf16")
+    x, W, t, g = _inputs(40, 700, 64, "bf16", 10)
+    x[7, 3] = float("nan")
+    got = _ce(P, x, W, t, g, dW=False)
+    bad = torch.isnan(got["loss"])
+    assert bad[7] and bad.sum() == 1
+    assert torch.isfinite(got["dx"][[r for r in range(40) if r != 7]]).all()
+
+
+def test_ce_target_beyond_the_vocabulary(P):
+    x, W, t, g = _inputs(20, 90, 64, "bf16", 11)
+    t[4] = 90
+    got = _ce(P, x, W, t, g)
+    t[4] = -1
+    ref = _ce(P, x, W, t, g)
+    assert torch.isnan(got["loss"][4]) and not got["dx"][4].any()
+    assert torch.equal(got["dW"], ref["dW"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("N,V,D,K,T", [(1, 40, 64, 1, 1.0), (5, 300, 72, 300, 2.0),
+                                       (130, 1001, 128, 7, 4.0), (257, 3001, 200, 64, 2.0),
+                                       (33, 5000, 64, 1024, 1.0)])
+def test_distill(P, N, V, D, K, T, dt):
+    x, W, t, g = _inputs(N, V, D, dt, N + V + K)
+    r = np.random.default_rng(K)
+    idx = np.stack([r.permutation(V)[:K] for _ in range(N)]).astype(np.int32)
+    idx[:, 0] = t if K == 1 else idx[:, 0]
+    u = r.uniform(0, 10, (N, K)).astype(np.float32)
+    _near(_distill(P, x, W, idx, u, g, T), H.head_distill(host(x), host(W), idx, u, g, T), dt)
+    a = _distill(P, x, W, idx, u, g, T, grads=False)
+    b = _distill(P, x, W, idx, u, g, T)
+    assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["lse"], b["lse"])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_distill_absent_repeated_and_empty(P, dt):
+    x, W, _, g = _inputs(60, 400, 64, dt, 12)
+    r = np.random.default_rng(1)
+    idx = np.stack([r.permutation(400)[:9] for _ in range(60)]).astype(np.int32)
+    u = r.uniform(-3, 6, (60, 9)).astype(np.float32)
+    idx[3] = -1                       # an empty row
+    u[4] = -np.inf                    # one whose every weight is zero
+    idx[5, 2:] = -7
+    u[5, 2:] = np.nan                 # absent entries are not read
+    u[6, 0] = -np.inf
+    u[7, 1:] = np.finfo(np.float32).min
+    idx[8, :] = 17                    # one entry, nine times
+    idx[9, 4] = idx[9, 0]
+    got = _distill(P, x, W, idx, u, g, 2.0)
+    ref = H.head_distill(host(x), host(W), idx, u, g, 2.0)
+    _near(got, ref, dt)
+    for row in (3, 4):
+        assert host(got["loss"])[row] == 0 and not host(got["dx"])[row].any()
+
+
+def test_distill_of_one_entry_is_cross_entropy(P):
+    x, W, t, g = _inputs(140, 900, 128, "bf16", 13)
+    a = _ce(P, x, W, t, g)
+    b = _distill(P, x, W, t[:, None], np.zeros((140, 1), np.float32), g)
+    for k in a:
+        assert O.rel_fro(host(b[k]), host(a[k])) <= TOL_F32, k
+
+
+def _torch64(x, W, t, g):
+    x, W, g = x.double(), W.double(), g.double()
+    z = x @ W.T
+    lse = torch.logsumexp(z, 1)
+    rows = torch.arange(len(t), device=DEV)
+    loss = lse - z[rows, t.long()]
+    dz = torch.exp(z - lse[:, None])
+    dz[rows, t.long()] -= 1
+    dz *= g[:, None]
+    return {"loss": loss, "lse": lse, "dx": dz @ W, "dW": dz.T @ x}
+
+
+@pytest.mark.parametrize("acc", [None, 0.001])
+def test_ce_in_pieces_of_rows(P, acc):
+    """More rows than one piece holds (about 1 GB of 16-bit values): dW is the sum over the pieces,
+    rounded once."""
+    r = torch.Generator(device=DEV).manual_seed(3)
+    N, V, D = 4500, 128001, 64
+    W = (torch.randn(V, D, generator=r, device=DEV) / 8).bfloat16()
+    x = torch.randn(N, D, generator=r, device=DEV).bfloat16()
+    t = torch.randint(0, V, (N,), generator=r, device=DEV).int()
+    g = torch.full((N,), 1.0 / N, device=DEV)
+    assert P.poetx_head_workspace_bytes(P.BF16, N, D, V) > V * D * 4
+    got = _ce(P, x, W, t.cpu().numpy(), g.cpu().numpy(), acc=acc)
+    ref = _torch64(x, W, t, g)
+    if acc:
+        # the sum is of the size of acc here: its rounding is the error
+        ref["dW"] = ref["dW"] + float(torch.tensor(acc).bfloat16())
+    for k in ref:
+        tol = TOL_BF16_STEP if k in ("dx", "dW") else TOL_F32
+        err = ((got[k].double() - ref[k]).norm() / ref[k].norm()).item()
+        assert err <= tol, (k, err)
+
+
+def test_head_on_another_stream(P):
+    x, W, t, g = _inputs(300, 2000, 256, "bf16", 14)
+    ref = _ce(P, x, W, t, g)
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = _ce(P, x, W, t, g, stream=s)
+    s.synchronize()
+    for k in ref:
+        assert torch.equal(got[k], ref[k]), k
+
+
+def test_head_empty_batch(P):
+    W = torch.randn(50, 64, device=DEV).bfloat16()
+    x, e = W[:0], torch.empty(0, device=DEV)
+    dW = torch.ones_like(W)
+    P.poetx_head_ce(x, W, e.int(), e, dloss=e, dx=torch.empty_like(x), dW=dW, accumulate=True)
+    assert (dW == 1).all()
+    P.poetx_head_ce(x, W, e.int(), e, dloss=e, dx=torch.empty_like(x), dW=dW)
+    assert not dW.any()
