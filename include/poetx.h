@@ -69,7 +69,8 @@ poetx_status poetx_get_device_error(cudaStream_t stream);
 /* Where the first expired bounded wait seen by poetx_get_device_error happened: a site id,
  * (source file id) x 10000 + (source line) of the waiting call (file ids: 1 the tensor-core
  * GEMM engine, 2 the CNP products, 3 the index kernels, 4 the self-test, 5 the fused
- * backward block-diagonal product, 6 the linear head's products), or 0 if none was
+ * backward block-diagonal product, 6 the linear head's products,
+ * 7 the layer norm's backward), or 0 if none was
  * recorded.  Host-only (no synchronisation); for diagnosis. */
 int poetx_timeout_site(void);
 

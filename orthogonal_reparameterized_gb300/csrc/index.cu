@@ -254,15 +254,6 @@ struct VecT<2> { using T = uint16_t; };
 template <>
 struct VecT<4> { using T = uint32_t; };
 
-__device__ __forceinline__ void bulk_load(void* smem_dst, const void* src, uint32_t bytes,
-                                          uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-          smem_u32(smem_dst)),
-      "l"(src), "r"(bytes), "r"(smem_u32(bar))
-      : "memory");
-}
-
 // V consecutive gather indices, read from shared memory with one aligned vector load per
 // 16 bytes (8-byte loads when the V indices take 8 bytes).
 template <typename IdxT, int V>

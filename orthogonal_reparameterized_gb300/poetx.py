@@ -484,17 +484,35 @@ def poetx_group_step_host(G, xs, dys, ys, dxs, dq_R, dq_P, dev, stream=None):
 
 # ---------------------------------------------------------------- layer norm
 def _want(fn: str, what: str, t, shape, dtype):
-    if t is not None and (tuple(t.shape) != tuple(shape) or t.dtype != dtype):
+    if t is not None and (t.shape != shape or t.dtype is not dtype):
         raise ValueError(f"{fn}: {what} must be {tuple(shape)} of {dtype}, "
                          f"got {tuple(t.shape)} of {t.dtype}")
+
+
+def _addr(t):
+    """A tensor's device address as an integer (None: None)."""
+    if t is None:
+        return None
+    if not t.is_cuda:
+        raise ValueError("poetx: tensors must live on a CUDA device")
+    if not t.is_contiguous():
+        raise ValueError("poetx: tensors must be contiguous")
+    return t.data_ptr()
+
+
+def _raw_stream(stream, t):
+    """The stream's handle (None: the current one of t's device, without building its object)."""
+    if stream is None:
+        return torch._C._cuda_getCurrentRawStream(t.get_device())
+    return stream.cuda_stream
 
 
 def _scratch(nbytes: int, device, stream):
     """Scratch for one call, from the allocator pool of the stream that will use it."""
     if stream is None:
-        return workspace(nbytes, device)
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
     with torch.cuda.stream(stream):
-        return workspace(nbytes, device)
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
 
 
 def poetx_layernorm_fwd(x, y, gamma=None, beta=None, mean=None, rstd=None, eps=1e-5, stream=None):
@@ -502,13 +520,15 @@ def poetx_layernorm_fwd(x, y, gamma=None, beta=None, mean=None, rstd=None, eps=1
     fp32 outputs, kept for the backward."""
     fn, f32 = "poetx_layernorm_fwd", torch.float32
     N, D = x.shape
-    _want(fn, "y", y, (N, D), x.dtype)
+    _want(fn, "y", y, x.shape, x.dtype)
     _want(fn, "gamma", gamma, (D,), f32)
     _want(fn, "beta", beta, (D,), f32)
     _want(fn, "mean", mean, (N,), f32)
     _want(fn, "rstd", rstd, (N,), f32)
-    _check(fn, lib().poetx_layernorm_fwd(dtype_code(x), _p(x), N, D, _p(gamma), _p(beta), eps,
-                                         _p(y), _p(mean), _p(rstd), _stream(stream)))
+    st = lib().poetx_layernorm_fwd(_DT[x.dtype], _addr(x), N, D, _addr(gamma), _addr(beta), eps,
+                                   _addr(y), _addr(mean), _addr(rstd), _raw_stream(stream, x))
+    if st:
+        _check(fn, st)
 
 
 def poetx_layernorm_bwd_workspace_bytes(dt: int, N: int, D: int) -> int:
@@ -521,18 +541,21 @@ def poetx_layernorm_bwd(x, dy, mean, rstd, dx, gamma=None, dgamma=None, dbeta=No
     rstd."""
     fn, f32 = "poetx_layernorm_bwd", torch.float32
     N, D = x.shape
-    _want(fn, "dy", dy, (N, D), x.dtype)
-    _want(fn, "dx", dx, (N, D), x.dtype)
-    for what, t in (("gamma", gamma), ("dgamma", dgamma), ("dbeta", dbeta)):
-        _want(fn, what, t, (D,), f32)
-    for what, t in (("mean", mean), ("rstd", rstd)):
-        _want(fn, what, t, (N,), f32)
-    dt = dtype_code(x)
+    _want(fn, "dy", dy, x.shape, x.dtype)
+    _want(fn, "dx", dx, x.shape, x.dtype)
+    _want(fn, "gamma", gamma, (D,), f32)
+    _want(fn, "dgamma", dgamma, (D,), f32)
+    _want(fn, "dbeta", dbeta, (D,), f32)
+    _want(fn, "mean", mean, (N,), f32)
+    _want(fn, "rstd", rstd, (N,), f32)
+    dt, L, px = _DT[x.dtype], lib(), _addr(x)
     if ws is None:
-        ws = _scratch(poetx_layernorm_bwd_workspace_bytes(dt, N, D), x.device, stream)
-    _check(fn, lib().poetx_layernorm_bwd(dt, _p(x), _p(dy), N, D, _p(gamma), _p(mean), _p(rstd),
-                                         _p(dx), _p(dgamma), _p(dbeta), int(bool(accumulate)),
-                                         _p(ws), ws.numel(), _stream(stream)))
+        ws = _scratch(L.poetx_layernorm_bwd_workspace_bytes(dt, N, D), x.device, stream)
+    st = L.poetx_layernorm_bwd(dt, px, _addr(dy), N, D, _addr(gamma), _addr(mean), _addr(rstd),
+                               _addr(dx), _addr(dgamma), _addr(dbeta), 1 if accumulate else 0,
+                               _addr(ws), ws.numel(), _raw_stream(stream, x))
+    if st:
+        _check(fn, st)
 
 
 # ---------------------------------------------------------------- the linear head's loss
@@ -541,19 +564,27 @@ def poetx_head_workspace_bytes(dt: int, N: int, D: int, V: int, K: int = 1, want
     return lib().poetx_head_workspace_bytes(dt, N, D, V, K, int(want_dx), int(want_dW))
 
 
-def _head_args(fn, x, W, K, loss, dloss, dx, dW, lse, ws, stream):
+def _head(fn, call, x, W, K, target, logit, loss, dloss, dx, dW, lse, ws, stream, option, accumulate):
+    """Checks and marshals what both head losses share (logit: None for labels; option: the call's
+    own argument before dloss)."""
     f32 = torch.float32
     (N, D), V = x.shape, W.shape[0]
     _want(fn, "W", W, (V, D), x.dtype)
-    _want(fn, "dx", dx, (N, D), x.dtype)
+    _want(fn, "dx", dx, x.shape, x.dtype)
     _want(fn, "dW", dW, (V, D), x.dtype)
-    for what, t in (("loss", loss), ("lse", lse), ("dloss", dloss)):
-        _want(fn, what, t, (N,), f32)
-    dt = dtype_code(x)
+    _want(fn, "loss", loss, (N,), f32)
+    _want(fn, "lse", lse, (N,), f32)
+    _want(fn, "dloss", dloss, (N,), f32)
+    dt, px = _DT[x.dtype], _addr(x)
+    targets = (_addr(target),) if logit is None else (_addr(target), _addr(logit), K)
     if ws is None:
-        ws = _scratch(poetx_head_workspace_bytes(dt, N, D, V, K, dx is not None, dW is not None),
-                      x.device, stream)
-    return dt, N, D, V, ws
+        ws = _scratch(lib().poetx_head_workspace_bytes(dt, N, D, V, K, dx is not None,
+                                                       dW is not None), x.device, stream)
+    st = call(dt, px, N, D, _addr(W), V, *targets, option, _addr(dloss), _addr(loss), _addr(lse),
+              _addr(dx), _addr(dW), 1 if accumulate else 0, _addr(ws), ws.numel(),
+              _raw_stream(stream, x))
+    if st:
+        _check(fn, st)
 
 
 def poetx_head_ce(x, W, target, loss, dloss=None, dx=None, dW=None, lse=None, z_loss=0.0,
@@ -562,10 +593,8 @@ def poetx_head_ce(x, W, target, loss, dloss=None, dx=None, dW=None, lse=None, z_
     ignored), and with dloss [N] fp32 (the upstream gradients) dx and / or dW."""
     fn = "poetx_head_ce"
     _want(fn, "target", target, (x.shape[0],), torch.int32)
-    dt, N, D, V, ws = _head_args(fn, x, W, 1, loss, dloss, dx, dW, lse, ws, stream)
-    _check(fn, lib().poetx_head_ce(dt, _p(x), N, D, _p(W), V, _p(target), z_loss, _p(dloss),
-                                   _p(loss), _p(lse), _p(dx), _p(dW), int(bool(accumulate)),
-                                   _p(ws), ws.numel(), _stream(stream)))
+    _head(fn, lib().poetx_head_ce, x, W, 1, target, None, loss, dloss, dx, dW, lse, ws, stream,
+          z_loss, accumulate)
 
 
 def poetx_head_distill(x, W, t_index, t_logit, loss, dloss=None, dx=None, dW=None, lse=None,
@@ -573,11 +602,8 @@ def poetx_head_distill(x, W, t_index, t_logit, loss, dloss=None, dx=None, dW=Non
     """loss [N] fp32 of T^2 KL(teacher || student) from the teacher's top logits t_logit [N, K]
     fp32 at the entries t_index [N, K] int32 (negative: absent), and with dloss the gradients."""
     fn = "poetx_head_distill"
-    N, K = t_index.shape
-    _want(fn, "t_index", t_index, (x.shape[0], K), torch.int32)
-    _want(fn, "t_logit", t_logit, (N, K), torch.float32)
-    dt, N, D, V, ws = _head_args(fn, x, W, K, loss, dloss, dx, dW, lse, ws, stream)
-    _check(fn, lib().poetx_head_distill(dt, _p(x), N, D, _p(W), V, _p(t_index), _p(t_logit), K,
-                                        temperature, _p(dloss), _p(loss), _p(lse), _p(dx), _p(dW),
-                                        int(bool(accumulate)), _p(ws), ws.numel(),
-                                        _stream(stream)))
+    shape = (x.shape[0], t_index.shape[-1])
+    _want(fn, "t_index", t_index, shape, torch.int32)
+    _want(fn, "t_logit", t_logit, shape, torch.float32)
+    _head(fn, lib().poetx_head_distill, x, W, shape[1], t_index, t_logit, loss, dloss, dx, dW, lse,
+          ws, stream, temperature, accumulate)
