@@ -20,7 +20,8 @@
 // The products run on tcgen05 in 2-CTA pairs (256 x 256 tiles, operands by TMA).  The tensor core
 // truncates when it adds into its fp32 accumulator, which over a long K drifts by about 2^-24 of
 // the sum per step; so after every `chunk` of K the partial tile moves from TMEM into the epilogue's
-// registers and is added there with IEEE adds, while the next chunk runs in the other half of TMEM.
+// registers and is added there with IEEE adds, while the next chunk runs in the other half of TMEM
+// (K = 512 per chunk against 1024: 4 % of the products' time, which runs at the power limit).
 //
 // fp32 heads run on the same kernels: each fp32 operand is split into three bf16 pieces (8 + 8 + 8
 // significant bits) and a product takes the six pairs of pieces whose weight is above 2^-24, the
@@ -31,6 +32,7 @@
 #include <cuda_fp16.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -53,31 +55,39 @@ constexpr uint32_t kABytes = BM * BK * 2;
 constexpr uint32_t kBBytes = BN / 2 * BK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;  // 32 KB per CTA
 constexpr uint32_t kStgBytes = 32 * 128;             // one epilogue warp's box: 32 rows of 128 bytes
+// Tiles of a raster band: the pairs in flight then cover about 8 x 9 tiles, so that each operand stripe
+// is shared by many of them, and the band's stripes (16 MB at K = 4096) stay in L2 while the other
+// operand streams past.  Whole columns of tiles instead: 8192 x 128256 x 4096 read 14 GB for dx.
+constexpr int kBand = 8;
 constexpr int kGemmSmem = kStages * kStageBytes + kEpiWarps * kStgBytes + 1024 + 512;
 static_assert(kGemmSmem <= 227 * 1024, "head products: shared memory");
 constexpr int kMaxSegs = 6;
 
-enum Epi : int {
-  EPI_LSE = 0,    // groups' (max, sum) and, where the gradients are wanted, exp(z - max)
-  EPI_STORE = 1,  // the product itself
-};
-
 struct HeadMaps {
   CUtensorMap a[3], b[3];  // the operands' pieces (one for bf16)
-  CUtensorMap c;           // the stored tile
+  CUtensorMap c;           // the stored tensor
+};
+
+// One product C[M, N] = A[M, K] B[N, K]^T over 256 x 256 tiles and K splits.
+struct Product {
+  int tiles_m, tiles_n, num_tiles;  // num_tiles: with the splits (the split varies slowest)
+  int n_fast;            // raster: bands of kBand M tiles (1: N tiles), M (N) fastest in a band
+  int num_kb, kb_split;  // 64-wide K blocks in all, per split
+  int a_mn;              // A stored with its M axis contiguous ([K][M])
+  int M, N;              // valid rows and columns
+  int n_store;           // columns of the stored tensor
+  int c_rows;            // its rows per split
+  int c_f32;             // stored in fp32, else 16 bits
+  const float* add_f32;  // added before the store (nullable), as is
+  const __nv_bfloat16* add_bf16;
 };
 
 struct HeadGemm {
-  int tiles_m, tiles_n, splits, num_tiles;
-  int n_fast;            // raster: 1: tiles of a row stripe first (A read once), 0: of a column stripe
-  int num_kb, kb_split;  // 64-wide K blocks in all, per split
+  Product prod[2];       // the tiles of the first, then those of the second (none: num_tiles 0)
+  int num_tiles;
   int chunk;             // K blocks per accumulator hand-over
-  int nseg;              // products of operand pieces per K block
-  int8_t seg_a[kMaxSegs], seg_b[kMaxSegs];
-  int M, N;              // valid rows and columns
-  int n_store;           // columns of the stored tensor
-  int c_rows;            // EPI_STORE: rows of the stored tensor per split
-  // EPI_LSE
+  int8_t seg_a[kMaxSegs], seg_b[kMaxSegs];  // fp32: the operand pieces multiplied, in order
+  // logits' product
   float scale2;          // log2(e) / T
   float2* part;          // [M][groups]
   int groups;
@@ -85,18 +95,14 @@ struct HeadGemm {
   const uint16_t* gstart;  // [M][groups + 1] first of them in each group; NULL: K = 1
   int K;
   float* tl;             // [M][K] their logits, before 1/T
-  int store;             // whether c is stored
-  // EPI_STORE: added before the store (nullable)
-  const float* add_f32;
-  const __nv_bfloat16* add_bf16;
+  int store;             // whether exp(z - m) is stored
+  const float* dloss;    // with store: [M] upstream gradients, whose largest magnitude goes to
+  float* unit;           //   unit (head_unit), read back as
+  const float* out_scale;  // gradients' products: factor of the sums
+  float T;
   int* err;
   unsigned long long limit_ns;
 };
-
-template <bool MN>
-__device__ __forceinline__ uint64_t tile_desc(uint32_t base, int k) {
-  return MN ? make_sdesc(base + k * 2048, 8192, 1024) : make_sdesc(base + k * 32, 16, 1024);
-}
 
 __device__ __forceinline__ float ex2(float v) {
   float r;
@@ -104,29 +110,76 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
+// K-major tile: rows of 128 bytes (64 along K), 8-row groups 1024 bytes apart, the k-th K = 16 slice
+// 32 bytes further; MN-major tile: boxes of 64 K rows x 64 side by side (8 KB), the slice 16 rows
+// (2048 bytes) further.
+template <bool MN>
+__device__ __forceinline__ uint64_t tile_desc(uint32_t base) {
+  return MN ? make_sdesc(base, 8192, 1024) : make_sdesc(base, 16, 1024);
+}
+
 struct Tile {
+  int which;  // product
   int mi, nt, split, kb0, kb1;
 };
 __device__ __forceinline__ Tile tile_of(const HeadGemm& p, int t) {
   Tile c;
-  const int per = p.tiles_m * p.tiles_n;
+  c.which = t >= p.prod[0].num_tiles;
+  if (c.which) t -= p.prod[0].num_tiles;
+  const Product& d = p.prod[c.which];
+  const int per = d.tiles_m * d.tiles_n;
   c.split = t / per;
   const int r = t - c.split * per;
-  c.mi = p.n_fast ? r / p.tiles_n : r % p.tiles_m;
-  c.nt = p.n_fast ? r % p.tiles_n : r / p.tiles_m;
-  c.kb0 = c.split * p.kb_split;
-  c.kb1 = min(p.num_kb, c.kb0 + p.kb_split);
+  const int fast = d.n_fast ? d.tiles_n : d.tiles_m, slow = d.n_fast ? d.tiles_m : d.tiles_n;
+  const int f0 = r / (kBand * slow) * kBand;  // the band's first tile of the fast axis
+  const int width = min(kBand, fast - f0), q = r - f0 * slow;
+  const int f = f0 + q % width, o = q / width;
+  c.mi = d.n_fast ? o : f;
+  c.nt = d.n_fast ? f : o;
+  c.kb0 = c.split * d.kb_split;
+  c.kb1 = min(d.num_kb, c.kb0 + d.kb_split);
   return c;
 }
 
-// C[M, N] = A[M, K] B[N, K]^T over 256 x 256 tiles; A_MN / B_MN: the operand is stored with its M
-// or N axis contiguous ([K][M], [K][N]).  Warp 0 of each CTA loads its 128 rows of A and its half
-// of B, one thread of the even CTA's warp 1 issues the MMAs, warps 2-9 read the accumulators back
-// (warp w: rows 32 (w % 4).. of the CTA's 128, columns 128 ((w - 2) / 4)..).
-template <bool A_MN, bool B_MN, int EPI, bool OUT_F32>
+// Position in a ring of n buffers.  (Counted, not divided: the issuing threads have some 500 cycles
+// per K block, and 64-bit remainders by the stage count alone cost the products 8 %.)
+template <int n>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == n) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
+// Bounded wait that looks at the abort flag only where the barrier is not ready.
+__device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
+                                          const HeadGemm& p, int site) {
+  if (mbar_try_wait(bar, parity)) return true;
+  if (*abort_flag || !mbar_wait_bounded(bar, parity, p.err, p.limit_ns, site)) {
+    *abort_flag = 1;
+    return false;
+  }
+  return true;
+}
+
+// The unit of dz: the largest |dloss| of the piece.  dz is kept over unit * T, so that with equal
+// upstream gradients (a mean) the bf16 rounding sees p - q alone and not a constant's mantissa too;
+// the sums get the factor back in fp32.  1 where there is no finite positive maximum.
+__device__ __forceinline__ float head_unit(float top) { return top > 0.f && top < 3.0e38f ? top : 1.f; }
+
+// LSE: the logits' product with its softmax epilogue (one product, both operands K-major).
+// Otherwise the gradients' products, dx and dW in one launch, so that the second's tiles fill the
+// first's last wave.  Warp 0 of each CTA loads its 128 rows of A and its half of B, one thread of
+// the even CTA's warp 1 issues the MMAs, warps 2-9 read the accumulators back (warp w: rows
+// 32 (w % 4).. of the CTA's 128, columns 128 ((w - 2) / 4)..).
+template <bool LSE, bool F32>
 __global__ void __launch_bounds__(kGemmThreads, 1)
-    head_gemm_kernel(const __grid_constant__ HeadMaps maps, const HeadGemm p) {
-  constexpr uint32_t IDESC = make_idesc(2 * BM, BN, A_MN, B_MN);
+    head_gemm_kernel(const __grid_constant__ HeadMaps maps0, const __grid_constant__ HeadMaps maps1,
+                     const __grid_constant__ HeadGemm p) {
   constexpr uint32_t TMEM_COLS = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -153,8 +206,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&maps.a[0]);
-    tma_prefetch_desc(&maps.b[0]);
+    tma_prefetch_desc(&maps0.a[0]);
+    tma_prefetch_desc(&maps0.b[0]);
   }
   if (warp == 1) {
     tmem_alloc_pair(tmem_slot, TMEM_COLS);
@@ -170,116 +223,126 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 
   if (warp == 0 && lane == 0) {
     // ------------------------------------------------------------ TMA producer
-    long long g = 0;
+    Ring<kStages> rg;
     bool ok = true;
+    long long issued = 0;
+    const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
     for (int t = t0; t < p.num_tiles && ok; t += t_step) {
       const Tile c = tile_of(p, t);
-      const int m0 = (2 * c.mi + crank) * BM, n0 = c.nt * BN;
+      const HeadMaps& maps = c.which ? maps1 : maps0;
+      const bool a_mn = !LSE && p.prod[c.which].a_mn;
+      constexpr bool b_mn = !LSE;
+      const int m0 = (2 * c.mi + crank) * BM, n0 = c.nt * BN + crank * (BN / 2);
       for (int kb = c.kb0; kb < c.kb1 && ok; ++kb)
-        for (int sg = 0; sg < p.nseg; ++sg, ++g) {
-          const int s = (int)(g % kStages);
-          if (*abort_flag || !mbar_wait_bounded(&empty[s], (uint32_t)((g / kStages) & 1) ^ 1, p.err,
-                                                p.limit_ns, kSite + __LINE__)) {
-            *abort_flag = 1;
+        for (int sg = 0; sg < (F32 ? kMaxSegs : 1); ++sg, rg.next(), ++issued) {
+          if (!ring_wait(&empty[rg.s], rg.ph ^ 1, abort_flag, p, kSite + __LINE__)) {
             ok = false;
             break;
           }
-          uint8_t* sa = smem + s * kStageBytes;
+          uint8_t* sa = smem + rg.s * kStageBytes;
           uint8_t* sb = sa + kABytes;
-          const CUtensorMap* ma = &maps.a[p.seg_a[sg]];
-          const CUtensorMap* mb = &maps.b[p.seg_b[sg]];
+          const CUtensorMap* ma = &maps.a[F32 ? p.seg_a[sg] : 0];
+          const CUtensorMap* mb = &maps.b[F32 ? p.seg_b[sg] : 0];
           const int k = kb * BK;
-          if (crank == 0) mbar_arrive_expect_tx(&full[s], 2 * kStageBytes);
-          const uint32_t fb = mapa_shared(&full[s], 0);
-          if (!A_MN) {
+          if (crank == 0) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
+          const uint32_t fb = full0 + rg.s * 8;
+          if (!a_mn) {
             tma_load_2d_pair(sa, ma, fb, k, m0);
-          } else {
+          } else {  // two boxes of 64 rows of K x 64 of M
             tma_load_2d_pair(sa, ma, fb, m0, k);
             tma_load_2d_pair(sa + 8192, ma, fb, m0 + 64, k);
           }
-          if (!B_MN) {
-            tma_load_2d_pair(sb, mb, fb, k, n0 + crank * (BN / 2));
+          if (!b_mn) {
+            tma_load_2d_pair(sb, mb, fb, k, n0);
           } else {
-            tma_load_2d_pair(sb, mb, fb, n0 + crank * (BN / 2), k);
-            tma_load_2d_pair(sb + 8192, mb, fb, n0 + crank * (BN / 2) + 64, k);
+            tma_load_2d_pair(sb, mb, fb, n0, k);
+            tma_load_2d_pair(sb + 8192, mb, fb, n0 + 64, k);
           }
         }
     }
     // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
-    for (long long j = g - 1; j >= 0 && j >= g - kStages; --j)
+    for (long long j = issued - 1; j >= 0 && j >= issued - kStages; --j)
       mbar_wait_bounded(&empty[j % kStages], (uint32_t)((j / kStages) & 1), p.err, p.limit_ns,
                         kSite + __LINE__);
   } else if (warp == 1 && lane == 0 && crank == 0) {
     // ------------------------------------------------------------ MMA issuer
-    long long g = 0, it = 0;  // ring position; accumulator hand-overs
-    bool ok = true;
-    for (int t = t0; t < p.num_tiles && ok; t += t_step) {
-      const Tile c = tile_of(p, t);
-      for (int kb = c.kb0; kb < c.kb1 && ok; kb += p.chunk, ++it) {
-        const int a = (int)(it & 1);
-        if (*abort_flag || !mbar_wait_bounded(&tempty[a], (uint32_t)((it >> 1) & 1) ^ 1, p.err,
-                                              p.limit_ns, kSite + __LINE__)) {
-          *abort_flag = 1;
-          ok = false;
-          break;
-        }
+    Ring<kStages> rg;
+    Ring<2> acc;
+    bool any = false;
+    // one tile; the operands' orders are compile-time constants (as run-time values they cost the
+    // issuing thread 15 % of the products' time)
+    auto tile = [&](const Tile& c, auto a_mn_t) -> bool {
+      constexpr bool A_MN = decltype(a_mn_t)::value, B_MN = !LSE;
+      constexpr uint32_t IDESC = make_idesc(2 * BM, BN, A_MN, B_MN);
+      for (int kb = c.kb0; kb < c.kb1; kb += p.chunk, acc.next()) {
+        if (!ring_wait(&tempty[acc.s], acc.ph ^ 1, abort_flag, p, kSite + __LINE__)) return false;
         tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(a * BN);
-        const int blocks = (min(c.kb1, kb + p.chunk) - kb) * p.nseg;
-        for (int j = 0; j < blocks; ++j, ++g) {
-          const int s = (int)(g % kStages);
-          if (*abort_flag || !mbar_wait_bounded(&full[s], (uint32_t)((g / kStages) & 1), p.err,
-                                                p.limit_ns, kSite + __LINE__)) {
-            *abort_flag = 1;
-            ok = false;
-            break;
-          }
+        const uint32_t d = tmem_base + (uint32_t)(acc.s * BN);
+        const int blocks = (min(c.kb1, kb + p.chunk) - kb) * (F32 ? kMaxSegs : 1);
+        for (int j = 0; j < blocks; ++j, rg.next()) {
+          if (!ring_wait(&full[rg.s], rg.ph, abort_flag, p, kSite + __LINE__)) return false;
           tc_fence_after();
-          const uint32_t a_base = smem_base + s * kStageBytes;
-          const uint32_t b_base = a_base + kABytes;
+          const uint32_t a_base = smem_base + rg.s * kStageBytes;
+          const uint64_t ad = tile_desc<A_MN>(a_base), bd = tile_desc<B_MN>(a_base + kABytes);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16_pair(d, tile_desc<A_MN>(a_base, k), tile_desc<B_MN>(b_base, k), IDESC,
+          for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
+            umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
                            (j | k) != 0);
-          umma_commit_pair(&empty[s]);
+          umma_commit_pair(&empty[rg.s]);
         }
-        umma_commit_pair(&tfull[a]);
+        umma_commit_pair(&tfull[acc.s]);
+        any = true;
       }
+      return true;
+    };
+    for (int t = t0; t < p.num_tiles; t += t_step) {
+      const Tile c = tile_of(p, t);
+      if (!(!LSE && p.prod[c.which].a_mn ? tile(c, std::true_type{}) : tile(c, std::false_type{})))
+        break;
     }
-    if (it > 0)  // TMEM is freed after the final barrier: wait for the last MMAs
-      mbar_wait_bounded(&tfull[(it - 1) & 1], (uint32_t)(((it - 1) >> 1) & 1), p.err, p.limit_ns,
+    if (any) {  // TMEM is freed after the final barrier: wait for the last hand-over's MMAs
+      const int last = acc.s ^ 1;
+      mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns,
                         kSite + __LINE__);
+    }
+  } else if (LSE && warp == 1 && blockIdx.x == 1 && p.store) {
+    // ------------------------------------------------------------ an idle warp: the unit of dz
+    float top = 0.f;
+    for (int r = lane; r < p.prod[0].M; r += 32) top = fmaxf(top, fabsf(p.dloss[r]));
+#pragma unroll
+    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) *p.unit = head_unit(top);
   } else if (warp >= 2) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int cbeg = ((warp - 2) >> 2) * kGroup;
     uint8_t* stg = staging + (warp - 2) * kStgBytes;
-    long long it = 0;
+    const float out_scale = LSE ? 1.f : *p.out_scale * p.T;
+    Ring<2> acc;
     bool ok = true;
     for (int t = t0; t < p.num_tiles && ok; t += t_step) {
       const Tile c = tile_of(p, t);
+      const Product& d = p.prod[LSE ? 0 : c.which];
       const int row_w = (2 * c.mi + crank) * BM + q * 32;  // the warp's first row
       const int row = row_w + lane;
       const int col0 = c.nt * BN + cbeg;
       // the row's targets in this group: [u0, u1) of its list (read ahead of the wait)
       int u0 = 0, u1 = 0;
-      if (EPI == EPI_LSE && row < p.M && col0 < p.N) {
+      if (LSE && row < d.M && col0 < d.N) {
         if (p.gstart) {
           const uint16_t* gs = p.gstart + (long long)row * (p.groups + 1) + col0 / kGroup;
           u0 = gs[0];
           u1 = gs[1];
         } else {
           const int tc = p.ucol[row];
-          u1 = tc >= col0 && tc < min(col0 + kGroup, p.N);
+          u1 = tc >= col0 && tc < min(col0 + kGroup, d.N);
         }
       }
       float v[kGroup];
-      for (int kb = c.kb0; kb < c.kb1; kb += p.chunk, ++it) {
-        const int a = (int)(it & 1);
-        const bool got = !*abort_flag && mbar_wait_bounded(&tfull[a], (uint32_t)((it >> 1) & 1),
-                                                           p.err, p.limit_ns, kSite + __LINE__);
+      for (int kb = c.kb0; kb < c.kb1; kb += p.chunk, acc.next()) {
+        const int a = acc.s;
+        const bool got = ring_wait(&tfull[a], acc.ph, abort_flag, p, kSite + __LINE__);
         if (!__all_sync(0xffffffffu, got)) {
-          *abort_flag = 1;
           ok = false;
           break;
         }
@@ -303,12 +366,12 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
         if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[a], 0));
       }
       if (!ok) break;
-      if (col0 >= p.N || row_w >= p.M) continue;
-      if (EPI == EPI_LSE) {
-        if (col0 + kGroup > p.N) {
+      if (col0 >= d.N || row_w >= d.M) continue;
+      if (LSE) {
+        if (col0 + kGroup > d.N) {
 #pragma unroll
           for (int i = 0; i < kGroup; ++i)
-            if (col0 + i >= p.N) v[i] = __int_as_float(0xff800000);  // -inf: exp 0
+            if (col0 + i >= d.N) v[i] = __int_as_float(0xff800000);  // -inf: exp 0
         }
         if (__any_sync(0xffffffffu, u0 < u1)) {  // take the targets out of the group
           uint32_t mask[kGroup / 32] = {};
@@ -340,15 +403,17 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           s0 += v[i];
           s1 += v[i + 1];
         }
-        if (row < p.M)
+        if (row < d.M)
           p.part[(long long)row * p.groups + (col0 / kGroup)] = make_float2(m, s0 + s1);
         if (!p.store) continue;
       } else {
-        if (p.add_f32 && row < p.M) {
-          const float* src = p.add_f32 + (long long)row * p.N + col0;
+#pragma unroll
+        for (int i = 0; i < kGroup; ++i) v[i] *= out_scale;
+        if (d.add_f32 && row < d.M) {
+          const float* src = d.add_f32 + (long long)row * d.N + col0;
 #pragma unroll
           for (int i = 0; i < kGroup; i += 4)
-            if (col0 + i < p.N) {  // N is a multiple of 8
+            if (col0 + i < d.N) {  // N is a multiple of 8
               const float4 w = *reinterpret_cast<const float4*>(src + i);
               v[i] += w.x;
               v[i + 1] += w.y;
@@ -356,11 +421,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
               v[i + 3] += w.w;
             }
         }
-        if (p.add_bf16 && row < p.M) {
-          const __nv_bfloat16* src = p.add_bf16 + (long long)row * p.N + col0;
+        if (!F32 && d.add_bf16 && row < d.M) {
+          const __nv_bfloat16* src = d.add_bf16 + (long long)row * d.N + col0;
 #pragma unroll
           for (int i = 0; i < kGroup; i += 8)
-            if (col0 + i < p.N) {
+            if (col0 + i < d.N) {
               const uint4 w = *reinterpret_cast<const uint4*>(src + i);
               const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -373,40 +438,44 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       }
       // store by TMA: boxes of 32 rows x 128 bytes, 128-byte swizzle; rows and columns outside
       // the tensor are clipped
-      constexpr int PASS = OUT_F32 ? 32 : 64;
-      const int orow = EPI == EPI_STORE ? c.split * p.c_rows + row_w : row_w;
-#pragma unroll
-      for (int j = 0; j < kGroup; j += PASS) {
-        if (col0 + j >= p.n_store) break;
+      const int orow = LSE ? row_w : c.split * d.c_rows + row_w;
+      const CUtensorMap* mc = &(c.which ? maps1 : maps0).c;
+      auto box = [&](int j, auto chunk) {  // chunk(i): 16 bytes i of the lane's row
         if (lane == 0) bulk_wait_read<0>();  // the previous box has been read
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          uint4 w;
-          if (OUT_F32) {
-            w = make_uint4(__float_as_uint(v[j + 4 * i]), __float_as_uint(v[j + 4 * i + 1]),
-                           __float_as_uint(v[j + 4 * i + 2]), __float_as_uint(v[j + 4 * i + 3]));
-          } else {
-            uint32_t u[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float lo = v[j + 8 * i + 2 * k], hi = v[j + 8 * i + 2 * k + 1];
-              if (EPI == EPI_LSE) {
-                const __half2 h = __floats2half2_rn(lo, hi);
-                u[k] = *reinterpret_cast<const uint32_t*>(&h);
-              } else {
-                u[k] = pack_bf16x2(lo, hi);
-              }
-            }
-            w = make_uint4(u[0], u[1], u[2], u[3]);
-          }
-          *reinterpret_cast<uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = w;
-        }
+        for (int i = 0; i < 8; ++i)
+          *reinterpret_cast<uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = chunk(i);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
-          tma_store_2d(&maps.c, stg, col0 + j, orow);
+          tma_store_2d(mc, stg, col0 + j, orow);
           bulk_commit();
+        }
+      };
+      if (F32 || (!LSE && d.c_f32)) {
+#pragma unroll
+        for (int j = 0; j < kGroup; j += 32) {
+          if (col0 + j >= d.n_store) break;
+          box(j, [&](int i) {
+            const float* f = v + j + 4 * i;
+            return make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]),
+                              __float_as_uint(f[3]));
+          });
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < kGroup; j += 64) {
+          if (col0 + j >= d.n_store) break;
+          box(j, [&](int i) {
+            const float* f = v + j + 8 * i;
+            auto two = [](float lo, float hi) {
+              if (!LSE) return pack_bf16x2(lo, hi);
+              const __half2 h = __floats2half2_rn(lo, hi);
+              return *reinterpret_cast<const uint32_t*>(&h);
+            };
+            return make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
+          });
         }
       }
     }
@@ -482,6 +551,7 @@ struct RowArgs {
   const uint16_t* slot;   // [rows][K] place of idx in ucol
   const float* tlogit;    // [rows][K] the teacher's logits; NULL: cross entropy (K = 1)
   const float* dloss;     // [rows] upstream gradients (with e)
+  const float* unit;      // dz is kept over *unit * T
   float T, zl;
   float* loss;
   float* lse;             // nullable
@@ -630,7 +700,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   }
   if (!p.e) return;
   const bool live = some > 0.f && !bad;
-  const float gT = live ? p.dloss[row] * p.T : 0.f;
+  const float gT = live ? p.dloss[row] / *p.unit : 0.f;
   const float coef = gT * weight;
   for (int g = t; g < p.groups; g += kRowThreads) fac[g] = coef * exp2f(fac[g] - lse2);
   __syncthreads();
@@ -748,13 +818,14 @@ unsigned grid_for(long long items, int threads) {
   return (unsigned)(b < 1 ? 1 : b);
 }
 
-template <bool A_MN, bool B_MN, int EPI, bool OUT_F32>
-poetx_status gemm(const HeadMaps& maps, HeadGemm p, cudaStream_t s) {
-  auto k = head_gemm_kernel<A_MN, B_MN, EPI, OUT_F32>;
+// Co-resident CTA pairs of a GEMM kernel (one CTA per SM).
+template <bool LSE, bool F32>
+cudaError_t gemm_pairs(int* pairs) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int max_pairs = 0;
   std::call_once(once, [&] {
+    auto k = head_gemm_kernel<LSE, F32>;
     attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
@@ -771,41 +842,66 @@ poetx_status gemm(const HeadMaps& maps, HeadGemm p, cudaStream_t s) {
     attr_err = cudaOccupancyMaxActiveClusters(&max_pairs, k, &cfg);
     if (attr_err == cudaSuccess && max_pairs < 1) attr_err = cudaErrorInvalidConfiguration;
   });
-  POETX_CUDA_TRY(attr_err);
-  const long long tiles = (long long)p.tiles_m * p.tiles_n * p.splits;
+  *pairs = max_pairs;
+  return attr_err;
+}
+
+template <bool LSE, bool F32>
+poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStream_t s) {
+  int max_pairs = 0;
+  POETX_CUDA_TRY((gemm_pairs<LSE, F32>(&max_pairs)));
+  long long tiles = 0;
+  for (const Product& d : p.prod) {
+    if ((long long)d.tiles_m * d.tiles_n > 0x3fffffffLL) return POETX_ERR_SHAPE;
+    tiles += d.num_tiles;
+  }
   if (tiles > 0x7fffffffLL) return POETX_ERR_SHAPE;
   p.num_tiles = (int)tiles;
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
   const int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
-  POETX_CUDA_TRY(launch_pdl_cluster(k, dim3(2 * pairs), dim3(kGemmThreads), kGemmSmem, s, 2, maps, p));
+  POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, F32>, dim3(2 * pairs), dim3(kGemmThreads),
+                                    kGemmSmem, s, 2, m0, m1, p));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_HEAD_GEMM);
   return POETX_OK;
 }
 
-// The K splits of dx: enough work units to fill the pairs evenly, against the partials' traffic
-// (per unit, a 64-wide K block of a 256 x 256 tile takes about 0.3 us of a pair, and the partials
-// move at about 5 TB/s).
-int dx_splits(long long rows, int D, int V) {
-  const long long tiles = (long long)ceil_div(rows, 2 * BM) * ceil_div(D, BN);
-  const int kb = ceil_div(V, BK), pairs = sm_count() / 2;
+// The K splits of dx, which runs alone or in one launch with dW on pairs that take every P-th tile:
+// the split with the shortest longest pair, with the partials' traffic (at about 5 TB/s) against it.
+// A 64-wide K block of a 256 x 256 tile takes about 0.3 us of a pair, a tile 0.6 us besides.  One
+// split for both uses (the sum of the two times decides), so that dx has the same bits in both.
+int dx_splits(long long rows, int D, int V, int nseg) {
+  const long long t1 = (long long)ceil_div(rows, 2 * BM) * ceil_div(D, BN);
+  const long long t2 = (long long)ceil_div(V, 2 * BM) * ceil_div(D, BN);
+  const int kb1 = ceil_div(V, BK), kb2 = ceil_div(rows, BK), pairs = sm_count() / 2;
   int best = 1;
   double best_us = 1e30;
-  for (int S = 1; S <= 64 && S <= kb; ++S) {
-    const long long waves = (tiles * S + pairs - 1) / pairs;
-    double us = (double)waves * (ceil_div(kb, S) * 0.3 + 2.0);
-    if (S > 1) us += 3.0 + 8e-6 * (double)S * (double)rows * D / 5.0;
+  for (int S = 1; S <= 64 && S <= kb1; ++S) {
+    const long long n1 = t1 * S, all = n1 + t2;
+    const double us1 = 0.6 + 0.3 * nseg * ceil_div(kb1, S), us2 = 0.6 + 0.3 * nseg * kb2;
+    double alone = 0, both = 0;
+    // pair i has n1 / P (+ 1 where i < n1 % P) tiles of dx, likewise of all: three kinds of pairs
+    for (const long long i : {0LL, n1 % pairs, all % pairs}) {
+      const long long a = n1 / pairs + (i < n1 % pairs), c = all / pairs + (i < all % pairs);
+      if (a * us1 > alone) alone = a * us1;
+      if (a * us1 + (c - a) * us2 > both) both = a * us1 + (c - a) * us2;
+    }
+    double us = alone + both;
+    if (S > 1) us += 2 * (3.0 + 8e-6 * (double)S * (double)rows * D / 5.0);
     if (us < best_us) {
       best_us = us;
       best = S;
     }
   }
   // every split non-empty
-  return ceil_div(kb, ceil_div(kb, best));
+  return ceil_div(kb1, ceil_div(kb1, best));
 }
 
-constexpr size_t kPieceBytes = (size_t)1 << 30;  // bound of a piece's stored exponentials
+// Bound of a piece's stored exponentials, where there is more than one piece: each piece but the
+// first reads and writes dW's fp32 sums (8 V D bytes against 6 rows V D flops: at 2 GB per piece of a
+// 128-thousand vocabulary about a tenth of the piece's time).
+constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
 constexpr int kMaxTargets = 1024;
 
 struct Plan {
@@ -816,7 +912,7 @@ struct Plan {
   int pieces;
   int splits;        // K splits of dx
   // workspace offsets
-  size_t part, tl, ucol, slot, gstart, e, dz, xs, ws, acc, dxp, bytes;
+  size_t unit, part, tl, ucol, slot, gstart, e, dz, xs, ws, acc, dxp, bytes;
 };
 
 bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o) {
@@ -828,14 +924,19 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   o->groups = ceil_div(V, kGroup);
   const size_t row_bytes = (o->grads ? (size_t)o->Vp * (o->f32 ? 10 : 2) : 0) +
                            (size_t)o->groups * 8 * (o->grads ? 1 : 4);
-  long long rows = (long long)(kPieceBytes / row_bytes) / 256 * 256;
-  if (rows < 256) rows = 256;
-  if (rows > (1 << 18)) rows = 1 << 18;
   const long long n = N > 0 ? N : 1;
+  // one piece where that takes no more memory than a piece and dW's fp32 sums would
+  const size_t whole = kPieceBytes + (!o->f32 && dW ? (size_t)V * D * 4 : 0);
+  long long rows = n;
+  if ((unsigned long long)n > whole / row_bytes) {
+    rows = (long long)(kPieceBytes / row_bytes) / 256 * 256;
+    if (rows < 256) rows = 256;
+  }
+  if (rows > (1 << 18)) rows = 1 << 18;
   o->pieces = ceil_div(n, rows);
   o->rows = o->pieces == 1 ? n : (long long)align_up((size_t)ceil_div(n, o->pieces), 256);
   o->pieces = ceil_div(n, o->rows);
-  o->splits = dx ? dx_splits(o->rows, D, V) : 1;
+  o->splits = dx ? dx_splits(o->rows, D, V, o->f32 ? kMaxSegs : 1) : 1;
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t a = at;
@@ -843,6 +944,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
     return a;
   };
   const size_t R = (size_t)o->rows;
+  o->unit = take(4);
   o->part = take(R * o->groups * sizeof(float2));
   o->tl = take(R * K * 4);
   // the sorted target lists of a distillation (a call with K = 1 may be either: both fit)
@@ -863,16 +965,16 @@ bool bf16_map(CUtensorMap* m, const void* p, long long inner, long long outer, i
   return encode_tma_2d(m, p, TMA_BF16, inner, outer, inner, bi, bo, true);
 }
 
-void set_segs(HeadGemm* g, bool f32) {
+void set_segs(HeadGemm* g, bool f32, bool lse) {
   // small pieces first, so that the accumulator is small while they are added
   static const int8_t a[kMaxSegs] = {1, 0, 2, 1, 0, 0}, b[kMaxSegs] = {1, 2, 0, 0, 1, 0};
-  g->nseg = f32 ? kMaxSegs : 1;
   for (int i = 0; i < kMaxSegs; ++i) {
-    g->seg_a[i] = f32 ? a[i] : 0;
-    g->seg_b[i] = f32 ? b[i] : 0;
+    g->seg_a[i] = a[i];
+    g->seg_b[i] = b[i];
   }
-  // K of one accumulator: 512 (32 adds of 16 products) in bf16, 64 per piece pair in fp32
-  g->chunk = f32 ? 1 : 8;
+  // K of one accumulator: 64 per piece pair in fp32; in bf16 1024 for the logits (64 adds of 16
+  // products) and 4096 for the gradients, which are rounded to bf16 (256 adds: 1.5e-5)
+  g->chunk = f32 ? 1 : (lse ? 16 : 64);
 }
 
 struct HeadCall {
@@ -946,6 +1048,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     POETX_TRY(run_split(static_cast<const float*>(c.W), (long long)c.V * c.D, w + pl.ws, w_step, s));
   float2* part = reinterpret_cast<float2*>(w + pl.part);
   float* tl = reinterpret_cast<float*>(w + pl.tl);
+  float* unit = reinterpret_cast<float*>(w + pl.unit);
   const uint8_t* wp = pl.f32 ? w + pl.ws : static_cast<const uint8_t*>(c.W);
 
   for (int pc = 0; pc < pl.pieces; ++pc) {
@@ -971,20 +1074,21 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       ucol = u;
     }
     // the logits' product
-    HeadMaps mp;
+    HeadMaps mp, mw;
     HeadGemm g{};
-    set_segs(&g, pl.f32);
+    set_segs(&g, pl.f32, true);
     for (int i = 0; i < np; ++i)
       if (!bf16_map(&mp.a[i], xp + i * x_step, c.D, rows, 64, 128) ||
           !bf16_map(&mp.b[i], wp + i * w_step, c.D, c.V, 64, 128))
         return POETX_ERR_CUDA;
-    g.tiles_m = ceil_div(rows, 2 * BM);
-    g.tiles_n = ceil_div(c.V, BN);
-    g.splits = 1;
-    g.num_kb = g.kb_split = ceil_div(c.D, BK);
-    g.M = rows;
-    g.N = c.V;
-    g.n_store = (int)pl.Vp;  // columns V .. Vp - 1 are stored as zeros
+    Product& lg = g.prod[0];
+    lg.tiles_m = ceil_div(rows, 2 * BM);
+    lg.tiles_n = ceil_div(c.V, BN);
+    lg.num_tiles = lg.tiles_m * lg.tiles_n;
+    lg.num_kb = lg.kb_split = ceil_div(c.D, BK);
+    lg.M = rows;
+    lg.N = c.V;
+    lg.n_store = (int)pl.Vp;  // columns V .. Vp - 1 are stored as zeros
     g.scale2 = kLog2e / c.T;
     g.part = part;
     g.groups = pl.groups;
@@ -993,14 +1097,16 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     g.K = c.K;
     g.tl = tl;
     g.store = pl.grads;
+    g.dloss = c.dloss ? c.dloss + r0 : nullptr;
+    g.unit = unit;
     if (pl.grads && !encode_tma_2d(&mp.c, w + pl.e, pl.f32 ? TMA_F32 : TMA_BF16, pl.Vp, rows, pl.Vp,
                                    pl.f32 ? 32 : 64, 32, true))
       return POETX_ERR_CUDA;
     if (!pl.grads) mp.c = mp.a[0];
     if (pl.f32)
-      POETX_TRY((gemm<false, false, EPI_LSE, true>(mp, g, s)));
+      POETX_TRY((gemm<true, true>(mp, mp, g, s)));
     else
-      POETX_TRY((gemm<false, false, EPI_LSE, false>(mp, g, s)));
+      POETX_TRY((gemm<true, false>(mp, mp, g, s)));
     // rows: lse, loss, dz
     RowArgs ra{};
     ra.V = c.V;
@@ -1018,6 +1124,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     ra.zl = c.zl;
     ra.loss = c.loss + r0;
     ra.lse = c.lse ? c.lse + r0 : nullptr;
+    ra.unit = unit;
     ra.e = pl.grads ? w + pl.e : nullptr;
     for (int i = 0; i < 3; ++i)
       ra.piece[i] = reinterpret_cast<__nv_bfloat16*>(w + pl.dz + i * z_step);
@@ -1027,79 +1134,80 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       POETX_CUDA_TRY(launch_pdl(head_row_kernel<false>, dim3(rows), dim3(kRowThreads), row_smem, s, ra));
     POETX_CUDA_TRY(cudaGetLastError());
     after_launch(s, ST_HEAD_ROW);
-    // dx = dz W
+    if (!pl.grads) continue;
+    // dx = dz W and dW (+)= dz^T x; between the pieces of a bf16 head dW's sum stays in fp32
+    HeadGemm h{};
+    set_segs(&h, pl.f32, false);
+    h.out_scale = unit;
+    h.T = c.T;
+    int used = 0;
+    uint8_t* dxr = static_cast<uint8_t*>(c.dx) + (size_t)r0 * c.D * esz;
+    const int c_rows = (int)align_up((size_t)rows, 256);
     if (c.dx) {
-      uint8_t* dxr = static_cast<uint8_t*>(c.dx) + (size_t)r0 * c.D * esz;
-      HeadGemm h{};
-      set_segs(&h, pl.f32);
+      Product& d = h.prod[used++];
       for (int i = 0; i < np; ++i)
         if (!bf16_map(&mp.a[i], w + pl.dz + i * z_step, pl.Vp, rows, 64, 128) ||
             !bf16_map(&mp.b[i], wp + i * w_step, c.D, c.V, 64, 64))
           return POETX_ERR_CUDA;
-      h.tiles_m = ceil_div(rows, 2 * BM);
-      h.tiles_n = ceil_div(c.D, BN);
-      h.splits = pl.splits;
-      h.num_kb = ceil_div(c.V, BK);
-      h.kb_split = ceil_div(h.num_kb, h.splits);
-      h.M = rows;
-      h.N = h.n_store = c.D;
-      h.c_rows = (int)align_up(rows, 256);
-      const bool f32_out = pl.f32 || pl.splits > 1;
+      d.tiles_m = ceil_div(rows, 2 * BM);
+      d.tiles_n = ceil_div(c.D, BN);
+      d.num_tiles = d.tiles_m * d.tiles_n * pl.splits;
+      d.num_kb = ceil_div(c.V, BK);
+      d.kb_split = ceil_div(d.num_kb, pl.splits);
+      d.M = rows;
+      d.N = d.n_store = c.D;
+      d.c_rows = c_rows;
+      d.c_f32 = pl.f32 || pl.splits > 1;
       const void* dst = pl.splits > 1 ? w + pl.dxp : dxr;
-      const long long drows = pl.splits > 1 ? (long long)pl.splits * h.c_rows : rows;
-      if (!encode_tma_2d(&mp.c, dst, f32_out ? TMA_F32 : TMA_BF16, c.D, drows, c.D, f32_out ? 32 : 64,
+      const long long drows = pl.splits > 1 ? (long long)pl.splits * c_rows : rows;
+      if (!encode_tma_2d(&mp.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, drows, c.D, d.c_f32 ? 32 : 64,
                          32, true))
         return POETX_ERR_CUDA;
-      if (f32_out)
-        POETX_TRY((gemm<false, true, EPI_STORE, true>(mp, h, s)));
-      else
-        POETX_TRY((gemm<false, true, EPI_STORE, false>(mp, h, s)));
-      if (pl.splits > 1) {
-        const long long quads = (long long)rows * c.D / 4;
-        const float* pp = reinterpret_cast<const float*>(w + pl.dxp);
-        const long long stride = (long long)h.c_rows * c.D;
-        if (pl.f32)
-          POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, dim3(grid_for(quads, 256)), dim3(256), 0,
-                                    s, pp, pl.splits, stride, quads, reinterpret_cast<float*>(dxr)));
-        else
-          POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, dim3(grid_for(quads, 256)),
-                                    dim3(256), 0, s, pp, pl.splits, stride, quads,
-                                    reinterpret_cast<__nv_bfloat16*>(dxr)));
-        POETX_CUDA_TRY(cudaGetLastError());
-        after_launch(s, ST_HEAD_ROW);
-      }
     }
-    // dW (+)= dz^T x; between the pieces of a bf16 head the sum stays in fp32
     if (c.dW) {
-      HeadGemm h{};
-      set_segs(&h, pl.f32);
+      Product& d = h.prod[used];
+      HeadMaps& m = used++ ? mw : mp;
       for (int i = 0; i < np; ++i)
-        if (!bf16_map(&mp.a[i], w + pl.dz + i * z_step, pl.Vp, rows, 64, 64) ||
-            !bf16_map(&mp.b[i], xp + i * x_step, c.D, rows, 64, 64))
+        if (!bf16_map(&m.a[i], w + pl.dz + i * z_step, pl.Vp, rows, 64, 64) ||
+            !bf16_map(&m.b[i], xp + i * x_step, c.D, rows, 64, 64))
           return POETX_ERR_CUDA;
-      h.tiles_m = ceil_div(c.V, 2 * BM);
-      h.tiles_n = ceil_div(c.D, BN);
-      h.n_fast = 1;
-      h.splits = 1;
-      h.num_kb = h.kb_split = ceil_div(rows, BK);
-      h.M = c.V;
-      h.N = h.n_store = c.D;
-      h.c_rows = c.V;
+      d.tiles_m = ceil_div(c.V, 2 * BM);
+      d.tiles_n = ceil_div(c.D, BN);
+      d.num_tiles = d.tiles_m * d.tiles_n;
+      d.n_fast = 1;
+      d.num_kb = d.kb_split = ceil_div(rows, BK);
+      d.a_mn = 1;
+      d.M = d.c_rows = c.V;
+      d.N = d.n_store = c.D;
       const bool first = pc == 0, last = pc + 1 == pl.pieces;
-      const bool f32_out = pl.f32 || !last;
+      d.c_f32 = pl.f32 || !last;
       void* dst = pl.f32 || last ? c.dW : static_cast<void*>(w + pl.acc);
       if (pl.f32)
-        h.add_f32 = !first || c.accumulate ? static_cast<const float*>(c.dW) : nullptr;
+        d.add_f32 = !first || c.accumulate ? static_cast<const float*>(c.dW) : nullptr;
       else
-        h.add_f32 = !first ? reinterpret_cast<const float*>(w + pl.acc) : nullptr;
-      if (!pl.f32 && last && c.accumulate) h.add_bf16 = static_cast<const __nv_bfloat16*>(c.dW);
-      if (!encode_tma_2d(&mp.c, dst, f32_out ? TMA_F32 : TMA_BF16, c.D, c.V, c.D, f32_out ? 32 : 64,
-                         32, true))
+        d.add_f32 = !first ? reinterpret_cast<const float*>(w + pl.acc) : nullptr;
+      if (!pl.f32 && last && c.accumulate) d.add_bf16 = static_cast<const __nv_bfloat16*>(c.dW);
+      if (!encode_tma_2d(&m.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, c.V, c.D, d.c_f32 ? 32 : 64, 32,
+                         true))
         return POETX_ERR_CUDA;
-      if (f32_out)
-        POETX_TRY((gemm<true, true, EPI_STORE, true>(mp, h, s)));
+    }
+    if (pl.f32)
+      POETX_TRY((gemm<false, true>(mp, used > 1 ? mw : mp, h, s)));
+    else
+      POETX_TRY((gemm<false, false>(mp, used > 1 ? mw : mp, h, s)));
+    if (c.dx && pl.splits > 1) {
+      const long long quads = (long long)rows * c.D / 4;
+      const float* pp = reinterpret_cast<const float*>(w + pl.dxp);
+      const long long stride = (long long)c_rows * c.D;
+      if (pl.f32)
+        POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, dim3(grid_for(quads, 256)), dim3(256), 0, s,
+                                  pp, pl.splits, stride, quads, reinterpret_cast<float*>(dxr)));
       else
-        POETX_TRY((gemm<true, true, EPI_STORE, false>(mp, h, s)));
+        POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, dim3(grid_for(quads, 256)),
+                                  dim3(256), 0, s, pp, pl.splits, stride, quads,
+                                  reinterpret_cast<__nv_bfloat16*>(dxr)));
+      POETX_CUDA_TRY(cudaGetLastError());
+      after_launch(s, ST_HEAD_ROW);
     }
   }
   return POETX_OK;

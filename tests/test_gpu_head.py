@@ -213,12 +213,13 @@ def _torch64(x, W, t, g):
     return {"loss": loss, "lse": lse, "dx": dz @ W, "dW": dz.T @ x}
 
 
+@pytest.mark.parametrize("N", [4500, 9500])
 @pytest.mark.parametrize("acc", [None, 0.001])
-def test_ce_in_pieces_of_rows(P, acc):
-    """More rows than one piece holds (about 1 GB of 16-bit values): dW is the sum over the pieces,
-    rounded once."""
+def test_ce_in_pieces_of_rows(P, acc, N):
+    """Many rows, and more than one piece holds (about 2 GB of 16-bit values): dW is the sum over the
+    pieces, rounded once."""
     r = torch.Generator(device=DEV).manual_seed(3)
-    N, V, D = 4500, 128001, 64
+    V, D = 128001, 64
     W = (torch.randn(V, D, generator=r, device=DEV) / 8).bfloat16()
     x = torch.randn(N, D, generator=r, device=DEV).bfloat16()
     t = torch.randint(0, V, (N,), generator=r, device=DEV).int()
