@@ -55,10 +55,10 @@ constexpr uint32_t kABytes = BM * BK * 2;
 constexpr uint32_t kBBytes = BN / 2 * BK * 2;
 constexpr uint32_t kStageBytes = kABytes + kBBytes;  // 32 KB per CTA
 constexpr uint32_t kStgBytes = 32 * 128;             // one epilogue warp's box: 32 rows of 128 bytes
-// Tiles of a raster band: the pairs in flight then cover about 8 x 9 tiles, so that each operand stripe
-// is shared by many of them, and the band's stripes (16 MB at K = 4096) stay in L2 while the other
-// operand streams past.  Whole columns of tiles instead: 8192 x 128256 x 4096 read 14 GB for dx.
-constexpr int kBand = 8;
+// Tiles of a raster band: the operand stripes of a band (32 MB at K = 4096) stay in L2 while the other
+// operand streams past.  Bands of 4, 8, 16 and 32 at 8192 x 128256 x 4096 with gradients: 17.7, 17.1,
+// 16.9 and 17.3 ms.
+constexpr int kBand = 16;
 constexpr int kGemmSmem = kStages * kStageBytes + kEpiWarps * kStgBytes + 1024 + 512;
 static_assert(kGemmSmem <= 227 * 1024, "head products: shared memory");
 constexpr int kMaxSegs = 6;
@@ -490,14 +490,246 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   }
 }
 
+// ---------------------------------------------------------------- few rows, loss alone
+// The logits' product for at most 128 rows without gradients (a next token's score, a few sequences'
+// ends): bound by reading W once, so the roles are swapped.  W is the 128-row operand (one CTA, tiles
+// of `height` vocabulary rows, chosen so that every SM gets the same number of them), the NT (16 to
+// 128) padded tokens are the columns, and nearly all of the shared memory is a ring of W tiles in
+// flight.  A warp of the epilogue holds 32 vocabulary rows: it takes the targets out, turns its
+// 32 x NT logits over through shared memory and leaves one (max, sum) per token.
+struct HeadScore {
+  int tiles, height;
+  int V, rows, num_kb, chunk, stages;
+  float scale2;
+  float2* part;            // [rows][4 tiles]
+  const int32_t* ucol;     // [rows][K] the rows' distinct target columns
+  const uint16_t* gstart;  // [rows][tiles + 1] first of them in each tile; NULL: K = 1
+  int K;
+  float* tl;               // [rows][K]
+  int* err;
+  unsigned long long limit_ns;
+};
+constexpr int kScoreRows = 128;       // rows at most
+constexpr int kScoreThreads = 64 + 128;
+constexpr int kScoreRing = 12;        // stages at most
+constexpr int kScoreSmem = 220 * 1024;
+constexpr int score_turn_bytes(int NT) { return 4 * 32 * (NT + 1) * 4; }
+constexpr int score_stage_bytes(int NT) { return kABytes + NT * BK * 2; }
+
+template <int NT>
+__global__ void __launch_bounds__(kScoreThreads, 1)
+    head_score_kernel(const __grid_constant__ CUtensorMap mW, const __grid_constant__ CUtensorMap mx,
+                      const HeadScore p) {
+  constexpr uint32_t IDESC = make_idesc(BM, NT, false, false);
+  constexpr uint32_t TMEM_COLS = 2 * NT;
+  constexpr uint32_t STAGE = score_stage_bytes(NT);
+  constexpr int TOK = (NT + 31) / 32;  // tokens a lane looks after
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  float* turn = reinterpret_cast<float*>(smem + p.stages * STAGE);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * STAGE + (score_turn_bytes(NT) + 15) / 16 * 16);
+  uint64_t* empty = full + kScoreRing;
+  uint64_t* tfull = empty + kScoreRing;
+  uint64_t* tempty = tfull + 2;
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_trigger();
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < p.stages; ++s) {
+      mbar_init(&full[s], 1);
+      mbar_init(&empty[s], 1);
+    }
+    for (int a = 0; a < 2; ++a) {
+      mbar_init(&tfull[a], 1);
+      mbar_init(&tempty[a], 4);
+    }
+    *abort_flag = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&mW);
+    tma_prefetch_desc(&mx);
+  }
+  if (warp == 1) {
+    tmem_alloc(tmem_slot, TMEM_COLS);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem_base = *tmem_slot;
+  const uint32_t smem_base = smem_u32(smem);
+  pdl_wait();
+  auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
+    if (mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag || !mbar_wait_bounded(bar, parity, p.err, p.limit_ns, site)) {
+      *abort_flag = 1;
+      return false;
+    }
+    return true;
+  };
+  int s = 0;
+  uint32_t ph = 0;
+  auto next = [&]() {
+    if (++s == p.stages) {
+      s = 0;
+      ph ^= 1;
+    }
+  };
+  if (warp == 0 && lane == 0) {
+    const uint32_t bytes = (uint32_t)(p.height + NT) * BK * 2;
+    int issued = 0;
+    bool ok = true;
+    for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x)
+      for (int kb = 0; kb < p.num_kb; ++kb, next(), ++issued) {
+        if (!wait(&empty[s], ph ^ 1, kSite + __LINE__)) {
+          ok = false;
+          break;
+        }
+        uint8_t* sa = smem + s * STAGE;
+        mbar_arrive_expect_tx(&full[s], bytes);
+        tma_load_2d(sa, &mW, &full[s], kb * BK, t * p.height);
+        tma_load_2d(sa + kABytes, &mx, &full[s], kb * BK, 0);
+      }
+    for (int j = issued - 1; j >= 0 && j >= issued - p.stages; --j)  // every copy has landed
+      mbar_wait_bounded(&full[j % p.stages], (uint32_t)((j / p.stages) & 1), p.err, p.limit_ns,
+                        kSite + __LINE__);
+  } else if (warp == 1 && lane == 0) {
+    Ring<2> acc;
+    bool any = false, ok = true;
+    for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x)
+      for (int kb0 = 0; kb0 < p.num_kb && ok; kb0 += p.chunk, acc.next()) {
+        if (!wait(&tempty[acc.s], acc.ph ^ 1, kSite + __LINE__)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t d = tmem_base + (uint32_t)(acc.s * NT);
+        const int blocks = min(p.num_kb - kb0, p.chunk);
+        for (int j = 0; j < blocks; ++j, next()) {
+          if (!wait(&full[s], ph, kSite + __LINE__)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint32_t a_base = smem_base + s * STAGE;
+          const uint64_t ad = tile_desc<false>(a_base), bd = tile_desc<false>(a_base + kABytes);
+#pragma unroll
+          for (int k = 0; k < BK / 16; ++k)
+            umma_bf16(d, ad + k * 2, bd + k * 2, IDESC, (j | k) != 0);
+          umma_commit(&empty[s]);
+        }
+        umma_commit(&tfull[acc.s]);
+        any = true;
+      }
+    if (any) {
+      const int last = acc.s ^ 1;
+      mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns,
+                        kSite + __LINE__);
+    }
+  } else if (warp >= 2) {
+    const int q = warp & 3;
+    float* tw = turn + q * 32 * (NT + 1);
+    const float ninf = __int_as_float(0xff800000);
+    Ring<2> acc;
+    bool ok = true;
+    for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
+      const int v0 = t * p.height, mine = q * 32 + lane;  // the lane's vocabulary row in the tile
+      const int vrow = mine < p.height && v0 + mine < p.V ? v0 + mine : -1;
+      // targets of the lane's tokens in this tile (read ahead of the wait)
+      int u0[TOK], u1[TOK];
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        const int c = lane + 32 * j;
+        u0[j] = u1[j] = 0;
+        if (c < p.rows) {
+          if (p.gstart) {
+            const uint16_t* gs = p.gstart + (long long)c * (p.tiles + 1) + t;
+            u0[j] = gs[0];
+            u1[j] = gs[1];
+          } else {
+            const int tc = p.ucol[c];
+            u1[j] = tc >= v0 && tc < min(v0 + p.height, p.V);
+          }
+        }
+      }
+      float v[NT];
+      for (int kb0 = 0; kb0 < p.num_kb; kb0 += p.chunk, acc.next()) {
+        const bool got = wait(&tfull[acc.s], acc.ph, kSite + __LINE__);
+        if (!__all_sync(0xffffffffu, got)) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * NT);
+#pragma unroll
+        for (int j = 0; j < NT; j += 16) {
+          uint32_t r[16];
+          tmem_ld_32x32b_x16(ta + j, r);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < 16; ++i)
+            v[j + i] = kb0 == 0 ? __uint_as_float(r[i]) : v[j + i] + __uint_as_float(r[i]);
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[acc.s]);
+      }
+      if (!ok) break;
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, u0[j] < u1[j]);
+#pragma unroll
+        for (int i = 0; i < 32 && 32 * j + i < NT; ++i)
+          if (hit >> i & 1u) {
+            const int c = 32 * j + i;
+            const int b = __shfl_sync(0xffffffffu, u0[j], i), e = __shfl_sync(0xffffffffu, u1[j], i);
+            bool out = false;
+            for (int u = b; u < e; ++u)
+              if (p.ucol[(long long)c * p.K + u] == vrow) {
+                p.tl[(long long)c * p.K + u] = v[c];
+                out = true;
+              }
+            if (out) v[c] = ninf;
+          }
+      }
+#pragma unroll
+      for (int c = 0; c < NT; ++c) tw[lane * (NT + 1) + c] = vrow >= 0 ? v[c] * p.scale2 : ninf;
+      __syncwarp();
+#pragma unroll
+      for (int j = 0; j < TOK; ++j) {
+        const int c = lane + 32 * j;
+        if (c < p.rows) {
+          float m = ninf;
+#pragma unroll
+          for (int r = 0; r < 32; ++r) m = fmaxf(m, tw[r * (NT + 1) + c]);
+          const float off = m == ninf ? 0.f : m;
+          float sum = 0.f;
+#pragma unroll
+          for (int r = 0; r < 32; ++r) sum += ex2(tw[r * (NT + 1) + c] - off);
+          p.part[(long long)c * (4 * p.tiles) + 4 * t + q] = make_float2(m, sum);
+        }
+      }
+      __syncwarp();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    tmem_dealloc(tmem_base, TMEM_COLS);
+  }
+}
+
 // ---------------------------------------------------------------- CUDA-core kernels
 constexpr uint16_t kNoSlot = 0xffff;
 
 // A row's K target columns: slot[k] = place of idx[k] among the row's distinct columns in ascending
 // order (kNoSlot for an absent entry or one beyond the vocabulary), ucol = those columns, gstart =
-// the first of them in each group of 128.  By ranks: K is at most a thousand.
+// the first of them in each group of `width` columns.  By ranks: K is at most a thousand.
 __global__ void __launch_bounds__(256)
-    head_targets_kernel(const int32_t* __restrict__ idx, int K, int V, int groups,
+    head_targets_kernel(const int32_t* __restrict__ idx, int K, int V, int groups, int width,
                         uint16_t* __restrict__ slot, int32_t* __restrict__ ucol,
                         uint16_t* __restrict__ gstart) {
   extern __shared__ int tsm[];
@@ -535,7 +767,7 @@ __global__ void __launch_bounds__(256)
   const int n = nu;
   uint16_t* gs = gstart + row * (groups + 1);
   for (int u = t; u <= n; u += 256) {  // groups after the previous column's, up to this one's
-    const int lo = u ? us[u - 1] / kGroup + 1 : 0, hi = u < n ? us[u] / kGroup : groups;
+    const int lo = u ? us[u - 1] / width + 1 : 0, hi = u < n ? us[u] / width : groups;
     for (int g = lo; g <= hi; ++g) gs[g] = (uint16_t)u;
     if (u < n) ucol[row * K + u] = us[u];
   }
@@ -597,8 +829,8 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
 template <bool F32>
 __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) {
   extern __shared__ float sm[];
-  float* fac = sm;            // [groups] maximum, then factor of each group
-  float* z2 = fac + p.groups;  // [K] the distinct targets' logits in log2 units
+  float* fac = sm;            // [groups] factor of each group (with e)
+  float* z2 = fac + (p.e ? p.groups : 0);  // [K] the distinct targets' logits in log2 units
   float* qs = z2 + p.K;       // [K] their weights q
   float* qk = qs + p.K;       // [K] the entries' weights
   __shared__ float red[kRowThreads / 32];
@@ -630,10 +862,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   // log-sum-exp in log2 units: the groups leave the targets out
   const float2* part = p.part + row * p.groups;
   float m = zm;
-  for (int g = t; g < p.groups; g += kRowThreads) {
-    fac[g] = part[g].x;
-    m = fmaxf(m, fac[g]);
-  }
+  for (int g = t; g < p.groups; g += kRowThreads) m = fmaxf(m, part[g].x);
   m = block_max(m, red);
   const float off = m == ninf ? 0.f : m;
   // the largest target on its own (the first of equals), all others with the groups
@@ -642,7 +871,10 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     if (z2[u] == zm) um = fminf(um, (float)u);
   const int umax = (int)-block_max(-um, red);
   float s = 0.f;
-  for (int g = t; g < p.groups; g += kRowThreads) s += part[g].y * exp2f(fac[g] - off);
+  for (int g = t; g < p.groups; g += kRowThreads) {
+    const float2 w = part[g];
+    s += w.y * exp2f(w.x - off);
+  }
   for (int u = t; u < nu; u += kRowThreads)
     if (u != umax) s += exp2f(z2[u] - off);
   const float others = block_sum(s, red);
@@ -702,25 +934,36 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   const bool live = some > 0.f && !bad;
   const float gT = live ? p.dloss[row] / *p.unit : 0.f;
   const float coef = gT * weight;
-  for (int g = t; g < p.groups; g += kRowThreads) fac[g] = coef * exp2f(fac[g] - lse2);
+  for (int g = t; g < p.groups; g += kRowThreads) fac[g] = coef * exp2f(part[g].x - lse2);
   __syncthreads();
   if (!F32) {
     uint4* er = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e) + row * p.pitch);
-    for (long long i = t; i < p.pitch / 8; i += kRowThreads) {
-      uint4 o = make_uint4(0u, 0u, 0u, 0u);
-      if (live) {
-        const uint4 w = er[i];
-        const float f = fac[i / (kGroup / 8)];
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-        uint32_t r[4];
+    const int n = (int)(p.pitch / 8);
+    constexpr int U = 4;  // loads in flight per thread
+    for (int i0 = t; i0 < n; i0 += U * kRowThreads) {
+      uint4 w[U];
+      if (live)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-          r[j] = pack_bf16x2(v.x * f, v.y * f);
+        for (int k = 0; k < U; ++k)
+          if (i0 + k * kRowThreads < n) w[k] = er[i0 + k * kRowThreads];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * kRowThreads;
+        if (i >= n) break;
+        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        if (live) {
+          const float f = fac[i / (kGroup / 8)];
+          const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+          uint32_t r[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            r[j] = pack_bf16x2(v.x * f, v.y * f);
+          }
+          o = make_uint4(r[0], r[1], r[2], r[3]);
         }
-        o = make_uint4(r[0], r[1], r[2], r[3]);
+        er[i] = o;
       }
-      er[i] = o;
     }
   } else {
     const float4* er = reinterpret_cast<const float4*>(static_cast<float*>(p.e) + row * p.pitch);
@@ -818,6 +1061,26 @@ unsigned grid_for(long long items, int threads) {
   return (unsigned)(b < 1 ? 1 : b);
 }
 
+template <int NT>
+poetx_status score(const CUtensorMap& mW, const CUtensorMap& mx, HeadScore p, cudaStream_t s) {
+  auto k = head_score_kernel<NT>;
+  static std::once_flag once;
+  static cudaError_t attr_err = cudaSuccess;
+  std::call_once(once, [&] {
+    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
+  });
+  POETX_CUDA_TRY(attr_err);
+  p.stages = (kScoreSmem - 1024 - 512 - score_turn_bytes(NT)) / score_stage_bytes(NT);
+  if (p.stages > kScoreRing) p.stages = kScoreRing;
+  p.err = device_error_word();
+  p.limit_ns = kWaitLimitNs;
+  const int grid = p.tiles < sm_count() ? p.tiles : sm_count();
+  POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kScoreThreads), kScoreSmem, s, mW, mx, p));
+  POETX_CUDA_TRY(cudaGetLastError());
+  after_launch(s, ST_HEAD_GEMM);
+  return POETX_OK;
+}
+
 // Co-resident CTA pairs of a GEMM kernel (one CTA per SM).
 template <bool LSE, bool F32>
 cudaError_t gemm_pairs(int* pairs) {
@@ -911,6 +1174,7 @@ struct Plan {
   long long rows;    // rows of a piece
   int pieces;
   int splits;        // K splits of dx
+  int height, tiles;  // few rows, loss alone: vocabulary rows of a tile and tiles (else 0)
   // workspace offsets
   size_t unit, part, tl, ucol, slot, gstart, e, dz, xs, ws, acc, dxp, bytes;
 };
@@ -922,6 +1186,15 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   o->grads = dx || dW;
   o->Vp = (long long)align_up((size_t)V, 64);
   o->groups = ceil_div(V, kGroup);
+  o->height = o->tiles = 0;
+  if (!o->f32 && !o->grads && N <= kScoreRows) {
+    // every SM the same number of tiles, of at most 128 rows; no lower than 16
+    const int sms = sm_count(), each = ceil_div(V, (long long)sms * BM);
+    o->height = ceil_div(V, (long long)sms * each);
+    if (o->height < 16) o->height = 16;
+    o->tiles = ceil_div(V, o->height);
+    o->groups = 4 * o->tiles;
+  }
   const size_t row_bytes = (o->grads ? (size_t)o->Vp * (o->f32 ? 10 : 2) : 0) +
                            (size_t)o->groups * 8 * (o->grads ? 1 : 4);
   const long long n = N > 0 ? N : 1;
@@ -950,7 +1223,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   // the sorted target lists of a distillation (a call with K = 1 may be either: both fit)
   o->ucol = take(R * K * 4);
   o->slot = take(R * K * 2);
-  o->gstart = take(R * (o->groups + 1) * 2);
+  o->gstart = take(R * ((o->tiles ? o->tiles : o->groups) + 1) * 2);
   o->e = o->grads ? take(R * o->Vp * (o->f32 ? 4 : 2)) : 0;
   o->dz = o->f32 && o->grads ? take(3 * align_up(R * o->Vp * 2, 1024)) : o->e;
   o->xs = o->f32 ? take(3 * align_up(R * D * 2, 1024)) : 0;
@@ -1027,7 +1300,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
   if (!c.x || !c.W || !c.idx || !c.loss || !c.ws || (pl.grads && !c.dloss)) return POETX_ERR_ARG;
   if (c.ws_bytes < pl.bytes) return POETX_ERR_WORKSPACE;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
-  const size_t row_smem = (size_t)pl.groups * 4 + (size_t)c.K * 12;
+  const size_t row_smem = (pl.grads ? (size_t)pl.groups * 4 : 0) + (size_t)c.K * 12;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
@@ -1068,45 +1341,72 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       int32_t* u = reinterpret_cast<int32_t*>(w + pl.ucol);
       gstart = reinterpret_cast<uint16_t*>(w + pl.gstart);
       POETX_CUDA_TRY(launch_pdl(head_targets_kernel, dim3(rows), dim3(256), (size_t)c.K * 12, s, idx,
-                                c.K, c.V, pl.groups, slot, u, gstart));
+                                c.K, c.V, pl.tiles ? pl.tiles : pl.groups,
+                                pl.tiles ? pl.height : kGroup, slot, u, gstart));
       POETX_CUDA_TRY(cudaGetLastError());
       after_launch(s, ST_HEAD_ROW);
       ucol = u;
     }
     // the logits' product
     HeadMaps mp, mw;
-    HeadGemm g{};
-    set_segs(&g, pl.f32, true);
-    for (int i = 0; i < np; ++i)
-      if (!bf16_map(&mp.a[i], xp + i * x_step, c.D, rows, 64, 128) ||
-          !bf16_map(&mp.b[i], wp + i * w_step, c.D, c.V, 64, 128))
+    if (pl.tiles) {
+      const int nt = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
+      HeadScore h{};
+      h.tiles = pl.tiles;
+      h.height = pl.height;
+      h.V = c.V;
+      h.rows = rows;
+      h.num_kb = ceil_div(c.D, BK);
+      h.chunk = 16;
+      h.scale2 = kLog2e / c.T;
+      h.part = part;
+      h.ucol = ucol;
+      h.gstart = gstart;
+      h.K = c.K;
+      h.tl = tl;
+      if (!bf16_map(&mp.a[0], wp, c.D, c.V, 64, pl.height) ||
+          !bf16_map(&mp.b[0], xp, c.D, rows, 64, nt))
         return POETX_ERR_CUDA;
-    Product& lg = g.prod[0];
-    lg.tiles_m = ceil_div(rows, 2 * BM);
-    lg.tiles_n = ceil_div(c.V, BN);
-    lg.num_tiles = lg.tiles_m * lg.tiles_n;
-    lg.num_kb = lg.kb_split = ceil_div(c.D, BK);
-    lg.M = rows;
-    lg.N = c.V;
-    lg.n_store = (int)pl.Vp;  // columns V .. Vp - 1 are stored as zeros
-    g.scale2 = kLog2e / c.T;
-    g.part = part;
-    g.groups = pl.groups;
-    g.ucol = ucol;
-    g.gstart = gstart;
-    g.K = c.K;
-    g.tl = tl;
-    g.store = pl.grads;
-    g.dloss = c.dloss ? c.dloss + r0 : nullptr;
-    g.unit = unit;
-    if (pl.grads && !encode_tma_2d(&mp.c, w + pl.e, pl.f32 ? TMA_F32 : TMA_BF16, pl.Vp, rows, pl.Vp,
-                                   pl.f32 ? 32 : 64, 32, true))
-      return POETX_ERR_CUDA;
-    if (!pl.grads) mp.c = mp.a[0];
-    if (pl.f32)
-      POETX_TRY((gemm<true, true>(mp, mp, g, s)));
-    else
-      POETX_TRY((gemm<true, false>(mp, mp, g, s)));
+      switch (nt) {
+        case 16: POETX_TRY(score<16>(mp.a[0], mp.b[0], h, s)); break;
+        case 32: POETX_TRY(score<32>(mp.a[0], mp.b[0], h, s)); break;
+        case 64: POETX_TRY(score<64>(mp.a[0], mp.b[0], h, s)); break;
+        default: POETX_TRY(score<128>(mp.a[0], mp.b[0], h, s)); break;
+      }
+    } else {
+      HeadGemm g{};
+      set_segs(&g, pl.f32, true);
+      for (int i = 0; i < np; ++i)
+        if (!bf16_map(&mp.a[i], xp + i * x_step, c.D, rows, 64, 128) ||
+            !bf16_map(&mp.b[i], wp + i * w_step, c.D, c.V, 64, 128))
+          return POETX_ERR_CUDA;
+      Product& lg = g.prod[0];
+      lg.tiles_m = ceil_div(rows, 2 * BM);
+      lg.tiles_n = ceil_div(c.V, BN);
+      lg.num_tiles = lg.tiles_m * lg.tiles_n;
+      lg.num_kb = lg.kb_split = ceil_div(c.D, BK);
+      lg.M = rows;
+      lg.N = c.V;
+      lg.n_store = (int)pl.Vp;  // columns V .. Vp - 1 are stored as zeros
+      g.scale2 = kLog2e / c.T;
+      g.part = part;
+      g.groups = pl.groups;
+      g.ucol = ucol;
+      g.gstart = gstart;
+      g.K = c.K;
+      g.tl = tl;
+      g.store = pl.grads;
+      g.dloss = c.dloss ? c.dloss + r0 : nullptr;
+      g.unit = unit;
+      if (pl.grads && !encode_tma_2d(&mp.c, w + pl.e, pl.f32 ? TMA_F32 : TMA_BF16, pl.Vp, rows, pl.Vp,
+                                     pl.f32 ? 32 : 64, 32, true))
+        return POETX_ERR_CUDA;
+      if (!pl.grads) mp.c = mp.a[0];
+      if (pl.f32)
+        POETX_TRY((gemm<true, true>(mp, mp, g, s)));
+      else
+        POETX_TRY((gemm<true, false>(mp, mp, g, s)));
+    }
     // rows: lse, loss, dz
     RowArgs ra{};
     ra.V = c.V;

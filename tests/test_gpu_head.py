@@ -107,6 +107,22 @@ def test_ce_parts_agree(P, dt):
             assert torch.equal(got[k], full[k]), (k, dx, dW)
 
 
+# one row to a full 128, one tile to several per SM, tiles of 16 rows and of odd heights, K past one
+# accumulator hand-over
+@pytest.mark.parametrize("N,V,D", [(1, 5, 64), (1, 32000, 2048), (2, 1, 8), (16, 333, 200),
+                                   (17, 2433, 1032), (31, 40001, 128), (33, 5003, 72),
+                                   (64, 50257, 64), (65, 19457, 2056), (128, 3000, 1600)])
+def test_ce_loss_of_few_rows(P, N, V, D):
+    x, W, t, g = _inputs(N, V, D, "bf16", N + V + D)
+    t[N // 2] = -1 if N > 2 else t[N // 2]
+    got = _ce(P, x, W, t, g, dx=False, dW=False)
+    ref = H.head_ce(host(x), host(W), t)
+    if V == 1:
+        assert np.abs(host(got["loss"])).max() <= 1e-5 * np.abs(ref["lse"]).max()
+        return
+    _near(got, ref, "bf16")
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_ce_accumulates_dW(P, dt):
     x, W, t, g = _inputs(150, 500, 128, dt, 7)
@@ -168,8 +184,11 @@ def test_distill(P, N, V, D, K, T, dt):
     u = r.uniform(0, 10, (N, K)).astype(np.float32)
     _near(_distill(P, x, W, idx, u, g, T), H.head_distill(host(x), host(W), idx, u, g, T), dt)
     a = _distill(P, x, W, idx, u, g, T, grads=False)
-    b = _distill(P, x, W, idx, u, g, T)
-    assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["lse"], b["lse"])
+    if dt == "f32" or N > 128:
+        b = _distill(P, x, W, idx, u, g, T)
+        assert torch.equal(a["loss"], b["loss"]) and torch.equal(a["lse"], b["lse"])
+    else:  # few rows, loss alone: a product of its own
+        _near(a, H.head_distill(host(x), host(W), idx, u, None, T), dt)
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
