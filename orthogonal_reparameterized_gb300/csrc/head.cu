@@ -677,24 +677,21 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       }
       if (!ok) break;
 #pragma unroll
-      for (int j = 0; j < TOK; ++j) {
-        const uint32_t hit = __ballot_sync(0xffffffffu, u0[j] < u1[j]);
+      for (int c = 0; c < NT; ++c) tw[lane * (NT + 1) + c] = vrow >= 0 ? v[c] : ninf;
 #pragma unroll
-        for (int i = 0; i < 32 && 32 * j + i < NT; ++i)
-          if (hit >> i & 1u) {
-            const int c = 32 * j + i;
-            const int b = __shfl_sync(0xffffffffu, u0[j], i), e = __shfl_sync(0xffffffffu, u1[j], i);
-            bool out = false;
-            for (int u = b; u < e; ++u)
-              if (p.ucol[(long long)c * p.K + u] == vrow) {
-                p.tl[(long long)c * p.K + u] = v[c];
-                out = true;
-              }
-            if (out) v[c] = ninf;
-          }
+      for (int j = 0; j < TOK; ++j) {  // the targets leave through their vocabulary row's lane
+        uint32_t hit = __ballot_sync(0xffffffffu, u0[j] < u1[j]);
+        while (hit) {
+          const int i = __ffs(hit) - 1, c = 32 * j + i;
+          hit &= hit - 1;
+          const int b = __shfl_sync(0xffffffffu, u0[j], i), e = __shfl_sync(0xffffffffu, u1[j], i);
+          for (int u = b; u < e; ++u)
+            if (p.ucol[(long long)c * p.K + u] == vrow) {
+              p.tl[(long long)c * p.K + u] = tw[lane * (NT + 1) + c];
+              tw[lane * (NT + 1) + c] = ninf;
+            }
+        }
       }
-#pragma unroll
-      for (int c = 0; c < NT; ++c) tw[lane * (NT + 1) + c] = vrow >= 0 ? v[c] * p.scale2 : ninf;
       __syncwarp();
 #pragma unroll
       for (int j = 0; j < TOK; ++j) {
@@ -703,10 +700,11 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           float m = ninf;
 #pragma unroll
           for (int r = 0; r < 32; ++r) m = fmaxf(m, tw[r * (NT + 1) + c]);
+          m *= p.scale2;
           const float off = m == ninf ? 0.f : m;
           float sum = 0.f;
 #pragma unroll
-          for (int r = 0; r < 32; ++r) sum += ex2(tw[r * (NT + 1) + c] - off);
+          for (int r = 0; r < 32; ++r) sum += ex2(fmaf(tw[r * (NT + 1) + c], p.scale2, -off));
           p.part[(long long)c * (4 * p.tiles) + 4 * t + q] = make_float2(m, sum);
         }
       }
@@ -794,27 +792,28 @@ struct RowArgs {
 constexpr int kRowThreads = 256;
 constexpr float kLn2 = 0.69314718055994530942f, kLog2e = 1.44269504088896340736f;
 
-__device__ __forceinline__ float block_sum(float v, float* red) {
+// Two sums (maxima) over the CTA, with one pair of barriers.
+template <bool MAX>
+__device__ __forceinline__ void block_reduce2(float& a, float& b, float2* red) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+  for (int o = 16; o; o >>= 1) {
+    const float x = __shfl_xor_sync(0xffffffffu, a, o), y = __shfl_xor_sync(0xffffffffu, b, o);
+    a = MAX ? fmaxf(a, x) : a + x;
+    b = MAX ? fmaxf(b, y) : b + y;
+  }
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = make_float2(a, b);
   __syncthreads();
-  v = 0.f;
+  float2 w[kRowThreads / 32];
 #pragma unroll
-  for (int w = 0; w < kRowThreads / 32; ++w) v += red[w];
-  return v;
-}
-__device__ __forceinline__ float block_max(float v, float* red) {
+  for (int i = 0; i < kRowThreads / 32; ++i) w[i] = red[i];
+  a = w[0].x;
+  b = w[0].y;
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = red[0];
-#pragma unroll
-  for (int w = 1; w < kRowThreads / 32; ++w) v = fmaxf(v, red[w]);
-  return v;
+  for (int i = 1; i < kRowThreads / 32; ++i) {
+    a = MAX ? fmaxf(a, w[i].x) : a + w[i].x;
+    b = MAX ? fmaxf(b, w[i].y) : b + w[i].y;
+  }
 }
 
 __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
@@ -833,7 +832,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   float* z2 = fac + (p.e ? p.groups : 0);  // [K] the distinct targets' logits in log2 units
   float* qs = z2 + p.K;       // [K] their weights q
   float* qk = qs + p.K;       // [K] the entries' weights
-  __shared__ float red[kRowThreads / 32];
+  __shared__ float2 red[kRowThreads / 32];
   pdl_trigger();
   pdl_wait();
   const long long row = blockIdx.x;
@@ -843,41 +842,62 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   const int32_t* idx = p.idx + row * p.K;
   const uint16_t* slot = p.slot + row * p.K;
   const int32_t* ucol = p.ucol + row * p.K;
-  // the distinct targets: nu of them
-  float nbad = 0.f, top = -1.f;  // (slots are below 1024: exact in fp32)
-  for (int k = t; k < p.K; k += kRowThreads) {
-    const int c = idx[k];
-    nbad += c >= p.V ? 1.f : 0.f;
-    if (c >= 0 && c < p.V) top = fmaxf(top, p.tlogit ? (float)slot[k] : 0.f);
-  }
-  const bool bad = block_max(nbad, red) > 0.f;  // an index beyond the vocabulary
-  const int nu = (int)block_max(top, red) + 1;
-  float zm = ninf;
-  for (int u = t; u < nu; u += kRowThreads) {
-    z2[u] = p.tl[row * p.K + u] * scale2;
-    qs[u] = 0.f;
-    zm = fmaxf(zm, z2[u]);
-  }
-  zm = block_max(zm, red);
-  // log-sum-exp in log2 units: the groups leave the targets out
+  const float* u = p.tlogit ? p.tlogit + row * p.K : nullptr;
+  const float invT = 1.f / p.T;
   const float2* part = p.part + row * p.groups;
-  float m = zm;
+  float m = ninf;
   for (int g = t; g < p.groups; g += kRowThreads) m = fmaxf(m, part[g].x);
-  m = block_max(m, red);
+  // the distinct targets: nu of them
+  bool bad;  // an index beyond the vocabulary
+  int nu;
+  if (!u) {
+    const int c = idx[0];
+    bad = c >= p.V;
+    nu = c >= 0 && c < p.V;
+  } else {
+    float nbad = 0.f, top = -1.f;  // (slots are below 1024: exact in fp32)
+    for (int k = t; k < p.K; k += kRowThreads) {
+      const int c = idx[k];
+      if (c >= p.V) nbad = 1.f;
+      if (c >= 0 && c < p.V) top = fmaxf(top, (float)slot[k]);
+    }
+    block_reduce2<true>(nbad, top, red);
+    bad = nbad > 0.f;
+    nu = (int)top + 1;
+  }
+  float zm = ninf;
+  for (int v = t; v < nu; v += kRowThreads) {
+    z2[v] = p.tl[row * p.K + v] * scale2;
+    qs[v] = 1.f;
+    zm = fmaxf(zm, z2[v]);
+  }
+  // log-sum-exp in log2 units: the groups leave the targets out
+  block_reduce2<true>(zm, m, red);
+  m = fmaxf(m, zm);
   const float off = m == ninf ? 0.f : m;
   // the largest target on its own (the first of equals), all others with the groups
-  float um = 2048.f;
-  for (int u = t; u < nu; u += kRowThreads)
-    if (z2[u] == zm) um = fminf(um, (float)u);
-  const int umax = (int)-block_max(-um, red);
-  float s = 0.f;
+  int umax = 0;
+  float tm = ninf;  // the teacher's largest logit
+  if (u) {
+    float first = -2048.f;
+    for (int v = t; v < nu; v += kRowThreads)
+      if (z2[v] == zm) first = fmaxf(first, -(float)v);
+    for (int k = t; k < p.K; k += kRowThreads)
+      if (idx[k] >= 0) tm = fmaxf(tm, u[k] * invT);
+    block_reduce2<true>(first, tm, red);
+    umax = (int)-first;
+  }
+  float others = 0.f, us = 0.f;
   for (int g = t; g < p.groups; g += kRowThreads) {
     const float2 w = part[g];
-    s += w.y * exp2f(w.x - off);
+    others += w.y * exp2f(w.x - off);
   }
-  for (int u = t; u < nu; u += kRowThreads)
-    if (u != umax) s += exp2f(z2[u] - off);
-  const float others = block_sum(s, red);
+  for (int v = t; v < nu; v += kRowThreads)
+    if (v != umax) others += exp2f(z2[v] - off);
+  if (u && tm != ninf)
+    for (int k = t; k < p.K; k += kRowThreads)
+      if (idx[k] >= 0) us += expf(u[k] * invT - tm);
+  block_reduce2<false>(others, us, red);
   const float emax = nu ? exp2f(zm - off) : 0.f;
   const float total = others + emax;
   const float lse2 = off + log2f(total);
@@ -886,23 +906,12 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   const float lnp_max = sure ? -log1pf(others / emax) : (zm - lse2) * kLn2;
   float some, loss, weight;  // weight: of p in dz, before the upstream gradient
   float rest = 0.f;          // 1 - q of the largest target
-  if (!p.tlogit) {
+  if (!u) {
     some = nu ? 1.f : 0.f;
     loss = p.zl * lse * lse - lnp_max;
     weight = 1.f + 2.f * p.zl * lse;
-    if (t == 0) qs[0] = 1.f;
   } else {
-    const float* u = p.tlogit + row * p.K;
-    const float invT = 1.f / p.T;
-    float tm = ninf;
-    for (int k = t; k < p.K; k += kRowThreads)
-      if (idx[k] >= 0) tm = fmaxf(tm, u[k] * invT);
-    tm = block_max(tm, red);
     some = tm == ninf ? 0.f : 1.f;
-    float us = 0.f;
-    for (int k = t; k < p.K; k += kRowThreads)
-      if (idx[k] >= 0 && some > 0.f) us += expf(u[k] * invT - tm);
-    us = block_sum(us, red);
     const float lus = logf(us);
     float l = 0.f;
     for (int k = t; k < p.K; k += kRowThreads) {
@@ -915,11 +924,11 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
       }
       qk[k] = q;
     }
-    loss = block_sum(l, red) * p.T * p.T;
-    rest = block_sum(rest, red);
+    block_reduce2<false>(l, rest, red);
+    loss = l * p.T * p.T;
     weight = 1.f;
     // weights per distinct column, the entries added in their order
-    for (int v = t; v < nu; v += kRowThreads) {
+    for (int v = t; v < nu && p.e; v += kRowThreads) {
       float q = 0.f;
       for (int k = 0; k < p.K; ++k)
         if (slot[k] == v) q += qk[k];
@@ -990,7 +999,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     const float pv = exp2f(z2[u] - lse2);
     float dz;
     if (u == umax && sure)
-      dz = gT * ((weight - 1.f) * pv + ((p.tlogit ? rest : 0.f) - others / total));
+      dz = gT * ((weight - 1.f) * pv + (rest - others / total));
     else
       dz = coef * pv - gT * qs[u];
     const int c = ucol[u];
