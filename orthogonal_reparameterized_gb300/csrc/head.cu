@@ -233,8 +233,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
       const bool a_mn = !LSE && p.prod[c.which].a_mn;
       constexpr bool b_mn = !LSE;
       const int m0 = (2 * c.mi + crank) * BM, n0 = c.nt * BN + crank * (BN / 2);
-      for (int kb = c.kb0; kb < c.kb1 && ok; ++kb)
-        for (int sg = 0; sg < (F32 ? kMaxSegs : 1); ++sg, rg.next(), ++issued) {
+      for (int c0 = c.kb0; c0 < c.kb1 && ok; c0 += p.chunk) {
+        const int len = min(c.kb1 - c0, p.chunk);
+        int sg = 0, i = 0;  // fp32: a chunk's K blocks once per pair of pieces
+        for (int j = 0; j < len * (F32 ? kMaxSegs : 1); ++j, rg.next(), ++issued) {
           if (!ring_wait(&empty[rg.s], rg.ph ^ 1, abort_flag, p, kSite + __LINE__)) {
             ok = false;
             break;
@@ -243,7 +245,11 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           uint8_t* sb = sa + kABytes;
           const CUtensorMap* ma = &maps.a[F32 ? p.seg_a[sg] : 0];
           const CUtensorMap* mb = &maps.b[F32 ? p.seg_b[sg] : 0];
-          const int k = kb * BK;
+          const int k = (c0 + i) * BK;
+          if (++i == len) {
+            i = 0;
+            ++sg;
+          }
           if (crank == 0) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
           const uint32_t fb = full0 + rg.s * 8;
           if (!a_mn) {
@@ -259,6 +265,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             tma_load_2d_pair(sb + 8192, mb, fb, n0 + 64, k);
           }
         }
+      }
     }
     // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
     for (long long j = issued - 1; j >= 0 && j >= issued - kStages; --j)
@@ -1248,15 +1255,17 @@ bool bf16_map(CUtensorMap* m, const void* p, long long inner, long long outer, i
 }
 
 void set_segs(HeadGemm* g, bool f32, bool lse) {
-  // small pieces first, so that the accumulator is small while they are added
+  // small pieces first, so that the accumulator is small while they are added (a chunk runs pair by
+  // pair of pieces: the adds at full size are those of the last pair)
   static const int8_t a[kMaxSegs] = {1, 0, 2, 1, 0, 0}, b[kMaxSegs] = {1, 2, 0, 0, 1, 0};
   for (int i = 0; i < kMaxSegs; ++i) {
     g->seg_a[i] = a[i];
     g->seg_b[i] = b[i];
   }
-  // K of one accumulator: 64 per piece pair in fp32; in bf16 1024 for the logits (64 adds of 16
-  // products) and 4096 for the gradients, which are rounded to bf16 (256 adds: 1.5e-5)
-  g->chunk = f32 ? 1 : (lse ? 16 : 64);
+  // K of one accumulator: 256 in fp32 (16 adds of 16 products at full size; 64: a fifth slower); in
+  // bf16 1024 for the logits (64 adds) and 4096 for the gradients, which are rounded to bf16 (256
+  // adds: 1.5e-5)
+  g->chunk = f32 ? 4 : (lse ? 16 : 64);
 }
 
 struct HeadCall {
