@@ -53,6 +53,50 @@ __device__ __forceinline__ Vec<T, VEC> pack(const float (&f)[VEC]) {
   return o;
 }
 
+// Two fp32 operations per instruction.
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mul.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "mov.b64 z, {%6, %7};\n\tfma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 both(float v) { return make_float2(v, v); }
+template <typename T, int VEC>
+__device__ __forceinline__ void unpack2(const Vec<T, VEC>& a, float2 (&f)[VEC / 2]) {
+  float w[VEC];
+  unpack(a, w);
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) f[j] = make_float2(w[2 * j], w[2 * j + 1]);
+}
+template <typename T, int VEC>
+__device__ __forceinline__ Vec<T, VEC> pack2(const float2 (&f)[VEC / 2]) {
+  float w[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC / 2; ++j) {
+    w[2 * j] = f[j].x;
+    w[2 * j + 1] = f[j].y;
+  }
+  return pack<T, VEC>(w);
+}
+
 // Sum of s[0..NS) over the TPR threads of a row group; every thread gets it.  red: one slot set
 // per warp; two sets, used in turn, so that one barrier per call is enough.
 template <int TPR, int NS>
@@ -115,7 +159,7 @@ __global__ void __launch_bounds__(kThreads)
         s[0] += d * d;
       }
   group_sum<TPR>(s, red, 1);
-  const float rs = 1.f / sqrtf(s[0] / (float)D + eps);
+  const float rs = rsqrtf(s[0] / (float)D + eps);
   if (!live) return;
   if (t == 0) {
     if (mean) mean[row] = mu;
@@ -136,22 +180,22 @@ __global__ void __launch_bounds__(kThreads)
     }
 }
 
-// Many rows: persistent CTAs, a warp per row (lane l holds vectors l, l + 32, ...), gamma and beta
-// staged in shared memory once per CTA.  No barrier between rows, so the warps of an SM are at
-// different phases of load, sums and store.  Two CTAs per SM: 16 rows in flight (more registers
-// per thread, one CTA: 2.2 times as long at 8192 x 4096).
+// Many rows of up to 512 vectors: persistent CTAs, a warp per row (lane l holds vectors l, l + 32,
+// ...), gamma and beta staged in shared memory once per CTA.  No barrier between rows, so the warps of
+// an SM are at different phases of load, sums and store.  gamma and beta lie in planes of 16 bytes per
+// vector (plane k: elements 4 k .. 4 k + 3 of every vector), which a warp reads without conflicts.
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(kThreads, 2)
     layernorm_fwd_rows_kernel(const T* __restrict__ x, int N, int D, const float* __restrict__ gamma,
                               const float* __restrict__ beta, float eps, T* __restrict__ y,
                               float* __restrict__ mean, float* __restrict__ rstd) {
-  extern __shared__ float gb[];  // gamma [D], beta [D]
+  extern __shared__ float4 gb[];  // gamma's VEC / 4 planes of nvec, beta's
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31, nvec = D / VEC;
+  const int lane = threadIdx.x & 31, nvec = D / VEC, warps = (int)blockDim.x / 32;
   const float inv = 1.f / (float)D;
-  const long long step = (long long)gridDim.x * (kThreads / 32);
-  long long row = (long long)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5);
+  const long long step = (long long)gridDim.x * warps;
+  long long row = (long long)blockIdx.x * warps + (threadIdx.x >> 5);
   Vec<T, VEC> a[NV];
   auto load = [&](long long r) {
     const Vec<T, VEC>* xr = reinterpret_cast<const Vec<T, VEC>*>(x + r * D);
@@ -160,9 +204,10 @@ __global__ void __launch_bounds__(kThreads, 2)
       if (lane + 32 * i < nvec) a[i] = xr[lane + 32 * i];
   };
   if (row < N) load(row);  // in flight while gamma and beta are staged
-  for (int c = threadIdx.x; c < D; c += kThreads) {
-    gb[c] = gamma ? gamma[c] : 1.f;
-    gb[D + c] = beta ? beta[c] : 0.f;
+  for (int q = threadIdx.x; q < D / 4; q += blockDim.x) {  // quad q: vector q / (VEC / 4)
+    const int at = q % (VEC / 4) * nvec + q / (VEC / 4);
+    gb[at] = gamma ? reinterpret_cast<const float4*>(gamma)[q] : make_float4(1.f, 1.f, 1.f, 1.f);
+    gb[D / 4 + at] = beta ? reinterpret_cast<const float4*>(beta)[q] : make_float4(0.f, 0.f, 0.f, 0.f);
   }
   __syncthreads();
   for (; row < N; row += step) {
@@ -192,21 +237,26 @@ __global__ void __launch_bounds__(kThreads, 2)
       }
     s[0] = p[0] + p[1];
     group_sum<32>(s, nullptr, 0);
-    const float rs = 1.f / sqrtf(s[0] * inv + eps);
+    const float rs = rsqrtf(s[0] * inv + eps);
     if (lane == 0) {
       if (mean) mean[row] = mu;
       if (rstd) rstd[row] = rs;
     }
+    const float nmr = -mu * rs;
     Vec<T, VEC>* yr = reinterpret_cast<Vec<T, VEC>*>(y + row * D);
 #pragma unroll
     for (int i = 0; i < NV; ++i)
       if (lane + 32 * i < nvec) {
-        const Vec<float, VEC> g = reinterpret_cast<const Vec<float, VEC>*>(gb)[lane + 32 * i];
-        const Vec<float, VEC> b = reinterpret_cast<const Vec<float, VEC>*>(gb + D)[lane + 32 * i];
         float f[VEC];
         unpack(a[i], f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = fmaf((f[j] - mu) * rs, g.v[j], b.v[j]);
+        for (int k = 0; k < VEC / 4; ++k) {
+          const float4 g = gb[k * nvec + lane + 32 * i], b = gb[D / 4 + k * nvec + lane + 32 * i];
+          const float gv[4] = {g.x, g.y, g.z, g.w}, bv[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            f[4 * k + j] = fmaf(fmaf(f[4 * k + j], rs, nmr), gv[j], bv[j]);
+        }
         yr[lane + 32 * i] = pack<T, VEC>(f);
       }
     if (row + step < N) load(row + step);
@@ -235,7 +285,7 @@ __global__ void __launch_bounds__(kThreads)
     s[0] += d * d;
   }
   group_sum<kThreads>(s, red, 1);
-  const float rs = 1.f / sqrtf(s[0] / (float)D + eps);
+  const float rs = rsqrtf(s[0] / (float)D + eps);
   if (threadIdx.x == 0) {
     if (mean) mean[row] = mu;
     if (rstd) rstd[row] = rs;
@@ -338,32 +388,110 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// Backward of rows of 129 to 1024 16-byte vectors: one persistent CTA per SM of GROUPS thread groups,
-// each on rows of its own (while one waits at its barrier another computes).  A group's first thread
-// streams its rows of x and dy into the group's shared-memory ring by 1-D TMA bulk copies, so that
-// the next rows are in flight whatever the group does; the barrier that joins a row's two sums also
-// says that the row has been read, and its stage is refilled after it.  A thread keeps gamma and the
-// sums of dy h and dy of its NV vectors in registers over all rows.  At the end the groups' sums are
-// added through shared memory, so that there is one row of partials per SM.
+// The ring forms, for rows of 129 to 1024 16-byte vectors: one persistent CTA per SM of GROUPS thread
+// groups, each on rows of its own (while one waits at its barrier another computes).  A group's first
+// thread streams its rows into the group's shared-memory ring by 1-D TMA bulk copies, so that the
+// next rows are in flight whatever the group does; the barrier that joins a row's sums also says that
+// the row has been read, and its stage is refilled after it.  A thread owns NV vectors of every row
+// and keeps what belongs to their columns in registers over all rows.
 constexpr int kSite = 7 * 10000;
 constexpr int kRingThreads = 512;
 
+// Rows row0 + k stride (k < rows) of ARRAYS arrays, in the group's ring.
+template <typename T, int ARRAYS>
+struct RowRing {
+  const T* src[ARRAYS];
+  uint8_t* buf;      // [stages][ARRAYS][row]
+  uint64_t* full;    // [stages]
+  int stages, rows, D;
+  long long row0, stride;
+  int st = 0;        // stage and phase of the row being read
+  uint32_t ph = 0;
+
+  __device__ __forceinline__ uint32_t row_bytes() const { return (uint32_t)D * sizeof(T); }
+  __device__ __forceinline__ const uint8_t* stage() const {
+    return buf + (size_t)st * ARRAYS * row_bytes();
+  }
+  __device__ __forceinline__ void issue(int k, int s) {
+    const long long row = row0 + k * stride;
+    uint8_t* dst = buf + (size_t)s * ARRAYS * row_bytes();
+    mbar_arrive_expect_tx(&full[s], ARRAYS * row_bytes());
+#pragma unroll
+    for (int a = 0; a < ARRAYS; ++a)
+      bulk_load(dst + a * row_bytes(), src[a] + row * D, row_bytes(), &full[s]);
+  }
+  __device__ __forceinline__ void start() {
+    for (int k = 0; k < rows && k < stages; ++k) issue(k, k);
+  }
+  __device__ __forceinline__ int before() const { return st ? st - 1 : stages - 1; }
+  __device__ __forceinline__ void refill(int k, int s) {  // row k, in stage s, has been read by all
+    if (k + stages < rows) issue(k + stages, s);
+  }
+  __device__ __forceinline__ void next() {
+    if (++st == stages) {
+      st = 0;
+      ph ^= 1;
+    }
+  }
+  // no copy may be in flight when the CTA exits (passes at once but after a timeout)
+  __device__ __forceinline__ void drain(int* err, unsigned long long limit_ns) {
+    for (int k = rows > stages ? rows - stages : 0; k < rows; ++k)
+      mbar_wait_bounded(&full[k % stages], (uint32_t)((k / stages) & 1), err, limit_ns,
+                        kSite + __LINE__);
+  }
+};
+
+// Sum of v over the warps of a group (at most 16), through red; one barrier.
+__device__ __forceinline__ float2 ring_join(float2 v, float2* red, int warp, int lane, int warps,
+                                            int barrier, int threads) {
+#pragma unroll
+  for (int o = 16; o; o >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                            __shfl_xor_sync(0xffffffffu, v.y, o)));
+  if (lane == 0) red[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+  v = (lane & 15) < warps ? red[lane & 15] : make_float2(0.f, 0.f);
+#pragma unroll
+  for (int o = 8; o; o >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                            __shfl_xor_sync(0xffffffffu, v.y, o)));
+  return v;
+}
+
+__device__ __forceinline__ float4 ring_join4(float4 v, float4* red, int warp, int lane, int warps,
+                                             int barrier, int threads) {
+  auto step = [&](int o) {
+    const float2 a = add2(make_float2(v.x, v.y), make_float2(__shfl_xor_sync(0xffffffffu, v.x, o),
+                                                             __shfl_xor_sync(0xffffffffu, v.y, o)));
+    const float2 b = add2(make_float2(v.z, v.w), make_float2(__shfl_xor_sync(0xffffffffu, v.z, o),
+                                                             __shfl_xor_sync(0xffffffffu, v.w, o)));
+    v = make_float4(a.x, a.y, b.x, b.y);
+  };
+#pragma unroll
+  for (int o = 16; o; o >>= 1) step(o);
+  if (lane == 0) red[warp] = v;
+  asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(threads) : "memory");
+  v = (lane & 15) < warps ? red[lane & 15] : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int o = 8; o; o >>= 1) step(o);
+  return v;
+}
+
+// Forward: gamma and beta of the thread's columns in registers; two joins for two rows (the means,
+// then the squared deviations from them).
 template <typename T, int NV, int GROUPS>
 __global__ void __launch_bounds__(kRingThreads)
-    layernorm_bwd_ring_kernel(const T* __restrict__ x, const T* __restrict__ dy, int N, int D,
-                              const float* __restrict__ gamma, const float* __restrict__ mean,
-                              const float* __restrict__ rstd, T* __restrict__ dx,
-                              float* __restrict__ pg, float* __restrict__ pb, int stages, int* err,
-                              unsigned long long limit_ns) {
-  constexpr int VEC = 16 / sizeof(T);
-  constexpr int MAXW = kRingThreads / 32 / GROUPS;  // warps of a group
-  extern __shared__ __align__(128) uint8_t ring[];  // [GROUPS][stages][x row, dy row]
+    layernorm_fwd_ring_kernel(const T* __restrict__ x, int N, int D, const float* __restrict__ gamma,
+                              const float* __restrict__ beta, float eps, T* __restrict__ y,
+                              float* __restrict__ mean, float* __restrict__ rstd, int stages,
+                              int* err, unsigned long long limit_ns) {
+  constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+  extern __shared__ __align__(128) uint8_t ring_mem[];
   __shared__ uint64_t full[GROUPS][kMaxRing];
-  __shared__ float2 red[GROUPS][2][MAXW];
+  __shared__ float2 red[GROUPS][2][kRingThreads / 32 / GROUPS];
   const int threads = (int)blockDim.x / GROUPS, warps = threads / 32;
   const int grp = (int)threadIdx.x / threads, t = (int)threadIdx.x - grp * threads;
   const int warp = t >> 5, lane = t & 31;
-  const uint32_t row_bytes = (uint32_t)D * sizeof(T);
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int g = 0; g < GROUPS; ++g)
@@ -372,112 +500,217 @@ __global__ void __launch_bounds__(kRingThreads)
   }
   __syncthreads();
   pdl_wait();
-  // rows blockIdx.x + (k GROUPS + grp) gridDim.x, k = 0, 1, ...
   const long long row0 = blockIdx.x + (long long)grp * gridDim.x;
   const long long stride = (long long)gridDim.x * GROUPS;
   const int rows = row0 < N ? (int)((N - 1 - row0) / stride) + 1 : 0;
-  uint8_t* mine = ring + (size_t)grp * stages * 2 * row_bytes;
-  auto issue = [&](int k) {
-    const int st = k % stages;
-    const long long row = row0 + k * stride;
-    uint8_t* dst = mine + (size_t)st * 2 * row_bytes;
-    mbar_arrive_expect_tx(&full[grp][st], 2 * row_bytes);
-    bulk_load(dst, x + row * D, row_bytes, &full[grp][st]);
-    bulk_load(dst + row_bytes, dy + row * D, row_bytes, &full[grp][st]);
-  };
-  if (t == 0)
-    for (int k = 0; k < rows && k < stages; ++k) issue(k);
+  RowRing<T, 1> ring{{x}, ring_mem + (size_t)grp * stages * D * sizeof(T), full[grp], stages, rows, D,
+                     row0, stride};
+  if (t == 0) ring.start();
   const int nvec = D / VEC;
-  float ag[NV][VEC], ab[NV][VEC], gm[NV][VEC];
+  float2 gm[NV][H], bt[NV][H];
 #pragma unroll
   for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      ag[i][j] = ab[i][j] = 0.f;
-      const int v = t + i * threads;
-      gm[i][j] = v < nvec ? (gamma ? gamma[v * VEC + j] : 1.f) : 0.f;
+    for (int j = 0; j < H; ++j) {
+      const int c = (t + i * threads) * VEC + 2 * j;
+      const bool in = t + i * threads < nvec;
+      gm[i][j] = in && gamma ? make_float2(gamma[c], gamma[c + 1]) : both(1.f);
+      bt[i][j] = in && beta ? make_float2(beta[c], beta[c + 1]) : both(0.f);
     }
   const float inv = 1.f / (float)D;
-  float mu_next = 0.f, rs_next = 0.f;  // read one row ahead
-  if (rows > 0) {
-    mu_next = mean[row0];
-    rs_next = rstd[row0];
-  }
   bool ok = true;  // after an expired wait: no more waits, but every barrier
-  for (int k = 0; k < rows; ++k) {
-    const long long row = row0 + k * stride;
-    const int st = k % stages;
-    const float mu = mu_next, rs = rs_next;
-    if (k + 1 < rows) {
-      mu_next = mean[row + stride];
-      rs_next = rstd[row + stride];
-    }
-    ok = ok && mbar_wait_bounded(&full[grp][st], (uint32_t)((k / stages) & 1), err, limit_ns,
-                                 kSite + __LINE__);
-    const Vec<T, VEC>* xr =
-        reinterpret_cast<const Vec<T, VEC>*>(mine + (size_t)st * 2 * row_bytes);
-    const Vec<T, VEC>* dr =
-        reinterpret_cast<const Vec<T, VEC>*>(mine + (size_t)st * 2 * row_bytes + row_bytes);
-    float h[NV][VEC], u[NV][VEC];
-    float s0 = 0.f, s1 = 0.f;
-    const float nmr = -mu * rs;
+  for (int k = 0; k < rows; k += 2) {
+    // rows k and k + 1, one in each half of the joins (the last may be alone: its partner repeats it)
+    const bool two = k + 1 < rows;
+    const long long row[2] = {row0 + k * stride, row0 + (k + two) * stride};
+    float2 h[2][NV][H], s[2];
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (t + i * threads < nvec) {
-        float d[VEC];
-        unpack(xr[t + i * threads], h[i]);
-        unpack(dr[t + i * threads], d);
+    for (int r = 0; r < 2; ++r) {
+      ok = ok && mbar_wait_bounded(&full[grp][ring.st], ring.ph, err, limit_ns, kSite + __LINE__);
+      const Vec<T, VEC>* xr = reinterpret_cast<const Vec<T, VEC>*>(ring.stage());
+      s[r] = both(0.f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          h[i][j] = fmaf(h[i][j], rs, nmr);
-          u[i][j] = d[j] * gm[i][j];
-          s0 += u[i][j];
-          s1 = fmaf(u[i][j], h[i][j], s1);
-          ag[i][j] = fmaf(d[j], h[i][j], ag[i][j]);
-          ab[i][j] += d[j];
+      for (int i = 0; i < NV; ++i)
+        if (t + i * threads < nvec) {
+          unpack2(xr[t + i * threads], h[r][i]);
+#pragma unroll
+          for (int j = 0; j < H; ++j) s[r] = add2(s[r], h[r][i][j]);
         }
-      }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-      s0 += __shfl_xor_sync(0xffffffffu, s0, o);
-      s1 += __shfl_xor_sync(0xffffffffu, s1, o);
+      if (r == 0 && two) ring.next();
     }
-    if (lane == 0) red[grp][k & 1][warp] = make_float2(s0, s1);
-    asm volatile("bar.sync %0, %1;" ::"r"(1 + grp), "r"(threads) : "memory");
-    if (t == 0 && k + stages < rows) issue(k + stages);  // every thread has read the stage
-    s0 = s1 = 0.f;
-    for (int w = 0; w < warps; ++w) {
-      const float2 v = red[grp][k & 1][w];
-      s0 += v.x;
-      s1 += v.y;
+    float2 w = ring_join(make_float2(s[0].x + s[0].y, s[1].x + s[1].y), red[grp][0], warp, lane, warps,
+                         1 + grp, threads);
+    if (t == 0) {
+      if (two) ring.refill(k, ring.before());
+      ring.refill(k + two, ring.st);
     }
-    const float c0 = -s0 * inv * rs, c1 = -s1 * inv * rs;
-    Vec<T, VEC>* o = reinterpret_cast<Vec<T, VEC>*>(dx + row * D);
+    ring.next();
+    const float mu[2] = {w.x * inv, w.y * inv};
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
-      if (t + i * threads < nvec) {
-        float f[VEC];
+    for (int r = 0; r < 2; ++r) {
+      s[r] = both(0.f);
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) f[j] = fmaf(u[i][j], rs, fmaf(h[i][j], c1, c0));
-        o[t + i * threads] = pack<T, VEC>(f);
+      for (int i = 0; i < NV; ++i)
+        if (t + i * threads < nvec)
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            h[r][i][j] = add2(h[r][i][j], both(-mu[r]));
+            s[r] = fma2(h[r][i][j], h[r][i][j], s[r]);
+          }
+    }
+    w = ring_join(make_float2(s[0].x + s[0].y, s[1].x + s[1].y), red[grp][1], warp, lane, warps, 1 + grp,
+                  threads);
+    const float rs[2] = {rsqrtf(w.x * inv + eps), rsqrtf(w.y * inv + eps)};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      if (t == 0) {
+        if (mean) mean[row[r]] = mu[r];
+        if (rstd) rstd[row[r]] = rs[r];
       }
+      Vec<T, VEC>* o = reinterpret_cast<Vec<T, VEC>*>(y + row[r] * D);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (t + i * threads < nvec) {
+#pragma unroll
+          for (int j = 0; j < H; ++j)
+            h[r][i][j] = fma2(mul2(h[r][i][j], both(rs[r])), gm[i][j], bt[i][j]);
+          o[t + i * threads] = pack2<T, VEC>(h[r][i]);
+        }
+    }
   }
-  if (t == 0)  // no copy may be in flight when the CTA exits (passes at once but after a timeout)
-    for (int k = rows > stages ? rows - stages : 0; k < rows; ++k)
-      mbar_wait_bounded(&full[grp][k % stages], (uint32_t)((k / stages) & 1), err, limit_ns,
-                        kSite + __LINE__);
-  if (GROUPS > 1) {  // the other groups' sums through the ring's memory: dgamma [D], dbeta [D]
+  if (t == 0) ring.drain(err, limit_ns);
+}
+
+// Backward: a thread keeps gamma and the sums of dy h and dy of its columns; one join per row.  At the
+// end the groups' sums are added through shared memory, so that there is one row of partials per SM.
+template <typename T, int NV, int GROUPS>
+__global__ void __launch_bounds__(kRingThreads)
+    layernorm_bwd_ring_kernel(const T* __restrict__ x, const T* __restrict__ dy, int N, int D,
+                              const float* __restrict__ gamma, const float* __restrict__ mean,
+                              const float* __restrict__ rstd, T* __restrict__ dx,
+                              float* __restrict__ pg, float* __restrict__ pb, int stages, int* err,
+                              unsigned long long limit_ns) {
+  constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+  extern __shared__ __align__(128) uint8_t ring_mem[];
+  __shared__ uint64_t full[GROUPS][kMaxRing];
+  __shared__ float4 red[GROUPS][2][kRingThreads / 32 / GROUPS];
+  const int threads = (int)blockDim.x / GROUPS, warps = threads / 32;
+  const int grp = (int)threadIdx.x / threads, t = (int)threadIdx.x - grp * threads;
+  const int warp = t >> 5, lane = t & 31;
+  pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int g = 0; g < GROUPS; ++g)
+      for (int i = 0; i < stages; ++i) mbar_init(&full[g][i], 1);
+    fence_mbar_init();
+  }
+  __syncthreads();
+  pdl_wait();
+  const long long row0 = blockIdx.x + (long long)grp * gridDim.x;
+  const long long stride = (long long)gridDim.x * GROUPS;
+  const int rows = row0 < N ? (int)((N - 1 - row0) / stride) + 1 : 0;
+  RowRing<T, 2> ring{{x, dy}, ring_mem + (size_t)grp * stages * 2 * D * sizeof(T), full[grp], stages,
+                     rows, D, row0, stride};
+  if (t == 0) ring.start();
+  const int nvec = D / VEC;
+  float2 ag[NV][H], ab[NV][H], gm[NV][H];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < H; ++j) {
+      ag[i][j] = ab[i][j] = both(0.f);
+      const int c = (t + i * threads) * VEC + 2 * j;
+      gm[i][j] = t + i * threads < nvec && gamma ? make_float2(gamma[c], gamma[c + 1]) : both(1.f);
+    }
+  const float inv = 1.f / (float)D;
+  // mean and rstd are read two rows ahead
+  float2 mu_next = both(0.f), rs_next = both(0.f);
+  auto stats = [&](int k) {
+    if (k < rows) {
+      const long long r0 = row0 + k * stride, r1 = k + 1 < rows ? r0 + stride : r0;
+      mu_next = make_float2(mean[r0], mean[r1]);
+      rs_next = make_float2(rstd[r0], rstd[r1]);
+    }
+  };
+  stats(0);
+  bool ok = true;  // after an expired wait: no more waits, but every barrier
+  for (int k = 0; k < rows; k += 2) {
+    // rows k and k + 1, their sums in one join (the last may be alone)
+    const bool two = k + 1 < rows;
+    const long long row[2] = {row0 + k * stride, row0 + (k + two) * stride};
+    const float mu[2] = {mu_next.x, mu_next.y}, rs[2] = {rs_next.x, rs_next.y};
+    stats(k + 2);
+    // the rows stay packed between the two passes over them (unpacking twice is cheaper than the
+    // registers of both rows' h and u)
+    Vec<T, VEC> xv[2][NV], dv[2][NV];
+    float2 s0[2] = {both(0.f), both(0.f)}, s1[2] = {both(0.f), both(0.f)};
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      if (r == 1) ring.next();
+      ok = ok && mbar_wait_bounded(&full[grp][ring.st], ring.ph, err, limit_ns, kSite + __LINE__);
+      const Vec<T, VEC>* xr = reinterpret_cast<const Vec<T, VEC>*>(ring.stage());
+      const Vec<T, VEC>* dr = reinterpret_cast<const Vec<T, VEC>*>(ring.stage() + ring.row_bytes());
+      const float2 rs2 = both(rs[r]), nmr = both(-mu[r] * rs[r]);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (t + i * threads < nvec) {
+          xv[r][i] = xr[t + i * threads];
+          dv[r][i] = dr[t + i * threads];
+          float2 h[H], u[H];
+          unpack2(xv[r][i], h);
+          unpack2(dv[r][i], u);
+#pragma unroll
+          for (int j = 0; j < H; ++j) {
+            h[j] = fma2(h[j], rs2, nmr);
+            ag[i][j] = fma2(u[j], h[j], ag[i][j]);
+            ab[i][j] = add2(ab[i][j], u[j]);
+            u[j] = mul2(u[j], gm[i][j]);
+            s0[r] = add2(s0[r], u[j]);
+            s1[r] = fma2(u[j], h[j], s1[r]);
+          }
+        }
+    }
+    const float4 w = ring_join4(make_float4(s0[0].x + s0[0].y, s1[0].x + s1[0].y, s0[1].x + s0[1].y,
+                                            s1[1].x + s1[1].y),
+                                red[grp][k >> 1 & 1], warp, lane, warps, 1 + grp, threads);
+    if (t == 0) {
+      if (two) ring.refill(k, ring.before());
+      ring.refill(k + two, ring.st);
+    }
+    ring.next();
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      if (r == 1 && !two) break;
+      // dx = dy (gamma rs) + x (rs c1) + (c0 - mu rs c1),  c0 = -rs mean(u), c1 = -rs mean(u h)
+      const float c0 = -(r ? w.z : w.x) * inv * rs[r], c1 = -(r ? w.w : w.y) * inv * rs[r];
+      const float2 rs2 = both(rs[r]), kx = both(rs[r] * c1), k0 = both(fmaf(-mu[r] * rs[r], c1, c0));
+      Vec<T, VEC>* o = reinterpret_cast<Vec<T, VEC>*>(dx + row[r] * D);
+#pragma unroll
+      for (int i = 0; i < NV; ++i)
+        if (t + i * threads < nvec) {
+          float2 a[H], d[H];
+          unpack2(xv[r][i], a);
+          unpack2(dv[r][i], d);
+#pragma unroll
+          for (int j = 0; j < H; ++j) d[j] = fma2(d[j], mul2(gm[i][j], rs2), fma2(a[j], kx, k0));
+          o[t + i * threads] = pack2<T, VEC>(d);
+        }
+    }
+  }
+  if (t == 0) ring.drain(err, limit_ns);
+  if (GROUPS > 1) {  // the second group's sums through the ring's memory: dgamma [D], dbeta [D]
     static_assert(GROUPS <= 2, "two groups are added");
-    float* sums = reinterpret_cast<float*>(ring);
+    float2* sums = reinterpret_cast<float2*>(ring_mem);
     __syncthreads();
     if (grp == 1)
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (t + i * threads < nvec)
 #pragma unroll
-          for (int j = 0; j < VEC; ++j) {
-            sums[(t + i * threads) * VEC + j] = ag[i][j];
-            sums[D + (t + i * threads) * VEC + j] = ab[i][j];
+          for (int j = 0; j < H; ++j) {
+            sums[(t + i * threads) * H + j] = ag[i][j];
+            sums[D / 2 + (t + i * threads) * H + j] = ab[i][j];
           }
     __syncthreads();
     if (grp == 1) return;
@@ -485,17 +718,17 @@ __global__ void __launch_bounds__(kRingThreads)
     for (int i = 0; i < NV; ++i)
       if (t + i * threads < nvec)
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) {
-          ag[i][j] += sums[(t + i * threads) * VEC + j];
-          ab[i][j] += sums[D + (t + i * threads) * VEC + j];
+        for (int j = 0; j < H; ++j) {
+          ag[i][j] = add2(ag[i][j], sums[(t + i * threads) * H + j]);
+          ab[i][j] = add2(ab[i][j], sums[D / 2 + (t + i * threads) * H + j]);
         }
   }
 #pragma unroll
   for (int i = 0; i < NV; ++i)
     if (t + i * threads < nvec) {
       const long long at = (long long)blockIdx.x * D + (t + i * threads) * VEC;
-      if (pg) *reinterpret_cast<Vec<float, VEC>*>(pg + at) = pack<float, VEC>(ag[i]);
-      if (pb) *reinterpret_cast<Vec<float, VEC>*>(pb + at) = pack<float, VEC>(ab[i]);
+      if (pg) *reinterpret_cast<Vec<float, VEC>*>(pg + at) = pack2<float, VEC>(ag[i]);
+      if (pb) *reinterpret_cast<Vec<float, VEC>*>(pb + at) = pack2<float, VEC>(ab[i]);
     }
 }
 
@@ -588,8 +821,8 @@ NormShape norm_shape(size_t esize, int D) {
   return {vec, 0, 0};
 }
 
-// The backward's ring form: rows of 129 to 1024 16-byte vectors.
-bool bwd_ring(const NormShape& f, int D) { return f.vec > 1 && D / f.vec > 128 && D / f.vec <= 1024; }
+// The ring forms: rows of 129 to 1024 16-byte vectors.
+bool ring_rows(const NormShape& f, int D) { return f.vec > 1 && D / f.vec > 128 && D / f.vec <= 1024; }
 // Its groups and the vectors per thread: two groups of up to 256 threads with one or two vectors, or
 // one of up to 512 with two (more would not fit the 128 registers of a thread).
 struct RingShape {
@@ -603,7 +836,7 @@ RingShape ring_shape(int nvec) {
 // Backward CTAs (= rows of partials): one (ring form) or two per SM, no more than there are rows
 // or row groups.
 int norm_bwd_parts(long long N, const NormShape& f, int D) {
-  const bool ring = bwd_ring(f, D);
+  const bool ring = ring_rows(f, D);
   const long long rpc = f.nv && !ring ? kThreads / f.tpr : 1;
   const long long want = (N + rpc - 1) / rpc;
   const long long cap = (ring ? 1LL : 2LL) * sm_count();
@@ -620,14 +853,52 @@ cudaError_t fwd_launch(const void* x, int N, int D, const float* gamma, const fl
                     rstd);
 }
 
+// Two CTAs per SM of 5 to 8 warps: of these the count whose last round over the rows is fullest
+// (8192 rows: 7 warps, four rounds at 96 %; 8 warps would leave the fourth at 37 %).
 template <typename T, int VEC, int NV>
 cudaError_t fwd_rows(const void* x, int N, int D, const float* gamma, const float* beta, float eps,
                      void* y, float* mean, float* rstd, cudaStream_t s) {
-  long long ctas = ((long long)N + kThreads / 32 - 1) / (kThreads / 32);
-  const long long cap = 2LL * sm_count();
-  return launch_pdl(layernorm_fwd_rows_kernel<T, VEC, NV>, dim3((unsigned)(ctas < cap ? ctas : cap)),
-                    dim3(kThreads), (size_t)D * 8, s, static_cast<const T*>(x), N, D, gamma, beta, eps,
-                    static_cast<T*>(y), mean, rstd);
+  const long long ctas = 2LL * sm_count();
+  int warps = 8;
+  double fill = 0;
+  for (int w = 8; w >= 5; --w) {
+    const long long at_once = ctas * w;
+    const double f = (double)N / (double)((N + at_once - 1) / at_once * at_once);
+    if (f > fill + 1e-9) {
+      fill = f;
+      warps = w;
+    }
+  }
+  const long long want = ((long long)N + warps - 1) / warps;
+  return launch_pdl(layernorm_fwd_rows_kernel<T, VEC, NV>, dim3((unsigned)(want < ctas ? want : ctas)),
+                    dim3(32 * warps), (size_t)D * 8, s, static_cast<const T*>(x), N, D, gamma, beta,
+                    eps, static_cast<T*>(y), mean, rstd);
+}
+
+// Stages of a group's ring for `bytes` per stage, and the shared memory of all rings.
+int ring_stages(size_t bytes, int groups) {
+  const int n = (int)((size_t)kRingBytes / (groups * bytes));
+  return n < kMaxRing ? n : kMaxRing;
+}
+template <typename K>
+cudaError_t ring_attr(K k) {
+  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
+}
+
+template <typename T, int NV, int GROUPS>
+cudaError_t fwd_ring(const void* x, int N, int D, const float* gamma, const float* beta, float eps,
+                     void* y, float* mean, float* rstd, cudaStream_t s) {
+  const size_t stage = (size_t)D * sizeof(T);
+  const int threads = ring_shape(D / (16 / (int)sizeof(T))).threads;
+  const int stages = ring_stages(stage, GROUPS), grid = N < sm_count() ? N : sm_count();
+  auto k = layernorm_fwd_ring_kernel<T, NV, GROUPS>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [&] { attr = ring_attr(k); });
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(k, dim3(grid), dim3(GROUPS * threads), GROUPS * stages * stage, s,
+                    static_cast<const T*>(x), N, D, gamma, beta, eps, static_cast<T*>(y), mean, rstd,
+                    stages, device_error_word(), kWaitLimitNs);
 }
 
 template <typename T, int NV, int GROUPS>
@@ -636,14 +907,11 @@ cudaError_t bwd_ring_launch(const void* x, const void* dy, int N, int D, const f
                             int parts, cudaStream_t s) {
   const size_t stage = 2 * (size_t)D * sizeof(T);
   const int threads = ring_shape(D / (16 / (int)sizeof(T))).threads;
-  int stages = (int)((size_t)kRingBytes / (GROUPS * stage));
-  if (stages > kMaxRing) stages = kMaxRing;
+  const int stages = ring_stages(stage, GROUPS);
   auto k = layernorm_bwd_ring_kernel<T, NV, GROUPS>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-  });
+  std::call_once(once, [&] { attr = ring_attr(k); });
   if (attr != cudaSuccess) return attr;
   return launch_pdl(k, dim3(parts), dim3(GROUPS * threads), GROUPS * stages * stage, s,
                     static_cast<const T*>(x), static_cast<const T*>(dy), N, D, gamma, mean, rstd,
@@ -654,13 +922,15 @@ template <typename T, int VEC>
 cudaError_t fwd_pick(const NormShape& f, const void* x, int N, int D, const float* gamma,
                      const float* beta, float eps, void* y, float* mean, float* rstd,
                      cudaStream_t s) {
-  // from a few rows per SM on, and up to 16 vectors per lane: a warp per row
+  // from a few rows per SM on: a warp per row, or the ring for the rows that a warp's registers do
+  // not hold (at 8192 x 4096 the ring takes 35 us, a warp per row 27)
   if constexpr (VEC > 1) {
     const int nvec = D / VEC;
-    if (N >= 8 * sm_count() && nvec <= 512) {
+    if (N >= 8 * sm_count()) {
       if (nvec <= 128) return fwd_rows<T, VEC, 4>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
       if (nvec <= 256) return fwd_rows<T, VEC, 8>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
-      return fwd_rows<T, VEC, 16>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
+      if (nvec <= 512) return fwd_rows<T, VEC, 16>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
+      if (ring_rows(f, D)) return fwd_ring<T, 2, 1>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
     }
   }
   if (f.tpr == 32) return fwd_launch<T, VEC, 32, 4>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
@@ -686,7 +956,7 @@ cudaError_t bwd_pick(const NormShape& f, const void* x, const void* dy, int N, i
                      const float* gamma, const float* mean, const float* rstd, void* dx, float* pg,
                      float* pb, int parts, cudaStream_t s) {
   if constexpr (VEC > 1) {
-    if (bwd_ring(f, D)) {
+    if (ring_rows(f, D)) {
       const RingShape r = ring_shape(D / VEC);
       if (r.groups == 1)
         return bwd_ring_launch<T, 2, 1>(x, dy, N, D, gamma, mean, rstd, dx, pg, pb, parts, s);
