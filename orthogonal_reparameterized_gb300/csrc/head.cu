@@ -1254,7 +1254,7 @@ bool bf16_map(CUtensorMap* m, const void* p, long long inner, long long outer, i
   return encode_tma_2d(m, p, TMA_BF16, inner, outer, inner, bi, bo, true);
 }
 
-void set_segs(HeadGemm* g, bool f32, bool lse) {
+void set_segs(HeadGemm* g, bool f32, bool lse, int rows) {
   // small pieces first, so that the accumulator is small while they are added (a chunk runs pair by
   // pair of pieces: the adds at full size are those of the last pair)
   static const int8_t a[kMaxSegs] = {1, 0, 2, 1, 0, 0}, b[kMaxSegs] = {1, 2, 0, 0, 1, 0};
@@ -1263,9 +1263,10 @@ void set_segs(HeadGemm* g, bool f32, bool lse) {
     g->seg_b[i] = b[i];
   }
   // K of one accumulator: 256 in fp32 (16 adds of 16 products at full size; 64: a fifth slower); in
-  // bf16 1024 for the logits (64 adds) and 4096 for the gradients, which are rounded to bf16 (256
-  // adds: 1.5e-5)
-  g->chunk = f32 ? 4 : (lse ? 16 : 64);
+  // bf16 4096 for the gradients, which are rounded to bf16 (256 adds: 1.5e-5), and for the logits
+  // 1024 (64 adds: losses to 7e-7 at K = 2048), or 256 for few rows, whose products are not what
+  // their time goes into (one row's loss: 1.3e-6 with 1024, 2e-7 with 256)
+  g->chunk = f32 ? 4 : (lse ? (rows <= 512 ? 4 : 16) : 64);
 }
 
 struct HeadCall {
@@ -1375,7 +1376,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       h.V = c.V;
       h.rows = rows;
       h.num_kb = ceil_div(c.D, BK);
-      h.chunk = 16;
+      h.chunk = 4;
       h.scale2 = kLog2e / c.T;
       h.part = part;
       h.ucol = ucol;
@@ -1393,7 +1394,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       }
     } else {
       HeadGemm g{};
-      set_segs(&g, pl.f32, true);
+      set_segs(&g, pl.f32, true, rows);
       for (int i = 0; i < np; ++i)
         if (!bf16_map(&mp.a[i], xp + i * x_step, c.D, rows, 64, 128) ||
             !bf16_map(&mp.b[i], wp + i * w_step, c.D, c.V, 64, 128))
@@ -1455,7 +1456,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     if (!pl.grads) continue;
     // dx = dz W and dW (+)= dz^T x; between the pieces of a bf16 head dW's sum stays in fp32
     HeadGemm h{};
-    set_segs(&h, pl.f32, false);
+    set_segs(&h, pl.f32, false, rows);
     h.out_scale = unit;
     h.T = c.T;
     int used = 0;
