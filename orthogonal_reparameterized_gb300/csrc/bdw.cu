@@ -55,16 +55,6 @@ constexpr int BDW_SMEM = BDW_BAR_OFF + 256 + 1024;    // + barriers + alignment 
 static_assert(BDW_SMEM <= 227 * 1024, "fused block-diagonal backward: shared memory");
 constexpr uint32_t G_COL = 0, Y_COL = 128, DG_COL = 256;
 
-// Load a 3-D box into this CTA's shared memory, completing on `bar`.
-__device__ __forceinline__ void tma_load_3d(void* smem_dst, const CUtensorMap* map, uint64_t* bar,
-                                            int c0, int c1, int c2) {
-  asm volatile(
-      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(smem_dst)),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
-      : "memory");
-}
-
 struct BdwParams {
   int b, halves, nblk, splits, chunk_tiles, ntiles, num_units;
   const __nv_bfloat16* G;    // [nblk, b, b]

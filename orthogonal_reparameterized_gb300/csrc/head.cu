@@ -49,7 +49,8 @@ constexpr int BN = 256;           // columns per pair tile
 constexpr int BK = 64;
 constexpr int kStages = 5;  // (6: 3 % slower at 8192 x 128256 x 4096; 4: dx and dW 4 % slower)
 constexpr int kEpiWarps = 8;      // two per TMEM lane quarter, each 128 columns
-constexpr int kGemmThreads = 64 + 32 * kEpiWarps;
+constexpr int kBWarp = 2 + kEpiWarps;  // the gradients' second producer
+constexpr int gemm_threads(bool lse) { return 32 * (kBWarp + (lse ? 0 : 1)); }
 constexpr int kGroup = 128;       // columns of one (max, sum) group
 constexpr uint32_t kABytes = BM * BK * 2;
 constexpr uint32_t kBBytes = BN / 2 * BK * 2;
@@ -74,6 +75,7 @@ struct Product {
   int n_fast;            // raster: bands of kBand M tiles (1: N tiles), M (N) fastest in a band
   int num_kb, kb_split;  // 64-wide K blocks in all, per split
   int a_mn;              // A stored with its M axis contiguous ([K][M])
+  int b_groups;          // B's map (MN-major) is one of 64-column groups: one box instead of two
   int M, N;              // valid rows and columns
   int n_store;           // columns of the stored tensor
   int c_rows;            // its rows per split
@@ -173,11 +175,11 @@ __device__ __forceinline__ float head_unit(float top) { return top > 0.f && top 
 
 // LSE: the logits' product with its softmax epilogue (one product, both operands K-major).
 // Otherwise the gradients' products, dx and dW in one launch, so that the second's tiles fill the
-// first's last wave.  Warp 0 of each CTA loads its 128 rows of A and its half of B, one thread of
-// the even CTA's warp 1 issues the MMAs, warps 2-9 read the accumulators back (warp w: rows
+// first's last wave.  Warps 0 and 10 of each CTA load its 128 rows of A and its half of B, one thread
+// of the even CTA's warp 1 issues the MMAs, warps 2-9 read the accumulators back (warp w: rows
 // 32 (w % 4).. of the CTA's 128, columns 128 ((w - 2) / 4)..).
 template <bool LSE, bool F32>
-__global__ void __launch_bounds__(kGemmThreads, 1)
+__global__ void __launch_bounds__(gemm_threads(LSE), 1)
     head_gemm_kernel(const __grid_constant__ HeadMaps maps0, const __grid_constant__ HeadMaps maps1,
                      const __grid_constant__ HeadGemm p) {
   constexpr uint32_t TMEM_COLS = 2 * BN;
@@ -221,18 +223,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
   pdl_wait();
   const int t0 = (int)blockIdx.x / 2, t_step = (int)gridDim.x / 2;
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ TMA producer
+  if ((warp == 0 || warp == kBWarp) && lane == 0) {
+    // ------------------------------------------------------------ TMA producers
+    // gradients: warp 0 loads A, warp 10 B (each up to two boxes); logits: warp 0 both (two warps
+    // measured 3 % slower there, one 6 % slower for the gradients)
+    const bool is_b = !LSE && warp == kBWarp;
     Ring<kStages> rg;
     bool ok = true;
     long long issued = 0;
     const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
+    uint8_t* const dst0 = smem + (is_b ? kABytes : 0);
     for (int t = t0; t < p.num_tiles && ok; t += t_step) {
       const Tile c = tile_of(p, t);
       const HeadMaps& maps = c.which ? maps1 : maps0;
-      const bool a_mn = !LSE && p.prod[c.which].a_mn;
-      constexpr bool b_mn = !LSE;
-      const int m0 = (2 * c.mi + crank) * BM, n0 = c.nt * BN + crank * (BN / 2);
+      const CUtensorMap* const set = is_b ? maps.b : maps.a;
+      const int8_t* const seg = is_b ? p.seg_b : p.seg_a;
+      // the operand's first row of M (N), and how it is loaded: K-major; MN-major as one box of two
+      // 64-column groups (dz: always) or as two boxes
+      const int r0 = is_b ? c.nt * BN + crank * (BN / 2) : (2 * c.mi + crank) * BM;
+      const int how = LSE ? 0 : (is_b ? (p.prod[c.which].b_groups ? 1 : 2) : p.prod[c.which].a_mn);
+      const bool expect = !is_b && crank == 0;
       for (int c0 = c.kb0; c0 < c.kb1 && ok; c0 += p.chunk) {
         const int len = min(c.kb1 - c0, p.chunk);
         int sg = 0, i = 0;  // fp32: a chunk's K blocks once per pair of pieces
@@ -241,28 +251,26 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
             ok = false;
             break;
           }
-          uint8_t* sa = smem + rg.s * kStageBytes;
-          uint8_t* sb = sa + kABytes;
-          const CUtensorMap* ma = &maps.a[F32 ? p.seg_a[sg] : 0];
-          const CUtensorMap* mb = &maps.b[F32 ? p.seg_b[sg] : 0];
+          uint8_t* dst = dst0 + rg.s * kStageBytes;
+          const int at = sg;
+          const CUtensorMap* m = F32 ? &set[seg[at]] : set;
           const int k = (c0 + i) * BK;
           if (++i == len) {
             i = 0;
             ++sg;
           }
-          if (crank == 0) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
+          if (expect) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
           const uint32_t fb = full0 + rg.s * 8;
-          if (!a_mn) {
-            tma_load_2d_pair(sa, ma, fb, k, m0);
-          } else {  // two boxes of 64 rows of K x 64 of M
-            tma_load_2d_pair(sa, ma, fb, m0, k);
-            tma_load_2d_pair(sa + 8192, ma, fb, m0 + 64, k);
-          }
-          if (!b_mn) {
-            tma_load_2d_pair(sb, mb, fb, k, n0);
+          if (how == 0) {
+            tma_load_2d_pair(dst, m, fb, k, r0);
+            if (LSE)
+              tma_load_2d_pair(dst + kABytes, &maps.b[F32 ? p.seg_b[at] : 0], fb, k,
+                               c.nt * BN + crank * (BN / 2));
+          } else if (how == 1) {
+            tma_load_3d_pair(dst, m, fb, 0, k, r0 / 64);
           } else {
-            tma_load_2d_pair(sb, mb, fb, n0, k);
-            tma_load_2d_pair(sb + 8192, mb, fb, n0 + 64, k);
+            tma_load_2d_pair(dst, m, fb, r0, k);
+            tma_load_2d_pair(dst + 8192, m, fb, r0 + 64, k);
           }
         }
       }
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) *p.unit = head_unit(top);
-  } else if (warp >= 2) {
+  } else if (warp >= 2 && warp < kBWarp) {
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int cbeg = ((warp - 2) >> 2) * kGroup;
@@ -514,8 +522,10 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
 // flight.  A warp of the epilogue holds 32 vocabulary rows: it takes the targets out, turns its
 // 32 x NT logits over through shared memory and leaves one (max, sum) per token.
 struct HeadScore {
-  int tiles, height;
-  int V, rows, num_kb, chunk, stages;
+  int tiles, height;       // height: a multiple of 8 (the swizzle's rows)
+  int V, rows, stages;
+  int kps;                 // K blocks per stage: 1 (two-dimensional maps), or the groups of the maps
+  int num_st, chunk;       // stages per tile, per accumulator hand-over
   float scale2;
   float2* part;            // [rows][4 tiles]
   const int32_t* ucol;     // [rows][K] the rows' distinct target columns
@@ -530,7 +540,7 @@ constexpr int kScoreThreads = 64 + 128;
 constexpr int kScoreRing = 12;        // stages at most
 constexpr int kScoreSmem = 220 * 1024;
 constexpr int score_turn_bytes(int NT) { return 4 * 32 * (NT + 1) * 4; }
-constexpr int score_stage_bytes(int NT) { return kABytes + NT * BK * 2; }
+int score_stage_bytes(int NT, int height, int kps) { return kps * (height + NT) * BK * 2; }
 
 template <int NT>
 __global__ void __launch_bounds__(kScoreThreads, 1)
@@ -538,13 +548,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
                       const HeadScore p) {
   constexpr uint32_t IDESC = make_idesc(BM, NT, false, false);
   constexpr uint32_t TMEM_COLS = 2 * NT;
-  constexpr uint32_t STAGE = score_stage_bytes(NT);
+  const uint32_t a_kb = (uint32_t)p.height * BK * 2, x_off = p.kps * a_kb;  // one K block; the tokens
+  const uint32_t stage = x_off + p.kps * NT * BK * 2;
   constexpr int TOK = (NT + 31) / 32;  // tokens a lane looks after
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  float* turn = reinterpret_cast<float*>(smem + p.stages * STAGE);
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * STAGE + (score_turn_bytes(NT) + 15) / 16 * 16);
+  float* turn = reinterpret_cast<float*>(smem + p.stages * stage);
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage +
+                                               (score_turn_bytes(NT) + 15) / 16 * 16);
   uint64_t* empty = full + kScoreRing;
   uint64_t* tfull = empty + kScoreRing;
   uint64_t* tempty = tfull + 2;
@@ -593,19 +605,23 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     }
   };
   if (warp == 0 && lane == 0) {
-    const uint32_t bytes = (uint32_t)(p.height + NT) * BK * 2;
     int issued = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x)
-      for (int kb = 0; kb < p.num_kb; ++kb, next(), ++issued) {
+      for (int kb = 0; kb < p.num_st * p.kps; kb += p.kps, next(), ++issued) {
         if (!wait(&empty[s], ph ^ 1, kSite + __LINE__)) {
           ok = false;
           break;
         }
-        uint8_t* sa = smem + s * STAGE;
-        mbar_arrive_expect_tx(&full[s], bytes);
-        tma_load_2d(sa, &mW, &full[s], kb * BK, t * p.height);
-        tma_load_2d(sa + kABytes, &mx, &full[s], kb * BK, 0);
+        uint8_t* sa = smem + s * stage;
+        mbar_arrive_expect_tx(&full[s], stage);
+        if (p.kps > 1) {
+          tma_load_3d(sa, &mW, &full[s], 0, t * p.height, kb);
+          tma_load_3d(sa + x_off, &mx, &full[s], 0, 0, kb);
+        } else {
+          tma_load_2d(sa, &mW, &full[s], kb * BK, t * p.height);
+          tma_load_2d(sa + x_off, &mx, &full[s], kb * BK, 0);
+        }
       }
     for (int j = issued - 1; j >= 0 && j >= issued - p.stages; --j)  // every copy has landed
       mbar_wait_bounded(&full[j % p.stages], (uint32_t)((j / p.stages) & 1), p.err, p.limit_ns,
@@ -614,25 +630,29 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     Ring<2> acc;
     bool any = false, ok = true;
     for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x)
-      for (int kb0 = 0; kb0 < p.num_kb && ok; kb0 += p.chunk, acc.next()) {
+      for (int st0 = 0; st0 < p.num_st && ok; st0 += p.chunk, acc.next()) {
         if (!wait(&tempty[acc.s], acc.ph ^ 1, kSite + __LINE__)) {
           ok = false;
           break;
         }
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc.s * NT);
-        const int blocks = min(p.num_kb - kb0, p.chunk);
-        for (int j = 0; j < blocks; ++j, next()) {
+        const int len = min(p.num_st - st0, p.chunk);
+        for (int j = 0; j < len; ++j, next()) {
           if (!wait(&full[s], ph, kSite + __LINE__)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_base + s * STAGE;
-          const uint64_t ad = tile_desc<false>(a_base), bd = tile_desc<false>(a_base + kABytes);
+          // (rows past `height` of the 128 are whatever follows in shared memory: not looked at)
+          const uint32_t a_base = smem_base + s * stage;
+          for (int i = 0; i < p.kps; ++i) {
+            const uint64_t ad = tile_desc<false>(a_base + i * a_kb);
+            const uint64_t bd = tile_desc<false>(a_base + x_off + i * NT * BK * 2);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16(d, ad + k * 2, bd + k * 2, IDESC, (j | k) != 0);
+            for (int k = 0; k < BK / 16; ++k)
+              umma_bf16(d, ad + k * 2, bd + k * 2, IDESC, (j | i | k) != 0);
+          }
           umma_commit(&empty[s]);
         }
         umma_commit(&tfull[acc.s]);
@@ -670,7 +690,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
         }
       }
       float v[NT];
-      for (int kb0 = 0; kb0 < p.num_kb; kb0 += p.chunk, acc.next()) {
+      for (int st0 = 0; st0 < p.num_st; st0 += p.chunk, acc.next()) {
         const bool got = wait(&tfull[acc.s], acc.ph, kSite + __LINE__);
         if (!__all_sync(0xffffffffu, got)) {
           ok = false;
@@ -685,7 +705,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < 16; ++i)
-            v[j + i] = kb0 == 0 ? __uint_as_float(r[i]) : v[j + i] + __uint_as_float(r[i]);
+            v[j + i] = st0 == 0 ? __uint_as_float(r[i]) : v[j + i] + __uint_as_float(r[i]);
         }
         tc_fence_before();
         __syncwarp();
@@ -1095,7 +1115,9 @@ poetx_status score(const CUtensorMap& mW, const CUtensorMap& mx, HeadScore p, cu
     attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
   });
   POETX_CUDA_TRY(attr_err);
-  p.stages = (kScoreSmem - 1024 - 512 - score_turn_bytes(NT)) / score_stage_bytes(NT);
+  // (16 KB kept behind the last stage: the MMAs read 128 rows from its last K block's first)
+  p.stages = (kScoreSmem - 1024 - 512 - score_turn_bytes(NT) - (int)kABytes) /
+             score_stage_bytes(NT, p.height, p.kps);
   if (p.stages > kScoreRing) p.stages = kScoreRing;
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
@@ -1118,7 +1140,7 @@ cudaError_t gemm_pairs(int* pairs) {
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sm_count() / 2 * 2);
-    cfg.blockDim = dim3(kGemmThreads);
+    cfg.blockDim = dim3(gemm_threads(LSE));
     cfg.dynamicSmemBytes = kGemmSmem;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1148,7 +1170,8 @@ poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStrea
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
   const int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
-  POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, F32>, dim3(2 * pairs), dim3(kGemmThreads),
+  POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, F32>, dim3(2 * pairs),
+                                    dim3(gemm_threads(LSE)),
                                     kGemmSmem, s, 2, m0, m1, p));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_HEAD_GEMM);
@@ -1216,7 +1239,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
     // every SM the same number of tiles, of at most 128 rows; no lower than 16
     const int sms = sm_count(), each = ceil_div(V, (long long)sms * BM);
     o->height = ceil_div(V, (long long)sms * each);
-    if (o->height < 16) o->height = 16;
+    o->height = (int)align_up(o->height < 16 ? 16 : (size_t)o->height, 8);
     o->tiles = ceil_div(V, o->height);
     o->groups = 4 * o->tiles;
   }
@@ -1261,6 +1284,13 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
 
 bool bf16_map(CUtensorMap* m, const void* p, long long inner, long long outer, int bi, int bo) {
   return encode_tma_2d(m, p, TMA_BF16, inner, outer, inner, bi, bo, true);
+}
+
+// An MN-major operand [K][MN]: 64 rows of K and 128 of MN per load, as one box of two 64-column groups
+// where MN is a multiple of 64, else as two boxes.
+bool mn_map(CUtensorMap* m, const void* p, long long inner, long long outer) {
+  return inner % 64 == 0 ? encode_tma_groups(m, p, inner, outer, 64, 2)
+                         : bf16_map(m, p, inner, outer, 64, 64);
 }
 
 void set_segs(HeadGemm* g, bool f32, bool lse, int rows) {
@@ -1384,17 +1414,22 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       h.height = pl.height;
       h.V = c.V;
       h.rows = rows;
-      h.num_kb = ceil_div(c.D, BK);
-      h.chunk = 4;
+      // One box per stage and operand over several K blocks where D is a multiple of 64 (one thread
+      // issues all copies, and 14 KB boxes come in at some 50 GB/s per SM, four together at 70)
+      h.kps = c.D % 64 ? 1 : (nt <= 32 ? 4 : 2);
+      h.num_st = ceil_div(ceil_div(c.D, BK), h.kps);
+      h.chunk = 4 / h.kps;  // 256 of K per accumulator
       h.scale2 = kLog2e / c.T;
       h.part = part;
       h.ucol = ucol;
       h.gstart = gstart;
       h.K = c.K;
       h.tl = tl;
-      if (!bf16_map(&mp.a[0], wp, c.D, c.V, 64, pl.height) ||
-          !bf16_map(&mp.b[0], xp, c.D, rows, 64, nt))
-        return POETX_ERR_CUDA;
+      const bool maps = h.kps > 1 ? encode_tma_groups(&mp.a[0], wp, c.D, c.V, pl.height, h.kps) &&
+                                        encode_tma_groups(&mp.b[0], xp, c.D, rows, nt, h.kps)
+                                  : bf16_map(&mp.a[0], wp, c.D, c.V, 64, pl.height) &&
+                                        bf16_map(&mp.b[0], xp, c.D, rows, 64, nt);
+      if (!maps) return POETX_ERR_CUDA;
       switch (nt) {
         case 16: POETX_TRY(score<16>(mp.a[0], mp.b[0], h, s)); break;
         case 32: POETX_TRY(score<32>(mp.a[0], mp.b[0], h, s)); break;
@@ -1475,8 +1510,9 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       Product& d = h.prod[used++];
       for (int i = 0; i < np; ++i)
         if (!bf16_map(&mp.a[i], w + pl.dz + i * z_step, pl.Vp, rows, 64, 128) ||
-            !bf16_map(&mp.b[i], wp + i * w_step, c.D, c.V, 64, 64))
+            !mn_map(&mp.b[i], wp + i * w_step, c.D, c.V))
           return POETX_ERR_CUDA;
+      d.b_groups = c.D % 64 == 0;
       d.tiles_m = ceil_div(rows, 2 * BM);
       d.tiles_n = ceil_div(c.D, BN);
       d.num_tiles = d.tiles_m * d.tiles_n * pl.splits;
@@ -1496,9 +1532,10 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       Product& d = h.prod[used];
       HeadMaps& m = used++ ? mw : mp;
       for (int i = 0; i < np; ++i)
-        if (!bf16_map(&m.a[i], w + pl.dz + i * z_step, pl.Vp, rows, 64, 64) ||
-            !bf16_map(&m.b[i], xp + i * x_step, c.D, rows, 64, 64))
+        if (!mn_map(&m.a[i], w + pl.dz + i * z_step, pl.Vp, rows) ||
+            !mn_map(&m.b[i], xp + i * x_step, c.D, rows))
           return POETX_ERR_CUDA;
+      d.b_groups = c.D % 64 == 0;
       d.tiles_m = ceil_div(c.V, 2 * BM);
       d.tiles_n = ceil_div(c.D, BN);
       d.num_tiles = d.tiles_m * d.tiles_n;

@@ -162,6 +162,10 @@ enum TmaElem : int { TMA_U8 = 0, TMA_BF16 = 1, TMA_F32 = 2 };
 // box_outer}, 128-byte swizzle or none (cached per thread).
 bool encode_tma_2d(CUtensorMap* m, const void* ptr, TmaElem et, uint64_t inner, uint64_t outer,
                    uint64_t pitch_elems, uint32_t box_inner, uint32_t box_outer, bool swizzle128);
+// A bf16 matrix [outer][inner] (inner a multiple of 64) as {64 columns, rows, groups of 64 columns},
+// box {64, rows, groups}, 128-byte swizzle (cached per thread).
+bool encode_tma_groups(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t rows,
+                       uint32_t groups);
 // Y = X . op(G) per block (bf16), op = identity (trans=0) or transpose; optional column
 // scale; optional output permutation (column c of the product is stored at out_perm[c]).
 poetx_status umma_blockdiag(const void* X, long long N, int nblk, int b, const void* G, int trans,

@@ -1350,6 +1350,48 @@ bool encode_tma_2d(CUtensorMap* m, const void* ptr, TmaElem et, uint64_t inner, 
   return true;
 }
 
+// A bf16 matrix [outer][inner] (inner a multiple of 64) viewed as {64 columns, rows, groups of 64
+// columns}: one box takes `rows` rows of `groups` neighbouring groups, group by group (each the
+// 128-byte-swizzled tile of a 2-D box).  Kept in a per-thread cache like encode_tma_2d's.
+bool encode_tma_groups(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t rows,
+                       uint32_t groups) {
+  struct Entry {
+    const void* ptr;
+    uint64_t inner, outer;
+    uint32_t rows, groups;
+    int dev;
+    CUtensorMap map;
+  };
+  constexpr int kEntries = 16;
+  thread_local Entry cache[kEntries];
+  thread_local int next = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  for (int i = 0; i < kEntries; ++i) {
+    const Entry& e = cache[i];
+    if (e.ptr == ptr && ptr && e.inner == inner && e.outer == outer && e.rows == rows &&
+        e.groups == groups && e.dev == dev) {
+      *m = e.map;
+      return true;
+    }
+  }
+  EncodeTiledFn fn = encode_fn();
+  if (!fn || inner % 64) return false;
+  cuuint64_t dims[3] = {64, outer, inner / 64};
+  cuuint64_t strides[2] = {inner * 2, 128};
+  cuuint32_t box[3] = {64, rows, groups};
+  cuuint32_t es[3] = {1, 1, 1};
+  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  Entry& e = cache[next];
+  next = (next + 1) % kEntries;
+  e.ptr = ptr; e.inner = inner; e.outer = outer; e.rows = rows; e.groups = groups; e.dev = dev;
+  e.map = *m;
+  return true;
+}
+
 bool umma_supported() {
   // sm_103 and a driver entry point for tensor maps; cached per device
   static std::atomic<int> cached[64];
