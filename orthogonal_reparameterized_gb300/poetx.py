@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import threading
 from typing import Optional
 
 import torch
@@ -507,12 +508,26 @@ def _raw_stream(stream, t):
     return stream.cuda_stream
 
 
-def _scratch(nbytes: int, device, stream):
-    """Scratch for one call, from the allocator pool of the stream that will use it."""
+_kept = threading.local()
+_KEPT_BYTES = 64 << 20
+
+
+def _scratch(nbytes: int, t, stream, handle: int):
+    """Scratch for one call on the device of t.  On the default stream, where a thread's calls follow
+    one another, the thread keeps one buffer of up to 64 MB (allocating and freeing one costs more
+    host time than a small call's launches); elsewhere it comes from the allocator pool of the stream
+    that will use it."""
     if stream is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        if handle == 0 and nbytes <= _KEPT_BYTES:
+            kept, dev = _kept.__dict__, t.get_device()
+            ws = kept.get(dev)
+            if ws is None or ws.numel() < nbytes:
+                ws = kept[dev] = torch.empty(max(nbytes, 1 << 20), dtype=torch.uint8,
+                                             device=t.device)
+            return ws
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=t.device)
     with torch.cuda.stream(stream):
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=t.device)
 
 
 def poetx_layernorm_fwd(x, y, gamma=None, beta=None, mean=None, rstd=None, eps=1e-5, stream=None):
@@ -549,11 +564,12 @@ def poetx_layernorm_bwd(x, dy, mean, rstd, dx, gamma=None, dgamma=None, dbeta=No
     _want(fn, "mean", mean, (N,), f32)
     _want(fn, "rstd", rstd, (N,), f32)
     dt, L, px = _DT[x.dtype], lib(), _addr(x)
+    handle = _raw_stream(stream, x)
     if ws is None:
-        ws = _scratch(L.poetx_layernorm_bwd_workspace_bytes(dt, N, D), x.device, stream)
+        ws = _scratch(L.poetx_layernorm_bwd_workspace_bytes(dt, N, D), x, stream, handle)
     st = L.poetx_layernorm_bwd(dt, px, _addr(dy), N, D, _addr(gamma), _addr(mean), _addr(rstd),
                                _addr(dx), _addr(dgamma), _addr(dbeta), 1 if accumulate else 0,
-                               _addr(ws), ws.numel(), _raw_stream(stream, x))
+                               _addr(ws), ws.numel(), handle)
     if st:
         _check(fn, st)
 
@@ -577,12 +593,12 @@ def _head(fn, call, x, W, K, target, logit, loss, dloss, dx, dW, lse, ws, stream
     _want(fn, "dloss", dloss, (N,), f32)
     dt, px = _DT[x.dtype], _addr(x)
     targets = (_addr(target),) if logit is None else (_addr(target), _addr(logit), K)
+    handle = _raw_stream(stream, x)
     if ws is None:
         ws = _scratch(lib().poetx_head_workspace_bytes(dt, N, D, V, K, dx is not None,
-                                                       dW is not None), x.device, stream)
+                                                       dW is not None), x, stream, handle)
     st = call(dt, px, N, D, _addr(W), V, *targets, option, _addr(dloss), _addr(loss), _addr(lse),
-              _addr(dx), _addr(dW), 1 if accumulate else 0, _addr(ws), ws.numel(),
-              _raw_stream(stream, x))
+              _addr(dx), _addr(dW), 1 if accumulate else 0, _addr(ws), ws.numel(), handle)
     if st:
         _check(fn, st)
 

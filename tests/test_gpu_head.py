@@ -274,3 +274,49 @@ def test_head_empty_batch(P):
     assert (dW == 1).all()
     P.poetx_head_ce(x, W, e.int(), e, dloss=e, dx=torch.empty_like(x), dW=dW)
     assert not dW.any()
+
+
+def test_head_default_stream_scratch_is_per_thread(P):
+    """Calls of two threads on the default stream, interleaved as they come: each thread has its own
+    scratch."""
+    import threading
+    cases = [_inputs(200, 1500, 128, "bf16", 15), _inputs(90, 2500, 256, "bf16", 16)]
+    refs = [_ce(P, *c) for c in cases]
+    errors = []
+
+    def work(i):
+        try:
+            for _ in range(20):
+                got = _ce(P, *cases[i])
+                for k in got:
+                    if not torch.equal(got[k], refs[i][k]):
+                        errors.append((i, k))
+        except Exception as e:  # noqa: BLE001
+            errors.append((i, repr(e)))
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+
+
+def test_head_in_a_cuda_graph(P):
+    """Captured and replayed on new inputs, with its scratch from the graph's pool."""
+    x, W, t, g = _inputs(130, 1100, 128, "bf16", 17)
+    x2, _, t2, _ = _inputs(130, 1100, 128, "bf16", 18)
+    ref = _ce(P, x2, W, t2, g)
+    xd, Wd, td, gd = x.to(DEV), W.to(DEV), dev(t, torch.int32), dev(g, torch.float32)
+    out = {"loss": torch.empty(130, device=DEV), "lse": torch.empty(130, device=DEV),
+           "dx": torch.empty_like(xd), "dW": torch.empty_like(Wd)}
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.poetx_head_ce(xd, Wd, td, out["loss"], lse=out["lse"], dloss=gd, dx=out["dx"],
+                        dW=out["dW"])
+    xd.copy_(x2)
+    td.copy_(dev(t2, torch.int32))
+    graph.replay()
+    torch.cuda.synchronize()
+    for k in ref:
+        assert torch.equal(out[k], ref[k]), k
