@@ -860,6 +860,22 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
   o[2] = __float2bfloat16_rn(v);
 }
 
+// The pieces of four neighbouring values, to d[0], d[1] and d[2].
+__device__ __forceinline__ void store3(float4 w, __nv_bfloat16* const (&d)[3]) {
+  __nv_bfloat16 o[4][3];
+  split3(w.x, o[0]);
+  split3(w.y, o[1]);
+  split3(w.z, o[2]);
+  split3(w.w, o[3]);
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const __nv_bfloat162 lo = __halves2bfloat162(o[0][k], o[1][k]);
+    const __nv_bfloat162 hi = __halves2bfloat162(o[2][k], o[3][k]);
+    *reinterpret_cast<uint2*>(d[k]) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                 *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
 // One CTA per row: joins the groups, writes loss and lse and turns e into dz.
 template <bool F32>
 __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) {
@@ -1012,19 +1028,23 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     }
   } else {
     const float4* er = reinterpret_cast<const float4*>(static_cast<float*>(p.e) + row * p.pitch);
-    for (long long i = t; i < p.pitch / 4; i += kRowThreads) {
-      __nv_bfloat16 o[4][3];
-      const float4 w = live ? er[i] : make_float4(0.f, 0.f, 0.f, 0.f);
-      const float f = live ? fac[i / (kGroup / 4)] : 0.f;
-      split3(w.x * f, o[0]);
-      split3(w.y * f, o[1]);
-      split3(w.z * f, o[2]);
-      split3(w.w * f, o[3]);
+    const int n = (int)(p.pitch / 4);
+    constexpr int U = 4;
+    for (int i0 = t; i0 < n; i0 += U * kRowThreads) {
+      float4 w[U];
 #pragma unroll
-      for (int k = 0; k < 3; ++k) {
-        __nv_bfloat16* d = p.piece[k] + row * p.pitch + 4 * i;
-        *reinterpret_cast<__nv_bfloat162*>(d) = __halves2bfloat162(o[0][k], o[1][k]);
-        *reinterpret_cast<__nv_bfloat162*>(d + 2) = __halves2bfloat162(o[2][k], o[3][k]);
+      for (int k = 0; k < U; ++k)
+        w[k] = live && i0 + k * kRowThreads < n ? er[i0 + k * kRowThreads]
+                                                : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        const int i = i0 + k * kRowThreads;
+        if (i >= n) break;
+        const float f = live ? fac[i / (kGroup / 4)] : 0.f;
+        __nv_bfloat16* d[3];
+#pragma unroll
+        for (int j = 0; j < 3; ++j) d[j] = p.piece[j] + row * p.pitch + 4 * i;
+        store3(make_float4(w[k].x * f, w[k].y * f, w[k].z * f, w[k].w * f), d);
       }
     }
   }
@@ -1050,25 +1070,34 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   }
 }
 
-// The three bf16 pieces of `count` fp32 values (a multiple of 4).
-__global__ void __launch_bounds__(256)
-    head_split_kernel(const float4* __restrict__ src, long long quads, __nv_bfloat16* p0,
-                      __nv_bfloat16* p1, __nv_bfloat16* p2) {
+// The three bf16 pieces of two fp32 arrays (of quads * 4 values; the second may be empty).
+struct SplitArray {
+  const float4* src;
+  long long quads;
+  __nv_bfloat16* dst[3];
+};
+__global__ void __launch_bounds__(256) head_split_kernel(const SplitArray a, const SplitArray b) {
   pdl_trigger();
   pdl_wait();
-  const long long stride = (long long)gridDim.x * blockDim.x;
-  for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += stride) {
-    const float4 w = src[i];
-    __nv_bfloat16 o[4][3];
-    split3(w.x, o[0]);
-    split3(w.y, o[1]);
-    split3(w.z, o[2]);
-    split3(w.w, o[3]);
-    __nv_bfloat16* d[3] = {p0, p1, p2};
+  constexpr int U = 4;  // loads in flight per thread
+  const long long step = (long long)gridDim.x * blockDim.x, n = a.quads + b.quads;
+  for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < n; i0 += U * step) {
+    float4 w[U];
 #pragma unroll
-    for (int k = 0; k < 3; ++k) {
-      *reinterpret_cast<__nv_bfloat162*>(d[k] + 4 * i) = __halves2bfloat162(o[0][k], o[1][k]);
-      *reinterpret_cast<__nv_bfloat162*>(d[k] + 4 * i + 2) = __halves2bfloat162(o[2][k], o[3][k]);
+    for (int k = 0; k < U; ++k) {
+      const long long i = i0 + k * step;
+      if (i < n) w[k] = i < a.quads ? a.src[i] : b.src[i - a.quads];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const long long i = i0 + k * step;
+      if (i >= n) break;
+      const bool first = i < a.quads;
+      const long long at = 4 * (first ? i : i - a.quads);
+      __nv_bfloat16* d[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) d[j] = (first ? a.dst[j] : b.dst[j]) + at;
+      store3(w[k], d);
     }
   }
 }
@@ -1328,15 +1357,10 @@ struct HeadCall {
   size_t ws_bytes;
 };
 
-poetx_status run_split(const float* src, long long count, uint8_t* dst, size_t step, cudaStream_t s) {
-  POETX_CUDA_TRY(launch_pdl(head_split_kernel, dim3(grid_for(count / 4, 256)), dim3(256), 0, s,
-                            reinterpret_cast<const float4*>(src), count / 4,
-                            reinterpret_cast<__nv_bfloat16*>(dst),
-                            reinterpret_cast<__nv_bfloat16*>(dst + step),
-                            reinterpret_cast<__nv_bfloat16*>(dst + 2 * step)));
-  POETX_CUDA_TRY(cudaGetLastError());
-  after_launch(s, ST_HEAD_ROW);
-  return POETX_OK;
+SplitArray split_of(const float* src, long long count, uint8_t* dst, size_t step) {
+  SplitArray a{reinterpret_cast<const float4*>(src), count / 4, {}};
+  for (int j = 0; j < 3; ++j) a.dst[j] = reinterpret_cast<__nv_bfloat16*>(dst + j * step);
+  return a;
 }
 
 poetx_status run_head(const HeadCall& c, cudaStream_t s) {
@@ -1375,8 +1399,6 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
   const size_t w_step = align_up((size_t)c.V * c.D * 2, 1024);
   const size_t z_step = align_up((size_t)pl.rows * pl.Vp * 2, 1024);
   const int np = pl.f32 ? 3 : 1;
-  if (pl.f32)
-    POETX_TRY(run_split(static_cast<const float*>(c.W), (long long)c.V * c.D, w + pl.ws, w_step, s));
   float2* part = reinterpret_cast<float2*>(w + pl.part);
   float* tl = reinterpret_cast<float*>(w + pl.tl);
   float* unit = reinterpret_cast<float*>(w + pl.unit);
@@ -1387,9 +1409,16 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     const int rows = (int)((long long)c.N - r0 < pl.rows ? (long long)c.N - r0 : pl.rows);
     const uint8_t* xr = static_cast<const uint8_t*>(c.x) + (size_t)r0 * c.D * esz;
     const uint8_t* xp = pl.f32 ? w + pl.xs : xr;
-    if (pl.f32)
-      POETX_TRY(run_split(reinterpret_cast<const float*>(xr), (long long)rows * c.D, w + pl.xs,
-                          x_step, s));
+    if (pl.f32) {  // the pieces of these rows, and with the first ones of W
+      const SplitArray xa = split_of(reinterpret_cast<const float*>(xr), (long long)rows * c.D,
+                                     w + pl.xs, x_step);
+      const SplitArray wa = split_of(static_cast<const float*>(c.W), pc ? 0 : (long long)c.V * c.D,
+                                     w + pl.ws, w_step);
+      POETX_CUDA_TRY(launch_pdl(head_split_kernel, dim3(grid_for((xa.quads + wa.quads) / 4 + 1, 256)),
+                                dim3(256), 0, s, xa, wa));
+      POETX_CUDA_TRY(cudaGetLastError());
+      after_launch(s, ST_HEAD_ROW);
+    }
     // a teacher's entries: distinct columns in order
     const int32_t* idx = c.idx + r0 * c.K;
     const int32_t* ucol = idx;
