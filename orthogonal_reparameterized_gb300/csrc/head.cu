@@ -323,7 +323,14 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   } else if (LSE && warp == 1 && blockIdx.x == 1 && p.store) {
     // ------------------------------------------------------------ an idle warp: the unit of dz
     float top = 0.f;
-    for (int r = lane; r < p.prod[0].M; r += 32) top = fmaxf(top, fabsf(p.dloss[r]));
+    const int M = p.prod[0].M, quads = M / 4;
+    const float4* d4 = reinterpret_cast<const float4*>(p.dloss);
+#pragma unroll 4
+    for (int r = lane; r < quads; r += 32) {
+      const float4 w = d4[r];
+      top = fmaxf(fmaxf(top, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(w.z), fabsf(w.w)));
+    }
+    if (lane < M - 4 * quads) top = fmaxf(top, fabsf(p.dloss[4 * quads + lane]));
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) *p.unit = head_unit(top);
@@ -1243,6 +1250,7 @@ int dx_splits(long long rows, int D, int V, int nseg) {
 // 128-thousand vocabulary about a tenth of the piece's time).
 constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
 constexpr int kMaxTargets = 1024;
+constexpr long long kMaxRows = 1 << 16;  // of a piece (one warp looks through its upstream gradients)
 
 struct Plan {
   bool f32, grads;
@@ -1282,7 +1290,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
     rows = (long long)(kPieceBytes / row_bytes) / 256 * 256;
     if (rows < 256) rows = 256;
   }
-  if (rows > (1 << 18)) rows = 1 << 18;
+  if (rows > kMaxRows) rows = kMaxRows;
   o->pieces = ceil_div(n, rows);
   o->rows = o->pieces == 1 ? n : (long long)align_up((size_t)ceil_div(n, o->pieces), 256);
   o->pieces = ceil_div(n, o->rows);

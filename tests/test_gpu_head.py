@@ -255,6 +255,34 @@ def test_ce_in_pieces_of_rows(P, acc, N):
         assert err <= tol, (k, err)
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ce_many_rows(P, dt):
+    """More rows than a piece takes whatever its bytes: dW over three pieces."""
+    x, W, t, g = _inputs(150001, 7, 8, dt, 20)
+    t[::5] = -1
+    _near(_ce(P, x, W, t, g), H.head_ce(host(x), host(W), t, g), dt)
+    got = _ce(P, x, W, t, g, dx=False, dW=False)
+    _near(got, H.head_ce(host(x), host(W), t), dt)
+
+
+@pytest.mark.parametrize("N,V,D", [(3, 4194304, 8), (5, 300, 131072)])
+def test_ce_at_the_limits(P, N, V, D):
+    x, W, t, g = _inputs(N, V, D, "bf16", 21)
+    ref = H.head_ce(host(x), host(W), t, g)
+    _near(_ce(P, x, W, t, g), ref, "bf16")
+    _near(_ce(P, x, W, t, g, dx=False, dW=False), ref, "bf16")
+
+
+def test_ce_uneven_upstream_gradients(P):
+    """Upstream gradients over ten decades, zeros and signs among them; and all zero."""
+    x, W, t, g = _inputs(300, 700, 64, "bf16", 22)
+    r = np.random.default_rng(5)
+    g = (10.0 ** r.uniform(-10, 0, 300) * r.choice([-1, 1, 0], 300)).astype(np.float32)
+    _near(_ce(P, x, W, t, g), H.head_ce(host(x), host(W), t, g), "bf16")
+    got = _ce(P, x, W, t, np.zeros(300, np.float32))
+    assert not host(got["dx"]).any() and not host(got["dW"]).any()
+
+
 def test_head_on_another_stream(P):
     x, W, t, g = _inputs(300, 2000, 256, "bf16", 14)
     ref = _ce(P, x, W, t, g)
