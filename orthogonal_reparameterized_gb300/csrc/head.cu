@@ -521,13 +521,14 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   }
 }
 
-// ---------------------------------------------------------------- few rows, loss alone
-// The logits' product for at most 128 rows without gradients (a next token's score, a few sequences'
-// ends): bound by reading W once, so the roles are swapped.  W is the 128-row operand (one CTA, tiles
+// ---------------------------------------------------------------- few rows
+// The logits' product for at most 128 rows (a next token's score, a few sequences' ends, a short
+// step): bound by reading W once, so the roles are swapped.  W is the 128-row operand (one CTA, tiles
 // of `height` vocabulary rows, chosen so that every SM gets the same number of them), the NT (16 to
 // 128) padded tokens are the columns, and nearly all of the shared memory is a ring of W tiles in
 // flight.  A warp of the epilogue holds 32 vocabulary rows: it takes the targets out, turns its
-// 32 x NT logits over through shared memory and leaves one (max, sum) per token.
+// 32 x NT logits over through shared memory and leaves one (max, sum) per token and, where the
+// gradients are wanted, the 32 values exp(z - max) of each token in fp16.
 struct HeadScore {
   int tiles, height;       // height: a multiple of 8 (the swizzle's rows)
   int V, rows, stages;
@@ -539,6 +540,10 @@ struct HeadScore {
   const uint16_t* gstart;  // [rows][tiles + 1] first of them in each tile; NULL: K = 1
   int K;
   float* tl;               // [rows][K]
+  __half* e;               // [rows][pitch] exp(z - max); NULL: the loss alone
+  long long pitch;
+  const float* dloss;      // with e: [rows], whose largest magnitude goes to unit
+  float* unit;
   int* err;
   unsigned long long limit_ns;
 };
@@ -674,6 +679,13 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int q = warp & 3;
     float* tw = turn + q * 32 * (NT + 1);
     const float ninf = __int_as_float(0xff800000);
+    if (p.e && blockIdx.x == 0 && warp == 2) {
+      float top = 0.f;
+      for (int r = lane; r < p.rows; r += 32) top = fmaxf(top, fabsf(p.dloss[r]));
+#pragma unroll
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) *p.unit = head_unit(top);
+    }
     Ring<2> acc;
     bool ok = true;
     for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x) {
@@ -746,9 +758,25 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           m *= p.scale2;
           const float off = m == ninf ? 0.f : m;
           float sum = 0.f;
+          __half* er = p.e + c * p.pitch + v0 + q * 32;  // (v0 is a multiple of 8: 16-byte stores)
 #pragma unroll
-          for (int r = 0; r < 32; ++r) sum += ex2(fmaf(tw[r * (NT + 1) + c], p.scale2, -off));
+          for (int r = 0; r < 32; r += 8) {
+            uint32_t u[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float a = ex2(fmaf(tw[(r + 2 * i) * (NT + 1) + c], p.scale2, -off));
+              const float b = ex2(fmaf(tw[(r + 2 * i + 1) * (NT + 1) + c], p.scale2, -off));
+              sum += a + b;
+              const __half2 h = __floats2half2_rn(a, b);
+              u[i] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+            if (p.e && q * 32 + r < p.height && v0 + q * 32 + r < p.pitch)
+              *reinterpret_cast<uint4*>(er + r) = make_uint4(u[0], u[1], u[2], u[3]);
+          }
           p.part[(long long)c * (4 * p.tiles) + 4 * t + q] = make_float2(m, sum);
+          if (p.e && q == 0 && t == p.tiles - 1)  // the rest of the row's padding
+            for (long long k = (long long)p.tiles * p.height; k < p.pitch; k += 8)
+              *reinterpret_cast<uint4*>(p.e + c * p.pitch + k) = make_uint4(0u, 0u, 0u, 0u);
         }
       }
       __syncwarp();
@@ -817,6 +845,7 @@ __global__ void __launch_bounds__(256)
 struct RowArgs {
   int V, groups, K;
   long long pitch;        // columns of a row of e
+  int height;             // groups: 0: of 128 columns; else of 32 in each tile of `height` columns
   const float2* part;     // [rows][groups], log2 units
   const float* tl;        // [rows][K] logits of the distinct targets (before 1/T)
   const int32_t* idx;     // [rows][K] the targets as given
@@ -1020,7 +1049,12 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
         if (i >= n) break;
         uint4 o = make_uint4(0u, 0u, 0u, 0u);
         if (live) {
-          const float f = fac[i / (kGroup / 8)];
+          int g = i / (kGroup / 8);
+          if (p.height) {  // (columns past the last tile hold zeros)
+            const uint32_t tile = 8u * i / p.height;
+            g = min((int)(4 * tile + (8u * i - tile * p.height) / 32), p.groups - 1);
+          }
+          const float f = fac[g];
           const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
           uint32_t r[4];
 #pragma unroll
@@ -1250,6 +1284,7 @@ int dx_splits(long long rows, int D, int V, int nseg) {
 // 128-thousand vocabulary about a tenth of the piece's time).
 constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
 constexpr int kMaxTargets = 1024;
+constexpr int kMaxFactors = 32768;  // groups of a row with gradients (4194304 columns of 128)
 constexpr long long kMaxRows = 1 << 16;  // of a piece (one warp looks through its upstream gradients)
 
 struct Plan {
@@ -1259,7 +1294,7 @@ struct Plan {
   long long rows;    // rows of a piece
   int pieces;
   int splits;        // K splits of dx
-  int height, tiles;  // few rows, loss alone: vocabulary rows of a tile and tiles (else 0)
+  int height, tiles;  // few rows: vocabulary rows of a tile and tiles (else 0)
   // workspace offsets
   size_t unit, part, tl, ucol, slot, gstart, e, dz, xs, ws, acc, dxp, bytes;
 };
@@ -1272,13 +1307,18 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   o->Vp = (long long)align_up((size_t)V, 64);
   o->groups = ceil_div(V, kGroup);
   o->height = o->tiles = 0;
-  if (!o->f32 && !o->grads && N <= kScoreRows) {
+  if (!o->f32 && N <= kScoreRows) {
     // every SM the same number of tiles, of at most 128 rows; no lower than 16
     const int sms = sm_count(), each = ceil_div(V, (long long)sms * BM);
-    o->height = ceil_div(V, (long long)sms * each);
-    o->height = (int)align_up(o->height < 16 ? 16 : (size_t)o->height, 8);
-    o->tiles = ceil_div(V, o->height);
-    o->groups = 4 * o->tiles;
+    int height = ceil_div(V, (long long)sms * each);
+    height = (int)align_up(height < 16 ? 16 : (size_t)height, 8);
+    const int tiles = ceil_div(V, height);
+    // (with gradients the row kernel keeps a factor per group in shared memory: V up to a million)
+    if (!o->grads || 4 * tiles <= kMaxFactors) {
+      o->height = height;
+      o->tiles = tiles;
+      o->groups = 4 * tiles;
+    }
   }
   const size_t row_bytes = (o->grads ? (size_t)o->Vp * (o->f32 ? 10 : 2) : 0) +
                            (size_t)o->groups * 8 * (o->grads ? 1 : 4);
@@ -1462,6 +1502,10 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       h.gstart = gstart;
       h.K = c.K;
       h.tl = tl;
+      h.e = pl.grads ? reinterpret_cast<__half*>(w + pl.e) : nullptr;
+      h.pitch = pl.Vp;
+      h.dloss = c.dloss ? c.dloss + r0 : nullptr;
+      h.unit = unit;
       const bool maps = h.kps > 1 ? encode_tma_groups(&mp.a[0], wp, c.D, c.V, pl.height, h.kps) &&
                                         encode_tma_groups(&mp.b[0], xp, c.D, rows, nt, h.kps)
                                   : bf16_map(&mp.a[0], wp, c.D, c.V, 64, pl.height) &&
@@ -1513,6 +1557,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     ra.groups = pl.groups;
     ra.K = c.K;
     ra.pitch = pl.Vp;
+    ra.height = pl.height;
     ra.part = part;
     ra.tl = tl;
     ra.idx = idx;
