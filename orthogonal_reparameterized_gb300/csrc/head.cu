@@ -60,8 +60,11 @@ constexpr uint32_t kStgBytes = 32 * 128;             // one epilogue warp's box:
 // operand streams past.  Bands of 4, 8, 16 and 32 at 8192 x 128256 x 4096 with gradients: 17.7, 17.1,
 // 16.9 and 17.3 ms.
 constexpr int kBand = 16;
-constexpr int kGemmSmem = kStages * kStageBytes + kEpiWarps * kStgBytes + 1024 + 512;
-static_assert(kGemmSmem <= 227 * 1024, "head products: shared memory");
+constexpr int gemm_smem(int segs) {  // (see SEGS == 2 below)
+  return (segs == 2 ? (kStages - 1) * (int)(kStageBytes + kABytes) : kStages * (int)kStageBytes) +
+         kEpiWarps * (int)kStgBytes + 1024 + 512;
+}
+static_assert(gemm_smem(1) <= 227 * 1024 && gemm_smem(2) <= 227 * 1024, "head products: shared memory");
 constexpr int kMaxSegs = 6;
 
 struct HeadMaps {
@@ -178,18 +181,24 @@ __device__ __forceinline__ float head_unit(float top) { return top > 0.f && top 
 // first's last wave.  Warps 0 and 10 of each CTA load its 128 rows of A and its half of B, one thread
 // of the even CTA's warp 1 issues the MMAs, warps 2-9 read the accumulators back (warp w: rows
 // 32 (w % 4).. of the CTA's 128, columns 128 ((w - 2) / 4)..).
-template <bool LSE, bool F32>
+template <bool LSE, int SEGS>
 __global__ void __launch_bounds__(gemm_threads(LSE), 1)
     head_gemm_kernel(const __grid_constant__ HeadMaps maps0, const __grid_constant__ HeadMaps maps1,
                      const __grid_constant__ HeadGemm p) {
+  constexpr bool F32 = SEGS == kMaxSegs;
+  // SEGS == 2: both pieces of A and the one of B share a stage (B is loaded once)
+  constexpr bool BOTH = SEGS == 2;
+  constexpr int STAGES = BOTH ? kStages - 1 : kStages;
+  constexpr uint32_t B_OFF = BOTH ? 2 * kABytes : kABytes, STAGE = B_OFF + kBBytes;
+  constexpr int STEPS = BOTH ? 1 : SEGS;  // stages per K block
   constexpr uint32_t TMEM_COLS = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* staging = smem + kStages * kStageBytes;
+  uint8_t* staging = smem + STAGES * STAGE;
   uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStgBytes);
-  uint64_t* empty = full + kStages;
-  uint64_t* tfull = empty + kStages;  // [2] accumulator written
+  uint64_t* empty = full + STAGES;
+  uint64_t* tfull = empty + STAGES;  // [2] accumulator written
   uint64_t* tempty = tfull + 2;       // [2] accumulator read by both CTAs' epilogue warps
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
@@ -198,7 +207,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   const int crank = (int)cluster_ctarank();
   pdl_trigger();
   if (warp == 0 && lane == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
     }
@@ -228,11 +237,11 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
     // gradients: warp 0 loads A, warp 10 B (each up to two boxes); logits: warp 0 both (two warps
     // measured 3 % slower there, one 6 % slower for the gradients)
     const bool is_b = !LSE && warp == kBWarp;
-    Ring<kStages> rg;
+    Ring<STAGES> rg;
     bool ok = true;
     long long issued = 0;
     const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
-    uint8_t* const dst0 = smem + (is_b ? kABytes : 0);
+    uint8_t* const dst0 = smem + (is_b ? B_OFF : 0);
     for (int t = t0; t < p.num_tiles && ok; t += t_step) {
       const Tile c = tile_of(p, t);
       const HeadMaps& maps = c.which ? maps1 : maps0;
@@ -245,13 +254,13 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
       const bool expect = !is_b && crank == 0;
       for (int c0 = c.kb0; c0 < c.kb1 && ok; c0 += p.chunk) {
         const int len = min(c.kb1 - c0, p.chunk);
-        int sg = 0, i = 0;  // fp32: a chunk's K blocks once per pair of pieces
-        for (int j = 0; j < len * (F32 ? kMaxSegs : 1); ++j, rg.next(), ++issued) {
+        int sg = 0, i = 0;  // a chunk's K blocks once per pair of pieces
+        for (int j = 0; j < len * STEPS; ++j, rg.next(), ++issued) {
           if (!ring_wait(&empty[rg.s], rg.ph ^ 1, abort_flag, p, kSite + __LINE__)) {
             ok = false;
             break;
           }
-          uint8_t* dst = dst0 + rg.s * kStageBytes;
+          uint8_t* dst = dst0 + rg.s * STAGE;
           const int at = sg;
           const CUtensorMap* m = F32 ? &set[seg[at]] : set;
           const int k = (c0 + i) * BK;
@@ -259,15 +268,17 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
             i = 0;
             ++sg;
           }
-          if (expect) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
+          if (expect) mbar_arrive_expect_tx(&full[rg.s], 2 * STAGE);
           const uint32_t fb = full0 + rg.s * 8;
           if (how == 0) {
             tma_load_2d_pair(dst, m, fb, k, r0);
+            if (BOTH && !is_b) tma_load_2d_pair(dst + kABytes, set + 1, fb, k, r0);
             if (LSE)
-              tma_load_2d_pair(dst + kABytes, &maps.b[F32 ? p.seg_b[at] : 0], fb, k,
+              tma_load_2d_pair(dst + B_OFF, &maps.b[F32 ? p.seg_b[at] : 0], fb, k,
                                c.nt * BN + crank * (BN / 2));
           } else if (how == 1) {
             tma_load_3d_pair(dst, m, fb, 0, k, r0 / 64);
+            if (BOTH && !is_b) tma_load_3d_pair(dst + kABytes, set + 1, fb, 0, k, r0 / 64);
           } else {
             tma_load_2d_pair(dst, m, fb, r0, k);
             tma_load_2d_pair(dst + 8192, m, fb, r0 + 64, k);
@@ -276,12 +287,12 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
       }
     }
     // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
-    for (long long j = issued - 1; j >= 0 && j >= issued - kStages; --j)
-      mbar_wait_bounded(&empty[j % kStages], (uint32_t)((j / kStages) & 1), p.err, p.limit_ns,
+    for (long long j = issued - 1; j >= 0 && j >= issued - STAGES; --j)
+      mbar_wait_bounded(&empty[j % STAGES], (uint32_t)((j / STAGES) & 1), p.err, p.limit_ns,
                         kSite + __LINE__);
   } else if (warp == 1 && lane == 0 && crank == 0) {
     // ------------------------------------------------------------ MMA issuer
-    Ring<kStages> rg;
+    Ring<STAGES> rg;
     Ring<2> acc;
     bool any = false;
     // one tile; the operands' orders are compile-time constants (as run-time values they cost the
@@ -293,16 +304,20 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
         if (!ring_wait(&tempty[acc.s], acc.ph ^ 1, abort_flag, p, kSite + __LINE__)) return false;
         tc_fence_after();
         const uint32_t d = tmem_base + (uint32_t)(acc.s * BN);
-        const int blocks = (min(c.kb1, kb + p.chunk) - kb) * (F32 ? kMaxSegs : 1);
+        const int blocks = (min(c.kb1, kb + p.chunk) - kb) * STEPS;
         for (int j = 0; j < blocks; ++j, rg.next()) {
           if (!ring_wait(&full[rg.s], rg.ph, abort_flag, p, kSite + __LINE__)) return false;
           tc_fence_after();
-          const uint32_t a_base = smem_base + rg.s * kStageBytes;
-          const uint64_t ad = tile_desc<A_MN>(a_base), bd = tile_desc<B_MN>(a_base + kABytes);
+          const uint32_t a_base = smem_base + rg.s * STAGE;
+          const uint64_t bd = tile_desc<B_MN>(a_base + B_OFF);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
-            umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
-                           (j | k) != 0);
+          for (int pc = BOTH ? 1 : 0; pc >= 0; --pc) {  // the small piece first
+            const uint64_t ad = tile_desc<A_MN>(a_base + pc * kABytes);
+#pragma unroll
+            for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
+              umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
+                             (j | k) != 0 || pc != (BOTH ? 1 : 0));
+          }
           umma_commit_pair(&empty[rg.s]);
         }
         umma_commit_pair(&tfull[acc.s]);
@@ -858,7 +873,7 @@ struct RowArgs {
   float* loss;
   float* lse;             // nullable
   void* e;                // exp(z - m) of the rows, turned into dz (nullable: loss only)
-  __nv_bfloat16* piece[3];  // fp32 heads: dz in three bf16 pieces
+  __nv_bfloat16* piece[3];  // fp32 heads: dz in three bf16 pieces; bf16 ones: [1] its second (nullable)
 };
 
 constexpr int kRowThreads = 256;
@@ -886,6 +901,11 @@ __device__ __forceinline__ void block_reduce2(float& a, float& b, float2* red) {
     a = MAX ? fmaxf(a, w[i].x) : a + w[i].x;
     b = MAX ? fmaxf(b, w[i].y) : b + w[i].y;
   }
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 
 __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
@@ -1035,6 +1055,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   __syncthreads();
   if (!F32) {
     uint4* er = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e) + row * p.pitch);
+    uint4* second = p.piece[1] ? reinterpret_cast<uint4*>(p.piece[1] + row * p.pitch) : nullptr;
     const int n = (int)(p.pitch / 8);
     constexpr int U = 4;  // loads in flight per thread
     for (int i0 = t; i0 < n; i0 += U * kRowThreads) {
@@ -1047,7 +1068,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
       for (int k = 0; k < U; ++k) {
         const int i = i0 + k * kRowThreads;
         if (i >= n) break;
-        uint4 o = make_uint4(0u, 0u, 0u, 0u);
+        uint4 o = make_uint4(0u, 0u, 0u, 0u), o2 = o;
         if (live) {
           int g = i / (kGroup / 8);
           if (p.height) {  // (columns past the last tile hold zeros)
@@ -1056,14 +1077,25 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
           }
           const float f = fac[g];
           const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
-          uint32_t r[4];
+          float v[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 v = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
-            r[j] = pack_bf16x2(v.x * f, v.y * f);
+            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            v[2 * j] = h.x * f;
+            v[2 * j + 1] = h.y * f;
           }
-          o = make_uint4(r[0], r[1], r[2], r[3]);
+          o = pack8(v);
+          if (second) {
+            const uint32_t r[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              v[2 * j] -= __uint_as_float(r[j] << 16);
+              v[2 * j + 1] -= __uint_as_float(r[j] & 0xffff0000u);
+            }
+            o2 = pack8(v);
+          }
         }
+        if (second) second[i] = o2;
         er[i] = o;
       }
     }
@@ -1101,7 +1133,10 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
       dz = coef * pv - gT * qs[u];
     const int c = ucol[u];
     if (!F32) {
-      static_cast<__nv_bfloat16*>(p.e)[row * p.pitch + c] = __float2bfloat16_rn(dz);
+      const __nv_bfloat16 hi = __float2bfloat16_rn(dz);
+      static_cast<__nv_bfloat16*>(p.e)[row * p.pitch + c] = hi;
+      if (p.piece[1])
+        p.piece[1][row * p.pitch + c] = __float2bfloat16_rn(dz - __bfloat162float(hi));
     } else {
       __nv_bfloat16 o[3];
       split3(dz, o);
@@ -1199,19 +1234,19 @@ poetx_status score(const CUtensorMap& mW, const CUtensorMap& mx, HeadScore p, cu
 }
 
 // Co-resident CTA pairs of a GEMM kernel (one CTA per SM).
-template <bool LSE, bool F32>
+template <bool LSE, int SEGS>
 cudaError_t gemm_pairs(int* pairs) {
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int max_pairs = 0;
   std::call_once(once, [&] {
-    auto k = head_gemm_kernel<LSE, F32>;
-    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kGemmSmem);
+    auto k = head_gemm_kernel<LSE, SEGS>;
+    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem(SEGS));
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sm_count() / 2 * 2);
     cfg.blockDim = dim3(gemm_threads(LSE));
-    cfg.dynamicSmemBytes = kGemmSmem;
+    cfg.dynamicSmemBytes = gemm_smem(SEGS);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
     attr[0].val.clusterDim.x = 2;
@@ -1226,10 +1261,10 @@ cudaError_t gemm_pairs(int* pairs) {
   return attr_err;
 }
 
-template <bool LSE, bool F32>
+template <bool LSE, int SEGS>
 poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStream_t s) {
   int max_pairs = 0;
-  POETX_CUDA_TRY((gemm_pairs<LSE, F32>(&max_pairs)));
+  POETX_CUDA_TRY((gemm_pairs<LSE, SEGS>(&max_pairs)));
   long long tiles = 0;
   for (const Product& d : p.prod) {
     if ((long long)d.tiles_m * d.tiles_n > 0x3fffffffLL) return POETX_ERR_SHAPE;
@@ -1240,9 +1275,9 @@ poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStrea
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
   const int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
-  POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, F32>, dim3(2 * pairs),
+  POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, SEGS>, dim3(2 * pairs),
                                     dim3(gemm_threads(LSE)),
-                                    kGemmSmem, s, 2, m0, m1, p));
+                                    gemm_smem(SEGS), s, 2, m0, m1, p));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_HEAD_GEMM);
   return POETX_OK;
@@ -1284,11 +1319,16 @@ int dx_splits(long long rows, int D, int V, int nseg) {
 // 128-thousand vocabulary about a tenth of the piece's time).
 constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
 constexpr int kMaxTargets = 1024;
+// Rows up to which dz is kept in two bf16 pieces: the rounding of a few large p - q is not averaged
+// over many rows there (error of dx against the output's own rounding: 1.54 times with one piece, 1.0
+// with two), and the products are bound by W and dW, not by the tensor pipe.
+constexpr int kFineRows = 16;
 constexpr int kMaxFactors = 32768;  // groups of a row with gradients (4194304 columns of 128)
 constexpr long long kMaxRows = 1 << 16;  // of a piece (one warp looks through its upstream gradients)
 
 struct Plan {
   bool f32, grads;
+  bool fine;         // bf16, few rows: dz in two pieces
   long long Vp;      // columns of a stored row
   int groups;
   long long rows;    // rows of a piece
@@ -1296,7 +1336,7 @@ struct Plan {
   int splits;        // K splits of dx
   int height, tiles;  // few rows: vocabulary rows of a tile and tiles (else 0)
   // workspace offsets
-  size_t unit, part, tl, ucol, slot, gstart, e, dz, xs, ws, acc, dxp, bytes;
+  size_t unit, part, tl, ucol, slot, gstart, e, dz, dz2, xs, ws, acc, dxp, bytes;
 };
 
 bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o) {
@@ -1304,6 +1344,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
     return false;
   o->f32 = dt == POETX_F32;
   o->grads = dx || dW;
+  o->fine = !o->f32 && o->grads && N <= kFineRows;
   o->Vp = (long long)align_up((size_t)V, 64);
   o->groups = ceil_div(V, kGroup);
   o->height = o->tiles = 0;
@@ -1351,6 +1392,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   o->gstart = take(R * ((o->tiles ? o->tiles : o->groups) + 1) * 2);
   o->e = o->grads ? take(R * o->Vp * (o->f32 ? 4 : 2)) : 0;
   o->dz = o->f32 && o->grads ? take(3 * align_up(R * o->Vp * 2, 1024)) : o->e;
+  o->dz2 = o->fine ? take(R * o->Vp * 2) : 0;
   o->xs = o->f32 ? take(3 * align_up(R * D * 2, 1024)) : 0;
   o->ws = o->f32 ? take(3 * align_up((size_t)V * D * 2, 1024)) : 0;
   o->acc = !o->f32 && dW && o->pieces > 1 ? take((size_t)V * D * 4) : 0;
@@ -1370,18 +1412,18 @@ bool mn_map(CUtensorMap* m, const void* p, long long inner, long long outer) {
                          : bf16_map(m, p, inner, outer, 64, 64);
 }
 
+// Operand pieces and the K of one accumulator.  fp32: small pieces first, so that the accumulator is
+// small while they are added (a chunk runs pair by pair of pieces: the adds at full size are those of
+// the last pair); 256 of K (16 adds of 16 products at full size; 64: a fifth slower).  bf16: 1024 for
+// the logits (64 adds: losses to 7e-7 at K = 2048), or 256 for few rows, whose products are not what
+// their time goes into (one row's loss: 1.3e-6 with 1024, 2e-7 with 256); 4096 for the gradients, which
+// are rounded to bf16 (256 adds: 1.5e-5).
 void set_segs(HeadGemm* g, bool f32, bool lse, int rows) {
-  // small pieces first, so that the accumulator is small while they are added (a chunk runs pair by
-  // pair of pieces: the adds at full size are those of the last pair)
   static const int8_t a[kMaxSegs] = {1, 0, 2, 1, 0, 0}, b[kMaxSegs] = {1, 2, 0, 0, 1, 0};
   for (int i = 0; i < kMaxSegs; ++i) {
     g->seg_a[i] = a[i];
     g->seg_b[i] = b[i];
   }
-  // K of one accumulator: 256 in fp32 (16 adds of 16 products at full size; 64: a fifth slower); in
-  // bf16 4096 for the gradients, which are rounded to bf16 (256 adds: 1.5e-5), and for the logits
-  // 1024 (64 adds: losses to 7e-7 at K = 2048), or 256 for few rows, whose products are not what
-  // their time goes into (one row's loss: 1.3e-6 with 1024, 2e-7 with 256)
   g->chunk = f32 ? 4 : (lse ? (rows <= 512 ? 4 : 16) : 64);
 }
 
@@ -1529,7 +1571,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       lg.tiles_n = ceil_div(c.V, BN);
       lg.num_tiles = lg.tiles_m * lg.tiles_n;
       lg.num_kb = lg.kb_split = ceil_div(c.D, BK);
-      lg.M = rows;
+        lg.M = rows;
       lg.N = c.V;
       lg.n_store = (int)pl.Vp;  // columns V .. Vp - 1 are stored as zeros
       g.scale2 = kLog2e / c.T;
@@ -1547,9 +1589,9 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
         return POETX_ERR_CUDA;
       if (!pl.grads) mp.c = mp.a[0];
       if (pl.f32)
-        POETX_TRY((gemm<true, true>(mp, mp, g, s)));
+        POETX_TRY((gemm<true, kMaxSegs>(mp, mp, g, s)));
       else
-        POETX_TRY((gemm<true, false>(mp, mp, g, s)));
+        POETX_TRY((gemm<true, 1>(mp, mp, g, s)));
     }
     // rows: lse, loss, dz
     RowArgs ra{};
@@ -1571,8 +1613,11 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     ra.lse = c.lse ? c.lse + r0 : nullptr;
     ra.unit = unit;
     ra.e = pl.grads ? w + pl.e : nullptr;
-    for (int i = 0; i < 3; ++i)
-      ra.piece[i] = reinterpret_cast<__nv_bfloat16*>(w + pl.dz + i * z_step);
+    if (pl.f32)
+      for (int i = 0; i < 3; ++i)
+        ra.piece[i] = reinterpret_cast<__nv_bfloat16*>(w + pl.dz + i * z_step);
+    else if (pl.fine)
+      ra.piece[1] = reinterpret_cast<__nv_bfloat16*>(w + pl.dz2);
     if (pl.f32)
       POETX_CUDA_TRY(launch_pdl(head_row_kernel<true>, dim3(rows), dim3(kRowThreads), row_smem, s, ra));
     else
@@ -1582,6 +1627,9 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     if (!pl.grads) continue;
     // dx = dz W and dW (+)= dz^T x; between the pieces of a bf16 head dW's sum stays in fp32
     HeadGemm h{};
+    const uint8_t* zp[3];  // dz's pieces
+    const int nz = pl.f32 ? 3 : (pl.fine ? 2 : 1);
+    for (int i = 0; i < 3; ++i) zp[i] = pl.fine && i ? w + pl.dz2 : w + pl.dz + i * z_step;
     set_segs(&h, pl.f32, false, rows);
     h.out_scale = unit;
     h.T = c.T;
@@ -1590,10 +1638,10 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     const int c_rows = (int)align_up((size_t)rows, 256);
     if (c.dx) {
       Product& d = h.prod[used++];
+      for (int i = 0; i < nz; ++i)
+        if (!bf16_map(&mp.a[i], zp[i], pl.Vp, rows, 64, 128)) return POETX_ERR_CUDA;
       for (int i = 0; i < np; ++i)
-        if (!bf16_map(&mp.a[i], w + pl.dz + i * z_step, pl.Vp, rows, 64, 128) ||
-            !mn_map(&mp.b[i], wp + i * w_step, c.D, c.V))
-          return POETX_ERR_CUDA;
+        if (!mn_map(&mp.b[i], wp + i * w_step, c.D, c.V)) return POETX_ERR_CUDA;
       d.b_groups = c.D % 64 == 0;
       d.tiles_m = ceil_div(rows, 2 * BM);
       d.tiles_n = ceil_div(c.D, BN);
@@ -1613,10 +1661,10 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     if (c.dW) {
       Product& d = h.prod[used];
       HeadMaps& m = used++ ? mw : mp;
+      for (int i = 0; i < nz; ++i)
+        if (!mn_map(&m.a[i], zp[i], pl.Vp, rows)) return POETX_ERR_CUDA;
       for (int i = 0; i < np; ++i)
-        if (!mn_map(&m.a[i], w + pl.dz + i * z_step, pl.Vp, rows) ||
-            !mn_map(&m.b[i], xp + i * x_step, c.D, rows))
-          return POETX_ERR_CUDA;
+        if (!mn_map(&m.b[i], xp + i * x_step, c.D, rows)) return POETX_ERR_CUDA;
       d.b_groups = c.D % 64 == 0;
       d.tiles_m = ceil_div(c.V, 2 * BM);
       d.tiles_n = ceil_div(c.D, BN);
@@ -1638,10 +1686,13 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
                          true))
         return POETX_ERR_CUDA;
     }
+    const HeadMaps& second = used > 1 ? mw : mp;
     if (pl.f32)
-      POETX_TRY((gemm<false, true>(mp, used > 1 ? mw : mp, h, s)));
+      POETX_TRY((gemm<false, kMaxSegs>(mp, second, h, s)));
+    else if (pl.fine)
+      POETX_TRY((gemm<false, 2>(mp, second, h, s)));
     else
-      POETX_TRY((gemm<false, false>(mp, used > 1 ? mw : mp, h, s)));
+      POETX_TRY((gemm<false, 1>(mp, second, h, s)));
     if (c.dx && pl.splits > 1) {
       const long long quads = (long long)rows * c.D / 4;
       const float* pp = reinterpret_cast<const float*>(w + pl.dxp);
