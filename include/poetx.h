@@ -508,9 +508,10 @@ poetx_status poetx_layernorm_bwd(poetx_dtype dt, const void* x, const void* dy, 
  *           accumulate != 0 adds dW to its contents (dx is always overwritten).
  *   ws      scratch of poetx_head_workspace_bytes(dt, N, D, V, 1, dx != NULL, dW != NULL) bytes
  * bf16: products of bf16 operands summed in fp32; dz is rounded to bf16 for the gradients'
- * products, dx and dW are rounded once (over all rows).  fp32: about fp32 accuracy throughout.
- * With gradients, rows are taken in pieces, so that at most about 2 GB of 16-bit exponentials is
- * held at a time (or as much as the fp32 sums of dW that pieces need would take besides).  Outputs must not alias inputs.  z_loss >= 0. */
+ * products (to two bf16 pieces where N <= 16), dx and dW are rounded once (over all rows).  fp32:
+ * about fp32 accuracy throughout.  With gradients, rows are taken in pieces, so that at most about
+ * 2 GB of 16-bit exponentials is held at a time (or as much as the fp32 sums of dW that pieces need
+ * would take besides).  Outputs must not alias inputs.  z_loss >= 0. */
 size_t poetx_head_workspace_bytes(poetx_dtype dt, int N, int D, int V, int K, int want_dx,
                                   int want_dW);
 poetx_status poetx_head_ce(poetx_dtype dt, const void* x, int N, int D, const void* W, int V,

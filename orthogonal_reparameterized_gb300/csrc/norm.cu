@@ -96,7 +96,7 @@ __device__ __forceinline__ void group_sum(float (&s)[NS], float (*red)[kThreads 
   }
 }
 
-// Few rows, or wide ones: a row per group of TPR threads, NV vectors of VEC elements per thread
+// Few rows, or wide or odd ones (1 x 4096: 4 us, latency): a row per group of TPR threads, NV vectors of VEC elements per thread
 // (NV * TPR * VEC >= D; D a multiple of VEC).
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(kThreads)
@@ -158,6 +158,8 @@ __global__ void __launch_bounds__(kThreads)
 // ...), gamma and beta staged in shared memory once per CTA.  No barrier between rows, so the warps of
 // an SM are at different phases of load, sums and store.  gamma and beta lie in planes of 16 bytes per
 // vector (plane k: elements 4 k .. 4 k + 3 of every vector), which a warp reads without conflicts.
+// 8192 x 4096 bf16: 26.8 us, 5.0 TB/s (0.75 of a plain copy's rate); bound by latency at 14 warps per
+// SM, whose rows fill the registers.
 template <typename T, int VEC, int NV>
 __global__ void __launch_bounds__(kThreads, 2)
     layernorm_fwd_rows_kernel(const T* __restrict__ x, int N, int D, const float* __restrict__ gamma,
@@ -556,8 +558,10 @@ __global__ void __launch_bounds__(kRingThreads)
   if (t == 0) ring.drain(err, limit_ns);
 }
 
-// Backward: a thread keeps gamma and the sums of dy h and dy of its columns; one join per row.  At the
-// end the groups' sums are added through shared memory, so that there is one row of partials per SM.
+// Backward: a thread keeps gamma and the sums of dy h and dy of its columns; one join for two rows.  At
+// the end the groups' sums are added through shared memory, so that there is one row of partials per SM.
+// 8192 x 4096 bf16: 40.2 us with the reduction, 5.0 TB/s; without its loads and stores it takes 30 us
+// (320 instructions per warp and row, and the join's chain).
 template <typename T, int NV, int GROUPS>
 __global__ void __launch_bounds__(kRingThreads)
     layernorm_bwd_ring_kernel(const T* __restrict__ x, const T* __restrict__ dy, int N, int D,
