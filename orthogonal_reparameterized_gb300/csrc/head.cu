@@ -235,7 +235,9 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t smem_base = smem_u32(smem);
-  pdl_wait();
+  // With target lists the kernel before this one made them, and started it after everything earlier
+  // was complete: only the epilogue, which reads the lists and writes, waits for it.
+  if (!LSE || !p.gstart || (warp >= 2 && warp < kBWarp)) pdl_wait();
   const int t0 = (int)blockIdx.x / 2, t_step = (int)gridDim.x / 2;
 
   if ((warp == 0 || warp == kBWarp) && lane == 0) {
@@ -622,7 +624,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   tc_fence_after();
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t smem_base = smem_u32(smem);
-  pdl_wait();
+  if (!p.gstart || warp >= 2) pdl_wait();  // (as in the products: the copies need not wait for the lists)
   auto wait = [&](uint64_t* bar, uint32_t parity, int site) -> bool {
     if (mbar_try_wait(bar, parity)) return true;
     if (*abort_flag || !mbar_wait_bounded(bar, parity, p.err, p.limit_ns, site)) {
@@ -816,53 +818,112 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
 
 // ---------------------------------------------------------------- CUDA-core kernels
 constexpr uint16_t kNoSlot = 0xffff;
+constexpr int kMaxTargets = 1024;
 
 // A row's K target columns: slot[k] = place of idx[k] among the row's distinct columns in ascending
 // order (kNoSlot for an absent entry or one beyond the vocabulary), ucol = those columns, gstart =
-// the first of them in each group of `width` columns.  By ranks: K is at most a thousand (2047 rows of
-// 64: 20 us, latency).
-__global__ void __launch_bounds__(256)
+// the first of them in each group of `width` columns.  A sort by ranks (K is at most a thousand; each
+// thread compares its entry with all others, four per read), then a scan of the changes of column.  The
+// logits' product needs the lists in its epilogue only, and starts beside this kernel: the trigger comes
+// after the wait, so that what precedes this kernel is complete when the next one's copies begin.
+constexpr int kListThreads = 256;
+__global__ void __launch_bounds__(kListThreads)
     head_targets_kernel(const int32_t* __restrict__ idx, int K, int V, int groups, int width,
                         uint16_t* __restrict__ slot, int32_t* __restrict__ ucol,
                         uint16_t* __restrict__ gstart) {
-  extern __shared__ int tsm[];
-  int* is = tsm;           // [K] columns
-  int* first = is + K;     // [K] whether it is the column's first entry
-  int* us = first + K;     // [K] distinct columns, ascending
-  __shared__ int nu;
-  pdl_trigger();
+  extern __shared__ __align__(16) int tsm[];
+  const int K4 = (K + 3) / 4 * 4;
+  int* is = tsm;         // [K4] columns, none: the largest integer
+  int* ss = is + K4;     // [K4] sorted, then the distinct ones
+  int* sl = ss + K4;     // [K4] slot of each sorted place
+  __shared__ int warp_sum[kListThreads / 32];
+  constexpr int NONE = 0x7fffffff;
   pdl_wait();
+  pdl_trigger();
   const long long row = blockIdx.x;
   const int t = threadIdx.x;
-  if (t == 0) nu = 0;
-  for (int k = t; k < K; k += 256) is[k] = idx[row * K + k];
-  __syncthreads();
-  for (int k = t; k < K; k += 256) {
-    const int c = is[k];
-    bool f = c >= 0 && c < V;
-    for (int j = 0; j < k && f; ++j) f = is[j] != c;
-    first[k] = f;
-    if (f) atomicAdd(&nu, 1);
+  for (int k = t; k < K4; k += kListThreads) {
+    const int c = k < K ? idx[row * K + k] : NONE;
+    is[k] = c >= 0 && c < V ? c : NONE;
+    ss[k] = NONE;
   }
   __syncthreads();
-  for (int k = t; k < K; k += 256) {
-    const int c = is[k];
-    int r = 0;
-    if (c >= 0 && c < V) {
-      for (int j = 0; j < K; ++j) r += first[j] && is[j] < c;
-      if (first[k]) us[r] = c;
-    } else {
-      r = kNoSlot;
+  constexpr int EACH = kMaxTargets / kListThreads;  // entries of a thread
+  int pos[EACH];
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int k = t + e * kListThreads;
+    pos[e] = -1;
+    if (k < K && is[k] != NONE) {
+      const int c = is[k];
+      int r = 0;  // smaller ones, and equal ones before it
+      for (int j = 0; j < K4; j += 4) {
+        const int4 w = *reinterpret_cast<const int4*>(is + j);
+        r += (w.x < c || (w.x == c && j < k)) + (w.y < c || (w.y == c && j + 1 < k)) +
+             (w.z < c || (w.z == c && j + 2 < k)) + (w.w < c || (w.w == c && j + 3 < k));
+      }
+      pos[e] = r;
+      ss[r] = c;
     }
-    slot[row * K + k] = (uint16_t)r;
   }
   __syncthreads();
-  const int n = nu;
+  // slot of place p: the changes of column up to it, less one; a thread takes neighbouring places
+  const int per = (K4 + kListThreads - 1) / kListThreads;
+  int own[EACH], n = 0;
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int p = t * per + e;
+    own[e] = 0;
+    if (e < per && p < K4 && ss[p] != NONE) own[e] = p == 0 || ss[p] != ss[p - 1];
+    n += own[e];
+  }
+  int scan = n;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, scan, o);
+    if ((t & 31) >= o) scan += v;
+  }
+  if ((t & 31) == 31) warp_sum[t >> 5] = scan;
+  __syncthreads();
+  int total = 0, before = scan - n;
+#pragma unroll
+  for (int w = 0; w < kListThreads / 32; ++w) {
+    if (w < (t >> 5)) before += warp_sum[w];
+    total += warp_sum[w];
+  }
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    const int p = t * per + e;
+    if (e < per && p < K4) {
+      before += own[e];
+      sl[p] = before - 1;
+      own[e] = own[e] ? ss[p] : NONE;  // the column, where it begins here
+    } else {
+      own[e] = NONE;
+    }
+  }
+  __syncthreads();  // ss has been read
+#pragma unroll
+  for (int e = 0; e < EACH; ++e) {
+    if (own[e] != NONE) {
+      const int u = sl[t * per + e];
+      ss[u] = own[e];
+      ucol[row * K + u] = own[e];
+    }
+    const int k = t + e * kListThreads;
+    if (k < K) slot[row * K + k] = pos[e] < 0 ? kNoSlot : (uint16_t)sl[pos[e]];
+  }
+  __syncthreads();
   uint16_t* gs = gstart + row * (groups + 1);
-  for (int u = t; u <= n; u += 256) {  // groups after the previous column's, up to this one's
-    const int lo = u ? us[u - 1] / width + 1 : 0, hi = u < n ? us[u] / width : groups;
-    for (int g = lo; g <= hi; ++g) gs[g] = (uint16_t)u;
-    if (u < n) ucol[row * K + u] = us[u];
+  for (int g = t; g <= groups; g += kListThreads) {  // the distinct columns below the group's first
+    const long long c = (long long)g * width;
+    int lo = 0, hi = total;
+    while (lo < hi) {
+      const int mid = (lo + hi) >> 1;
+      if (ss[mid] < c) lo = mid + 1;
+      else hi = mid;
+    }
+    gs[g] = (uint16_t)lo;
   }
 }
 
@@ -1330,7 +1391,6 @@ int dx_splits(long long rows, int D, int V, int nseg) {
 // first reads and writes dW's fp32 sums (8 V D bytes against 6 rows V D flops: at 2 GB per piece of a
 // 128-thousand vocabulary about a tenth of the piece's time).
 constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
-constexpr int kMaxTargets = 1024;
 // Rows up to which dz is kept in two bf16 pieces: the rounding of a few large p - q is not averaged
 // over many rows there (error of dx against the output's own rounding: 1.54 times with one piece, 1.0
 // with two), and the products are bound by W and dW, not by the tensor pipe.
@@ -1529,7 +1589,8 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     if (c.tlogit) {
       int32_t* u = reinterpret_cast<int32_t*>(w + pl.ucol);
       gstart = reinterpret_cast<uint16_t*>(w + pl.gstart);
-      POETX_CUDA_TRY(launch_pdl(head_targets_kernel, dim3(rows), dim3(256), (size_t)c.K * 12, s, idx,
+      POETX_CUDA_TRY(launch_pdl(head_targets_kernel, dim3(rows), dim3(kListThreads),
+                                align_up((size_t)c.K, 4) * 12, s, idx,
                                 c.K, c.V, pl.tiles ? pl.tiles : pl.groups,
                                 pl.tiles ? pl.height : kGroup, slot, u, gstart));
       POETX_CUDA_TRY(cudaGetLastError());
