@@ -1006,8 +1006,10 @@ __device__ __forceinline__ void store3(float4 w, __nv_bfloat16* const (&d)[3]) {
 // e read and written (4096 x 32000: 524 MB in 85 us, 6.2 TB/s; 8192 x 128256: 0.64 ms, 6.6 TB/s).
 template <bool F32>
 __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) {
-  extern __shared__ float sm[];
-  float* fac = sm;            // [groups] factor of each group (with e)
+  extern __shared__ __align__(16) float sm[];
+  const int K8 = (p.K + 7) / 8 * 8;
+  uint16_t* ks = reinterpret_cast<uint16_t*>(sm);  // [K8] slots of the entries (distillation)
+  float* fac = sm + K8 / 2;   // [groups] factor of each group (with e)
   float* z2 = fac + (p.e ? p.groups : 0);  // [K] the distinct targets' logits in log2 units
   float* qs = z2 + p.K;       // [K] their weights q
   float* qk = qs + p.K;       // [K] the entries' weights
@@ -1035,10 +1037,11 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     nu = c >= 0 && c < p.V;
   } else {
     float nbad = 0.f, top = -1.f;  // (slots are below 1024: exact in fp32)
-    for (int k = t; k < p.K; k += kRowThreads) {
-      const int c = idx[k];
+    for (int k = t; k < K8; k += kRowThreads) {
+      const int c = k < p.K ? idx[k] : -1;
+      ks[k] = k < p.K ? slot[k] : kNoSlot;
       if (c >= p.V) nbad = 1.f;
-      if (c >= 0 && c < p.V) top = fmaxf(top, (float)slot[k]);
+      if (c >= 0 && c < p.V) top = fmaxf(top, (float)ks[k]);
     }
     block_reduce2<true>(nbad, top, red);
     bad = nbad > 0.f;
@@ -1095,11 +1098,11 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     float l = 0.f;
     for (int k = t; k < p.K; k += kRowThreads) {
       float q = 0.f;
-      if (slot[k] != kNoSlot && some > 0.f) {
+      if (ks[k] != kNoSlot && some > 0.f) {
         const float lq = u[k] * invT - tm - lus;
         q = expf(lq);
-        if (q > 0.f) l += q * (lq - (slot[k] == umax ? lnp_max : (z2[slot[k]] - lse2) * kLn2));
-        if (slot[k] != umax) rest += q;
+        if (q > 0.f) l += q * (lq - (ks[k] == umax ? lnp_max : (z2[ks[k]] - lse2) * kLn2));
+        if (ks[k] != umax) rest += q;
       }
       qk[k] = q;
     }
@@ -1109,8 +1112,15 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     // weights per distinct column, the entries added in their order
     for (int v = t; v < nu && p.e; v += kRowThreads) {
       float q = 0.f;
-      for (int k = 0; k < p.K; ++k)
-        if (slot[k] == v) q += qk[k];
+      for (int k = 0; k < K8; k += 8) {
+        const uint4 w = *reinterpret_cast<const uint4*>(ks + k);
+        const uint32_t x[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          if ((x[j] & 0xffffu) == (uint32_t)v) q += qk[k + 2 * j];
+          if ((x[j] >> 16) == (uint32_t)v) q += qk[k + 2 * j + 1];
+        }
+      }
       qs[v] = q;
     }
   }
@@ -1544,7 +1554,8 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
   if (!c.x || !c.W || !c.idx || !c.loss || !c.ws || (pl.grads && !c.dloss)) return POETX_ERR_ARG;
   if (c.ws_bytes < pl.bytes) return POETX_ERR_WORKSPACE;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
-  const size_t row_smem = (pl.grads ? (size_t)pl.groups * 4 : 0) + (size_t)c.K * 12;
+  const size_t row_smem = align_up((size_t)c.K, 8) * 2 + (pl.grads ? (size_t)pl.groups * 4 : 0) +
+                          (size_t)c.K * 12;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [] {
