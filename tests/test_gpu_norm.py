@@ -132,3 +132,29 @@ def test_layernorm_on_another_stream(P):
     s.synchronize()
     assert torch.equal(dx, ref["dx"]) and torch.equal(dg, ref["dgamma"])
     assert torch.equal(db, ref["dbeta"])
+
+
+def test_layernorm_beyond_32_bit_offsets(P):
+    """More than 2^31 elements: the last rows are the same as in a call of their own."""
+    N, D = 264000, 8200
+    free, _ = torch.cuda.mem_get_info()
+    if free < 6 * N * D * 2:
+        pytest.skip("needs 26 GB")
+    g = torch.Generator(device=DEV).manual_seed(4)
+    x = torch.zeros(N, D, dtype=torch.bfloat16, device=DEV)
+    dy = torch.zeros_like(x)
+    tail = 40
+    x[-tail:] = torch.randn(tail, D, generator=g, device=DEV).bfloat16()
+    dy[-tail:] = torch.randn(tail, D, generator=g, device=DEV).bfloat16()
+    y, dx = torch.empty_like(x), torch.empty_like(x)
+    mean, rstd = torch.empty(N, device=DEV), torch.empty(N, device=DEV)
+    dg, db = torch.empty(D, device=DEV), torch.empty(D, device=DEV)
+    P.poetx_layernorm_fwd(x, y, mean=mean, rstd=rstd)
+    P.poetx_layernorm_bwd(x, dy, mean, rstd, dx, dgamma=dg, dbeta=db)
+    ref = _norms(P, x[-tail:].cpu(), dy[-tail:].cpu(), None, None)
+    for got, k in ((y, "y"), (dx, "dx")):
+        assert not got[:-tail].any()
+        # (few and many rows take different forms: the same value up to its last rounding)
+        assert O.rel_fro(host(got[-tail:]), host(ref[k])) <= 2.0 ** -8
+    assert O.rel_fro(host(dg), host(ref["dgamma"])) <= TOL_F32
+    assert O.rel_fro(host(db), host(ref["dbeta"])) <= TOL_F32
