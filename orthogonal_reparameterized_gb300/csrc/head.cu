@@ -1401,10 +1401,12 @@ int dx_splits(long long rows, int D, int V, int nseg) {
 // first reads and writes dW's fp32 sums (8 V D bytes against 6 rows V D flops: at 2 GB per piece of a
 // 128-thousand vocabulary about a tenth of the piece's time).
 constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
-// Rows up to which dz is kept in two bf16 pieces: the rounding of a few large p - q is not averaged
-// over many rows there (error of dx against the output's own rounding: 1.54 times with one piece, 1.0
-// with two), and the products are bound by W and dW, not by the tensor pipe.
-constexpr int kFineRows = 16;
+// Rows up to which dz is kept in two bf16 pieces: over few rows the gradients hang on a few large
+// p - q, whose rounding is not averaged (over many rows one piece stays below 1.45 times).  Error of dx and dW against their own output's
+// rounding, 1 to 128 rows: 1.15-1.54 times it with one piece, 1.0 with two.  The time, one piece and
+// two: 120 -> 134 us at 33 x 32000 x 2048, 140 -> 162 us at 128, 800 -> 936 us at 128 x 128256 x 4096
+// (a pass over W and one over dW set most of it; beyond 128 rows the second piece's MMAs do).
+constexpr int kFineRows = kScoreRows;
 constexpr int kMaxFactors = 32768;  // groups of a row with gradients (4194304 columns of 128)
 constexpr long long kMaxRows = 1 << 16;  // of a piece (one warp looks through its upstream gradients)
 
