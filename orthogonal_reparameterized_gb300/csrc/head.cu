@@ -62,11 +62,10 @@ constexpr uint32_t kStgBytes = 32 * 128;             // one epilogue warp's box:
 // operand streams past.  Bands of 4, 8, 16 and 32 at 8192 x 128256 x 4096 with gradients: 17.7, 17.1,
 // 16.9 and 17.3 ms.
 constexpr int kBand = 16;
-constexpr int gemm_smem(int segs) {  // (see SEGS == 2 below)
-  return (segs == 2 ? (kStages - 1) * (int)(kStageBytes + kABytes) : kStages * (int)kStageBytes) +
-         kEpiWarps * (int)kStgBytes + 1024 + 512;
+constexpr int gemm_smem(int segs) {  // (SEGS == 2: two boxes a warp)
+  return kStages * (int)kStageBytes + (segs == 2 ? 2 : 1) * kEpiWarps * (int)kStgBytes + 1024 + 512;
 }
-static_assert(gemm_smem(1) <= 227 * 1024 && gemm_smem(2) <= 227 * 1024, "head products: shared memory");
+static_assert(gemm_smem(2) <= 227 * 1024, "head products: shared memory");
 constexpr int kMaxSegs = 6;
 
 struct HeadMaps {
@@ -192,17 +191,22 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
     head_gemm_kernel(const __grid_constant__ HeadMaps maps0, const __grid_constant__ HeadMaps maps1,
                      const __grid_constant__ HeadGemm p) {
   constexpr bool F32 = SEGS == kMaxSegs;
-  // SEGS == 2: both pieces of A and the one of B share a stage (B is loaded once)
-  constexpr bool BOTH = SEGS == 2;
-  constexpr int STAGES = BOTH ? kStages - 1 : kStages;
-  constexpr uint32_t B_OFF = BOTH ? 2 * kABytes : kABytes, STAGE = B_OFF + kBBytes;
-  constexpr int STEPS = BOTH ? 1 : SEGS;  // stages per K block
+  // SEGS == 2: gradients of at most 128 rows with dz in two pieces.  dx's tile holds the first piece's
+  // rows in the even CTA and the second's in the odd one, which would multiply padding otherwise (their
+  // sums are added with those of the splits); dW's K axis runs over the second piece, then the first.
+  constexpr bool FINE = SEGS == 2;
+  // (Its dW's tiles have at most four K blocks and little but an epilogue: both of a warp's boxes are
+  // staged at once.)
+  constexpr int BOXES = FINE ? 2 : 1, STAGES = kStages;
+  constexpr uint32_t STG = BOXES * kStgBytes;
+  constexpr uint32_t B_OFF = kABytes, STAGE = kStageBytes;
+  constexpr int STEPS = F32 ? SEGS : 1;  // stages per K block
   constexpr uint32_t TMEM_COLS = 2 * BN;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* staging = smem + STAGES * STAGE;
-  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * kStgBytes);
+  uint64_t* full = reinterpret_cast<uint64_t*>(staging + kEpiWarps * STG);
   uint64_t* empty = full + STAGES;
   uint64_t* tfull = empty + STAGES;  // [2] accumulator written
   uint64_t* tempty = tfull + 2;       // [2] accumulator read by both CTAs' epilogue warps
@@ -257,8 +261,11 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
       const int8_t* const seg = is_b ? p.seg_b : p.seg_a;
       // the operand's first row of M (N), and how it is loaded: K-major; MN-major as one box of two
       // 64-column groups (dz: always) or as two boxes
-      const int r0 = is_b ? c.nt * BN + crank * (BN / 2) : (2 * c.mi + crank) * BM;
-      const int how = LSE ? 0 : (is_b ? (p.prod[c.which].b_groups ? 1 : 2) : p.prod[c.which].a_mn);
+      const bool a_mn = !LSE && p.prod[c.which].a_mn;
+      const int r0 = is_b ? c.nt * BN + crank * (BN / 2)
+                          : (FINE && !a_mn ? 0 : (2 * c.mi + crank) * BM);
+      const int half = FINE && a_mn ? p.prod[c.which].num_kb / 2 : 0;
+      const int how = LSE ? 0 : (is_b ? (p.prod[c.which].b_groups ? 1 : 2) : a_mn);
       const bool expect = !is_b && crank == 0;
       for (int c0 = c.kb0; c0 < c.kb1 && ok; c0 += p.chunk) {
         const int len = min(c.kb1 - c0, p.chunk);
@@ -271,7 +278,11 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
           uint8_t* dst = dst0 + rg.s * STAGE;
           const int at = sg;
           const CUtensorMap* m = F32 ? &set[seg[at]] : set;
-          const int k = (c0 + i) * BK;
+          int k = (c0 + i) * BK;
+          if (FINE) {
+            if (!is_b) m = set + (a_mn ? c0 + i < half : crank);
+            if (c0 + i >= half) k -= half * BK;
+          }
           if (++i == len) {
             i = 0;
             ++sg;
@@ -280,13 +291,11 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
           const uint32_t fb = full0 + rg.s * 8;
           if (how == 0) {
             tma_load_2d_pair(dst, m, fb, k, r0);
-            if (BOTH && !is_b) tma_load_2d_pair(dst + kABytes, set + 1, fb, k, r0);
             if (LSE)
               tma_load_2d_pair(dst + B_OFF, &maps.b[F32 ? p.seg_b[at] : 0], fb, k,
                                c.nt * BN + crank * (BN / 2));
           } else if (how == 1) {
             tma_load_3d_pair(dst, m, fb, 0, k, r0 / 64);
-            if (BOTH && !is_b) tma_load_3d_pair(dst + kABytes, set + 1, fb, 0, k, r0 / 64);
           } else {
             tma_load_2d_pair(dst, m, fb, r0, k);
             tma_load_2d_pair(dst + 8192, m, fb, r0 + 64, k);
@@ -318,14 +327,11 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
           tc_fence_after();
           const uint32_t a_base = smem_base + rg.s * STAGE;
           const uint64_t bd = tile_desc<B_MN>(a_base + B_OFF);
+          const uint64_t ad = tile_desc<A_MN>(a_base);
 #pragma unroll
-          for (int pc = BOTH ? 1 : 0; pc >= 0; --pc) {  // the small piece first
-            const uint64_t ad = tile_desc<A_MN>(a_base + pc * kABytes);
-#pragma unroll
-            for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
-              umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
-                             (j | k) != 0 || pc != (BOTH ? 1 : 0));
-          }
+          for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
+            umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
+                           (j | k) != 0);
           umma_commit_pair(&empty[rg.s]);
         }
         umma_commit_pair(&tfull[acc.s]);
@@ -361,7 +367,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
     const int cbeg = ((warp - 2) >> 2) * kGroup;
-    uint8_t* stg = staging + (warp - 2) * kStgBytes;
+    uint8_t* stg = staging + (warp - 2) * STG;
     const float out_scale = LSE ? 1.f : *p.out_scale * p.T;
     Ring<2> acc;
     bool ok = true;
@@ -393,6 +399,14 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
         }
         tc_fence_after();
         const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * BN + cbeg);
+        if (FINE && kb == c.kb0) {  // every load ahead of one wait
+          uint32_t r[kGroup / 32][32];
+#pragma unroll
+          for (int j = 0; j < kGroup / 32; ++j) tmem_ld_32x32b_x32(ta + 32 * j, r[j]);
+          tmem_ld_wait();
+#pragma unroll
+          for (int i = 0; i < kGroup; ++i) v[i] = __uint_as_float(r[i / 32][i % 32]);
+        } else
 #pragma unroll
         for (int j = 0; j < kGroup; j += 32) {
           uint32_t r[32];
@@ -416,7 +430,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
         if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[a], 0));
       }
       if (!ok) break;
-      if (col0 >= d.N || row_w >= d.M) continue;
+      if (col0 >= d.N || (FINE && !d.a_mn ? q * 32 : row_w) >= d.M) continue;
       if (LSE) {
         if (col0 + kGroup > d.N) {
 #pragma unroll
@@ -494,12 +508,15 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
       // the tensor are clipped
       const int orow = LSE ? row_w : c.split * d.c_rows + row_w;
       const CUtensorMap* mc = &(c.which ? maps1 : maps0).c;
-      auto box = [&](int j, auto chunk) {  // chunk(i): 16 bytes i of the lane's row
-        if (lane == 0) bulk_wait_read<0>();  // the previous box has been read
-        __syncwarp();
+      auto fill = [&](uint8_t* at, auto chunk) {  // chunk(i): 16 bytes i of the lane's row
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-          *reinterpret_cast<uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4)) = chunk(i);
+          *reinterpret_cast<uint4*>(at + lane * 128 + ((i ^ (lane & 7)) << 4)) = chunk(i);
+      };
+      auto box = [&](int j, auto chunk) {
+        if (lane == 0) bulk_wait_read<0>();  // the previous box has been read
+        __syncwarp();
+        fill(stg, chunk);
         fence_async_shared();
         __syncwarp();
         if (lane == 0) {
@@ -518,10 +535,8 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
           });
         }
       } else {
-#pragma unroll
-        for (int j = 0; j < kGroup; j += 64) {
-          if (col0 + j >= d.n_store) break;
-          box(j, [&](int i) {
+        auto half = [&](int j) {  // 64 columns from j
+          return [&v, j](int i) {
             const float* f = v + j + 8 * i;
             auto two = [](float lo, float hi) {
               if (!LSE) return pack_bf16x2(lo, hi);
@@ -529,7 +544,26 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
               return *reinterpret_cast<const uint32_t*>(&h);
             };
             return make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
-          });
+          };
+        };
+        if (FINE) {
+          if (lane == 0) bulk_wait_read<0>();
+          __syncwarp();
+          fill(stg, half(0));
+          fill(stg + (BOXES - 1) * kStgBytes, half(64));
+          fence_async_shared();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(mc, stg, col0, orow);
+            if (col0 + 64 < d.n_store) tma_store_2d(mc, stg + (BOXES - 1) * kStgBytes, col0 + 64, orow);
+            bulk_commit();
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < kGroup; j += 64) {
+            if (col0 + j >= d.n_store) break;
+            box(j, half(j));
+          }
         }
       }
     }
@@ -944,6 +978,7 @@ struct RowArgs {
   float* lse;             // nullable
   void* e;                // exp(z - m) of the rows, turned into dz (nullable: loss only)
   __nv_bfloat16* piece[3];  // fp32 heads: dz in three bf16 pieces; bf16 ones: [1] its second (nullable)
+  int slice;  // 16-byte vectors of e per CTA (of a row's grid.y)
 };
 
 constexpr int kRowThreads = 256;
@@ -1004,8 +1039,10 @@ __device__ __forceinline__ void store3(float4 w, __nv_bfloat16* const (&d)[3]) {
 
 // One CTA per row: joins the groups, writes loss and lse and turns e into dz.  Bound by HBM: a row of
 // e read and written (4096 x 32000: 524 MB in 85 us, 6.2 TB/s; 8192 x 128256: 0.64 ms, 6.6 TB/s).
+// Where there are few rows, several CTAs share one: each joins the groups again and turns its columns.
+// (Five CTAs per SM: 48 registers; four, with 63, cost 1 % of a call of 2047 rows.)
 template <bool F32>
-__global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) {
+__global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs p) {
   extern __shared__ __align__(16) float sm[];
   const int K8 = (p.K + 7) / 8 * 8;
   uint16_t* ks = reinterpret_cast<uint16_t*>(sm);  // [K8] slots of the entries (distillation)
@@ -1124,7 +1161,7 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
       qs[v] = q;
     }
   }
-  if (t == 0) {
+  if (t == 0 && blockIdx.y == 0) {
     p.loss[row] = bad ? __int_as_float(0x7fc00000) : (some > 0.f ? loss : 0.f);
     if (p.lse) p.lse[row] = lse;
   }
@@ -1134,12 +1171,14 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   const float coef = gT * weight;
   for (int g = t; g < p.groups; g += kRowThreads) fac[g] = coef * exp2f(part[g].x - lse2);
   __syncthreads();
+  // the CTA's vectors [lo, n) of the row
+  constexpr int VEC = F32 ? 4 : 8;
+  const int lo = (int)blockIdx.y * p.slice, n = min(lo + p.slice, (int)(p.pitch / VEC));
   if (!F32) {
     uint4* er = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.e) + row * p.pitch);
     uint4* second = p.piece[1] ? reinterpret_cast<uint4*>(p.piece[1] + row * p.pitch) : nullptr;
-    const int n = (int)(p.pitch / 8);
     constexpr int U = 4;  // loads in flight per thread
-    for (int i0 = t; i0 < n; i0 += U * kRowThreads) {
+    for (int i0 = lo + t; i0 < n; i0 += U * kRowThreads) {
       uint4 w[U];
       if (live)
 #pragma unroll
@@ -1182,9 +1221,8 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
     }
   } else {
     const float4* er = reinterpret_cast<const float4*>(static_cast<float*>(p.e) + row * p.pitch);
-    const int n = (int)(p.pitch / 4);
     constexpr int U = 4;
-    for (int i0 = t; i0 < n; i0 += U * kRowThreads) {
+    for (int i0 = lo + t; i0 < n; i0 += U * kRowThreads) {
       float4 w[U];
 #pragma unroll
       for (int k = 0; k < U; ++k)
@@ -1206,13 +1244,14 @@ __global__ void __launch_bounds__(kRowThreads) head_row_kernel(const RowArgs p) 
   __syncthreads();
   // the targets' own columns: weight p - q, without cancellation where p is near 1
   for (int u = t; u < nu; u += kRowThreads) {
+    const int c = ucol[u];
+    if (c / VEC < lo || c / VEC >= n) continue;
     const float pv = exp2f(z2[u] - lse2);
     float dz;
     if (u == umax && sure)
       dz = gT * ((weight - 1.f) * pv + (rest - others / total));
     else
       dz = coef * pv - gT * qs[u];
-    const int c = ucol[u];
     if (!F32) {
       const __nv_bfloat16 hi = __float2bfloat16_rn(dz);
       static_cast<__nv_bfloat16*>(p.e)[row * p.pitch + c] = hi;
@@ -1271,6 +1310,7 @@ __global__ void __launch_bounds__(256)
   const long long step = (long long)gridDim.x * blockDim.x;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += step) {
     float4 a = *reinterpret_cast<const float4*>(part + 4 * i);
+#pragma unroll 4
     for (int k = 1; k < S; ++k) {
       const float4 b = *reinterpret_cast<const float4*>(part + k * stride + 4 * i);
       a.x += b.x;
@@ -1402,10 +1442,11 @@ int dx_splits(long long rows, int D, int V, int nseg) {
 // 128-thousand vocabulary about a tenth of the piece's time).
 constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
 // Rows up to which dz is kept in two bf16 pieces: over few rows the gradients hang on a few large
-// p - q, whose rounding is not averaged (over many rows one piece stays below 1.45 times).  Error of dx and dW against their own output's
-// rounding, 1 to 128 rows: 1.15-1.54 times it with one piece, 1.0 with two.  The time, one piece and
-// two: 120 -> 134 us at 33 x 32000 x 2048, 140 -> 162 us at 128, 800 -> 936 us at 128 x 128256 x 4096
-// (a pass over W and one over dW set most of it; beyond 128 rows the second piece's MMAs do).
+// p - q, whose rounding is not averaged (over many rows one piece stays below 1.45 times).  Error of dx
+// and dW against their own output's rounding, 1 to 128 rows: 1.15-1.54 times it with one piece, 1.0
+// with two.  The second piece costs next to nothing: dx's tile has the room for it, and of a dW of so
+// few rows its stores are the most (whole call, one piece and two: 120 and 126 us at 33 x 32000 x 2048,
+// 140 and 144 us at 128, 683 and 664 us at 33 x 128256 x 4096, 800 and 751 us at 128).
 constexpr int kFineRows = kScoreRows;
 constexpr int kMaxFactors = 32768;  // groups of a row with gradients (4194304 columns of 128)
 constexpr long long kMaxRows = 1 << 16;  // of a piece (one warp looks through its upstream gradients)
@@ -1418,6 +1459,7 @@ struct Plan {
   long long rows;    // rows of a piece
   int pieces;
   int splits;        // K splits of dx
+  int sums;          // partial sums of dx (the splits, times dz's pieces)
   int height, tiles;  // few rows: vocabulary rows of a tile and tiles (else 0)
   // workspace offsets
   size_t unit, part, tl, ucol, slot, gstart, e, dz, dz2, xs, ws, acc, dxp, bytes;
@@ -1480,7 +1522,8 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   o->xs = o->f32 ? take(3 * align_up(R * D * 2, 1024)) : 0;
   o->ws = o->f32 ? take(3 * align_up((size_t)V * D * 2, 1024)) : 0;
   o->acc = !o->f32 && dW && o->pieces > 1 ? take((size_t)V * D * 4) : 0;
-  o->dxp = o->splits > 1 ? take((size_t)o->splits * align_up(R, 256) * D * 4) : 0;
+  o->sums = o->fine && dx ? 2 * o->splits : o->splits;
+  o->dxp = o->sums > 1 ? take((size_t)o->splits * align_up(R, 256) * D * 4) : 0;
   o->bytes = at;
   return true;
 }
@@ -1704,10 +1747,18 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
         ra.piece[i] = reinterpret_cast<__nv_bfloat16*>(w + pl.dz + i * z_step);
     else if (pl.fine)
       ra.piece[1] = reinterpret_cast<__nv_bfloat16*>(w + pl.dz2);
+    // a row's CTAs: up to four per SM in all, with at least 1024 vectors of columns (16 bytes) each
+    // (64 x 60416: 19 -> 13 us)
+    const int vecs = (int)(pl.Vp * (pl.f32 ? 4 : 2) / 16), room = 4 * sm_count() / rows;
+    int ctas = ceil_div(vecs, 1024);
+    if (ctas > room) ctas = room;
+    if (ctas < 1 || !pl.grads) ctas = 1;
+    ra.slice = ceil_div(vecs, ctas);
+    const dim3 row_grid(rows, ctas);
     if (pl.f32)
-      POETX_CUDA_TRY(launch_pdl(head_row_kernel<true>, dim3(rows), dim3(kRowThreads), row_smem, s, ra));
+      POETX_CUDA_TRY(launch_pdl(head_row_kernel<true>, row_grid, dim3(kRowThreads), row_smem, s, ra));
     else
-      POETX_CUDA_TRY(launch_pdl(head_row_kernel<false>, dim3(rows), dim3(kRowThreads), row_smem, s, ra));
+      POETX_CUDA_TRY(launch_pdl(head_row_kernel<false>, row_grid, dim3(kRowThreads), row_smem, s, ra));
     POETX_CUDA_TRY(cudaGetLastError());
     after_launch(s, ST_HEAD_ROW);
     if (!pl.grads) continue;
@@ -1737,9 +1788,9 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       d.M = rows;
       d.N = d.n_store = c.D;
       d.c_rows = c_rows;
-      d.c_f32 = pl.f32 || pl.splits > 1;
-      const void* dst = pl.splits > 1 ? w + pl.dxp : dxr;
-      const long long drows = pl.splits > 1 ? (long long)pl.splits * c_rows : rows;
+      d.c_f32 = pl.f32 || pl.sums > 1;
+      const void* dst = pl.sums > 1 ? w + pl.dxp : dxr;
+      const long long drows = pl.sums > 1 ? (long long)pl.splits * c_rows : rows;
       if (!encode_tma_2d(&mp.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, drows, c.D, d.c_f32 ? 32 : 64,
                          32, true))
         return POETX_ERR_CUDA;
@@ -1755,8 +1806,8 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       d.tiles_m = ceil_div(c.V, 2 * BM);
       d.tiles_n = ceil_div(c.D, BN);
       d.num_tiles = d.tiles_m * d.tiles_n;
-      d.n_fast = 1;
-      d.num_kb = d.kb_split = ceil_div(rows, BK);
+      d.n_fast = !pl.fine;  // (few rows: down the vocabulary 1-3 % faster)
+      d.num_kb = d.kb_split = ceil_div(rows, BK) * (pl.fine ? 2 : 1);
       d.a_mn = 1;
       d.M = d.c_rows = c.V;
       d.N = d.n_store = c.D;
@@ -1779,16 +1830,16 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       POETX_TRY((gemm<false, 2>(mp, second, h, s)));
     else
       POETX_TRY((gemm<false, 1>(mp, second, h, s)));
-    if (c.dx && pl.splits > 1) {
+    if (c.dx && pl.sums > 1) {
       const long long quads = (long long)rows * c.D / 4;
       const float* pp = reinterpret_cast<const float*>(w + pl.dxp);
-      const long long stride = (long long)c_rows * c.D;
+      const long long stride = (long long)(pl.fine ? BM : c_rows) * c.D;
       if (pl.f32)
         POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, dim3(grid_for(quads, 256)), dim3(256), 0, s,
-                                  pp, pl.splits, stride, quads, reinterpret_cast<float*>(dxr)));
+                                  pp, pl.sums, stride, quads, reinterpret_cast<float*>(dxr)));
       else
         POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, dim3(grid_for(quads, 256)),
-                                  dim3(256), 0, s, pp, pl.splits, stride, quads,
+                                  dim3(256), 0, s, pp, pl.sums, stride, quads,
                                   reinterpret_cast<__nv_bfloat16*>(dxr)));
       POETX_CUDA_TRY(cudaGetLastError());
       after_launch(s, ST_HEAD_ROW);
