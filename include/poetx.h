@@ -521,7 +521,8 @@ poetx_status poetx_head_ce(poetx_dtype dt, const void* x, int N, int D, const vo
 
 /* Distillation from a teacher's K top logits.  t_index [N, K] int32, t_logit [N, K] fp32: the
  * vocabulary entries the teacher kept and its logits; an entry with a negative index is absent (its
- * logit is not read) and a row without entries (or with all of them -inf) is ignored.  With
+ * logit is not read) and a row without entries (or with all of them -inf) is ignored.  A NaN or +inf
+ * among a row's entries makes its loss and its dx NaN.  With
  * T = temperature > 0, z = x W^T / T and q = softmax over the row's entries of t_logit / T:
  *   loss[r] = T^2 sum_k q_k (ln q_k - z_{i_k} + lse),  lse = ln sum over all V of exp z_v
  *   d(x W^T) = dloss[r] T (softmax(z) - sum_k q_k onehot_{i_k})

@@ -57,7 +57,8 @@ def head_ce(x, W, target, dloss=None, z_loss=0.0):
 
 def head_distill(x, W, t_index, t_logit, dloss=None, temperature=1.0):
     """dict of loss = T^2 KL(teacher || student), lse and, with dloss, dx and dW; entries with a
-    negative index are absent, rows without entries are ignored."""
+    negative index are absent, rows without entries (or with all of them -inf) are ignored; a NaN or
+    +inf among a row's entries leaves it no distribution: NaN."""
     T = float(temperature)
     x, W = np.asarray(x, np.float64), np.asarray(W, np.float64)
     z = x @ W.T / T
@@ -66,7 +67,7 @@ def head_distill(x, W, t_index, t_logit, dloss=None, temperature=1.0):
     dz = np.zeros_like(z)
     for r in range(x.shape[0]):
         ks = [k for k in range(t_index.shape[1])
-              if t_index[r, k] >= 0 and t_logit[r, k] > -np.inf]
+              if t_index[r, k] >= 0 and t_logit[r, k] != -np.inf]
         if not ks:
             continue
         u = np.asarray(t_logit[r, ks], np.float64) / T

@@ -1102,7 +1102,10 @@ __global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs 
     for (int v = t; v < nu; v += kRowThreads)
       if (z2[v] == zm) first = fmaxf(first, -(float)v);
     for (int k = t; k < p.K; k += kRowThreads)
-      if (idx[k] >= 0) tm = fmaxf(tm, u[k] * invT);
+      if (idx[k] >= 0) {  // (a NaN makes it +inf, and with that the sum below NaN)
+        const float a = u[k] * invT;
+        tm = a != a ? -ninf : fmaxf(tm, a);
+      }
     block_reduce2<true>(first, tm, red);
     umax = (int)-first;
   }
@@ -1138,7 +1141,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs 
       if (ks[k] != kNoSlot && some > 0.f) {
         const float lq = u[k] * invT - tm - lus;
         q = expf(lq);
-        if (q > 0.f) l += q * (lq - (ks[k] == umax ? lnp_max : (z2[ks[k]] - lse2) * kLn2));
+        if (!(q == 0.f)) l += q * (lq - (ks[k] == umax ? lnp_max : (z2[ks[k]] - lse2) * kLn2));
         if (ks[k] != umax) rest += q;
       }
       qk[k] = q;

@@ -1,0 +1,55 @@
+"""Infinities and NaN in the linear head's inputs: what the definition calls NaN is NaN, it stays in
+the rows (and vocabulary entries) it belongs to, and a logit of -inf is a probability of 0."""
+import numpy as np
+import pytest
+import torch
+
+from gpu_util import DEV, P, dev, host  # noqa: F401
+from oracle import head_oracle as H
+from test_gpu_head import _ce, _distill, _inputs, _near
+
+pytestmark = pytest.mark.gpu
+
+# bf16: the product of few rows and the one of many; fp32: one for both
+ROWS = [("bf16", 40), ("bf16", 140), ("f32", 40)]
+
+
+@pytest.mark.parametrize("dt,N", ROWS)
+@pytest.mark.parametrize("T", [1.0, 2.0])
+def test_distill_teacher_logits_not_finite(P, dt, N, T):
+    """A NaN or +inf among a row's present entries leaves the row no distribution: its loss and its
+    dx are NaN, and dW where the row's entries are.  Absent entries are not read."""
+    V = 900
+    x, W, _, g = _inputs(N, V, 64, dt, 30)
+    r = np.random.default_rng(2)
+    idx = np.stack([r.permutation(V)[:6] for _ in range(N)]).astype(np.int32)
+    u = r.uniform(-3, 6, (N, 6)).astype(np.float32)
+    u[2, 3] = np.nan
+    u[5, 0] = np.inf
+    u[6] = np.nan
+    u[7] = np.inf
+    u[8], u[8, 2] = -np.inf, np.nan
+    idx[9, 1:], u[9, 0] = -1, np.nan
+    bad = [2, 5, 6, 7, 8, 9]
+    idx[10, 2], u[10, 2] = -1, np.nan
+    idx[11, 2], u[11, 2] = -1, np.inf
+    u[12, 4] = -np.inf
+    ok = np.setdiff1d(np.arange(N), bad)
+    for grads in (False, True):
+        got = _distill(P, x, W, idx, u, g, T, grads=grads)
+        assert np.isnan(host(got["loss"])[bad]).all()
+        ref = H.head_distill(host(x)[ok], host(W), idx[ok], u[ok], g[ok] if grads else None, T)
+        ref["lse"] = H.head_distill(host(x), host(W), idx, u, None, T)["lse"]
+        for k in ("loss", "dx"):
+            if k in got:
+                got[k] = got[k][torch.as_tensor(ok, device=DEV)]
+        _near({k: v for k, v in got.items() if k != "dW"}, ref, dt)
+    got = _distill(P, x, W, idx, u, g, T)
+    assert np.isnan(host(got["dx"])[bad]).all()
+    named = np.unique(idx[bad][idx[bad] >= 0])
+    dW = host(got["dW"])
+    assert np.isnan(dW[idx[[2, 5, 6, 7]].ravel()]).all()
+    g0 = g.copy()
+    full = H.head_distill(host(x), host(W), idx, np.where(np.isfinite(u) | (u < 0), u, 0), g0, T)
+    rest = np.setdiff1d(np.arange(V), named)  # there p alone counts
+    _near({"dW": torch.as_tensor(dW[rest])}, {"dW": full["dW"][rest]}, dt)
