@@ -1120,7 +1120,9 @@ __global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs 
     for (int k = t; k < p.K; k += kRowThreads)
       if (idx[k] >= 0) us += expf(u[k] * invT - tm);
   block_reduce2<false>(others, us, red);
-  const float emax = nu ? exp2f(zm - off) : 0.f;
+  // (a label's logit itself, not the maximum, which drops a NaN; among a teacher's entries a NaN is none
+  // that equals the maximum, and is in `others`)
+  const float emax = nu ? exp2f((u ? zm : z2[0]) - off) : 0.f;
   const float total = others + emax;
   const float lse2 = off + log2f(total);
   const float lse = lse2 * kLn2;

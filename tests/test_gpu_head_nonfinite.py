@@ -53,3 +53,26 @@ def test_distill_teacher_logits_not_finite(P, dt, N, T):
     full = H.head_distill(host(x), host(W), idx, np.where(np.isfinite(u) | (u < 0), u, 0), g0, T)
     rest = np.setdiff1d(np.arange(V), named)  # there p alone counts
     _near({"dW": torch.as_tensor(dW[rest])}, {"dW": full["dW"][rest]}, dt)
+
+
+@pytest.mark.parametrize("dt,N", ROWS)
+@pytest.mark.parametrize("how", ["nan", "inf-inf"])
+def test_target_logit_not_a_number(P, dt, N, how):
+    """A vocabulary entry whose logit is NaN takes every row with it, those that have it as their
+    target too; an ignored row's loss is 0 all the same."""
+    x, W, t, g = _inputs(N, 700, 64, dt, 31)
+    if how == "nan":
+        W[300] = float("nan")
+    else:
+        x[:, :2] = x[:, :2].abs() + 0.1
+        W[300, 0], W[300, 1] = float("inf"), float("-inf")
+    t[3], t[4], t[5] = 300, -1, 300
+    kept = t >= 0
+    for grads in (False, True):
+        got = _ce(P, x, W, t, g, dx=grads, dW=grads)
+        assert np.isnan(host(got["lse"])).all()
+        assert np.isnan(host(got["loss"])[kept]).all() and host(got["loss"])[4] == 0
+    assert np.isnan(host(got["dx"])[kept]).all()
+    idx = t[:, None].astype(np.int32)
+    got = _distill(P, x, W, idx, np.zeros((N, 1), np.float32), g)
+    assert np.isnan(host(got["loss"])[kept]).all() and np.isnan(host(got["dx"])[kept]).all()
