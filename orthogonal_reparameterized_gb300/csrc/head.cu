@@ -1013,8 +1013,22 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
+// Three bf16 pieces of v, whose sum it is.  An infinity or NaN goes into the third with zeros before it:
+// the products take the third piece with the other operand's first alone, so that it meets each number
+// once, with that number's own sign (inf - inf in the split and inf times a rest of either sign would make
+// NaN of a plain infinity).  A finite value that would round to infinity is cut off at bf16's largest.
+constexpr float kBf16Max = 0x1.fep127f;
+template <bool CHECK = true>
 __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
   o[0] = __float2bfloat16_rn(v);
+  if (CHECK && !(fabsf(v) <= kBf16Max)) {
+    if (!isfinite(v)) {
+      o[0] = o[1] = __float2bfloat16_rn(0.f);
+      o[2] = __float2bfloat16_rn(v);
+      return;
+    }
+    o[0] = __float2bfloat16_rz(v);
+  }
   v -= __bfloat162float(o[0]);
   o[1] = __float2bfloat16_rn(v);
   v -= __bfloat162float(o[1]);
@@ -1024,10 +1038,17 @@ __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
 // The pieces of four neighbouring values, to d[0], d[1] and d[2].
 __device__ __forceinline__ void store3(float4 w, __nv_bfloat16* const (&d)[3]) {
   __nv_bfloat16 o[4][3];
-  split3(w.x, o[0]);
-  split3(w.y, o[1]);
-  split3(w.z, o[2]);
-  split3(w.w, o[3]);
+  if (fabsf(w.x) + fabsf(w.y) + fabsf(w.z) + fabsf(w.w) <= kBf16Max) {  // (false for a NaN)
+    split3<false>(w.x, o[0]);
+    split3<false>(w.y, o[1]);
+    split3<false>(w.z, o[2]);
+    split3<false>(w.w, o[3]);
+  } else {
+    split3(w.x, o[0]);
+    split3(w.y, o[1]);
+    split3(w.z, o[2]);
+    split3(w.w, o[3]);
+  }
 #pragma unroll
   for (int k = 0; k < 3; ++k) {
     const __nv_bfloat162 lo = __halves2bfloat162(o[0][k], o[1][k]);

@@ -76,3 +76,53 @@ def test_target_logit_not_a_number(P, dt, N, how):
     idx = t[:, None].astype(np.int32)
     got = _distill(P, x, W, idx, np.zeros((N, 1), np.float32), g)
     assert np.isnan(host(got["loss"])[kept]).all() and np.isnan(host(got["dx"])[kept]).all()
+
+
+@pytest.mark.parametrize("N", [40, 300])
+@pytest.mark.parametrize("where", ["row", "element"])
+def test_fp32_infinite_weights(P, N, where):
+    """fp32: an entry whose logit is -inf has probability 0, with fp32 accuracy for all others."""
+    x, W, t, g = _inputs(N, 700, 64, "f32", 32)
+    x = x.abs() + 0.1 if where == "row" else x
+    x[:, 5] = x[:, 5].abs() + 0.1
+    out = np.zeros(700, bool)
+    out[128:256] = out[300] = True
+    W[torch.as_tensor(out), 0 if where == "row" else 5:(64 if where == "row" else 6)] = float("-inf")
+    t[out[t]] = 5
+    keep, place = ~out, np.cumsum(~out) - 1
+    ref = H.head_ce(host(x), host(W)[keep], place[t], g)
+    got = _ce(P, x, W, t, g)
+    assert not host(got["dW"])[out].any()  # p is 0
+    got["dW"] = got["dW"][torch.as_tensor(keep, device=DEV)]
+    del got["dx"]  # 0 x -inf
+    _near(got, ref, "f32")
+
+
+def test_fp32_infinities_give_what_the_definition_gives(P):
+    """+inf in W, and infinities and NaN in x: NaN where the log-sum-exp of such logits is NaN."""
+    x, W, t, g = _inputs(60, 500, 64, "f32", 33)
+    x[:, 5] = x[:, 5].abs() + 0.1
+    W[10, 5] = float("inf")
+    got = _ce(P, x, W, t, g, dx=False, dW=False)
+    assert np.isnan(host(got["lse"])).all() and np.isnan(host(got["loss"])).all()
+    x, W, t, g = _inputs(60, 500, 64, "f32", 34)
+    x[7, 3], x[8, 9], x[9, 11] = float("inf"), float("-inf"), float("nan")
+    got = _ce(P, x, W, t, g, dW=False)
+    ok = np.setdiff1d(np.arange(60), [7, 8, 9])
+    for k in ("loss", "lse", "dx"):
+        assert np.isnan(host(got[k])[[7, 8, 9]]).all(), k
+        got[k] = got[k][torch.as_tensor(ok, device=DEV)]
+    ref = H.head_ce(host(x)[ok], host(W), t[ok], g[ok])
+    _near(got, ref, "f32")
+
+
+def test_fp32_largest_numbers(P):
+    """Values that bf16 rounds to infinity are finite in fp32: a logit of 8 from the largest one."""
+    x, W, t, g = _inputs(50, 500, 64, "f32", 35)
+    W[:, 1] = 0
+    x[:, 1] = 2.0 ** -125
+    W[50, 1], W[51, 1] = torch.finfo(torch.float32).max, -3.4e38
+    t[:5] = 50
+    ref = H.head_ce(host(x), host(W), t, g)
+    got = _ce(P, x, W, t, g, dx=False)  # (dx reaches the size of W)
+    _near(got, ref, "f32")
