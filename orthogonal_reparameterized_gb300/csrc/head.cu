@@ -11,8 +11,8 @@
 // Both are the same three products with a sparse target, so they share every kernel.  The rows are
 // taken in pieces.  Per piece: (1) the logits' product, whose epilogue leaves for each row and each
 // group of 128 columns the maximum m and the sum of exp(z - m), and stores exp(z - m) in 16 bits
-// (fp16: it lies in [0, 1], so its rounding, 2^-12, stays below the bf16 rounding of dz that
-// follows; no fp32 logit is stored); (2) a row kernel that joins the groups into lse, writes the
+// (pack_exp: 11 significant bits down to 43 nats below m, so that its rounding, 2^-11, stays below the
+// bf16 rounding of dz that follows; no fp32 logit is stored); (2) a row kernel that joins the groups into lse, writes the
 // loss and turns the row into dz in place (bf16); (3) dx = dz W and dW (+)= dz^T x.  That is 6 N V D
 // flops: nothing is computed twice.  The logits of the sparse targets leave the first product in
 // fp32, and the groups' sums leave the targets out: with O the sum of all other exponentials and e
@@ -31,8 +31,6 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, drains its own
 // copies, frees its TMEM and returns.
-#include <cuda_fp16.h>
-
 #include <mutex>
 #include <type_traits>
 
@@ -116,6 +114,23 @@ __device__ __forceinline__ float ex2(float v) {
   return r;
 }
 
+// exp(z - m) as it is stored, a number of [0, 1]: 6 bits of exponent and 10 of mantissa.  These are bits 28
+// to 13 of the fp32 number 2^-64 times as large, whose upper ones are 0, rounded to nearest: 11 significant
+// bits down to 2^-62 (43 nats below the group's maximum), fewer down to 2^-72.  (An fp16 would lose bits
+// below 2^-14, 10 nats, and be 0 from 17 nats on: the gradients of rare entries in a head that has
+// learned; 2^15 times as large in fp16 it would be exact to 20 nats.)  The factor 2^64 returns with the row
+// kernel's factor of the group.  Four instructions per pair where fp16 takes one: nothing on wide heads
+// (4096 x 32000 x 2048 with gradients 967 and 966 us), 3 % at 1000 x 16000 x 1024 (112.6 and 115.7 us), 6 %
+// at 300 x 32000 x 512 (89 and 95 us), where the epilogues are a larger part.
+constexpr float kExpStore = 0x1p-64f, kExpLoad = 0x1p64f;
+__device__ __forceinline__ uint32_t pack_exp(float a, float b) {
+  const float2 w = mul2(make_float2(a, b), both(kExpStore));
+  return __byte_perm(8u * __float_as_uint(w.x) + 0x8000u, 8u * __float_as_uint(w.y) + 0x8000u, 0x7632);
+}
+__device__ __forceinline__ float2 unpack_exp(uint32_t u) {  // times 2^-64
+  return make_float2(__uint_as_float((u << 13) & 0x1fffe000u), __uint_as_float((u >> 3) & 0x1fffe000u));
+}
+
 // K-major tile: rows of 128 bytes (64 along K), 8-row groups 1024 bytes apart, the k-th K = 16 slice
 // 32 bytes further; MN-major tile: boxes of 64 K rows x 64 side by side (8 KB), the slice 16 rows
 // (2048 bytes) further.
@@ -174,8 +189,11 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volati
 
 // The unit of dz: the largest |dloss| of the piece.  dz is kept over unit * T, so that with equal
 // upstream gradients (a mean) the bf16 rounding sees p - q alone and not a constant's mantissa too;
-// the sums get the factor back in fp32.  1 where there is no finite positive maximum.
-__device__ __forceinline__ float head_unit(float top) { return top > 0.f && top < 3.0e38f ? top : 1.f; }
+// the sums get the factor back in fp32.  At most 2^100, so that with kExpLoad or T nothing overflows; 1
+// where there is no finite positive maximum.
+__device__ __forceinline__ float head_unit(float top) {
+  return top > 0.f && isfinite(top) ? fminf(top, 0x1p100f) : 1.f;
+}
 
 // LSE: the logits' product with its softmax epilogue (one product, both operands K-major).
 // Otherwise the gradients' products, dx and dW in one launch, so that the second's tiles fill the
@@ -457,7 +475,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
         float m = v[0];
 #pragma unroll
         for (int i = 1; i < kGroup; ++i) m = fmaxf(m, v[i]);
-        m *= p.scale2;
+        m = __fmul_ru(m, p.scale2);  // rounded up: no stored exponential is above 1
         const float off = m == __int_as_float(0xff800000) ? 0.f : m;  // a group of -inf sums to 0
         float2 sum = both(0.f);
 #pragma unroll
@@ -539,9 +557,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
           return [&v, j](int i) {
             const float* f = v + j + 8 * i;
             auto two = [](float lo, float hi) {
-              if (!LSE) return pack_bf16x2(lo, hi);
-              const __half2 h = __floats2half2_rn(lo, hi);
-              return *reinterpret_cast<const uint32_t*>(&h);
+              return LSE ? pack_exp(lo, hi) : pack_bf16x2(lo, hi);
             };
             return make_uint4(two(f[0], f[1]), two(f[2], f[3]), two(f[4], f[5]), two(f[6], f[7]));
           };
@@ -585,7 +601,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
 // 128) padded tokens are the columns, and nearly all of the shared memory is a ring of W tiles in
 // flight.  A warp of the epilogue holds 32 vocabulary rows: it takes the targets out, turns its
 // 32 x NT logits over through shared memory and leaves one (max, sum) per token and, where the
-// gradients are wanted, the 32 values exp(z - max) of each token in fp16.  1 x 32000 x 2048: 131 MB
+// gradients are wanted, the 32 values exp(z - max) of each token in 16 bits.  1 x 32000 x 2048: 131 MB
 // in 22 us among other calls (26.6 us from a cold start); 3 x 100003 x 3000 with the store: 600 MB in
 // 115 us (5.2 TB/s).
 struct HeadScore {
@@ -599,7 +615,7 @@ struct HeadScore {
   const uint16_t* gstart;  // [rows][tiles + 1] first of them in each tile; NULL: K = 1
   int K;
   float* tl;               // [rows][K]
-  __half* e;               // [rows][pitch] exp(z - max); NULL: the loss alone
+  uint16_t* e;             // [rows][pitch] exp(z - max); NULL: the loss alone
   long long pitch;
   const float* dloss;      // with e: [rows], whose largest magnitude goes to unit
   float* unit;
@@ -814,10 +830,10 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           float m = ninf;
 #pragma unroll
           for (int r = 0; r < 32; ++r) m = fmaxf(m, tw[r * (NT + 1) + c]);
-          m *= p.scale2;
+          m = __fmul_ru(m, p.scale2);
           const float off = m == ninf ? 0.f : m;
           float sum = 0.f;
-          __half* er = p.e + c * p.pitch + v0 + q * 32;  // (v0 is a multiple of 8: 16-byte stores)
+          uint16_t* er = p.e + c * p.pitch + v0 + q * 32;  // (v0 is a multiple of 8: 16-byte stores)
 #pragma unroll
           for (int r = 0; r < 32; r += 8) {
             uint32_t u[4];
@@ -826,8 +842,7 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
               const float a = ex2(fmaf(tw[(r + 2 * i) * (NT + 1) + c], p.scale2, -off));
               const float b = ex2(fmaf(tw[(r + 2 * i + 1) * (NT + 1) + c], p.scale2, -off));
               sum += a + b;
-              const __half2 h = __floats2half2_rn(a, b);
-              u[i] = *reinterpret_cast<const uint32_t*>(&h);
+              u[i] = pack_exp(a, b);
             }
             if (p.e && q * 32 + r < p.height && v0 + q * 32 + r < p.pitch)
               *reinterpret_cast<uint4*>(er + r) = make_uint4(u[0], u[1], u[2], u[3]);
@@ -1195,7 +1210,8 @@ __global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs 
   const bool live = some > 0.f && !bad;
   const float gT = live ? p.dloss[row] / *p.unit : 0.f;
   const float coef = gT * weight;
-  for (int g = t; g < p.groups; g += kRowThreads) fac[g] = coef * exp2f(part[g].x - lse2);
+  const float gcoef = F32 ? coef : coef * kExpLoad;
+  for (int g = t; g < p.groups; g += kRowThreads) fac[g] = gcoef * exp2f(part[g].x - lse2);
   __syncthreads();
   // the CTA's vectors [lo, n) of the row
   constexpr int VEC = F32 ? 4 : 8;
@@ -1226,7 +1242,7 @@ __global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs 
           float v[8];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 h = __half22float2(*reinterpret_cast<const __half2*>(&u[j]));
+            const float2 h = unpack_exp(u[j]);
             v[2 * j] = h.x * f;
             v[2 * j + 1] = h.y * f;
           }
@@ -1699,7 +1715,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       h.gstart = gstart;
       h.K = c.K;
       h.tl = tl;
-      h.e = pl.grads ? reinterpret_cast<__half*>(w + pl.e) : nullptr;
+      h.e = pl.grads ? reinterpret_cast<uint16_t*>(w + pl.e) : nullptr;
       h.pitch = pl.Vp;
       h.dloss = c.dloss ? c.dloss + r0 : nullptr;
       h.unit = unit;
