@@ -502,7 +502,8 @@ poetx_status poetx_layernorm_bwd(poetx_dtype dt, const void* x, const void* dy, 
  *           1 <= V <= 4194304, N >= 0 (POETX_ERR_SHAPE otherwise).
  *   target  [N] int32.  A target >= V is the caller's error: that row's loss is NaN, its gradient 0.
  *   dloss   [N] fp32: the upstream gradient of each row's loss (for a mean over the kept rows,
- *           1 / their number); required where dx or dW is wanted, else unused
+ *           1 / their number); required where dx or dW is wanted, else unused.  What it holds for an
+ *           ignored row does not matter.
  *   loss, lse [N] fp32 outputs (lse nullable; written for ignored rows too)
  *   dx [N, D], dW [V, D] outputs of dtype dt (each nullable; both NULL: the loss alone).
  *           accumulate != 0 adds dW to its contents (dx is always overwritten).

@@ -100,8 +100,8 @@ struct HeadGemm {
   int K;
   float* tl;             // [M][K] their logits, before 1/T
   int store;             // whether exp(z - m) is stored
-  const float* dloss;    // with store: [M] upstream gradients, whose largest magnitude goes to
-  float* unit;           //   unit (head_unit), read back as
+  const float* dloss;    // with store: [M] upstream gradients (lists: of the rows with one, else 0), whose
+  float* unit;           //   largest magnitude goes to unit (head_unit), read back as
   const float* out_scale;  // gradients' products: factor of the sums
   float T;
   int* err;
@@ -194,6 +194,11 @@ __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volati
 __device__ __forceinline__ float head_unit(float top) {
   return top > 0.f && isfinite(top) ? fminf(top, 0x1p100f) : 1.f;
 }
+// A row's share in that maximum: nothing where it has no gradient (target outside [0, V): ignored or bad),
+// whatever its dloss holds.
+__device__ __forceinline__ float unit_share(float dloss, int target, int V) {
+  return (unsigned)target < (unsigned)V ? fabsf(dloss) : 0.f;
+}
 
 // LSE: the logits' product with its softmax epilogue (one product, both operands K-major).
 // Otherwise the gradients' products, dx and dW in one launch, so that the second's tiles fill the
@@ -258,8 +263,9 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   const uint32_t tmem_base = *tmem_slot;
   const uint32_t smem_base = smem_u32(smem);
   // With target lists the kernel before this one made them, and started it after everything earlier
-  // was complete: only the epilogue, which reads the lists and writes, waits for it.
-  if (!LSE || !p.gstart || (warp >= 2 && warp < kBWarp)) pdl_wait();
+  // was complete: only the epilogue, which reads the lists and writes, waits for it (and the warp that
+  // makes dz's unit from what that kernel left of dloss).
+  if (!LSE || !p.gstart || (warp >= 2 && warp < kBWarp) || (warp == 1 && blockIdx.x == 1)) pdl_wait();
   const int t0 = (int)blockIdx.x / 2, t_step = (int)gridDim.x / 2;
 
   if ((warp == 0 || warp == kBWarp) && lane == 0) {
@@ -370,14 +376,20 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   } else if (LSE && warp == 1 && blockIdx.x == 1 && p.store) {
     // ------------------------------------------------------------ an idle warp: the unit of dz
     float top = 0.f;
-    const int M = p.prod[0].M, quads = M / 4;
+    const int M = p.prod[0].M, V = p.prod[0].N, quads = M / 4;
     const float4* d4 = reinterpret_cast<const float4*>(p.dloss);
+    const int4* t4 = reinterpret_cast<const int4*>(p.ucol);
 #pragma unroll 4
     for (int r = lane; r < quads; r += 32) {
       const float4 w = d4[r];
-      top = fmaxf(fmaxf(top, fmaxf(fabsf(w.x), fabsf(w.y))), fmaxf(fabsf(w.z), fabsf(w.w)));
+      const int4 t = p.gstart ? make_int4(0, 0, 0, 0) : t4[r];
+      top = fmaxf(fmaxf(top, fmaxf(unit_share(w.x, t.x, V), unit_share(w.y, t.y, V))),
+                  fmaxf(unit_share(w.z, t.z, V), unit_share(w.w, t.w, V)));
     }
-    if (lane < M - 4 * quads) top = fmaxf(top, fabsf(p.dloss[4 * quads + lane]));
+    if (lane < M - 4 * quads) {
+      const int r = 4 * quads + lane;
+      top = fmaxf(top, unit_share(p.dloss[r], p.gstart ? 0 : p.ucol[r], V));
+    }
 #pragma unroll
     for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     if (lane == 0) *p.unit = head_unit(top);
@@ -617,7 +629,7 @@ struct HeadScore {
   float* tl;               // [rows][K]
   uint16_t* e;             // [rows][pitch] exp(z - max); NULL: the loss alone
   long long pitch;
-  const float* dloss;      // with e: [rows], whose largest magnitude goes to unit
+  const float* dloss;      // with e: [rows], whose largest magnitude goes to unit (as in HeadGemm)
   float* unit;
   int* err;
   unsigned long long limit_ns;
@@ -756,7 +768,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const float ninf = __int_as_float(0xff800000);
     if (p.e && blockIdx.x == 0 && warp == 2) {
       float top = 0.f;
-      for (int r = lane; r < p.rows; r += 32) top = fmaxf(top, fabsf(p.dloss[r]));
+      for (int r = lane; r < p.rows; r += 32)
+        top = fmaxf(top, unit_share(p.dloss[r], p.gstart ? 0 : p.ucol[r], p.V));
 #pragma unroll
       for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
       if (lane == 0) *p.unit = head_unit(top);
@@ -871,7 +884,8 @@ constexpr int kMaxTargets = 1024;
 
 // A row's K target columns: slot[k] = place of idx[k] among the row's distinct columns in ascending
 // order (kNoSlot for an absent entry or one beyond the vocabulary), ucol = those columns, gstart =
-// the first of them in each group of `width` columns.  A sort by ranks (K is at most a thousand; each
+// the first of them in each group of `width` columns; up = its dloss, or 0 where the row has no gradient (no
+// entry, only ones of weight 0, or one beyond the vocabulary).  A sort by ranks (K is at most a thousand; each
 // thread compares its entry with all others, four per read), then a scan of the changes of column.  The
 // logits' product needs the lists in its epilogue only, and starts beside this kernel: the trigger comes
 // after the wait, so that what precedes this kernel is complete when the next one's copies begin.
@@ -879,7 +893,8 @@ constexpr int kListThreads = 256;
 __global__ void __launch_bounds__(kListThreads)
     head_targets_kernel(const int32_t* __restrict__ idx, int K, int V, int groups, int width,
                         uint16_t* __restrict__ slot, int32_t* __restrict__ ucol,
-                        uint16_t* __restrict__ gstart) {
+                        uint16_t* __restrict__ gstart, const float* __restrict__ tlogit, float invT,
+                        const float* __restrict__ dloss, float* __restrict__ up) {
   extern __shared__ __align__(16) int tsm[];
   const int K4 = (K + 3) / 4 * 4;
   int* is = tsm;         // [K4] columns, none: the largest integer
@@ -891,12 +906,15 @@ __global__ void __launch_bounds__(kListThreads)
   pdl_trigger();
   const long long row = blockIdx.x;
   const int t = threadIdx.x;
+  int weighs = 0, beyond = 0;
   for (int k = t; k < K4; k += kListThreads) {
-    const int c = k < K ? idx[row * K + k] : NONE;
+    const int c = k < K ? idx[row * K + k] : -1;
     is[k] = c >= 0 && c < V ? c : NONE;
     ss[k] = NONE;
+    beyond |= c >= V;
+    if (dloss && c >= 0) weighs |= tlogit[row * K + k] * invT != __int_as_float(0xff800000);
   }
-  __syncthreads();
+  weighs = __syncthreads_or(weighs);
   constexpr int EACH = kMaxTargets / kListThreads;  // entries of a thread
   int pos[EACH];
 #pragma unroll
@@ -915,7 +933,8 @@ __global__ void __launch_bounds__(kListThreads)
       ss[r] = c;
     }
   }
-  __syncthreads();
+  beyond = __syncthreads_or(beyond);
+  if (dloss && t == 0) up[row] = weighs && !beyond ? dloss[row] : 0.f;
   // slot of place p: the changes of column up to it, less one; a thread takes neighbouring places
   const int per = (K4 + kListThreads - 1) / kListThreads;
   int own[EACH], n = 0;
@@ -1504,7 +1523,7 @@ struct Plan {
   int sums;          // partial sums of dx (the splits, times dz's pieces)
   int height, tiles;  // few rows: vocabulary rows of a tile and tiles (else 0)
   // workspace offsets
-  size_t unit, part, tl, ucol, slot, gstart, e, dz, dz2, xs, ws, acc, dxp, bytes;
+  size_t unit, part, tl, ucol, slot, gstart, up, e, dz, dz2, xs, ws, acc, dxp, bytes;
 };
 
 bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o) {
@@ -1558,6 +1577,7 @@ bool plan(poetx_dtype dt, int N, int D, int V, int K, bool dx, bool dW, Plan* o)
   o->ucol = take(R * K * 4);
   o->slot = take(R * K * 2);
   o->gstart = take(R * ((o->tiles ? o->tiles : o->groups) + 1) * 2);
+  o->up = o->grads ? take(R * 4) : 0;
   o->e = o->grads ? take(R * o->Vp * (o->f32 ? 4 : 2)) : 0;
   o->dz = o->f32 && o->grads ? take(3 * align_up(R * o->Vp * 2, 1024)) : o->e;
   o->dz2 = o->fine ? take(R * o->Vp * 2) : 0;
@@ -1684,16 +1704,20 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     const int32_t* ucol = idx;
     uint16_t* slot = reinterpret_cast<uint16_t*>(w + pl.slot);
     uint16_t* gstart = nullptr;
+    const float* unit_of = c.dloss ? c.dloss + r0 : nullptr;
     if (c.tlogit) {
+      float* up = reinterpret_cast<float*>(w + pl.up);
       int32_t* u = reinterpret_cast<int32_t*>(w + pl.ucol);
       gstart = reinterpret_cast<uint16_t*>(w + pl.gstart);
       POETX_CUDA_TRY(launch_pdl(head_targets_kernel, dim3(rows), dim3(kListThreads),
                                 align_up((size_t)c.K, 4) * 12, s, idx,
                                 c.K, c.V, pl.tiles ? pl.tiles : pl.groups,
-                                pl.tiles ? pl.height : kGroup, slot, u, gstart));
+                                pl.tiles ? pl.height : kGroup, slot, u, gstart, c.tlogit + r0 * c.K,
+                                1.f / c.T, pl.grads ? unit_of : (const float*)nullptr, up));
       POETX_CUDA_TRY(cudaGetLastError());
       after_launch(s, ST_HEAD_ROW);
       ucol = u;
+      unit_of = up;
     }
     // the logits' product
     HeadMaps mp, mw;
@@ -1717,7 +1741,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       h.tl = tl;
       h.e = pl.grads ? reinterpret_cast<uint16_t*>(w + pl.e) : nullptr;
       h.pitch = pl.Vp;
-      h.dloss = c.dloss ? c.dloss + r0 : nullptr;
+      h.dloss = unit_of;
       h.unit = unit;
       const bool maps = h.kps > 1 ? encode_tma_groups(&mp.a[0], wp, c.D, c.V, pl.height, h.kps) &&
                                         encode_tma_groups(&mp.b[0], xp, c.D, rows, nt, h.kps)
@@ -1753,7 +1777,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       g.K = c.K;
       g.tl = tl;
       g.store = pl.grads;
-      g.dloss = c.dloss ? c.dloss + r0 : nullptr;
+      g.dloss = unit_of;
       g.unit = unit;
       if (pl.grads && !encode_tma_2d(&mp.c, w + pl.e, pl.f32 ? TMA_F32 : TMA_BF16, pl.Vp, rows, pl.Vp,
                                      pl.f32 ? 32 : 64, 32, true))
