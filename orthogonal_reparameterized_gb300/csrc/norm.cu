@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(kRingThreads)
       ok = ok && mbar_wait_bounded(&full[grp][ring.st], ring.ph, err, limit_ns, kSite + __LINE__);
       const Vec<T, VEC>* xr = reinterpret_cast<const Vec<T, VEC>*>(ring.stage());
       const Vec<T, VEC>* dr = reinterpret_cast<const Vec<T, VEC>*>(ring.stage() + ring.row_bytes());
-      const float2 rs2 = both(rs[r]), nmr = both(-mu[r] * rs[r]);
+      const float2 rs2 = both(rs[r]), nmu = both(-mu[r]);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
         if (t + i * threads < nvec) {
@@ -650,7 +650,7 @@ __global__ void __launch_bounds__(kRingThreads)
           unpack2(dv[r][i], u);
 #pragma unroll
           for (int j = 0; j < H; ++j) {
-            h[j] = fma2(h[j], rs2, nmr);
+            h[j] = mul2(add2(h[j], nmu), rs2);
             ag[i][j] = fma2(u[j], h[j], ag[i][j]);
             ab[i][j] = add2(ab[i][j], u[j]);
             u[j] = mul2(u[j], gm[i][j]);
@@ -670,9 +670,9 @@ __global__ void __launch_bounds__(kRingThreads)
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
       if (r == 1 && !two) break;
-      // dx = dy (gamma rs) + x (rs c1) + (c0 - mu rs c1),  c0 = -rs mean(u), c1 = -rs mean(u h)
+      // dx = dy (gamma rs) + ((x - mu) rs c1 + c0),  c0 = -rs mean(u), c1 = -rs mean(u h)
       const float c0 = -(r ? w.z : w.x) * inv * rs[r], c1 = -(r ? w.w : w.y) * inv * rs[r];
-      const float2 rs2 = both(rs[r]), kx = both(rs[r] * c1), k0 = both(fmaf(-mu[r] * rs[r], c1, c0));
+      const float2 rs2 = both(rs[r]), nmu = both(-mu[r]), kx = both(rs[r] * c1), k0 = both(c0);
       Vec<T, VEC>* o = reinterpret_cast<Vec<T, VEC>*>(dx + row[r] * D);
 #pragma unroll
       for (int i = 0; i < NV; ++i)
@@ -681,7 +681,8 @@ __global__ void __launch_bounds__(kRingThreads)
           unpack2(xv[r][i], a);
           unpack2(dv[r][i], d);
 #pragma unroll
-          for (int j = 0; j < H; ++j) d[j] = fma2(d[j], mul2(gm[i][j], rs2), fma2(a[j], kx, k0));
+          for (int j = 0; j < H; ++j)
+            d[j] = fma2(d[j], mul2(gm[i][j], rs2), fma2(add2(a[j], nmu), kx, k0));
           o[t + i * threads] = pack2<T, VEC>(d);
         }
     }

@@ -89,3 +89,22 @@ def test_constant_rows_give_beta(P, vectors, N, dt):
     got = torch.empty_like(x)
     P.poetx_layernorm_fwd(x, got, gamma=gamma, beta=beta)
     assert torch.equal(got, beta.to(DT[dt]).expand(N, D))
+
+
+@pytest.mark.parametrize("N", [3, 4000])
+@pytest.mark.parametrize("vectors", [100, 200, 500, 1000])
+def test_backward_far_from_zero(P, vectors, N):
+    """Rows of 416 + N(0, 1) / 100 in fp32, with the forward's mean and rstd: x - mean is exact there,
+    and the gradients keep it."""
+    D = 4 * vectors
+    x, dy, gamma, beta = _inputs(N, D, "f32", vectors)
+    g = torch.Generator(device=DEV).manual_seed(9)
+    x = 416 + torch.randn(N, D, generator=g, device=DEV) / 100
+    got = _run(P, x, dy, gamma, beta)
+    ref, h, u = _definition(x, dy, gamma, beta, 1e-5, got["mean"], got["rstd"])
+    row = lambda a: a.abs().amax(1, keepdim=True)
+    _within(got["dx"], ref["dx"], 0, ref["rstd"][:, None] * row(u), "dx")
+    _within(got["dgamma"], ref["dgamma"], 0, (dy.double() * h).abs().sum(0), "dgamma")
+    x.fill_(416.0)
+    got = _run(P, x, dy, gamma, beta)
+    assert (got["mean"] == 416).all() and not got["dgamma"].any()
