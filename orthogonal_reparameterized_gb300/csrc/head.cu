@@ -12,9 +12,9 @@
 // taken in pieces.  Per piece: (1) the logits' product, whose epilogue leaves for each row and each
 // group of 128 columns the maximum m and the sum of exp(z - m), and stores exp(z - m) in 16 bits
 // (pack_exp: 11 significant bits down to 43 nats below m, so that its rounding, 2^-11, stays below the
-// bf16 rounding of dz that follows; no fp32 logit is stored); (2) a row kernel that joins the groups into lse, writes the
-// loss and turns the row into dz in place (bf16); (3) dx = dz W and dW (+)= dz^T x.  That is 6 N V D
-// flops: nothing is computed twice.  The logits of the sparse targets leave the first product in
+// bf16 rounding of dz that follows; no fp32 logit is stored); (2) a row kernel that joins the groups into
+// lse, writes the loss and turns the row into dz in place (bf16); (3) dx = dz W and dW (+)= dz^T x.  That
+// is 6 N V D flops: nothing is computed twice.  The logits of the sparse targets leave the first product in
 // fp32, and the groups' sums leave the targets out: with O the sum of all other exponentials and e
 // the target's, -ln p = log1p(O / e) and p - 1 = -O / (O + e) keep their relative accuracy where p is
 // near 1 (lse - z_t and p - 1 would cancel).
@@ -436,22 +436,23 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
           tmem_ld_wait();
 #pragma unroll
           for (int i = 0; i < kGroup; ++i) v[i] = __uint_as_float(r[i / 32][i % 32]);
-        } else
+        } else {
 #pragma unroll
-        for (int j = 0; j < kGroup; j += 32) {
-          uint32_t r[32];
-          tmem_ld_32x32b_x32(ta + j, r);
-          tmem_ld_wait();
-          if (kb == c.kb0) {
+          for (int j = 0; j < kGroup; j += 32) {
+            uint32_t r[32];
+            tmem_ld_32x32b_x32(ta + j, r);
+            tmem_ld_wait();
+            if (kb == c.kb0) {
 #pragma unroll
-            for (int i = 0; i < 32; ++i) v[j + i] = __uint_as_float(r[i]);
-          } else {
+              for (int i = 0; i < 32; ++i) v[j + i] = __uint_as_float(r[i]);
+            } else {
 #pragma unroll
-            for (int i = 0; i < 32; i += 2) {
-              const float2 w = add2(make_float2(v[j + i], v[j + i + 1]),
-                                    make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
-              v[j + i] = w.x;
-              v[j + i + 1] = w.y;
+              for (int i = 0; i < 32; i += 2) {
+                const float2 w = add2(make_float2(v[j + i], v[j + i + 1]),
+                                      make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+                v[j + i] = w.x;
+                v[j + i + 1] = w.y;
+              }
             }
           }
         }
@@ -1766,7 +1767,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       lg.tiles_n = ceil_div(c.V, BN);
       lg.num_tiles = lg.tiles_m * lg.tiles_n;
       lg.num_kb = lg.kb_split = ceil_div(c.D, BK);
-        lg.M = rows;
+      lg.M = rows;
       lg.N = c.V;
       lg.n_store = (int)pl.Vp;  // columns V .. Vp - 1 are stored as zeros
       g.scale2 = kLog2e / c.T;

@@ -106,8 +106,8 @@ __device__ __forceinline__ float row_mean(float s, float D, float inv) {
   return r == r ? fmaf(r, inv, q) : q;  // (an infinite sum has no remainder)
 }
 
-// Few rows, or wide or odd ones (1 x 4096: 4 us, latency): a row per group of TPR threads, NV vectors of VEC elements per thread
-// (NV * TPR * VEC >= D; D a multiple of VEC).
+// Few rows, or wide or odd ones (1 x 4096: 4 us, latency): a row per group of TPR threads, NV vectors of VEC
+// elements per thread (NV * TPR * VEC >= D; D a multiple of VEC).
 template <typename T, int VEC, int TPR, int NV>
 __global__ void __launch_bounds__(kThreads)
     layernorm_fwd_kernel(const T* __restrict__ x, int N, int D, const float* __restrict__ gamma,
@@ -373,11 +373,11 @@ __global__ void __launch_bounds__(kThreads)
 }
 
 // The ring forms, for rows of 129 to 1024 16-byte vectors: one persistent CTA per SM of GROUPS thread
-// groups, each on rows of its own (while one waits at its barrier another computes).  A group's first
-// thread streams its rows into the group's shared-memory ring by 1-D TMA bulk copies, so that the
-// next rows are in flight whatever the group does; the barrier that joins a row's sums also says that
-// the row has been read, and its stage is refilled after it.  A thread owns NV vectors of every row
-// and keeps what belongs to their columns in registers over all rows.
+// groups (the forward: one), each on rows of its own (while one waits at its barrier another computes).  A
+// group's first thread streams its rows into the group's shared-memory ring by 1-D TMA bulk copies, so that
+// the next rows are in flight whatever the group does; the barrier that joins a row's sums also says that
+// the row has been read, and its stage is refilled after it.  A thread owns NV vectors of every row and
+// keeps what belongs to their columns in registers over all rows.
 constexpr int kSite = 7 * 10000;
 constexpr int kRingThreads = 512;
 
@@ -461,36 +461,33 @@ __device__ __forceinline__ float4 ring_join4(float4 v, float4* red, int warp, in
   return v;
 }
 
-// Forward: gamma and beta of the thread's columns in registers; two joins for two rows (the means,
-// then the squared deviations from them).
+// Forward, for many rows of more vectors than a warp's registers hold (513 to 1024): one group, two vectors
+// per thread, gamma and beta of the thread's columns in registers; two joins for two rows (the means, then
+// the squared deviations from them).
 // 4096 x 8192 bf16: 28.4 us, 4.7 TB/s (without the bound of one CTA per SM, which the ring's memory is,
 // the compiler kept to 64 or 98 registers: 33.3 us).
-template <typename T, int NV, int GROUPS>
+template <typename T>
 __global__ void __launch_bounds__(kRingThreads, 1)
     layernorm_fwd_ring_kernel(const T* __restrict__ x, int N, int D, const float* __restrict__ gamma,
                               const float* __restrict__ beta, float eps, T* __restrict__ y,
                               float* __restrict__ mean, float* __restrict__ rstd, int stages,
                               int* err, unsigned long long limit_ns) {
-  constexpr int VEC = 16 / sizeof(T), H = VEC / 2;
+  constexpr int VEC = 16 / sizeof(T), H = VEC / 2, NV = 2;
   extern __shared__ __align__(128) uint8_t ring_mem[];
-  __shared__ uint64_t full[GROUPS][kMaxRing];
-  __shared__ float2 red[GROUPS][2][kRingThreads / 32 / GROUPS];
-  const int threads = (int)blockDim.x / GROUPS, warps = threads / 32;
-  const int grp = (int)threadIdx.x / threads, t = (int)threadIdx.x - grp * threads;
-  const int warp = t >> 5, lane = t & 31;
+  __shared__ uint64_t full[kMaxRing];
+  __shared__ float2 red[2][kRingThreads / 32];
+  const int threads = (int)blockDim.x, warps = threads / 32;
+  const int t = (int)threadIdx.x, warp = t >> 5, lane = t & 31;
   pdl_trigger();
-  if (threadIdx.x == 0) {
-    for (int g = 0; g < GROUPS; ++g)
-      for (int i = 0; i < stages; ++i) mbar_init(&full[g][i], 1);
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(&full[i], 1);
     fence_mbar_init();
   }
   __syncthreads();
   pdl_wait();
-  const long long row0 = blockIdx.x + (long long)grp * gridDim.x;
-  const long long stride = (long long)gridDim.x * GROUPS;
+  const long long row0 = blockIdx.x, stride = gridDim.x;
   const int rows = row0 < N ? (int)((N - 1 - row0) / stride) + 1 : 0;
-  RowRing<T, 1> ring{{x}, ring_mem + (size_t)grp * stages * D * sizeof(T), full[grp], stages, rows, D,
-                     row0, stride};
+  RowRing<T, 1> ring{{x}, ring_mem, full, stages, rows, D, row0, stride};
   if (t == 0) ring.start();
   const int nvec = D / VEC;
   float2 gm[NV][H], bt[NV][H];
@@ -512,7 +509,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
     float2 h[2][NV][H], s[2];
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-      ok = ok && mbar_wait_bounded(&full[grp][ring.st], ring.ph, err, limit_ns, kSite + __LINE__);
+      ok = ok && mbar_wait_bounded(&full[ring.st], ring.ph, err, limit_ns, kSite + __LINE__);
       const Vec<T, VEC>* xr = reinterpret_cast<const Vec<T, VEC>*>(ring.stage());
       s[r] = both(0.f);
 #pragma unroll
@@ -524,8 +521,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
         }
       if (r == 0 && two) ring.next();
     }
-    float2 w = ring_join(make_float2(s[0].x + s[0].y, s[1].x + s[1].y), red[grp][0], warp, lane, warps,
-                         1 + grp, threads);
+    float2 w = ring_join(make_float2(s[0].x + s[0].y, s[1].x + s[1].y), red[0], warp, lane, warps, 1,
+                         threads);
     if (t == 0) {
       if (two) ring.refill(k, ring.before());
       ring.refill(k + two, ring.st);
@@ -544,8 +541,7 @@ __global__ void __launch_bounds__(kRingThreads, 1)
             s[r] = fma2(h[r][i][j], h[r][i][j], s[r]);
           }
     }
-    w = ring_join(make_float2(s[0].x + s[0].y, s[1].x + s[1].y), red[grp][1], warp, lane, warps, 1 + grp,
-                  threads);
+    w = ring_join(make_float2(s[0].x + s[0].y, s[1].x + s[1].y), red[1], warp, lane, warps, 1, threads);
     const float rs[2] = {rsqrtf(w.x * inv + eps), rsqrtf(w.y * inv + eps)};
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
@@ -874,18 +870,18 @@ cudaError_t ring_attr(K k) {
   return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
 }
 
-template <typename T, int NV, int GROUPS>
+template <typename T>
 cudaError_t fwd_ring(const void* x, int N, int D, const float* gamma, const float* beta, float eps,
                      void* y, float* mean, float* rstd, cudaStream_t s) {
   const size_t stage = (size_t)D * sizeof(T);
   const int threads = ring_shape(D / (16 / (int)sizeof(T))).threads;
-  const int stages = ring_stages(stage, GROUPS), grid = N < sm_count() ? N : sm_count();
-  auto k = layernorm_fwd_ring_kernel<T, NV, GROUPS>;
+  const int stages = ring_stages(stage, 1);
+  auto k = layernorm_fwd_ring_kernel<T>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [&] { attr = ring_attr(k); });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(k, dim3(grid), dim3(GROUPS * threads), GROUPS * stages * stage, s,
+  return launch_pdl(k, dim3(N < sm_count() ? N : sm_count()), dim3(threads), stages * stage, s,
                     static_cast<const T*>(x), N, D, gamma, beta, eps, static_cast<T*>(y), mean, rstd,
                     stages, device_error_word(), kWaitLimitNs);
 }
@@ -919,7 +915,7 @@ cudaError_t fwd_pick(const NormShape& f, const void* x, int N, int D, const floa
       if (nvec <= 128) return fwd_rows<T, VEC, 4>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
       if (nvec <= 256) return fwd_rows<T, VEC, 8>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
       if (nvec <= 512) return fwd_rows<T, VEC, 16>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
-      if (ring_rows(f, D)) return fwd_ring<T, 2, 1>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
+      if (ring_rows(f, D)) return fwd_ring<T>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
     }
   }
   if (f.tpr == 32) return fwd_launch<T, VEC, 32, 4>(x, N, D, gamma, beta, eps, y, mean, rstd, s);
