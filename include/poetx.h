@@ -70,7 +70,7 @@ poetx_status poetx_get_device_error(cudaStream_t stream);
  * (source file id) x 10000 + (source line) of the waiting call (file ids: 1 the tensor-core
  * GEMM engine, 2 the CNP products, 3 the index kernels, 4 the self-test, 5 the fused
  * backward block-diagonal product, 6 the linear head's products,
- * 7 the layer norm's backward), or 0 if none was
+ * 7 the layer norm's rings, forward and backward), or 0 if none was
  * recorded.  Host-only (no synchronisation); for diagnosis. */
 int poetx_timeout_site(void);
 
@@ -509,10 +509,11 @@ poetx_status poetx_layernorm_bwd(poetx_dtype dt, const void* x, const void* dy, 
  *           accumulate != 0 adds dW to its contents (dx is always overwritten).
  *   ws      scratch of poetx_head_workspace_bytes(dt, N, D, V, 1, dx != NULL, dW != NULL) bytes
  * bf16: products of bf16 operands summed in fp32; dz is rounded to bf16 for the gradients'
- * products (to two bf16 pieces where N <= 16), dx and dW are rounded once (over all rows).  fp32:
- * about fp32 accuracy throughout.  With gradients, rows are taken in pieces, so that at most about
- * 2 GB of 16-bit exponentials is held at a time (or as much as the fp32 sums of dW that pieces need
- * would take besides).  Outputs must not alias inputs.  z_loss >= 0. */
+ * products (to two bf16 pieces where N <= 128), dx and dW are rounded once (over all rows).  fp32:
+ * about fp32 accuracy throughout.  With gradients, rows are taken in pieces, so that at most
+ * 2.25 GiB of 16-bit exponentials is held at a time (or as much as the fp32 sums of dW that pieces need
+ * would take besides).  A logit of -inf is a probability of 0; a NaN logit makes its row's loss, lse and
+ * dx NaN.  Outputs must not alias inputs.  z_loss >= 0. */
 size_t poetx_head_workspace_bytes(poetx_dtype dt, int N, int D, int V, int K, int want_dx,
                                   int want_dW);
 poetx_status poetx_head_ce(poetx_dtype dt, const void* x, int N, int D, const void* W, int V,

@@ -464,8 +464,8 @@ __device__ __forceinline__ float4 ring_join4(float4 v, float4* red, int warp, in
 // Forward, for many rows of more vectors than a warp's registers hold (513 to 1024): one group, two vectors
 // per thread, gamma and beta of the thread's columns in registers; two joins for two rows (the means, then
 // the squared deviations from them).
-// 4096 x 8192 bf16: 28.4 us, 4.7 TB/s (without the bound of one CTA per SM, which the ring's memory is,
-// the compiler kept to 64 or 98 registers: 33.3 us).
+// 4096 x 8192 bf16: 28.0 us, 4.8 TB/s (32.0 us without the bound of one CTA per SM, which the ring's memory
+// sets: the compiler then keeps to fewer registers).
 template <typename T>
 __global__ void __launch_bounds__(kRingThreads, 1)
     layernorm_fwd_ring_kernel(const T* __restrict__ x, int N, int D, const float* __restrict__ gamma,
@@ -566,8 +566,8 @@ __global__ void __launch_bounds__(kRingThreads, 1)
 
 // Backward: a thread keeps gamma and the sums of dy h and dy of its columns; one join for two rows.  At
 // the end the groups' sums are added through shared memory, so that there is one row of partials per SM.
-// 8192 x 4096 bf16: 40.2 us with the reduction, 5.0 TB/s; without its loads and stores it takes 30 us
-// (320 instructions per warp and row, and the join's chain).
+// 8192 x 4096 bf16: 40.5 us with the reduction, 5.0 TB/s; without its loads and stores it takes three
+// quarters of that (some 340 instructions per warp and row, and the join's chain).
 template <typename T, int NV, int GROUPS>
 __global__ void __launch_bounds__(kRingThreads)
     layernorm_bwd_ring_kernel(const T* __restrict__ x, const T* __restrict__ dy, int N, int D,
