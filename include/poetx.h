@@ -70,8 +70,8 @@ poetx_status poetx_get_device_error(cudaStream_t stream);
  * (source file id) x 10000 + (source line) of the waiting call (file ids: 1 the tensor-core
  * GEMM engine, 2 the CNP products, 3 the index kernels, 4 the self-test, 5 the fused
  * backward block-diagonal product, 6 the linear head's products,
- * 7 the layer norm's rings, forward and backward), or 0 if none was
- * recorded.  Host-only (no synchronisation); for diagnosis. */
+ * 7 the layer norm's rings, forward and backward, 8 the gated feed-forward block's
+ * projections), or 0 if none was recorded.  Host-only (no synchronisation); for diagnosis. */
 int poetx_timeout_site(void);
 
 /* Self-test of the bounded-wait machinery: launches one block that waits on a shared-memory
@@ -535,6 +535,131 @@ poetx_status poetx_head_distill(poetx_dtype dt, const void* x, int N, int D, con
                                 float temperature, const float* dloss, float* loss, float* lse,
                                 void* dx, void* dW, int accumulate, void* ws, size_t ws_bytes,
                                 cudaStream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * The gated feed-forward block: h = a(g) u of a gate g and a value u, alone (between the gate, up
+ * and down POET-X layers) or with both projections in front of it
+ * ------------------------------------------------------------------------------------- */
+
+/* a(g) = g s with s = 1 / (1 + exp(-t)):
+ *   POETX_SILU  t = g
+ *   POETX_GELU  t = 2 sqrt(2 / pi) (g + 0.044715 g^3), which is the tanh form of GELU
+ * and a'(g) = s + g s (1 - s) t'(g). */
+typedef enum { POETX_SILU = 0, POETX_GELU = 1 } poetx_activation;
+
+/* h = a(g) u, elementwise in fp32, rounded once to dt (POETX_BF16 or POETX_F32).
+ *   g, u    [N, F] with rows `pitch` elements apart (F: two arrays of their own; 2 F: the halves of
+ *           one [N, 2 F] array);  h [N, F], not an alias of either
+ *   F       a multiple of 8, 8 <= F <= 2097152;  pitch a multiple of 8, >= F  (else POETX_ERR_SHAPE) */
+poetx_status poetx_glu_fwd(poetx_dtype dt, poetx_activation act, const void* g, const void* u, int N,
+                           int F, long long pitch, void* h, cudaStream_t stream);
+/* dg = dh u a'(g), du = dh a(g), rows d_pitch elements apart (as pitch); dh [N, F].  dg may be g itself
+ * and du u itself (in place, with the same pitch); other overlaps are the caller's error. */
+poetx_status poetx_glu_bwd(poetx_dtype dt, poetx_activation act, const void* g, const void* u,
+                           const void* dh, int N, int F, long long pitch, void* dg, void* du,
+                           long long d_pitch, cudaStream_t stream);
+
+/* z = x W^T with W [2 F, D], whose first F rows give the gate and the others the value;
+ * h = a(z[:, :F]) z[:, F:] from the fp32 sums, rounded once.
+ *   dt      POETX_BF16 or POETX_F32: x [N, D], W, h [N, F], z.  D and F multiples of 8,
+ *           8 <= D <= 131072, 8 <= F <= 2097152, N >= 0 (POETX_ERR_SHAPE otherwise)
+ *   z       [N, 2 F] output (nullable): the projections, for the backward
+ *   ws      scratch of poetx_ffn_fwd_workspace_bytes(dt, N, D, F) bytes (bf16: 0, ws may be NULL)
+ * Outputs must not alias inputs. */
+size_t poetx_ffn_fwd_workspace_bytes(poetx_dtype dt, int N, int D, int F);
+poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, const void* x, int N, int D,
+                           const void* W, int F, void* h, void* z, void* ws, size_t ws_bytes,
+                           cudaStream_t stream);
+/* Backward from dh [N, F], with x and W of the forward: dz = [dh u a'(g) | dh a(g)],
+ *   dx = dz W [N, D],  dW = dz^T x [2 F, D]   (each nullable, not both; dtype dt)
+ *   z       the forward's projections [N, 2 F], or NULL: they are computed again (half as much
+ *           arithmetic again, nothing kept between forward and backward)
+ *   accumulate != 0 adds dW to its contents (dx is always overwritten)
+ *   ws      scratch of poetx_ffn_bwd_workspace_bytes(dt, N, D, F, z != NULL, dx != NULL, dW != NULL)
+ * bf16: dz is rounded to bf16 for the products (to two bf16 pieces where N <= 128); without z the
+ * projections are rounded to bf16 too.  fp32: about fp32 accuracy throughout. */
+size_t poetx_ffn_bwd_workspace_bytes(poetx_dtype dt, int N, int D, int F, int have_z, int want_dx,
+                                     int want_dW);
+poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, const void* x, int N, int D,
+                           const void* W, int F, const void* z, const void* dh, void* dx, void* dW,
+                           int accumulate, void* ws, size_t ws_bytes, cudaStream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * Queries and keys: the norm of each head and the rotation by the tokens' positions, in one pass
+ * ------------------------------------------------------------------------------------- */
+
+/* For each head's row x [head_dim] of a token with positions pos[0 .. axes-1]:
+ *   n = x rstd gamma, rstd = 1 / sqrt(mean(x^2) + eps)       (norm = 0: n = x)
+ *   the pairs (a, b) = (n_i, n_{i + rot_dim/2}) (interleaved: (n_2i, n_{2i+1})), i < rot_dim / 2,
+ *   become (a cos - b sin, a sin + b cos) of the angle pos[axis[i]] inv_freq[i]; the elements from
+ *   rot_dim on stay n.
+ * head_dim and rot_dim are multiples of 8, 8 <= rot_dim <= head_dim <= 256 (512 where both are
+ * multiples of 16), 1 <= axes <= 8.
+ * inv_freq [rot_dim / 2] fp32; axis [rot_dim / 2] int32 in 0 .. axes-1 (nullable: all 0; a value outside
+ * makes its pair NaN); both device.  Positions are int32, of either sign.  Angles are reduced in
+ * 64-bit fixed point, exact to 2^-32 turns at any position for |inv_freq| <= 2 pi. */
+typedef struct poetx_rope {
+  int head_dim, rot_dim;
+  int interleaved;
+  int axes;
+  int norm;
+  float eps;
+  const float* inv_freq;
+  const int32_t* axis;
+} poetx_rope;
+
+/* One side of a call (queries or keys): `heads` heads of every token, a token's rows one after the
+ * other, tokens `*pitch` elements apart (a multiple of 8, at least heads * head_dim). */
+typedef struct poetx_heads {
+  int heads;             /* 0: no such side */
+  const void* x;         /* input of the forward (backward without the norm: unused) */
+  long long x_pitch;
+  const float* gamma;    /* [head_dim] fp32 (nullable: 1; used with norm) */
+  const void* dy;        /* backward: gradient of the rotated output */
+  long long dy_pitch;
+  void* y;               /* forward: the output; backward: the gradient of x */
+  long long y_pitch;
+  float* dgamma;         /* backward, with norm: [head_dim] fp32 (nullable) */
+} poetx_heads;
+
+/* Forward for queries and keys in one launch.  pos [axes, N] int32 (pos, inv_freq and axis need no more
+ * than their elements' alignment: a slice of a longer array will do).  dt: POETX_BF16 or POETX_F32.  A
+ * side's y may be its x itself (with the same pitch). */
+poetx_status poetx_qk_rope_fwd(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, int N,
+                               const poetx_heads* q, const poetx_heads* k, cudaStream_t stream);
+/* Backward: with dn = the rotation of dy by the opposite angle, h = x rstd and u = dn gamma,
+ *   dx = rstd (u - h mean(u h)),  dgamma (+)= sum over tokens and heads of dn h  (fixed order)
+ * (norm = 0: dx = dn).  A side's y may be its dy itself.  ws: poetx_qk_rope_bwd_workspace_bytes(r)
+ * bytes; may be NULL when no dgamma is wanted.  accumulate != 0 adds to dgamma. */
+size_t poetx_qk_rope_bwd_workspace_bytes(const poetx_rope* r);
+poetx_status poetx_qk_rope_bwd(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, int N,
+                               const poetx_heads* q, const poetx_heads* k, int accumulate, void* ws,
+                               size_t ws_bytes, cudaStream_t stream);
+
+/* ----------------------------------------------------------------------------------------
+ * The global norm of many gradients, clipping by it, and the optimizer step on many tensors
+ * ------------------------------------------------------------------------------------- */
+
+/* norm[0] = sqrt(sum over every element of every tensor of g^2), fp32 on the device, summed in a fixed
+ * order (fp32 within a thread's few thousand terms, 64 bits above).  g, count, dt: HOST arrays of n
+ * device pointers (16-byte aligned), element counts (0 to 2^33; POETX_ERR_SHAPE above) and types
+ * (POETX_F32 or POETX_BF16), read before the call returns.  Squares that would leave fp32's range are taken in 64 bits.  n >= 0 (0:
+ * norm 0).  ws: poetx_grad_norm_workspace_bytes(n) bytes. */
+size_t poetx_grad_norm_workspace_bytes(int n);
+poetx_status poetx_grad_norm(const void* const* g, const poetx_dtype* dt, const long long* count,
+                             int n, float* norm, void* ws, size_t ws_bytes, cudaStream_t stream);
+/* g <- g min(1, max_norm / (norm[0] + 1e-6)) in place for every tensor (arrays as above); nothing is
+ * written where the factor is 1.  With a finite max_norm an infinite norm gives the factor 0; a NaN norm
+ * gives the factor NaN.  max_norm >= 0 (POETX_ERR_ARG otherwise).  The tensors do not overlap. */
+poetx_status poetx_grad_clip(void* const* g, const poetx_dtype* dt, const long long* count, int n,
+                             float max_norm, const float* norm, cudaStream_t stream);
+/* poetx_adam_triu on n sets of tensors (HOST arrays of device pointers; count[i] elements each), with
+ * every gradient multiplied by the factor of poetx_grad_clip as it is read (norm NULL: not at all;
+ * dq itself is not written).  Without norm, or with the factor 1, bit for bit the result of
+ * poetx_adam_triu on each. */
+poetx_status poetx_adam_group(float* const* q, const float* const* dq, float* const* m,
+                              float* const* v, const long long* count, int n, const poetx_adam* hp,
+                              float max_norm, const float* norm, cudaStream_t stream);
 
 #ifdef __cplusplus
 }

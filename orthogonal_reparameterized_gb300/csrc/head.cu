@@ -102,7 +102,7 @@ struct HeadGemm {
   int store;             // whether exp(z - m) is stored
   const float* dloss;    // with store: [M] upstream gradients (lists: of the rows with one, else 0), whose
   float* unit;           //   largest magnitude goes to unit (head_unit), read back as
-  const float* out_scale;  // gradients' products: factor of the sums
+  const float* out_scale;  // gradients' products: factor of the sums (nullable: 1), times T
   float T;
   int* err;
   unsigned long long limit_ns;
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
     const int q = warp & 3;
     const int cbeg = ((warp - 2) >> 2) * kGroup;
     uint8_t* stg = staging + (warp - 2) * STG;
-    const float out_scale = LSE ? 1.f : *p.out_scale * p.T;
+    const float out_scale = LSE ? 1.f : (p.out_scale ? *p.out_scale * p.T : p.T);
     Ring<2> acc;
     bool ok = true;
     for (int t = t0; t < p.num_tiles && ok; t += t_step) {
@@ -1643,6 +1643,108 @@ SplitArray split_of(const float* src, long long count, uint8_t* dst, size_t step
   return a;
 }
 
+}  // namespace
+
+// The products behind dz (see kernels.h); between the pieces of a bf16 head dW's sum stays in fp32.
+poetx_status grad_products(const GradProducts& c, cudaStream_t s) {
+  const int np = c.f32 ? 3 : 1, rows = c.rows;
+  const int sums = c.fine ? 2 * c.splits : c.splits;  // partial sums of dx
+  HeadMaps mp, mw;
+  HeadGemm h{};
+  const int nz = c.f32 ? 3 : (c.fine ? 2 : 1);  // dz's pieces
+  set_segs(&h, c.f32, false, rows);
+  h.out_scale = c.unit;
+  h.T = c.T;
+  int used = 0;
+  const int c_rows = (int)align_up((size_t)rows, 256);
+  if (c.dx) {
+    Product& d = h.prod[used++];
+    for (int i = 0; i < nz; ++i)
+      if (!bf16_map(&mp.a[i], c.z[i], c.pitch, rows, 64, 128)) return POETX_ERR_CUDA;
+    for (int i = 0; i < np; ++i)
+      if (!mn_map(&mp.b[i], c.w + i * c.w_step, c.D, c.V)) return POETX_ERR_CUDA;
+    d.b_groups = c.D % 64 == 0;
+    d.tiles_m = ceil_div(rows, 2 * BM);
+    d.tiles_n = ceil_div(c.D, BN);
+    d.num_tiles = d.tiles_m * d.tiles_n * c.splits;
+    d.num_kb = ceil_div(c.V, BK);
+    d.kb_split = ceil_div(d.num_kb, c.splits);
+    d.M = rows;
+    d.N = d.n_store = c.D;
+    d.c_rows = c_rows;
+    d.c_f32 = c.f32 || sums > 1;
+    const void* dst = sums > 1 ? static_cast<const void*>(c.dxp) : c.dx;
+    const long long drows = sums > 1 ? (long long)c.splits * c_rows : rows;
+    if (!encode_tma_2d(&mp.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, drows, c.D, d.c_f32 ? 32 : 64, 32,
+                       true))
+      return POETX_ERR_CUDA;
+  }
+  if (c.dW) {
+    Product& d = h.prod[used];
+    HeadMaps& m = used++ ? mw : mp;
+    for (int i = 0; i < nz; ++i)
+      if (!mn_map(&m.a[i], c.z[i], c.pitch, rows)) return POETX_ERR_CUDA;
+    for (int i = 0; i < np; ++i)
+      if (!mn_map(&m.b[i], c.x + i * c.x_step, c.D, rows)) return POETX_ERR_CUDA;
+    d.b_groups = c.D % 64 == 0;
+    d.tiles_m = ceil_div(c.V, 2 * BM);
+    d.tiles_n = ceil_div(c.D, BN);
+    d.num_tiles = d.tiles_m * d.tiles_n;
+    d.n_fast = !c.fine;  // (few rows: down the vocabulary 1-3 % faster)
+    d.num_kb = d.kb_split = ceil_div(rows, BK) * (c.fine ? 2 : 1);
+    d.a_mn = 1;
+    d.M = d.c_rows = c.V;
+    d.N = d.n_store = c.D;
+    d.c_f32 = c.f32 || !c.last;
+    void* dst = c.f32 || c.last ? c.dW : static_cast<void*>(c.acc);
+    if (c.f32)
+      d.add_f32 = !c.first || c.accumulate ? static_cast<const float*>(c.dW) : nullptr;
+    else
+      d.add_f32 = !c.first ? c.acc : nullptr;
+    if (!c.f32 && c.last && c.accumulate) d.add_bf16 = static_cast<const __nv_bfloat16*>(c.dW);
+    if (!encode_tma_2d(&m.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, c.V, c.D, d.c_f32 ? 32 : 64, 32,
+                       true))
+      return POETX_ERR_CUDA;
+  }
+  const HeadMaps& second = used > 1 ? mw : mp;
+  if (c.f32)
+    POETX_TRY((gemm<false, kMaxSegs>(mp, second, h, s)));
+  else if (c.fine)
+    POETX_TRY((gemm<false, 2>(mp, second, h, s)));
+  else
+    POETX_TRY((gemm<false, 1>(mp, second, h, s)));
+  if (c.dx && sums > 1) {
+    const long long quads = (long long)rows * c.D / 4;
+    const float* pp = c.dxp;
+    const long long stride = (long long)(c.fine ? BM : c_rows) * c.D;
+    if (c.f32)
+      POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, dim3(grid_for(quads, 256)), dim3(256), 0, s, pp,
+                                sums, stride, quads, static_cast<float*>(c.dx)));
+    else
+      POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, dim3(grid_for(quads, 256)), dim3(256), 0,
+                                s, pp, sums, stride, quads, static_cast<__nv_bfloat16*>(c.dx)));
+    POETX_CUDA_TRY(cudaGetLastError());
+    after_launch(s, ST_HEAD_ROW);
+  }
+  return POETX_OK;
+}
+
+int grad_splits(long long rows, int D, int V, bool f32) {
+  return dx_splits(rows, D, V, f32 ? kMaxSegs : 1);
+}
+
+poetx_status split_pieces(const float* a, long long na, uint8_t* da, size_t a_step, const float* b,
+                          long long nb, uint8_t* db, size_t b_step, cudaStream_t s) {
+  const SplitArray xa = split_of(a, na, da, a_step), wa = split_of(b, nb, db, b_step);
+  POETX_CUDA_TRY(launch_pdl(head_split_kernel, dim3(grid_for((xa.quads + wa.quads) / 4 + 1, 256)),
+                            dim3(256), 0, s, xa, wa));
+  POETX_CUDA_TRY(cudaGetLastError());
+  after_launch(s, ST_HEAD_ROW);
+  return POETX_OK;
+}
+
+namespace {
+
 poetx_status run_head(const HeadCall& c, cudaStream_t s) {
   if (c.N < 0 || c.D < 0 || c.V < 0) return POETX_ERR_ARG;
   if (c.dt != POETX_F32 && c.dt != POETX_BF16) return POETX_ERR_DTYPE;
@@ -1691,14 +1793,9 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     const uint8_t* xr = static_cast<const uint8_t*>(c.x) + (size_t)r0 * c.D * esz;
     const uint8_t* xp = pl.f32 ? w + pl.xs : xr;
     if (pl.f32) {  // the pieces of these rows, and with the first ones of W
-      const SplitArray xa = split_of(reinterpret_cast<const float*>(xr), (long long)rows * c.D,
-                                     w + pl.xs, x_step);
-      const SplitArray wa = split_of(static_cast<const float*>(c.W), pc ? 0 : (long long)c.V * c.D,
-                                     w + pl.ws, w_step);
-      POETX_CUDA_TRY(launch_pdl(head_split_kernel, dim3(grid_for((xa.quads + wa.quads) / 4 + 1, 256)),
-                                dim3(256), 0, s, xa, wa));
-      POETX_CUDA_TRY(cudaGetLastError());
-      after_launch(s, ST_HEAD_ROW);
+      POETX_TRY(split_pieces(reinterpret_cast<const float*>(xr), (long long)rows * c.D, w + pl.xs, x_step,
+                             static_cast<const float*>(c.W), pc ? 0 : (long long)c.V * c.D, w + pl.ws,
+                             w_step, s));
     }
     // a teacher's entries: distinct columns in order
     const int32_t* idx = c.idx + r0 * c.K;
@@ -1721,7 +1818,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
       unit_of = up;
     }
     // the logits' product
-    HeadMaps mp, mw;
+    HeadMaps mp;
     if (pl.tiles) {
       const int nt = rows <= 16 ? 16 : (rows <= 32 ? 32 : (rows <= 64 ? 64 : 128));
       HeadScore h{};
@@ -1829,88 +1926,30 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     POETX_CUDA_TRY(cudaGetLastError());
     after_launch(s, ST_HEAD_ROW);
     if (!pl.grads) continue;
-    // dx = dz W and dW (+)= dz^T x; between the pieces of a bf16 head dW's sum stays in fp32
-    HeadGemm h{};
-    const uint8_t* zp[3];  // dz's pieces
-    const int nz = pl.f32 ? 3 : (pl.fine ? 2 : 1);
-    for (int i = 0; i < 3; ++i) zp[i] = pl.fine && i ? w + pl.dz2 : w + pl.dz + i * z_step;
-    set_segs(&h, pl.f32, false, rows);
-    h.out_scale = unit;
-    h.T = c.T;
-    int used = 0;
-    uint8_t* dxr = static_cast<uint8_t*>(c.dx) + (size_t)r0 * c.D * esz;
-    const int c_rows = (int)align_up((size_t)rows, 256);
-    if (c.dx) {
-      Product& d = h.prod[used++];
-      for (int i = 0; i < nz; ++i)
-        if (!bf16_map(&mp.a[i], zp[i], pl.Vp, rows, 64, 128)) return POETX_ERR_CUDA;
-      for (int i = 0; i < np; ++i)
-        if (!mn_map(&mp.b[i], wp + i * w_step, c.D, c.V)) return POETX_ERR_CUDA;
-      d.b_groups = c.D % 64 == 0;
-      d.tiles_m = ceil_div(rows, 2 * BM);
-      d.tiles_n = ceil_div(c.D, BN);
-      d.num_tiles = d.tiles_m * d.tiles_n * pl.splits;
-      d.num_kb = ceil_div(c.V, BK);
-      d.kb_split = ceil_div(d.num_kb, pl.splits);
-      d.M = rows;
-      d.N = d.n_store = c.D;
-      d.c_rows = c_rows;
-      d.c_f32 = pl.f32 || pl.sums > 1;
-      const void* dst = pl.sums > 1 ? w + pl.dxp : dxr;
-      const long long drows = pl.sums > 1 ? (long long)pl.splits * c_rows : rows;
-      if (!encode_tma_2d(&mp.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, drows, c.D, d.c_f32 ? 32 : 64,
-                         32, true))
-        return POETX_ERR_CUDA;
-    }
-    if (c.dW) {
-      Product& d = h.prod[used];
-      HeadMaps& m = used++ ? mw : mp;
-      for (int i = 0; i < nz; ++i)
-        if (!mn_map(&m.a[i], zp[i], pl.Vp, rows)) return POETX_ERR_CUDA;
-      for (int i = 0; i < np; ++i)
-        if (!mn_map(&m.b[i], xp + i * x_step, c.D, rows)) return POETX_ERR_CUDA;
-      d.b_groups = c.D % 64 == 0;
-      d.tiles_m = ceil_div(c.V, 2 * BM);
-      d.tiles_n = ceil_div(c.D, BN);
-      d.num_tiles = d.tiles_m * d.tiles_n;
-      d.n_fast = !pl.fine;  // (few rows: down the vocabulary 1-3 % faster)
-      d.num_kb = d.kb_split = ceil_div(rows, BK) * (pl.fine ? 2 : 1);
-      d.a_mn = 1;
-      d.M = d.c_rows = c.V;
-      d.N = d.n_store = c.D;
-      const bool first = pc == 0, last = pc + 1 == pl.pieces;
-      d.c_f32 = pl.f32 || !last;
-      void* dst = pl.f32 || last ? c.dW : static_cast<void*>(w + pl.acc);
-      if (pl.f32)
-        d.add_f32 = !first || c.accumulate ? static_cast<const float*>(c.dW) : nullptr;
-      else
-        d.add_f32 = !first ? reinterpret_cast<const float*>(w + pl.acc) : nullptr;
-      if (!pl.f32 && last && c.accumulate) d.add_bf16 = static_cast<const __nv_bfloat16*>(c.dW);
-      if (!encode_tma_2d(&m.c, dst, d.c_f32 ? TMA_F32 : TMA_BF16, c.D, c.V, c.D, d.c_f32 ? 32 : 64, 32,
-                         true))
-        return POETX_ERR_CUDA;
-    }
-    const HeadMaps& second = used > 1 ? mw : mp;
-    if (pl.f32)
-      POETX_TRY((gemm<false, kMaxSegs>(mp, second, h, s)));
-    else if (pl.fine)
-      POETX_TRY((gemm<false, 2>(mp, second, h, s)));
-    else
-      POETX_TRY((gemm<false, 1>(mp, second, h, s)));
-    if (c.dx && pl.sums > 1) {
-      const long long quads = (long long)rows * c.D / 4;
-      const float* pp = reinterpret_cast<const float*>(w + pl.dxp);
-      const long long stride = (long long)(pl.fine ? BM : c_rows) * c.D;
-      if (pl.f32)
-        POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, dim3(grid_for(quads, 256)), dim3(256), 0, s,
-                                  pp, pl.sums, stride, quads, reinterpret_cast<float*>(dxr)));
-      else
-        POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, dim3(grid_for(quads, 256)),
-                                  dim3(256), 0, s, pp, pl.sums, stride, quads,
-                                  reinterpret_cast<__nv_bfloat16*>(dxr)));
-      POETX_CUDA_TRY(cudaGetLastError());
-      after_launch(s, ST_HEAD_ROW);
-    }
+    // dx = dz W and dW (+)= dz^T x
+    GradProducts gp{};
+    gp.f32 = pl.f32;
+    gp.fine = pl.fine;
+    gp.rows = rows;
+    gp.D = c.D;
+    gp.V = c.V;
+    gp.pitch = pl.Vp;
+    for (int i = 0; i < 3; ++i) gp.z[i] = pl.fine && i ? w + pl.dz2 : w + pl.dz + i * z_step;
+    gp.x = xp;
+    gp.x_step = x_step;
+    gp.w = wp;
+    gp.w_step = w_step;
+    gp.unit = unit;
+    gp.T = c.T;
+    gp.dx = c.dx ? static_cast<uint8_t*>(c.dx) + (size_t)r0 * c.D * esz : nullptr;
+    gp.dW = c.dW;
+    gp.accumulate = c.accumulate;
+    gp.first = pc == 0;
+    gp.last = pc + 1 == pl.pieces;
+    gp.acc = reinterpret_cast<float*>(w + pl.acc);
+    gp.splits = pl.splits;
+    gp.dxp = reinterpret_cast<float*>(w + pl.dxp);
+    POETX_TRY(grad_products(gp, s));
   }
   return POETX_OK;
 }

@@ -201,4 +201,33 @@ poetx_status umma_bdw(const void* T, const void* S, long long N, int nblk, int b
 poetx_status umma_wgrad(const void* X, const void* dY, long long N, int nblk, int b, int splits,
                         float* dG, cudaStream_t s);
 
+// ---- head.cu: dx = unit T dz W and dW (+)= unit T dz^T x from dz [rows][pitch] (pitch a multiple of 64
+// from V on, zeros past V) in one launch (and one for the sums of dx's splits).  bf16: dz in one piece, or
+// in two (fine, at most 128 rows); f32: dz, x and W in three bf16 pieces each, `step` bytes apart.  More
+// than one piece of rows: `first` and `last` say which, acc [V][D] holds dW's fp32 sum in between.
+struct GradProducts {
+  bool f32, fine;
+  int rows, D, V;
+  long long pitch;
+  const uint8_t* z[3];
+  const uint8_t* x;
+  size_t x_step;
+  const uint8_t* w;
+  size_t w_step;
+  const float* unit;  // device, nullable: 1
+  float T;
+  void* dx;           // [rows][D], nullable
+  void* dW;           // [V][D], nullable
+  int accumulate;     // dW
+  bool first, last;
+  float* acc;
+  int splits;         // K splits of dx (grad_splits)
+  float* dxp;         // [splits][rows up to 256][D] where splits or dz's pieces are more than one
+};
+poetx_status grad_products(const GradProducts& g, cudaStream_t s);
+int grad_splits(long long rows, int D, int V, bool f32);
+// The three bf16 pieces of two fp32 arrays (counts multiples of 4; the second may be empty).
+poetx_status split_pieces(const float* a, long long na, uint8_t* da, size_t a_step, const float* b,
+                          long long nb, uint8_t* db, size_t b_step, cudaStream_t s);
+
 }  // namespace poetx

@@ -19,10 +19,12 @@ LIB_PATH = os.path.join(_HERE, "libpoetx.so")
 
 F32, BF16, I8 = 0, 1, 2
 FAST, MEM = 0, 1
+SILU, GELU = 0, 1
 _DT = {torch.float32: F32, torch.bfloat16: BF16, torch.int8: I8}
 _TORCH_DT = {F32: torch.float32, BF16: torch.bfloat16, I8: torch.int8}
 
 _vp, _i, _sz, _f = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_float
+_ll = ctypes.c_longlong
 
 
 class PoetxError(RuntimeError):
@@ -42,6 +44,18 @@ class AdamDesc(ctypes.Structure):
     """Mirror of ``poetx_adam``."""
     _fields_ = [("lr", _f), ("beta1", _f), ("beta2", _f), ("eps", _f), ("weight_decay", _f),
                 ("step", _i)]
+
+
+class RopeDesc(ctypes.Structure):
+    """Mirror of ``poetx_rope``."""
+    _fields_ = [("head_dim", _i), ("rot_dim", _i), ("interleaved", _i), ("axes", _i), ("norm", _i),
+                ("eps", _f), ("inv_freq", _vp), ("axis", _vp)]
+
+
+class HeadsDesc(ctypes.Structure):
+    """Mirror of ``poetx_heads``."""
+    _fields_ = [("heads", _i), ("x", _vp), ("x_pitch", _ll), ("gamma", _vp), ("dy", _vp),
+                ("dy_pitch", _ll), ("y", _vp), ("y_pitch", _ll), ("dgamma", _vp)]
 
 
 _SIGS = {
@@ -110,6 +124,21 @@ _SIGS = {
                            _sz, _vp]),
     "poetx_head_distill": (_i, [_i, _vp, _i, _i, _vp, _i, _vp, _vp, _i, _f, _vp, _vp, _vp, _vp,
                                 _vp, _i, _vp, _sz, _vp]),
+    "poetx_glu_fwd": (_i, [_i, _i, _vp, _vp, _i, _i, _ll, _vp, _vp]),
+    "poetx_glu_bwd": (_i, [_i, _i, _vp, _vp, _vp, _i, _i, _ll, _vp, _vp, _ll, _vp]),
+    "poetx_ffn_fwd_workspace_bytes": (_sz, [_i, _i, _i, _i]),
+    "poetx_ffn_fwd": (_i, [_i, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
+    "poetx_ffn_bwd_workspace_bytes": (_sz, [_i, _i, _i, _i, _i, _i, _i]),
+    "poetx_ffn_bwd": (_i, [_i, _i, _vp, _i, _i, _vp, _i, _vp, _vp, _vp, _vp, _i, _vp, _sz, _vp]),
+    "poetx_qk_rope_fwd": (_i, [ctypes.POINTER(RopeDesc), _i, _vp, _i, ctypes.POINTER(HeadsDesc),
+                               ctypes.POINTER(HeadsDesc), _vp]),
+    "poetx_qk_rope_bwd_workspace_bytes": (_sz, [ctypes.POINTER(RopeDesc)]),
+    "poetx_qk_rope_bwd": (_i, [ctypes.POINTER(RopeDesc), _i, _vp, _i, ctypes.POINTER(HeadsDesc),
+                               ctypes.POINTER(HeadsDesc), _i, _vp, _sz, _vp]),
+    "poetx_grad_norm_workspace_bytes": (_sz, [_i]),
+    "poetx_grad_norm": (_i, [_vp, _vp, _vp, _i, _vp, _vp, _sz, _vp]),
+    "poetx_grad_clip": (_i, [_vp, _vp, _vp, _i, _f, _vp, _vp]),
+    "poetx_adam_group": (_i, [_vp, _vp, _vp, _vp, _vp, _i, ctypes.POINTER(AdamDesc), _f, _vp, _vp]),
 }
 
 _lib: Optional[ctypes.CDLL] = None
@@ -623,3 +652,254 @@ def poetx_head_distill(x, W, t_index, t_logit, loss, dloss=None, dx=None, dW=Non
     _want(fn, "t_logit", t_logit, shape, torch.float32)
     _head(fn, lib().poetx_head_distill, x, W, shape[1], t_index, t_logit, loss, dloss, dx, dW, lse,
           ws, stream, temperature, accumulate)
+
+
+# ---------------------------------------------------------------- the gated feed-forward block
+def _dtype(fn: str, t) -> int:
+    """The code of t's type; t must live on the current device."""
+    if not t.is_cuda:
+        raise ValueError("poetx: tensors must live on a CUDA device")
+    if t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors must live on the current device")
+    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+        raise ValueError(f"{fn}: bf16 or fp32, got {t.dtype}")
+    return _DT[t.dtype]
+
+
+def _rows(fn: str, what: str, t, width: int):
+    """(address, elements from row to row) of t [N, ...] whose rows of `width` elements are each
+    contiguous."""
+    if not t.is_cuda:
+        raise ValueError("poetx: tensors must live on a CUDA device")
+    at = width
+    for size, stride in zip(t.shape[1:], t.stride()[1:]):
+        at //= size if size else 1
+        if size > 1 and stride != at:
+            raise ValueError(f"{fn}: the rows of {what} must be contiguous")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else width
+
+
+def poetx_glu_fwd(g, u, h, act=SILU, stream=None):
+    """h [N, F] = a(g) u (bf16 or fp32); g and u [N, F] may be the halves of one [N, 2 F] tensor, or
+    any two with the same distance from row to row."""
+    fn = "poetx_glu_fwd"
+    N, F = g.shape
+    _want(fn, "u", u, g.shape, g.dtype)
+    _want(fn, "h", h, g.shape, g.dtype)
+    dt = _dtype(fn, g)
+    (pg, pitch), (pu, pitch_u) = _rows(fn, "g", g, F), _rows(fn, "u", u, F)
+    if pitch != pitch_u:
+        raise ValueError(f"{fn}: g and u must have the same distance from row to row")
+    st = lib().poetx_glu_fwd(dt, act, pg, pu, N, F, pitch, _addr(h), _raw_stream(stream, g))
+    if st:
+        _check(fn, st)
+
+
+def poetx_glu_bwd(g, u, dh, dg, du, act=SILU, stream=None):
+    """dg = dh u a'(g) and du = dh a(g); dg and du have the same distance from row to row, and may be g
+    and u themselves."""
+    fn = "poetx_glu_bwd"
+    N, F = g.shape
+    for what, t in (("u", u), ("dh", dh), ("dg", dg), ("du", du)):
+        _want(fn, what, t, g.shape, g.dtype)
+    dt = _dtype(fn, g)
+    (pg, pitch), (pu, pitch_u) = _rows(fn, "g", g, F), _rows(fn, "u", u, F)
+    (pdg, d_pitch), (pdu, d_pitch_u) = _rows(fn, "dg", dg, F), _rows(fn, "du", du, F)
+    if pitch != pitch_u or d_pitch != d_pitch_u:
+        raise ValueError(f"{fn}: g and u (dg and du) must have the same distance from row to row")
+    st = lib().poetx_glu_bwd(dt, act, pg, pu, _addr(dh), N, F, pitch, pdg, pdu, d_pitch,
+                             _raw_stream(stream, g))
+    if st:
+        _check(fn, st)
+
+
+def poetx_ffn_fwd_workspace_bytes(dt: int, N: int, D: int, F: int) -> int:
+    return lib().poetx_ffn_fwd_workspace_bytes(dt, N, D, F)
+
+
+def poetx_ffn_fwd(x, W, h, z=None, act=SILU, ws=None, stream=None):
+    """h [N, F] = a(x Wg^T) (x Wu^T) with W [2 F, D] = Wg's rows, then Wu's (bf16 or fp32); z [N, 2 F]
+    (optional): the projections, for the backward."""
+    fn = "poetx_ffn_fwd"
+    (N, D), F = x.shape, W.shape[0] // 2
+    _want(fn, "W", W, (2 * F, D), x.dtype)
+    _want(fn, "h", h, (N, F), x.dtype)
+    _want(fn, "z", z, (N, 2 * F), x.dtype)
+    dt, L, px = _dtype(fn, x), lib(), _addr(x)
+    handle = _raw_stream(stream, x)
+    if ws is None and dt == F32:
+        ws = _scratch(L.poetx_ffn_fwd_workspace_bytes(dt, N, D, F), x, stream, handle)
+    st = L.poetx_ffn_fwd(dt, act, px, N, D, _addr(W), F, _addr(h), _addr(z), _addr(ws),
+                         0 if ws is None else ws.numel(), handle)
+    if st:
+        _check(fn, st)
+
+
+def poetx_ffn_bwd_workspace_bytes(dt: int, N: int, D: int, F: int, have_z: bool = True,
+                                  want_dx: bool = True, want_dW: bool = True) -> int:
+    return lib().poetx_ffn_bwd_workspace_bytes(dt, N, D, F, int(have_z), int(want_dx), int(want_dW))
+
+
+def poetx_ffn_bwd(x, W, dh, z=None, dx=None, dW=None, act=SILU, accumulate=False, ws=None,
+                  stream=None):
+    """dx [N, D] and / or dW [2 F, D] from dh [N, F]; z: the forward's projections, or None (they are
+    computed again)."""
+    fn = "poetx_ffn_bwd"
+    (N, D), F = x.shape, W.shape[0] // 2
+    _want(fn, "W", W, (2 * F, D), x.dtype)
+    _want(fn, "dh", dh, (N, F), x.dtype)
+    _want(fn, "z", z, (N, 2 * F), x.dtype)
+    _want(fn, "dx", dx, x.shape, x.dtype)
+    _want(fn, "dW", dW, (2 * F, D), x.dtype)
+    dt, L, px = _dtype(fn, x), lib(), _addr(x)
+    handle = _raw_stream(stream, x)
+    if ws is None:
+        ws = _scratch(L.poetx_ffn_bwd_workspace_bytes(dt, N, D, F, z is not None, dx is not None,
+                                                      dW is not None), x, stream, handle)
+    st = L.poetx_ffn_bwd(dt, act, px, N, D, _addr(W), F, _addr(z), _addr(dh), _addr(dx), _addr(dW),
+                         1 if accumulate else 0, _addr(ws), ws.numel(), handle)
+    if st:
+        _check(fn, st)
+
+
+# ---------------------------------------------------------------- queries and keys
+def _rope(fn, x, pos, inv_freq, rot_dim, axis, interleaved, norm, eps):
+    """The checked descriptor and (type, N) of a call on x [N, heads, head_dim]."""
+    N, _, dh = x.shape
+    rot = dh if rot_dim is None else rot_dim
+    pos2 = pos if pos.dim() == 2 else pos[None]
+    _want(fn, "pos", pos2, (pos2.shape[0], N), torch.int32)
+    _want(fn, "inv_freq", inv_freq, (rot // 2,), torch.float32)
+    _want(fn, "axis", axis, (rot // 2,), torch.int32)
+    dt = _dtype(fn, x)
+    return dt, RopeDesc(dh, rot, int(bool(interleaved)), pos2.shape[0], int(bool(norm)), eps,
+                        _addr(inv_freq), _addr(axis))
+
+
+def _heads(fn, what, x, gamma, y, like, dt, dy=None, dgamma=None):
+    """The descriptor of one side (None: x is None)."""
+    if x is None:
+        return None
+    N, H, dh = x.shape
+    if (N, dh, x.dtype) != (like.shape[0], like.shape[2], like.dtype):
+        raise ValueError(f"{fn}: queries and keys must have the same tokens, head width and type")
+    for name, t in ((what, x), (f"the output for {what}", y), (f"d{what}", dy)):
+        if t is not None:
+            _want(fn, name, t, x.shape, x.dtype)
+    _want(fn, f"gamma_{what}", gamma, (dh,), torch.float32)
+    _want(fn, f"dgamma_{what}", dgamma, (dh,), torch.float32)
+    px, pitch = _rows(fn, what, x, H * dh)
+    py, y_pitch = _rows(fn, f"the output for {what}", y, H * dh)
+    pd, d_pitch = (None, 0) if dy is None else _rows(fn, f"d{what}", dy, H * dh)
+    return HeadsDesc(H, px, pitch, _addr(gamma), pd, d_pitch, py, y_pitch, _addr(dgamma))
+
+
+def poetx_qk_rope_fwd(q, k, pos, inv_freq, q_out, k_out, rot_dim=None, axis=None, interleaved=False,
+                      norm=True, gamma_q=None, gamma_k=None, eps=1e-6, stream=None):
+    """q_out [N, Hq, dh], k_out [N, Hk, dh] = queries and keys with each head normalised (norm) and
+    rotated by the angles pos * inv_freq.  pos [N] or [axes, N] int32; inv_freq [rot_dim / 2] fp32; axis
+    [rot_dim / 2] int32 (which positions each pair takes).  Tokens may be any distance apart, so that
+    q and k can lie in one row with the values; k may be None; an output may be its input."""
+    fn = "poetx_qk_rope_fwd"
+    dt, r = _rope(fn, q, pos, inv_freq, rot_dim, axis, interleaved, norm, eps)
+    sq = _heads(fn, "q", q, gamma_q, q_out, q, dt)
+    sk = _heads(fn, "k", k, gamma_k, k_out, q, dt)
+    st = lib().poetx_qk_rope_fwd(r, dt, _addr(pos), q.shape[0], sq, sk, _raw_stream(stream, q))
+    if st:
+        _check(fn, st)
+
+
+def poetx_qk_rope_bwd_workspace_bytes(r: RopeDesc) -> int:
+    return lib().poetx_qk_rope_bwd_workspace_bytes(ctypes.byref(r))
+
+
+def poetx_qk_rope_bwd(q, k, dq, dk, pos, inv_freq, dq_in, dk_in, rot_dim=None, axis=None,
+                      interleaved=False, norm=True, gamma_q=None, gamma_k=None, dgamma_q=None,
+                      dgamma_k=None, eps=1e-6, accumulate=False, ws=None, stream=None):
+    """dq_in, dk_in (the gradients of the forward's q and k) and, with norm and where given, dgamma_q,
+    dgamma_k [dh] fp32, from dq, dk (those of its outputs)."""
+    fn = "poetx_qk_rope_bwd"
+    dt, r = _rope(fn, q, pos, inv_freq, rot_dim, axis, interleaved, norm, eps)
+    sq = _heads(fn, "q", q, gamma_q, dq_in, q, dt, dq, dgamma_q)
+    sk = _heads(fn, "k", k, gamma_k, dk_in, q, dt, dk, dgamma_k)
+    handle, L = _raw_stream(stream, q), lib()
+    if ws is None and norm and (dgamma_q is not None or dgamma_k is not None):
+        ws = _scratch(L.poetx_qk_rope_bwd_workspace_bytes(r), q, stream, handle)
+    st = L.poetx_qk_rope_bwd(r, dt, _addr(pos), q.shape[0], sq, sk, 1 if accumulate else 0, _addr(ws),
+                             0 if ws is None else ws.numel(), handle)
+    if st:
+        _check(fn, st)
+
+
+# ---------------------------------------------------------------- many tensors
+def _arrays(fn, what, ts, dtypes):
+    """Pointers of the tensors as an array for the library."""
+    dev = torch.cuda.current_device()
+    for t in ts:
+        if t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError(f"{fn}: {what} must be contiguous tensors of {dtypes} on the current "
+                             f"CUDA device, got {t.dtype} on {t.device}")
+    return (_vp * len(ts))(*[t.data_ptr() for t in ts])
+
+
+_GRAD_TYPES = (torch.float32, torch.bfloat16)
+
+
+def _gradients(fn, grads):
+    p = _arrays(fn, "gradients", grads, _GRAD_TYPES)
+    n = len(grads)
+    return p, (_i * n)(*[_DT[t.dtype] for t in grads]), (_ll * n)(*[t.numel() for t in grads]), n
+
+
+def poetx_grad_norm_workspace_bytes(n: int) -> int:
+    return lib().poetx_grad_norm_workspace_bytes(n)
+
+
+def poetx_grad_norm(grads, norm, ws=None, stream=None):
+    """norm [1] fp32 = the 2-norm over all elements of the tensors in the list grads (fp32 or bf16,
+    mixed)."""
+    fn = "poetx_grad_norm"
+    _want(fn, "norm", norm, (1,), torch.float32)
+    pn = _addr(norm)
+    p, dts, counts, n = _gradients(fn, grads)
+    handle = _raw_stream(stream, norm)
+    if ws is None:
+        ws = _scratch(lib().poetx_grad_norm_workspace_bytes(n), norm, stream, handle)
+    st = lib().poetx_grad_norm(p, dts, counts, n, pn, _addr(ws), ws.numel(), handle)
+    if st:
+        _check(fn, st)
+
+
+def poetx_grad_clip(grads, norm, max_norm: float, stream=None):
+    """Every tensor of the list times min(1, max_norm / (norm + 1e-6)), in place; norm [1] as
+    poetx_grad_norm leaves it."""
+    fn = "poetx_grad_clip"
+    _want(fn, "norm", norm, (1,), torch.float32)
+    pn = _addr(norm)
+    p, dts, counts, n = _gradients(fn, grads)
+    st = lib().poetx_grad_clip(p, dts, counts, n, max_norm, pn, _raw_stream(stream, norm))
+    if st:
+        _check(fn, st)
+
+
+def poetx_adam_group(q, dq, m, v, step: int, lr: float, beta1: float = 0.9, beta2: float = 0.999,
+                     eps: float = 1e-8, weight_decay: float = 0.0, norm=None,
+                     max_norm: float = float("inf"), stream=None):
+    """poetx_adam_triu on lists of fp32 tensors at once; with norm [1] every gradient is multiplied by
+    min(1, max_norm / (norm + 1e-6)) as it is read (dq is not written)."""
+    fn = "poetx_adam_group"
+    n = len(q)
+    if len(dq) != n or len(m) != n or len(v) != n:
+        raise ValueError(f"{fn}: one dq, m and v per q")
+    count = [t.numel() for t in q]
+    for ts in (dq, m, v):
+        if [t.numel() for t in ts] != count:
+            raise ValueError(f"{fn}: dq, m and v must have the sizes of q")
+    _want(fn, "norm", norm, (1,), torch.float32)
+    arrays = [_arrays(fn, what, ts, (torch.float32,))
+              for what, ts in (("q", q), ("dq", dq), ("m", m), ("v", v))]
+    hp = AdamDesc(lr, beta1, beta2, eps, weight_decay, step)
+    handle = _stream(stream) if n == 0 else _raw_stream(stream, q[0])
+    st = lib().poetx_adam_group(*arrays, (_ll * n)(*count), n, hp, max_norm, _addr(norm), handle)
+    if st:
+        _check(fn, st)

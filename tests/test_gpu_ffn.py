@@ -1,0 +1,216 @@
+"""The gated product and the gated feed-forward block against the fp64 definitions.
+
+Tolerances.  A bf16 rounding is off by at most half a step, 2^-8 of the value.  Elementwise bf16
+results: one rounding of fp32 arithmetic (a few 2^-22).  Products, relative Frobenius error: h and z
+carry one rounding; dx and dW the rounding of dz and their own, in a mean over the terms no more than
+two roundings; without kept projections dz also carries theirs, which move a gate's derivative and
+the value by up to two roundings more.  fp32: sums of six products of bf16 pieces, TOL_F32."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from gpu_util import DEV, P, TOL_F32, dev, host  # noqa: F401
+from oracle import block_oracle as B
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "f32": torch.float32}
+R = 2.0 ** -8  # one bf16 rounding
+EXTRA = 1e-4   # fp32 sums of products, against it
+
+
+def _glu_inputs(N, F, dt, seed):
+    r = np.random.default_rng(seed)
+    return [torch.tensor(r.standard_normal((N, F)) * s).to(DT[dt]) for s in (3.0, 1.0, 1.0)]
+
+
+def _near(got, ref, dt):
+    """Elementwise: one rounding and the arithmetic before it; a derivative near its zero is as
+    exact as its terms."""
+    scale = np.abs(ref) + 1e-2 * (np.abs(ref).max() if ref.size else 0)
+    tol = R * np.abs(ref) + 1e-5 * scale if dt == "bf16" else 2e-6 * scale
+    return (np.abs(got - ref) <= tol).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", [B.SILU, B.GELU])
+@pytest.mark.parametrize("N,F", [(1, 8), (3, 8), (7, 24), (130, 264), (33, 13824), (1000, 1096)])
+@pytest.mark.parametrize("halves", [False, True])
+def test_glu(P, N, F, act, dt, halves):
+    g, u, dh = _glu_inputs(N, F, dt, N + F + act)
+    ref, (rdg, rdu) = B.glu(host(g), host(u), act), B.glu_bwd(host(g), host(u), host(dh), act)
+    if halves:  # of one array, and the gradients of another
+        z = torch.cat([g, u], 1).to(DEV)
+        gd, ud = z[:, :F], z[:, F:]
+        dz = torch.empty_like(z)
+        dg, du = dz[:, :F], dz[:, F:]
+    else:
+        gd, ud = g.to(DEV), u.to(DEV)
+        dg, du = torch.empty_like(gd), torch.empty_like(ud)
+    h = torch.empty(N, F, dtype=DT[dt], device=DEV)
+    P.poetx_glu_fwd(gd, ud, h, act=act)
+    P.poetx_glu_bwd(gd, ud, dh.to(DEV), dg, du, act=act)
+    torch.cuda.synchronize()
+    assert _near(host(h), ref, dt)
+    assert _near(host(dg), rdg, dt) and _near(host(du), rdu, dt)
+    P.poetx_glu_bwd(gd, ud, dh.to(DEV), gd, ud, act=act)  # in place
+    assert torch.equal(gd, dg) and torch.equal(ud, du)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", [B.SILU, B.GELU])
+def test_glu_far_gates(P, act, dt):
+    """Gates far from zero: 0 or g itself, no NaN; an infinite gate of the positive side and NaN."""
+    inf = float("inf")
+    g = torch.tensor([[200.0, -200.0, 1e30, -1e30, inf, float("nan"), 0.0, -20.0]]).to(DT[dt])
+    u = torch.full((1, 8), 2.0).to(DT[dt])
+    h = torch.empty(1, 8, dtype=DT[dt], device=DEV)
+    P.poetx_glu_fwd(g.to(DEV), u.to(DEV), h, act=act)
+    got = host(h)[0]
+    assert got[0] == 2 * host(g)[0, 0] and got[2] == 2 * host(g)[0, 2] and got[4] == inf
+    assert got[1] == 0 and got[3] == 0 and got[6] == 0 and np.isnan(got[5])
+    ref = B.glu(host(g)[:, 7:], [[2.0]], act)[0, 0]
+    # in fp64 the tanh form has lost this tail, so only SiLU's is compared
+    assert act == B.GELU and abs(got[7]) < 1e-9 or abs(got[7] - ref) <= 1.1 * R * abs(ref)
+
+
+def _ffn_inputs(N, D, F, dt, seed):
+    r = np.random.default_rng(seed)
+    x = torch.tensor(r.standard_normal((N, D))).to(DT[dt])
+    W = torch.tensor(r.standard_normal((2 * F, D)) / np.sqrt(D)).to(DT[dt])
+    dh = torch.tensor(r.standard_normal((N, F)) / max(N, 1)).to(DT[dt])
+    return x, W, dh
+
+
+def _run(P, x, W, dh, act, kept, dx=True, dW=True, keep_z=True, **kw):
+    N, D, F = x.shape[0], x.shape[1], W.shape[0] // 2
+    xd, Wd, dhd = x.to(DEV), W.to(DEV), dh.to(DEV)
+    new = lambda *s: torch.full(s, float("nan"), dtype=x.dtype, device=DEV)
+    h, z = new(N, F), new(N, 2 * F) if keep_z else None
+    P.poetx_ffn_fwd(xd, Wd, h, z=z, act=act)
+    out = {"h": h, "z": z, "dx": new(N, D) if dx else None, "dW": new(2 * F, D) if dW else None}
+    P.poetx_ffn_bwd(xd, Wd, dhd, z=z if kept else None, dx=out["dx"], dW=out["dW"], act=act, **kw)
+    torch.cuda.synchronize()
+    assert P.poetx_get_device_error() == 0
+    return out
+
+
+SHAPES = [(1, 8, 8), (2, 64, 128), (5, 72, 40), (16, 256, 1000), (17, 264, 2056), (40, 192, 136),
+          (65, 128, 4096), (128, 520, 808), (129, 64, 64), (256, 136, 520), (300, 512, 1416),
+          (257, 1032, 264), (1021, 328, 648)]
+
+
+@pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
+@pytest.mark.parametrize("act", [B.SILU, B.GELU])
+@pytest.mark.parametrize("N,D,F", SHAPES)
+def test_ffn_bf16(P, N, D, F, act, kept):
+    x, W, dh = _ffn_inputs(N, D, F, "bf16", 7 * N + D + F)
+    got = _run(P, x, W, dh, act, kept)
+    h, z = B.ffn(host(x), host(W), act)
+    assert O.rel_fro(host(got["z"]), z) <= R + EXTRA
+    assert O.rel_fro(host(got["h"]), h) <= R + EXTRA
+    # the gradients of the kept projections as they are, or of the inputs
+    dx, dW = B.ffn_bwd(host(x), host(W), host(dh), act, host(got["z"]) if kept else None)
+    tol = (2 if kept else 4) * R + EXTRA
+    assert O.rel_fro(host(got["dx"]), dx) <= tol
+    assert O.rel_fro(host(got["dW"]), dW) <= tol
+
+
+@pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
+@pytest.mark.parametrize("N,D,F", [(1, 8, 8), (5, 72, 40), (130, 264, 392), (300, 512, 1000)])
+@pytest.mark.parametrize("act", [B.SILU, B.GELU])
+def test_ffn_f32(P, N, D, F, act, kept):
+    x, W, dh = _ffn_inputs(N, D, F, "f32", 5 * N + D + F)
+    got = _run(P, x, W, dh, act, kept)
+    h, z = B.ffn(host(x), host(W), act)
+    dx, dW = B.ffn_bwd(host(x), host(W), host(dh), act)
+    assert O.rel_fro(host(got["z"]), z) <= TOL_F32
+    for k, ref in (("h", h), ("dx", dx), ("dW", dW)):  # the product behind another: twice
+        assert O.rel_fro(host(got[k]), ref) <= 2 * TOL_F32, k
+
+
+@pytest.mark.parametrize("N,dt", [(40, "bf16"), (200, "bf16"), (70, "f32")])
+def test_ffn_options(P, N, dt):
+    """The same bits whatever else is asked for; dW added to what is there."""
+    x, W, dh = _ffn_inputs(N, 136, 328, dt, N)
+    full = _run(P, x, W, dh, B.SILU, True)
+    again = _run(P, x, W, dh, B.SILU, True)
+    for k in full:
+        assert torch.equal(full[k], again[k]), k
+    h = torch.empty_like(full["h"])
+    P.poetx_ffn_fwd(x.to(DEV), W.to(DEV), h)
+    assert torch.equal(h, full["h"])
+    only = _run(P, x, W, dh, B.SILU, True, dW=False)
+    assert torch.equal(only["dx"], full["dx"])
+    only = _run(P, x, W, dh, B.SILU, True, dx=False)
+    assert torch.equal(only["dW"], full["dW"])
+    base = torch.randn(full["dW"].shape, generator=torch.Generator().manual_seed(1)).to(DT[dt])
+    dW = base.to(DEV)
+    P.poetx_ffn_bwd(x.to(DEV), W.to(DEV), dh.to(DEV), z=full["z"], dW=dW, accumulate=True)
+    ref = B.ffn_bwd(host(x), host(W), host(dh), B.SILU, host(full["z"]))[1] + host(base)
+    assert O.rel_fro(host(dW), ref) <= (2 * R if dt == "bf16" else TOL_F32)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ffn_rows_on_their_own(P, dt):
+    """Each row's result is its own: a NaN row leaves the others' bits alone."""
+    for N in (33, 200):
+        x, W, dh = _ffn_inputs(N, 72, 200, dt, 3)
+        ref = _run(P, x, W, dh, B.SILU, True, dW=False)
+        x[7, 3] = float("nan")
+        got = _run(P, x, W, dh, B.SILU, True, dW=False)
+        keep = [i for i in range(N) if i != 7]
+        for k in ("h", "z", "dx"):
+            assert torch.isnan(got[k][7]).all(), k
+            assert torch.equal(got[k][keep], ref[k][keep]), k
+
+
+def test_ffn_empty_batch(P):
+    W = torch.randn(48, 64, device=DEV).bfloat16()
+    x, h = torch.empty(0, 64, device=DEV).bfloat16(), torch.empty(0, 24, device=DEV).bfloat16()
+    dW = torch.ones(48, 64, device=DEV).bfloat16()
+    P.poetx_ffn_fwd(x, W, h)
+    P.poetx_ffn_bwd(x, W, h.clone(), dW=dW, accumulate=True)
+    assert (dW == 1).all()
+    P.poetx_ffn_bwd(x, W, h.clone(), dW=dW)
+    assert not dW.any()
+    P.poetx_glu_fwd(h, h, h.clone())
+    P.poetx_glu_bwd(h, h, h, h.clone(), h.clone())
+
+
+@pytest.mark.parametrize("N", [1, 20, 150])
+def test_ffn_writes_only_its_rows(P, N):
+    x, W, dh = _ffn_inputs(N, 72, 136, "bf16", N)
+    xd, Wd, dhd = x.to(DEV), W.to(DEV), dh.to(DEV)
+    big = {k: torch.full((N + 3, w), 7.0, dtype=torch.bfloat16, device=DEV)
+           for k, w in (("h", 136), ("z", 272), ("dx", 72))}
+    P.poetx_ffn_fwd(xd, Wd, big["h"][:N], z=big["z"][:N])
+    P.poetx_ffn_bwd(xd, Wd, dhd, z=big["z"][:N], dx=big["dx"][:N])
+    torch.cuda.synchronize()
+    for k, t in big.items():
+        assert (t[N:] == 7).all(), k
+
+
+def test_ffn_on_another_stream_and_in_a_graph(P):
+    x, W, dh = _ffn_inputs(140, 128, 264, "bf16", 5)
+    ref = _run(P, x, W, dh, B.SILU, False)
+    xd, Wd, dhd = x.to(DEV), W.to(DEV), dh.to(DEV)
+    h, dx, dW = (torch.zeros_like(ref[k]) for k in ("h", "dx", "dW"))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    P.poetx_ffn_fwd(xd, Wd, h, stream=s)
+    P.poetx_ffn_bwd(xd, Wd, dhd, dx=dx, dW=dW, stream=s)
+    s.synchronize()
+    assert torch.equal(h, ref["h"]) and torch.equal(dx, ref["dx"]) and torch.equal(dW, ref["dW"])
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        P.poetx_ffn_fwd(xd, Wd, h)
+        P.poetx_ffn_bwd(xd, Wd, dhd, dx=dx, dW=dW)
+    for t in (h, dx, dW):
+        t.zero_()
+    xd.copy_(xd.roll(1, 0)), dhd.copy_(dhd.roll(1, 0))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(h, ref["h"].roll(1, 0)) and torch.equal(dx, ref["dx"].roll(1, 0))
+    assert O.rel_fro(host(dW), host(ref["dW"])) <= 2 * R  # (other order of its sums)
