@@ -576,8 +576,8 @@ poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, const void* x, 
  *           arithmetic again, nothing kept between forward and backward)
  *   accumulate != 0 adds dW to its contents (dx is always overwritten)
  *   ws      scratch of poetx_ffn_bwd_workspace_bytes(dt, N, D, F, z != NULL, dx != NULL, dW != NULL)
- * bf16: dz is rounded to bf16 for the products (to two bf16 pieces where N <= 128); without z the
- * projections are rounded to bf16 too.  fp32: about fp32 accuracy throughout. */
+ * bf16: dz is rounded to bf16 for the products (to two bf16 pieces where N <= 128).  fp32: about fp32
+ * accuracy throughout. */
 size_t poetx_ffn_bwd_workspace_bytes(poetx_dtype dt, int N, int D, int F, int have_z, int want_dx,
                                      int want_dW);
 poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, const void* x, int N, int D,

@@ -261,7 +261,8 @@ constexpr int kSegs = 6;
 
 struct FfnMaps {
   CUtensorMap a[3], g[3], u[3];  // x, W's gate rows, W's value rows (their pieces)
-  CUtensorMap h, zg, zu;
+  CUtensorMap h;       // DZ: dh
+  CUtensorMap zg, zu;  // DZ: dz's halves
 };
 struct FfnGemm {
   int tiles_m, tiles_f, num_tiles, num_kb;
@@ -306,7 +307,10 @@ __device__ __forceinline__ void tile_at(const FfnGemm& p, int t, int* mi, int* f
 // Warp 0 of each CTA loads its 128 rows of x and its 128 rows of W, one thread of the even CTA's warp 1
 // issues the MMAs, warps 2-9 read the accumulators back (warp w: rows 32 (w % 4).. of the CTA's 128,
 // features 64 ((w - 2) / 4).. of the tile's 128: their gates and their values).
-template <int SEGS>
+// DZ: the backward without kept projections.  The epilogue turns the fp32 sums into dz with the warp's box of
+// dh, which arrives by TMA in one of the warp's two staging boxes while the products run, so that the
+// projections are neither rounded nor stored.
+template <int SEGS, bool DZ>
 __global__ void __launch_bounds__(kThreads, 1)
     ffn_gemm_kernel(const __grid_constant__ FfnMaps maps, const __grid_constant__ FfnGemm p) {
   constexpr bool F32 = SEGS == kSegs;
@@ -321,7 +325,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint64_t* empty = full + kStages;
   uint64_t* tfull = empty + kStages;  // [2] accumulator written
   uint64_t* tempty = tfull + 2;       // [2] accumulator read by both CTAs' epilogue warps
-  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(tempty + 2);
+  uint64_t* dfull = tempty + 2;       // [kEpiWarps] the warp's box of dh has landed
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(dfull + kEpiWarps);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_slot + 1);
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -336,6 +341,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&tfull[a], 1);
       mbar_init(&tempty[a], 2 * kEpiWarps);
     }
+    for (int w = 0; w < kEpiWarps; ++w) mbar_init(&dfull[w], 1);
     *abort_flag = 0;
     fence_mbar_init();
     tma_prefetch_desc(&maps.a[0]);
@@ -434,6 +440,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int fbeg = ((warp - 2) >> 2) * (BF / 2);
     uint8_t* stg = staging + (warp - 2) * kBoxes * kStgBytes;
     Ring<2> acc;
+    uint64_t* dbar = &dfull[warp - 2];
+    uint32_t dph = 0;
     int buf = 0;
     bool ok = true;
     for (int t = t0; t < p.num_tiles && ok; t += t_step) {
@@ -441,6 +449,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tile_at(p, t, &mi, &fi);
       const int row_w = (2 * mi + crank) * BM + q * 32;  // the warp's first row
       const int f0 = fi * BF + fbeg;
+      const bool live = f0 < p.F && row_w < p.M;
+      if (DZ && live && lane == 0) {
+        bulk_wait_read<0>();  // the boxes of the tile before have been read
+        mbar_arrive_expect_tx(dbar, kStgBytes);
+        tma_load_2d(stg, &maps.h, dbar, f0, row_w);
+      }
       float v[BF];  // 64 gates, then their 64 values
       for (int c0 = 0; c0 < p.num_kb; c0 += p.chunk, acc.next()) {
         const int a = acc.s;
@@ -473,8 +487,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[a], 0));
       }
+      if (DZ && live) {  // (also where the products were given up: the copy must have landed at the end)
+        const bool got = mbar_wait_bounded(dbar, dph, p.err, p.limit_ns, kSite + __LINE__);
+        dph ^= 1;
+        if (!__all_sync(0xffffffffu, got)) {
+          *abort_flag = 1;
+          ok = false;
+        }
+      }
       if (!ok) break;
-      if (f0 >= p.F || row_w >= p.M) continue;
+      if (!live) continue;
       // Stores by TMA: boxes of 32 rows x 128 bytes, 128-byte swizzle; rows and features outside the
       // tensor are clipped.
       auto box = [&](const CUtensorMap* map, int col, auto chunk) {  // chunk(i): 16 bytes i of the row
@@ -510,6 +532,24 @@ __global__ void __launch_bounds__(kThreads, 1)
           });
         }
       };
+      if constexpr (DZ) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint4 w = *reinterpret_cast<const uint4*>(stg + lane * 128 + ((i ^ (lane & 7)) << 4));
+          const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float d = __uint_as_float(j & 1 ? u[j / 2] & 0xffff0000u : u[j / 2] << 16);
+            const float2 o = gated_grad<false>(v[8 * i + j], v[BF / 2 + 8 * i + j], d, p.act);
+            v[8 * i + j] = o.x;
+            v[BF / 2 + 8 * i + j] = o.y;
+          }
+        }
+        buf = 1;  // (the first box into the buffer that dh is not in)
+        put(&maps.zu, v + BF / 2);
+        put(&maps.zg, v);
+        continue;
+      }
       if (p.store_z) {
         put(&maps.zg, v);
         put(&maps.zu, v + BF / 2);
@@ -542,7 +582,10 @@ struct FfnScore {
   int tiles, height;  // height: a multiple of 8 (the swizzle's rows)
   int F, rows, stages;
   int kps, num_st;    // K blocks per stage, stages per tile
-  __nv_bfloat16 *h, *z;  // nullable
+  __nv_bfloat16 *h, *z;  // [rows][F], [rows][z_pitch] (each nullable)
+  const __nv_bfloat16* dh;  // [rows][F]: z and z2 are dz's two pieces (nullable)
+  __nv_bfloat16* z2;
+  long long z_pitch;
   Act act;
   int* err;
   unsigned long long limit_ns;
@@ -674,17 +717,29 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     const int q = warp & 3, mine = q * 32 + lane;  // the thread's feature of the tile
     Ring<2> acc;
     for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, acc.next()) {
-      const bool got = wait(&tfull[acc.s], acc.ph, kSite + __LINE__);
-      if (!__all_sync(0xffffffffu, got)) break;
-      tc_fence_after();
       const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 2 * NT);
       const long long f = (long long)t * p.height + mine;
       const bool on = mine < p.height && f < p.F;
+      float d[16], d_next[16];
+      auto upstream = [&](int j) {  // dh of the feature, 16 tokens ahead of their use
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+          d_next[i] = on && j + i < p.rows ? __bfloat162float(p.dh[(long long)(j + i) * p.F + f]) : 0.f;
+      };
+      if (p.dh) upstream(0);
+      const bool got = wait(&tfull[acc.s], acc.ph, kSite + __LINE__);
+      if (!__all_sync(0xffffffffu, got)) break;
+      tc_fence_after();
 #pragma unroll 1
       for (int j = 0; j < NT && j < p.rows; j += 16) {
         uint32_t g[16], u[16];
         tmem_ld_32x32b_x16(ta + j, g);
         tmem_ld_32x32b_x16(ta + NT + j, u);
+        if (p.dh) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) d[i] = d_next[i];
+          upstream(j + 16);
+        }
         tmem_ld_wait();
         if (!on) continue;
 #pragma unroll
@@ -692,10 +747,15 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           if (j + i >= p.rows) break;
           const float gv = __uint_as_float(g[i]), uv = __uint_as_float(u[i]);
           if (p.h) p.h[(long long)(j + i) * p.F + f] = __float2bfloat16_rn(gated<false>(gv, uv, p.act));
-          if (p.z) {
-            __nv_bfloat16* z = p.z + (long long)(j + i) * 2 * p.F + f;
-            z[0] = __float2bfloat16_rn(gv);
-            z[p.F] = __float2bfloat16_rn(uv);
+          if (!p.z) continue;
+          const long long at = (long long)(j + i) * p.z_pitch + f;
+          const float2 o = p.dh ? gated_grad<false>(gv, uv, d[i], p.act) : make_float2(gv, uv);
+          const __nv_bfloat16 a = __float2bfloat16_rn(o.x), b = __float2bfloat16_rn(o.y);
+          p.z[at] = a;
+          p.z[at + p.F] = b;
+          if (p.dh) {
+            p.z2[at] = __float2bfloat16_rn(o.x - __bfloat162float(a));
+            p.z2[at + p.F] = __float2bfloat16_rn(o.y - __bfloat162float(b));
           }
         }
       }
@@ -802,9 +862,9 @@ poetx_status score(const CUtensorMap& mg, const CUtensorMap& mu, const CUtensorM
   return POETX_OK;
 }
 
-template <int SEGS>
+template <int SEGS, bool DZ>
 poetx_status gemm(const FfnMaps& m, FfnGemm& p, cudaStream_t s) {
-  auto k = ffn_gemm_kernel<SEGS>;
+  auto k = ffn_gemm_kernel<SEGS, DZ>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   static int max_pairs = 0;  // co-resident CTA pairs
@@ -847,15 +907,25 @@ bool tiles_ok(int N, int F) {
 // Bytes between the three pieces of an fp32 array of `count` values.
 size_t piece_step(size_t count) { return align_up(count * 2, 1024); }
 
-// h and / or z (each nullable) of the projections; xp, wp: x and W, or their fp32 pieces.
+// What a projection leaves: h and / or z (each nullable), or with dh (bf16) dz in rows of `pitch` elements,
+// in two pieces (z2) for few rows.
+struct Outputs {
+  void *h, *z;
+  const void* dh;
+  void* z2;
+  long long pitch;  // of z
+};
+bool few_rows(int N, int D) { return N <= kScoreRows && D <= kScoreMaxD; }
+
+// xp, wp: x and W, or their fp32 pieces.
 poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, const uint8_t* wp, int F,
-                     void* h, void* z, cudaStream_t s) {
+                     const Outputs& o, cudaStream_t s) {
   const bool f32 = dt == POETX_F32;
   const size_t half = (size_t)F * D * 2;  // bytes of W's gate rows in bf16
   auto bf16_map = [&](CUtensorMap* m, const void* p, long long outer, int bi, int bo) {
     return encode_tma_2d(m, p, TMA_BF16, D, outer, D, bi, bo, true);
   };
-  if (!f32 && N <= kScoreRows && D <= kScoreMaxD) {
+  if (!f32 && few_rows(N, D)) {
     FfnScore p{};
     const int sms = sm_count(), each = ceil_div(F, (long long)sms * BM);
     const int height = ceil_div(F, (long long)sms * each);
@@ -863,8 +933,11 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
     p.tiles = ceil_div(F, p.height);
     p.F = F;
     p.rows = N;
-    p.h = static_cast<__nv_bfloat16*>(h);
-    p.z = static_cast<__nv_bfloat16*>(z);
+    p.h = static_cast<__nv_bfloat16*>(o.h);
+    p.z = static_cast<__nv_bfloat16*>(o.z);
+    p.dh = static_cast<const __nv_bfloat16*>(o.dh);
+    p.z2 = static_cast<__nv_bfloat16*>(o.z2);
+    p.z_pitch = o.pitch;
     p.act = act;
     const int nt = N <= 16 ? 16 : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
     // one box per stage and operand over several K blocks where D is a multiple of 64 (one thread issues
@@ -901,10 +974,11 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
   const int bi = f32 ? 32 : 64;
   const size_t esz = dtype_size(dt);
   m.h = m.zg = m.zu = m.a[0];
+  const void* h = o.dh ? o.dh : o.h;
   if (h && !encode_tma_2d(&m.h, h, et, F, N, F, bi, 32, true)) return POETX_ERR_CUDA;
-  if (z && (!encode_tma_2d(&m.zg, z, et, F, N, 2 * (uint64_t)F, bi, 32, true) ||
-            !encode_tma_2d(&m.zu, static_cast<uint8_t*>(z) + (size_t)F * esz, et, F, N, 2 * (uint64_t)F, bi,
-                           32, true)))
+  if (o.z && (!encode_tma_2d(&m.zg, o.z, et, F, N, o.pitch, bi, 32, true) ||
+              !encode_tma_2d(&m.zu, static_cast<uint8_t*>(o.z) + (size_t)F * esz, et, F, N, o.pitch, bi, 32,
+                             true)))
     return POETX_ERR_CUDA;
   p.tiles_m = ceil_div(N, 2 * BM);
   p.tiles_f = ceil_div(F, BF);
@@ -913,16 +987,17 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
   p.chunk = f32 ? 4 : 64;
   p.M = N;
   p.F = F;
-  p.store_h = h != nullptr;
-  p.store_z = z != nullptr;
+  p.store_h = o.h != nullptr;
+  p.store_z = o.z != nullptr;
   p.act = act;
-  if (f32) return gemm<kSegs>(m, p, s);
-  return gemm<1>(m, p, s);
+  if (f32) return gemm<kSegs, false>(m, p, s);
+  return o.dh ? gemm<1, true>(m, p, s) : gemm<1, false>(m, p, s);
 }
 
 // The backward's workspace.
 struct Plan {
   bool f32, fine;
+  bool direct;      // dz from the projections' sums (else from z, kept or written to the workspace)
   long long pitch;  // of dz: 2 F up to a multiple of 64
   int splits;
   size_t xs, ws, z, dz, z_step, dxp, bytes;
@@ -942,7 +1017,9 @@ Plan plan(poetx_dtype dt, int N, int D, int F, bool have_z, bool dx) {
   };
   o.xs = o.f32 ? take(3 * piece_step(n * D)) : 0;
   o.ws = o.f32 ? take(3 * piece_step((size_t)2 * F * D)) : 0;
-  o.z = have_z ? 0 : take(n * 2 * F * dtype_size(dt));
+  // (128 rows or fewer of a D beyond the few-row kernel's go by z: dz is then in two pieces)
+  o.direct = !have_z && !o.f32 && (!o.fine || few_rows(N, D));
+  o.z = have_z || o.direct ? 0 : take(n * 2 * F * dtype_size(dt));
   o.z_step = align_up(n * o.pitch * 2, 1024);
   o.dz = take((o.f32 ? 3 : (o.fine ? 2 : 1)) * o.z_step);
   o.dxp = dx && (o.splits > 1 || o.fine) ? take((size_t)o.splits * align_up(n, 256) * D * 4) : 0;
@@ -1018,7 +1095,7 @@ extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, cons
     xp = w;
     wp = w + 3 * x_step;
   }
-  return project(dt, act_of(act), xp, N, D, wp, F, h, z, stream);
+  return project(dt, act_of(act), xp, N, D, wp, F, Outputs{h, z, nullptr, nullptr, 2ll * F}, stream);
 }
 
 extern "C" size_t poetx_ffn_bwd_workspace_bytes(poetx_dtype dt, int N, int D, int F, int have_z,
@@ -1054,19 +1131,26 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
     xp = w + pl.xs;
     wp = w + pl.ws;
   }
-  if (!z) {
-    POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F, nullptr, w + pl.z, stream));
-    z = w + pl.z;
-  }
-  // dz: the gate's half, then the value's, in one to three bf16 pieces
   const int pieces = pl.f32 ? 3 : (pl.fine ? 2 : 1);
-  GluCall c{dt, act_of(act), z, static_cast<const uint8_t*>(z) + (size_t)F * esz, dh, N, F, 2ll * F,
-            pl.pitch, {}, pieces == 1 ? 0 : pieces};
-  for (int i = 0; i < pieces; ++i) {
-    c.out[2 * i] = w + pl.dz + i * pl.z_step;
-    c.out[2 * i + 1] = w + pl.dz + i * pl.z_step + (size_t)F * 2;
+  if (pl.direct) {
+    POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
+                      Outputs{nullptr, w + pl.dz, dh, pl.fine ? w + pl.dz + pl.z_step : nullptr, pl.pitch},
+                      stream));
+  } else {
+    if (!z) {
+      z = w + pl.z;
+      POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
+                        Outputs{nullptr, w + pl.z, nullptr, nullptr, 2ll * F}, stream));
+    }
+    // dz: the gate's half, then the value's, in one to three bf16 pieces
+    GluCall c{dt, act_of(act), z, static_cast<const uint8_t*>(z) + (size_t)F * esz, dh, N, F, 2ll * F,
+              pl.pitch, {}, pieces == 1 ? 0 : pieces};
+    for (int i = 0; i < pieces; ++i) {
+      c.out[2 * i] = w + pl.dz + i * pl.z_step;
+      c.out[2 * i + 1] = w + pl.dz + i * pl.z_step + (size_t)F * 2;
+    }
+    POETX_TRY(run_glu(c, stream));
   }
-  POETX_TRY(run_glu(c, stream));
   if (pl.pitch > 2ll * F) {
     const long long n = (long long)N * ((pl.pitch - 2 * F) / 8);
     POETX_CUDA_TRY(launch_pdl(ffn_pad_kernel, dim3(grid_for(n, 256)), dim3(256), 0, stream,

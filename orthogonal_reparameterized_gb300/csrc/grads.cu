@@ -230,9 +230,9 @@ __global__ void __launch_bounds__(kThreads)
   const int chunks = t.start[t.n];
   const int c0 = (int)((long long)chunks * blockIdx.x / gridDim.x);
   const int c1 = (int)((long long)chunks * (blockIdx.x + 1) / gridDim.x);
-  int k = c0 < c1 ? find_tensor(t.start, t.n, c0) : 0;
-  for (int c = c0; c < c1; ++c) {
-    while (c >= t.start[k + 1]) ++k;
+  int k = c0 < c1 ? find_tensor(t.start, t.n, c1 - 1) : 0;
+  for (int c = c1 - 1; c >= c0; --c) {  // (backwards: the norm has left each CTA's last chunks in L2)
+    while (c < t.start[k]) --k;
     const long long e0 = (long long)(c - t.start[k]) * (kChunkBytes / 4);
     const int n = (int)min((long long)(kChunkBytes / 4), t.count[k] - e0);
     const float* g = static_cast<const float*>(t.p[0][k]) + e0;

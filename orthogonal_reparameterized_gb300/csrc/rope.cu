@@ -9,7 +9,10 @@
 // Bound by HBM: every element is read once and written once.  A group of G lanes (a power of two) holds
 // one head: lane c its c-th chunk, CH pairs in two vectors of CH elements, so that both elements of a
 // pair, their angle and their gamma are in one lane's registers whatever the pairing.  All heads of a token
-// use the same angles: a lane makes those of its CH pairs once per token and keeps them over the heads.
+// use the same angles: a lane makes those of its CH pairs once per token and keeps them over the heads,
+// multiplied by gamma where that saves instructions.  What is in flight waits in shared memory: each
+// thread copies the chunks of its own next heads there asynchronously (256 bytes ahead) and is the only one
+// to read them, so that no barrier is needed.
 //
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
 // turn), pos * f modulo 2^64 is the angle modulo a turn, exact to 2^-32 turns at any int32 position (an
@@ -25,7 +28,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = 256;   // pairs of a head
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 3;   // at most
+constexpr int kAhead = 256;     // bytes of input that a thread has in flight
 constexpr int kMaxAxes = 8;
 
 struct Side {
@@ -51,78 +55,134 @@ struct RopeArgs {
   float eps;
 };
 
-template <int CH>
-__device__ __forceinline__ void widen(const uint32_t (&r)[CH / 2], float* v, __nv_bfloat16) {
-#pragma unroll
-  for (int i = 0; i < CH / 2; ++i) {
-    v[2 * i] = __uint_as_float(r[i] << 16);
-    v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
-  }
+template <int B>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
+  if constexpr (B == 8)
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
+  else
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
-template <int CH>
-__device__ __forceinline__ void widen(const uint32_t (&r)[CH], float* v, float) {
-#pragma unroll
-  for (int i = 0; i < CH; ++i) v[i] = __uint_as_float(r[i]);
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// One chunk as it lies in memory: two vectors of CH elements.
-template <typename T, int CH>
+// A lane's chunk of one head in one array: CH first and CH second elements of its pairs.
+template <typename T, int CH, bool INTER>
 struct Chunk {
-  static constexpr int WORDS = CH * (int)sizeof(T) / 4;
-  uint32_t r[2][WORDS];
-  __device__ __forceinline__ void load(const T* p, int o0, int o1) {
+  static constexpr int BYTES = 2 * CH * (int)sizeof(T);
+  static constexpr int UNIT = BYTES / 2 < 16 ? BYTES / 2 : 16;  // bytes of one copy
+  static constexpr int UNITS = BYTES / UNIT, WORDS = BYTES / 4;
+  // slot: the chunk's first unit of this thread; units are kThreads * UNIT apart (no bank conflicts)
+  static __device__ __forceinline__ void fetch(uint32_t slot, const T* head, int o0, int o1) {
 #pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      const T* q = p + (k ? o1 : o0);
-      if constexpr (WORDS == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(q);
-        r[k][0] = w.x;
-        r[k][1] = w.y;
+    for (int k = 0; k < UNITS; ++k) {
+      const char* half = reinterpret_cast<const char*>(head + (k < UNITS / 2 ? o0 : o1));
+      copy_async<UNIT>(slot + k * kThreads * UNIT, half + (k % (UNITS / 2)) * UNIT);
+    }
+  }
+  static __device__ __forceinline__ void read(const char* slot, uint32_t (&r)[WORDS]) {
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+      const char* at = slot + k * kThreads * UNIT;
+      if constexpr (UNIT == 8) {
+        const uint2 w = *reinterpret_cast<const uint2*>(at);
+        r[2 * k] = w.x;
+        r[2 * k + 1] = w.y;
       } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 4) {
-          const uint4 w = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint32_t*>(q) + i);
-          r[k][i] = w.x;
-          r[k][i + 1] = w.y;
-          r[k][i + 2] = w.z;
-          r[k][i + 3] = w.w;
-        }
+        const uint4 w = *reinterpret_cast<const uint4*>(at);
+        r[4 * k] = w.x;
+        r[4 * k + 1] = w.y;
+        r[4 * k + 2] = w.z;
+        r[4 * k + 3] = w.w;
       }
     }
   }
-  __device__ __forceinline__ void get(float (&v)[2 * CH]) const {
-    widen<CH>(r[0], v, T());
-    widen<CH>(r[1], v + CH, T());
-  }
-  __device__ __forceinline__ void put(const float (&v)[2 * CH]) {
+  // words as they lie in memory <-> the pairs' first and second elements, two by two
+  static __device__ __forceinline__ void split(const uint32_t (&r)[WORDS], float2 (&a)[CH / 2],
+                                               float2 (&b)[CH / 2]) {
+    float v[2 * CH];
 #pragma unroll
-    for (int k = 0; k < 2; ++k)
-#pragma unroll
-      for (int i = 0; i < WORDS; ++i)
-        r[k][i] = sizeof(T) == 2 ? pack_bf16x2(v[k * CH + 2 * i], v[k * CH + 2 * i + 1])
-                                 : __float_as_uint(v[k * CH + i]);
-  }
-  __device__ __forceinline__ void store(T* p, int o0, int o1) const {
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      T* q = p + (k ? o1 : o0);
-      if constexpr (WORDS == 2) {
-        *reinterpret_cast<uint2*>(q) = make_uint2(r[k][0], r[k][1]);
+    for (int i = 0; i < WORDS; ++i) {
+      if constexpr (sizeof(T) == 2) {
+        v[2 * i] = __uint_as_float(r[i] << 16);
+        v[2 * i + 1] = __uint_as_float(r[i] & 0xffff0000u);
       } else {
-#pragma unroll
-        for (int i = 0; i < WORDS; i += 4)
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint32_t*>(q) + i) =
-              make_uint4(r[k][i], r[k][i + 1], r[k][i + 2], r[k][i + 3]);
+        v[i] = __uint_as_float(r[i]);
       }
     }
+#pragma unroll
+    for (int j = 0; j < CH / 2; ++j) {
+      a[j] = INTER ? make_float2(v[4 * j], v[4 * j + 2]) : make_float2(v[2 * j], v[2 * j + 1]);
+      b[j] = INTER ? make_float2(v[4 * j + 1], v[4 * j + 3])
+                   : make_float2(v[CH + 2 * j], v[CH + 2 * j + 1]);
+    }
+  }
+  static __device__ __forceinline__ void store(T* head, int o0, int o1, const float2 (&a)[CH / 2],
+                                               const float2 (&b)[CH / 2]) {
+    float v[2 * CH];
+#pragma unroll
+    for (int j = 0; j < CH / 2; ++j) {
+      v[INTER ? 4 * j : 2 * j] = a[j].x;
+      v[INTER ? 4 * j + 2 : 2 * j + 1] = a[j].y;
+      v[INTER ? 4 * j + 1 : CH + 2 * j] = b[j].x;
+      v[INTER ? 4 * j + 3 : CH + 2 * j + 1] = b[j].y;
+    }
+    uint32_t r[WORDS];
+#pragma unroll
+    for (int i = 0; i < WORDS; ++i)
+      r[i] = sizeof(T) == 2 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
+#pragma unroll
+    for (int k = 0; k < UNITS; ++k) {
+      char* at = reinterpret_cast<char*>(head + (k < UNITS / 2 ? o0 : o1)) + (k % (UNITS / 2)) * UNIT;
+      if constexpr (UNIT == 8)
+        *reinterpret_cast<uint2*>(at) = make_uint2(r[2 * k], r[2 * k + 1]);
+      else
+        *reinterpret_cast<uint4*>(at) = make_uint4(r[4 * k], r[4 * k + 1], r[4 * k + 2], r[4 * k + 3]);
+    }
+  }
+};
+template <typename T, int CH, bool NORM, bool BWD>
+constexpr int slot_bytes() {  // a thread's bytes of one head
+  return (NORM && BWD ? 2 : 1) * 2 * CH * (int)sizeof(T);
+}
+template <typename T, int CH, bool NORM, bool BWD>
+constexpr int slots() {
+  return kAhead / slot_bytes<T, CH, NORM, BWD>();
+}
+
+// Where a warp is in its tasks: a token and the first of the group of 32 / G heads that are next.
+struct Cursor {
+  long long task;
+  int token, h0, h_end;
+  __device__ __forceinline__ void begin(const Side& s) {
+    if (task >= s.tasks) return;
+    token = s.parts == 1 ? (int)task : (int)(task / s.parts);
+    const int part = s.parts == 1 ? 0 : (int)(task - (long long)token * s.parts);
+    h0 = part * s.hs;
+    h_end = min(s.H, h0 + s.hs);
+  }
+  __device__ __forceinline__ bool next(const Side& s, int HW, long long step) {  // true: another token
+    h0 += HW;
+    if (h0 < h_end) return false;
+    task += step;
+    begin(s);
+    return true;
   }
 };
 
 template <typename T, int CH, bool INTER, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid_constant__ RopeArgs a) {
+__global__ void __launch_bounds__(kThreads, BWD && NORM ? 2 : 3)
+    rope_kernel(const __grid_constant__ RopeArgs a) {
+  using C = Chunk<T, CH, INTER>;
+  constexpr int SLOTS = slots<T, CH, NORM, BWD>(), SLOT = slot_bytes<T, CH, NORM, BWD>() * kThreads;
+  constexpr bool BOTH = BWD && NORM;  // both x and dy are read
+  constexpr int N2 = CH / 2;
+  extern __shared__ __align__(16) char ring[];   // [slot][array][unit][thread]
   __shared__ unsigned long long turn[kMaxHalf];  // inv_freq / 2 pi, in 2^-64 turns
   __shared__ int ax[kMaxHalf];                   // the pair's axis, -1: NaN
-  __shared__ float red[BWD && NORM ? kWarps * 2 * CH * 32 : 1];
+  __shared__ float gsm[NORM ? 2 * kMaxHalf : 1];
   pdl_trigger();
   pdl_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
@@ -134,7 +194,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid
     turn[t] = w < 1.0 ? (unsigned long long)(w * 18446744073709551616.0) : 0ull;
     ax[t] = isfinite(f) && axis >= 0 && axis < a.axes ? axis : -1;
   }
-  __syncthreads();
   const int which = (int)blockIdx.x >= a.s[0].ctas;
   const Side& s = a.s[which];
   const int cta = (int)blockIdx.x - (which ? a.s[0].ctas : 0);
@@ -144,108 +203,200 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid
   const int tail = 2 * a.half + 2 * CH * (c - pr);
   const int o0 = rot ? (INTER ? 2 * CH * c : CH * c) : tail;
   const int o1 = rot && !INTER ? a.half + CH * c : o0 + CH;
-  float gm[2 * CH], dg[2 * CH];
-#pragma unroll
-  for (int i = 0; i < 2 * CH; ++i) {
-    gm[i] = NORM && mine && s.gamma ? s.gamma[(i < CH ? o0 : o1 - CH) + i] : 1.f;
-    dg[i] = 0.f;
-  }
-  const float inv_dh = 1.f / (float)a.dh;
   const T* const x = static_cast<const T*>(s.x);
   const T* const dy = static_cast<const T*>(s.dy);
   T* const y = static_cast<T*>(s.y);
+  const uint32_t ring_at = smem_u32(ring) + t * C::UNIT;
+  const char* const my_ring = ring + t * C::UNIT;
+  constexpr int SECOND = C::BYTES * kThreads;  // dy's chunk behind x's
 
-  for (long long task = (long long)cta * kWarps + warp; task < s.tasks;
-       task += (long long)s.ctas * kWarps) {
-    const int token = s.parts == 1 ? (int)task : (int)(task / s.parts);
-    const int part = s.parts == 1 ? 0 : (int)(task - (long long)token * s.parts);
-    float cs[CH], sn[CH];
-    if (rot) {
-#pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        const int k = ax[CH * c + j];
-        const int p = k < 0 ? 0 : a.pos[(long long)k * a.N + token];
-        const unsigned long long ang = (unsigned long long)(long long)p * turn[CH * c + j];
-        const float h = (float)(int)(ang >> 32) * 0x1p-32f;  // turns, in [-1/2, 1/2]
-        // bf16: the hardware's sine and cosine, within 2^-21 on (-pi, pi), far below the result's
-        // rounding
-        if (sizeof(T) == 2) __sincosf(h * 6.28318530717958647692f, &sn[j], &cs[j]);
-        else sincospif(2.f * h, &sn[j], &cs[j]);
-        if (k < 0) cs[j] = sn[j] = __int_as_float(0x7fc00000);
+  const long long step = (long long)s.ctas * kWarps;
+  Cursor at{(long long)cta * kWarps + warp, 0, 0, 0}, ahead = at;
+  at.begin(s);
+  ahead.begin(s);
+  auto fetch = [&](int slot) {
+    if (ahead.task < s.tasks) {
+      const int h = ahead.h0 + sub;
+      if (mine && h < ahead.h_end) {
+        const uint32_t to = ring_at + slot * SLOT;
+        if (!BWD || NORM)
+          C::fetch(to, x + (long long)ahead.token * s.xp + (long long)h * a.dh, o0, o1);
+        if (BWD)
+          C::fetch(to + (BOTH ? SECOND : 0), dy + (long long)ahead.token * s.dyp + (long long)h * a.dh, o0,
+                   o1);
       }
+      ahead.next(s, HW, step);
     }
-    const int h_end = min(s.H, (part + 1) * s.hs);
-    constexpr int U = BWD && NORM ? 2 : 4;  // heads in flight per group
-    for (int h0 = part * s.hs; h0 < h_end; h0 += U * HW) {
-      Chunk<T, CH> rx[U], ry[U];
+    copy_commit();
+  };
+#pragma unroll 1
+  for (int i = 0; i < SLOTS; ++i) fetch(i);
+  if (NORM)
+    for (int i = t; i < a.dh; i += kThreads) gsm[i] = s.gamma ? s.gamma[i] : 1.f;
+  const float inv_dh = 1.f / (float)a.dh;
+  __syncthreads();
+  // gamma of the pairs' first and second elements (the forward reads it once per token)
+  auto gamma2 = [&](int j, float2& p, float2& q) {
+    p = q = both(1.f);
+    if (!NORM || !mine) return;
+    const int i = INTER ? 4 * j : 2 * j, d = INTER ? 2 : 1;
+    p = make_float2(gsm[o0 + i], gsm[o0 + i + d]);
+    q = INTER ? make_float2(gsm[o0 + i + 1], gsm[o0 + i + 3]) : make_float2(gsm[o1 + i], gsm[o1 + i + 1]);
+  };
+  float2 ga[N2], gb[N2], dga[N2], dgb[N2];
+  if (BOTH) {
 #pragma unroll
-      for (int k = 0; k < U; ++k) {
-        const int h = h0 + k * HW + sub;
-        if (mine && h < h_end) {
-          if (!BWD || NORM) rx[k].load(x + (long long)token * s.xp + (long long)h * a.dh, o0, o1);
-          if (BWD) ry[k].load(dy + (long long)token * s.dyp + (long long)h * a.dh, o0, o1);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < U; ++k) {
-        if (h0 + k * HW >= h_end) break;  // (the same for the whole warp)
-        const int h = h0 + k * HW + sub;
-        const bool on = mine && h < h_end;
-        float v[2 * CH], d[2 * CH];
-#pragma unroll
-        for (int i = 0; i < 2 * CH; ++i) v[i] = d[i] = 0.f;
-        if (on) {
-          if (!BWD || NORM) rx[k].get(v);
-          if (BWD) ry[k].get(d);
-        }
-        auto rotate = [&](float (&w)[2 * CH], float sign) {
-          if (!rot) return;
-#pragma unroll
-          for (int j = 0; j < CH; ++j) {
-            const int i0 = INTER ? 2 * j : j, i1 = INTER ? 2 * j + 1 : CH + j;
-            const float p = w[i0], q = w[i1], si = sign * sn[j];
-            w[i0] = p * cs[j] - q * si;
-            w[i1] = p * si + q * cs[j];
-          }
-        };
-        if (BWD) rotate(d, -1.f);
-        float ss = 0.f, su = 0.f;
-        if (NORM) {
-#pragma unroll
-          for (int i = 0; i < 2 * CH; ++i) {
-            ss = fmaf(v[i], v[i], ss);
-            if (BWD) su = fmaf(d[i] * gm[i], v[i], su);
-          }
-          for (int o = G / 2; o; o >>= 1) {
-            ss += __shfl_xor_sync(0xffffffffu, ss, o);
-            if (BWD) su += __shfl_xor_sync(0xffffffffu, su, o);
-          }
-          const float rstd = 1.f / sqrtf(ss * inv_dh + a.eps);
-          if (!BWD) {
-#pragma unroll
-            for (int i = 0; i < 2 * CH; ++i) v[i] = v[i] * rstd * gm[i];
-          } else {
-            const float m = su * rstd * inv_dh;
-#pragma unroll
-            for (int i = 0; i < 2 * CH; ++i) {
-              const float hh = v[i] * rstd;
-              if (on) dg[i] = fmaf(d[i], hh, dg[i]);
-              d[i] = rstd * (d[i] * gm[i] - hh * m);
-            }
-          }
-        }
-        if (!BWD) rotate(v, 1.f);
-        if (on) {
-          Chunk<T, CH> o;
-          o.put(BWD ? d : v);
-          o.store(y + (long long)token * s.yp + (long long)h * a.dh, o0, o1);
-        }
-      }
+    for (int j = 0; j < N2; ++j) {
+      gamma2(j, ga[j], gb[j]);
+      dga[j] = dgb[j] = both(0.f);
     }
   }
-  if (BWD && NORM && s.part) {  // the CTA's sums of dgamma, in the order of warps and lanes
+  float2 cs[N2], sn[N2];  // of the token's angles
+  // forward with the norm: gamma_a cos, -gamma_b sin, gamma_a sin, gamma_b cos
+  float2 fa[N2], fb[N2], fc[N2], fd[N2];
+  bool fresh = true;
+  int slot = 0;
+#pragma unroll 1
+  while (at.task < s.tasks) {
+    if (fresh) {
+      float cv[CH], sv[CH];
 #pragma unroll
-    for (int i = 0; i < 2 * CH; ++i) red[(warp * 2 * CH + i) * 32 + lane] = dg[i];
+      for (int j = 0; j < CH; ++j) {
+        cv[j] = 1.f;
+        sv[j] = 0.f;
+        if (rot) {
+          const int k = ax[CH * c + j];
+          const int p = k < 0 ? 0 : a.pos[(long long)k * a.N + at.token];
+          const unsigned long long ang = (unsigned long long)(long long)p * turn[CH * c + j];
+          const float h = (float)(int)(ang >> 32) * 0x1p-32f;  // turns, in [-1/2, 1/2]
+          // bf16: the hardware's sine and cosine, within 2^-21 on (-pi, pi), far below the result's
+          // rounding
+          if (sizeof(T) == 2) __sincosf(h * 6.28318530717958647692f, &sv[j], &cv[j]);
+          else sincospif(2.f * h, &sv[j], &cv[j]);
+          if (k < 0) cv[j] = sv[j] = __int_as_float(0x7fc00000);
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < N2; ++j) {
+        cs[j] = make_float2(cv[2 * j], cv[2 * j + 1]);
+        sn[j] = make_float2(sv[2 * j], sv[2 * j + 1]);
+        if (NORM && !BWD) {
+          float2 p, q;
+          gamma2(j, p, q);
+          fa[j] = mul2(p, cs[j]);
+          fb[j] = mul2(q, make_float2(-sn[j].x, -sn[j].y));
+          fc[j] = mul2(p, sn[j]);
+          fd[j] = mul2(q, cs[j]);
+        }
+      }
+    }
+    const int h = at.h0 + sub;
+    const bool on = mine && h < at.h_end;
+    copy_wait<SLOTS - 1>();
+    uint32_t rx[C::WORDS], ry[C::WORDS];
+#pragma unroll
+    for (int i = 0; i < C::WORDS; ++i) rx[i] = ry[i] = 0u;
+    if (on) {
+      C::read(my_ring + slot * SLOT, rx);
+      if (BOTH) C::read(my_ring + slot * SLOT + SECOND, ry);
+    }
+    float2 xa[N2], xb[N2];  // x (backward without the norm: dy)
+    C::split(rx, xa, xb);
+    const long long token = at.token;
+    if constexpr (!BWD) {
+      float rstd = 1.f;
+      if (NORM) {
+        float2 sq = both(0.f);
+#pragma unroll
+        for (int j = 0; j < N2; ++j) sq = fma2(xb[j], xb[j], fma2(xa[j], xa[j], sq));
+        float ss = sq.x + sq.y;
+        for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        rstd = rsqrtf(ss * inv_dh + a.eps);
+      }
+      fetch(slot);
+      float2 ya[N2], yb[N2];
+#pragma unroll
+      for (int j = 0; j < N2; ++j) {
+        if (NORM) {
+          if (rot) {
+            ya[j] = mul2(fma2(xb[j], fb[j], mul2(xa[j], fa[j])), both(rstd));
+            yb[j] = mul2(fma2(xb[j], fd[j], mul2(xa[j], fc[j])), both(rstd));
+          } else {  // (no product with a zero sine: the partner may be infinite)
+            ya[j] = mul2(mul2(xa[j], fa[j]), both(rstd));
+            yb[j] = mul2(mul2(xb[j], fd[j]), both(rstd));
+          }
+        } else {
+          if (rot) {
+            ya[j] = fma2(xb[j], make_float2(-sn[j].x, -sn[j].y), mul2(xa[j], cs[j]));
+            yb[j] = fma2(xb[j], cs[j], mul2(xa[j], sn[j]));
+          } else {
+            ya[j] = xa[j];
+            yb[j] = xb[j];
+          }
+        }
+      }
+      if (on) C::store(y + token * s.yp + (long long)h * a.dh, o0, o1, ya, yb);
+    } else {
+      float2 da[N2], db[N2];  // the gradient of the rotated head, then of the normalised one
+      if constexpr (BOTH) {
+        C::split(ry, da, db);
+      } else {
+#pragma unroll
+        for (int j = 0; j < N2; ++j) {
+          da[j] = xa[j];
+          db[j] = xb[j];
+        }
+      }
+      fetch(slot);
+      if (rot) {
+#pragma unroll
+        for (int j = 0; j < N2; ++j) {
+          const float2 p = da[j], q = db[j];
+          da[j] = fma2(q, sn[j], mul2(p, cs[j]));
+          db[j] = fma2(q, cs[j], mul2(p, make_float2(-sn[j].x, -sn[j].y)));
+        }
+      }
+      if constexpr (NORM) {
+        float2 sq = both(0.f), sd = both(0.f);
+#pragma unroll
+        for (int j = 0; j < N2; ++j) {
+          sq = fma2(xb[j], xb[j], fma2(xa[j], xa[j], sq));
+          sd = fma2(mul2(db[j], gb[j]), xb[j], fma2(mul2(da[j], ga[j]), xa[j], sd));
+        }
+        float ss = sq.x + sq.y, su = sd.x + sd.y;
+        for (int o = G / 2; o; o >>= 1) {
+          ss += __shfl_xor_sync(0xffffffffu, ss, o);
+          su += __shfl_xor_sync(0xffffffffu, su, o);
+        }
+        const float rstd = rsqrtf(ss * inv_dh + a.eps);
+        const float m = -su * rstd * inv_dh;
+        if (on) {
+#pragma unroll
+          for (int j = 0; j < N2; ++j) {
+            const float2 ha = mul2(xa[j], both(rstd)), hb = mul2(xb[j], both(rstd));
+            dga[j] = fma2(da[j], ha, dga[j]);
+            dgb[j] = fma2(db[j], hb, dgb[j]);
+            da[j] = mul2(fma2(ha, both(m), mul2(da[j], ga[j])), both(rstd));
+            db[j] = mul2(fma2(hb, both(m), mul2(db[j], gb[j])), both(rstd));
+          }
+        }
+      }
+      if (on) C::store(y + token * s.yp + (long long)h * a.dh, o0, o1, da, db);
+    }
+    if (++slot == SLOTS) slot = 0;
+    fresh = at.next(s, HW, step);
+  }
+  if (BOTH && s.part) {  // the CTA's sums of dgamma, in the order of warps and lanes
+    copy_wait<0>();
+    __syncthreads();
+    float* red = reinterpret_cast<float*>(ring);  // [warp][element of the chunk][lane]
+#pragma unroll
+    for (int j = 0; j < N2; ++j) {
+      const float v[4] = {dga[j].x, dga[j].y, dgb[j].x, dgb[j].y};
+#pragma unroll
+      for (int k = 0; k < 4; ++k)
+        red[(warp * 2 * CH + (k < 2 ? 2 * j + k : CH + 2 * j + k - 2)) * 32 + lane] = v[k];
+    }
     __syncthreads();
     for (int e = t; e < 2 * CH * G; e += kThreads) {
       const int i = e / G, cc = e - i * G;
@@ -254,10 +405,11 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) rope_kernel(const __grid
       for (int w = 0; w < kWarps; ++w)
         for (int l = cc; l < 32; l += G) sum += red[(w * 2 * CH + i) * 32 + l];
       const bool r = cc < pr;
-      const int tl = 2 * a.half + 2 * CH * (cc - pr);
-      const int b0 = r ? (INTER ? 2 * CH * cc : CH * cc) : tl;
+      const int b0 = r ? (INTER ? 2 * CH * cc : CH * cc) : 2 * a.half + 2 * CH * (cc - pr);
       const int b1 = r && !INTER ? a.half + CH * cc : b0 + CH;
-      s.part[(long long)cta * a.dh + (i < CH ? b0 + i : b1 + i - CH)] = sum;
+      const int j = i < CH ? i : i - CH;  // pair of the chunk
+      const int el = INTER ? b0 + 2 * j + (i >= CH) : (i < CH ? b0 : b1) + j;
+      s.part[(long long)cta * a.dh + el] = sum;
     }
   }
 }
@@ -297,14 +449,22 @@ bool rope_ok(const poetx_rope* r) {
   return r->head_dim <= (wide ? 512 : 256) && r->axes >= 1 && r->axes <= kMaxAxes;
 }
 
+template <typename T, int CH, bool INTER, bool NORM, bool BWD>
+cudaError_t rope_launch1(const RopeArgs& a, cudaStream_t s) {
+  auto k = rope_kernel<T, CH, INTER, NORM, BWD>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [&] {
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * kThreads);
+  });
+  if (attr != cudaSuccess) return attr;
+  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), kAhead * kThreads, s, a);
+}
 template <typename T, int CH, bool BWD>
 cudaError_t rope_launch(const RopeArgs& a, bool inter, bool norm, cudaStream_t s) {
-  const dim3 grid(a.s[0].ctas + a.s[1].ctas), block(kThreads);
   if (inter)
-    return norm ? launch_pdl(rope_kernel<T, CH, true, true, BWD>, grid, block, 0, s, a)
-                : launch_pdl(rope_kernel<T, CH, true, false, BWD>, grid, block, 0, s, a);
-  return norm ? launch_pdl(rope_kernel<T, CH, false, true, BWD>, grid, block, 0, s, a)
-              : launch_pdl(rope_kernel<T, CH, false, false, BWD>, grid, block, 0, s, a);
+    return norm ? rope_launch1<T, CH, true, true, BWD>(a, s) : rope_launch1<T, CH, true, false, BWD>(a, s);
+  return norm ? rope_launch1<T, CH, false, true, BWD>(a, s) : rope_launch1<T, CH, false, false, BWD>(a, s);
 }
 
 // A side's tasks: whole tokens where they give every warp some, else a token's heads in parts.
@@ -369,7 +529,7 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
   a.eps = r->eps;
   a.G = 1;
   while (a.G * 2 * CH < a.dh) a.G *= 2;
-  const int max_ctas = kCtasPerSm * sm_count();
+  const int max_ctas = (BWD && r->norm ? 2 : kCtasPerSm) * sm_count();
   const int heads = (q ? q->heads : 0) + (k ? k->heads : 0);
   float* part = static_cast<float*>(ws);
   RopeSum rs{};

@@ -10,6 +10,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from array import array
 from typing import Optional
 
 import torch
@@ -671,6 +672,8 @@ def _rows(fn: str, what: str, t, width: int):
     contiguous."""
     if not t.is_cuda:
         raise ValueError("poetx: tensors must live on a CUDA device")
+    if t.is_contiguous():
+        return t.data_ptr(), width
     at = width
     for size, stride in zip(t.shape[1:], t.stride()[1:]):
         at //= size if size else 1
@@ -767,12 +770,12 @@ def _rope(fn, x, pos, inv_freq, rot_dim, axis, interleaved, norm, eps):
     """The checked descriptor and (type, N) of a call on x [N, heads, head_dim]."""
     N, _, dh = x.shape
     rot = dh if rot_dim is None else rot_dim
-    pos2 = pos if pos.dim() == 2 else pos[None]
-    _want(fn, "pos", pos2, (pos2.shape[0], N), torch.int32)
+    axes = pos.shape[0] if pos.dim() == 2 else 1
+    _want(fn, "pos", pos, (axes, N) if pos.dim() == 2 else (N,), torch.int32)
     _want(fn, "inv_freq", inv_freq, (rot // 2,), torch.float32)
     _want(fn, "axis", axis, (rot // 2,), torch.int32)
     dt = _dtype(fn, x)
-    return dt, RopeDesc(dh, rot, int(bool(interleaved)), pos2.shape[0], int(bool(norm)), eps,
+    return dt, RopeDesc(dh, rot, int(bool(interleaved)), axes, int(bool(norm)), eps,
                         _addr(inv_freq), _addr(axis))
 
 
@@ -781,16 +784,17 @@ def _heads(fn, what, x, gamma, y, like, dt, dy=None, dgamma=None):
     if x is None:
         return None
     N, H, dh = x.shape
-    if (N, dh, x.dtype) != (like.shape[0], like.shape[2], like.dtype):
+    if x is not like and (N, dh, x.dtype) != (like.shape[0], like.shape[2], like.dtype):
         raise ValueError(f"{fn}: queries and keys must have the same tokens, head width and type")
-    for name, t in ((what, x), (f"the output for {what}", y), (f"d{what}", dy)):
-        if t is not None:
-            _want(fn, name, t, x.shape, x.dtype)
-    _want(fn, f"gamma_{what}", gamma, (dh,), torch.float32)
-    _want(fn, f"dgamma_{what}", dgamma, (dh,), torch.float32)
+    _want(fn, what + "'s output", y, x.shape, x.dtype)
+    _want(fn, "gamma_" + what, gamma, (dh,), torch.float32)
     px, pitch = _rows(fn, what, x, H * dh)
-    py, y_pitch = _rows(fn, f"the output for {what}", y, H * dh)
-    pd, d_pitch = (None, 0) if dy is None else _rows(fn, f"d{what}", dy, H * dh)
+    py, y_pitch = _rows(fn, what + "'s output", y, H * dh)
+    pd, d_pitch = None, 0
+    if dy is not None:
+        _want(fn, "d" + what, dy, x.shape, x.dtype)
+        _want(fn, "dgamma_" + what, dgamma, (dh,), torch.float32)
+        pd, d_pitch = _rows(fn, "d" + what, dy, H * dh)
     return HeadsDesc(H, px, pitch, _addr(gamma), pd, d_pitch, py, y_pitch, _addr(dgamma))
 
 
@@ -832,23 +836,29 @@ def poetx_qk_rope_bwd(q, k, dq, dk, pos, inv_freq, dq_in, dk_in, rot_dim=None, a
 
 
 # ---------------------------------------------------------------- many tensors
-def _arrays(fn, what, ts, dtypes):
-    """Pointers of the tensors as an array for the library."""
-    dev = torch.cuda.current_device()
-    for t in ts:
-        if t.dtype not in dtypes or not t.is_contiguous() or t.get_device() != dev:
-            raise ValueError(f"{fn}: {what} must be contiguous tensors of {dtypes} on the current "
-                             f"CUDA device, got {t.dtype} on {t.device}")
-    return (_vp * len(ts))(*[t.data_ptr() for t in ts])
+_GRAD_TYPES = {torch.float32, torch.bfloat16}
+_FP32 = {torch.float32}
 
 
-_GRAD_TYPES = (torch.float32, torch.bfloat16)
+def _arrays(fn, what, ts, dtypes, types):
+    """The tensors' addresses as an array for the library (maps: hundreds of tensors cost the host as
+    much as the kernels)."""
+    if not types.issuperset(dtypes) or not all(map(torch.Tensor.is_contiguous, ts)) or \
+            not {torch.cuda.current_device()}.issuperset(map(torch.Tensor.get_device, ts)):
+        raise ValueError(f"{fn}: {what} must be contiguous tensors on the current CUDA device, of "
+                         f"{' or '.join(map(str, types))}")
+    return array("Q", map(torch.Tensor.data_ptr, ts))
+
+
+def _at(a):
+    return a.buffer_info()[0]
 
 
 def _gradients(fn, grads):
-    p = _arrays(fn, "gradients", grads, _GRAD_TYPES)
-    n = len(grads)
-    return p, (_i * n)(*[_DT[t.dtype] for t in grads]), (_ll * n)(*[t.numel() for t in grads]), n
+    dtypes = [t.dtype for t in grads]
+    p = _arrays(fn, "gradients", grads, dtypes, _GRAD_TYPES)
+    return (p, array("i", map(_DT.__getitem__, dtypes)),
+            array("q", map(torch.Tensor.numel, grads)))
 
 
 def poetx_grad_norm_workspace_bytes(n: int) -> int:
@@ -861,11 +871,11 @@ def poetx_grad_norm(grads, norm, ws=None, stream=None):
     fn = "poetx_grad_norm"
     _want(fn, "norm", norm, (1,), torch.float32)
     pn = _addr(norm)
-    p, dts, counts, n = _gradients(fn, grads)
+    p, dts, counts = _gradients(fn, grads)
     handle = _raw_stream(stream, norm)
     if ws is None:
-        ws = _scratch(lib().poetx_grad_norm_workspace_bytes(n), norm, stream, handle)
-    st = lib().poetx_grad_norm(p, dts, counts, n, pn, _addr(ws), ws.numel(), handle)
+        ws = _scratch(lib().poetx_grad_norm_workspace_bytes(len(p)), norm, stream, handle)
+    st = lib().poetx_grad_norm(_at(p), _at(dts), _at(counts), len(p), pn, _addr(ws), ws.numel(), handle)
     if st:
         _check(fn, st)
 
@@ -876,8 +886,9 @@ def poetx_grad_clip(grads, norm, max_norm: float, stream=None):
     fn = "poetx_grad_clip"
     _want(fn, "norm", norm, (1,), torch.float32)
     pn = _addr(norm)
-    p, dts, counts, n = _gradients(fn, grads)
-    st = lib().poetx_grad_clip(p, dts, counts, n, max_norm, pn, _raw_stream(stream, norm))
+    p, dts, counts = _gradients(fn, grads)
+    st = lib().poetx_grad_clip(_at(p), _at(dts), _at(counts), len(p), max_norm, pn,
+                               _raw_stream(stream, norm))
     if st:
         _check(fn, st)
 
@@ -891,15 +902,15 @@ def poetx_adam_group(q, dq, m, v, step: int, lr: float, beta1: float = 0.9, beta
     n = len(q)
     if len(dq) != n or len(m) != n or len(v) != n:
         raise ValueError(f"{fn}: one dq, m and v per q")
-    count = [t.numel() for t in q]
-    for ts in (dq, m, v):
-        if [t.numel() for t in ts] != count:
+    count = array("q", map(torch.Tensor.numel, q))
+    arrays = []
+    for what, ts in (("q", q), ("dq", dq), ("m", m), ("v", v)):
+        if ts is not q and array("q", map(torch.Tensor.numel, ts)) != count:
             raise ValueError(f"{fn}: dq, m and v must have the sizes of q")
+        arrays.append(_arrays(fn, what, ts, [t.dtype for t in ts], _FP32))
     _want(fn, "norm", norm, (1,), torch.float32)
-    arrays = [_arrays(fn, what, ts, (torch.float32,))
-              for what, ts in (("q", q), ("dq", dq), ("m", m), ("v", v))]
     hp = AdamDesc(lr, beta1, beta2, eps, weight_decay, step)
     handle = _stream(stream) if n == 0 else _raw_stream(stream, q[0])
-    st = lib().poetx_adam_group(*arrays, (_ll * n)(*count), n, hp, max_norm, _addr(norm), handle)
+    st = lib().poetx_adam_group(*map(_at, arrays), _at(count), n, hp, max_norm, _addr(norm), handle)
     if st:
         _check(fn, st)
