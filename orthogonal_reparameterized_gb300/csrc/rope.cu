@@ -28,7 +28,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = 256;   // pairs of a head
-constexpr int kCtasPerSm = 3;   // at most
+constexpr int kCtasPerSm = 3;   // at most (the partial sums of dgamma)
 constexpr int kAhead = 256;     // bytes of input that a thread has in flight
 constexpr int kMaxAxes = 8;
 
@@ -40,9 +40,9 @@ struct Side {
   float* part;              // backward: [ctas][dh] partial sums of dgamma (nullable)
   long long xp, dyp, yp;
   int H;
-  int hs, parts;            // heads of a task, tasks of a token
+  int per_token;            // items of a token: an item is what a warp does at a time, 32 / G heads
   int ctas;
-  long long tasks;
+  long long items;
 };
 struct RopeArgs {
   Side s[2];
@@ -54,6 +54,15 @@ struct RopeArgs {
   int G;                    // lanes of a head
   float eps;
 };
+
+__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
+
+// f / 2 pi in units of 2^-64 turns, modulo a turn (in 64-bit integers the same took as long).
+__device__ __forceinline__ unsigned long long turns_of(float f) {
+  double w = (double)f * 0.15915494309189533577;  // 1 / 2 pi
+  w -= floor(w);
+  return w < 1.0 ? (unsigned long long)(w * 18446744073709551616.0) : 0ull;
+}
 
 template <int B>
 __device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
@@ -75,12 +84,13 @@ struct Chunk {
   static constexpr int UNIT = BYTES / 2 < 16 ? BYTES / 2 : 16;  // bytes of one copy
   static constexpr int UNITS = BYTES / UNIT, WORDS = BYTES / 4;
   // slot: the chunk's first unit of this thread; units are kThreads * UNIT apart (no bank conflicts)
-  static __device__ __forceinline__ void fetch(uint32_t slot, const T* head, int o0, int o1) {
+  // (`far`: elements from the first to the second vector of the chunk)
+  static __device__ __forceinline__ void fetch(uint32_t slot, const T* at, int far) {
 #pragma unroll
-    for (int k = 0; k < UNITS; ++k) {
-      const char* half = reinterpret_cast<const char*>(head + (k < UNITS / 2 ? o0 : o1));
-      copy_async<UNIT>(slot + k * kThreads * UNIT, half + (k % (UNITS / 2)) * UNIT);
-    }
+    for (int k = 0; k < UNITS; ++k)
+      copy_async<UNIT>(slot + k * kThreads * UNIT,
+                       reinterpret_cast<const char*>(k < UNITS / 2 ? at : at + far) +
+                           (k % (UNITS / 2)) * UNIT);
   }
   static __device__ __forceinline__ void read(const char* slot, uint32_t (&r)[WORDS]) {
 #pragma unroll
@@ -112,6 +122,10 @@ struct Chunk {
         v[i] = __uint_as_float(r[i]);
       }
     }
+    pairs(v, a, b);
+  }
+  static __device__ __forceinline__ void pairs(const float (&v)[2 * CH], float2 (&a)[CH / 2],
+                                               float2 (&b)[CH / 2]) {
 #pragma unroll
     for (int j = 0; j < CH / 2; ++j) {
       a[j] = INTER ? make_float2(v[4 * j], v[4 * j + 2]) : make_float2(v[2 * j], v[2 * j + 1]);
@@ -119,7 +133,7 @@ struct Chunk {
                    : make_float2(v[CH + 2 * j], v[CH + 2 * j + 1]);
     }
   }
-  static __device__ __forceinline__ void store(T* head, int o0, int o1, const float2 (&a)[CH / 2],
+  static __device__ __forceinline__ void store(T* to, int far, const float2 (&a)[CH / 2],
                                                const float2 (&b)[CH / 2]) {
     float v[2 * CH];
 #pragma unroll
@@ -135,7 +149,7 @@ struct Chunk {
       r[i] = sizeof(T) == 2 ? pack_bf16x2(v[2 * i], v[2 * i + 1]) : __float_as_uint(v[i]);
 #pragma unroll
     for (int k = 0; k < UNITS; ++k) {
-      char* at = reinterpret_cast<char*>(head + (k < UNITS / 2 ? o0 : o1)) + (k % (UNITS / 2)) * UNIT;
+      char* at = reinterpret_cast<char*>(k < UNITS / 2 ? to : to + far) + (k % (UNITS / 2)) * UNIT;
       if constexpr (UNIT == 8)
         *reinterpret_cast<uint2*>(at) = make_uint2(r[2 * k], r[2 * k + 1]);
       else
@@ -143,248 +157,284 @@ struct Chunk {
     }
   }
 };
-template <typename T, int CH, bool NORM, bool BWD>
-constexpr int slot_bytes() {  // a thread's bytes of one head
-  return (NORM && BWD ? 2 : 1) * 2 * CH * (int)sizeof(T);
-}
-template <typename T, int CH, bool NORM, bool BWD>
-constexpr int slots() {
-  return kAhead / slot_bytes<T, CH, NORM, BWD>();
-}
+constexpr int ctas_per_sm(bool norm, bool bwd) { return norm && bwd ? 2 : 3; }
 
-// Where a warp is in its tasks: a token and the first of the group of 32 / G heads that are next.
+// Where a warp is in its items: how many are left, the token and the first head of the next one, and the
+// thread's own chunk there in up to two arrays.
+template <typename T>
 struct Cursor {
-  long long task;
-  int token, h0, h_end;
-  __device__ __forceinline__ void begin(const Side& s) {
-    if (task >= s.tasks) return;
-    token = s.parts == 1 ? (int)task : (int)(task / s.parts);
-    const int part = s.parts == 1 ? 0 : (int)(task - (long long)token * s.parts);
-    h0 = part * s.hs;
-    h_end = min(s.H, h0 + s.hs);
-  }
-  __device__ __forceinline__ bool next(const Side& s, int HW, long long step) {  // true: another token
-    h0 += HW;
-    if (h0 < h_end) return false;
-    task += step;
-    begin(s);
-    return true;
-  }
+  int left, token, h0;
+  const T *p0, *p1;
 };
 
+// Sums over the G lanes of a head.
+template <int n>
+__device__ __forceinline__ void group_sum(float (&v)[n], int G) {
+  auto add = [&](int o) {
+#pragma unroll
+    for (int i = 0; i < n; ++i) v[i] += __shfl_xor_sync(0xffffffffu, v[i], o);
+  };
+  if (G == 8) {  // (most heads: 128 wide, or 64 in chunks of four pairs)
+    add(4);
+    add(2);
+    add(1);
+  } else {
+    for (int o = G / 2; o; o >>= 1) add(o);
+  }
+}
+
 template <typename T, int CH, bool INTER, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kThreads, BWD && NORM ? 2 : 3)
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
     rope_kernel(const __grid_constant__ RopeArgs a) {
   using C = Chunk<T, CH, INTER>;
-  constexpr int SLOTS = slots<T, CH, NORM, BWD>(), SLOT = slot_bytes<T, CH, NORM, BWD>() * kThreads;
   constexpr bool BOTH = BWD && NORM;  // both x and dy are read
+  constexpr int HEAD = C::BYTES * kThreads, SLOT = (BOTH ? 2 : 1) * HEAD;
+  constexpr int SLOTS = kAhead * kThreads / SLOT;
   constexpr int N2 = CH / 2;
-  extern __shared__ __align__(16) char ring[];   // [slot][array][unit][thread]
-  __shared__ unsigned long long turn[kMaxHalf];  // inv_freq / 2 pi, in 2^-64 turns
+  // [slot][array][unit][thread], then each warp's cosines and sines of its token [half]
+  extern __shared__ __align__(16) char ring[];
+  __shared__ unsigned long long turn[kMaxHalf];  // the frequencies in 2^-64 turns
   __shared__ int ax[kMaxHalf];                   // the pair's axis, -1: NaN
-  __shared__ float gsm[NORM ? 2 * kMaxHalf : 1];
+  __shared__ __align__(16) float gsm[NORM ? 2 * kMaxHalf : 4];
   pdl_trigger();
   pdl_wait();
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  if (t < a.half) {
-    const float f = a.inv_freq[t];
-    const int axis = a.axis ? a.axis[t] : 0;
-    double w = (double)f * 0.15915494309189533577;  // 1 / 2 pi
-    w -= floor(w);
-    turn[t] = w < 1.0 ? (unsigned long long)(w * 18446744073709551616.0) : 0ull;
-    ax[t] = isfinite(f) && axis >= 0 && axis < a.axes ? axis : -1;
-  }
+  const float freq = t < a.half ? a.inv_freq[t] : 0.f;
+  const int axis = t < a.half && a.axis ? a.axis[t] : 0;
   const int which = (int)blockIdx.x >= a.s[0].ctas;
   const Side& s = a.s[which];
   const int cta = (int)blockIdx.x - (which ? a.s[0].ctas : 0);
-  const int G = a.G, c = lane & (G - 1), sub = lane / G, HW = 32 / G;
+  const int G = a.G, c = lane & (G - 1), sub = lane / G, HW = 32 / G, dh = a.dh, H = s.H;
   const int pr = a.half / CH;  // rotated chunks
-  const bool mine = c < a.dh / (2 * CH), rot = c < pr;
+  const bool mine = c < dh / (2 * CH), rot = c < pr;
   const int tail = 2 * a.half + 2 * CH * (c - pr);
   const int o0 = rot ? (INTER ? 2 * CH * c : CH * c) : tail;
   const int o1 = rot && !INTER ? a.half + CH * c : o0 + CH;
-  const T* const x = static_cast<const T*>(s.x);
-  const T* const dy = static_cast<const T*>(s.dy);
-  T* const y = static_cast<T*>(s.y);
+  const int far = o1 - o0, ahead_by = HW * dh;
   const uint32_t ring_at = smem_u32(ring) + t * C::UNIT;
-  const char* const my_ring = ring + t * C::UNIT;
-  constexpr int SECOND = C::BYTES * kThreads;  // dy's chunk behind x's
+  char* const my_ring = ring + t * C::UNIT;
+  float2* const angles = reinterpret_cast<float2*>(ring + kAhead * kThreads) + warp * a.half;
 
-  const long long step = (long long)s.ctas * kWarps;
-  Cursor at{(long long)cta * kWarps + warp, 0, 0, 0}, ahead = at;
-  at.begin(s);
-  ahead.begin(s);
+  const T* const in0 = static_cast<const T*>(BWD && !NORM ? s.dy : s.x);
+  const T* const in1 = BOTH ? static_cast<const T*>(s.dy) : nullptr;
+  const long long pitch0 = BWD && !NORM ? s.dyp : s.xp;
+  T* const y = static_cast<T*>(s.y);
+  const int own = sub * dh + o0;  // the thread's chunk in the heads of an item
+  // The warp's items: an equal share of all, one after the other, whatever tokens they belong to.
+  Cursor<T> at, ahead;  // the heads being computed, the heads being fetched
+  {
+    const long long w = (long long)cta * kWarps + warp, W = (long long)s.ctas * kWarps;
+    const long long first = s.items * w / W;
+    at.left = (int)(s.items * (w + 1) / W - first);
+    at.token = (int)(first / s.per_token);
+    at.h0 = (int)(first - (long long)at.token * s.per_token) * HW;
+    ahead = at;
+    at.p0 = y + at.token * s.yp + (at.h0 * dh + own);
+    ahead.p0 = in0 + at.token * pitch0 + (at.h0 * dh + own);
+    ahead.p1 = BOTH ? in1 + at.token * s.dyp + (at.h0 * dh + own) : nullptr;
+  }
   auto fetch = [&](int slot) {
-    if (ahead.task < s.tasks) {
-      const int h = ahead.h0 + sub;
-      if (mine && h < ahead.h_end) {
-        const uint32_t to = ring_at + slot * SLOT;
-        if (!BWD || NORM)
-          C::fetch(to, x + (long long)ahead.token * s.xp + (long long)h * a.dh, o0, o1);
-        if (BWD)
-          C::fetch(to + (BOTH ? SECOND : 0), dy + (long long)ahead.token * s.dyp + (long long)h * a.dh, o0,
-                   o1);
+    if (ahead.left > 0) {
+      if (mine && ahead.h0 + sub < H) {
+        C::fetch(ring_at + slot * SLOT, ahead.p0, far);
+        if (BOTH) C::fetch(ring_at + slot * SLOT + HEAD, ahead.p1, far);
       }
-      ahead.next(s, HW, step);
+      --ahead.left;
+      ahead.h0 += HW;
+      ahead.p0 += ahead_by;
+      if (BOTH) ahead.p1 += ahead_by;
+      if (ahead.h0 >= H) {
+        ahead.h0 = 0;
+        ++ahead.token;
+        ahead.p0 = in0 + ahead.token * pitch0 + own;
+        if (BOTH) ahead.p1 = in1 + ahead.token * s.dyp + own;
+      }
     }
     copy_commit();
   };
 #pragma unroll 1
   for (int i = 0; i < SLOTS; ++i) fetch(i);
+  if (t < a.half) {
+    turn[t] = turns_of(freq);
+    ax[t] = isfinite(freq) && axis >= 0 && axis < a.axes ? axis : -1;
+  }
+  if (!mine)  // lanes beyond the head's width: zeros in the sums
+    for (int i = 0; i < kAhead / C::UNIT; ++i) {
+      if (C::UNIT == 8) *reinterpret_cast<uint2*>(my_ring + i * kThreads * C::UNIT) = make_uint2(0u, 0u);
+      else *reinterpret_cast<uint4*>(my_ring + i * kThreads * C::UNIT) = make_uint4(0u, 0u, 0u, 0u);
+    }
   if (NORM)
-    for (int i = t; i < a.dh; i += kThreads) gsm[i] = s.gamma ? s.gamma[i] : 1.f;
-  const float inv_dh = 1.f / (float)a.dh;
+    for (int i = t; i < dh; i += kThreads) gsm[i] = s.gamma ? s.gamma[i] : 1.f;
+  const float inv_dh = 1.f / (float)dh;
   __syncthreads();
   // gamma of the pairs' first and second elements (the forward reads it once per token)
-  auto gamma2 = [&](int j, float2& p, float2& q) {
-    p = q = both(1.f);
-    if (!NORM || !mine) return;
-    const int i = INTER ? 4 * j : 2 * j, d = INTER ? 2 : 1;
-    p = make_float2(gsm[o0 + i], gsm[o0 + i + d]);
-    q = INTER ? make_float2(gsm[o0 + i + 1], gsm[o0 + i + 3]) : make_float2(gsm[o1 + i], gsm[o1 + i + 1]);
+  auto gamma2 = [&](float2 (&p)[N2], float2 (&q)[N2]) {
+    float v[2 * CH];
+    if (NORM && mine) {
+#pragma unroll
+      for (int i = 0; i < CH; i += 4) {
+        const float4 w = *reinterpret_cast<const float4*>(gsm + o0 + i);
+        const float4 z = *reinterpret_cast<const float4*>(gsm + o1 + i);
+        v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
+        v[CH + i] = z.x, v[CH + i + 1] = z.y, v[CH + i + 2] = z.z, v[CH + i + 3] = z.w;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < 2 * CH; ++i) v[i] = 1.f;
+    }
+    C::pairs(v, p, q);
   };
   float2 ga[N2], gb[N2], dga[N2], dgb[N2];
   if (BOTH) {
+    gamma2(ga, gb);
 #pragma unroll
-    for (int j = 0; j < N2; ++j) {
-      gamma2(j, ga[j], gb[j]);
-      dga[j] = dgb[j] = both(0.f);
-    }
+    for (int j = 0; j < N2; ++j) dga[j] = dgb[j] = both(0.f);
   }
   float2 cs[N2], sn[N2];  // of the token's angles
   // forward with the norm: gamma_a cos, -gamma_b sin, gamma_a sin, gamma_b cos
   float2 fa[N2], fb[N2], fc[N2], fd[N2];
+  // the positions of the token, lane i those of axis i (read while the token before is worked on)
+  int pos = lane < a.axes && at.left > 0 ? a.pos[(long long)lane * a.N + at.token] : 0;
   bool fresh = true;
   int slot = 0;
 #pragma unroll 1
-  while (at.task < s.tasks) {
-    if (fresh) {
-      float cv[CH], sv[CH];
+  for (; at.left > 0; --at.left) {
+    if (fresh) {  // the token's angles, each made once by the warp
+      __syncwarp();
+      for (int i0 = 0; i0 < a.half; i0 += 32) {
+        const int i = i0 + lane, k = i < a.half ? ax[i] : -1;
+        const int p = __shfl_sync(0xffffffffu, pos, k < 0 ? 0 : k);
+        if (i >= a.half) break;
+        const unsigned long long ang = (unsigned long long)(long long)p * turn[i];
+        const float h = (float)(int)(ang >> 32) * 0x1p-32f;  // turns, in [-1/2, 1/2]
+        float sv, cv;
+        // bf16: the hardware's sine and cosine, within 2^-21 on (-pi, pi), far below the result's
+        // rounding
+        if (sizeof(T) == 2) __sincosf(h * 6.28318530717958647692f, &sv, &cv);
+        else sincospif(2.f * h, &sv, &cv);
+        if (k < 0) cv = sv = __int_as_float(0x7fc00000);
+        angles[i] = make_float2(cv, sv);
+      }
+      if (lane < a.axes && at.token + 1 < a.N) pos = a.pos[(long long)lane * a.N + at.token + 1];
+      __syncwarp();
 #pragma unroll
-      for (int j = 0; j < CH; ++j) {
-        cv[j] = 1.f;
-        sv[j] = 0.f;
+      for (int j = 0; j < N2; ++j) {
+        cs[j] = both(1.f);
+        sn[j] = both(0.f);
         if (rot) {
-          const int k = ax[CH * c + j];
-          const int p = k < 0 ? 0 : a.pos[(long long)k * a.N + at.token];
-          const unsigned long long ang = (unsigned long long)(long long)p * turn[CH * c + j];
-          const float h = (float)(int)(ang >> 32) * 0x1p-32f;  // turns, in [-1/2, 1/2]
-          // bf16: the hardware's sine and cosine, within 2^-21 on (-pi, pi), far below the result's
-          // rounding
-          if (sizeof(T) == 2) __sincosf(h * 6.28318530717958647692f, &sv[j], &cv[j]);
-          else sincospif(2.f * h, &sv[j], &cv[j]);
-          if (k < 0) cv[j] = sv[j] = __int_as_float(0x7fc00000);
+          const float4 w = *reinterpret_cast<const float4*>(angles + CH * c + 2 * j);
+          cs[j] = make_float2(w.x, w.z);
+          sn[j] = make_float2(w.y, w.w);
         }
       }
-#pragma unroll
-      for (int j = 0; j < N2; ++j) {
-        cs[j] = make_float2(cv[2 * j], cv[2 * j + 1]);
-        sn[j] = make_float2(sv[2 * j], sv[2 * j + 1]);
-        if (NORM && !BWD) {
-          float2 p, q;
-          gamma2(j, p, q);
-          fa[j] = mul2(p, cs[j]);
-          fb[j] = mul2(q, make_float2(-sn[j].x, -sn[j].y));
-          fc[j] = mul2(p, sn[j]);
-          fd[j] = mul2(q, cs[j]);
-        }
-      }
-    }
-    const int h = at.h0 + sub;
-    const bool on = mine && h < at.h_end;
-    copy_wait<SLOTS - 1>();
-    uint32_t rx[C::WORDS], ry[C::WORDS];
-#pragma unroll
-    for (int i = 0; i < C::WORDS; ++i) rx[i] = ry[i] = 0u;
-    if (on) {
-      C::read(my_ring + slot * SLOT, rx);
-      if (BOTH) C::read(my_ring + slot * SLOT + SECOND, ry);
-    }
-    float2 xa[N2], xb[N2];  // x (backward without the norm: dy)
-    C::split(rx, xa, xb);
-    const long long token = at.token;
-    if constexpr (!BWD) {
-      float rstd = 1.f;
-      if (NORM) {
-        float2 sq = both(0.f);
-#pragma unroll
-        for (int j = 0; j < N2; ++j) sq = fma2(xb[j], xb[j], fma2(xa[j], xa[j], sq));
-        float ss = sq.x + sq.y;
-        for (int o = G / 2; o; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        rstd = rsqrtf(ss * inv_dh + a.eps);
-      }
-      fetch(slot);
-      float2 ya[N2], yb[N2];
-#pragma unroll
-      for (int j = 0; j < N2; ++j) {
-        if (NORM) {
-          if (rot) {
-            ya[j] = mul2(fma2(xb[j], fb[j], mul2(xa[j], fa[j])), both(rstd));
-            yb[j] = mul2(fma2(xb[j], fd[j], mul2(xa[j], fc[j])), both(rstd));
-          } else {  // (no product with a zero sine: the partner may be infinite)
-            ya[j] = mul2(mul2(xa[j], fa[j]), both(rstd));
-            yb[j] = mul2(mul2(xb[j], fd[j]), both(rstd));
-          }
-        } else {
-          if (rot) {
-            ya[j] = fma2(xb[j], make_float2(-sn[j].x, -sn[j].y), mul2(xa[j], cs[j]));
-            yb[j] = fma2(xb[j], cs[j], mul2(xa[j], sn[j]));
-          } else {
-            ya[j] = xa[j];
-            yb[j] = xb[j];
-          }
-        }
-      }
-      if (on) C::store(y + token * s.yp + (long long)h * a.dh, o0, o1, ya, yb);
-    } else {
-      float2 da[N2], db[N2];  // the gradient of the rotated head, then of the normalised one
-      if constexpr (BOTH) {
-        C::split(ry, da, db);
-      } else {
+      if (NORM && !BWD) {
+        float2 p[N2], q[N2];
+        gamma2(p, q);
 #pragma unroll
         for (int j = 0; j < N2; ++j) {
-          da[j] = xa[j];
-          db[j] = xb[j];
+          fa[j] = mul2(p[j], cs[j]);
+          fb[j] = mul2(q[j], neg2(sn[j]));
+          fc[j] = mul2(p[j], sn[j]);
+          fd[j] = mul2(q[j], cs[j]);
         }
       }
-      fetch(slot);
+    }
+    copy_wait<SLOTS - 1>();
+    float2 xa[N2], xb[N2];  // x (backward without the norm: dy)
+    float2 da[N2], db[N2];  // the gradient of the rotated head, then of the normalised one
+    {
+      uint32_t r[C::WORDS];
+      C::read(my_ring + slot * SLOT, r);
+      C::split(r, xa, xb);
+      if (BOTH) {
+        C::read(my_ring + slot * SLOT + HEAD, r);
+        C::split(r, da, db);
+      }
+    }
+    float sum[BOTH ? 2 : 1];  // of x^2, and of u x
+    if (NORM) {
+      float2 sq = mul2(xa[0], xa[0]), sr = mul2(xb[0], xb[0]);
+#pragma unroll
+      for (int j = 1; j < N2; ++j) {
+        sq = fma2(xa[j], xa[j], sq);
+        sr = fma2(xb[j], xb[j], sr);
+      }
+      sq = add2(sq, sr);
+      sum[0] = sq.x + sq.y;
+    }
+    if (BWD && rot) {
+#pragma unroll
+      for (int j = 0; j < N2; ++j) {
+        const float2 p = BOTH ? da[j] : xa[j], q = BOTH ? db[j] : xb[j];
+        da[j] = fma2(q, sn[j], mul2(p, cs[j]));
+        db[j] = fma2(q, cs[j], mul2(p, neg2(sn[j])));
+      }
+    } else if (BWD && !NORM) {
+#pragma unroll
+      for (int j = 0; j < N2; ++j) {
+        da[j] = xa[j];
+        db[j] = xb[j];
+      }
+    }
+    if constexpr (BOTH) {
+      float2 sd = mul2(mul2(da[0], ga[0]), xa[0]), se = mul2(mul2(db[0], gb[0]), xb[0]);
+#pragma unroll
+      for (int j = 1; j < N2; ++j) {
+        sd = fma2(mul2(da[j], ga[j]), xa[j], sd);
+        se = fma2(mul2(db[j], gb[j]), xb[j], se);
+      }
+      sd = add2(sd, se);
+      sum[1] = sd.x + sd.y;
+    }
+    fetch(slot);  // into the slot just read
+    if (NORM) group_sum(sum, G);
+    const float2 rstd = both(NORM ? rsqrtf(sum[0] * inv_dh + a.eps) : 1.f);
+    const bool on = mine && at.h0 + sub < H;
+    T* const out = const_cast<T*>(at.p0);
+    if constexpr (!BWD) {
       if (rot) {
 #pragma unroll
         for (int j = 0; j < N2; ++j) {
-          const float2 p = da[j], q = db[j];
-          da[j] = fma2(q, sn[j], mul2(p, cs[j]));
-          db[j] = fma2(q, cs[j], mul2(p, make_float2(-sn[j].x, -sn[j].y)));
-        }
-      }
-      if constexpr (NORM) {
-        float2 sq = both(0.f), sd = both(0.f);
-#pragma unroll
-        for (int j = 0; j < N2; ++j) {
-          sq = fma2(xb[j], xb[j], fma2(xa[j], xa[j], sq));
-          sd = fma2(mul2(db[j], gb[j]), xb[j], fma2(mul2(da[j], ga[j]), xa[j], sd));
-        }
-        float ss = sq.x + sq.y, su = sd.x + sd.y;
-        for (int o = G / 2; o; o >>= 1) {
-          ss += __shfl_xor_sync(0xffffffffu, ss, o);
-          su += __shfl_xor_sync(0xffffffffu, su, o);
-        }
-        const float rstd = rsqrtf(ss * inv_dh + a.eps);
-        const float m = -su * rstd * inv_dh;
-        if (on) {
-#pragma unroll
-          for (int j = 0; j < N2; ++j) {
-            const float2 ha = mul2(xa[j], both(rstd)), hb = mul2(xb[j], both(rstd));
-            dga[j] = fma2(da[j], ha, dga[j]);
-            dgb[j] = fma2(db[j], hb, dgb[j]);
-            da[j] = mul2(fma2(ha, both(m), mul2(da[j], ga[j])), both(rstd));
-            db[j] = mul2(fma2(hb, both(m), mul2(db[j], gb[j])), both(rstd));
+          const float2 p = xa[j], q = xb[j];
+          if (NORM) {
+            xa[j] = mul2(fma2(q, fb[j], mul2(p, fa[j])), rstd);
+            xb[j] = mul2(fma2(q, fd[j], mul2(p, fc[j])), rstd);
+          } else {
+            xa[j] = fma2(q, neg2(sn[j]), mul2(p, cs[j]));
+            xb[j] = fma2(q, cs[j], mul2(p, sn[j]));
           }
         }
+      } else if (NORM) {  // (no product with a zero sine: the partner may be infinite)
+#pragma unroll
+        for (int j = 0; j < N2; ++j) {
+          xa[j] = mul2(mul2(xa[j], fa[j]), rstd);
+          xb[j] = mul2(mul2(xb[j], fd[j]), rstd);
+        }
       }
-      if (on) C::store(y + token * s.yp + (long long)h * a.dh, o0, o1, da, db);
+      if (on) C::store(out, far, xa, xb);
+    } else if (on) {
+      if constexpr (NORM) {
+        const float2 m = both(-sum[1] * rstd.x * inv_dh);
+#pragma unroll
+        for (int j = 0; j < N2; ++j) {
+          const float2 ha = mul2(xa[j], rstd), hb = mul2(xb[j], rstd);
+          dga[j] = fma2(da[j], ha, dga[j]);
+          dgb[j] = fma2(db[j], hb, dgb[j]);
+          da[j] = mul2(fma2(ha, m, mul2(da[j], ga[j])), rstd);
+          db[j] = mul2(fma2(hb, m, mul2(db[j], gb[j])), rstd);
+        }
+      }
+      C::store(out, far, da, db);
     }
     if (++slot == SLOTS) slot = 0;
-    fresh = at.next(s, HW, step);
+    at.h0 += HW;
+    at.p0 += ahead_by;
+    fresh = at.h0 >= H;
+    if (fresh) {
+      at.h0 = 0;
+      ++at.token;
+      at.p0 = y + at.token * s.yp + own;
+    }
   }
   if (BOTH && s.part) {  // the CTA's sums of dgamma, in the order of warps and lanes
     copy_wait<0>();
@@ -400,7 +450,7 @@ __global__ void __launch_bounds__(kThreads, BWD && NORM ? 2 : 3)
     __syncthreads();
     for (int e = t; e < 2 * CH * G; e += kThreads) {
       const int i = e / G, cc = e - i * G;
-      if (cc >= a.dh / (2 * CH)) continue;
+      if (cc >= dh / (2 * CH)) continue;
       float sum = 0.f;
       for (int w = 0; w < kWarps; ++w)
         for (int l = cc; l < 32; l += G) sum += red[(w * 2 * CH + i) * 32 + l];
@@ -409,7 +459,7 @@ __global__ void __launch_bounds__(kThreads, BWD && NORM ? 2 : 3)
       const int b1 = r && !INTER ? a.half + CH * cc : b0 + CH;
       const int j = i < CH ? i : i - CH;  // pair of the chunk
       const int el = INTER ? b0 + 2 * j + (i >= CH) : (i < CH ? b0 : b1) + j;
-      s.part[(long long)cta * a.dh + el] = sum;
+      s.part[(long long)cta * dh + el] = sum;
     }
   }
 }
@@ -449,31 +499,29 @@ bool rope_ok(const poetx_rope* r) {
   return r->head_dim <= (wide ? 512 : 256) && r->axes >= 1 && r->axes <= kMaxAxes;
 }
 
+constexpr int rope_smem(int half) { return kAhead * kThreads + kWarps * half * (int)sizeof(float2); }
+// CTAs that an SM holds: by the kernels' registers, and by shared memory (with 5 KB of tables each).
+int rope_ctas(bool norm, bool bwd, int half) {
+  const int by_smem = 227 * 1024 / (rope_smem(half) + 6 * 1024), by_regs = ctas_per_sm(norm, bwd);
+  return by_smem < by_regs ? by_smem : by_regs;
+}
+
 template <typename T, int CH, bool INTER, bool NORM, bool BWD>
 cudaError_t rope_launch1(const RopeArgs& a, cudaStream_t s) {
   auto k = rope_kernel<T, CH, INTER, NORM, BWD>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kAhead * kThreads);
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rope_smem(kMaxHalf));
   });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), kAhead * kThreads, s, a);
+  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), rope_smem(a.half), s, a);
 }
 template <typename T, int CH, bool BWD>
 cudaError_t rope_launch(const RopeArgs& a, bool inter, bool norm, cudaStream_t s) {
   if (inter)
     return norm ? rope_launch1<T, CH, true, true, BWD>(a, s) : rope_launch1<T, CH, true, false, BWD>(a, s);
   return norm ? rope_launch1<T, CH, false, true, BWD>(a, s) : rope_launch1<T, CH, false, false, BWD>(a, s);
-}
-
-// A side's tasks: whole tokens where they give every warp some, else a token's heads in parts.
-void rope_tasks(Side* s, int N, int HW, int warps) {
-  const int most = ceil_div(s->H, HW), want = ceil_div(warps, N);
-  const int parts = want < most ? want : most;
-  s->hs = ceil_div(ceil_div(s->H, parts), HW) * HW;
-  s->parts = ceil_div(s->H, s->hs);
-  s->tasks = (long long)N * s->parts;
 }
 
 template <bool BWD>
@@ -529,7 +577,7 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
   a.eps = r->eps;
   a.G = 1;
   while (a.G * 2 * CH < a.dh) a.G *= 2;
-  const int max_ctas = (BWD && r->norm ? 2 : kCtasPerSm) * sm_count();
+  const int max_ctas = rope_ctas(r->norm != 0, BWD, a.half) * sm_count();
   const int heads = (q ? q->heads : 0) + (k ? k->heads : 0);
   float* part = static_cast<float*>(ws);
   RopeSum rs{};
@@ -548,9 +596,10 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
     // the CTAs in proportion to the sides' heads
     int ctas = (int)((long long)max_ctas * s.H / heads);
     if (ctas < 1) ctas = 1;
-    rope_tasks(&s, N, 32 / a.G, ctas * kWarps);
-    const int need = ceil_div(s.tasks, kWarps);
-    s.ctas = need < ctas ? need : ctas;
+    s.per_token = ceil_div(s.H, 32 / a.G);
+    s.items = (long long)N * s.per_token;
+    const long long need = (s.items + kWarps - 1) / kWarps;
+    s.ctas = need < ctas ? (int)need : ctas;
     if (BWD && r->norm && h->dgamma) {
       s.part = part;
       rs.part[i] = part;
