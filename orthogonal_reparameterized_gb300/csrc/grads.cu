@@ -11,6 +11,7 @@
 //
 #include <algorithm>
 #include <mutex>
+#include <type_traits>
 
 #include "adam.cuh"
 #include "common.cuh"
@@ -20,24 +21,25 @@ namespace poetx {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kTensors = 512;               // of one launch
+constexpr int kTensors = 512;               // of one launch,
+constexpr int kFewTensors = 48;             // or of a launch with a table of a tenth
 constexpr long long kMaxCount = 1ll << 33;  // elements of a tensor
 constexpr int kMaxParts = 8;                // CTAs per SM at most, whatever the kernel
 
 // ARRAYS pointers per tensor (the gradient first).
-template <int ARRAYS>
+template <int MAX, int ARRAYS>
 struct Table {
   int n;
-  long long start[kTensors + 1];  // the tensors' first units (the last one of a tensor may be part of one)
-  void* p[ARRAYS][kTensors];
-  long long count[kTensors];
-  uint8_t bf16[kTensors];
+  long long start[MAX + 1];  // the tensors' first units (the last one of a tensor may be part of one)
+  void* p[ARRAYS][MAX];
+  long long count[MAX];
+  uint8_t bf16[MAX];
 };
 
 // Calls f(tensor, first unit in it, whole units, elements of a part of a unit behind them) for each
 // piece of the CTA's share.
-template <int ARRAYS, typename F>
-__device__ __forceinline__ void for_share(const Table<ARRAYS>& t, F f) {
+template <int MAX, int ARRAYS, typename F>
+__device__ __forceinline__ void for_share(const Table<MAX, ARRAYS>& t, F f) {
   const long long total = t.start[t.n];
   long long u = total * blockIdx.x / gridDim.x;
   const long long end = total * (blockIdx.x + 1) / gridDim.x;
@@ -137,8 +139,9 @@ __device__ __forceinline__ double block_sum(const Squares& s) {
   return (double)sum + wide;
 }
 
+template <int MAX>
 __global__ void __launch_bounds__(kThreads, 6)
-    norm_kernel(const __grid_constant__ Table<1> t, double* part) {
+    norm_kernel(const __grid_constant__ Table<MAX, 1> t, double* part) {
   pdl_trigger();
   pdl_wait();
   Squares sq;
@@ -191,8 +194,9 @@ __global__ void __launch_bounds__(kJoinThreads) norm_join_kernel(const double* p
   if (threadIdx.x == 0) *norm = (float)sqrt((red[0] + red[1]) + (red[2] + red[3]));
 }
 
+template <int MAX>
 __global__ void __launch_bounds__(kThreads, 6)
-    clip_kernel(const __grid_constant__ Table<1> t, float max_norm, const float* norm) {
+    clip_kernel(const __grid_constant__ Table<MAX, 1> t, float max_norm, const float* norm) {
   pdl_trigger();
   pdl_wait();
   const float f = clip_factor(norm, max_norm);
@@ -234,8 +238,9 @@ __global__ void __launch_bounds__(kThreads, 6)
   });
 }
 
+template <int MAX>
 __global__ void __launch_bounds__(kThreads, 4)
-    adam_group_kernel(const __grid_constant__ Table<4> t, AdamK h, float max_norm, const float* norm) {
+    adam_group_kernel(const __grid_constant__ Table<MAX, 4> t, AdamK h, float max_norm, const float* norm) {
   pdl_trigger();
   pdl_wait();
   const float f = clip_factor(norm, max_norm);
@@ -300,14 +305,14 @@ poetx_status check_arrays(void* const* const (&p)[ARRAYS], const poetx_dtype* dt
   return POETX_OK;
 }
 
-// The table of the next tensors from *at on (those without elements left out), at most kTensors of them;
-// false when none is left.
-template <int ARRAYS>
+// The table of the next tensors from *at on (those without elements left out), at most MAX of them; false
+// when none is left.
+template <int MAX, int ARRAYS>
 bool next_table(void* const* const (&p)[ARRAYS], const poetx_dtype* dt, const long long* count, int n,
-                int* at, Table<ARRAYS>* t) {
+                int* at, Table<MAX, ARRAYS>* t) {
   t->n = 0;
   t->start[0] = 0;
-  while (*at < n && t->n < kTensors) {
+  while (*at < n && t->n < MAX) {
     const int i = (*at)++;
     const bool half = dt && dt[i] == POETX_BF16;
     if (!count[i]) continue;
@@ -319,6 +324,9 @@ bool next_table(void* const* const (&p)[ARRAYS], const poetx_dtype* dt, const lo
   }
   return t->n > 0;
 }
+
+using Few = std::integral_constant<int, kFewTensors>;
+using Many = std::integral_constant<int, kTensors>;
 
 // CTAs of a kernel: one per kThreads units up to the resident ones, or, where `small` units are enough
 // for a CTA, as many as there are such shares.  The norm, which only reads, runs at the copy's rate with
@@ -362,17 +370,21 @@ extern "C" poetx_status poetx_grad_norm(const void* const* g, const poetx_dtype*
   if (!aligned16(norm) || !aligned16(ws)) return POETX_ERR_ALIGN;
   if (ws_bytes < poetx_grad_norm_workspace_bytes(n)) return POETX_ERR_WORKSPACE;
   double* part = static_cast<double*>(ws);
-  int parts = 0, at = 0;
-  Table<1> t;
-  while (next_table(p, dt, count, n, &at, &t)) {
-    const int grid = grid_of(norm_kernel, t.start[t.n]);
-    POETX_CUDA_TRY(launch_pdl(norm_kernel, dim3(grid), dim3(kThreads), 0, stream, t, part + parts));
-    POETX_CUDA_TRY(cudaGetLastError());
-    after_launch(stream, ST_GRAD_NORM);
-    parts += grid;
-  }
-  POETX_CUDA_TRY(launch_pdl(norm_join_kernel, dim3(1), dim3(kJoinThreads), 0, stream, (const double*)part, parts,
-                            norm));
+  int parts = 0;
+  auto run = [&](auto kernel, auto max) -> poetx_status {
+    Table<decltype(max)::value, 1> t;
+    for (int at = 0; next_table(p, dt, count, n, &at, &t);) {
+      const int grid = grid_of(kernel, t.start[t.n]);
+      POETX_CUDA_TRY(launch_pdl(kernel, dim3(grid), dim3(kThreads), 0, stream, t, part + parts));
+      POETX_CUDA_TRY(cudaGetLastError());
+      after_launch(stream, ST_GRAD_NORM);
+      parts += grid;
+    }
+    return POETX_OK;
+  };
+  POETX_TRY(n <= kFewTensors ? run(norm_kernel<kFewTensors>, Few{}) : run(norm_kernel<kTensors>, Many{}));
+  POETX_CUDA_TRY(launch_pdl(norm_join_kernel, dim3(1), dim3(kJoinThreads), 0, stream, (const double*)part,
+                            parts, norm));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(stream, ST_GRAD_NORM);
   return POETX_OK;
@@ -385,15 +397,17 @@ extern "C" poetx_status poetx_grad_clip(void* const* g, const poetx_dtype* dt, c
   POETX_TRY(check_arrays(p, dt, count, n));
   if (!(max_norm >= 0.f) || !norm) return POETX_ERR_ARG;
   if (!aligned16(norm)) return POETX_ERR_ALIGN;
-  int at = 0;
-  Table<1> t;
-  while (next_table(p, dt, count, n, &at, &t)) {
-    POETX_CUDA_TRY(launch_pdl(clip_kernel, dim3(grid_of(clip_kernel, t.start[t.n])), dim3(kThreads), 0,
-                              stream, t, max_norm, norm));
-    POETX_CUDA_TRY(cudaGetLastError());
-    after_launch(stream, ST_GRAD_NORM);
-  }
-  return POETX_OK;
+  auto run = [&](auto kernel, auto max) -> poetx_status {
+    Table<decltype(max)::value, 1> t;
+    for (int at = 0; next_table(p, dt, count, n, &at, &t);) {
+      POETX_CUDA_TRY(launch_pdl(kernel, dim3(grid_of(kernel, t.start[t.n])), dim3(kThreads), 0, stream, t,
+                                max_norm, norm));
+      POETX_CUDA_TRY(cudaGetLastError());
+      after_launch(stream, ST_GRAD_NORM);
+    }
+    return POETX_OK;
+  };
+  return n <= kFewTensors ? run(clip_kernel<kFewTensors>, Few{}) : run(clip_kernel<kTensors>, Many{});
 }
 
 extern "C" poetx_status poetx_adam_group(float* const* q, const float* const* dq, float* const* m,
@@ -406,13 +420,16 @@ extern "C" poetx_status poetx_adam_group(float* const* q, const float* const* dq
   POETX_TRY(check_arrays(p, nullptr, count, n));
   if (norm && !(max_norm >= 0.f)) return POETX_ERR_ARG;
   if (!aligned16(norm)) return POETX_ERR_ALIGN;
-  int at = 0;
-  Table<4> t;
-  while (next_table(p, nullptr, count, n, &at, &t)) {
-    POETX_CUDA_TRY(launch_pdl(adam_group_kernel, dim3(grid_of(adam_group_kernel, t.start[t.n], 512)), dim3(kThreads),
-                              0, stream, t, h, max_norm, norm));
-    POETX_CUDA_TRY(cudaGetLastError());
-    after_launch(stream, ST_OPTIM);
-  }
-  return POETX_OK;
+  auto run = [&](auto kernel, auto max) -> poetx_status {
+    Table<decltype(max)::value, 4> t;
+    for (int at = 0; next_table(p, nullptr, count, n, &at, &t);) {
+      POETX_CUDA_TRY(launch_pdl(kernel, dim3(grid_of(kernel, t.start[t.n], 512)), dim3(kThreads), 0, stream,
+                                t, h, max_norm, norm));
+      POETX_CUDA_TRY(cudaGetLastError());
+      after_launch(stream, ST_OPTIM);
+    }
+    return POETX_OK;
+  };
+  return n <= kFewTensors ? run(adam_group_kernel<kFewTensors>, Few{})
+                          : run(adam_group_kernel<kTensors>, Many{});
 }

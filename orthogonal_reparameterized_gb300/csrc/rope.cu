@@ -207,10 +207,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
   const int G = a.G, c = lane & (G - 1), sub = lane / G, HW = 32 / G, dh = a.dh, H = s.H;
   const int pr = a.half / CH;  // rotated chunks
   const bool mine = c < dh / (2 * CH), rot = c < pr;
-  const int tail = 2 * a.half + 2 * CH * (c - pr);
-  const int o0 = rot ? (INTER ? 2 * CH * c : CH * c) : tail;
-  const int o1 = rot && !INTER ? a.half + CH * c : o0 + CH;
-  const int far = o1 - o0, ahead_by = HW * dh;
+  // its two vectors, half of the rotated (of the other) elements apart, so that the lanes of a head read
+  // and write whole lines whatever the pairing (interleaved pairs in neighbouring vectors: 49 us, not 37)
+  const int o0 = rot ? CH * c : 2 * a.half + CH * (c - pr);
+  const int far = rot ? a.half : dh / 2 - a.half, ahead_by = HW * dh;
   const uint32_t ring_at = smem_u32(ring) + t * C::UNIT;
   char* const my_ring = ring + t * C::UNIT;
   float2* const angles = reinterpret_cast<float2*>(ring + kAhead * kThreads) + warp * a.half;
@@ -274,7 +274,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
 #pragma unroll
       for (int i = 0; i < CH; i += 4) {
         const float4 w = *reinterpret_cast<const float4*>(gsm + o0 + i);
-        const float4 z = *reinterpret_cast<const float4*>(gsm + o1 + i);
+        const float4 z = *reinterpret_cast<const float4*>(gsm + o0 + far + i);
         v[i] = w.x, v[i + 1] = w.y, v[i + 2] = w.z, v[i + 3] = w.w;
         v[CH + i] = z.x, v[CH + i + 1] = z.y, v[CH + i + 2] = z.z, v[CH + i + 3] = z.w;
       }
@@ -322,7 +322,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
         cs[j] = both(1.f);
         sn[j] = both(0.f);
         if (rot) {
-          const float4 w = *reinterpret_cast<const float4*>(angles + CH * c + 2 * j);
+          const int i = !INTER ? CH * c + 2 * j : CH / 2 * c + 2 * j + (j < N2 / 2 ? 0 : (a.half - CH) / 2);
+          const float4 w = *reinterpret_cast<const float4*>(angles + i);
           cs[j] = make_float2(w.x, w.z);
           sn[j] = make_float2(w.y, w.w);
         }
@@ -455,10 +456,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
       for (int w = 0; w < kWarps; ++w)
         for (int l = cc; l < 32; l += G) sum += red[(w * 2 * CH + i) * 32 + l];
       const bool r = cc < pr;
-      const int b0 = r ? (INTER ? 2 * CH * cc : CH * cc) : 2 * a.half + 2 * CH * (cc - pr);
-      const int b1 = r && !INTER ? a.half + CH * cc : b0 + CH;
+      const int b0 = r ? CH * cc : 2 * a.half + CH * (cc - pr), b1 = b0 + (r ? a.half : dh / 2 - a.half);
       const int j = i < CH ? i : i - CH;  // pair of the chunk
-      const int el = INTER ? b0 + 2 * j + (i >= CH) : (i < CH ? b0 : b1) + j;
+      const int el = INTER ? (j < CH / 2 ? b0 : b1 - CH) + 2 * j + (i >= CH) : (i < CH ? b0 : b1) + j;
       s.part[(long long)cta * dh + el] = sum;
     }
   }

@@ -660,11 +660,12 @@ def _dtype(fn: str, t) -> int:
     """The code of t's type; t must live on the current device."""
     if not t.is_cuda:
         raise ValueError("poetx: tensors must live on a CUDA device")
-    if t.get_device() != torch.cuda.current_device():
+    if t.get_device() != torch._C._cuda_getDevice():
         raise ValueError(f"{fn}: tensors must live on the current device")
-    if t.dtype is not torch.bfloat16 and t.dtype is not torch.float32:
+    dt = _DT.get(t.dtype)
+    if dt is None or dt == I8:
         raise ValueError(f"{fn}: bf16 or fp32, got {t.dtype}")
-    return _DT[t.dtype]
+    return dt
 
 
 def _rows(fn: str, what: str, t, width: int):
@@ -767,35 +768,37 @@ def poetx_ffn_bwd(x, W, dh, z=None, dx=None, dW=None, act=SILU, accumulate=False
 
 # ---------------------------------------------------------------- queries and keys
 def _rope(fn, x, pos, inv_freq, rot_dim, axis, interleaved, norm, eps):
-    """The checked descriptor and (type, N) of a call on x [N, heads, head_dim]."""
+    """The checked descriptor and type of a call on x [N, heads, head_dim]."""
     N, _, dh = x.shape
-    rot = dh if rot_dim is None else rot_dim
+    half = (dh if rot_dim is None else rot_dim) // 2
     axes = pos.shape[0] if pos.dim() == 2 else 1
     _want(fn, "pos", pos, (axes, N) if pos.dim() == 2 else (N,), torch.int32)
-    _want(fn, "inv_freq", inv_freq, (rot // 2,), torch.float32)
-    _want(fn, "axis", axis, (rot // 2,), torch.int32)
-    dt = _dtype(fn, x)
-    return dt, RopeDesc(dh, rot, int(bool(interleaved)), axes, int(bool(norm)), eps,
-                        _addr(inv_freq), _addr(axis))
+    _want(fn, "inv_freq", inv_freq, (half,), torch.float32)
+    _want(fn, "axis", axis, (half,), torch.int32)
+    return _dtype(fn, x), RopeDesc(dh, dh if rot_dim is None else rot_dim, 1 if interleaved else 0,
+                                   axes, 1 if norm else 0, eps, _addr(inv_freq), _addr(axis))
 
 
-def _heads(fn, what, x, gamma, y, like, dt, dy=None, dgamma=None):
+def _heads(fn, what, x, gamma, y, like, dy=None, dgamma=None):
     """The descriptor of one side (None: x is None)."""
     if x is None:
         return None
-    N, H, dh = x.shape
-    if x is not like and (N, dh, x.dtype) != (like.shape[0], like.shape[2], like.dtype):
+    shape, dtype = x.shape, x.dtype
+    N, H, dh = shape
+    if x is not like and (N, dh, dtype) != (like.shape[0], like.shape[2], like.dtype):
         raise ValueError(f"{fn}: queries and keys must have the same tokens, head width and type")
-    _want(fn, what + "'s output", y, x.shape, x.dtype)
-    _want(fn, "gamma_" + what, gamma, (dh,), torch.float32)
+    _want(fn, what + "'s output", y, shape, dtype)
+    if gamma is not None:
+        _want(fn, "gamma_" + what, gamma, (dh,), torch.float32)
+        gamma = _addr(gamma)
     px, pitch = _rows(fn, what, x, H * dh)
     py, y_pitch = _rows(fn, what + "'s output", y, H * dh)
-    pd, d_pitch = None, 0
-    if dy is not None:
-        _want(fn, "d" + what, dy, x.shape, x.dtype)
-        _want(fn, "dgamma_" + what, dgamma, (dh,), torch.float32)
-        pd, d_pitch = _rows(fn, "d" + what, dy, H * dh)
-    return HeadsDesc(H, px, pitch, _addr(gamma), pd, d_pitch, py, y_pitch, _addr(dgamma))
+    if dy is None:
+        return HeadsDesc(H, px, pitch, gamma, None, 0, py, y_pitch, None)
+    _want(fn, "d" + what, dy, shape, dtype)
+    _want(fn, "dgamma_" + what, dgamma, (dh,), torch.float32)
+    return HeadsDesc(H, px, pitch, gamma, *_rows(fn, "d" + what, dy, H * dh), py, y_pitch,
+                     _addr(dgamma))
 
 
 def poetx_qk_rope_fwd(q, k, pos, inv_freq, q_out, k_out, rot_dim=None, axis=None, interleaved=False,
@@ -806,8 +809,8 @@ def poetx_qk_rope_fwd(q, k, pos, inv_freq, q_out, k_out, rot_dim=None, axis=None
     q and k can lie in one row with the values; k may be None; an output may be its input."""
     fn = "poetx_qk_rope_fwd"
     dt, r = _rope(fn, q, pos, inv_freq, rot_dim, axis, interleaved, norm, eps)
-    sq = _heads(fn, "q", q, gamma_q, q_out, q, dt)
-    sk = _heads(fn, "k", k, gamma_k, k_out, q, dt)
+    sq = _heads(fn, "q", q, gamma_q, q_out, q)
+    sk = _heads(fn, "k", k, gamma_k, k_out, q)
     st = lib().poetx_qk_rope_fwd(r, dt, _addr(pos), q.shape[0], sq, sk, _raw_stream(stream, q))
     if st:
         _check(fn, st)
@@ -824,8 +827,8 @@ def poetx_qk_rope_bwd(q, k, dq, dk, pos, inv_freq, dq_in, dk_in, rot_dim=None, a
     dgamma_k [dh] fp32, from dq, dk (those of its outputs)."""
     fn = "poetx_qk_rope_bwd"
     dt, r = _rope(fn, q, pos, inv_freq, rot_dim, axis, interleaved, norm, eps)
-    sq = _heads(fn, "q", q, gamma_q, dq_in, q, dt, dq, dgamma_q)
-    sk = _heads(fn, "k", k, gamma_k, dk_in, q, dt, dk, dgamma_k)
+    sq = _heads(fn, "q", q, gamma_q, dq_in, q, dq, dgamma_q)
+    sk = _heads(fn, "k", k, gamma_k, dk_in, q, dk, dgamma_k)
     handle, L = _raw_stream(stream, q), lib()
     if ws is None and norm and (dgamma_q is not None or dgamma_k is not None):
         ws = _scratch(L.poetx_qk_rope_bwd_workspace_bytes(r), q, stream, handle)
@@ -844,7 +847,7 @@ def _arrays(fn, what, ts, dtypes, types):
     """The tensors' addresses as an array for the library (maps: hundreds of tensors cost the host as
     much as the kernels)."""
     if not types.issuperset(dtypes) or not all(map(torch.Tensor.is_contiguous, ts)) or \
-            not {torch.cuda.current_device()}.issuperset(map(torch.Tensor.get_device, ts)):
+            set(map(torch.Tensor.get_device, ts)) - {torch._C._cuda_getDevice()}:
         raise ValueError(f"{fn}: {what} must be contiguous tensors on the current CUDA device, of "
                          f"{' or '.join(map(str, types))}")
     return array("Q", map(torch.Tensor.data_ptr, ts))
