@@ -230,19 +230,6 @@ __global__ void __launch_bounds__(kGluThreads) glu_bwd_kernel(const GluArgs p) {
   }
 }
 
-// Zeros in dz's columns 2 F .. pitch - 1 (the products' last K block reads them).
-__global__ void __launch_bounds__(256) ffn_pad_kernel(__nv_bfloat16* z, size_t step, int pieces, int rows,
-                                                      int col, int pitch) {
-  pdl_trigger();
-  pdl_wait();
-  const int per = (pitch - col) / 8;
-  const long long n = (long long)rows * per;
-  for (long long i = (long long)blockIdx.x * 256 + threadIdx.x; i < n; i += (long long)gridDim.x * 256)
-    for (int k = 0; k < pieces; ++k)
-      *reinterpret_cast<uint4*>(z + k * step + i / per * pitch + col + 8 * (i % per)) =
-          make_uint4(0u, 0u, 0u, 0u);
-}
-
 // ---------------------------------------------------------------- the projections
 constexpr int BM = 128;  // rows per CTA (256 per pair)
 constexpr int BF = 128;  // features per pair tile: 128 gate and 128 value columns
@@ -1151,14 +1138,6 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
     }
     POETX_TRY(run_glu(c, stream));
   }
-  if (pl.pitch > 2ll * F) {
-    const long long n = (long long)N * ((pl.pitch - 2 * F) / 8);
-    POETX_CUDA_TRY(launch_pdl(ffn_pad_kernel, dim3(grid_for(n, 256)), dim3(256), 0, stream,
-                              reinterpret_cast<__nv_bfloat16*>(w + pl.dz), pl.z_step / 2, pieces, N, 2 * F,
-                              (int)pl.pitch));
-    POETX_CUDA_TRY(cudaGetLastError());
-    after_launch(stream, ST_GLU);
-  }
   GradProducts g{};
   g.f32 = pl.f32;
   g.fine = pl.fine;
@@ -1166,6 +1145,7 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   g.D = D;
   g.V = 2 * F;
   g.pitch = pl.pitch;
+  g.z_cols = 2ll * F;
   for (int i = 0; i < pieces; ++i) g.z[i] = w + pl.dz + i * pl.z_step;
   g.x = xp;
   g.x_step = piece_step((size_t)N * D);

@@ -1660,7 +1660,8 @@ poetx_status grad_products(const GradProducts& c, cudaStream_t s) {
   if (c.dx) {
     Product& d = h.prod[used++];
     for (int i = 0; i < nz; ++i)
-      if (!bf16_map(&mp.a[i], c.z[i], c.pitch, rows, 64, 128)) return POETX_ERR_CUDA;
+      if (!encode_tma_2d(&mp.a[i], c.z[i], TMA_BF16, c.z_cols, rows, c.pitch, 64, 128, true))
+        return POETX_ERR_CUDA;
     for (int i = 0; i < np; ++i)
       if (!mn_map(&mp.b[i], c.w + i * c.w_step, c.D, c.V)) return POETX_ERR_CUDA;
     d.b_groups = c.D % 64 == 0;
@@ -1933,7 +1934,7 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
     gp.rows = rows;
     gp.D = c.D;
     gp.V = c.V;
-    gp.pitch = pl.Vp;
+    gp.pitch = gp.z_cols = pl.Vp;
     for (int i = 0; i < 3; ++i) gp.z[i] = pl.fine && i ? w + pl.dz2 : w + pl.dz + i * z_step;
     gp.x = xp;
     gp.x_step = x_step;
