@@ -562,13 +562,20 @@ __global__ void __launch_bounds__(kThreads, 1)
 // At most 128 rows (a token being served, a short step): bound by reading W once, so the roles are
 // swapped.  W is the 128-row operand (one CTA per tile of `height` features, chosen so that every SM gets
 // the same number of them), the NT (16 to 128) padded tokens are the columns, and nearly all of the shared
-// memory is a ring of W tiles in flight.  The gate rows and the value rows of a tile are two accumulators
-// side by side, so that a thread of the epilogue reads both of its feature.  One accumulator over all of K
-// (at most 16384: 1024 adds, 6e-5).
+// memory is a ring of W tiles in flight.
+//
+// A box costs its issuing thread some 0.25 us whatever its size, so there are few of them: one box brings
+// both halves' rows of several K blocks, and x's come from a thread of their own.  An MMA of 128 rows costs
+// about as much for 16 tokens as for 64, so up to 64 features per tile the gate and the value rows are one
+// operand (MERGED; the epilogue brings them together through shared memory), above that two accumulators
+// side by side.  Neighbouring K blocks go to different accumulators (kAccs of them, added in fp32 by the
+// epilogue), so that an MMA need not wait for the one before; D is at most 16384, at most 1024 adds into
+// one (6e-5).
 struct FfnScore {
   int tiles, height;  // height: a multiple of 8 (the swizzle's rows)
   int F, rows, stages;
   int kps, num_st;    // K blocks per stage, stages per tile
+  int grouped;        // the maps are of groups of 64 columns (else kps is 1)
   __nv_bfloat16 *h, *z;  // [rows][F], [rows][z_pitch] (each nullable)
   const __nv_bfloat16* dh;  // [rows][F]: z and z2 are dz's two pieces (nullable)
   __nv_bfloat16* z2;
@@ -579,25 +586,53 @@ struct FfnScore {
 };
 constexpr int kScoreRows = 128;
 constexpr int kScoreMaxD = 16384;
-constexpr int kScoreThreads = 64 + 128;
 constexpr int kScoreRing = 12;
 constexpr int kScoreSmem = 220 * 1024;
+// Sets of four epilogue warps, which take turns with the groups of 16 tokens.
+constexpr int score_sets(int NT) { return NT >= 64 ? 2 : 1; }
+constexpr int score_threads(int NT) { return 32 * (3 + 4 * score_sets(NT)); }
+constexpr int kTurnPitch = 17;  // floats of a row of 16 tokens (MERGED)
+constexpr int kTurnBytes = 128 * kTurnPitch * 4;  // of one set
+int score_room(int NT, bool merged) {  // shared memory of the ring
+  return kScoreSmem - 1024 - 512 - (int)kABytes - (merged ? score_sets(NT) * kTurnBytes : 0);
+}
 int score_stage_bytes(int NT, int height, int kps) { return kps * (2 * height + NT) * BK * 2; }
+constexpr int score_accs(int NT, bool merged) {  // (two buffers of them in 512 columns)
+  return !merged ? 1 : (NT <= 64 ? 4 : 2);
+}
+// The barrier of a set of four epilogue warps, with or without a vote.
+__device__ __forceinline__ void bar_sync(int id) {
+  asm volatile("barrier.sync %0, 128;" ::"r"(id) : "memory");
+}
+__device__ __forceinline__ int bar_all(int id, bool v) {
+  int r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.b32 p, %2, 0;\n\tbarrier.red.and.pred q, %1, 128, p;\n\t"
+      "selp.b32 %0, 1, 0, q;\n\t}\n"
+      : "=r"(r)
+      : "r"(id), "r"((int)v)
+      : "memory");
+  return r;
+}
 
-template <int NT>
-__global__ void __launch_bounds__(kScoreThreads, 1)
-    ffn_score_kernel(const __grid_constant__ CUtensorMap mg, const __grid_constant__ CUtensorMap mu,
-                     const __grid_constant__ CUtensorMap mx, const FfnScore p) {
+template <int NT, bool MERGED>
+__global__ void __launch_bounds__(score_threads(NT), 1)
+    ffn_score_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mx,
+                     const FfnScore p) {
   constexpr uint32_t IDESC = make_idesc(BM, NT, false, false);
-  constexpr uint32_t TMEM_COLS = 4 * NT;
-  const uint32_t w_kb = (uint32_t)p.height * BK * 2;  // one K block of gate (value) rows
-  const uint32_t u_off = p.kps * w_kb, x_off = 2 * u_off;
+  constexpr int SETS = score_sets(NT), XWARP = 2 + 4 * SETS;
+  constexpr int ACCS = score_accs(NT, MERGED), COLS = (MERGED ? 1 : 2) * NT;  // columns of an accumulator
+  constexpr uint32_t TMEM_COLS = 2 * ACCS * COLS;
+  const uint32_t half = (uint32_t)p.height * BK * 2;  // one K block of gate (value) rows
+  const uint32_t x_off = p.kps * 2 * half;
   const uint32_t stage = x_off + p.kps * NT * BK * 2;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   // (16 KB kept behind the last stage: the MMAs read 128 rows from its last K block's first)
-  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage + kABytes);
+  float* turn = reinterpret_cast<float*>(smem + p.stages * stage + kABytes);  // [128][kTurnPitch]
+  uint64_t* full = reinterpret_cast<uint64_t*>(smem + p.stages * stage + kABytes +
+                                               (MERGED ? SETS * kTurnBytes : 0));
   uint64_t* empty = full + kScoreRing;
   uint64_t* tfull = empty + kScoreRing;
   uint64_t* tempty = tfull + 2;
@@ -607,17 +642,16 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
   pdl_trigger();
   if (warp == 0 && lane == 0) {
     for (int s = 0; s < p.stages; ++s) {
-      mbar_init(&full[s], 1);
+      mbar_init(&full[s], 2);  // W's thread and x's
       mbar_init(&empty[s], 1);
     }
     for (int a = 0; a < 2; ++a) {
       mbar_init(&tfull[a], 1);
-      mbar_init(&tempty[a], 4);
+      mbar_init(&tempty[a], 4 * SETS);
     }
     *abort_flag = 0;
     fence_mbar_init();
-    tma_prefetch_desc(&mg);
-    tma_prefetch_desc(&mu);
+    tma_prefetch_desc(&mw);
     tma_prefetch_desc(&mx);
   }
   if (warp == 1) {
@@ -641,7 +675,8 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       ph ^= 1;
     }
   };
-  if (warp == 0 && lane == 0) {
+  if ((warp == 0 || warp == XWARP) && lane == 0) {
+    const bool is_x = warp == XWARP;
     int issued = 0;
     bool ok = true;
     for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x)
@@ -651,18 +686,17 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
           break;
         }
         uint8_t* at = smem + s * stage;
-        mbar_arrive_expect_tx(&full[s], stage);
-        if (p.kps > 1) {
-          tma_load_3d(at, &mg, &full[s], 0, t * p.height, st * p.kps);
-          tma_load_3d(at + u_off, &mu, &full[s], 0, t * p.height, st * p.kps);
-          tma_load_3d(at + x_off, &mx, &full[s], 0, 0, st * p.kps);
+        mbar_arrive_expect_tx(&full[s], is_x ? stage - x_off : x_off);
+        if (is_x) {
+          if (p.grouped) tma_load_3d(at + x_off, &mx, &full[s], 0, 0, st * p.kps);
+          else tma_load_2d(at + x_off, &mx, &full[s], st * BK, 0);
         } else {
-          tma_load_2d(at, &mg, &full[s], st * BK, t * p.height);
-          tma_load_2d(at + u_off, &mu, &full[s], st * BK, t * p.height);
-          tma_load_2d(at + x_off, &mx, &full[s], st * BK, 0);
+          if (p.grouped) tma_load_4d(at, &mw, &full[s], 0, t * p.height, 0, st * p.kps);
+          else tma_load_3d(at, &mw, &full[s], st * BK, t * p.height, 0);
         }
       }
-    for (int j = issued - 1; j >= 0 && j >= issued - p.stages; --j)  // every copy has landed
+    // every copy has landed (of this thread, and where both went on, the other's)
+    for (int j = issued - 1; j >= 0 && j >= issued - p.stages; --j)
       mbar_wait_bounded(&full[j % p.stages], (uint32_t)((j / p.stages) & 1), p.err, p.limit_ns,
                         kSite + __LINE__);
   } else if (warp == 1 && lane == 0) {
@@ -671,23 +705,25 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
     for (int t = blockIdx.x; t < p.tiles && ok; t += gridDim.x, acc.next()) {
       if (!wait(&tempty[acc.s], acc.ph ^ 1, kSite + __LINE__)) break;
       tc_fence_after();
-      const uint32_t d = tmem_base + (uint32_t)(acc.s * 2 * NT);
+      const uint32_t d0 = tmem_base + (uint32_t)(acc.s * ACCS * COLS);
+      int kb = 0;
       for (int j = 0; j < p.num_st; ++j, next()) {
         if (!wait(&full[s], ph, kSite + __LINE__)) {
           ok = false;
           break;
         }
         tc_fence_after();
-        // (rows past `height` of the 128 are whatever follows in shared memory: not looked at)
+        // (rows past the box's are whatever follows in shared memory: not looked at)
         const uint32_t base = smem_base + s * stage;
-        for (int i = 0; i < p.kps; ++i) {
-          const uint64_t gd = make_sdesc(base + i * w_kb, 16, 1024);
-          const uint64_t ud = make_sdesc(base + u_off + i * w_kb, 16, 1024);
+        for (int i = 0; i < p.kps; ++i, ++kb) {
+          const uint32_t d = d0 + (uint32_t)(kb % ACCS * COLS);
+          const uint64_t gd = make_sdesc(base + 2 * i * half, 16, 1024);
+          const uint64_t ud = make_sdesc(base + (2 * i + 1) * half, 16, 1024);
           const uint64_t xd = make_sdesc(base + x_off + i * NT * BK * 2, 16, 1024);
 #pragma unroll
           for (int k = 0; k < BK / 16; ++k) {
-            umma_bf16(d, gd + k * 2, xd + k * 2, IDESC, (j | i | k) != 0);
-            umma_bf16(d + NT, ud + k * 2, xd + k * 2, IDESC, (j | i | k) != 0);
+            umma_bf16(d, gd + k * 2, xd + k * 2, IDESC, kb >= ACCS || k != 0);
+            if (!MERGED) umma_bf16(d + NT, ud + k * 2, xd + k * 2, IDESC, kb >= ACCS || k != 0);
           }
         }
         umma_commit(&empty[s]);
@@ -700,51 +736,91 @@ __global__ void __launch_bounds__(kScoreThreads, 1)
       const int last = acc.s ^ 1;
       mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns, kSite + __LINE__);
     }
-  } else if (warp >= 2) {
-    const int q = warp & 3, mine = q * 32 + lane;  // the thread's feature of the tile
+  } else if (warp >= 2 && warp < XWARP) {
+    const int set = (warp - 2) >> 2, q = warp & 3, mine = q * 32 + lane;  // the thread's lane of the accumulators
+    const int used = min(ACCS, p.num_st * p.kps);
+    // h, z or dz of a feature and a token
+    auto put = [&](long long f, int token, float g, float u, float d) {
+      if (p.h) p.h[(long long)token * p.F + f] = __float2bfloat16_rn(gated<false>(g, u, p.act));
+      if (!p.z) return;
+      const long long at = (long long)token * p.z_pitch + f;
+      const float2 o = p.dh ? gated_grad<false>(g, u, d, p.act) : make_float2(g, u);
+      const __nv_bfloat16 a = __float2bfloat16_rn(o.x), b = __float2bfloat16_rn(o.y);
+      p.z[at] = a;
+      p.z[at + p.F] = b;
+      if (p.dh) {
+        p.z2[at] = __float2bfloat16_rn(o.x - __bfloat162float(a));
+        p.z2[at + p.F] = __float2bfloat16_rn(o.y - __bfloat162float(b));
+      }
+    };
+    // the values that a thread makes of 16 tokens, token << 8 | feature: all tokens of its own feature, or
+    // (MERGED) eight of features and tokens in turn, features fastest
+    constexpr int EACH = MERGED ? 8 : 16;
+    int where[EACH];
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int e = i * 128 + mine;
+      if (MERGED) where[i] = e < 16 * p.height ? (e / p.height) << 8 | e % p.height : -1;
+      else where[i] = mine < p.height ? i << 8 | mine : -1;
+    }
+    turn += set * 128 * kTurnPitch;
     Ring<2> acc;
     for (int t = blockIdx.x; t < p.tiles; t += gridDim.x, acc.next()) {
-      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * 2 * NT);
-      const long long f = (long long)t * p.height + mine;
-      const bool on = mine < p.height && f < p.F;
-      float d[16], d_next[16];
-      auto upstream = [&](int j) {  // dh of the feature, 16 tokens ahead of their use
+      const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(acc.s * ACCS * COLS);
+      const long long f0 = (long long)t * p.height;
+      float d[EACH], d_next[EACH];
+      auto upstream = [&](int j) {  // dh of the thread's values, a group of tokens ahead of their use
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-          d_next[i] = on && j + i < p.rows ? __bfloat162float(p.dh[(long long)(j + i) * p.F + f]) : 0.f;
+        for (int i = 0; i < EACH; ++i) {
+          const int token = j + (where[i] >> 8);
+          const long long f = f0 + (where[i] & 255);
+          d_next[i] = where[i] >= 0 && f < p.F && token < p.rows
+                          ? __bfloat162float(p.dh[(long long)token * p.F + f]) : 0.f;
+        }
       };
-      if (p.dh) upstream(0);
+      if (p.dh) upstream(16 * set);
       const bool got = wait(&tfull[acc.s], acc.ph, kSite + __LINE__);
-      if (!__all_sync(0xffffffffu, got)) break;
+      // (MERGED: all four warps go on or none, for their barrier)
+      if (MERGED ? bar_all(1 + set, got) == 0 : !__all_sync(0xffffffffu, got)) break;
       tc_fence_after();
 #pragma unroll 1
-      for (int j = 0; j < NT && j < p.rows; j += 16) {
-        uint32_t g[16], u[16];
-        tmem_ld_32x32b_x16(ta + j, g);
-        tmem_ld_32x32b_x16(ta + NT + j, u);
-        if (p.dh) {
+      for (int j = 16 * set; j < NT && j < p.rows; j += 16 * SETS) {
+        float g[16], u[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) d[i] = d_next[i];
-          upstream(j + 16);
-        }
-        tmem_ld_wait();
-        if (!on) continue;
+        for (int k = 0; k < ACCS; ++k) {
+          if (k >= used) break;
+          uint32_t r[16], v[16];
+          tmem_ld_32x32b_x16(ta + k * COLS + j, r);
+          if (!MERGED) tmem_ld_32x32b_x16(ta + k * COLS + NT + j, v);
+          tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          if (j + i >= p.rows) break;
-          const float gv = __uint_as_float(g[i]), uv = __uint_as_float(u[i]);
-          if (p.h) p.h[(long long)(j + i) * p.F + f] = __float2bfloat16_rn(gated<false>(gv, uv, p.act));
-          if (!p.z) continue;
-          const long long at = (long long)(j + i) * p.z_pitch + f;
-          const float2 o = p.dh ? gated_grad<false>(gv, uv, d[i], p.act) : make_float2(gv, uv);
-          const __nv_bfloat16 a = __float2bfloat16_rn(o.x), b = __float2bfloat16_rn(o.y);
-          p.z[at] = a;
-          p.z[at + p.F] = b;
-          if (p.dh) {
-            p.z2[at] = __float2bfloat16_rn(o.x - __bfloat162float(a));
-            p.z2[at + p.F] = __float2bfloat16_rn(o.y - __bfloat162float(b));
+          for (int i = 0; i < 16; ++i) {
+            g[i] = k ? g[i] + __uint_as_float(r[i]) : __uint_as_float(r[i]);
+            if (!MERGED) u[i] = k ? u[i] + __uint_as_float(v[i]) : __uint_as_float(v[i]);
           }
         }
+        if (p.dh) {
+#pragma unroll
+          for (int i = 0; i < EACH; ++i) d[i] = d_next[i];
+          upstream(j + 16 * SETS);
+        }
+        if (MERGED) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) turn[mine * kTurnPitch + i] = g[i];
+          bar_sync(1 + set);
+        }
+#pragma unroll
+        for (int i = 0; i < EACH; ++i) {
+          const int token = where[i] >> 8, in = where[i] & 255;
+          if (where[i] < 0 || f0 + in >= p.F || j + token >= p.rows) continue;
+          if (MERGED) {
+            const float* at = turn + in * kTurnPitch + token;
+            put(f0 + in, j + token, at[0], at[p.height * kTurnPitch], d[i]);
+          } else {
+            put(f0 + in, j + token, g[i], u[i], d[i]);
+          }
+        }
+        if (MERGED) bar_sync(1 + set);
       }
       tc_fence_before();
       __syncwarp();
@@ -828,22 +904,21 @@ poetx_status run_glu(const GluCall& c, cudaStream_t s) {
   return POETX_OK;
 }
 
-template <int NT>
-poetx_status score(const CUtensorMap& mg, const CUtensorMap& mu, const CUtensorMap& mx, FfnScore p,
-                   cudaStream_t s) {
-  auto k = ffn_score_kernel<NT>;
+template <int NT, bool MERGED>
+poetx_status score(const CUtensorMap& mw, const CUtensorMap& mx, FfnScore p, cudaStream_t s) {
+  auto k = ffn_score_kernel<NT, MERGED>;
   static std::once_flag once;
   static cudaError_t attr_err = cudaSuccess;
   std::call_once(once, [&] {
     attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
   });
   POETX_CUDA_TRY(attr_err);
-  p.stages = (kScoreSmem - 1024 - 512 - (int)kABytes) / score_stage_bytes(NT, p.height, p.kps);
+  p.stages = score_room(NT, MERGED) / score_stage_bytes(NT, p.height, p.kps);
   if (p.stages > kScoreRing) p.stages = kScoreRing;
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
   const int grid = p.tiles < sm_count() ? p.tiles : sm_count();
-  POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kScoreThreads), kScoreSmem, s, mg, mu, mx, p));
+  POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(score_threads(NT)), kScoreSmem, s, mw, mx, p));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_FFN_GEMM);
   return POETX_OK;
@@ -927,23 +1002,23 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
     p.z_pitch = o.pitch;
     p.act = act;
     const int nt = N <= 16 ? 16 : (N <= 32 ? 32 : (N <= 64 ? 64 : 128));
-    // one box per stage and operand over several K blocks where D is a multiple of 64 (one thread issues
-    // all copies, and larger boxes come in faster)
-    p.kps = D % 64 ? 1 : (nt <= 32 ? 2 : 1);
-    p.num_st = ceil_div(ceil_div(D, BK), p.kps);
-    CUtensorMap mg, mu, mx;
-    const bool maps =
-        p.kps > 1 ? encode_tma_groups(&mg, wp, D, F, p.height, p.kps) &&
-                        encode_tma_groups(&mu, wp + half, D, F, p.height, p.kps) &&
-                        encode_tma_groups(&mx, xp, D, N, nt, p.kps)
-                  : bf16_map(&mg, wp, F, BK, p.height) && bf16_map(&mu, wp + half, F, BK, p.height) &&
-                        bf16_map(&mx, xp, N, BK, nt);
-    if (!maps) return POETX_ERR_CUDA;
+    // K blocks per stage: as many as leave four stages (three where two blocks go in)
+    p.grouped = D % 64 == 0;
+    p.kps = 1;
+    const bool merged = 2 * p.height <= BM;
+    const int blocks = ceil_div(D, BK), room = score_room(nt, merged);
+    for (int k = 2; p.grouped && k <= 8 && k < 2 * blocks; k *= 2)
+      if ((k == 2 ? 3 : 4) * score_stage_bytes(nt, p.height, k) <= room) p.kps = k;
+    p.num_st = ceil_div(blocks, p.kps);
+    CUtensorMap mw, mx;
+    if (!encode_tma_halves(&mw, wp, D, F, p.height, p.kps) ||
+        !(p.grouped ? encode_tma_groups(&mx, xp, D, N, nt, p.kps) : bf16_map(&mx, xp, N, BK, nt)))
+      return POETX_ERR_CUDA;
     switch (nt) {
-      case 16: return score<16>(mg, mu, mx, p, s);
-      case 32: return score<32>(mg, mu, mx, p, s);
-      case 64: return score<64>(mg, mu, mx, p, s);
-      default: return score<128>(mg, mu, mx, p, s);
+      case 16: return merged ? score<16, true>(mw, mx, p, s) : score<16, false>(mw, mx, p, s);
+      case 32: return merged ? score<32, true>(mw, mx, p, s) : score<32, false>(mw, mx, p, s);
+      case 64: return merged ? score<64, true>(mw, mx, p, s) : score<64, false>(mw, mx, p, s);
+      default: return merged ? score<128, true>(mw, mx, p, s) : score<128, false>(mw, mx, p, s);
     }
   }
   FfnMaps m;

@@ -166,6 +166,11 @@ bool encode_tma_2d(CUtensorMap* m, const void* ptr, TmaElem et, uint64_t inner, 
 // box {64, rows, groups}, 128-byte swizzle (cached per thread).
 bool encode_tma_groups(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t rows,
                        uint32_t groups);
+// A bf16 matrix [2 outer][inner] as {64 columns, outer, 2 halves of its rows, groups of 64 columns} (inner not
+// a multiple of 64: {inner, outer, 2}, groups 1), box {64, rows, 2, groups}, 128-byte swizzle (cached per
+// thread).
+bool encode_tma_halves(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t rows,
+                       uint32_t groups);
 // Y = X . op(G) per block (bf16), op = identity (trans=0) or transpose; optional column
 // scale; optional output permutation (column c of the product is stored at out_perm[c]).
 poetx_status umma_blockdiag(const void* X, long long N, int nblk, int b, const void* G, int trans,

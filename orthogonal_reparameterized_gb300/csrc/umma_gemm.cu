@@ -1392,6 +1392,49 @@ bool encode_tma_groups(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t
   return true;
 }
 
+// A bf16 matrix [2 outer][inner] as its two halves of rows side by side: {64 columns, outer, 2, groups of
+// 64 columns}, box {64, rows, 2, groups}, where inner is a multiple of 64 (else groups must be 1: {inner,
+// outer, 2}, box {64, rows, 2}); 128-byte swizzle.  Kept in a per-thread cache like encode_tma_2d's.
+bool encode_tma_halves(CUtensorMap* m, const void* ptr, uint64_t inner, uint64_t outer, uint32_t rows,
+                       uint32_t groups) {
+  struct Entry {
+    const void* ptr;
+    uint64_t inner, outer;
+    uint32_t rows, groups;
+    int dev;
+    CUtensorMap map;
+  };
+  constexpr int kEntries = 16;
+  thread_local Entry cache[kEntries];
+  thread_local int next = 0;
+  int dev = 0;
+  cudaGetDevice(&dev);
+  for (int i = 0; i < kEntries; ++i) {
+    const Entry& e = cache[i];
+    if (e.ptr == ptr && ptr && e.inner == inner && e.outer == outer && e.rows == rows &&
+        e.groups == groups && e.dev == dev) {
+      *m = e.map;
+      return true;
+    }
+  }
+  EncodeTiledFn fn = encode_fn();
+  const bool grouped = inner % 64 == 0;
+  if (!fn || (!grouped && groups != 1)) return false;
+  cuuint64_t dims[4] = {grouped ? 64 : inner, outer, 2, inner / 64};
+  cuuint64_t strides[3] = {inner * 2, outer * inner * 2, 128};
+  cuuint32_t box[4] = {64, rows, 2, groups};
+  cuuint32_t es[4] = {1, 1, 1, 1};
+  if (fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, grouped ? 4 : 3, const_cast<void*>(ptr), dims, strides, box,
+         es, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+         CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    return false;
+  Entry& e = cache[next];
+  next = (next + 1) % kEntries;
+  e.ptr = ptr; e.inner = inner; e.outer = outer; e.rows = rows; e.groups = groups; e.dev = dev;
+  e.map = *m;
+  return true;
+}
+
 bool umma_supported() {
   // sm_103 and a driver entry point for tensor maps; cached per device
   static std::atomic<int> cached[64];
