@@ -42,7 +42,8 @@ struct Side {
   int H;
   int per_token;            // items of a token: an item is what a warp does at a time, 32 / G heads
   int ctas;
-  long long items;
+  int share, extra;         // items of a warp; the first `extra` warps have one more
+  bool wide;                // the items' numbers take 64 bits
 };
 struct RopeArgs {
   Side s[2];
@@ -223,10 +224,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
   // The warp's items: an equal share of all, one after the other, whatever tokens they belong to.
   Cursor<T> at, ahead;  // the heads being computed, the heads being fetched
   {
-    const long long w = (long long)cta * kWarps + warp, W = (long long)s.ctas * kWarps;
-    const long long first = s.items * w / W;
-    at.left = (int)(s.items * (w + 1) / W - first);
-    at.token = (int)(first / s.per_token);
+    const int w = cta * kWarps + warp;
+    const long long first = (long long)w * s.share + min(w, s.extra);
+    at.left = s.share + (w < s.extra);
+    at.token = s.wide ? (int)(first / s.per_token) : (int)((uint32_t)first / (uint32_t)s.per_token);
     at.h0 = (int)(first - (long long)at.token * s.per_token) * HW;
     ahead = at;
     at.p0 = y + at.token * s.yp + (at.h0 * dh + own);
@@ -317,16 +318,17 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
       }
       if (lane < a.axes && at.token + 1 < a.N) pos = a.pos[(long long)lane * a.N + at.token + 1];
       __syncwarp();
+      if (rot) {
 #pragma unroll
-      for (int j = 0; j < N2; ++j) {
-        cs[j] = both(1.f);
-        sn[j] = both(0.f);
-        if (rot) {
+        for (int j = 0; j < N2; ++j) {
           const int i = !INTER ? CH * c + 2 * j : CH / 2 * c + 2 * j + (j < N2 / 2 ? 0 : (a.half - CH) / 2);
           const float4 w = *reinterpret_cast<const float4*>(angles + i);
           cs[j] = make_float2(w.x, w.z);
           sn[j] = make_float2(w.y, w.w);
         }
+      } else if (NORM && !BWD) {
+#pragma unroll
+        for (int j = 0; j < N2; ++j) cs[j] = both(1.f), sn[j] = both(0.f);
       }
       if (NORM && !BWD) {
         float2 p[N2], q[N2];
@@ -597,9 +599,11 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
     int ctas = (int)((long long)max_ctas * s.H / heads);
     if (ctas < 1) ctas = 1;
     s.per_token = ceil_div(s.H, 32 / a.G);
-    s.items = (long long)N * s.per_token;
-    const long long need = (s.items + kWarps - 1) / kWarps;
+    const long long items = (long long)N * s.per_token, need = (items + kWarps - 1) / kWarps;
     s.ctas = need < ctas ? (int)need : ctas;
+    s.share = (int)(items / (s.ctas * kWarps));
+    s.extra = (int)(items % (s.ctas * kWarps));
+    s.wide = items > 0x7fffffffLL;
     if (BWD && r->norm && h->dgamma) {
       s.part = part;
       rs.part[i] = part;
