@@ -11,7 +11,7 @@
 // pair, their angle and their gamma are in one lane's registers whatever the pairing.  All heads of a token
 // use the same angles: a lane makes those of its CH pairs once per token and keeps them over the heads,
 // multiplied by gamma where that saves instructions.  What is in flight waits in shared memory: each
-// thread copies the chunks of its own next heads there asynchronously (256 bytes ahead) and is the only one
+// thread copies the chunks of its own next heads there asynchronously (160 or 256 bytes ahead) and is the only one
 // to read them, so that no barrier is needed.
 //
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
@@ -28,8 +28,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = 256;   // pairs of a head
-constexpr int kCtasPerSm = 3;   // at most (the partial sums of dgamma)
-constexpr int kAhead = 256;     // bytes of input that a thread has in flight
+// By the pairs of a lane, CH: resident CTAs (by registers), and bytes of input that a thread has in flight.
+constexpr int ctas_per_sm(int CH, bool both) { return (CH == 8 ? 3 : 4) - both; }
+constexpr int lead(int CH) { return CH == 8 ? 256 : 160; }
+constexpr int kMostCtas = 3;  // per SM with dgamma's partial sums
 constexpr int kMaxAxes = 8;
 
 struct Side {
@@ -158,8 +160,6 @@ struct Chunk {
     }
   }
 };
-constexpr int ctas_per_sm(bool norm, bool bwd) { return norm && bwd ? 2 : 3; }
-
 // Where a warp is in its items: how many are left, the token and the first head of the next one, and the
 // thread's own chunk there in up to two arrays.
 template <typename T>
@@ -185,12 +185,12 @@ __device__ __forceinline__ void group_sum(float (&v)[n], int G) {
 }
 
 template <typename T, int CH, bool INTER, bool NORM, bool BWD>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
     rope_kernel(const __grid_constant__ RopeArgs a) {
   using C = Chunk<T, CH, INTER>;
   constexpr bool BOTH = BWD && NORM;  // both x and dy are read
   constexpr int HEAD = C::BYTES * kThreads, SLOT = (BOTH ? 2 : 1) * HEAD;
-  constexpr int SLOTS = kAhead * kThreads / SLOT;
+  constexpr int SLOTS = lead(CH) * kThreads / SLOT;
   constexpr int N2 = CH / 2;
   // [slot][array][unit][thread], then each warp's cosines and sines of its token [half]
   extern __shared__ __align__(16) char ring[];
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
   const int far = rot ? a.half : dh / 2 - a.half, ahead_by = HW * dh;
   const uint32_t ring_at = smem_u32(ring) + t * C::UNIT;
   char* const my_ring = ring + t * C::UNIT;
-  float2* const angles = reinterpret_cast<float2*>(ring + kAhead * kThreads) + warp * a.half;
+  float2* const angles = reinterpret_cast<float2*>(ring + lead(CH) * kThreads) + warp * a.half;
 
   const T* const in0 = static_cast<const T*>(BWD && !NORM ? s.dy : s.x);
   const T* const in1 = BOTH ? static_cast<const T*>(s.dy) : nullptr;
@@ -260,7 +260,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(NORM, BWD))
     ax[t] = isfinite(freq) && axis >= 0 && axis < a.axes ? axis : -1;
   }
   if (!mine)  // lanes beyond the head's width: zeros in the sums
-    for (int i = 0; i < kAhead / C::UNIT; ++i) {
+    for (int i = 0; i < lead(CH) / C::UNIT; ++i) {
       if (C::UNIT == 8) *reinterpret_cast<uint2*>(my_ring + i * kThreads * C::UNIT) = make_uint2(0u, 0u);
       else *reinterpret_cast<uint4*>(my_ring + i * kThreads * C::UNIT) = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -501,10 +501,12 @@ bool rope_ok(const poetx_rope* r) {
   return r->head_dim <= (wide ? 512 : 256) && r->axes >= 1 && r->axes <= kMaxAxes;
 }
 
-constexpr int rope_smem(int half) { return kAhead * kThreads + kWarps * half * (int)sizeof(float2); }
+constexpr int rope_smem(int CH, int half) {
+  return lead(CH) * kThreads + kWarps * half * (int)sizeof(float2);
+}
 // CTAs that an SM holds: by the kernels' registers, and by shared memory (with 5 KB of tables each).
-int rope_ctas(bool norm, bool bwd, int half) {
-  const int by_smem = 227 * 1024 / (rope_smem(half) + 6 * 1024), by_regs = ctas_per_sm(norm, bwd);
+int rope_ctas(int CH, bool both, int half) {
+  const int by_smem = 227 * 1024 / (rope_smem(CH, half) + 6 * 1024), by_regs = ctas_per_sm(CH, both);
   return by_smem < by_regs ? by_smem : by_regs;
 }
 
@@ -514,10 +516,10 @@ cudaError_t rope_launch1(const RopeArgs& a, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rope_smem(kMaxHalf));
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rope_smem(CH, kMaxHalf));
   });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), rope_smem(a.half), s, a);
+  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), rope_smem(CH, a.half), s, a);
 }
 template <typename T, int CH, bool BWD>
 cudaError_t rope_launch(const RopeArgs& a, bool inter, bool norm, cudaStream_t s) {
@@ -567,7 +569,10 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
   }
   if (!pos || !r->inv_freq) return POETX_ERR_ARG;
 
-  const int CH = r->head_dim % 16 == 0 && r->rot_dim % 16 == 0 ? 8 : 4;
+  // a lane's vectors of 16 bytes, bf16 or fp32, where the widths allow (fp32 in vectors of 32 bytes, of
+  // which each access takes half: 43 us for 29.8 at 4096 x 40 heads of 128)
+  const bool wide = r->head_dim % 16 == 0 && r->rot_dim % 16 == 0;
+  const int CH = wide && (dt == POETX_BF16 || r->head_dim > 256) ? 8 : 4;
   RopeArgs a{};
   a.pos = pos;
   a.inv_freq = r->inv_freq;
@@ -579,7 +584,7 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
   a.eps = r->eps;
   a.G = 1;
   while (a.G * 2 * CH < a.dh) a.G *= 2;
-  const int max_ctas = rope_ctas(r->norm != 0, BWD, a.half) * sm_count();
+  const int max_ctas = rope_ctas(CH, BWD && r->norm, a.half) * sm_count();
   const int heads = (q ? q->heads : 0) + (k ? k->heads : 0);
   float* part = static_cast<float*>(ws);
   RopeSum rs{};
@@ -645,7 +650,7 @@ extern "C" poetx_status poetx_qk_rope_fwd(const poetx_rope* r, poetx_dtype dt, c
 
 extern "C" size_t poetx_qk_rope_bwd_workspace_bytes(const poetx_rope* r) {
   if (!r || !rope_ok(r)) return 0;
-  return align_up((size_t)(kCtasPerSm * sm_count() + 2) * r->head_dim * sizeof(float), 256);
+  return align_up((size_t)(kMostCtas * sm_count() + 2) * r->head_dim * sizeof(float), 256);
 }
 
 extern "C" poetx_status poetx_qk_rope_bwd(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, int N,
