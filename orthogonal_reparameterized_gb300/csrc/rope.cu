@@ -11,7 +11,7 @@
 // pair, their angle and their gamma are in one lane's registers whatever the pairing.  All heads of a token
 // use the same angles: a lane makes those of its CH pairs once per token and keeps them over the heads,
 // multiplied by gamma where that saves instructions.  What is in flight waits in shared memory: each
-// thread copies the chunks of its own next heads there asynchronously (160 or 256 bytes ahead) and is the only one
+// thread copies the chunks of its own next heads there asynchronously (two ahead) and is the only one
 // to read them, so that no barrier is needed.
 //
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
@@ -28,9 +28,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = 256;   // pairs of a head
-// By the pairs of a lane, CH: resident CTAs (by registers), and bytes of input that a thread has in flight.
-constexpr int ctas_per_sm(int CH, bool both) { return (CH == 8 ? 3 : 4) - both; }
-constexpr int lead(int CH) { return CH == 8 ? 256 : 160; }
+constexpr int ctas_per_sm(int CH, bool both) { return (CH == 8 ? 3 : 4) - both; }  // (by registers)
+// Items that a thread has in flight.  (More are slower: eight, with 8192 x 40 heads of 128, 35.2 us instead of
+// 33.7 forward, four instead of two backward 48 us instead of 45.)
+constexpr int kSlots = 2;
 constexpr int kMostCtas = 3;  // per SM with dgamma's partial sums
 constexpr int kMaxAxes = 8;
 
@@ -190,7 +191,6 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
   using C = Chunk<T, CH, INTER>;
   constexpr bool BOTH = BWD && NORM;  // both x and dy are read
   constexpr int HEAD = C::BYTES * kThreads, SLOT = (BOTH ? 2 : 1) * HEAD;
-  constexpr int SLOTS = lead(CH) * kThreads / SLOT;
   constexpr int N2 = CH / 2;
   // [slot][array][unit][thread], then each warp's cosines and sines of its token [half]
   extern __shared__ __align__(16) char ring[];
@@ -214,7 +214,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
   const int far = rot ? a.half : dh / 2 - a.half, ahead_by = HW * dh;
   const uint32_t ring_at = smem_u32(ring) + t * C::UNIT;
   char* const my_ring = ring + t * C::UNIT;
-  float2* const angles = reinterpret_cast<float2*>(ring + lead(CH) * kThreads) + warp * a.half;
+  float2* const angles = reinterpret_cast<float2*>(ring + kSlots * SLOT) + warp * a.half;
 
   const T* const in0 = static_cast<const T*>(BWD && !NORM ? s.dy : s.x);
   const T* const in1 = BOTH ? static_cast<const T*>(s.dy) : nullptr;
@@ -254,13 +254,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
     copy_commit();
   };
 #pragma unroll 1
-  for (int i = 0; i < SLOTS; ++i) fetch(i);
+  for (int i = 0; i < kSlots; ++i) fetch(i);
   if (t < a.half) {
     turn[t] = turns_of(freq);
     ax[t] = isfinite(freq) && axis >= 0 && axis < a.axes ? axis : -1;
   }
   if (!mine)  // lanes beyond the head's width: zeros in the sums
-    for (int i = 0; i < lead(CH) / C::UNIT; ++i) {
+    for (int i = 0; i < kSlots * SLOT / (kThreads * C::UNIT); ++i) {
       if (C::UNIT == 8) *reinterpret_cast<uint2*>(my_ring + i * kThreads * C::UNIT) = make_uint2(0u, 0u);
       else *reinterpret_cast<uint4*>(my_ring + i * kThreads * C::UNIT) = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
         }
       }
     }
-    copy_wait<SLOTS - 1>();
+    copy_wait<kSlots - 1>();
     float2 xa[N2], xb[N2];  // x (backward without the norm: dy)
     float2 da[N2], db[N2];  // the gradient of the rotated head, then of the normalised one
     {
@@ -429,7 +429,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
       }
       C::store(out, far, da, db);
     }
-    if (++slot == SLOTS) slot = 0;
+    if (++slot == kSlots) slot = 0;
     at.h0 += HW;
     at.p0 += ahead_by;
     fresh = at.h0 >= H;
@@ -501,12 +501,14 @@ bool rope_ok(const poetx_rope* r) {
   return r->head_dim <= (wide ? 512 : 256) && r->axes >= 1 && r->axes <= kMaxAxes;
 }
 
-constexpr int rope_smem(int CH, int half) {
-  return lead(CH) * kThreads + kWarps * half * (int)sizeof(float2);
+constexpr int rope_smem(int esz, int CH, bool both, int half) {
+  const int ring = kSlots * (both ? 2 : 1) * 2 * CH * esz * kThreads, red = both ? kWarps * 2 * CH * 32 * 4 : 0;
+  return (ring > red ? ring : red) + kWarps * half * (int)sizeof(float2);
 }
 // CTAs that an SM holds: by the kernels' registers, and by shared memory (with 5 KB of tables each).
-int rope_ctas(int CH, bool both, int half) {
-  const int by_smem = 227 * 1024 / (rope_smem(CH, half) + 6 * 1024), by_regs = ctas_per_sm(CH, both);
+int rope_ctas(int esz, int CH, bool both, int half) {
+  const int by_smem = 227 * 1024 / (rope_smem(esz, CH, both, half) + 6 * 1024);
+  const int by_regs = ctas_per_sm(CH, both);
   return by_smem < by_regs ? by_smem : by_regs;
 }
 
@@ -516,10 +518,11 @@ cudaError_t rope_launch1(const RopeArgs& a, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rope_smem(CH, kMaxHalf));
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rope_smem(sizeof(T), CH, BWD && NORM, kMaxHalf));
   });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), rope_smem(CH, a.half), s, a);
+  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), rope_smem(sizeof(T), CH, BWD && NORM, a.half), s,
+                    a);
 }
 template <typename T, int CH, bool BWD>
 cudaError_t rope_launch(const RopeArgs& a, bool inter, bool norm, cudaStream_t s) {
@@ -584,7 +587,7 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
   a.eps = r->eps;
   a.G = 1;
   while (a.G * 2 * CH < a.dh) a.G *= 2;
-  const int max_ctas = rope_ctas(CH, BWD && r->norm, a.half) * sm_count();
+  const int max_ctas = rope_ctas((int)dtype_size(dt), CH, BWD && r->norm, a.half) * sm_count();
   const int heads = (q ? q->heads : 0) + (k ? k->heads : 0);
   float* part = static_cast<float*>(ws);
   RopeSum rs{};
