@@ -611,7 +611,7 @@ typedef struct poetx_rope {
 /* One side of a call (queries or keys): `heads` heads of every token, a token's rows one after the
  * other, tokens `*pitch` elements apart (a multiple of 8, at least heads * head_dim). */
 typedef struct poetx_heads {
-  int heads;             /* 0: no such side */
+  int heads;             /* 0: no such side; heads * head_dim <= 2^30 */
   const void* x;         /* input of the forward (backward without the norm: unused) */
   long long x_pitch;
   const float* gamma;    /* [head_dim] fp32 (nullable: 1; used with norm) */
@@ -619,7 +619,8 @@ typedef struct poetx_heads {
   long long dy_pitch;
   void* y;               /* forward: the output; backward: the gradient of x */
   long long y_pitch;
-  float* dgamma;         /* backward, with norm: [head_dim] fp32 (nullable) */
+  float* dgamma;         /* backward, with norm: [head_dim] fp32 (nullable; both sides may name the same
+                            array, whose gradient is then the sum) */
 } poetx_heads;
 
 /* Forward for queries and keys in one launch.  pos [axes, N] int32 (pos, inv_freq and axis need no more

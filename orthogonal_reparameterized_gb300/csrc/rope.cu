@@ -549,6 +549,7 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
     if (h->heads == 0) continue;
     any = true;
     const long long row = (long long)h->heads * r->head_dim;
+    if (row > (1ll << 30)) return POETX_ERR_SHAPE;
     const bool reads_x = !BWD || r->norm;
     if ((reads_x && (h->x_pitch < row || h->x_pitch % 8)) || h->y_pitch < row || h->y_pitch % 8 ||
         (BWD && (h->dy_pitch < row || h->dy_pitch % 8)))
@@ -619,6 +620,10 @@ poetx_status rope_run(const poetx_rope* r, poetx_dtype dt, const int32_t* pos, i
       rs.out[i] = h->dgamma;
       part += (size_t)s.ctas * a.dh;
     }
+  }
+  if (rs.out[0] && rs.out[0] == rs.out[1]) {  // one gamma for both: k's partial sums follow q's
+    rs.ctas[0] += rs.ctas[1];
+    rs.out[1] = nullptr;
   }
   const bool inter = r->interleaved != 0, norm = r->norm != 0;
   cudaError_t e;

@@ -124,7 +124,8 @@ ROPE = [(dict(N=-1), ARG), (dict(dt=2), DTYPE), (dict(q=False, k=False), ARG), (
         (dict(side=dict(x_pitch=260)), SHAPE), (dict(side=dict(y_pitch=255)), SHAPE),
         (dict(side=dict(x=None)), ARG), (dict(side=dict(y=None)), ARG), (dict(side=dict(x=ODD)), ALIGN),
         (dict(side=dict(y=ODD)), ALIGN), (dict(side=dict(gamma=ODD)), ALIGN),
-        (dict(side=dict(heads=0)), 0)]
+        (dict(side=dict(heads=0)), 0),
+        (dict(side=dict(heads=1 << 25, x_pitch=1 << 31, y_pitch=1 << 31, dy_pitch=1 << 31)), SHAPE)]
 
 
 @pytest.mark.parametrize("kw,st", ROPE + [(dict(N=0), 0)])

@@ -147,6 +147,23 @@ def test_rope_one_side_and_options(P):
     assert not acc.any()
 
 
+def test_rope_shared_gamma(P):
+    """One gamma for queries and keys: its gradient is the sum of both sides'."""
+    N, dh = 90, 96
+    c = _case(N, 6, 2, dh, dh, 1, "f32", 8)
+    c["gk"] = c["gq"]
+    _, dg = _check(P, c, "f32", dh)
+    pos, freq = dev(c["pos"], torch.int32), dev(c["freq"], torch.float32)
+    t = {k: c[k].to(DEV) for k in ("q", "k", "dq", "dk")}
+    for acc in (False, True):
+        both = torch.full((dh,), 0.5, device=DEV)
+        P.poetx_qk_rope_bwd(t["q"], t["k"], t["dq"], t["dk"], pos, freq, torch.empty_like(t["q"]),
+                            torch.empty_like(t["k"]), dgamma_q=both, dgamma_k=both, accumulate=acc,
+                            **_opt(c, False, True, True, dh))
+        ref = dg["q"] + dg["k"] + (0.5 if acc else 0.0)
+        assert (both - ref).abs().max() <= TOL_F32 * float(ref.abs().max() + 1) * 4
+
+
 def test_rope_nan_stays_in_its_head_and_bad_axis_in_its_pair(P):
     N, dh = 20, 64
     c = _case(N, 3, 1, dh, 32, 2, "f32", 6)
