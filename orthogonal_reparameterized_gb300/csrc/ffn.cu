@@ -24,6 +24,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pieces.cuh"
 
 namespace poetx {
 
@@ -113,10 +114,10 @@ __device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-// What is left of v after its rounding to bf16, which is v's first piece.
-__device__ __forceinline__ void rest8(float (&v)[8]) {
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] -= __bfloat162float(__float2bfloat16_rn(v[i]));
+// What is left of v after its rounding to bf16, which is v's first piece (nothing, where that is not finite).
+__device__ __forceinline__ float rest_of(float v, __nv_bfloat16 first) {
+  const float f = __bfloat162float(first);
+  return isfinite(f) ? v - f : 0.f;
 }
 
 // What the elementwise kernels read and write, in vectors of eight elements: vector i lies in row i / vpr
@@ -171,14 +172,12 @@ __global__ void __launch_bounds__(kGluThreads) glu_fwd_kernel(const GluArgs p) {
   }
 }
 
-// PIECES 0: dg and du of type T.  Otherwise they are dz's 1 to 3 bf16 pieces.
+// PIECES 0: dg and du of type T.  Otherwise they are dz's 2 or 3 bf16 pieces.  The share of thread `t` of
+// `step`.
 template <typename T, int PIECES>
-__global__ void __launch_bounds__(kGluThreads) glu_bwd_kernel(const GluArgs p) {
-  pdl_trigger();
-  pdl_wait();
+__device__ __forceinline__ void glu_bwd_share(const GluArgs& p, long long t, long long step) {
   constexpr int U = 2;
-  const long long step = (long long)gridDim.x * kGluThreads;
-  for (long long i0 = (long long)blockIdx.x * kGluThreads + threadIdx.x; i0 < p.vecs; i0 += U * step) {
+  for (long long i0 = t; i0 < p.vecs; i0 += U * step) {
     Eight<T> g[U], u[U], d[U];
     uint32_t row[U];
 #pragma unroll
@@ -210,24 +209,39 @@ __global__ void __launch_bounds__(kGluThreads) glu_bwd_kernel(const GluArgs p) {
       if constexpr (PIECES == 0) {
         put8(static_cast<T*>(p.a) + at, x);
         put8(static_cast<T*>(p.b) + at, y);
-      } else {
+      } else if constexpr (PIECES == 2) {
         put8(static_cast<__nv_bfloat16*>(p.a) + at, x);
         put8(static_cast<__nv_bfloat16*>(p.b) + at, y);
-        if constexpr (PIECES > 1) {
-          rest8(x);
-          rest8(y);
-          put8(static_cast<__nv_bfloat16*>(p.a2) + at, x);
-          put8(static_cast<__nv_bfloat16*>(p.b2) + at, y);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          x[j] = rest_of(x[j], __float2bfloat16_rn(x[j]));
+          y[j] = rest_of(y[j], __float2bfloat16_rn(y[j]));
         }
-        if constexpr (PIECES > 2) {
-          rest8(x);
-          rest8(y);
-          put8(static_cast<__nv_bfloat16*>(p.a3) + at, x);
-          put8(static_cast<__nv_bfloat16*>(p.b3) + at, y);
+        put8(static_cast<__nv_bfloat16*>(p.a2) + at, x);
+        put8(static_cast<__nv_bfloat16*>(p.b2) + at, y);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; j += 4) {
+          __nv_bfloat16* const da[3] = {static_cast<__nv_bfloat16*>(p.a) + at + j,
+                                        static_cast<__nv_bfloat16*>(p.a2) + at + j,
+                                        static_cast<__nv_bfloat16*>(p.a3) + at + j};
+          __nv_bfloat16* const db[3] = {static_cast<__nv_bfloat16*>(p.b) + at + j,
+                                        static_cast<__nv_bfloat16*>(p.b2) + at + j,
+                                        static_cast<__nv_bfloat16*>(p.b3) + at + j};
+          store3(make_float4(x[j], x[j + 1], x[j + 2], x[j + 3]), da);
+          store3(make_float4(y[j], y[j + 1], y[j + 2], y[j + 3]), db);
         }
       }
     }
   }
+}
+
+template <typename T, int PIECES>
+__global__ void __launch_bounds__(kGluThreads) glu_bwd_kernel(const GluArgs p) {
+  pdl_trigger();
+  pdl_wait();
+  glu_bwd_share<T, PIECES>(p, (long long)blockIdx.x * kGluThreads + threadIdx.x,
+                           (long long)gridDim.x * kGluThreads);
 }
 
 // ---------------------------------------------------------------- the projections
@@ -749,8 +763,8 @@ __global__ void __launch_bounds__(score_threads(NT), 1)
       p.z[at] = a;
       p.z[at + p.F] = b;
       if (p.dh) {
-        p.z2[at] = __float2bfloat16_rn(o.x - __bfloat162float(a));
-        p.z2[at + p.F] = __float2bfloat16_rn(o.y - __bfloat162float(b));
+        p.z2[at] = __float2bfloat16_rn(rest_of(o.x, a));
+        p.z2[at + p.F] = __float2bfloat16_rn(rest_of(o.y, b));
       }
     };
     // the values that a thread makes of 16 tokens, token << 8 | feature: all tokens of its own feature, or
@@ -1187,11 +1201,11 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   uint8_t* w = static_cast<uint8_t*>(ws);
   const uint8_t *xp = static_cast<const uint8_t*>(x), *wp = static_cast<const uint8_t*>(W);
   if (pl.f32) {
+    xp = w + pl.xs;
+    wp = w + pl.ws;
     POETX_TRY(split_pieces(static_cast<const float*>(x), (long long)N * D, w + pl.xs,
                            piece_step((size_t)N * D), static_cast<const float*>(W), 2ll * F * D, w + pl.ws,
                            piece_step((size_t)2 * F * D), stream));
-    xp = w + pl.xs;
-    wp = w + pl.ws;
   }
   const int pieces = pl.f32 ? 3 : (pl.fine ? 2 : 1);
   if (pl.direct) {

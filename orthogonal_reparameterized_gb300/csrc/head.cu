@@ -36,6 +36,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pieces.cuh"
 
 namespace poetx {
 
@@ -1048,51 +1049,6 @@ __device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
                     pack_bf16x2(v[6], v[7]));
 }
 
-// Three bf16 pieces of v, whose sum it is.  An infinity or NaN goes into the third with zeros before it:
-// the products take the third piece with the other operand's first alone, so that it meets each number
-// once, with that number's own sign (inf - inf in the split and inf times a rest of either sign would make
-// NaN of a plain infinity).  A finite value that would round to infinity is cut off at bf16's largest.
-constexpr float kBf16Max = 0x1.fep127f;
-template <bool CHECK = true>
-__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
-  o[0] = __float2bfloat16_rn(v);
-  if (CHECK && !(fabsf(v) <= kBf16Max)) {
-    if (!isfinite(v)) {
-      o[0] = o[1] = __float2bfloat16_rn(0.f);
-      o[2] = __float2bfloat16_rn(v);
-      return;
-    }
-    o[0] = __float2bfloat16_rz(v);
-  }
-  v -= __bfloat162float(o[0]);
-  o[1] = __float2bfloat16_rn(v);
-  v -= __bfloat162float(o[1]);
-  o[2] = __float2bfloat16_rn(v);
-}
-
-// The pieces of four neighbouring values, to d[0], d[1] and d[2].
-__device__ __forceinline__ void store3(float4 w, __nv_bfloat16* const (&d)[3]) {
-  __nv_bfloat16 o[4][3];
-  if (fabsf(w.x) + fabsf(w.y) + fabsf(w.z) + fabsf(w.w) <= kBf16Max) {  // (false for a NaN)
-    split3<false>(w.x, o[0]);
-    split3<false>(w.y, o[1]);
-    split3<false>(w.z, o[2]);
-    split3<false>(w.w, o[3]);
-  } else {
-    split3(w.x, o[0]);
-    split3(w.y, o[1]);
-    split3(w.z, o[2]);
-    split3(w.w, o[3]);
-  }
-#pragma unroll
-  for (int k = 0; k < 3; ++k) {
-    const __nv_bfloat162 lo = __halves2bfloat162(o[0][k], o[1][k]);
-    const __nv_bfloat162 hi = __halves2bfloat162(o[2][k], o[3][k]);
-    *reinterpret_cast<uint2*>(d[k]) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
-                                                 *reinterpret_cast<const uint32_t*>(&hi));
-  }
-}
-
 // One CTA per row: joins the groups, writes loss and lse and turns e into dz.  Bound by HBM: a row of
 // e read and written (4096 x 32000: 524 MB in 85 us, 6.2 TB/s; 8192 x 128256: 0.64 ms, 6.6 TB/s).
 // Where there are few rows, several CTAs share one: each joins the groups again and turns its columns.
@@ -1328,37 +1284,12 @@ __global__ void __launch_bounds__(kRowThreads, 5) head_row_kernel(const RowArgs 
   }
 }
 
-// The three bf16 pieces of two fp32 arrays (of quads * 4 values; the second may be empty).  Bound by
-// HBM: 4 bytes in, 6 out (8000 x 1024 and 512 x 1024: 87 MB in 16 us).
-struct SplitArray {
-  const float4* src;
-  long long quads;
-  __nv_bfloat16* dst[3];
-};
+// The three bf16 pieces of two fp32 arrays.  Bound by HBM: 4 bytes in, 6 out (8000 x 1024 and 512 x 1024:
+// 87 MB in 16 us).
 __global__ void __launch_bounds__(256) head_split_kernel(const SplitArray a, const SplitArray b) {
   pdl_trigger();
   pdl_wait();
-  constexpr int U = 4;  // loads in flight per thread
-  const long long step = (long long)gridDim.x * blockDim.x, n = a.quads + b.quads;
-  for (long long i0 = (long long)blockIdx.x * blockDim.x + threadIdx.x; i0 < n; i0 += U * step) {
-    float4 w[U];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const long long i = i0 + k * step;
-      if (i < n) w[k] = i < a.quads ? a.src[i] : b.src[i - a.quads];
-    }
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      const long long i = i0 + k * step;
-      if (i >= n) break;
-      const bool first = i < a.quads;
-      const long long at = 4 * (first ? i : i - a.quads);
-      __nv_bfloat16* d[3];
-#pragma unroll
-      for (int j = 0; j < 3; ++j) d[j] = (first ? a.dst[j] : b.dst[j]) + at;
-      store3(w[k], d);
-    }
-  }
+  split_arrays(a, b, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
 
 // out = sum over S fp32 partials of `stride` elements each, in order (count a multiple of 4).  The
@@ -1636,12 +1567,6 @@ struct HeadCall {
   void* ws;
   size_t ws_bytes;
 };
-
-SplitArray split_of(const float* src, long long count, uint8_t* dst, size_t step) {
-  SplitArray a{reinterpret_cast<const float4*>(src), count / 4, {}};
-  for (int j = 0; j < 3; ++j) a.dst[j] = reinterpret_cast<__nv_bfloat16*>(dst + j * step);
-  return a;
-}
 
 }  // namespace
 

@@ -1,0 +1,91 @@
+// fp32 values as three bf16 pieces, whose products on the tensor cores keep fp32's accuracy.
+#pragma once
+
+#include "common.cuh"
+
+namespace poetx {
+
+// Three bf16 pieces of v, whose sum it is.  An infinity or NaN goes into the third with zeros before it:
+// the products take the third piece with the other operand's first alone, so that it meets each number
+// once, with that number's own sign (inf - inf in the split and inf times a rest of either sign would make
+// NaN of a plain infinity).  A finite value that would round to infinity is cut off at bf16's largest.
+constexpr float kBf16Max = 0x1.fep127f;
+template <bool CHECK = true>
+__device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
+  o[0] = __float2bfloat16_rn(v);
+  if (CHECK && !(fabsf(v) <= kBf16Max)) {
+    if (!isfinite(v)) {
+      o[0] = o[1] = __float2bfloat16_rn(0.f);
+      o[2] = __float2bfloat16_rn(v);
+      return;
+    }
+    o[0] = __float2bfloat16_rz(v);
+  }
+  v -= __bfloat162float(o[0]);
+  o[1] = __float2bfloat16_rn(v);
+  v -= __bfloat162float(o[1]);
+  o[2] = __float2bfloat16_rn(v);
+}
+
+// The pieces of four neighbouring values, to d[0], d[1] and d[2].
+__device__ __forceinline__ void store3(float4 w, __nv_bfloat16* const (&d)[3]) {
+  __nv_bfloat16 o[4][3];
+  if (fabsf(w.x) + fabsf(w.y) + fabsf(w.z) + fabsf(w.w) <= kBf16Max) {  // (false for a NaN)
+    split3<false>(w.x, o[0]);
+    split3<false>(w.y, o[1]);
+    split3<false>(w.z, o[2]);
+    split3<false>(w.w, o[3]);
+  } else {
+    split3(w.x, o[0]);
+    split3(w.y, o[1]);
+    split3(w.z, o[2]);
+    split3(w.w, o[3]);
+  }
+#pragma unroll
+  for (int k = 0; k < 3; ++k) {
+    const __nv_bfloat162 lo = __halves2bfloat162(o[0][k], o[1][k]);
+    const __nv_bfloat162 hi = __halves2bfloat162(o[2][k], o[3][k]);
+    *reinterpret_cast<uint2*>(d[k]) = make_uint2(*reinterpret_cast<const uint32_t*>(&lo),
+                                                 *reinterpret_cast<const uint32_t*>(&hi));
+  }
+}
+
+// Two fp32 arrays (of quads * 4 values; the second may be empty) and where their pieces go.
+struct SplitArray {
+  const float4* src;
+  long long quads;
+  __nv_bfloat16* dst[3];
+};
+inline SplitArray split_of(const float* src, long long count, uint8_t* dst, size_t step) {
+  SplitArray a{reinterpret_cast<const float4*>(src), count / 4, {}};
+  for (int j = 0; j < 3; ++j) a.dst[j] = reinterpret_cast<__nv_bfloat16*>(dst + j * step);
+  return a;
+}
+
+// The pieces of both arrays, the share of thread `t` of `step`.
+__device__ __forceinline__ void split_arrays(const SplitArray& a, const SplitArray& b, long long t,
+                                             long long step) {
+  constexpr int U = 4;  // loads in flight per thread
+  const long long n = a.quads + b.quads;
+  for (long long i0 = t; i0 < n; i0 += U * step) {
+    float4 w[U];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const long long i = i0 + k * step;
+      if (i < n) w[k] = i < a.quads ? a.src[i] : b.src[i - a.quads];
+    }
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      const long long i = i0 + k * step;
+      if (i >= n) break;
+      const bool first = i < a.quads;
+      const long long at = 4 * (first ? i : i - a.quads);
+      __nv_bfloat16* d[3];
+#pragma unroll
+      for (int j = 0; j < 3; ++j) d[j] = (first ? a.dst[j] : b.dst[j]) + at;
+      store3(w[k], d);
+    }
+  }
+}
+
+}  // namespace poetx

@@ -165,6 +165,27 @@ def test_ffn_rows_on_their_own(P, dt):
             assert torch.equal(got[k][keep], ref[k][keep]), k
 
 
+@pytest.mark.parametrize("N,dt", [(40, "bf16"), (200, "bf16"), (40, "f32"), (200, "f32")])
+def test_ffn_infinite_upstream(P, N, dt):
+    """An infinite upstream gradient makes dz infinite in its feature: dx there is infinite or NaN as IEEE sums
+    are, dW's two rows infinite (one row of x meets it), and no other row of dx or dW sees it."""
+    x, W, dh = _ffn_inputs(N, 72, 64, dt, 11)
+    ref = _run(P, x, W, dh, B.SILU, True)
+    dh[5, 9] = float("inf")
+    got = _run(P, x, W, dh, B.SILU, True)
+    keep = [i for i in range(N) if i != 5]
+    rows = [i for i in range(128) if i not in (9, 73)]
+    assert torch.equal(got["dx"][keep], ref["dx"][keep]) and torch.equal(got["dW"][rows], ref["dW"][rows])
+    z = host(got["z"])
+    dz = B.glu_bwd(z[:, :64], z[:, 64:], host(dh), B.SILU)
+    with np.errstate(invalid="ignore"):
+        dx = dz[0][5, 9] * host(W)[9] + dz[1][5, 9] * host(W)[73]
+        dW = [d[5, 9] * host(x)[5] for d in dz]
+    assert np.array_equal(host(got["dx"][5]), dx, equal_nan=True)
+    for r, w in zip((9, 73), dW):
+        assert np.array_equal(host(got["dW"][r]), w, equal_nan=True)
+
+
 def test_ffn_empty_batch(P):
     W = torch.randn(48, 64, device=DEV).bfloat16()
     x, h = torch.empty(0, 64, device=DEV).bfloat16(), torch.empty(0, 24, device=DEV).bfloat16()
