@@ -9,7 +9,7 @@
 // of W (the even CTA's half of the B operand) beside the 128 value rows of the same features (the odd
 // CTA's), so that a row of the accumulator holds both g and u of its features and the epilogue forms h
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
-// kept z, or from z computed again), then the two products of the linear head's gradients (head.cu), for
+// kept z, or in the epilogue of the same product run again), then the two products of the linear head's gradients (head.cu), for
 // which dz is what that head's is.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
@@ -17,6 +17,10 @@
 // registers and is added there with IEEE adds: every 4096 of K in bf16 (256 adds, 1.5e-5, against the
 // result's 2^-9); fp32 operands are split into three bf16 pieces, the six pairs of pieces above 2^-24
 // multiplied, 256 of K per accumulator.
+//
+// Forward 8192 x 4096 x 14336 with z: 1.13-1.16 ms (1.66-1.70 PFLOP/s in a run of calls, at the board's power;
+// tensor pipe 89 %).  One row of 4096 x 14336: 235 MB of W in 38-39 us (6.1 TB/s).  Backward 4096 x 2048 x
+// 8192 from kept z: dz 46 us (335 MB, 7.3 TB/s), products 299 us (1.84 PFLOP/s).
 //
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, drains its own
 // copies, frees its TMEM and returns.
@@ -305,6 +309,7 @@ __device__ __forceinline__ void tile_at(const FfnGemm& p, int t, int* mi, int* f
   *fi = q / width;
 }
 
+// Bands of 16 row tiles as in the head's products; five stages of 32 KB leave room for two boxes a warp.
 // Warp 0 of each CTA loads its 128 rows of x and its 128 rows of W, one thread of the even CTA's warp 1
 // issues the MMAs, warps 2-9 read the accumulators back (warp w: rows 32 (w % 4).. of the CTA's 128,
 // features 64 ((w - 2) / 4).. of the tile's 128: their gates and their values).

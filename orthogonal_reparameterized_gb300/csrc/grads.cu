@@ -8,6 +8,8 @@
 // tensors, laid end to end in units of 16 bytes of gradient, are cut into equal shares, one per resident
 // CTA: found by one binary search, then followed from tensor to tensor, so that many small tensors and few
 // large ones cost the same and no CTA is left with a last round of its own.  Every sum has a fixed order.
+// Norm of 0.92 GB in 226 tensors: 138 us (6.6 TB/s).  Step of 11.2 M parameters in 14 tensors: 44 us; of
+// 360 M in 448, with the norm before it, 1.63 ms (11.5 GB at 7.0 TB/s).
 //
 #include <algorithm>
 #include <mutex>

@@ -14,6 +14,10 @@
 // thread copies the chunks of its own next heads there asynchronously (two ahead) and is the only one
 // to read them, so that no barrier is needed.
 //
+// 8192 x (32 + 8) heads of 128 in bf16: 168 MB in 33.9 us (5.0 TB/s; without the norm 29.6), 4096 in fp32 the same
+// bytes in 29.9 us; backward 4096 x (40 + 40) heads 252 MB in 45.4 us (5.5 TB/s).  What bounds it above HBM is
+// issue and latency: some 220 instructions per warp and four heads, 0.55 issued per cycle and quarter of an SM.
+//
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
 // turn), pos * f modulo 2^64 is the angle modulo a turn, exact to 2^-32 turns at any int32 position (an
 // fp32 product of position and frequency has lost the angle's second decimal at position 100000).
