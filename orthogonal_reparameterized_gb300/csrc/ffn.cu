@@ -15,7 +15,7 @@
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
 // registers and is added there with IEEE adds: every 4096 of K in bf16 (256 adds, 1.5e-5, against the
-// result's 2^-9); fp32 operands are split into three bf16 pieces, the six pairs of pieces above 2^-24
+// result's 2^-8); fp32 operands are split into three bf16 pieces, the six pairs of pieces above 2^-24
 // multiplied, 256 of K per accumulator.
 //
 // Forward 8192 x 4096 x 14336 with z: 1.13-1.16 ms (1.66-1.70 PFLOP/s in a run of calls, at the board's power;
@@ -49,7 +49,7 @@ Act act_of(poetx_activation a) {
 bool act_ok(poetx_activation a) { return a == POETX_SILU || a == POETX_GELU; }
 
 // s(t).  EXACT: for fp32 results.  Otherwise the hardware's exp2 and reciprocal, each within 2^-22; the
-// argument's rounding costs |t| 2^-24 besides (exp(-t) at t = -80: 5e-6), all far below bf16's 2^-9.
+// argument's rounding costs |t| 2^-24 besides (exp(-t) at t = -80: 5e-6), all far below bf16's 2^-8.
 template <bool EXACT>
 __device__ __forceinline__ float logistic(float t) {
   if (EXACT) return 1.f / (1.f + expf(-t));
