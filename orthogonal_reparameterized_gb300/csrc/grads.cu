@@ -286,6 +286,8 @@ __global__ void __launch_bounds__(kThreads, 4)
   });
 }
 
+bool aligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
 // The checks of n tensors' host arrays (ARRAYS of pointers): POETX_OK, or what is wrong.
 template <int ARRAYS>
 poetx_status check_arrays(void* const* const (&p)[ARRAYS], const poetx_dtype* dt, const long long* count,
@@ -369,7 +371,7 @@ extern "C" poetx_status poetx_grad_norm(const void* const* g, const poetx_dtype*
   if (n > 0 && !dt) return POETX_ERR_ARG;
   POETX_TRY(check_arrays(p, dt, count, n));
   if (!norm || !ws) return POETX_ERR_ARG;
-  if (!aligned16(norm) || !aligned16(ws)) return POETX_ERR_ALIGN;
+  if (!aligned4(norm) || !aligned16(ws)) return POETX_ERR_ALIGN;
   if (ws_bytes < poetx_grad_norm_workspace_bytes(n)) return POETX_ERR_WORKSPACE;
   double* part = static_cast<double*>(ws);
   int parts = 0;
@@ -398,7 +400,7 @@ extern "C" poetx_status poetx_grad_clip(void* const* g, const poetx_dtype* dt, c
   if (n > 0 && !dt) return POETX_ERR_ARG;
   POETX_TRY(check_arrays(p, dt, count, n));
   if (!(max_norm >= 0.f) || !norm) return POETX_ERR_ARG;
-  if (!aligned16(norm)) return POETX_ERR_ALIGN;
+  if (!aligned4(norm)) return POETX_ERR_ALIGN;
   auto run = [&](auto kernel, auto max) -> poetx_status {
     Table<decltype(max)::value, 1> t;
     for (int at = 0; next_table(p, dt, count, n, &at, &t);) {
@@ -421,7 +423,7 @@ extern "C" poetx_status poetx_adam_group(float* const* q, const float* const* dq
   void* const* const p[4] = {(void* const*)dq, (void* const*)q, (void* const*)m, (void* const*)v};
   POETX_TRY(check_arrays(p, nullptr, count, n));
   if (norm && !(max_norm >= 0.f)) return POETX_ERR_ARG;
-  if (!aligned16(norm)) return POETX_ERR_ALIGN;
+  if (!aligned4(norm)) return POETX_ERR_ALIGN;
   auto run = [&](auto kernel, auto max) -> poetx_status {
     Table<decltype(max)::value, 4> t;
     for (int at = 0; next_table(p, nullptr, count, n, &at, &t);) {

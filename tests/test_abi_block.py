@@ -155,7 +155,7 @@ def test_many_tensor_refusals(P):
 
     assert norm(k=-1) == norm(g=None) == norm(t=None) == norm(n=None) == ARG
     assert norm(out=None) == norm(ws=None) == ARG
-    assert norm(b=16) == WORKSPACE and norm(out=ODD) == norm(ws=ODD) == ALIGN
+    assert norm(b=16) == WORKSPACE and norm(out=HALF) == norm(ws=ODD) == ALIGN
     assert norm(t=_list(ci, P.F32, P.I8)) == DTYPE
     assert norm(n=_list(ll, 8, -1)) == ARG and norm(n=_list(ll, 8, (1 << 33) + 1)) == SHAPE
     assert norm(g=_list(vp, 4096, 8200)) == ALIGN and norm(g=_list(vp, 4096, None)) == ARG
@@ -164,7 +164,7 @@ def test_many_tensor_refusals(P):
         return lib.poetx_grad_clip(g, t, n, k, m, out, None)
 
     assert clip(m=-1.0) == clip(m=NAN) == clip(out=None) == clip(g=None) == ARG
-    assert clip(out=ODD) == clip(g=_list(vp, 4100, 4096)) == ALIGN
+    assert clip(out=HALF) == clip(g=_list(vp, 4100, 4096)) == ALIGN
     assert clip(k=0) == 0 and clip(n=_list(ll, 0, 0)) == 0
 
     def adam(q=p, g=p, m=p, v=p, n=c, k=2, step=1, limit=1.0, out=OK):
@@ -172,7 +172,7 @@ def test_many_tensor_refusals(P):
         return lib.poetx_adam_group(q, g, m, v, n, k, ctypes.byref(hp), limit, out, None)
 
     assert adam(step=0) == adam(q=None) == adam(v=None) == adam(n=None) == adam(k=-1) == ARG
-    assert adam(limit=-1.0) == ARG and adam(out=ODD) == ALIGN
+    assert adam(limit=-1.0) == ARG and adam(out=HALF) == ALIGN
     assert adam(m=_list(vp, 4096, 4100)) == ALIGN and adam(k=0) == 0
     assert lib.poetx_adam_group(p, p, p, p, c, 2, None, 1.0, None, None) == ARG
     assert P.poetx_grad_norm_workspace_bytes(-1) == 0

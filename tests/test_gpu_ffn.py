@@ -97,7 +97,9 @@ def _run(P, x, W, dh, act, kept, dx=True, dW=True, keep_z=True, **kw):
 
 SHAPES = [(1, 8, 8), (2, 64, 128), (5, 72, 40), (16, 256, 1000), (17, 264, 2056), (40, 192, 136),
           (65, 128, 4096), (128, 520, 808), (129, 64, 64), (256, 136, 520), (300, 512, 1416),
-          (257, 1032, 264), (1021, 328, 648)]
+          (257, 1032, 264), (1021, 328, 648),
+          # beyond the few-row kernel's width; more features than SMs times 128; several accumulators' K
+          (3, 16456, 16), (2, 64, 20000), (70, 72, 20008), (200, 4168, 136)]
 
 
 @pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])

@@ -32,7 +32,7 @@ def _norm(P, ts, **kw):
 
 
 SIZES = [[1], [7, 3], [0, 5, 0], [4096, 4097, 8191], [8192, 8193, 40000, 3], [1000003, 77, 500000],
-         list(range(1, 700))]
+         list(range(1, 700)), [5] * 48, [9] * 49, [3] * 512, [6] * 513]
 
 
 @pytest.mark.parametrize("sizes", SIZES, ids=lambda s: f"{len(s)}x{max(s)}")
@@ -42,6 +42,19 @@ def test_norm(P, sizes):
     ref = B.grad_norm([host(t) for t in ts])
     assert abs(float(got) - ref) <= 2.0 ** -18 * ref
     assert torch.equal(got, again)
+
+
+def test_norms_in_one_array(P):
+    """A norm per group of tensors, side by side."""
+    ts = [t.to(DEV) for t in _grads([100, 5000, 77], 3)]
+    norms = torch.zeros(5, device=DEV)
+    for i, t in enumerate(ts):
+        P.poetx_grad_norm([t], norms[i + 1:i + 2])
+    ref = [B.grad_norm([host(t)]) for t in ts]
+    assert np.abs(host(norms)[1:4] / ref - 1).max() <= 2.0 ** -18
+    assert float(norms[0]) == 0 and float(norms[4]) == 0
+    P.poetx_grad_clip(ts[:1], norms[1:2], 0.5 * ref[0])
+    assert abs(float(_norm(P, ts[:1])) / (0.5 * ref[0]) - 1) <= 1e-5
 
 
 def test_norm_of_nothing(P):
@@ -117,7 +130,8 @@ HP = dict(step=3, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-8, weight_decay=0.01)
 
 
 @pytest.mark.parametrize("sizes", [[1], [7, 0, 1001], [4096 * 3, 4095, 4097], [500000, 9],
-                                   list(range(1, 600))], ids=lambda s: f"{len(s)}x{max(s)}")
+                                   list(range(1, 600)), [5] * 48, [9] * 49, [3] * 512, [6] * 513],
+                         ids=lambda s: f"{len(s)}x{max(s)}")
 def test_adam_group(P, sizes):
     s = _state(sizes, len(sizes))
     a, b, c = ({k: [t.to(DEV) for t in ts] for k, ts in s.items()} for _ in range(3))
