@@ -8,6 +8,7 @@ if the library is missing, loading fails loudly.
 from __future__ import annotations
 
 import ctypes
+import operator
 import os
 import threading
 from array import array
@@ -841,16 +842,18 @@ def poetx_qk_rope_bwd(q, k, dq, dk, pos, inv_freq, dq_in, dk_in, rot_dim=None, a
 # ---------------------------------------------------------------- many tensors
 _GRAD_TYPES = {torch.float32, torch.bfloat16}
 _FP32 = {torch.float32}
+_dtype_of = operator.attrgetter("dtype")
 
 
-def _arrays(fn, what, ts, dtypes, types):
-    """The tensors' addresses as an array for the library (maps: hundreds of tensors cost the host as
-    much as the kernels)."""
-    if not types.issuperset(dtypes) or not all(map(torch.Tensor.is_contiguous, ts)) or \
+def _arrays(fn, what, ts, types):
+    """(the tensors' addresses as an array for the library, the set of their types).  Maps: with hundreds of
+    tensors the host's work is as long as the kernels'."""
+    found = set(map(_dtype_of, ts))
+    if found - types or not all(map(torch.Tensor.is_contiguous, ts)) or \
             set(map(torch.Tensor.get_device, ts)) - {torch._C._cuda_getDevice()}:
         raise ValueError(f"{fn}: {what} must be contiguous tensors on the current CUDA device, of "
                          f"{' or '.join(map(str, types))}")
-    return array("Q", map(torch.Tensor.data_ptr, ts))
+    return array("Q", map(torch.Tensor.data_ptr, ts)), found
 
 
 def _at(a):
@@ -858,10 +861,14 @@ def _at(a):
 
 
 def _gradients(fn, grads):
-    dtypes = [t.dtype for t in grads]
-    p = _arrays(fn, "gradients", grads, dtypes, _GRAD_TYPES)
-    return (p, array("i", map(_DT.__getitem__, dtypes)),
-            array("q", map(torch.Tensor.numel, grads)))
+    if not isinstance(grads, (list, tuple)):
+        grads = list(grads)  # (gone through several times)
+    p, found = _arrays(fn, "gradients", grads, _GRAD_TYPES)
+    if len(found) == 1:
+        codes = array("i", [_DT[found.pop()]]) * len(grads)
+    else:
+        codes = array("i", [_DT[t.dtype] for t in grads])
+    return p, codes, array("q", map(torch.Tensor.numel, grads))
 
 
 def poetx_grad_norm_workspace_bytes(n: int) -> int:
@@ -910,7 +917,7 @@ def poetx_adam_group(q, dq, m, v, step: int, lr: float, beta1: float = 0.9, beta
     for what, ts in (("q", q), ("dq", dq), ("m", m), ("v", v)):
         if ts is not q and array("q", map(torch.Tensor.numel, ts)) != count:
             raise ValueError(f"{fn}: dq, m and v must have the sizes of q")
-        arrays.append(_arrays(fn, what, ts, [t.dtype for t in ts], _FP32))
+        arrays.append(_arrays(fn, what, ts, _FP32)[0])
     _want(fn, "norm", norm, (1,), torch.float32)
     hp = AdamDesc(lr, beta1, beta2, eps, weight_decay, step)
     handle = _stream(stream) if n == 0 else _raw_stream(stream, q[0])
