@@ -11,12 +11,13 @@
 // pair, their angle and their gamma are in one lane's registers whatever the pairing.  All heads of a token
 // use the same angles: a lane makes those of its CH pairs once per token and keeps them over the heads,
 // multiplied by gamma where that saves instructions.  What is in flight waits in shared memory: each
-// thread copies the chunks of its own next heads there asynchronously (two ahead) and is the only one
+// thread copies the chunks of its own next heads there asynchronously (one or two ahead) and is the only one
 // to read them, so that no barrier is needed.
 //
-// 8192 x (32 + 8) heads of 128 in bf16: 168 MB in 33.9 us (5.0 TB/s; without the norm 29.6), 4096 in fp32 the same
-// bytes in 29.9 us; backward 4096 x (40 + 40) heads 252 MB in 45.4 us (5.5 TB/s).  What bounds it above HBM is
-// issue and latency: some 220 instructions per warp and four heads, 0.55 issued per cycle and quarter of an SM.
+// 8192 x (32 + 8) heads of 128 in bf16: 168 MB in 32.6 us (5.1 TB/s; at 65536 tokens 6.0; without the norm 30.2),
+// 4096 in fp32 the same bytes in 29.5 us; backward 4096 x (40 + 40) heads 252 MB in 45.4 us (5.5 TB/s).  What bounds
+// it besides HBM is a launch's ramp and latency: some 200 instructions per warp and four heads, 0.55 issued per
+// cycle and quarter of an SM.
 //
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
 // turn), pos * f modulo 2^64 is the angle modulo a turn, exact to 2^-32 turns at any int32 position (an
@@ -33,9 +34,10 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = 256;   // pairs of a head
 constexpr int ctas_per_sm(int CH, bool both) { return (CH == 8 ? 3 : 4) - both; }  // (by registers)
-// Items that a thread has in flight.  (More are slower: eight, with 8192 x 40 heads of 128, 35.2 us instead of
-// 33.7 forward, four instead of two backward 48 us instead of 45.)
-constexpr int kSlots = 2;
+// Items that a thread has in flight, by the pairs of a lane.  (More are slower: with 8192 x 40 heads of 128 one
+// takes 32.7 us, two 34.1, eight 35.2; at 65536 tokens 221 and 254; backward in bf16 one 50.6, two 45.3, four 48,
+// in fp32 one 46.2, two 48.1.)
+constexpr int ring_slots(int CH, bool both) { return both && CH == 8 ? 2 : 1; }
 constexpr int kMostCtas = 3;  // per SM with dgamma's partial sums
 constexpr int kMaxAxes = 8;
 
@@ -195,6 +197,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
   using C = Chunk<T, CH, INTER>;
   constexpr bool BOTH = BWD && NORM;  // both x and dy are read
   constexpr int HEAD = C::BYTES * kThreads, SLOT = (BOTH ? 2 : 1) * HEAD;
+  constexpr int SLOTS = ring_slots(CH, BOTH);
   constexpr int N2 = CH / 2;
   // [slot][array][unit][thread], then each warp's cosines and sines of its token [half]
   extern __shared__ __align__(16) char ring[];
@@ -218,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
   const int far = rot ? a.half : dh / 2 - a.half, ahead_by = HW * dh;
   const uint32_t ring_at = smem_u32(ring) + t * C::UNIT;
   char* const my_ring = ring + t * C::UNIT;
-  float2* const angles = reinterpret_cast<float2*>(ring + kSlots * SLOT) + warp * a.half;
+  float2* const angles = reinterpret_cast<float2*>(ring + SLOTS * SLOT) + warp * a.half;
 
   const T* const in0 = static_cast<const T*>(BWD && !NORM ? s.dy : s.x);
   const T* const in1 = BOTH ? static_cast<const T*>(s.dy) : nullptr;
@@ -258,13 +261,13 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
     copy_commit();
   };
 #pragma unroll 1
-  for (int i = 0; i < kSlots; ++i) fetch(i);
+  for (int i = 0; i < SLOTS; ++i) fetch(i);
   if (t < a.half) {
     turn[t] = turns_of(freq);
     ax[t] = isfinite(freq) && axis >= 0 && axis < a.axes ? axis : -1;
   }
   if (!mine)  // lanes beyond the head's width: zeros in the sums
-    for (int i = 0; i < kSlots * SLOT / (kThreads * C::UNIT); ++i) {
+    for (int i = 0; i < SLOTS * SLOT / (kThreads * C::UNIT); ++i) {
       if (C::UNIT == 8) *reinterpret_cast<uint2*>(my_ring + i * kThreads * C::UNIT) = make_uint2(0u, 0u);
       else *reinterpret_cast<uint4*>(my_ring + i * kThreads * C::UNIT) = make_uint4(0u, 0u, 0u, 0u);
     }
@@ -346,7 +349,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
         }
       }
     }
-    copy_wait<kSlots - 1>();
+    copy_wait<SLOTS - 1>();
     float2 xa[N2], xb[N2];  // x (backward without the norm: dy)
     float2 da[N2], db[N2];  // the gradient of the rotated head, then of the normalised one
     {
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
       }
       C::store(out, far, da, db);
     }
-    if (++slot == kSlots) slot = 0;
+    if (++slot == SLOTS) slot = 0;
     at.h0 += HW;
     at.p0 += ahead_by;
     fresh = at.h0 >= H;
@@ -506,7 +509,7 @@ bool rope_ok(const poetx_rope* r) {
 }
 
 constexpr int rope_smem(int esz, int CH, bool both, int half) {
-  const int ring = kSlots * (both ? 2 : 1) * 2 * CH * esz * kThreads, red = both ? kWarps * 2 * CH * 32 * 4 : 0;
+  const int ring = ring_slots(CH, both) * (both ? 2 : 1) * 2 * CH * esz * kThreads, red = both ? kWarps * 2 * CH * 32 * 4 : 0;
   return (ring > red ? ring : red) + kWarps * half * (int)sizeof(float2);
 }
 // CTAs that an SM holds: by the kernels' registers, and by shared memory (with 5 KB of tables each).
