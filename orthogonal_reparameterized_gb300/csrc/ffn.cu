@@ -9,8 +9,8 @@
 // of W (the even CTA's half of the B operand) beside the 128 value rows of the same features (the odd
 // CTA's), so that a row of the accumulator holds both g and u of its features and the epilogue forms h
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
-// kept z, or in the epilogue of the same product run again), then the two products of the linear head's gradients (head.cu), for
-// which dz is what that head's is.
+// kept z, or in the epilogue of the same product run again), then the two products of the linear head's
+// gradients (head.cu), for which dz is what that head's is.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
@@ -133,7 +133,6 @@ struct GluArgs {
   void *a2, *b2, *a3, *b3;  // dz's further pieces
   long long in_pitch, out_pitch;  // of g and u, of dg and du (h and dh: F)
   uint32_t vpr, magic, shift;
-  long long F;
   long long vecs;
   Act act;
 };
@@ -178,12 +177,14 @@ __global__ void __launch_bounds__(kGluThreads) glu_fwd_kernel(const GluArgs p) {
   }
 }
 
-// PIECES 0: dg and du of type T.  Otherwise they are dz's 2 or 3 bf16 pieces.  The share of thread `t` of
-// `step`.
+// PIECES 0: dg and du of type T.  Otherwise they are dz's 2 or 3 bf16 pieces.
 template <typename T, int PIECES>
-__device__ __forceinline__ void glu_bwd_share(const GluArgs& p, long long t, long long step) {
+__global__ void __launch_bounds__(kGluThreads) glu_bwd_kernel(const GluArgs p) {
+  pdl_trigger();
+  pdl_wait();
   constexpr int U = bwd_unroll(PIECES);
-  for (long long i0 = t; i0 < p.vecs; i0 += U * step) {
+  const long long step = (long long)gridDim.x * kGluThreads;
+  for (long long i0 = (long long)blockIdx.x * kGluThreads + threadIdx.x; i0 < p.vecs; i0 += U * step) {
     Eight<T> g[U], u[U], d[U];
     uint32_t row[U];
 #pragma unroll
@@ -240,14 +241,6 @@ __device__ __forceinline__ void glu_bwd_share(const GluArgs& p, long long t, lon
       }
     }
   }
-}
-
-template <typename T, int PIECES>
-__global__ void __launch_bounds__(kGluThreads) glu_bwd_kernel(const GluArgs p) {
-  pdl_trigger();
-  pdl_wait();
-  glu_bwd_share<T, PIECES>(p, (long long)blockIdx.x * kGluThreads + threadIdx.x,
-                           (long long)gridDim.x * kGluThreads);
 }
 
 // ---------------------------------------------------------------- the projections
@@ -589,7 +582,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // both halves' rows of several K blocks, and x's come from a thread of their own.  An MMA of 128 rows costs
 // about as much for 16 tokens as for 64, so up to 64 features per tile the gate and the value rows are one
 // operand (MERGED; the epilogue brings them together through shared memory), above that two accumulators
-// side by side.  Neighbouring K blocks go to different accumulators (kAccs of them, added in fp32 by the
+// side by side.  There neighbouring K blocks go to different accumulators (score_accs, added in fp32 by the
 // epilogue), so that an MMA need not wait for the one before; D is at most 16384, at most 1024 adds into
 // one (6e-5).
 struct FfnScore {
@@ -758,7 +751,8 @@ __global__ void __launch_bounds__(score_threads(NT), 1)
       mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns, kSite + __LINE__);
     }
   } else if (warp >= 2 && warp < XWARP) {
-    const int set = (warp - 2) >> 2, q = warp & 3, mine = q * 32 + lane;  // the thread's lane of the accumulators
+    const int set = (warp - 2) >> 2, q = warp & 3;
+    const int mine = q * 32 + lane;  // the thread's lane of the accumulators
     const int used = min(ACCS, p.num_st * p.kps);
     // h, z or dz of a feature and a token
     auto put = [&](long long f, int token, float g, float u, float d) {
@@ -892,7 +886,6 @@ poetx_status run_glu(const GluCall& c, cudaStream_t s) {
     for (int i = 0; i < 6; ++i) *dst[i] = c.out[i] ? static_cast<uint8_t*>(c.out[i]) + out : nullptr;
     a.in_pitch = c.in_pitch;
     a.out_pitch = c.out_pitch;
-    a.F = c.F;
     a.vecs = rows * vpr;
     a.vpr = (uint32_t)vpr;
     a.act = c.act;

@@ -207,9 +207,10 @@ poetx_status umma_wgrad(const void* X, const void* dY, long long N, int nblk, in
                         float* dG, cudaStream_t s);
 
 // ---- head.cu: dx = unit T dz W and dW (+)= unit T dz^T x from dz [rows][pitch] (pitch a multiple of 64
-// from V on; columns V .. z_cols - 1 hold zeros, those from z_cols on are not read for dx) in one launch (and one for the sums of dx's splits).  bf16: dz in one piece, or
-// in two (fine, at most 128 rows); f32: dz, x and W in three bf16 pieces each, `step` bytes apart.  More
-// than one piece of rows: `first` and `last` say which, acc [V][D] holds dW's fp32 sum in between.
+// from V on; columns V .. z_cols - 1 hold zeros, those from z_cols on are not read for dx) in one launch
+// (and one for the sums of dx's splits).  bf16: dz in one piece, or in two (fine, at most 128 rows); f32:
+// dz, x and W in three bf16 pieces each, `step` bytes apart.  More than one piece of rows: `first` and
+// `last` say which, acc [V][D] holds dW's fp32 sum in between.
 struct GradProducts {
   bool f32, fine;
   int rows, D, V;

@@ -11,13 +11,13 @@
 // pair, their angle and their gamma are in one lane's registers whatever the pairing.  All heads of a token
 // use the same angles: a lane makes those of its CH pairs once per token and keeps them over the heads,
 // multiplied by gamma where that saves instructions.  What is in flight waits in shared memory: each
-// thread copies the chunks of its own next heads there asynchronously (one or two ahead) and is the only one
-// to read them, so that no barrier is needed.
+// thread copies the chunks of its own next heads there asynchronously (one or two ahead) and is the only
+// one to read them, so that no barrier is needed.
 //
-// 8192 x (32 + 8) heads of 128 in bf16: 168 MB in 32.6 us (5.1 TB/s; at 65536 tokens 6.0; without the norm 30.2),
-// 4096 in fp32 the same bytes in 29.5 us; backward 4096 x (40 + 40) heads 252 MB in 45.4 us (5.5 TB/s).  What bounds
-// it besides HBM is a launch's ramp and latency: some 200 instructions per warp and four heads, 0.55 issued per
-// cycle and quarter of an SM.
+// 8192 x (32 + 8) heads of 128 in bf16: 168 MB in 32.6 us (5.1 TB/s; at 65536 tokens 6.0; without the norm
+// 30.2), 4096 in fp32 the same bytes in 29.5 us; backward 4096 x (40 + 40) heads 252 MB in 45.4 us
+// (5.5 TB/s).  What bounds it besides HBM is a launch's ramp and latency: some 200 instructions per warp
+// and four heads, 0.55 issued per cycle and quarter of an SM.
 //
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
 // turn), pos * f modulo 2^64 is the angle modulo a turn, exact to 2^-32 turns at any int32 position (an
@@ -34,9 +34,9 @@ constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxHalf = 256;   // pairs of a head
 constexpr int ctas_per_sm(int CH, bool both) { return (CH == 8 ? 3 : 4) - both; }  // (by registers)
-// Items that a thread has in flight, by the pairs of a lane.  (More are slower: with 8192 x 40 heads of 128 one
-// takes 32.7 us, two 34.1, eight 35.2; at 65536 tokens 221 and 254; backward in bf16 one 50.6, two 45.3, four 48,
-// in fp32 one 46.2, two 48.1.)
+// Items that a thread has in flight, by the pairs of a lane.  (More are slower: with 8192 x 40 heads of 128
+// one takes 32.7 us, two 34.1, eight 35.2; at 65536 tokens 221 and 254; backward in bf16 one 50.6, two 45.3,
+// four 48, in fp32 one 46.2, two 48.1.)
 constexpr int ring_slots(int CH, bool both) { return both && CH == 8 ? 2 : 1; }
 constexpr int kMostCtas = 3;  // per SM with dgamma's partial sums
 constexpr int kMaxAxes = 8;
@@ -509,7 +509,8 @@ bool rope_ok(const poetx_rope* r) {
 }
 
 constexpr int rope_smem(int esz, int CH, bool both, int half) {
-  const int ring = ring_slots(CH, both) * (both ? 2 : 1) * 2 * CH * esz * kThreads, red = both ? kWarps * 2 * CH * 32 * 4 : 0;
+  const int ring = ring_slots(CH, both) * (both ? 2 : 1) * 2 * CH * esz * kThreads;
+  const int red = both ? kWarps * 2 * CH * 32 * 4 : 0;
   return (ring > red ? ring : red) + kWarps * half * (int)sizeof(float2);
 }
 // CTAs that an SM holds: by the kernels' registers, and by shared memory (with 5 KB of tables each).
@@ -525,11 +526,12 @@ cudaError_t rope_launch1(const RopeArgs& a, cudaStream_t s) {
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, rope_smem(sizeof(T), CH, BWD && NORM, kMaxHalf));
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                rope_smem(sizeof(T), CH, BWD && NORM, kMaxHalf));
   });
   if (attr != cudaSuccess) return attr;
-  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads), rope_smem(sizeof(T), CH, BWD && NORM, a.half), s,
-                    a);
+  return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads),
+                    rope_smem(sizeof(T), CH, BWD && NORM, a.half), s, a);
 }
 template <typename T, int CH, bool BWD>
 cudaError_t rope_launch(const RopeArgs& a, bool inter, bool norm, cudaStream_t s) {
