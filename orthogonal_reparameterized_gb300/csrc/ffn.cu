@@ -10,7 +10,8 @@
 // CTA's), so that a row of the accumulator holds both g and u of its features and the epilogue forms h
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
 // kept z, or in the epilogue of the same product run again), then the two products of the linear head's
-// gradients (head.cu), for which dz is what that head's is.
+// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows and the gradients
+// of up to 16 fp32 or 8 bf16 rows are ffn_rows.cu's.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
@@ -24,9 +25,11 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, drains its own
 // copies, frees its TMEM and returns.
+#include <algorithm>
 #include <mutex>
 
 #include "common.cuh"
+#include "gated.cuh"
 #include "kernels.h"
 #include "pieces.cuh"
 
@@ -36,44 +39,6 @@ namespace poetx {
 constexpr int kSite = 8 * 10000;
 
 namespace {
-
-// ---------------------------------------------------------------- the activation
-// t = g (c0 + c1 g^2): SiLU 1 and 0, GELU 2 sqrt(2 / pi) and 0.044715 times that.
-struct Act {
-  float c0, c1;
-};
-Act act_of(poetx_activation a) {
-  const double c = 1.5957691216057307117;  // 2 sqrt(2 / pi)
-  return a == POETX_GELU ? Act{(float)c, (float)(0.044715 * c)} : Act{1.f, 0.f};
-}
-bool act_ok(poetx_activation a) { return a == POETX_SILU || a == POETX_GELU; }
-
-// s(t).  EXACT: for fp32 results.  Otherwise the hardware's exp2 and reciprocal, each within 2^-22; the
-// argument's rounding costs |t| 2^-24 besides (exp(-t) at t = -80: 5e-6), all far below bf16's 2^-8.
-template <bool EXACT>
-__device__ __forceinline__ float logistic(float t) {
-  if (EXACT) return 1.f / (1.f + expf(-t));
-  float e, r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(t * -1.44269504088896340736f));
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
-  return r;
-}
-// g^2, cut off where fp32 ends (0 times infinity would make SiLU's t NaN).
-__device__ __forceinline__ float square(float g) { return fminf(g * g, 0x1p120f); }
-
-template <bool EXACT>
-__device__ __forceinline__ float gated(float g, float u, Act a) {
-  return g * logistic<EXACT>(g * fmaf(a.c1, square(g), a.c0)) * u;
-}
-// (dg, du) of dh.
-template <bool EXACT>
-__device__ __forceinline__ float2 gated_grad(float g, float u, float dh, Act a) {
-  const float q = square(g);
-  const float s = logistic<EXACT>(g * fmaf(a.c1, q, a.c0));
-  const float v = g * s;
-  const float d = fmaf(v * (1.f - s), fmaf(3.f * a.c1, q, a.c0), s);
-  return make_float2(dh * u * d, dh * v);
-}
 
 // ---------------------------------------------------------------- elementwise kernels
 // Eight neighbouring elements.
@@ -1073,7 +1038,9 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
 // The backward's workspace.
 struct Plan {
   bool f32, fine;
+  bool rows;        // so few rows that ffn_rows.cu has the gradients (dz in fp32, or in two bf16 pieces)
   bool direct;      // dz from the projections' sums (else from z, kept or written to the workspace)
+  int pieces;       // bf16 pieces of dz (0: it is fp32)
   long long pitch;  // of dz: 2 F up to a multiple of 64
   int splits;
   size_t xs, ws, z, dz, z_step, dxp, bytes;
@@ -1083,22 +1050,25 @@ Plan plan(poetx_dtype dt, int N, int D, int F, bool have_z, bool dx) {
   const size_t n = N > 0 ? N : 1;
   o.f32 = dt == POETX_F32;
   o.fine = !o.f32 && N <= kScoreRows;
-  o.pitch = (long long)align_up((size_t)2 * F, 64);
-  o.splits = dx ? grad_splits(n, D, 2 * F, o.f32) : 1;
+  o.rows = rows_gradients_fit(o.f32, (int)n);
+  o.pieces = o.f32 ? (o.rows ? 0 : 3) : (o.fine ? 2 : 1);
+  o.pitch = o.pieces ? (long long)align_up((size_t)2 * F, 64) : 2ll * F;
+  o.splits = !dx ? 1 : (o.rows ? rows_splits(o.f32, (int)n, D, 2 * F) : grad_splits(n, D, 2 * F, o.f32));
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t a = at;
     at += align_up(bytes, 1024);
     return a;
   };
-  o.xs = o.f32 ? take(3 * piece_step(n * D)) : 0;
-  o.ws = o.f32 ? take(3 * piece_step((size_t)2 * F * D)) : 0;
+  o.xs = o.pieces == 3 ? take(3 * piece_step(n * D)) : 0;
+  o.ws = o.pieces == 3 ? take(3 * piece_step((size_t)2 * F * D)) : 0;
   // (128 rows or fewer of a D beyond the few-row kernel's go by z: dz is then in two pieces)
-  o.direct = !have_z && !o.f32 && (!o.fine || few_rows(N, D));
+  o.direct = !have_z && (o.f32 ? o.rows : !o.fine || few_rows(N, D));
   o.z = have_z || o.direct ? 0 : take(n * 2 * F * dtype_size(dt));
-  o.z_step = align_up(n * o.pitch * 2, 1024);
-  o.dz = take((o.f32 ? 3 : (o.fine ? 2 : 1)) * o.z_step);
-  o.dxp = dx && (o.splits > 1 || o.fine) ? take((size_t)o.splits * align_up(n, 256) * D * 4) : 0;
+  o.z_step = align_up(n * o.pitch * (o.pieces ? 2 : 4), 1024);
+  o.dz = take((o.pieces ? o.pieces : 1) * o.z_step);
+  if (dx && (o.splits > 1 || (o.fine && !o.rows)))
+    o.dxp = take((size_t)o.splits * (o.rows ? n : align_up(n, 256)) * D * 4);
   o.bytes = at;
   return o;
 }
@@ -1162,6 +1132,10 @@ extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, cons
   if (!x || !W || !h || (need && !ws)) return POETX_ERR_ARG;
   if (ws_bytes < need) return POETX_ERR_WORKSPACE;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
+  if (rows_forward_fits(dt == POETX_F32, N))
+    return rows_forward({static_cast<const float*>(x), static_cast<const float*>(W), N, D, F,
+                         static_cast<float*>(h), static_cast<float*>(z), nullptr, nullptr},
+                        act, stream);
   const uint8_t *xp = static_cast<const uint8_t*>(x), *wp = static_cast<const uint8_t*>(W);
   if (dt == POETX_F32) {
     uint8_t* w = static_cast<uint8_t*>(ws);
@@ -1200,33 +1174,47 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
   uint8_t* w = static_cast<uint8_t*>(ws);
   const uint8_t *xp = static_cast<const uint8_t*>(x), *wp = static_cast<const uint8_t*>(W);
-  if (pl.f32) {
+  if (pl.pieces == 3) {
     xp = w + pl.xs;
     wp = w + pl.ws;
     POETX_TRY(split_pieces(static_cast<const float*>(x), (long long)N * D, w + pl.xs,
                            piece_step((size_t)N * D), static_cast<const float*>(W), 2ll * F * D, w + pl.ws,
                            piece_step((size_t)2 * F * D), stream));
   }
-  const int pieces = pl.f32 ? 3 : (pl.fine ? 2 : 1);
-  if (pl.direct) {
+  const int pieces = pl.pieces;
+  const float *xf = static_cast<const float*>(x), *wf = static_cast<const float*>(W);
+  if (pl.direct && pl.f32) {
+    POETX_TRY(rows_forward({xf, wf, N, D, F, nullptr, nullptr, static_cast<const float*>(dh),
+                            reinterpret_cast<float*>(w + pl.dz)},
+                           act, stream));
+  } else if (pl.direct) {
     POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
                       Outputs{nullptr, w + pl.dz, dh, pl.fine ? w + pl.dz + pl.z_step : nullptr, pl.pitch},
                       stream));
   } else {
     if (!z) {
       z = w + pl.z;
-      POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
-                        Outputs{nullptr, w + pl.z, nullptr, nullptr, 2ll * F}, stream));
+      if (rows_forward_fits(pl.f32, N))
+        POETX_TRY(rows_forward({xf, wf, N, D, F, nullptr, reinterpret_cast<float*>(w + pl.z), nullptr, nullptr},
+                               act, stream));
+      else
+        POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
+                          Outputs{nullptr, w + pl.z, nullptr, nullptr, 2ll * F}, stream));
     }
-    // dz: the gate's half, then the value's, in one to three bf16 pieces
+    // dz: the gate's half, then the value's, in fp32 or in one to three bf16 pieces
     GluCall c{dt, act_of(act), z, static_cast<const uint8_t*>(z) + (size_t)F * esz, dh, N, F, 2ll * F,
               pl.pitch, {}, pieces == 1 ? 0 : pieces};
-    for (int i = 0; i < pieces; ++i) {
+    for (int i = 0; i < std::max(pieces, 1); ++i) {
       c.out[2 * i] = w + pl.dz + i * pl.z_step;
-      c.out[2 * i + 1] = w + pl.dz + i * pl.z_step + (size_t)F * 2;
+      c.out[2 * i + 1] = w + pl.dz + i * pl.z_step + (size_t)F * (pieces ? 2 : 4);
     }
     POETX_TRY(run_glu(c, stream));
   }
+  float* const dxp = reinterpret_cast<float*>(w + pl.dxp);
+  if (pl.rows)
+    return rows_gradients({pl.f32, w + pl.dz, w + pl.dz + pl.z_step, pl.pitch, x, W, N, D, 2 * F, dx, dW,
+                           accumulate, dxp},
+                          stream);
   GradProducts g{};
   g.f32 = pl.f32;
   g.fine = pl.fine;
@@ -1246,6 +1234,6 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   g.accumulate = accumulate;
   g.first = g.last = true;
   g.splits = pl.splits;
-  g.dxp = reinterpret_cast<float*>(w + pl.dxp);
+  g.dxp = dxp;
   return grad_products(g, stream);
 }

@@ -1,0 +1,443 @@
+// The gated feed-forward block (ffn.cu) for so few rows that its time is W's way through the SMs, on the
+// CUDA cores, in fp32 throughout.
+//
+//   forward (fp32):    z = x W^T, then h = a(g) u, or dz = [dh u a'(g) | dh a(g)] from the sums
+//   gradients (both):  dx = dz W,  dW = dz^T x
+//
+// Forward: a warp has the gate and value rows of two features, its lanes every 32nd float4 of them, and
+// multiplies them with up to eight tokens' x from shared memory (or L1); more tokens are further warps of the
+// same CTA, which find W's lines in L1.  The sums of a warp's 4 x 8 products are joined by halving: in each
+// of five steps a lane gives half of its sums away and keeps the other half, so that 31 shuffles leave one
+// sum per lane.  One row of 4096 x 14336: 470 MB in 66.8 us (7.0 TB/s); sixteen of 2048 x 5632 36 us (92 MB:
+// the loads of x bound it, 32 bytes for each of W's 16; the tensor cores with W in three pieces 124 us).
+//
+// Gradients: both products in one pass over W's rows, which reads a row and writes the same row of dW.  A
+// lane has 8 or 16 bytes of columns with x's values and dx's sums for every token in registers, a warp an
+// equal share of the rows, and a row costs 2 N multiply-adds per column and no exchange; dz's values come
+// from shared memory, where the warp lays those of its next eight rows.  Each thread copies its own bytes
+// of the next eight rows ahead (with a ring of registers instead sixteen fp32 rows took 92 us, not 48: a wait
+// for one of several loads in flight is a wait for all of them).  The warps' sums of dx are joined in shared
+// memory, the CTAs' by the head's kernel for partial sums.  Sixteen fp32 rows of 2048 x 5632: 48 us (115 on
+// the tensor cores), four bf16 rows of 4096 x 14336 82 us (470 MB, 5.7 TB/s; 124), eight 115 us (by the
+// multiply-adds; 124, which is also what nine to 128 rows take there).
+#include <algorithm>
+#include <mutex>
+#include <type_traits>
+
+#include "common.cuh"
+#include "gated.cuh"
+#include "kernels.h"
+
+namespace poetx {
+namespace {
+
+// ---------------------------------------------------------------- forward
+// Warps of a CTA.  HERE: all of x is in the shared memory of one CTA per SM, else a warp reads it through L1.
+constexpr int fwd_warps(bool here) { return here ? 12 : 4; }
+constexpr int kGroup = 8;  // tokens of a warp at most
+constexpr size_t kXBytes = 200 * 1024;
+
+struct FwdArgs {
+  RowsForward c;
+  int groups;  // of tokens, at most four
+  Act act;
+};
+
+// Two features' sums for the group's tokens.
+template <int NT, bool HERE>
+__device__ __forceinline__ void rows_fwd_unit(const FwdArgs& p, int f0, int n0, int lane,
+                                              const float4* x_here) {
+  const RowsForward& c = p.c;
+  const int quads = c.D / 4;
+  const float4* w[4];  // two gate rows, two value rows
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    w[r] = reinterpret_cast<const float4*>(c.W) + (long long)(f0 + (r & 1) + (r >> 1) * c.F) * quads;
+  // (a token beyond the last: the last one's, and its sums are not stored)
+  const float4* x[NT];
+  int x_at[NT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    x_at[n] = min(n0 + n, c.N - 1) * quads;
+    x[n] = reinterpret_cast<const float4*>(c.x) + x_at[n];
+  }
+  float2 acc[4][NT] = {};
+  constexpr int U = 2;
+  for (int q0 = lane; q0 < quads; q0 += 32 * U) {
+    float4 wv[U][4];
+#pragma unroll
+    for (int k = 0; k < U; ++k)
+#pragma unroll
+      for (int r = 0; r < 4; ++r)
+        if (q0 + 32 * k < quads) wv[k][r] = w[r][q0 + 32 * k];
+#pragma unroll
+    for (int k = 0; k < U; ++k) {
+      if (q0 + 32 * k >= quads) break;
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+        const float4 xv = HERE ? x_here[x_at[n] + q0 + 32 * k] : x[n][q0 + 32 * k];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+          acc[r][n] = fma2(make_float2(wv[k][r].x, wv[k][r].y), make_float2(xv.x, xv.y), acc[r][n]);
+          acc[r][n] = fma2(make_float2(wv[k][r].z, wv[k][r].w), make_float2(xv.z, xv.w), acc[r][n]);
+        }
+      }
+    }
+  }
+  constexpr int V = 4 * NT;
+  float v[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) v[i] = acc[i / NT][i % NT].x + acc[i / NT][i % NT].y;
+#pragma unroll
+  for (int o = 16, left = V / 2; o; o >>= 1, left >>= 1) {
+    if (left) {
+      const bool upper = lane & o;
+#pragma unroll
+      for (int i = 0; i < left; ++i) {
+        const float give = upper ? v[i] : v[i + left], keep = upper ? v[i + left] : v[i];
+        v[i] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+      }
+    } else {
+      v[0] += __shfl_xor_sync(0xffffffffu, v[0], o);
+    }
+  }
+  // sum i (of V, gates in the lower half) lies in the lanes from i * 32 / V on
+  const float g = v[0], u = __shfl_xor_sync(0xffffffffu, g, 16);
+  const int i = lane * V / 32, f = f0 + i / NT, n = n0 + i % NT;
+  if (lane >= 16 || lane % (32 / V) || n >= c.N) return;
+  const long long at = (long long)n * 2 * c.F + f;
+  if (c.dh) {
+    const float2 d = gated_grad<true>(g, u, c.dh[(long long)n * c.F + f], p.act);
+    c.dz[at] = d.x;
+    c.dz[at + c.F] = d.y;
+    return;
+  }
+  if (c.h) c.h[(long long)n * c.F + f] = gated<true>(g, u, p.act);
+  if (c.z) {
+    c.z[at] = g;
+    c.z[at + c.F] = u;
+  }
+}
+
+template <int NT, bool HERE>
+__global__ void __launch_bounds__(32 * fwd_warps(HERE), 1) rows_fwd_kernel(const FwdArgs p) {
+  extern __shared__ __align__(16) float4 x_here[];
+  pdl_trigger();
+  pdl_wait();
+  const RowsForward& c = p.c;
+  const int lane = threadIdx.x & 31, quads = c.D / 4;
+  if (HERE) {
+    const float4* const x = reinterpret_cast<const float4*>(c.x);
+    for (int i = threadIdx.x; i < c.N * quads; i += 32 * fwd_warps(HERE))
+      copy_async<16>(smem_u32(x_here + i), x + i);
+    copy_commit();
+    copy_wait<0>();
+    __syncthreads();
+  }
+  // the groups of a pair side by side in one CTA: they meet W's lines in L1
+  const int warp = threadIdx.x >> 5, teams = fwd_warps(HERE) / p.groups, team = warp / p.groups;
+  if (team >= teams) return;
+  for (int pair = HERE ? team * gridDim.x + blockIdx.x : blockIdx.x * teams + team; 2 * pair < c.F;
+       pair += teams * gridDim.x)
+    rows_fwd_unit<NT, HERE>(p, 2 * pair, warp % p.groups * NT, lane, x_here);
+}
+
+// ---------------------------------------------------------------- gradients
+constexpr int kGradWarps = 8;
+constexpr int kBatch = 8;  // rows whose dz a warp has in shared memory
+
+// Columns of a lane: 16 bytes of a row, in bf16 with more than four tokens 8.  That leaves x and dx of sixteen
+// fp32 tokens 128 registers and an SM one CTA, everything else 64 and two.  (16 bytes against 8: sixteen
+// fp32 tokens 47.9 and 56.8 us at 2048 x 5632, where the multiply-adds are most of it; eight bf16 tokens
+// 32.9 and 29.9 us.)
+template <typename T>
+constexpr int cols_of(int NT) { return sizeof(T) == 4 ? 4 : (NT > 4 ? 4 : 8); }
+template <typename T>
+constexpr int grad_ctas(int NT) { return NT * cols_of<T>(NT) > 32 ? 1 : 2; }  // of an SM
+template <typename T, bool ADD>
+constexpr int grad_smem(int NT) {  // two batches of W (and of dW), a batch's dz and the sums of dx of each warp
+  const int C = cols_of<T>(NT);
+  return kGradWarps * (2 * kBatch * 32 * C * (int)sizeof(T) * (ADD ? 2 : 1) +
+                       kBatch * NT * (int)sizeof(float2) + NT * 32 * C * (int)sizeof(float));
+}
+
+struct GradArgs {
+  RowsGradients c;
+  int tiles;   // of 32 lanes' columns
+  int splits;  // CTAs over the rows
+};
+
+// A lane's columns of a row, fp32 or bf16 by their number.
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[2]) {
+  v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
+  v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
+}
+__device__ __forceinline__ float2 halves(uint32_t w) {
+  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+}
+__device__ __forceinline__ void unpack(const uint2& w, float2 (&v)[2]) {
+  v[0] = halves(w.x), v[1] = halves(w.y);
+}
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[4]) {
+  v[0] = halves(w.x), v[1] = halves(w.y), v[2] = halves(w.z), v[3] = halves(w.w);
+}
+template <typename T, int P>
+__device__ __forceinline__ void store(T* p, const float2 (&v)[P]) {
+  if constexpr (sizeof(T) == 4) {
+#pragma unroll
+    for (int j = 0; j < P; j += 2)
+      *reinterpret_cast<float4*>(p + 2 * j) = make_float4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
+  } else {
+    uint32_t w[P];
+#pragma unroll
+    for (int j = 0; j < P; ++j) w[j] = pack_bf16x2(v[j].x, v[j].y);
+    if constexpr (P == 4)
+      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    else
+      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+  }
+}
+
+// ADD: dW is added to what is there.
+template <typename T, int NT, bool ADD>
+__global__ void __launch_bounds__(32 * kGradWarps, grad_ctas<T>(NT))
+    rows_grad_kernel(const GradArgs p) {
+  constexpr int C = cols_of<T>(NT), P = C / 2;
+  constexpr int kBytes = C * sizeof(T);
+  using Vec = std::conditional_t<kBytes == 16, uint4, uint2>;
+  extern __shared__ __align__(16) uint8_t smem[];
+  pdl_trigger();
+  pdl_wait();
+  const RowsGradients& c = p.c;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
+  const int col = (tile * 32 + lane) * C;
+  const bool mine = col < c.D, dx = c.dx != nullptr, dW = c.dW != nullptr;
+  const long long part = (long long)split * kGradWarps + warp, parts = (long long)p.splits * kGradWarps;
+  const int first = (int)(c.V * part / parts), end = (int)(c.V * (part + 1) / parts);
+
+  float2 x[NT][P], acc[NT][P] = {};
+#pragma unroll
+  for (int n = 0; n < NT; ++n) {
+    Vec v{};
+    if (mine && n < c.N)
+      v = *reinterpret_cast<const Vec*>(static_cast<const T*>(c.x) + (long long)n * c.D + col);
+    unpack(v, x[n]);
+  }
+  // a thread's own bytes of each row: it copies them a batch ahead and reads them itself (a lane without
+  // columns: the last ones', and stores nothing)
+  constexpr int kSlot = 32 * kBytes, kHalf = kBatch * kSlot, kArray = 2 * kHalf;
+  const int from = mine ? col : c.D - C;
+  uint8_t* const ring = smem + warp * (ADD ? 2 : 1) * kArray + lane * kBytes;
+  const uint32_t ring_at = smem_u32(ring);
+  const T* const W_at = static_cast<const T*>(dx ? c.W : c.x) + from;
+  T* const dW_at = static_cast<T*>(c.dW) + from;
+  const long long step = dx ? c.D : 0;
+  auto request = [&](int r, int half) {
+    if (r < end) {
+      const T* w = W_at + r * step;
+      const T* g = dW_at + (long long)r * c.D;
+      const bool whole = r + kBatch <= end;
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) {
+        if (whole || r + k < end) {
+          copy_async<kBytes>(ring_at + half + k * kSlot, w);
+          if (ADD) copy_async<kBytes>(ring_at + kArray + half + k * kSlot, g);
+        }
+        w += step;
+        g += c.D;
+      }
+    }
+    copy_commit();
+  };
+  request(first, 0);
+  // dz of a batch: lane's row lane % 8, tokens lane / 8 and every fourth one from there
+  constexpr int M = (NT + 3) / 4;
+  float v[M];
+  auto fetch = [&](int r) {
+    r += lane & 7;
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int n = (lane >> 3) + 4 * m;
+      v[m] = 0.f;
+      if (n < c.N && r < end) {
+        const long long at = n * c.pitch + r;
+        if (sizeof(T) == 4)
+          v[m] = static_cast<const float*>(c.dz)[at];
+        else
+          v[m] = __bfloat162float(static_cast<const __nv_bfloat16*>(c.dz)[at]) +
+                 __bfloat162float(static_cast<const __nv_bfloat16*>(c.dz2)[at]);
+      }
+    }
+  };
+  constexpr int kRings = kGradWarps * (ADD ? 2 : 1) * kArray;
+  float2* const dz = reinterpret_cast<float2*>(smem + kRings) + warp * kBatch * NT;
+  fetch(first);
+  int half = 0;
+  for (int r0 = first; r0 < end; r0 += kBatch, half ^= kHalf) {
+    __syncwarp();
+#pragma unroll
+    for (int m = 0; m < M; ++m) {
+      const int n = (lane >> 3) + 4 * m;
+      if (n < NT) dz[(lane & 7) * NT + n] = both(v[m]);
+    }
+    __syncwarp();
+    fetch(r0 + kBatch);
+    request(r0 + kBatch, half ^ kHalf);
+    copy_wait<1>();
+    T* out = dW_at + (long long)r0 * c.D;
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (r0 + k >= end) break;
+      float2 w[P], d[P];
+      const uint8_t* const slot = ring + half + k * kSlot;
+      unpack(*reinterpret_cast<const Vec*>(slot), w);
+      if (ADD) {
+        unpack(*reinterpret_cast<const Vec*>(slot + kArray), d);
+      } else {
+#pragma unroll
+        for (int j = 0; j < P; ++j) d[j] = both(0.f);
+      }
+#pragma unroll
+      for (int n = 0; n < NT; n += 2) {
+        const float4 two = *reinterpret_cast<const float4*>(dz + k * NT + n);
+        const float2 s0 = make_float2(two.x, two.y), s1 = make_float2(two.z, two.w);
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          d[j] = fma2(s0, x[n][j], d[j]);
+          acc[n][j] = fma2(s0, w[j], acc[n][j]);
+          d[j] = fma2(s1, x[n + 1][j], d[j]);
+          acc[n + 1][j] = fma2(s1, w[j], acc[n + 1][j]);
+        }
+      }
+      if (mine && dW) store(out, d);
+      out += c.D;
+    }
+  }
+  if (!dx) return;
+
+  // [warp][token][column]
+  float* const red = reinterpret_cast<float*>(smem + kRings + kGradWarps * kBatch * NT * sizeof(float2));
+  constexpr int kRow = 32 * C;
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+    store(red + (warp * NT + n) * kRow + lane * C, acc[n]);
+  __syncthreads();
+  for (int i = threadIdx.x; i < NT * kRow / 4; i += 32 * kGradWarps) {
+    const int n = i / (kRow / 4), q = i % (kRow / 4) * 4, at_col = tile * kRow + q;
+    if (n >= c.N || at_col >= c.D) continue;
+    float4 s = *reinterpret_cast<const float4*>(red + n * kRow + q);
+#pragma unroll
+    for (int k = 1; k < kGradWarps; ++k) {
+      const float4 b = *reinterpret_cast<const float4*>(red + (k * NT + n) * kRow + q);
+      s.x += b.x;
+      s.y += b.y;
+      s.z += b.z;
+      s.w += b.w;
+    }
+    if (p.splits > 1) {
+      *reinterpret_cast<float4*>(c.dxp + ((long long)split * c.N + n) * c.D + at_col) = s;
+    } else if (sizeof(T) == 4) {
+      *reinterpret_cast<float4*>(static_cast<float*>(c.dx) + (long long)n * c.D + at_col) = s;
+    } else {
+      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(c.dx) + (long long)n * c.D + at_col) =
+          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
+    }
+  }
+}
+
+template <int NT, bool HERE>
+poetx_status launch_fwd1(const FwdArgs& a, size_t smem, cudaStream_t s) {
+  auto k = rows_fwd_kernel<NT, HERE>;
+  if (HERE) {
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [&] {
+      attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kXBytes);
+    });
+    POETX_CUDA_TRY(attr);
+  }
+  const int grid = HERE ? std::min(a.c.F / 2, sm_count()) : ceil_div(a.c.F / 2, fwd_warps(HERE) / a.groups);
+  POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(32 * fwd_warps(HERE)), smem, s, a));
+  POETX_CUDA_TRY(cudaGetLastError());
+  after_launch(s, ST_FFN_GEMM);
+  return POETX_OK;
+}
+template <int NT>
+poetx_status launch_fwd(const FwdArgs& a, cudaStream_t s) {
+  const size_t x_bytes = (size_t)a.c.N * a.c.D * 4;
+  // From three rows on x in shared memory is faster (2048 x 5632: two rows 19.2 us there and 15.9 through
+  // L1, four 20.2 and 26.3, eight 22.0 and 27.2, sixteen 36.3 and 42.4); what does not fit goes through L1.
+  if constexpr (NT > 2)
+    if (x_bytes <= kXBytes) return launch_fwd1<NT, true>(a, x_bytes, s);
+  return launch_fwd1<NT, false>(a, 0, s);
+}
+
+template <typename T, int NT, bool ADD>
+poetx_status launch_grad1(const GradArgs& a, cudaStream_t s) {
+  auto k = rows_grad_kernel<T, NT, ADD>;
+  static std::once_flag once;
+  static cudaError_t attr = cudaSuccess;
+  std::call_once(once, [&] {
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem<T, ADD>(NT));
+  });
+  POETX_CUDA_TRY(attr);
+  POETX_CUDA_TRY(launch_pdl(k, dim3(a.tiles * a.splits), dim3(32 * kGradWarps), grad_smem<T, ADD>(NT), s, a));
+  POETX_CUDA_TRY(cudaGetLastError());
+  after_launch(s, ST_FFN_GEMM);
+  return POETX_OK;
+}
+template <typename T, int NT>
+poetx_status launch_grad(const GradArgs& a, cudaStream_t s) {
+  return a.c.dW && a.c.accumulate ? launch_grad1<T, NT, true>(a, s) : launch_grad1<T, NT, false>(a, s);
+}
+
+int tokens_of(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
+int tiles_of(bool f32, int N, int D) {
+  return ceil_div(D, 32 * (f32 ? cols_of<float>(tokens_of(N)) : cols_of<__nv_bfloat16>(tokens_of(N))));
+}
+
+}  // namespace
+
+bool rows_forward_fits(bool f32, int N) { return f32 && N <= kRowsForward; }
+bool rows_gradients_fit(bool f32, int N) { return N <= (f32 ? 16 : 8); }
+
+// CTAs over W's rows: as many as fill the SMs' places once or twice, whichever leaves fewer of them empty
+// (2048 columns in fp32 are 16 tiles: 9 splits fill 144 of 152 places, 19 all of two rounds), with sixteen
+// rows to a warp at least.
+int rows_splits(bool f32, int N, int D, int V) {
+  const int tiles = tiles_of(f32, N, D), nt = tokens_of(N);
+  const int places = sm_count() * (f32 ? grad_ctas<float>(nt) : grad_ctas<__nv_bfloat16>(nt));
+  const int one = places / tiles, two = 2 * places / tiles;
+  int s = 2 * one * 100 < two * 97 ? two : one;
+  const int most = V / (16 * kGradWarps);
+  if (s > most) s = most;
+  return s < 1 ? 1 : s;
+}
+
+poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s) {
+  const int nt = c.N == 1 ? 1 : (c.N == 2 ? 2 : (c.N <= 4 ? 4 : kGroup)), groups = ceil_div(c.N, nt);
+  const FwdArgs a{c, groups, act_of(act)};
+  switch (nt) {
+    case 1: return launch_fwd<1>(a, s);
+    case 2: return launch_fwd<2>(a, s);
+    case 4: return launch_fwd<4>(a, s);
+    default: return launch_fwd<kGroup>(a, s);
+  }
+}
+
+poetx_status rows_gradients(const RowsGradients& c, cudaStream_t s) {
+  const GradArgs a{c, tiles_of(c.f32, c.N, c.D), rows_splits(c.f32, c.N, c.D, c.V)};
+  const int nt = tokens_of(c.N);
+  using H = __nv_bfloat16;
+  if (c.f32)
+    POETX_TRY((nt == 4 ? launch_grad<float, 4>(a, s)
+                       : (nt == 8 ? launch_grad<float, 8>(a, s) : launch_grad<float, 16>(a, s))));
+  else
+    POETX_TRY((nt == 4 ? launch_grad<H, 4>(a, s) : launch_grad<H, 8>(a, s)));
+  if (!c.dx || a.splits == 1) return POETX_OK;
+  const long long count = (long long)c.N * c.D;
+  return sum_partials(c.f32, c.dxp, a.splits, count, count, c.dx, s);
+}
+
+}  // namespace poetx

@@ -1304,7 +1304,7 @@ __global__ void __launch_bounds__(256)
   const long long step = (long long)gridDim.x * blockDim.x;
   for (long long i = (long long)blockIdx.x * blockDim.x + threadIdx.x; i < quads; i += step) {
     float4 a = *reinterpret_cast<const float4*>(part + 4 * i);
-        auto add = [&](auto n) {  // n partials in flight, added in order
+    auto add = [&](auto n) {  // n partials in flight, added in order
       constexpr int U = decltype(n)::value;
       for (int k0 = 1; k0 < S; k0 += U) {
         float4 b[U];
@@ -1651,19 +1651,23 @@ poetx_status grad_products(const GradProducts& c, cudaStream_t s) {
     POETX_TRY((gemm<false, 2>(mp, second, h, s)));
   else
     POETX_TRY((gemm<false, 1>(mp, second, h, s)));
-  if (c.dx && sums > 1) {
-    const long long quads = (long long)rows * c.D / 4;
-    const float* pp = c.dxp;
-    const long long stride = (long long)(c.fine ? BM : c_rows) * c.D;
-    if (c.f32)
-      POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, dim3(grid_for(quads, 256)), dim3(256), 0, s, pp,
-                                sums, stride, quads, static_cast<float*>(c.dx)));
-    else
-      POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, dim3(grid_for(quads, 256)), dim3(256), 0,
-                                s, pp, sums, stride, quads, static_cast<__nv_bfloat16*>(c.dx)));
-    POETX_CUDA_TRY(cudaGetLastError());
-    after_launch(s, ST_HEAD_ROW);
-  }
+  if (c.dx && sums > 1)
+    POETX_TRY(sum_partials(c.f32, c.dxp, sums, (long long)(c.fine ? BM : c_rows) * c.D,
+                           (long long)rows * c.D, c.dx, s));
+  return POETX_OK;
+}
+
+poetx_status sum_partials(bool f32, const float* part, int S, long long stride, long long count, void* out,
+                          cudaStream_t s) {
+  const dim3 grid(grid_for(count / 4, 256)), block(256);
+  if (f32)
+    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, grid, block, 0, s, part, S, stride, count / 4,
+                              static_cast<float*>(out)));
+  else
+    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, grid, block, 0, s, part, S, stride, count / 4,
+                              static_cast<__nv_bfloat16*>(out)));
+  POETX_CUDA_TRY(cudaGetLastError());
+  after_launch(s, ST_HEAD_ROW);
   return POETX_OK;
 }
 

@@ -236,4 +236,33 @@ int grad_splits(long long rows, int D, int V, bool f32);
 poetx_status split_pieces(const float* a, long long na, uint8_t* da, size_t a_step, const float* b,
                           long long nb, uint8_t* db, size_t b_step, cudaStream_t s);
 
+// out = the sum of S partial sums of `count` values (a multiple of 4), `stride` apart.
+poetx_status sum_partials(bool f32, const float* part, int S, long long stride, long long count, void* out,
+                          cudaStream_t s);
+
+// ---- ffn_rows.cu: the gated feed-forward block of few rows
+constexpr int kRowsForward = 32;
+struct RowsForward {  // fp32
+  const float *x, *W;
+  int N, D, F;
+  float *h, *z;     // [N][F], [N][2 F], each nullable
+  const float* dh;  // nullable; else dz [N][2 F] is what is wanted
+  float* dz;
+};
+poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s);
+bool rows_forward_fits(bool f32, int N);
+struct RowsGradients {
+  bool f32;
+  const void *dz, *dz2;  // [N][pitch] of V columns: fp32, or two bf16 pieces
+  long long pitch;
+  const void *x, *W;
+  int N, D, V;
+  void *dx, *dW;  // each nullable
+  int accumulate;
+  float* dxp;     // [rows_splits][N][D] where that is more than one
+};
+poetx_status rows_gradients(const RowsGradients& c, cudaStream_t s);
+bool rows_gradients_fit(bool f32, int N);
+int rows_splits(bool f32, int N, int D, int V);
+
 }  // namespace poetx

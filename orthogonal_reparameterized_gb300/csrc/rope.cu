@@ -74,19 +74,6 @@ __device__ __forceinline__ unsigned long long turns_of(float f) {
   return w < 1.0 ? (unsigned long long)(w * 18446744073709551616.0) : 0ull;
 }
 
-template <int B>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src) {
-  if constexpr (B == 8)
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
-  else
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
 // A lane's chunk of one head in one array: CH first and CH second elements of its pairs.
 template <typename T, int CH, bool INTER>
 struct Chunk {

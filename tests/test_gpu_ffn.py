@@ -236,3 +236,83 @@ def test_ffn_on_another_stream_and_in_a_graph(P):
     torch.cuda.synchronize()
     assert torch.equal(h, ref["h"].roll(1, 0)) and torch.equal(dx, ref["dx"].roll(1, 0))
     assert O.rel_fro(host(dW), host(ref["dW"])) <= 2 * R  # (other order of its sums)
+
+
+@pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
+@pytest.mark.parametrize("act", [B.SILU, B.GELU])
+@pytest.mark.parametrize("N,D,F", [
+    (1, 136, 808), (2, 264, 72), (3, 8, 4096), (4, 520, 200), (7, 1032, 24), (8, 128, 1000), (9, 136, 520),
+    (16, 2056, 328), (17, 72, 136), (32, 264, 392), (33, 264, 392),
+    # more column tiles than places on the GPU; few rows of W to a warp
+    (3, 40968, 16), (16, 20488, 8)])
+def test_ffn_f32_few_rows(P, N, D, F, act, kept):
+    x, W, dh = _ffn_inputs(N, D, F, "f32", 3 * N + D + F)
+    got = _run(P, x, W, dh, act, kept)
+    h, z = B.ffn(host(x), host(W), act)
+    dx, dW = B.ffn_bwd(host(x), host(W), host(dh), act)
+    assert O.rel_fro(host(got["z"]), z) <= TOL_F32
+    for k, ref in (("h", h), ("dx", dx), ("dW", dW)):
+        assert O.rel_fro(host(got[k]), ref) <= 2 * TOL_F32, k
+
+
+@pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
+@pytest.mark.parametrize("N,D,F", [(1, 264, 4096), (4, 72, 1000), (6, 4104, 72), (8, 2056, 520), (9, 264, 200),
+                                   (3, 40968, 16), (8, 8, 20000)])
+def test_ffn_bf16_few_rows(P, N, D, F, kept):
+    x, W, dh = _ffn_inputs(N, D, F, "bf16", 11 * N + D + F)
+    got = _run(P, x, W, dh, B.GELU, kept)
+    dx, dW = B.ffn_bwd(host(x), host(W), host(dh), B.GELU, host(got["z"]) if kept else None)
+    for k, ref in (("dx", dx), ("dW", dW)):
+        assert O.rel_fro(host(got[k]), ref) <= 2 * R + EXTRA, k
+
+
+@pytest.mark.parametrize("N,dt", [(1, "bf16"), (8, "bf16"), (2, "f32"), (8, "f32"), (15, "f32"), (25, "f32")])
+def test_ffn_options_few_rows(P, N, dt):
+    test_ffn_options(P, N, dt)
+
+
+@pytest.mark.parametrize("N,dt", [(7, "bf16"), (8, "f32"), (14, "f32"), (30, "f32")])
+def test_ffn_few_rows_on_their_own(P, N, dt):
+    """A NaN row of x and an infinite upstream gradient stay in their rows."""
+    x, W, dh = _ffn_inputs(N, 136, 264, dt, 23)
+    ref = _run(P, x, W, dh, B.SILU, False)
+    x[N - 1, 3] = float("nan")
+    got = _run(P, x, W, dh, B.SILU, False)
+    for k in ("h", "z", "dx"):
+        assert torch.isnan(got[k][N - 1]).all(), k
+        assert torch.equal(got[k][:N - 1], ref[k][:N - 1]), k
+    x, W, dh = _ffn_inputs(N, 136, 264, dt, 23)
+    dh[0, 9] = float("inf")
+    got = _run(P, x, W, dh, B.SILU, False)
+    rows = [i for i in range(528) if i not in (9, 273)]
+    assert torch.equal(got["dx"][1:], ref["dx"][1:]) and torch.equal(got["dW"][rows], ref["dW"][rows])
+    assert not torch.isfinite(got["dx"][0]).any() and not torch.isfinite(got["dW"][[9, 273]]).any()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_ffn_few_rows_leave_what_lies_behind(P, dt):
+    """Outputs inside larger arrays: nothing before or behind them is written, and the workspace ends
+    where its size says."""
+    N, D, F = 5, 72, 136
+    x, W, dh = (t.to(DEV) for t in _ffn_inputs(N, D, F, dt, 4))
+    T = DT[dt]
+    pad = 64
+
+    def room(*shape):
+        n = int(np.prod(shape))
+        flat = torch.full((n + 2 * pad,), 7.0, dtype=T, device=DEV)
+        return flat, flat[pad:pad + n].view(*shape)
+
+    fh, h = room(N, F)
+    fz, z = room(N, 2 * F)
+    fx, dx = room(N, D)
+    fw, dW = room(2 * F, D)
+    P.poetx_ffn_fwd(x, W, h, z=z)
+    for zz in (z, None):
+        n = P.poetx_ffn_bwd_workspace_bytes(P.F32 if dt == "f32" else P.BF16, N, D, F, zz is not None)
+        ws = torch.full((n + 256,), 0x5a, dtype=torch.uint8, device=DEV)
+        P.poetx_ffn_bwd(x, W, dh, z=zz, dx=dx, dW=dW, ws=ws[:n])
+        torch.cuda.synchronize()
+        assert (ws[n:] == 0x5a).all()
+    for flat in (fh, fz, fx, fw):
+        assert (flat[:pad] == 7).all() and (flat[-pad:] == 7).all()
