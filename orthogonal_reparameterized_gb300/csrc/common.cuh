@@ -465,6 +465,12 @@ __device__ __forceinline__ void mbar_arrive_cluster(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                : "memory");
 }
+// The arrival that hands TMEM back: the reads before it are complete (tcgen05.wait) and ordered by
+// tc_fence_before, and no other memory is passed on, so that the thread's writes need not be waited for.
+__device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t bar_cluster) {
+  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
+               : "memory");
+}
 // Every thread of every CTA of the cluster (release / acquire: shared-memory writes before it,
 // e.g. mbarrier initialisation, are visible to the other CTAs after it).
 __device__ __forceinline__ void cluster_sync() {

@@ -11,7 +11,7 @@
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
 // kept z, or in the epilogue of the same product run again), then the two products of the linear head's
 // gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows and the gradients
-// of up to 16 fp32 or 8 bf16 rows are ffn_rows.cu's.
+// of up to 16 fp32 or 4 to 8 bf16 rows are ffn_rows.cu's.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
@@ -451,7 +451,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[a], 0));
+        if (lane == 0) mbar_arrive_cluster_tmem(mapa_shared(&tempty[a], 0));
       }
       if (DZ && live) {  // (also where the products were given up: the copy must have landed at the end)
         const bool got = mbar_wait_bounded(dbar, dph, p.err, p.limit_ns, kSite + __LINE__);
@@ -1050,7 +1050,7 @@ Plan plan(poetx_dtype dt, int N, int D, int F, bool have_z, bool dx) {
   const size_t n = N > 0 ? N : 1;
   o.f32 = dt == POETX_F32;
   o.fine = !o.f32 && N <= kScoreRows;
-  o.rows = rows_gradients_fit(o.f32, (int)n);
+  o.rows = rows_gradients_fit(o.f32, (int)n, D, 2 * F);
   o.pieces = o.f32 ? (o.rows ? 0 : 3) : (o.fine ? 2 : 1);
   o.pitch = o.pieces ? (long long)align_up((size_t)2 * F, 64) : 2ll * F;
   o.splits = !dx ? 1 : (o.rows ? rows_splits(o.f32, (int)n, D, 2 * F) : grad_splits(n, D, 2 * F, o.f32));

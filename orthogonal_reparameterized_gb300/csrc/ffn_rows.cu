@@ -18,8 +18,7 @@
 // of the next eight rows ahead (with a ring of registers instead sixteen fp32 rows took 92 us, not 48: a wait
 // for one of several loads in flight is a wait for all of them).  The warps' sums of dx are joined in shared
 // memory, the CTAs' by the head's kernel for partial sums.  Sixteen fp32 rows of 2048 x 5632: 48 us (115 on
-// the tensor cores), four bf16 rows of 4096 x 14336 82 us (470 MB, 5.7 TB/s; 124), eight 115 us (by the
-// multiply-adds; 124, which is also what nine to 128 rows take there).
+// the tensor cores), four bf16 rows of 4096 x 14336 82 us (470 MB, 5.7 TB/s; 101 there).
 #include <algorithm>
 #include <mutex>
 #include <type_traits>
@@ -400,7 +399,12 @@ int tiles_of(bool f32, int N, int D) {
 }  // namespace
 
 bool rows_forward_fits(bool f32, int N) { return f32 && N <= kRowsForward; }
-bool rows_gradients_fit(bool f32, int N) { return N <= (f32 ? 16 : 8); }
+// (bf16 with five to eight rows is bound by the multiply-adds, and on the tensor cores by their tiles: 8 x
+// 1024 x 2816 takes 13.7 us here and 16.9 there, 8 x 2048 x 5632 30.0 and 32.9, 5 x 4096 x 4096 40.2 and
+// 41.9, but 8 x 4096 x 14336 115 and 104.)
+bool rows_gradients_fit(bool f32, int N, int D, int V) {
+  return N <= (f32 ? 16 : 4) || (!f32 && N <= 8 && (long long)V * D <= 1 << 25);
+}
 
 // CTAs over W's rows: as many as fill the SMs' places once or twice, whichever leaves fewer of them empty
 // (2048 columns in fp32 are 16 tiles: 9 splits fill 144 of 152 places, 19 all of two rounds), with sixteen

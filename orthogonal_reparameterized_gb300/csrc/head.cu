@@ -459,7 +459,7 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
         }
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(mapa_shared(&tempty[a], 0));
+        if (lane == 0) mbar_arrive_cluster_tmem(mapa_shared(&tempty[a], 0));
       }
       if (!ok) break;
       if (col0 >= d.N || (FINE && !d.a_mn ? q * 32 : row_w) >= d.M) continue;

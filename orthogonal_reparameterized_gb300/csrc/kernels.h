@@ -262,7 +262,7 @@ struct RowsGradients {
   float* dxp;     // [rows_splits][N][D] where that is more than one
 };
 poetx_status rows_gradients(const RowsGradients& c, cudaStream_t s);
-bool rows_gradients_fit(bool f32, int N);
+bool rows_gradients_fit(bool f32, int N, int D, int V);
 int rows_splits(bool f32, int N, int D, int V);
 
 }  // namespace poetx

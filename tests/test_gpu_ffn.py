@@ -257,7 +257,7 @@ def test_ffn_f32_few_rows(P, N, D, F, act, kept):
 
 @pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
 @pytest.mark.parametrize("N,D,F", [(1, 264, 4096), (4, 72, 1000), (6, 4104, 72), (8, 2056, 520), (9, 264, 200),
-                                   (3, 40968, 16), (8, 8, 20000)])
+                                   (3, 40968, 16), (8, 8, 20000), (7, 2056, 8200)])
 def test_ffn_bf16_few_rows(P, N, D, F, kept):
     x, W, dh = _ffn_inputs(N, D, F, "bf16", 11 * N + D + F)
     got = _run(P, x, W, dh, B.GELU, kept)
