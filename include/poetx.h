@@ -71,7 +71,7 @@ poetx_status poetx_get_device_error(cudaStream_t stream);
  * GEMM engine, 2 the CNP products, 3 the index kernels, 4 the self-test, 5 the fused
  * backward block-diagonal product, 6 the linear head's products,
  * 7 the layer norm's rings, forward and backward, 8 the gated feed-forward block's
- * projections), or 0 if none was recorded.  Host-only (no synchronisation); for diagnosis. */
+ * projections, 9 its gradients of few rows), or 0 if none was recorded.  Host-only (no synchronisation); for diagnosis. */
 int poetx_timeout_site(void);
 
 /* Self-test of the bounded-wait machinery: launches one block that waits on a shared-memory

@@ -10,8 +10,8 @@
 // CTA's), so that a row of the accumulator holds both g and u of its features and the epilogue forms h
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
 // kept z, or in the epilogue of the same product run again), then the two products of the linear head's
-// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows and the gradients
-// of up to 16 fp32 or 4 to 8 bf16 rows are ffn_rows.cu's.
+// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows and gradients
+// of up to 16 are ffn_rows.cu's, bf16 gradients of up to 64 rows ffn_grad.cu's.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
@@ -1038,7 +1038,7 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
 // The backward's workspace.
 struct Plan {
   bool f32, fine;
-  bool rows;        // so few rows that ffn_rows.cu has the gradients (dz in fp32, or in two bf16 pieces)
+  bool rows, few;   // so few rows that ffn_rows.cu (fp32) or ffn_grad.cu has the gradients
   bool direct;      // dz from the projections' sums (else from z, kept or written to the workspace)
   int pieces;       // bf16 pieces of dz (0: it is fp32)
   long long pitch;  // of dz: 2 F up to a multiple of 64
@@ -1050,10 +1050,14 @@ Plan plan(poetx_dtype dt, int N, int D, int F, bool have_z, bool dx) {
   const size_t n = N > 0 ? N : 1;
   o.f32 = dt == POETX_F32;
   o.fine = !o.f32 && N <= kScoreRows;
-  o.rows = rows_gradients_fit(o.f32, (int)n, D, 2 * F);
+  o.rows = o.f32 && N <= kRowsGradients;
+  o.few = !o.f32 && N <= kFewGradients;
   o.pieces = o.f32 ? (o.rows ? 0 : 3) : (o.fine ? 2 : 1);
   o.pitch = o.pieces ? (long long)align_up((size_t)2 * F, 64) : 2ll * F;
-  o.splits = !dx ? 1 : (o.rows ? rows_splits(o.f32, (int)n, D, 2 * F) : grad_splits(n, D, 2 * F, o.f32));
+  o.splits = !dx      ? 1
+             : o.rows ? rows_splits((int)n, D, 2 * F)
+             : o.few  ? few_splits((int)n, D, 2 * F)
+                      : grad_splits(n, D, 2 * F, o.f32);
   size_t at = 0;
   auto take = [&](size_t bytes) {
     const size_t a = at;
@@ -1067,8 +1071,8 @@ Plan plan(poetx_dtype dt, int N, int D, int F, bool have_z, bool dx) {
   o.z = have_z || o.direct ? 0 : take(n * 2 * F * dtype_size(dt));
   o.z_step = align_up(n * o.pitch * (o.pieces ? 2 : 4), 1024);
   o.dz = take((o.pieces ? o.pieces : 1) * o.z_step);
-  if (dx && (o.splits > 1 || (o.fine && !o.rows)))
-    o.dxp = take((size_t)o.splits * (o.rows ? n : align_up(n, 256)) * D * 4);
+  if (dx && (o.splits > 1 || o.fine))
+    o.dxp = take((size_t)o.splits * (o.rows || o.few ? n : align_up(n, 256)) * D * 4);
   o.bytes = at;
   return o;
 }
@@ -1132,7 +1136,7 @@ extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, cons
   if (!x || !W || !h || (need && !ws)) return POETX_ERR_ARG;
   if (ws_bytes < need) return POETX_ERR_WORKSPACE;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
-  if (rows_forward_fits(dt == POETX_F32, N))
+  if (dt == POETX_F32 && N <= kRowsForward)
     return rows_forward({static_cast<const float*>(x), static_cast<const float*>(W), N, D, F,
                          static_cast<float*>(h), static_cast<float*>(z), nullptr, nullptr},
                         act, stream);
@@ -1194,7 +1198,7 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   } else {
     if (!z) {
       z = w + pl.z;
-      if (rows_forward_fits(pl.f32, N))
+      if (pl.f32 && N <= kRowsForward)
         POETX_TRY(rows_forward({xf, wf, N, D, F, nullptr, reinterpret_cast<float*>(w + pl.z), nullptr, nullptr},
                                act, stream));
       else
@@ -1212,9 +1216,13 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   }
   float* const dxp = reinterpret_cast<float*>(w + pl.dxp);
   if (pl.rows)
-    return rows_gradients({pl.f32, w + pl.dz, w + pl.dz + pl.z_step, pl.pitch, x, W, N, D, 2 * F, dx, dW,
-                           accumulate, dxp},
+    return rows_gradients({reinterpret_cast<const float*>(w + pl.dz), xf, wf, N, D, 2 * F,
+                           static_cast<float*>(dx), static_cast<float*>(dW), accumulate, dxp},
                           stream);
+  if (pl.few)
+    return few_gradients({w + pl.dz, w + pl.dz + pl.z_step, pl.pitch, x, W, N, D, 2 * F, dx, dW, accumulate,
+                          dxp},
+                         stream);
   GradProducts g{};
   g.f32 = pl.f32;
   g.fine = pl.fine;

@@ -1,8 +1,8 @@
-// The gated feed-forward block (ffn.cu) for so few rows that its time is W's way through the SMs, on the
-// CUDA cores, in fp32 throughout.
+// The gated feed-forward block (ffn.cu) for so few fp32 rows that its time is W's way through the SMs, on the
+// CUDA cores:
 //
-//   forward (fp32):    z = x W^T, then h = a(g) u, or dz = [dh u a'(g) | dh a(g)] from the sums
-//   gradients (both):  dx = dz W,  dW = dz^T x
+//   forward:    z = x W^T, then h = a(g) u, or dz = [dh u a'(g) | dh a(g)] from the sums
+//   gradients:  dx = dz W,  dW = dz^T x
 //
 // Forward: a warp has the gate and value rows of two features, its lanes every 32nd float4 of them, and
 // multiplies them with up to eight tokens' x from shared memory (or L1); more tokens are further warps of the
@@ -12,16 +12,14 @@
 // the loads of x bound it, 32 bytes for each of W's 16; the tensor cores with W in three pieces 124 us).
 //
 // Gradients: both products in one pass over W's rows, which reads a row and writes the same row of dW.  A
-// lane has 8 or 16 bytes of columns with x's values and dx's sums for every token in registers, a warp an
-// equal share of the rows, and a row costs 2 N multiply-adds per column and no exchange; dz's values come
-// from shared memory, where the warp lays those of its next eight rows.  Each thread copies its own bytes
-// of the next eight rows ahead (with a ring of registers instead sixteen fp32 rows took 92 us, not 48: a wait
-// for one of several loads in flight is a wait for all of them).  The warps' sums of dx are joined in shared
-// memory, the CTAs' by the head's kernel for partial sums.  Sixteen fp32 rows of 2048 x 5632: 48 us (115 on
-// the tensor cores), four bf16 rows of 4096 x 14336 82 us (470 MB, 5.7 TB/s; 101 there).
+// lane has four columns with x's values and dx's sums for every token in registers, a warp an equal share of
+// the rows, and a row costs 2 N multiply-adds per column and no exchange; dz's values come from shared
+// memory, where the warp lays those of its next eight rows.  Each thread copies its own bytes of the next
+// eight rows ahead (with a ring of registers instead sixteen rows took 92 us, not 48: a wait for one of
+// several loads in flight is a wait for all of them).  The warps' sums of dx are joined in shared memory, the
+// CTAs' by the head's kernel for partial sums.  Sixteen rows of 2048 x 5632: 48 us (115 on the tensor cores).
 #include <algorithm>
 #include <mutex>
-#include <type_traits>
 
 #include "common.cuh"
 #include "gated.cuh"
@@ -118,8 +116,10 @@ __device__ __forceinline__ void rows_fwd_unit(const FwdArgs& p, int f0, int n0, 
   }
 }
 
+// (Without a bound on its registers eight tokens through L1 get two CTAs an SM, not three: 16 x 4096 x 14336 221
+// us instead of 182; with four, 261.)
 template <int NT, bool HERE>
-__global__ void __launch_bounds__(32 * fwd_warps(HERE), 1) rows_fwd_kernel(const FwdArgs p) {
+__global__ void __launch_bounds__(32 * fwd_warps(HERE), HERE ? 1 : 3) rows_fwd_kernel(const FwdArgs p) {
   extern __shared__ __align__(16) float4 x_here[];
   pdl_trigger();
   pdl_wait();
@@ -136,28 +136,27 @@ __global__ void __launch_bounds__(32 * fwd_warps(HERE), 1) rows_fwd_kernel(const
   // the groups of a pair side by side in one CTA: they meet W's lines in L1
   const int warp = threadIdx.x >> 5, teams = fwd_warps(HERE) / p.groups, team = warp / p.groups;
   if (team >= teams) return;
-  for (int pair = HERE ? team * gridDim.x + blockIdx.x : blockIdx.x * teams + team; 2 * pair < c.F;
-       pair += teams * gridDim.x)
-    rows_fwd_unit<NT, HERE>(p, 2 * pair, warp % p.groups * NT, lane, x_here);
+  const int n0 = warp % p.groups * NT;
+  if (HERE) {
+    for (int pair = team * gridDim.x + blockIdx.x; 2 * pair < c.F; pair += teams * gridDim.x)
+      rows_fwd_unit<NT, HERE>(p, 2 * pair, n0, lane, x_here);
+  } else if (const int pair = blockIdx.x * teams + team; 2 * pair < c.F) {
+    rows_fwd_unit<NT, HERE>(p, 2 * pair, n0, lane, x_here);
+  }
 }
 
 // ---------------------------------------------------------------- gradients
 constexpr int kGradWarps = 8;
 constexpr int kBatch = 8;  // rows whose dz a warp has in shared memory
 
-// Columns of a lane: 16 bytes of a row, in bf16 with more than four tokens 8.  That leaves x and dx of sixteen
-// fp32 tokens 128 registers and an SM one CTA, everything else 64 and two.  (16 bytes against 8: sixteen
-// fp32 tokens 47.9 and 56.8 us at 2048 x 5632, where the multiply-adds are most of it; eight bf16 tokens
-// 32.9 and 29.9 us.)
-template <typename T>
-constexpr int cols_of(int NT) { return sizeof(T) == 4 ? 4 : (NT > 4 ? 4 : 8); }
-template <typename T>
-constexpr int grad_ctas(int NT) { return NT * cols_of<T>(NT) > 32 ? 1 : 2; }  // of an SM
-template <typename T, bool ADD>
-constexpr int grad_smem(int NT) {  // two batches of W (and of dW), a batch's dz and the sums of dx of each warp
-  const int C = cols_of<T>(NT);
-  return kGradWarps * (2 * kBatch * 32 * C * (int)sizeof(T) * (ADD ? 2 : 1) +
-                       kBatch * NT * (int)sizeof(float2) + NT * 32 * C * (int)sizeof(float));
+// CTAs of an SM, by the registers that a lane's four columns of x and dx take per token.  (Two columns and two
+// CTAs for sixteen tokens: 56.8 us instead of 47.9 at 2048 x 5632.)
+constexpr int grad_ctas(int NT) { return NT > 8 ? 1 : 2; }
+// Shared memory of a CTA: two batches of W (and of dW), a batch's dz and the sums of dx of each warp.
+constexpr int kSlot = 32 * 16;                   // a warp's bytes of a row
+constexpr int kArray = 2 * kBatch * kSlot;
+constexpr int grad_smem(int NT, bool add) {
+  return kGradWarps * ((add ? 2 : 1) * kArray + kBatch * NT * (int)sizeof(float2) + NT * kSlot);
 }
 
 struct GradArgs {
@@ -166,82 +165,47 @@ struct GradArgs {
   int splits;  // CTAs over the rows
 };
 
-// A lane's columns of a row, fp32 or bf16 by their number.
-__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[2]) {
-  v[0] = make_float2(__uint_as_float(w.x), __uint_as_float(w.y));
-  v[1] = make_float2(__uint_as_float(w.z), __uint_as_float(w.w));
-}
-__device__ __forceinline__ float2 halves(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
-}
-__device__ __forceinline__ void unpack(const uint2& w, float2 (&v)[2]) {
-  v[0] = halves(w.x), v[1] = halves(w.y);
-}
-__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[4]) {
-  v[0] = halves(w.x), v[1] = halves(w.y), v[2] = halves(w.z), v[3] = halves(w.w);
-}
-template <typename T, int P>
-__device__ __forceinline__ void store(T* p, const float2 (&v)[P]) {
-  if constexpr (sizeof(T) == 4) {
-#pragma unroll
-    for (int j = 0; j < P; j += 2)
-      *reinterpret_cast<float4*>(p + 2 * j) = make_float4(v[j].x, v[j].y, v[j + 1].x, v[j + 1].y);
-  } else {
-    uint32_t w[P];
-#pragma unroll
-    for (int j = 0; j < P; ++j) w[j] = pack_bf16x2(v[j].x, v[j].y);
-    if constexpr (P == 4)
-      *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-    else
-      *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
-  }
-}
-
 // ADD: dW is added to what is there.
-template <typename T, int NT, bool ADD>
-__global__ void __launch_bounds__(32 * kGradWarps, grad_ctas<T>(NT))
-    rows_grad_kernel(const GradArgs p) {
-  constexpr int C = cols_of<T>(NT), P = C / 2;
-  constexpr int kBytes = C * sizeof(T);
-  using Vec = std::conditional_t<kBytes == 16, uint4, uint2>;
+template <int NT, bool ADD>
+__global__ void __launch_bounds__(32 * kGradWarps, grad_ctas(NT)) rows_grad_kernel(const GradArgs p) {
   extern __shared__ __align__(16) uint8_t smem[];
   pdl_trigger();
   pdl_wait();
   const RowsGradients& c = p.c;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int tile = blockIdx.x % p.tiles, split = blockIdx.x / p.tiles;
-  const int col = (tile * 32 + lane) * C;
+  const int col = (tile * 32 + lane) * 4;
   const bool mine = col < c.D, dx = c.dx != nullptr, dW = c.dW != nullptr;
   const long long part = (long long)split * kGradWarps + warp, parts = (long long)p.splits * kGradWarps;
   const int first = (int)(c.V * part / parts), end = (int)(c.V * (part + 1) / parts);
 
-  float2 x[NT][P], acc[NT][P] = {};
+  float2 x[NT][2], acc[NT][2] = {};
 #pragma unroll
   for (int n = 0; n < NT; ++n) {
-    Vec v{};
-    if (mine && n < c.N)
-      v = *reinterpret_cast<const Vec*>(static_cast<const T*>(c.x) + (long long)n * c.D + col);
-    unpack(v, x[n]);
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (mine && n < c.N) v = *reinterpret_cast<const float4*>(c.x + (long long)n * c.D + col);
+    x[n][0] = make_float2(v.x, v.y);
+    x[n][1] = make_float2(v.z, v.w);
   }
   // a thread's own bytes of each row: it copies them a batch ahead and reads them itself (a lane without
   // columns: the last ones', and stores nothing)
-  constexpr int kSlot = 32 * kBytes, kHalf = kBatch * kSlot, kArray = 2 * kHalf;
-  const int from = mine ? col : c.D - C;
-  uint8_t* const ring = smem + warp * (ADD ? 2 : 1) * kArray + lane * kBytes;
+  constexpr int kHalf = kBatch * kSlot;
+  const int from = mine ? col : c.D - 4;
+  uint8_t* const ring = smem + warp * (ADD ? 2 : 1) * kArray + lane * 16;
   const uint32_t ring_at = smem_u32(ring);
-  const T* const W_at = static_cast<const T*>(dx ? c.W : c.x) + from;
-  T* const dW_at = static_cast<T*>(c.dW) + from;
+  const float* const W_at = (dx ? c.W : c.x) + from;
+  float* const dW_at = c.dW + from;
   const long long step = dx ? c.D : 0;
   auto request = [&](int r, int half) {
     if (r < end) {
-      const T* w = W_at + r * step;
-      const T* g = dW_at + (long long)r * c.D;
+      const float* w = W_at + r * step;
+      const float* g = dW_at + (long long)r * c.D;
       const bool whole = r + kBatch <= end;
 #pragma unroll
       for (int k = 0; k < kBatch; ++k) {
         if (whole || r + k < end) {
-          copy_async<kBytes>(ring_at + half + k * kSlot, w);
-          if (ADD) copy_async<kBytes>(ring_at + kArray + half + k * kSlot, g);
+          copy_async<16>(ring_at + half + k * kSlot, w);
+          if (ADD) copy_async<16>(ring_at + kArray + half + k * kSlot, g);
         }
         w += step;
         g += c.D;
@@ -259,14 +223,7 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas<T>(NT))
     for (int m = 0; m < M; ++m) {
       const int n = (lane >> 3) + 4 * m;
       v[m] = 0.f;
-      if (n < c.N && r < end) {
-        const long long at = n * c.pitch + r;
-        if (sizeof(T) == 4)
-          v[m] = static_cast<const float*>(c.dz)[at];
-        else
-          v[m] = __bfloat162float(static_cast<const __nv_bfloat16*>(c.dz)[at]) +
-                 __bfloat162float(static_cast<const __nv_bfloat16*>(c.dz2)[at]);
-      }
+      if (n < c.N && r < end) v[m] = c.dz[(long long)n * c.V + r];
     }
   };
   constexpr int kRings = kGradWarps * (ADD ? 2 : 1) * kArray;
@@ -284,32 +241,29 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas<T>(NT))
     fetch(r0 + kBatch);
     request(r0 + kBatch, half ^ kHalf);
     copy_wait<1>();
-    T* out = dW_at + (long long)r0 * c.D;
+    float* out = dW_at + (long long)r0 * c.D;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
       if (r0 + k >= end) break;
-      float2 w[P], d[P];
       const uint8_t* const slot = ring + half + k * kSlot;
-      unpack(*reinterpret_cast<const Vec*>(slot), w);
-      if (ADD) {
-        unpack(*reinterpret_cast<const Vec*>(slot + kArray), d);
-      } else {
-#pragma unroll
-        for (int j = 0; j < P; ++j) d[j] = both(0.f);
-      }
+      const float4 wv = *reinterpret_cast<const float4*>(slot);
+      float4 g = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (ADD) g = *reinterpret_cast<const float4*>(slot + kArray);
+      const float2 w[2] = {make_float2(wv.x, wv.y), make_float2(wv.z, wv.w)};
+      float2 d[2] = {make_float2(g.x, g.y), make_float2(g.z, g.w)};
 #pragma unroll
       for (int n = 0; n < NT; n += 2) {
         const float4 two = *reinterpret_cast<const float4*>(dz + k * NT + n);
         const float2 s0 = make_float2(two.x, two.y), s1 = make_float2(two.z, two.w);
 #pragma unroll
-        for (int j = 0; j < P; ++j) {
+        for (int j = 0; j < 2; ++j) {
           d[j] = fma2(s0, x[n][j], d[j]);
           acc[n][j] = fma2(s0, w[j], acc[n][j]);
           d[j] = fma2(s1, x[n + 1][j], d[j]);
           acc[n + 1][j] = fma2(s1, w[j], acc[n + 1][j]);
         }
       }
-      if (mine && dW) store(out, d);
+      if (mine && dW) *reinterpret_cast<float4*>(out) = make_float4(d[0].x, d[0].y, d[1].x, d[1].y);
       out += c.D;
     }
   }
@@ -317,10 +271,11 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas<T>(NT))
 
   // [warp][token][column]
   float* const red = reinterpret_cast<float*>(smem + kRings + kGradWarps * kBatch * NT * sizeof(float2));
-  constexpr int kRow = 32 * C;
+  constexpr int kRow = 32 * 4;
 #pragma unroll
   for (int n = 0; n < NT; ++n)
-    store(red + (warp * NT + n) * kRow + lane * C, acc[n]);
+    *reinterpret_cast<float4*>(red + (warp * NT + n) * kRow + lane * 4) =
+        make_float4(acc[n][0].x, acc[n][0].y, acc[n][1].x, acc[n][1].y);
   __syncthreads();
   for (int i = threadIdx.x; i < NT * kRow / 4; i += 32 * kGradWarps) {
     const int n = i / (kRow / 4), q = i % (kRow / 4) * 4, at_col = tile * kRow + q;
@@ -334,14 +289,8 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas<T>(NT))
       s.z += b.z;
       s.w += b.w;
     }
-    if (p.splits > 1) {
-      *reinterpret_cast<float4*>(c.dxp + ((long long)split * c.N + n) * c.D + at_col) = s;
-    } else if (sizeof(T) == 4) {
-      *reinterpret_cast<float4*>(static_cast<float*>(c.dx) + (long long)n * c.D + at_col) = s;
-    } else {
-      *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(c.dx) + (long long)n * c.D + at_col) =
-          make_uint2(pack_bf16x2(s.x, s.y), pack_bf16x2(s.z, s.w));
-    }
+    float* const out = p.splits > 1 ? c.dxp + (long long)split * c.N * c.D : c.dx;
+    *reinterpret_cast<float4*>(out + (long long)n * c.D + at_col) = s;
   }
 }
 
@@ -372,46 +321,35 @@ poetx_status launch_fwd(const FwdArgs& a, cudaStream_t s) {
   return launch_fwd1<NT, false>(a, 0, s);
 }
 
-template <typename T, int NT, bool ADD>
+template <int NT, bool ADD>
 poetx_status launch_grad1(const GradArgs& a, cudaStream_t s) {
-  auto k = rows_grad_kernel<T, NT, ADD>;
+  auto k = rows_grad_kernel<NT, ADD>;
   static std::once_flag once;
   static cudaError_t attr = cudaSuccess;
   std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem<T, ADD>(NT));
+    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(NT, ADD));
   });
   POETX_CUDA_TRY(attr);
-  POETX_CUDA_TRY(launch_pdl(k, dim3(a.tiles * a.splits), dim3(32 * kGradWarps), grad_smem<T, ADD>(NT), s, a));
+  POETX_CUDA_TRY(launch_pdl(k, dim3(a.tiles * a.splits), dim3(32 * kGradWarps), grad_smem(NT, ADD), s, a));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_FFN_GEMM);
   return POETX_OK;
 }
-template <typename T, int NT>
+template <int NT>
 poetx_status launch_grad(const GradArgs& a, cudaStream_t s) {
-  return a.c.dW && a.c.accumulate ? launch_grad1<T, NT, true>(a, s) : launch_grad1<T, NT, false>(a, s);
+  return a.c.dW && a.c.accumulate ? launch_grad1<NT, true>(a, s) : launch_grad1<NT, false>(a, s);
 }
 
 int tokens_of(int N) { return N <= 4 ? 4 : (N <= 8 ? 8 : 16); }
-int tiles_of(bool f32, int N, int D) {
-  return ceil_div(D, 32 * (f32 ? cols_of<float>(tokens_of(N)) : cols_of<__nv_bfloat16>(tokens_of(N))));
-}
+int tiles_of(int D) { return ceil_div(D, 32 * 4); }
 
 }  // namespace
 
-bool rows_forward_fits(bool f32, int N) { return f32 && N <= kRowsForward; }
-// (bf16 with five to eight rows is bound by the multiply-adds, and on the tensor cores by their tiles: 8 x
-// 1024 x 2816 takes 13.7 us here and 16.9 there, 8 x 2048 x 5632 30.0 and 32.9, 5 x 4096 x 4096 40.2 and
-// 41.9, but 8 x 4096 x 14336 115 and 104.)
-bool rows_gradients_fit(bool f32, int N, int D, int V) {
-  return N <= (f32 ? 16 : 4) || (!f32 && N <= 8 && (long long)V * D <= 1 << 25);
-}
-
 // CTAs over W's rows: as many as fill the SMs' places once or twice, whichever leaves fewer of them empty
-// (2048 columns in fp32 are 16 tiles: 9 splits fill 144 of 152 places, 19 all of two rounds), with sixteen
-// rows to a warp at least.
-int rows_splits(bool f32, int N, int D, int V) {
-  const int tiles = tiles_of(f32, N, D), nt = tokens_of(N);
-  const int places = sm_count() * (f32 ? grad_ctas<float>(nt) : grad_ctas<__nv_bfloat16>(nt));
+// (2048 columns are 16 tiles: 9 splits fill 144 of 152 places, 19 all of two rounds), with sixteen rows to a
+// warp at least.
+int rows_splits(int N, int D, int V) {
+  const int tiles = tiles_of(D), places = sm_count() * grad_ctas(tokens_of(N));
   const int one = places / tiles, two = 2 * places / tiles;
   int s = 2 * one * 100 < two * 97 ? two : one;
   const int most = V / (16 * kGradWarps);
@@ -431,17 +369,15 @@ poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream
 }
 
 poetx_status rows_gradients(const RowsGradients& c, cudaStream_t s) {
-  const GradArgs a{c, tiles_of(c.f32, c.N, c.D), rows_splits(c.f32, c.N, c.D, c.V)};
-  const int nt = tokens_of(c.N);
-  using H = __nv_bfloat16;
-  if (c.f32)
-    POETX_TRY((nt == 4 ? launch_grad<float, 4>(a, s)
-                       : (nt == 8 ? launch_grad<float, 8>(a, s) : launch_grad<float, 16>(a, s))));
-  else
-    POETX_TRY((nt == 4 ? launch_grad<H, 4>(a, s) : launch_grad<H, 8>(a, s)));
+  const GradArgs a{c, tiles_of(c.D), rows_splits(c.N, c.D, c.V)};
+  switch (tokens_of(c.N)) {
+    case 4: POETX_TRY(launch_grad<4>(a, s)); break;
+    case 8: POETX_TRY(launch_grad<8>(a, s)); break;
+    default: POETX_TRY(launch_grad<16>(a, s));
+  }
   if (!c.dx || a.splits == 1) return POETX_OK;
   const long long count = (long long)c.N * c.D;
-  return sum_partials(c.f32, c.dxp, a.splits, count, count, c.dx, s);
+  return sum_partials(true, c.dxp, a.splits, count, count, c.dx, s);
 }
 
 }  // namespace poetx

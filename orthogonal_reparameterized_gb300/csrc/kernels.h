@@ -240,9 +240,9 @@ poetx_status split_pieces(const float* a, long long na, uint8_t* da, size_t a_st
 poetx_status sum_partials(bool f32, const float* part, int S, long long stride, long long count, void* out,
                           cudaStream_t s);
 
-// ---- ffn_rows.cu: the gated feed-forward block of few rows
-constexpr int kRowsForward = 32;
-struct RowsForward {  // fp32
+// ---- ffn_rows.cu: the gated feed-forward block of few fp32 rows
+constexpr int kRowsForward = 32;  // at most
+struct RowsForward {
   const float *x, *W;
   int N, D, F;
   float *h, *z;     // [N][F], [N][2 F], each nullable
@@ -250,19 +250,29 @@ struct RowsForward {  // fp32
   float* dz;
 };
 poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s);
-bool rows_forward_fits(bool f32, int N);
+constexpr int kRowsGradients = 16;
 struct RowsGradients {
-  bool f32;
-  const void *dz, *dz2;  // [N][pitch] of V columns: fp32, or two bf16 pieces
+  const float *dz, *x, *W;  // dz [N][V]
+  int N, D, V;
+  float *dx, *dW;  // each nullable
+  int accumulate;
+  float* dxp;      // [rows_splits][N][D] where that is more than one
+};
+poetx_status rows_gradients(const RowsGradients& c, cudaStream_t s);
+int rows_splits(int N, int D, int V);
+
+// ---- ffn_grad.cu: its gradients of few bf16 rows
+constexpr int kFewGradients = 64;
+struct FewGradients {
+  const void *dz, *dz2;  // its two pieces, [N][pitch] of V columns
   long long pitch;
   const void *x, *W;
   int N, D, V;
   void *dx, *dW;  // each nullable
   int accumulate;
-  float* dxp;     // [rows_splits][N][D] where that is more than one
+  float* dxp;     // [few_splits][N][D]
 };
-poetx_status rows_gradients(const RowsGradients& c, cudaStream_t s);
-bool rows_gradients_fit(bool f32, int N, int D, int V);
-int rows_splits(bool f32, int N, int D, int V);
+poetx_status few_gradients(const FewGradients& c, cudaStream_t s);
+int few_splits(int N, int D, int V);
 
 }  // namespace poetx

@@ -257,7 +257,11 @@ def test_ffn_f32_few_rows(P, N, D, F, act, kept):
 
 @pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
 @pytest.mark.parametrize("N,D,F", [(1, 264, 4096), (4, 72, 1000), (6, 4104, 72), (8, 2056, 520), (9, 264, 200),
-                                   (3, 40968, 16), (8, 8, 20000), (7, 2056, 8200)])
+                                   (3, 40968, 16), (8, 8, 20000), (7, 2056, 8200),
+                                   # units of 128 rows and columns: one of both, ends inside them, more
+                                   # blocks of columns than SMs, several jobs of a CTA
+                                   (64, 8, 8), (9, 128, 64), (16, 136, 72), (33, 1032, 4104), (12, 20488, 72),
+                                   (32, 72, 30008), (64, 2056, 1000), (20, 4104, 1416), (65, 264, 200)])
 def test_ffn_bf16_few_rows(P, N, D, F, kept):
     x, W, dh = _ffn_inputs(N, D, F, "bf16", 11 * N + D + F)
     got = _run(P, x, W, dh, B.GELU, kept)
@@ -266,12 +270,12 @@ def test_ffn_bf16_few_rows(P, N, D, F, kept):
         assert O.rel_fro(host(got[k]), ref) <= 2 * R + EXTRA, k
 
 
-@pytest.mark.parametrize("N,dt", [(1, "bf16"), (8, "bf16"), (2, "f32"), (8, "f32"), (15, "f32"), (25, "f32")])
+@pytest.mark.parametrize("N,dt", [(1, "bf16"), (8, "bf16"), (11, "bf16"), (64, "bf16"), (2, "f32"), (8, "f32"), (15, "f32"), (25, "f32")])
 def test_ffn_options_few_rows(P, N, dt):
     test_ffn_options(P, N, dt)
 
 
-@pytest.mark.parametrize("N,dt", [(7, "bf16"), (8, "f32"), (14, "f32"), (30, "f32")])
+@pytest.mark.parametrize("N,dt", [(7, "bf16"), (15, "bf16"), (50, "bf16"), (8, "f32"), (14, "f32"), (30, "f32")])
 def test_ffn_few_rows_on_their_own(P, N, dt):
     """A NaN row of x and an infinite upstream gradient stay in their rows."""
     x, W, dh = _ffn_inputs(N, 136, 264, dt, 23)
@@ -289,11 +293,11 @@ def test_ffn_few_rows_on_their_own(P, N, dt):
     assert not torch.isfinite(got["dx"][0]).any() and not torch.isfinite(got["dW"][[9, 273]]).any()
 
 
-@pytest.mark.parametrize("dt", ["bf16", "f32"])
-def test_ffn_few_rows_leave_what_lies_behind(P, dt):
+@pytest.mark.parametrize("N,dt", [(5, "bf16"), (21, "bf16"), (5, "f32")])
+def test_ffn_few_rows_leave_what_lies_behind(P, N, dt):
     """Outputs inside larger arrays: nothing before or behind them is written, and the workspace ends
     where its size says."""
-    N, D, F = 5, 72, 136
+    D, F = 72, 136
     x, W, dh = (t.to(DEV) for t in _ffn_inputs(N, D, F, dt, 4))
     T = DT[dt]
     pad = 64
