@@ -41,7 +41,8 @@ constexpr int kThreads = 32 * (3 + kEpiWarps);
 constexpr int kZWarp = 2 + kEpiWarps;
 constexpr int kWBytes = kUnit * kUnit * 2;
 constexpr int kBoxBytes = 32 * 128;     // a warp's 32 rows of 64 columns of dW
-// Units on their way (three: 86.5 us at 16 x 4096 x 14336 instead of 81, 22.6 at 9 x 2048 x 5632 instead of 23.3).
+// Units on their way.  (Three: 86.5 us at 16 x 4096 x 14336 instead of 81, 22.6 at 9 x 2048 x 5632 instead
+// of 23.3.)
 constexpr int kStages = 2;
 constexpr int z_bytes(int NT) { return 4 * NT * 128; }  // two pieces of two groups of 64 features
 constexpr int x_bytes(int NT) { return 2 * NT * 128; }  // two groups of 64 columns

@@ -320,3 +320,74 @@ def test_ffn_few_rows_leave_what_lies_behind(P, N, dt):
         assert (ws[n:] == 0x5a).all()
     for flat in (fh, fz, fx, fw):
         assert (flat[:pad] == 7).all() and (flat[-pad:] == 7).all()
+
+
+@pytest.mark.parametrize("N,dt", [(3, "f32"), (20, "f32"), (2, "bf16"), (40, "bf16")])
+def test_ffn_few_rows_at_once_and_captured(P, N, dt):
+    """Two streams at the same time, then two graphs that share a workspace, replayed after each other with
+    other inputs."""
+    x, W, dh = _ffn_inputs(N, 264, 1000, dt, N)
+    ref = _run(P, x, W, dh, B.SILU, False)
+    xd, Wd, dhd = x.to(DEV), W.to(DEV), dh.to(DEV)
+    outs = [[torch.zeros_like(ref[k]) for k in ("h", "dx", "dW")] for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(5):
+        for s, (h, dx, dW) in zip(streams, outs):
+            P.poetx_ffn_fwd(xd, Wd, h, stream=s)
+            P.poetx_ffn_bwd(xd, Wd, dhd, dx=dx, dW=dW, stream=s)
+    torch.cuda.synchronize()
+    for out in outs:
+        for k, t in zip(("h", "dx", "dW"), out):
+            assert torch.equal(t, ref[k]), k
+    code = P.F32 if dt == "f32" else P.BF16
+    n = max(P.poetx_ffn_fwd_workspace_bytes(code, N, 264, 1000),
+            P.poetx_ffn_bwd_workspace_bytes(code, N, 264, 1000, False))
+    ws = torch.empty(n, dtype=torch.uint8, device=DEV)
+    ins = [(xd.clone(), dhd.clone()) for _ in range(2)]
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for g, (xi, di), (h, dx, dW) in zip(graphs, ins, outs):
+        with torch.cuda.graph(g):
+            P.poetx_ffn_fwd(xi, Wd, h, ws=ws)
+            P.poetx_ffn_bwd(xi, Wd, di, dx=dx, dW=dW, ws=ws)
+    ins[1][0].copy_(xd * 2), ins[1][1].copy_(dhd * 0.5)
+    other = _run(P, x * 2, W, dh * 0.5, B.SILU, False)
+    for _ in range(2):
+        for t in outs[0] + outs[1]:
+            t.zero_()
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        for want, out in ((ref, outs[0]), (other, outs[1])):
+            for k, t in zip(("h", "dx", "dW"), out):
+                assert torch.equal(t, want[k]), k
+
+
+@pytest.mark.parametrize("N,dt", [(2, "f32"), (11, "f32"), (5, "bf16")])
+def test_ffn_few_rows_beyond_32_bits(P, N, dt):
+    """W and dW of more than 2^31 elements: the last rows are read, multiplied and written where they are."""
+    D, F, K = 16384, 70000, 8
+    T = DT[dt]
+    g = torch.Generator().manual_seed(N)
+    W = torch.zeros(2 * F, D, dtype=T, device=DEV)
+    last = [(torch.randn(K, D, generator=g) / 128).to(T) for _ in range(2)]
+    W[F - K:F], W[2 * F - K:] = last[0].to(DEV), last[1].to(DEV)
+    x = torch.randn(N, D, generator=g).to(T)
+    dh = torch.zeros(N, F, dtype=T)
+    dh[:, F - K:] = torch.randn(N, K, generator=g).to(T)
+    new = lambda *s: torch.full(s, float("nan"), dtype=T, device=DEV)
+    h, dx, dW = new(N, F), new(N, D), new(2 * F, D)
+    P.poetx_ffn_fwd(x.to(DEV), W, h)
+    P.poetx_ffn_bwd(x.to(DEV), W, dh.to(DEV), dx=dx, dW=dW)
+    torch.cuda.synchronize()
+    assert P.poetx_get_device_error() == 0
+    small = np.concatenate([host(last[0]), host(last[1])])
+    rh, _ = B.ffn(host(x), small, B.SILU)
+    rdx, rdW = B.ffn_bwd(host(x), small, host(dh[:, F - K:]), B.SILU)
+    tol = 2 * R + EXTRA if dt == "bf16" else 2 * TOL_F32
+    assert not h[:, :F - K].any() and O.rel_fro(host(h[:, F - K:]), rh) <= tol
+    assert O.rel_fro(host(dx), rdx) <= tol
+    got = np.concatenate([host(dW[F - K:F]), host(dW[2 * F - K:])])
+    assert O.rel_fro(got, rdW) <= tol
+    dW[F - K:F].zero_(), dW[2 * F - K:].zero_()
+    assert not dW.any()
