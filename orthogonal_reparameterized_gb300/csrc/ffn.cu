@@ -10,8 +10,8 @@
 // CTA's), so that a row of the accumulator holds both g and u of its features and the epilogue forms h
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
 // kept z, or in the epilogue of the same product run again), then the two products of the linear head's
-// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows and gradients
-// of up to 16 are ffn_rows.cu's, bf16 gradients of up to 64 rows ffn_grad.cu's.
+// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows (or
+// more of small blocks) and gradients of up to 16 are ffn_rows.cu's, bf16 gradients of up to 64 rows ffn_grad.cu's.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
@@ -1136,7 +1136,7 @@ extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, cons
   if (!x || !W || !h || (need && !ws)) return POETX_ERR_ARG;
   if (ws_bytes < need) return POETX_ERR_WORKSPACE;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
-  if (dt == POETX_F32 && N <= kRowsForward)
+  if (dt == POETX_F32 && rows_forward_fits(N, D, F))
     return rows_forward({static_cast<const float*>(x), static_cast<const float*>(W), N, D, F,
                          static_cast<float*>(h), static_cast<float*>(z), nullptr, nullptr},
                         act, stream);

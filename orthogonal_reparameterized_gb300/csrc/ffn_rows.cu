@@ -6,7 +6,7 @@
 //
 // Forward: a warp has the gate and value rows of two features, its lanes every 32nd float4 of them, and
 // multiplies them with up to eight tokens' x from shared memory (or L1); more tokens are further warps of the
-// same CTA, which find W's lines in L1.  The sums of a warp's 4 x 8 products are joined by halving: in each
+// same CTA (up to 32; beyond that further CTAs), which find W's lines in L1.  The sums of a warp's 4 x 8 products are joined by halving: in each
 // of five steps a lane gives half of its sums away and keeps the other half, so that 31 shuffles leave one
 // sum per lane.  One row of 4096 x 14336: 470 MB in 66.8 us (7.0 TB/s); sixteen of 2048 x 5632 36 us (92 MB:
 // the loads of x bound it, 32 bytes for each of W's 16; the tensor cores with W in three pieces 124 us).
@@ -32,19 +32,19 @@ namespace {
 // Warps of a CTA.  HERE: all of x is in the shared memory of one CTA per SM, else a warp reads it through L1.
 constexpr int fwd_warps(bool here) { return here ? 12 : 4; }
 constexpr int kGroup = 8;  // tokens of a warp at most
+constexpr int kBlock = 32;  // tokens of a CTA at most
 constexpr size_t kXBytes = 200 * 1024;
 
 struct FwdArgs {
   RowsForward c;
-  int groups;  // of tokens, at most four
+  int groups;  // of a block's tokens, at most four
   Act act;
 };
 
 // Two features' sums for the group's tokens.
 template <int NT, bool HERE>
-__device__ __forceinline__ void rows_fwd_unit(const FwdArgs& p, int f0, int n0, int lane,
+__device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int f0, int n0, int lane,
                                               const float4* x_here) {
-  const RowsForward& c = p.c;
   const int quads = c.D / 4;
   const float4* w[4];  // two gate rows, two value rows
 #pragma unroll
@@ -104,26 +104,34 @@ __device__ __forceinline__ void rows_fwd_unit(const FwdArgs& p, int f0, int n0, 
   if (lane >= 16 || lane % (32 / V) || n >= c.N) return;
   const long long at = (long long)n * 2 * c.F + f;
   if (c.dh) {
-    const float2 d = gated_grad<true>(g, u, c.dh[(long long)n * c.F + f], p.act);
+    const float2 d = gated_grad<true>(g, u, c.dh[(long long)n * c.F + f], act);
     c.dz[at] = d.x;
     c.dz[at + c.F] = d.y;
     return;
   }
-  if (c.h) c.h[(long long)n * c.F + f] = gated<true>(g, u, p.act);
+  if (c.h) c.h[(long long)n * c.F + f] = gated<true>(g, u, act);
   if (c.z) {
     c.z[at] = g;
     c.z[at + c.F] = u;
   }
 }
 
-// (Without a bound on its registers eight tokens through L1 get two CTAs an SM, not three: 16 x 4096 x 14336 221
-// us instead of 182; with four, 261.)
+// (Without a bound on its registers eight tokens through L1 get two CTAs an SM, not three: 16 x 4096 x 14336
+// 221 us instead of 182; with four, 261.)
 template <int NT, bool HERE>
 __global__ void __launch_bounds__(32 * fwd_warps(HERE), HERE ? 1 : 3) rows_fwd_kernel(const FwdArgs p) {
   extern __shared__ __align__(16) float4 x_here[];
   pdl_trigger();
   pdl_wait();
-  const RowsForward& c = p.c;
+  RowsForward c = p.c;  // of the block's tokens
+  if (const long long t0 = (long long)blockIdx.y * kBlock; t0 > 0) {
+    c.x += t0 * c.D;
+    if (c.h) c.h += t0 * c.F;
+    if (c.z) c.z += t0 * 2 * c.F;
+    if (c.dh) c.dh += t0 * c.F, c.dz += t0 * 2 * c.F;
+    c.N -= (int)t0;
+  }
+  if (c.N > kBlock) c.N = kBlock;
   const int lane = threadIdx.x & 31, quads = c.D / 4;
   if (HERE) {
     const float4* const x = reinterpret_cast<const float4*>(c.x);
@@ -135,13 +143,13 @@ __global__ void __launch_bounds__(32 * fwd_warps(HERE), HERE ? 1 : 3) rows_fwd_k
   }
   // the groups of a pair side by side in one CTA: they meet W's lines in L1
   const int warp = threadIdx.x >> 5, teams = fwd_warps(HERE) / p.groups, team = warp / p.groups;
-  if (team >= teams) return;
+  if (team >= teams || warp % p.groups * NT >= c.N) return;
   const int n0 = warp % p.groups * NT;
   if (HERE) {
     for (int pair = team * gridDim.x + blockIdx.x; 2 * pair < c.F; pair += teams * gridDim.x)
-      rows_fwd_unit<NT, HERE>(p, 2 * pair, n0, lane, x_here);
+      rows_fwd_unit<NT, HERE>(c, p.act, 2 * pair, n0, lane, x_here);
   } else if (const int pair = blockIdx.x * teams + team; 2 * pair < c.F) {
-    rows_fwd_unit<NT, HERE>(p, 2 * pair, n0, lane, x_here);
+    rows_fwd_unit<NT, HERE>(c, p.act, 2 * pair, n0, lane, x_here);
   }
 }
 
@@ -305,15 +313,17 @@ poetx_status launch_fwd1(const FwdArgs& a, size_t smem, cudaStream_t s) {
     });
     POETX_CUDA_TRY(attr);
   }
-  const int grid = HERE ? std::min(a.c.F / 2, sm_count()) : ceil_div(a.c.F / 2, fwd_warps(HERE) / a.groups);
-  POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(32 * fwd_warps(HERE)), smem, s, a));
+  const int blocks = ceil_div(a.c.N, kBlock), pairs = a.c.F / 2;
+  const int grid = HERE ? std::max(1, std::min(pairs, sm_count() / blocks))
+                        : ceil_div(pairs, fwd_warps(HERE) / a.groups);
+  POETX_CUDA_TRY(launch_pdl(k, dim3(grid, blocks), dim3(32 * fwd_warps(HERE)), smem, s, a));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_FFN_GEMM);
   return POETX_OK;
 }
 template <int NT>
 poetx_status launch_fwd(const FwdArgs& a, cudaStream_t s) {
-  const size_t x_bytes = (size_t)a.c.N * a.c.D * 4;
+  const size_t x_bytes = (size_t)std::min(a.c.N, kBlock) * a.c.D * 4;
   // From three rows on x in shared memory is faster (2048 x 5632: two rows 19.2 us there and 15.9 through
   // L1, four 20.2 and 26.3, eight 22.0 and 27.2, sixteen 36.3 and 42.4); what does not fit goes through L1.
   if constexpr (NT > 2)
@@ -357,8 +367,22 @@ int rows_splits(int N, int D, int V) {
   return s < 1 ? 1 : s;
 }
 
+// Beyond a block of tokens, with x in shared memory, the multiply-adds are the time (16 TFMA/s of whole
+// blocks, a pair of features another 256 columns); on the tensor cores it is two launches, the split of W and
+// a tile's K: 11 us + 2 F D / 577,000 + D / 40.  (64 x 1024 x 2816: 28.0 us here and 43.8 there, 90: 40.5 and
+// 44.2; 128 x 256 x 512: 5.8 and 18.2, 512: 15.0 and 18.4, 700: 21.2 and 18.3; 100 x 1024 x 64: 4.7 and 36.8;
+// 100 x 64 x 2816: 15.1 and 13.4; 60 x 1600 x 4264: 71.8 and 74.5, 70: 101 and 74.6.)  Up to 32 rows are always
+// here, also where x goes through L1 (33 x 4096 x 14336 438 us there, 32 here 344).
+bool rows_forward_fits(int N, int D, int F) {
+  if (N <= kRowsForward) return true;
+  const double tokens = (double)align_up((size_t)N, kBlock), rows = 2.0 * F;
+  return (size_t)kBlock * D * 4 <= kXBytes &&
+         tokens * rows * (D + 256) / 16e6 < 11 + rows * D / 577e3 + D / 40.0;
+}
+
 poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s) {
-  const int nt = c.N == 1 ? 1 : (c.N == 2 ? 2 : (c.N <= 4 ? 4 : kGroup)), groups = ceil_div(c.N, nt);
+  const int nt = c.N == 1 ? 1 : (c.N == 2 ? 2 : (c.N <= 4 ? 4 : kGroup));
+  const int groups = ceil_div(std::min(c.N, kBlock), nt);
   const FwdArgs a{c, groups, act_of(act)};
   switch (nt) {
     case 1: return launch_fwd<1>(a, s);

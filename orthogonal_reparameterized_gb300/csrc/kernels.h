@@ -241,7 +241,8 @@ poetx_status sum_partials(bool f32, const float* part, int S, long long stride, 
                           cudaStream_t s);
 
 // ---- ffn_rows.cu: the gated feed-forward block of few fp32 rows
-constexpr int kRowsForward = 32;  // at most
+constexpr int kRowsForward = 32;  // at most, or by the size of the block
+bool rows_forward_fits(int N, int D, int F);
 struct RowsForward {
   const float *x, *W;
   int N, D, F;

@@ -243,6 +243,8 @@ def test_ffn_on_another_stream_and_in_a_graph(P):
 @pytest.mark.parametrize("N,D,F", [
     (1, 136, 808), (2, 264, 72), (3, 8, 4096), (4, 520, 200), (7, 1032, 24), (8, 128, 1000), (9, 136, 520),
     (16, 2056, 328), (17, 72, 136), (32, 264, 392), (33, 264, 392),
+    # several blocks of tokens, the last of one token or seven
+    (64, 136, 72), (65, 1032, 40), (199, 264, 520), (512, 64, 64), (97, 1600, 8),
     # more column tiles than places on the GPU; few rows of W to a warp
     (3, 40968, 16), (16, 20488, 8)])
 def test_ffn_f32_few_rows(P, N, D, F, act, kept):
