@@ -10,8 +10,8 @@
 // CTA's), so that a row of the accumulator holds both g and u of its features and the epilogue forms h
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
 // kept z, or in the epilogue of the same product run again), then the two products of the linear head's
-// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows (or
-// more of small blocks) and gradients of up to 16 are ffn_rows.cu's, bf16 gradients of up to 64 rows ffn_grad.cu's.
+// gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows (or more of small
+// blocks) and gradients of up to 16 are ffn_rows.cu's, bf16 gradients of up to 64 rows ffn_grad.cu's.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's

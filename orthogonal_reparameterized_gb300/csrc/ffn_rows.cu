@@ -6,10 +6,11 @@
 //
 // Forward: a warp has the gate and value rows of two features, its lanes every 32nd float4 of them, and
 // multiplies them with up to eight tokens' x from shared memory (or L1); more tokens are further warps of the
-// same CTA (up to 32; beyond that further CTAs), which find W's lines in L1.  The sums of a warp's 4 x 8 products are joined by halving: in each
-// of five steps a lane gives half of its sums away and keeps the other half, so that 31 shuffles leave one
-// sum per lane.  One row of 4096 x 14336: 470 MB in 66.8 us (7.0 TB/s); sixteen of 2048 x 5632 36 us (92 MB:
-// the loads of x bound it, 32 bytes for each of W's 16; the tensor cores with W in three pieces 124 us).
+// same CTA (up to 32; beyond that further CTAs), which find W's lines in L1.  The sums of a warp's 4 x 8
+// products are joined by halving: in each of five steps a lane gives half of its sums away and keeps the
+// other half, so that 31 shuffles leave one sum per lane.  One row of 4096 x 14336: 470 MB in 66.8 us (7.0
+// TB/s); sixteen of 2048 x 5632 36 us (92 MB: the loads of x bound it, 32 bytes for each of W's 16; the tensor
+// cores with W in three pieces 124 us).
 //
 // Gradients: both products in one pass over W's rows, which reads a row and writes the same row of dW.  A
 // lane has four columns with x's values and dx's sums for every token in registers, a warp an equal share of
