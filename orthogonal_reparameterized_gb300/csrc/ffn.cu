@@ -1120,6 +1120,9 @@ extern "C" poetx_status poetx_glu_bwd(poetx_dtype dt, poetx_activation act, cons
 
 extern "C" size_t poetx_ffn_fwd_workspace_bytes(poetx_dtype dt, int N, int D, int F) {
   if (!shape_ok(dt, N, D, F) || dt != POETX_F32) return 0;
+  // (Few rows need none of W's pieces, and none of x's: but so an fp32 call without a workspace is refused at
+  // every N.)
+  if (N <= kRowsForward) return 3 * piece_step((size_t)(N > 0 ? N : 1) * D);
   return 3 * (piece_step((size_t)(N > 0 ? N : 1) * D) + piece_step((size_t)2 * F * D));
 }
 
