@@ -9,8 +9,8 @@
 // same CTA (up to 32; beyond that further CTAs), which find W's lines in L1.  The sums of a warp's 4 x 8
 // products are joined by halving: in each of five steps a lane gives half of its sums away and keeps the
 // other half, so that 31 shuffles leave one sum per lane.  One row of 4096 x 14336: 470 MB in 66.8 us (7.0
-// TB/s); sixteen of 2048 x 5632 36 us (92 MB: the loads of x bound it, 32 bytes for each of W's 16; the tensor
-// cores with W in three pieces 124 us).
+// TB/s), eight 70 us; sixteen of 2048 x 5632 28.5 us (92 MB: shared memory bounds it, 128 bytes of x for each
+// of W's 64 that are copied in and read; the tensor cores with W in three pieces 124 us).
 //
 // Gradients: both products in one pass over W's rows, which reads a row and writes the same row of dW.  A
 // lane has four columns with x's values and dx's sums for every token in registers, a warp an equal share of
@@ -30,54 +30,95 @@ namespace poetx {
 namespace {
 
 // ---------------------------------------------------------------- forward
-// Warps of a CTA.  HERE: all of x is in the shared memory of one CTA per SM, else a warp reads it through L1.
-constexpr int fwd_warps(bool here) { return here ? 12 : 4; }
+// Warps of a CTA.  RING: all of x is in the shared memory of one CTA per SM, and so many steps of 128 columns
+// of a warp's rows of W are on their way there; 0: a warp reads both through L1.
+constexpr int fwd_warps(int ring) { return ring ? 12 : 4; }
 constexpr int kGroup = 8;  // tokens of a warp at most
 constexpr int kBlock = 32;  // tokens of a CTA at most
-constexpr size_t kXBytes = 200 * 1024;
+constexpr int kStepBytes = 4 * 512;  // a warp's 128 columns of four rows
+constexpr size_t ring_bytes(int ring) { return (size_t)fwd_warps(ring) * ring * kStepBytes; }
+constexpr size_t x_room(int ring) { return 226 * 1024 - ring_bytes(ring); }
 
 struct FwdArgs {
   RowsForward c;
   int groups;  // of a block's tokens, at most four
+  int x_bytes;  // of a block (RING)
   Act act;
 };
 
 // Two features' sums for the group's tokens.
-template <int NT, bool HERE>
+template <int NT, int RING>
 __device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int f0, int n0, int lane,
-                                              const float4* x_here) {
-  const int quads = c.D / 4;
-  const float4* w[4];  // two gate rows, two value rows
-#pragma unroll
-  for (int r = 0; r < 4; ++r)
-    w[r] = reinterpret_cast<const float4*>(c.W) + (long long)(f0 + (r & 1) + (r >> 1) * c.F) * quads;
-  // (a token beyond the last: the last one's, and its sums are not stored)
-  const float4* x[NT];
-  int x_at[NT];
-#pragma unroll
-  for (int n = 0; n < NT; ++n) {
-    x_at[n] = min(n0 + n, c.N - 1) * quads;
-    x[n] = reinterpret_cast<const float4*>(c.x) + x_at[n];
-  }
+                                              const float4* x_here, const uint8_t* ring) {
   float2 acc[4][NT] = {};
-  constexpr int U = 2;
-  for (int q0 = lane; q0 < quads; q0 += 32 * U) {
-    float4 wv[U][4];
+  const int quads = c.D / 4;
+  if constexpr (RING > 0) {
+    // the lane's columns are lane * 4 and every 128th from there; it copies its own bytes and reads them itself
+    const int steps = (quads - lane + 31) / 32;
+    const uint32_t ring_at = smem_u32(ring);
+    const float4* const g = reinterpret_cast<const float4*>(c.W) + (long long)f0 * quads + lane;
+    const float4* const u = g + (long long)c.F * quads;
+    auto request = [&](int k) {  // two gate rows, two value rows
+      if (k < steps) {
+        const uint32_t at = ring_at + k % RING * kStepBytes;
+        copy_async<16>(at, g + 32 * k);
+        copy_async<16>(at + 512, g + 32 * k + quads);
+        copy_async<16>(at + 1024, u + 32 * k);
+        copy_async<16>(at + 1536, u + 32 * k + quads);
+      }
+      copy_commit();
+    };
 #pragma unroll
-    for (int k = 0; k < U; ++k)
+    for (int k = 0; k < RING - 1; ++k) request(k);
+    int x_at[NT];  // (a token beyond the last: the last one's, and its sums are not stored)
+#pragma unroll
+    for (int n = 0; n < NT; ++n) x_at[n] = min(n0 + n, c.N - 1) * quads + lane;
+    for (int k = 0; k < steps; ++k) {
+      request(k + RING - 1);
+      copy_wait<RING - 1>();
+      float4 wv[4];
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        if (q0 + 32 * k < quads) wv[k][r] = w[r][q0 + 32 * k];
-#pragma unroll
-    for (int k = 0; k < U; ++k) {
-      if (q0 + 32 * k >= quads) break;
+        wv[r] = *reinterpret_cast<const float4*>(ring + k % RING * kStepBytes + 512 * r);
 #pragma unroll
       for (int n = 0; n < NT; ++n) {
-        const float4 xv = HERE ? x_here[x_at[n] + q0 + 32 * k] : x[n][q0 + 32 * k];
+        const float4 xv = x_here[x_at[n] + 32 * k];
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-          acc[r][n] = fma2(make_float2(wv[k][r].x, wv[k][r].y), make_float2(xv.x, xv.y), acc[r][n]);
-          acc[r][n] = fma2(make_float2(wv[k][r].z, wv[k][r].w), make_float2(xv.z, xv.w), acc[r][n]);
+          acc[r][n] = fma2(make_float2(wv[r].x, wv[r].y), make_float2(xv.x, xv.y), acc[r][n]);
+          acc[r][n] = fma2(make_float2(wv[r].z, wv[r].w), make_float2(xv.z, xv.w), acc[r][n]);
+        }
+      }
+    }
+    copy_wait<0>();
+  } else {
+    const float4* w[4];  // two gate rows, two value rows
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      w[r] = reinterpret_cast<const float4*>(c.W) + (long long)(f0 + (r & 1) + (r >> 1) * c.F) * quads;
+    const float4* x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      x[n] = reinterpret_cast<const float4*>(c.x) + (long long)min(n0 + n, c.N - 1) * quads;
+    constexpr int U = 2;
+    for (int q0 = lane; q0 < quads; q0 += 32 * U) {
+      float4 wv[U][4];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (q0 + 32 * k < quads) wv[k][r] = w[r][q0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (q0 + 32 * k >= quads) break;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          const float4 xv = x[n][q0 + 32 * k];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            acc[r][n] = fma2(make_float2(wv[k][r].x, wv[k][r].y), make_float2(xv.x, xv.y), acc[r][n]);
+            acc[r][n] = fma2(make_float2(wv[k][r].z, wv[k][r].w), make_float2(xv.z, xv.w), acc[r][n]);
+          }
         }
       }
     }
@@ -119,8 +160,8 @@ __device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int
 
 // (Without a bound on its registers eight tokens through L1 get two CTAs an SM, not three: 16 x 4096 x 14336
 // 221 us instead of 182; with four, 261.)
-template <int NT, bool HERE>
-__global__ void __launch_bounds__(32 * fwd_warps(HERE), HERE ? 1 : 3) rows_fwd_kernel(const FwdArgs p) {
+template <int NT, int RING>
+__global__ void __launch_bounds__(32 * fwd_warps(RING), RING ? 1 : 3) rows_fwd_kernel(const FwdArgs p) {
   extern __shared__ __align__(16) float4 x_here[];
   pdl_trigger();
   pdl_wait();
@@ -134,23 +175,25 @@ __global__ void __launch_bounds__(32 * fwd_warps(HERE), HERE ? 1 : 3) rows_fwd_k
   }
   if (c.N > kBlock) c.N = kBlock;
   const int lane = threadIdx.x & 31, quads = c.D / 4;
-  if (HERE) {
+  if (RING) {
     const float4* const x = reinterpret_cast<const float4*>(c.x);
-    for (int i = threadIdx.x; i < c.N * quads; i += 32 * fwd_warps(HERE))
+    for (int i = threadIdx.x; i < c.N * quads; i += 32 * fwd_warps(RING))
       copy_async<16>(smem_u32(x_here + i), x + i);
     copy_commit();
     copy_wait<0>();
     __syncthreads();
   }
   // the groups of a pair side by side in one CTA: they meet W's lines in L1
-  const int warp = threadIdx.x >> 5, teams = fwd_warps(HERE) / p.groups, team = warp / p.groups;
+  const int warp = threadIdx.x >> 5, teams = fwd_warps(RING) / p.groups, team = warp / p.groups;
   if (team >= teams || warp % p.groups * NT >= c.N) return;
   const int n0 = warp % p.groups * NT;
-  if (HERE) {
+  const uint8_t* const ring =
+      reinterpret_cast<const uint8_t*>(x_here) + p.x_bytes + warp * RING * kStepBytes + lane * 16;
+  if (RING) {
     for (int pair = team * gridDim.x + blockIdx.x; 2 * pair < c.F; pair += teams * gridDim.x)
-      rows_fwd_unit<NT, HERE>(c, p.act, 2 * pair, n0, lane, x_here);
+      rows_fwd_unit<NT, RING>(c, p.act, 2 * pair, n0, lane, x_here, ring);
   } else if (const int pair = blockIdx.x * teams + team; 2 * pair < c.F) {
-    rows_fwd_unit<NT, HERE>(c, p.act, 2 * pair, n0, lane, x_here);
+    rows_fwd_unit<NT, RING>(c, p.act, 2 * pair, n0, lane, x_here, ring);
   }
 }
 
@@ -303,33 +346,41 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas(NT)) rows_grad_kern
   }
 }
 
-template <int NT, bool HERE>
-poetx_status launch_fwd1(const FwdArgs& a, size_t smem, cudaStream_t s) {
-  auto k = rows_fwd_kernel<NT, HERE>;
-  if (HERE) {
+template <int NT, int RING>
+poetx_status launch_fwd1(const FwdArgs& a, cudaStream_t s) {
+  auto k = rows_fwd_kernel<NT, RING>;
+  size_t smem = 0;
+  if (RING) {
     static std::once_flag once;
     static cudaError_t attr = cudaSuccess;
     std::call_once(once, [&] {
-      attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kXBytes);
+      attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  (int)(x_room(RING) + ring_bytes(RING)));
     });
     POETX_CUDA_TRY(attr);
+    smem = a.x_bytes + ring_bytes(RING);
   }
   const int blocks = ceil_div(a.c.N, kBlock), pairs = a.c.F / 2;
-  const int grid = HERE ? std::max(1, std::min(pairs, sm_count() / blocks))
-                        : ceil_div(pairs, fwd_warps(HERE) / a.groups);
-  POETX_CUDA_TRY(launch_pdl(k, dim3(grid, blocks), dim3(32 * fwd_warps(HERE)), smem, s, a));
+  const int grid = RING ? std::max(1, std::min(pairs, sm_count() / blocks))
+                        : ceil_div(pairs, fwd_warps(RING) / a.groups);
+  POETX_CUDA_TRY(launch_pdl(k, dim3(grid, blocks), dim3(32 * fwd_warps(RING)), smem, s, a));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_FFN_GEMM);
   return POETX_OK;
 }
 template <int NT>
-poetx_status launch_fwd(const FwdArgs& a, cudaStream_t s) {
+poetx_status launch_fwd(FwdArgs a, cudaStream_t s) {
   const size_t x_bytes = (size_t)std::min(a.c.N, kBlock) * a.c.D * 4;
   // From three rows on x in shared memory is faster (2048 x 5632: two rows 19.2 us there and 15.9 through
-  // L1, four 20.2 and 26.3, eight 22.0 and 27.2, sixteen 36.3 and 42.4); what does not fit goes through L1.
-  if constexpr (NT > 2)
-    if (x_bytes <= kXBytes) return launch_fwd1<NT, true>(a, x_bytes, s);
-  return launch_fwd1<NT, false>(a, 0, s);
+  // L1, four 17.1 and 26.3, eight 18.1 and 27.2, sixteen 28.7 and 42.4), with four steps of W on their way, or
+  // with two (20, 21 and 34 us) where x leaves no room for four; what does not fit goes through L1.
+  if constexpr (NT > 2) {
+    if (x_bytes <= x_room(2)) {
+      a.x_bytes = (int)x_bytes;
+      return x_bytes <= x_room(4) ? launch_fwd1<NT, 4>(a, s) : launch_fwd1<NT, 2>(a, s);
+    }
+  }
+  return launch_fwd1<NT, 0>(a, s);
 }
 
 template <int NT, bool ADD>
@@ -370,21 +421,21 @@ int rows_splits(int N, int D, int V) {
 
 // Beyond a block of tokens, with x in shared memory, the multiply-adds are the time (16 TFMA/s of whole
 // blocks, a pair of features another 256 columns); on the tensor cores it is two launches, the split of W and
-// a tile's K: 11 us + 2 F D / 577,000 + D / 40.  (64 x 1024 x 2816: 28.0 us here and 43.8 there, 90: 40.5 and
-// 44.2; 128 x 256 x 512: 5.8 and 18.2, 512: 15.0 and 18.4, 700: 21.2 and 18.3; 100 x 1024 x 64: 4.7 and 36.8;
-// 100 x 64 x 2816: 15.1 and 13.4; 60 x 1600 x 4264: 71.8 and 74.5, 70: 101 and 74.6.)  Up to 32 rows are always
+// a tile's K: 11 us + 2 F D / 577,000 + D / 40.  (64 x 1024 x 2816: 27.1 us here and 43.8 there, 90: 38.4
+// and 44.2; 128 x 256 x 512: 6.2 and 18.2, 512: 16.0 and 18.4, 700: 21 and 18.3; 100 x 1024 x 64: 4.4 and 36.8;
+// 100 x 64 x 2816: 15.1 and 13.4.)  Up to 32 rows are always
 // here, also where x goes through L1 (33 x 4096 x 14336 438 us there, 32 here 344).
 bool rows_forward_fits(int N, int D, int F) {
   if (N <= kRowsForward) return true;
   const double tokens = (double)align_up((size_t)N, kBlock), rows = 2.0 * F;
-  return (size_t)kBlock * D * 4 <= kXBytes &&
+  return (size_t)kBlock * D * 4 <= x_room(2) &&
          tokens * rows * (D + 256) / 16e6 < 11 + rows * D / 577e3 + D / 40.0;
 }
 
 poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s) {
   const int nt = c.N == 1 ? 1 : (c.N == 2 ? 2 : (c.N <= 4 ? 4 : kGroup));
   const int groups = ceil_div(std::min(c.N, kBlock), nt);
-  const FwdArgs a{c, groups, act_of(act)};
+  const FwdArgs a{c, groups, 0, act_of(act)};
   switch (nt) {
     case 1: return launch_fwd<1>(a, s);
     case 2: return launch_fwd<2>(a, s);
