@@ -335,6 +335,16 @@ __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap* map) {
   asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
 }
 
+// Hands registers of the warpgroup's threads back, or takes them (N a thread from here on; both shares
+// together are what the block was launched with).
+template <int N>
+__device__ __forceinline__ void regs_give() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_take() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
 // Shared-memory writes of this thread (generic proxy) made visible to the tensor cores and
 // TMA (async proxy).
 __device__ __forceinline__ void fence_async_shared() {

@@ -214,7 +214,11 @@ constexpr int BF = 128;  // features per pair tile: 128 gate and 128 value colum
 constexpr int BK = 64;
 constexpr int kStages = 5;
 constexpr int kEpiWarps = 8;  // two per TMEM lane quarter, each 64 features
-constexpr int kThreads = 32 * (2 + kEpiWarps);
+constexpr int kEpiWarp0 = 4;  // (whole warpgroups for the split of the registers)
+constexpr int kThreads = 32 * (kEpiWarp0 + kEpiWarps);
+// Registers: 168 a thread at the launch, of which the first warpgroup keeps 72 and the epilogue's get 216.
+constexpr int kFewRegs = 72, kManyRegs = 216;
+static_assert(kFewRegs * 128 + kManyRegs * 32 * kEpiWarps == 168 * kThreads, "registers");
 constexpr uint32_t kABytes = BM * BK * 2;
 constexpr uint32_t kStageBytes = 2 * kABytes;
 constexpr uint32_t kStgBytes = 32 * 128;  // one epilogue warp's box: 32 rows of 128 bytes
@@ -271,8 +275,8 @@ __device__ __forceinline__ void tile_at(const FfnGemm& p, int t, int* mi, int* f
 
 // Bands of 16 row tiles as in the head's products; five stages of 32 KB leave room for two boxes a warp.
 // Warp 0 of each CTA loads its 128 rows of x and its 128 rows of W, one thread of the even CTA's warp 1
-// issues the MMAs, warps 2-9 read the accumulators back (warp w: rows 32 (w % 4).. of the CTA's 128,
-// features 64 ((w - 2) / 4).. of the tile's 128: their gates and their values).
+// issues the MMAs, warps 4-11 read the accumulators back (warp w: rows 32 (w % 4).. of the CTA's 128,
+// features 64 ((w - 4) / 4).. of the tile's 128: their gates and their values).
 // DZ: the backward without kept projections.  The epilogue turns the fp32 sums into dz with the warp's box of
 // dh, which arrives by TMA in one of the warp's two staging boxes while the products run, so that the
 // projections are neither rounded nor stored.
@@ -328,85 +332,89 @@ __global__ void __launch_bounds__(kThreads, 1)
     return ring_wait(bar, parity, abort_flag, p.err, p.limit_ns, site);
   };
 
-  if (warp == 0 && lane == 0) {
-    // ------------------------------------------------------------ TMA producer
-    Ring<kStages> rg;
-    bool ok = true;
-    long long issued = 0;
-    const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
-    const CUtensorMap* const wm = crank ? maps.u : maps.g;
-    for (int t = t0; t < p.num_tiles && ok; t += t_step) {
-      int mi, fi;
-      tile_at(p, t, &mi, &fi);
-      const int row = (2 * mi + crank) * BM, col = fi * BF;
-      for (int c0 = 0; c0 < p.num_kb && ok; c0 += p.chunk) {
-        const int len = min(p.num_kb - c0, p.chunk);
-        int sg = 0, i = 0;  // a chunk's K blocks once per pair of pieces
-        for (int j = 0; j < len * SEGS; ++j, rg.next(), ++issued) {
-          if (!wait(&empty[rg.s], rg.ph ^ 1, kSite + __LINE__)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = smem + rg.s * kStageBytes;
-          if (crank == 0) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
-          const uint32_t fb = full0 + rg.s * 8;
-          const int k = (c0 + i) * BK;
-          tma_load_2d_pair(dst, F32 ? &maps.a[SEG_X[sg]] : maps.a, fb, k, row);
-          tma_load_2d_pair(dst + kABytes, F32 ? wm + SEG_W[sg] : wm, fb, k, col);
-          if (++i == len) {
-            i = 0;
-            ++sg;
+  if (warp < kEpiWarp0) {
+    regs_give<kFewRegs>();
+    if (warp == 0 && lane == 0) {
+      // ------------------------------------------------------------ TMA producer
+      Ring<kStages> rg;
+      bool ok = true;
+      long long issued = 0;
+      const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
+      const CUtensorMap* const wm = crank ? maps.u : maps.g;
+      for (int t = t0; t < p.num_tiles && ok; t += t_step) {
+        int mi, fi;
+        tile_at(p, t, &mi, &fi);
+        const int row = (2 * mi + crank) * BM, col = fi * BF;
+        for (int c0 = 0; c0 < p.num_kb && ok; c0 += p.chunk) {
+          const int len = min(p.num_kb - c0, p.chunk);
+          int sg = 0, i = 0;  // a chunk's K blocks once per pair of pieces
+          for (int j = 0; j < len * SEGS; ++j, rg.next(), ++issued) {
+            if (!wait(&empty[rg.s], rg.ph ^ 1, kSite + __LINE__)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = smem + rg.s * kStageBytes;
+            if (crank == 0) mbar_arrive_expect_tx(&full[rg.s], 2 * kStageBytes);
+            const uint32_t fb = full0 + rg.s * 8;
+            const int k = (c0 + i) * BK;
+            tma_load_2d_pair(dst, F32 ? &maps.a[SEG_X[sg]] : maps.a, fb, k, row);
+            tma_load_2d_pair(dst + kABytes, F32 ? wm + SEG_W[sg] : wm, fb, k, col);
+            if (++i == len) {
+              i = 0;
+              ++sg;
+            }
           }
         }
       }
-    }
-    // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
-    for (long long j = issued - 1; j >= 0 && j >= issued - kStages; --j)
-      mbar_wait_bounded(&empty[j % kStages], (uint32_t)((j / kStages) & 1), p.err, p.limit_ns,
-                        kSite + __LINE__);
-  } else if (warp == 1 && lane == 0 && crank == 0) {
-    // ------------------------------------------------------------ MMA issuer
-    constexpr uint32_t IDESC = make_idesc(2 * BM, 2 * BF, false, false);
-    Ring<kStages> rg;
-    Ring<2> acc;
-    bool any = false, ok = true;
-    for (int t = t0; t < p.num_tiles && ok; t += t_step)
-      for (int c0 = 0; c0 < p.num_kb && ok; c0 += p.chunk, acc.next()) {
-        if (!wait(&tempty[acc.s], acc.ph ^ 1, kSite + __LINE__)) {
-          ok = false;
-          break;
-        }
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc.s * 2 * BF);
-        const int blocks = min(p.num_kb - c0, p.chunk) * SEGS;
-        for (int j = 0; j < blocks; ++j, rg.next()) {
-          if (!wait(&full[rg.s], rg.ph, kSite + __LINE__)) {
+      // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
+      for (long long j = issued - 1; j >= 0 && j >= issued - kStages; --j)
+        mbar_wait_bounded(&empty[j % kStages], (uint32_t)((j / kStages) & 1), p.err, p.limit_ns,
+                          kSite + __LINE__);
+    } else if (warp == 1 && lane == 0 && crank == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      constexpr uint32_t IDESC = make_idesc(2 * BM, 2 * BF, false, false);
+      Ring<kStages> rg;
+      Ring<2> acc;
+      bool any = false, ok = true;
+      for (int t = t0; t < p.num_tiles && ok; t += t_step)
+        for (int c0 = 0; c0 < p.num_kb && ok; c0 += p.chunk, acc.next()) {
+          if (!wait(&tempty[acc.s], acc.ph ^ 1, kSite + __LINE__)) {
             ok = false;
             break;
           }
           tc_fence_after();
-          const uint32_t a_base = smem_base + rg.s * kStageBytes;
-          const uint64_t ad = make_sdesc(a_base, 16, 1024), bd = make_sdesc(a_base + kABytes, 16, 1024);
+          const uint32_t d = tmem_base + (uint32_t)(acc.s * 2 * BF);
+          const int blocks = min(p.num_kb - c0, p.chunk) * SEGS;
+          for (int j = 0; j < blocks; ++j, rg.next()) {
+            if (!wait(&full[rg.s], rg.ph, kSite + __LINE__)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint32_t a_base = smem_base + rg.s * kStageBytes;
+            const uint64_t ad = make_sdesc(a_base, 16, 1024), bd = make_sdesc(a_base + kABytes, 16, 1024);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)
-            umma_bf16_pair(d, ad + k * 2, bd + k * 2, IDESC, (j | k) != 0);
-          umma_commit_pair(&empty[rg.s]);
+            for (int k = 0; k < BK / 16; ++k)
+              umma_bf16_pair(d, ad + k * 2, bd + k * 2, IDESC, (j | k) != 0);
+            umma_commit_pair(&empty[rg.s]);
+          }
+          if (!ok) break;
+          umma_commit_pair(&tfull[acc.s]);
+          any = true;
         }
-        if (!ok) break;
-        umma_commit_pair(&tfull[acc.s]);
-        any = true;
+      if (any) {  // TMEM is freed after the final barrier: wait for the last hand-over's MMAs
+        const int last = acc.s ^ 1;
+        mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns, kSite + __LINE__);
       }
-    if (any) {  // TMEM is freed after the final barrier: wait for the last hand-over's MMAs
-      const int last = acc.s ^ 1;
-      mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns, kSite + __LINE__);
     }
-  } else if (warp >= 2) {
+  } else {
+    regs_take<kManyRegs>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int fbeg = ((warp - 2) >> 2) * (BF / 2);
-    uint8_t* stg = staging + (warp - 2) * kBoxes * kStgBytes;
+    const int fbeg = ((warp - kEpiWarp0) >> 2) * (BF / 2);
+    uint8_t* stg = staging + (warp - kEpiWarp0) * kBoxes * kStgBytes;
     Ring<2> acc;
-    uint64_t* dbar = &dfull[warp - 2];
+    uint64_t* dbar = &dfull[warp - kEpiWarp0];
     uint32_t dph = 0;
     int buf = 0;
     bool ok = true;

@@ -50,8 +50,12 @@ constexpr int BN = 256;           // columns per pair tile
 constexpr int BK = 64;
 constexpr int kStages = 5;  // (6: 3 % slower at 8192 x 128256 x 4096; 4: dx and dW 4 % slower)
 constexpr int kEpiWarps = 8;      // two per TMEM lane quarter, each 128 columns
-constexpr int kBWarp = 2 + kEpiWarps;  // the gradients' second producer
-constexpr int gemm_threads(bool lse) { return 32 * (kBWarp + (lse ? 0 : 1)); }
+constexpr int kBWarp = 2;         // the gradients' second producer
+constexpr int kEpiWarp0 = 4;      // (whole warpgroups for the split of the registers)
+constexpr int kGemmThreads = 32 * (kEpiWarp0 + kEpiWarps);
+// Registers: 168 a thread at the launch, of which the first warpgroup keeps 72 and the epilogues' get 216.
+constexpr int kFewRegs = 72, kManyRegs = 216;
+static_assert(kFewRegs * 128 + kManyRegs * 32 * kEpiWarps == 168 * kGemmThreads, "registers");
 constexpr int kGroup = 128;       // columns of one (max, sum) group
 constexpr uint32_t kABytes = BM * BK * 2;
 constexpr uint32_t kBBytes = BN / 2 * BK * 2;
@@ -203,15 +207,15 @@ __device__ __forceinline__ float unit_share(float dloss, int target, int V) {
 
 // LSE: the logits' product with its softmax epilogue (one product, both operands K-major).
 // Otherwise the gradients' products, dx and dW in one launch, so that the second's tiles fill the
-// first's last wave.  Warps 0 and 10 of each CTA load its 128 rows of A and its half of B, one thread
-// of the even CTA's warp 1 issues the MMAs, warps 2-9 read the accumulators back (warp w: rows
-// 32 (w % 4).. of the CTA's 128, columns 128 ((w - 2) / 4)..).
+// first's last wave.  Warps 0 and 2 of each CTA load its 128 rows of A and its half of B, one thread
+// of the even CTA's warp 1 issues the MMAs, warps 4-11 read the accumulators back (warp w: rows
+// 32 (w % 4).. of the CTA's 128, columns 128 ((w - 4) / 4)..).
 //
 // Bound by the tensor pipe, and in a run of calls by the board's power.  4096 x 32000 x 2048: logits
 // 310-335 us (1.6-1.7 PFLOP/s, tensor pipe 78 % active), dx and dW 600-615 us (1.75-1.8, 86 %);
 // 8192 x 128256 x 4096: 5.0-5.3 ms and 9.6-10.2 ms at 1.4-1.55 GHz.
 template <bool LSE, int SEGS>
-__global__ void __launch_bounds__(gemm_threads(LSE), 1)
+__global__ void __launch_bounds__(kGemmThreads, 1)
     head_gemm_kernel(const __grid_constant__ HeadMaps maps0, const __grid_constant__ HeadMaps maps1,
                      const __grid_constant__ HeadGemm p) {
   constexpr bool F32 = SEGS == kMaxSegs;
@@ -266,139 +270,143 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
   // With target lists the kernel before this one made them, and started it after everything earlier
   // was complete: only the epilogue, which reads the lists and writes, waits for it (and the warp that
   // makes dz's unit from what that kernel left of dloss).
-  if (!LSE || !p.gstart || (warp >= 2 && warp < kBWarp) || (warp == 1 && blockIdx.x == 1)) pdl_wait();
+  if (!LSE || !p.gstart || warp >= kEpiWarp0 || (warp == 1 && blockIdx.x == 1)) pdl_wait();
   const int t0 = (int)blockIdx.x / 2, t_step = (int)gridDim.x / 2;
 
-  if ((warp == 0 || warp == kBWarp) && lane == 0) {
-    // ------------------------------------------------------------ TMA producers
-    // gradients: warp 0 loads A, warp 10 B (each up to two boxes); logits: warp 0 both (two warps
-    // measured 3 % slower there, one 6 % slower for the gradients)
-    const bool is_b = !LSE && warp == kBWarp;
-    Ring<STAGES> rg;
-    bool ok = true;
-    long long issued = 0;
-    const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
-    uint8_t* const dst0 = smem + (is_b ? B_OFF : 0);
-    for (int t = t0; t < p.num_tiles && ok; t += t_step) {
-      const Tile c = tile_of(p, t);
-      const HeadMaps& maps = c.which ? maps1 : maps0;
-      const CUtensorMap* const set = is_b ? maps.b : maps.a;
-      const int8_t* const seg = is_b ? p.seg_b : p.seg_a;
-      // the operand's first row of M (N), and how it is loaded: K-major; MN-major as one box of two
-      // 64-column groups (dz: always) or as two boxes
-      const bool a_mn = !LSE && p.prod[c.which].a_mn;
-      const int r0 = is_b ? c.nt * BN + crank * (BN / 2)
-                          : (FINE && !a_mn ? 0 : (2 * c.mi + crank) * BM);
-      const int half = FINE && a_mn ? p.prod[c.which].num_kb / 2 : 0;
-      const int how = LSE ? 0 : (is_b ? (p.prod[c.which].b_groups ? 1 : 2) : a_mn);
-      const bool expect = !is_b && crank == 0;
-      for (int c0 = c.kb0; c0 < c.kb1 && ok; c0 += p.chunk) {
-        const int len = min(c.kb1 - c0, p.chunk);
-        int sg = 0, i = 0;  // a chunk's K blocks once per pair of pieces
-        for (int j = 0; j < len * STEPS; ++j, rg.next(), ++issued) {
-          if (!ring_wait(&empty[rg.s], rg.ph ^ 1, abort_flag, p, kSite + __LINE__)) {
-            ok = false;
-            break;
-          }
-          uint8_t* dst = dst0 + rg.s * STAGE;
-          const int at = sg;
-          const CUtensorMap* m = F32 ? &set[seg[at]] : set;
-          int k = (c0 + i) * BK;
-          if (FINE) {
-            if (!is_b) m = set + (a_mn ? c0 + i < half : crank);
-            if (c0 + i >= half) k -= half * BK;
-          }
-          if (++i == len) {
-            i = 0;
-            ++sg;
-          }
-          if (expect) mbar_arrive_expect_tx(&full[rg.s], 2 * STAGE);
-          const uint32_t fb = full0 + rg.s * 8;
-          if (how == 0) {
-            tma_load_2d_pair(dst, m, fb, k, r0);
-            if (LSE)
-              tma_load_2d_pair(dst + B_OFF, &maps.b[F32 ? p.seg_b[at] : 0], fb, k,
-                               c.nt * BN + crank * (BN / 2));
-          } else if (how == 1) {
-            tma_load_3d_pair(dst, m, fb, 0, k, r0 / 64);
-          } else {
-            tma_load_2d_pair(dst, m, fb, r0, k);
-            tma_load_2d_pair(dst + 8192, m, fb, r0 + 64, k);
+  if (warp < kEpiWarp0) {
+    regs_give<kFewRegs>();
+    if ((warp == 0 || (!LSE && warp == kBWarp)) && lane == 0) {
+      // ------------------------------------------------------------ TMA producers
+      // gradients: warp 0 loads A, warp 2 B (each up to two boxes); logits: warp 0 both (two warps
+      // measured 3 % slower there, one 6 % slower for the gradients)
+      const bool is_b = !LSE && warp == kBWarp;
+      Ring<STAGES> rg;
+      bool ok = true;
+      long long issued = 0;
+      const uint32_t full0 = mapa_shared(full, 0);  // the even CTA's barriers
+      uint8_t* const dst0 = smem + (is_b ? B_OFF : 0);
+      for (int t = t0; t < p.num_tiles && ok; t += t_step) {
+        const Tile c = tile_of(p, t);
+        const HeadMaps& maps = c.which ? maps1 : maps0;
+        const CUtensorMap* const set = is_b ? maps.b : maps.a;
+        const int8_t* const seg = is_b ? p.seg_b : p.seg_a;
+        // the operand's first row of M (N), and how it is loaded: K-major; MN-major as one box of two
+        // 64-column groups (dz: always) or as two boxes
+        const bool a_mn = !LSE && p.prod[c.which].a_mn;
+        const int r0 = is_b ? c.nt * BN + crank * (BN / 2)
+                            : (FINE && !a_mn ? 0 : (2 * c.mi + crank) * BM);
+        const int half = FINE && a_mn ? p.prod[c.which].num_kb / 2 : 0;
+        const int how = LSE ? 0 : (is_b ? (p.prod[c.which].b_groups ? 1 : 2) : a_mn);
+        const bool expect = !is_b && crank == 0;
+        for (int c0 = c.kb0; c0 < c.kb1 && ok; c0 += p.chunk) {
+          const int len = min(c.kb1 - c0, p.chunk);
+          int sg = 0, i = 0;  // a chunk's K blocks once per pair of pieces
+          for (int j = 0; j < len * STEPS; ++j, rg.next(), ++issued) {
+            if (!ring_wait(&empty[rg.s], rg.ph ^ 1, abort_flag, p, kSite + __LINE__)) {
+              ok = false;
+              break;
+            }
+            uint8_t* dst = dst0 + rg.s * STAGE;
+            const int at = sg;
+            const CUtensorMap* m = F32 ? &set[seg[at]] : set;
+            int k = (c0 + i) * BK;
+            if (FINE) {
+              if (!is_b) m = set + (a_mn ? c0 + i < half : crank);
+              if (c0 + i >= half) k -= half * BK;
+            }
+            if (++i == len) {
+              i = 0;
+              ++sg;
+            }
+            if (expect) mbar_arrive_expect_tx(&full[rg.s], 2 * STAGE);
+            const uint32_t fb = full0 + rg.s * 8;
+            if (how == 0) {
+              tma_load_2d_pair(dst, m, fb, k, r0);
+              if (LSE)
+                tma_load_2d_pair(dst + B_OFF, &maps.b[F32 ? p.seg_b[at] : 0], fb, k,
+                                 c.nt * BN + crank * (BN / 2));
+            } else if (how == 1) {
+              tma_load_3d_pair(dst, m, fb, 0, k, r0 / 64);
+            } else {
+              tma_load_2d_pair(dst, m, fb, r0, k);
+              tma_load_2d_pair(dst + 8192, m, fb, r0 + 64, k);
+            }
           }
         }
       }
-    }
-    // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
-    for (long long j = issued - 1; j >= 0 && j >= issued - STAGES; --j)
-      mbar_wait_bounded(&empty[j % STAGES], (uint32_t)((j / STAGES) & 1), p.err, p.limit_ns,
-                        kSite + __LINE__);
-  } else if (warp == 1 && lane == 0 && crank == 0) {
-    // ------------------------------------------------------------ MMA issuer
-    Ring<STAGES> rg;
-    Ring<2> acc;
-    bool any = false;
-    // one tile; the operands' orders are compile-time constants (as run-time values they cost the
-    // issuing thread 15 % of the products' time)
-    auto tile = [&](const Tile& c, auto a_mn_t) -> bool {
-      constexpr bool A_MN = decltype(a_mn_t)::value, B_MN = !LSE;
-      constexpr uint32_t IDESC = make_idesc(2 * BM, BN, A_MN, B_MN);
-      for (int kb = c.kb0; kb < c.kb1; kb += p.chunk, acc.next()) {
-        if (!ring_wait(&tempty[acc.s], acc.ph ^ 1, abort_flag, p, kSite + __LINE__)) return false;
-        tc_fence_after();
-        const uint32_t d = tmem_base + (uint32_t)(acc.s * BN);
-        const int blocks = (min(c.kb1, kb + p.chunk) - kb) * STEPS;
-        for (int j = 0; j < blocks; ++j, rg.next()) {
-          if (!ring_wait(&full[rg.s], rg.ph, abort_flag, p, kSite + __LINE__)) return false;
+      // no copy may be in flight when the CTA exits: the MMAs release a stage after reading it
+      for (long long j = issued - 1; j >= 0 && j >= issued - STAGES; --j)
+        mbar_wait_bounded(&empty[j % STAGES], (uint32_t)((j / STAGES) & 1), p.err, p.limit_ns,
+                          kSite + __LINE__);
+    } else if (warp == 1 && lane == 0 && crank == 0) {
+      // ------------------------------------------------------------ MMA issuer
+      Ring<STAGES> rg;
+      Ring<2> acc;
+      bool any = false;
+      // one tile; the operands' orders are compile-time constants (as run-time values they cost the
+      // issuing thread 15 % of the products' time)
+      auto tile = [&](const Tile& c, auto a_mn_t) -> bool {
+        constexpr bool A_MN = decltype(a_mn_t)::value, B_MN = !LSE;
+        constexpr uint32_t IDESC = make_idesc(2 * BM, BN, A_MN, B_MN);
+        for (int kb = c.kb0; kb < c.kb1; kb += p.chunk, acc.next()) {
+          if (!ring_wait(&tempty[acc.s], acc.ph ^ 1, abort_flag, p, kSite + __LINE__)) return false;
           tc_fence_after();
-          const uint32_t a_base = smem_base + rg.s * STAGE;
-          const uint64_t bd = tile_desc<B_MN>(a_base + B_OFF);
-          const uint64_t ad = tile_desc<A_MN>(a_base);
+          const uint32_t d = tmem_base + (uint32_t)(acc.s * BN);
+          const int blocks = (min(c.kb1, kb + p.chunk) - kb) * STEPS;
+          for (int j = 0; j < blocks; ++j, rg.next()) {
+            if (!ring_wait(&full[rg.s], rg.ph, abort_flag, p, kSite + __LINE__)) return false;
+            tc_fence_after();
+            const uint32_t a_base = smem_base + rg.s * STAGE;
+            const uint64_t bd = tile_desc<B_MN>(a_base + B_OFF);
+            const uint64_t ad = tile_desc<A_MN>(a_base);
 #pragma unroll
-          for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
-            umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
-                           (j | k) != 0);
-          umma_commit_pair(&empty[rg.s]);
+            for (int k = 0; k < BK / 16; ++k)  // (the address counts 16 bytes in the low bits)
+              umma_bf16_pair(d, ad + k * (A_MN ? 128 : 2), bd + k * (B_MN ? 128 : 2), IDESC,
+                             (j | k) != 0);
+            umma_commit_pair(&empty[rg.s]);
+          }
+          umma_commit_pair(&tfull[acc.s]);
+          any = true;
         }
-        umma_commit_pair(&tfull[acc.s]);
-        any = true;
+        return true;
+      };
+      for (int t = t0; t < p.num_tiles; t += t_step) {
+        const Tile c = tile_of(p, t);
+        if (!(!LSE && p.prod[c.which].a_mn ? tile(c, std::true_type{}) : tile(c, std::false_type{})))
+          break;
       }
-      return true;
-    };
-    for (int t = t0; t < p.num_tiles; t += t_step) {
-      const Tile c = tile_of(p, t);
-      if (!(!LSE && p.prod[c.which].a_mn ? tile(c, std::true_type{}) : tile(c, std::false_type{})))
-        break;
-    }
-    if (any) {  // TMEM is freed after the final barrier: wait for the last hand-over's MMAs
-      const int last = acc.s ^ 1;
-      mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns,
-                        kSite + __LINE__);
-    }
-  } else if (LSE && warp == 1 && blockIdx.x == 1 && p.store) {
-    // ------------------------------------------------------------ an idle warp: the unit of dz
-    float top = 0.f;
-    const int M = p.prod[0].M, V = p.prod[0].N, quads = M / 4;
-    const float4* d4 = reinterpret_cast<const float4*>(p.dloss);
-    const int4* t4 = reinterpret_cast<const int4*>(p.ucol);
+      if (any) {  // TMEM is freed after the final barrier: wait for the last hand-over's MMAs
+        const int last = acc.s ^ 1;
+        mbar_wait_bounded(&tfull[last], last ? acc.ph ^ 1 : acc.ph, p.err, p.limit_ns,
+                          kSite + __LINE__);
+      }
+    } else if (LSE && warp == 1 && blockIdx.x == 1 && p.store) {
+      // ------------------------------------------------------------ an idle warp: the unit of dz
+      float top = 0.f;
+      const int M = p.prod[0].M, V = p.prod[0].N, quads = M / 4;
+      const float4* d4 = reinterpret_cast<const float4*>(p.dloss);
+      const int4* t4 = reinterpret_cast<const int4*>(p.ucol);
 #pragma unroll 4
-    for (int r = lane; r < quads; r += 32) {
-      const float4 w = d4[r];
-      const int4 t = p.gstart ? make_int4(0, 0, 0, 0) : t4[r];
-      top = fmaxf(fmaxf(top, fmaxf(unit_share(w.x, t.x, V), unit_share(w.y, t.y, V))),
-                  fmaxf(unit_share(w.z, t.z, V), unit_share(w.w, t.w, V)));
-    }
-    if (lane < M - 4 * quads) {
-      const int r = 4 * quads + lane;
-      top = fmaxf(top, unit_share(p.dloss[r], p.gstart ? 0 : p.ucol[r], V));
-    }
+      for (int r = lane; r < quads; r += 32) {
+        const float4 w = d4[r];
+        const int4 t = p.gstart ? make_int4(0, 0, 0, 0) : t4[r];
+        top = fmaxf(fmaxf(top, fmaxf(unit_share(w.x, t.x, V), unit_share(w.y, t.y, V))),
+                    fmaxf(unit_share(w.z, t.z, V), unit_share(w.w, t.w, V)));
+      }
+      if (lane < M - 4 * quads) {
+        const int r = 4 * quads + lane;
+        top = fmaxf(top, unit_share(p.dloss[r], p.gstart ? 0 : p.ucol[r], V));
+      }
 #pragma unroll
-    for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) *p.unit = head_unit(top);
-  } else if (warp >= 2 && warp < kBWarp) {
+      for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+      if (lane == 0) *p.unit = head_unit(top);
+    }
+  } else {
+    regs_take<kManyRegs>();
     // ------------------------------------------------------------ epilogue
     const int q = warp & 3;
-    const int cbeg = ((warp - 2) >> 2) * kGroup;
-    uint8_t* stg = staging + (warp - 2) * STG;
+    const int cbeg = ((warp - kEpiWarp0) >> 2) * kGroup;
+    uint8_t* stg = staging + (warp - kEpiWarp0) * STG;
     const float out_scale = LSE ? 1.f : (p.out_scale ? *p.out_scale * p.T : p.T);
     Ring<2> acc;
     bool ok = true;
@@ -430,30 +438,21 @@ __global__ void __launch_bounds__(gemm_threads(LSE), 1)
         }
         tc_fence_after();
         const uint32_t ta = tmem_base + ((uint32_t)(q * 32) << 16) + (uint32_t)(a * BN + cbeg);
-        if (FINE && kb == c.kb0) {  // every load ahead of one wait
-          uint32_t r[kGroup / 32][32];
 #pragma unroll
-          for (int j = 0; j < kGroup / 32; ++j) tmem_ld_32x32b_x32(ta + 32 * j, r[j]);
+        for (int j = 0; j < kGroup; j += 32) {
+          uint32_t r[32];
+          tmem_ld_32x32b_x32(ta + j, r);
           tmem_ld_wait();
+          if (kb == c.kb0) {
 #pragma unroll
-          for (int i = 0; i < kGroup; ++i) v[i] = __uint_as_float(r[i / 32][i % 32]);
-        } else {
+            for (int i = 0; i < 32; ++i) v[j + i] = __uint_as_float(r[i]);
+          } else {
 #pragma unroll
-          for (int j = 0; j < kGroup; j += 32) {
-            uint32_t r[32];
-            tmem_ld_32x32b_x32(ta + j, r);
-            tmem_ld_wait();
-            if (kb == c.kb0) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[j + i] = __uint_as_float(r[i]);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; i += 2) {
-                const float2 w = add2(make_float2(v[j + i], v[j + i + 1]),
-                                      make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
-                v[j + i] = w.x;
-                v[j + i + 1] = w.y;
-              }
+            for (int i = 0; i < 32; i += 2) {
+              const float2 w = add2(make_float2(v[j + i], v[j + i + 1]),
+                                    make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])));
+              v[j + i] = w.x;
+              v[j + i + 1] = w.y;
             }
           }
         }
@@ -1373,7 +1372,7 @@ cudaError_t gemm_pairs(int* pairs) {
     if (attr_err != cudaSuccess) return;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(sm_count() / 2 * 2);
-    cfg.blockDim = dim3(gemm_threads(LSE));
+    cfg.blockDim = dim3(kGemmThreads);
     cfg.dynamicSmemBytes = gemm_smem(SEGS);
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;
@@ -1404,7 +1403,7 @@ poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStrea
   p.limit_ns = kWaitLimitNs;
   const int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
   POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, SEGS>, dim3(2 * pairs),
-                                    dim3(gemm_threads(LSE)),
+                                    dim3(kGemmThreads),
                                     gemm_smem(SEGS), s, 2, m0, m1, p));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_HEAD_GEMM);
