@@ -11,7 +11,8 @@
 // from the fp32 sums; z is stored only where the backward wants it.  Backward: dz elementwise (from the
 // kept z, or in the epilogue of the same product run again), then the two products of the linear head's
 // gradients (head.cu), for which dz is what that head's is.  fp32 forwards of up to 32 rows (or more of small
-// blocks) and gradients of up to 16 are ffn_rows.cu's, bf16 gradients of up to 64 rows ffn_grad.cu's.
+// blocks) and gradients of up to 16, and bf16 forwards of one row (four of small blocks), are ffn_rows.cu's;
+// bf16 gradients of up to 64 rows ffn_grad.cu's.
 //
 // The tensor core truncates when it adds into its fp32 accumulator (about 2^-24 of the sum per add of 16
 // products, all in one direction), so after every `chunk` of K the partial tile moves into the epilogue's
@@ -20,7 +21,7 @@
 // multiplied, 256 of K per accumulator.
 //
 // Forward 8192 x 4096 x 14336 with z: 1.13-1.16 ms (1.66-1.70 PFLOP/s in a run of calls, at the board's power;
-// tensor pipe 89 %).  One row of 4096 x 14336: 235 MB of W in 38-39 us (6.1 TB/s).  Backward 4096 x 2048 x
+// tensor pipe 89 %).  Eight rows of 4096 x 14336: 235 MB of W in 39-40 us (6.0 TB/s).  Backward 4096 x 2048 x
 // 8192 from kept z: dz 46 us (335 MB, 7.3 TB/s), products 299 us (1.84 PFLOP/s).
 //
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, drains its own
@@ -83,12 +84,6 @@ __device__ __forceinline__ void put8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
 }
-// What is left of v after its rounding to bf16, which is v's first piece (nothing, where that is not finite).
-__device__ __forceinline__ float rest_of(float v, __nv_bfloat16 first) {
-  const float f = __bfloat162float(first);
-  return isfinite(f) ? v - f : 0.f;
-}
-
 // What the elementwise kernels read and write, in vectors of eight elements: vector i lies in row i / vpr
 // (the quotient by a multiplication: fewer than 2^31 vectors), or all in one row (magic 0) where the rows
 // follow each other.
@@ -974,6 +969,8 @@ poetx_status project(poetx_dtype dt, Act act, const uint8_t* xp, int N, int D, c
   auto bf16_map = [&](CUtensorMap* m, const void* p, long long outer, int bi, int bo) {
     return encode_tma_2d(m, p, TMA_BF16, D, outer, D, bi, bo, true);
   };
+  if (!f32 && rows_forward_fits_bf16(N, D, F))
+    return rows_forward({false, xp, wp, N, D, F, o.h, o.z, o.dh, o.z2, o.pitch}, act, s);
   if (!f32 && few_rows(N, D)) {
     FfnScore p{};
     const int sms = sm_count(), each = ceil_div(F, (long long)sms * BM);
@@ -1148,9 +1145,7 @@ extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, cons
   if (ws_bytes < need) return POETX_ERR_WORKSPACE;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
   if (dt == POETX_F32 && rows_forward_fits(N, D, F))
-    return rows_forward({static_cast<const float*>(x), static_cast<const float*>(W), N, D, F,
-                         static_cast<float*>(h), static_cast<float*>(z), nullptr, nullptr},
-                        act, stream);
+    return rows_forward({true, x, W, N, D, F, h, z, nullptr, nullptr, 2ll * F}, act_of(act), stream);
   const uint8_t *xp = static_cast<const uint8_t*>(x), *wp = static_cast<const uint8_t*>(W);
   if (dt == POETX_F32) {
     uint8_t* w = static_cast<uint8_t*>(ws);
@@ -1197,11 +1192,9 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
                            piece_step((size_t)2 * F * D), stream));
   }
   const int pieces = pl.pieces;
-  const float *xf = static_cast<const float*>(x), *wf = static_cast<const float*>(W);
   if (pl.direct && pl.f32) {
-    POETX_TRY(rows_forward({xf, wf, N, D, F, nullptr, nullptr, static_cast<const float*>(dh),
-                            reinterpret_cast<float*>(w + pl.dz)},
-                           act, stream));
+    POETX_TRY(rows_forward({true, x, W, N, D, F, nullptr, w + pl.dz, dh, nullptr, 2ll * F}, act_of(act),
+                           stream));
   } else if (pl.direct) {
     POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
                       Outputs{nullptr, w + pl.dz, dh, pl.fine ? w + pl.dz + pl.z_step : nullptr, pl.pitch},
@@ -1210,8 +1203,8 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
     if (!z) {
       z = w + pl.z;
       if (pl.f32 && N <= kRowsForward)
-        POETX_TRY(rows_forward({xf, wf, N, D, F, nullptr, reinterpret_cast<float*>(w + pl.z), nullptr, nullptr},
-                               act, stream));
+        POETX_TRY(rows_forward({true, x, W, N, D, F, nullptr, w + pl.z, nullptr, nullptr, 2ll * F},
+                               act_of(act), stream));
       else
         POETX_TRY(project(dt, act_of(act), xp, N, D, wp, F,
                           Outputs{nullptr, w + pl.z, nullptr, nullptr, 2ll * F}, stream));
@@ -1227,7 +1220,8 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   }
   float* const dxp = reinterpret_cast<float*>(w + pl.dxp);
   if (pl.rows)
-    return rows_gradients({reinterpret_cast<const float*>(w + pl.dz), xf, wf, N, D, 2 * F,
+    return rows_gradients({reinterpret_cast<const float*>(w + pl.dz), static_cast<const float*>(x),
+                           static_cast<const float*>(W), N, D, 2 * F,
                            static_cast<float*>(dx), static_cast<float*>(dW), accumulate, dxp},
                           stream);
   if (pl.few)

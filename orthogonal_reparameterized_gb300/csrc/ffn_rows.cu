@@ -1,5 +1,5 @@
-// The gated feed-forward block (ffn.cu) for so few fp32 rows that its time is W's way through the SMs, on the
-// CUDA cores:
+// The gated feed-forward block (ffn.cu) for so few rows that its time is W's way through the SMs, on the CUDA
+// cores (fp32, and the forward of one to four bf16 rows):
 //
 //   forward:    z = x W^T, then h = a(g) u, or dz = [dh u a'(g) | dh a(g)] from the sums
 //   gradients:  dx = dz W,  dW = dz^T x
@@ -46,17 +46,26 @@ struct FwdArgs {
   Act act;
 };
 
+// 16 bytes of a bf16 row in pairs of columns.
+__device__ __forceinline__ void unpack(const uint4& w, float2 (&v)[4]) {
+  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v[i] = make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
+}
+
 // Two features' sums for the group's tokens.
-template <int NT, int RING>
+template <typename T, int NT, int RING>
 __device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int f0, int n0, int lane,
                                               const float4* x_here, const uint8_t* ring) {
+  static_assert(sizeof(T) == 4 || RING == 0, "bf16: through L1");
   float2 acc[4][NT] = {};
-  const int quads = c.D / 4;
   if constexpr (RING > 0) {
+    const int quads = c.D / 4;
     // the lane's columns are lane * 4 and every 128th from there; it copies its own bytes and reads them itself
     const int steps = (quads - lane + 31) / 32;
     const uint32_t ring_at = smem_u32(ring);
-    const float4* const g = reinterpret_cast<const float4*>(c.W) + (long long)f0 * quads + lane;
+    const float4* const g = static_cast<const float4*>(c.W) + (long long)f0 * quads + lane;
     const float4* const u = g + (long long)c.F * quads;
     auto request = [&](int k) {  // two gate rows, two value rows
       if (k < steps) {
@@ -91,15 +100,16 @@ __device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int
       }
     }
     copy_wait<0>();
-  } else {
+  } else if constexpr (sizeof(T) == 4) {
+    const int quads = c.D / 4;
     const float4* w[4];  // two gate rows, two value rows
 #pragma unroll
     for (int r = 0; r < 4; ++r)
-      w[r] = reinterpret_cast<const float4*>(c.W) + (long long)(f0 + (r & 1) + (r >> 1) * c.F) * quads;
+      w[r] = static_cast<const float4*>(c.W) + (long long)(f0 + (r & 1) + (r >> 1) * c.F) * quads;
     const float4* x[NT];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
-      x[n] = reinterpret_cast<const float4*>(c.x) + (long long)min(n0 + n, c.N - 1) * quads;
+      x[n] = static_cast<const float4*>(c.x) + (long long)min(n0 + n, c.N - 1) * quads;
     constexpr int U = 2;
     for (int q0 = lane; q0 < quads; q0 += 32 * U) {
       float4 wv[U][4];
@@ -119,6 +129,42 @@ __device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int
             acc[r][n] = fma2(make_float2(wv[k][r].x, wv[k][r].y), make_float2(xv.x, xv.y), acc[r][n]);
             acc[r][n] = fma2(make_float2(wv[k][r].z, wv[k][r].w), make_float2(xv.z, xv.w), acc[r][n]);
           }
+        }
+      }
+    }
+  } else {
+    constexpr int P = 4;  // pairs of columns in 16 bytes
+    const int vecs = c.D / 8;
+    const uint4* w[4];  // two gate rows, two value rows
+#pragma unroll
+    for (int r = 0; r < 4; ++r)
+      w[r] = static_cast<const uint4*>(c.W) + (long long)(f0 + (r & 1) + (r >> 1) * c.F) * vecs;
+    const uint4* x[NT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+      x[n] = static_cast<const uint4*>(c.x) + (long long)min(n0 + n, c.N - 1) * vecs;
+    constexpr int U = 2;
+    for (int q0 = lane; q0 < vecs; q0 += 32 * U) {
+      uint4 wv[U][4];
+#pragma unroll
+      for (int k = 0; k < U; ++k)
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          if (q0 + 32 * k < vecs) wv[k][r] = w[r][q0 + 32 * k];
+#pragma unroll
+      for (int k = 0; k < U; ++k) {
+        if (q0 + 32 * k >= vecs) break;
+        float2 wp[4][P];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) unpack(wv[k][r], wp[r]);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+          float2 xp[P];
+          unpack(x[n][q0 + 32 * k], xp);
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+#pragma unroll
+            for (int j = 0; j < P; ++j) acc[r][n] = fma2(wp[r][j], xp[j], acc[r][n]);
         }
       }
     }
@@ -144,39 +190,49 @@ __device__ __forceinline__ void rows_fwd_unit(const RowsForward& c, Act act, int
   const float g = v[0], u = __shfl_xor_sync(0xffffffffu, g, 16);
   const int i = lane * V / 32, f = f0 + i / NT, n = n0 + i % NT;
   if (lane >= 16 || lane % (32 / V) || n >= c.N) return;
-  const long long at = (long long)n * 2 * c.F + f;
+  constexpr bool F32 = sizeof(T) == 4;
+  const long long at = (long long)n * c.z_pitch + f, at_h = (long long)n * c.F + f;
+  T* const z = static_cast<T*>(c.z);
   if (c.dh) {
-    const float2 d = gated_grad<true>(g, u, c.dh[(long long)n * c.F + f], act);
-    c.dz[at] = d.x;
-    c.dz[at + c.F] = d.y;
+    const float2 d = gated_grad<F32>(g, u, (float)static_cast<const T*>(c.dh)[at_h], act);
+    const T a = T(d.x), b = T(d.y);
+    z[at] = a;
+    z[at + c.F] = b;
+    if constexpr (!F32) {
+      static_cast<T*>(c.z2)[at] = T(rest_of(d.x, a));
+      static_cast<T*>(c.z2)[at + c.F] = T(rest_of(d.y, b));
+    }
     return;
   }
-  if (c.h) c.h[(long long)n * c.F + f] = gated<true>(g, u, act);
-  if (c.z) {
-    c.z[at] = g;
-    c.z[at + c.F] = u;
+  if (c.h) static_cast<T*>(c.h)[at_h] = T(gated<F32>(g, u, act));
+  if (z) {
+    z[at] = T(g);
+    z[at + c.F] = T(u);
   }
 }
 
-// (Without a bound on its registers eight tokens through L1 get two CTAs an SM, not three: 16 x 4096 x 14336
-// 221 us instead of 182; with four, 261.)
-template <int NT, int RING>
-__global__ void __launch_bounds__(32 * fwd_warps(RING), RING ? 1 : 3) rows_fwd_kernel(const FwdArgs p) {
+// CTAs of an SM: through L1 as many as the registers can be held to.  (Eight fp32 tokens, 16 x 4096 x 14336:
+// two 221 us, three 190, four 261; one bf16 token, 4096 x 8192: six 22.4, five 27.5.)
+constexpr int fwd_ctas(int NT, int ring) { return ring ? 1 : (NT == 1 ? 6 : (NT == 2 ? 5 : 3)); }
+template <typename T, int NT, int RING>
+__global__ void __launch_bounds__(32 * fwd_warps(RING), fwd_ctas(NT, RING))
+    rows_fwd_kernel(const FwdArgs p) {
   extern __shared__ __align__(16) float4 x_here[];
   pdl_trigger();
   pdl_wait();
-  RowsForward c = p.c;  // of the block's tokens
-  if (const long long t0 = (long long)blockIdx.y * kBlock; t0 > 0) {
-    c.x += t0 * c.D;
-    if (c.h) c.h += t0 * c.F;
-    if (c.z) c.z += t0 * 2 * c.F;
-    if (c.dh) c.dh += t0 * c.F, c.dz += t0 * 2 * c.F;
-    c.N -= (int)t0;
+  RowsForward c = p.c;
+  if constexpr (RING > 0) {  // the block's tokens (through L1 there is one block)
+    const long long t0 = (long long)blockIdx.y * kBlock;
+    c.x = static_cast<const T*>(c.x) + t0 * c.D;
+    if (c.h) c.h = static_cast<T*>(c.h) + t0 * c.F;
+    if (c.z) c.z = static_cast<T*>(c.z) + t0 * c.z_pitch;
+    if (c.dh) c.dh = static_cast<const T*>(c.dh) + t0 * c.F;
+    c.N = min(c.N - (int)t0, kBlock);
   }
-  if (c.N > kBlock) c.N = kBlock;
-  const int lane = threadIdx.x & 31, quads = c.D / 4;
+  const int lane = threadIdx.x & 31;
   if (RING) {
-    const float4* const x = reinterpret_cast<const float4*>(c.x);
+    const int quads = c.D / 4;
+    const float4* const x = static_cast<const float4*>(c.x);
     for (int i = threadIdx.x; i < c.N * quads; i += 32 * fwd_warps(RING))
       copy_async<16>(smem_u32(x_here + i), x + i);
     copy_commit();
@@ -191,9 +247,9 @@ __global__ void __launch_bounds__(32 * fwd_warps(RING), RING ? 1 : 3) rows_fwd_k
       reinterpret_cast<const uint8_t*>(x_here) + p.x_bytes + warp * RING * kStepBytes + lane * 16;
   if (RING) {
     for (int pair = team * gridDim.x + blockIdx.x; 2 * pair < c.F; pair += teams * gridDim.x)
-      rows_fwd_unit<NT, RING>(c, p.act, 2 * pair, n0, lane, x_here, ring);
+      rows_fwd_unit<T, NT, RING>(c, p.act, 2 * pair, n0, lane, x_here, ring);
   } else if (const int pair = blockIdx.x * teams + team; 2 * pair < c.F) {
-    rows_fwd_unit<NT, RING>(c, p.act, 2 * pair, n0, lane, x_here, ring);
+    rows_fwd_unit<T, NT, RING>(c, p.act, 2 * pair, n0, lane, x_here, ring);
   }
 }
 
@@ -346,9 +402,9 @@ __global__ void __launch_bounds__(32 * kGradWarps, grad_ctas(NT)) rows_grad_kern
   }
 }
 
-template <int NT, int RING>
+template <typename T, int NT, int RING>
 poetx_status launch_fwd1(const FwdArgs& a, cudaStream_t s) {
-  auto k = rows_fwd_kernel<NT, RING>;
+  auto k = rows_fwd_kernel<T, NT, RING>;
   size_t smem = 0;
   if (RING) {
     static std::once_flag once;
@@ -377,10 +433,10 @@ poetx_status launch_fwd(FwdArgs a, cudaStream_t s) {
   if constexpr (NT > 2) {
     if (x_bytes <= x_room(2)) {
       a.x_bytes = (int)x_bytes;
-      return x_bytes <= x_room(4) ? launch_fwd1<NT, 4>(a, s) : launch_fwd1<NT, 2>(a, s);
+      return x_bytes <= x_room(4) ? launch_fwd1<float, NT, 4>(a, s) : launch_fwd1<float, NT, 2>(a, s);
     }
   }
-  return launch_fwd1<NT, 0>(a, s);
+  return launch_fwd1<float, NT, 0>(a, s);
 }
 
 template <int NT, bool ADD>
@@ -432,10 +488,23 @@ bool rows_forward_fits(int N, int D, int F) {
          tokens * rows * (D + 256) / 16e6 < 11 + rows * D / 577e3 + D / 40.0;
 }
 
-poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s) {
+// One bf16 row is always here (4096 x 14336: 36.9 us, on the tensor cores 39.6; 1024 x 2816: 3.5 and 6.8), two
+// to four of blocks whose W is small enough (two: 2048 x 5632 10.4 and 11.6 us, 4096 x 14336 43.5 and 39.5;
+// four: 1024 x 4096 5.7 and 7.0, 1600 x 4264 9.9 and 9.5).
+bool rows_forward_fits_bf16(int N, int D, int F) {
+  const long long weights = 2ll * F * D;
+  return N == 1 || (N == 2 && weights <= 3 << 23) || (N <= 4 && weights <= 1 << 23);
+}
+
+poetx_status rows_forward(const RowsForward& c, const Act& act, cudaStream_t s) {
   const int nt = c.N == 1 ? 1 : (c.N == 2 ? 2 : (c.N <= 4 ? 4 : kGroup));
   const int groups = ceil_div(std::min(c.N, kBlock), nt);
-  const FwdArgs a{c, groups, 0, act_of(act)};
+  const FwdArgs a{c, groups, 0, act};
+  if (!c.f32) {
+    using H = __nv_bfloat16;
+    return nt == 1 ? launch_fwd1<H, 1, 0>(a, s)
+                   : (nt == 2 ? launch_fwd1<H, 2, 0>(a, s) : launch_fwd1<H, 4, 0>(a, s));
+  }
   switch (nt) {
     case 1: return launch_fwd<1>(a, s);
     case 2: return launch_fwd<2>(a, s);

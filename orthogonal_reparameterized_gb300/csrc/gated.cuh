@@ -42,4 +42,10 @@ __device__ __forceinline__ float2 gated_grad(float g, float u, float dh, Act a) 
   return make_float2(dh * u * d, dh * v);
 }
 
+// What is left of v after its rounding to bf16, which is v's first piece (nothing, where that is not finite).
+__device__ __forceinline__ float rest_of(float v, __nv_bfloat16 first) {
+  const float f = __bfloat162float(first);
+  return isfinite(f) ? v - f : 0.f;
+}
+
 }  // namespace poetx

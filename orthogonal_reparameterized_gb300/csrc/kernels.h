@@ -240,17 +240,21 @@ poetx_status split_pieces(const float* a, long long na, uint8_t* da, size_t a_st
 poetx_status sum_partials(bool f32, const float* part, int S, long long stride, long long count, void* out,
                           cudaStream_t s);
 
-// ---- ffn_rows.cu: the gated feed-forward block of few fp32 rows
+// ---- ffn_rows.cu: the gated feed-forward block of few rows (bf16: the forward of one to four)
 constexpr int kRowsForward = 32;  // at most, or by the size of the block
 bool rows_forward_fits(int N, int D, int F);
+bool rows_forward_fits_bf16(int N, int D, int F);
 struct RowsForward {
-  const float *x, *W;
+  bool f32;
+  const void *x, *W;
   int N, D, F;
-  float *h, *z;     // [N][F], [N][2 F], each nullable
-  const float* dh;  // nullable; else dz [N][2 F] is what is wanted
-  float* dz;
+  void *h, *z;      // [N][F], [N][z_pitch], each nullable
+  const void* dh;   // nullable; else z is to be dz, in bf16 its first piece
+  void* z2;         // and this its second
+  long long z_pitch;
 };
-poetx_status rows_forward(const RowsForward& c, poetx_activation act, cudaStream_t s);
+struct Act;
+poetx_status rows_forward(const RowsForward& c, const Act& act, cudaStream_t s);
 constexpr int kRowsGradients = 16;
 struct RowsGradients {
   const float *dz, *x, *W;  // dz [N][V]

@@ -258,7 +258,9 @@ def test_ffn_f32_few_rows(P, N, D, F, act, kept):
 
 
 @pytest.mark.parametrize("kept", [True, False], ids=["kept", "mem"])
-@pytest.mark.parametrize("N,D,F", [(1, 264, 4096), (4, 72, 1000), (6, 4104, 72), (8, 2056, 520), (9, 264, 200),
+@pytest.mark.parametrize("N,D,F", [(1, 264, 4096), (1, 8, 8), (1, 16456, 24), (1, 4104, 4104), (2, 1032, 808),
+                                   (2, 4104, 4104), (3, 136, 72), (4, 2056, 520), (4, 72, 1000), (6, 4104, 72),
+                                   (8, 2056, 520), (9, 264, 200),
                                    (3, 40968, 16), (8, 8, 20000), (7, 2056, 8200),
                                    # units of 128 rows and columns: one of both, ends inside them, more
                                    # blocks of columns than SMs, several jobs of a CTA
@@ -267,17 +269,21 @@ def test_ffn_f32_few_rows(P, N, D, F, act, kept):
 def test_ffn_bf16_few_rows(P, N, D, F, kept):
     x, W, dh = _ffn_inputs(N, D, F, "bf16", 11 * N + D + F)
     got = _run(P, x, W, dh, B.GELU, kept)
+    h, z = B.ffn(host(x), host(W), B.GELU)
+    assert O.rel_fro(host(got["z"]), z) <= R + EXTRA and O.rel_fro(host(got["h"]), h) <= R + EXTRA
     dx, dW = B.ffn_bwd(host(x), host(W), host(dh), B.GELU, host(got["z"]) if kept else None)
     for k, ref in (("dx", dx), ("dW", dW)):
         assert O.rel_fro(host(got[k]), ref) <= 2 * R + EXTRA, k
 
 
-@pytest.mark.parametrize("N,dt", [(1, "bf16"), (8, "bf16"), (11, "bf16"), (64, "bf16"), (2, "f32"), (8, "f32"), (15, "f32"), (25, "f32")])
+@pytest.mark.parametrize("N,dt", [(1, "bf16"), (8, "bf16"), (11, "bf16"), (64, "bf16"), (2, "f32"),
+                                  (8, "f32"), (15, "f32"), (25, "f32")])
 def test_ffn_options_few_rows(P, N, dt):
     test_ffn_options(P, N, dt)
 
 
-@pytest.mark.parametrize("N,dt", [(7, "bf16"), (15, "bf16"), (50, "bf16"), (8, "f32"), (14, "f32"), (30, "f32")])
+@pytest.mark.parametrize("N,dt", [(7, "bf16"), (15, "bf16"), (50, "bf16"), (8, "f32"), (14, "f32"),
+                                  (30, "f32")])
 def test_ffn_few_rows_on_their_own(P, N, dt):
     """A NaN row of x and an infinite upstream gradient stay in their rows."""
     x, W, dh = _ffn_inputs(N, 136, 264, dt, 23)
