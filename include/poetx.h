@@ -642,7 +642,8 @@ poetx_status poetx_qk_rope_bwd(const poetx_rope* r, poetx_dtype dt, const int32_
  * ------------------------------------------------------------------------------------- */
 
 /* norm[0] = sqrt(sum over every element of every tensor of g^2), fp32 on the device, summed in a fixed
- * order (fp32 within a thread's few thousand terms, 64 bits above).  g, count, dt: HOST arrays of n
+ * order: in fp32 over sixteen terms, in two fp32 numbers over a thread block, in 64 bits above; within 2^-21
+ * of its value for any number of elements.  g, count, dt: HOST arrays of n
  * device pointers (16-byte aligned), element counts (0 to 2^33; POETX_ERR_SHAPE above) and types
  * (POETX_F32 or POETX_BF16), read before the call returns.  Squares that would leave fp32's range are
  * taken in 64 bits.  n >= 0 (0: norm 0).  ws: poetx_grad_norm_workspace_bytes(n) bytes.  (norm itself

@@ -8,7 +8,7 @@
 // tensors, laid end to end in units of 16 bytes of gradient, are cut into equal shares, one per resident
 // CTA: found by one binary search, then followed from tensor to tensor, so that many small tensors and few
 // large ones cost the same and no CTA is left with a last round of its own.  Every sum has a fixed order.
-// Norm of 0.92 GB in 226 tensors: 138 us (6.6 TB/s).  Step of 11.2 M parameters in 14 tensors: 44 us; of
+// Norm of 0.92 GB in 226 tensors: 139 us (6.5 TB/s).  Step of 11.2 M parameters in 14 tensors: 44 us; of
 // 360 M in 448, with the norm before it, 1.63 ms (11.5 GB at 7.0 TB/s).
 //
 #include <algorithm>
@@ -69,11 +69,32 @@ __device__ __forceinline__ float clip_factor(const float* norm, float max_norm) 
   return f >= 1.f ? 1.f : f;
 }
 
-// Squares of eight (four) neighbouring values into the thread's fp32 sums, or, where the largest would
-// lose them to fp32's range (above 2^50, or below 2^-50 and not zero), into its 64-bit one.  The others
-// beside a largest of 2^-50 or more are below 2^-13 of it where their square leaves the normal range.
+// The rounding error of s = a + b, exactly (Knuth's two-sum), for each of two.
+__device__ __forceinline__ float2 lost_by(float2 a, float2 b, float2 s) {
+  const float2 b0 = add2(s, neg2(a)), a0 = add2(s, neg2(b0));
+  return add2(add2(a, neg2(a0)), add2(b, neg2(b0)));
+}
+
+// A sum in two numbers: what rounding took from the first is in the second, so that its error (2^-45 or so)
+// does not grow with the terms.  (64-bit adds run at two a cycle on an SM.)
+struct Sum2 {
+  float2 top = {0.f, 0.f}, rest = {0.f, 0.f};
+  __device__ __forceinline__ void add(float2 v) {
+    const float2 s = add2(top, v);
+    rest = add2(rest, lost_by(top, v, s));
+    top = s;
+  }
+};
+
+// A thread's sum of squares.  The kUnroll vectors that it loads at a time give two fp32 sums of eight terms
+// at most, whose sum (off by 9 x 2^-24 at most) a Sum2 takes up: the error is the same for any number of
+// elements.  Where the largest of a vector would lose its square to fp32's range (above 2^50, or below 2^-50
+// and not zero), that vector goes into a 64-bit sum.  The others beside a largest of 2^-50 or more are below
+// 2^-13 of it where their square leaves the normal range.
+constexpr int kUnroll = 4;
 struct Squares {
-  float2 a = {0.f, 0.f}, b = {0.f, 0.f};
+  float2 a = {0.f, 0.f}, b = {0.f, 0.f};  // since the last flush
+  Sum2 sum;
   double wide = 0.0;
   template <int N>
   __device__ __forceinline__ void add(const float (&v)[N]) {
@@ -96,6 +117,10 @@ struct Squares {
       for (int i = 0; i < N; ++i) wide += (double)v[i] * (double)v[i];
     }
   }
+  __device__ __forceinline__ void flush() {
+    sum.add(add2(a, b));
+    a = b = both(0.f);
+  }
 };
 
 __device__ __forceinline__ void words(const uint4& w, float (&v)[4]) {
@@ -113,36 +138,43 @@ __device__ __forceinline__ void halves(const uint4& w, float (&v)[8]) {
   }
 }
 
-// The CTA's sum over its threads, on thread 0: fp32 trees of positive terms, and 64 bits where a thread
-// had recourse to them (64-bit adds run at two a cycle on an SM: over all threads they cost 5 us).
+// The CTA's sum over its threads, on thread 0: two-number sums as well, and 64 bits where a thread had
+// recourse to them.
 __device__ __forceinline__ double block_sum(const Squares& s) {
-  __shared__ float red[kThreads / 32];
+  __shared__ float2 red[kThreads / 32];
   __shared__ double red_wide[kThreads / 32];
-  float v = (s.a.x + s.a.y) + (s.b.x + s.b.y);
+  // (both halves of a pair carry the same numbers from here on)
+  Sum2 v{both(s.sum.top.x), both(s.sum.rest.x)};
+  v.add(both(s.sum.top.y));
+  v.rest = add2(v.rest, both(s.sum.rest.y));
   double w = s.wide;
+  auto join = [&](int o) {
+    const float top = __shfl_xor_sync(0xffffffffu, v.top.x, o);
+    const float rest = __shfl_xor_sync(0xffffffffu, v.rest.x, o);
+    v.add(both(top));
+    v.rest = add2(v.rest, both(rest));
+    if (__any_sync(0xffffffffu, w != 0.0)) w += __shfl_xor_sync(0xffffffffu, w, o);
+  };
 #pragma unroll
-  for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-  if (__any_sync(0xffffffffu, w != 0.0)) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-  }
+  for (int o = 16; o; o >>= 1) join(o);
   if ((threadIdx.x & 31) == 0) {
-    red[threadIdx.x >> 5] = v;
+    red[threadIdx.x >> 5] = make_float2(v.top.x, v.rest.x);
     red_wide[threadIdx.x >> 5] = w;
   }
   __syncthreads();
-  float sum = red[0];
-  double wide = red_wide[0];
+  if (threadIdx.x >= 32) return 0.0;
+  constexpr int W = kThreads / 32;
+  const float2 mine = red[threadIdx.x % W];
+  v = Sum2{both(mine.x), both(mine.y)};
+  w = red_wide[threadIdx.x % W];
 #pragma unroll
-  for (int i = 1; i < kThreads / 32; ++i) {
-    sum += red[i];
-    if (red_wide[i] != 0.0) wide += red_wide[i];
-  }
-  return (double)sum + wide;
+  for (int o = W / 2; o; o >>= 1) join(o);
+  return ((double)v.top.x + (double)v.rest.x) + w;
 }
 
+// (Five CTAs per SM: with six the two-number sums spill and 0.92 GB take 149 us.)
 template <int MAX>
-__global__ void __launch_bounds__(kThreads, 6)
+__global__ void __launch_bounds__(kThreads, 5)
     norm_kernel(const __grid_constant__ Table<MAX, 1> t, double* part) {
   pdl_trigger();
   pdl_wait();
@@ -150,7 +182,7 @@ __global__ void __launch_bounds__(kThreads, 6)
   for_share(t, [&](int k, long long first, int units, int rest) {
     const uint4* g = static_cast<const uint4*>(t.p[0][k]) + first;
     const bool half = t.bf16[k];
-    constexpr int U = 4;
+    constexpr int U = kUnroll;
     for (int i0 = threadIdx.x; i0 < units; i0 += U * kThreads) {
       uint4 w[U];
 #pragma unroll
@@ -169,12 +201,14 @@ __global__ void __launch_bounds__(kThreads, 6)
           sq.add(v);
         }
       }
+      sq.flush();
     }
     if ((int)threadIdx.x < rest) {  // the tensor's last elements
       const void* e = g + units;
       const float v[4] = {half ? __bfloat162float(static_cast<const __nv_bfloat16*>(e)[threadIdx.x])
                                : static_cast<const float*>(e)[threadIdx.x], 0.f, 0.f, 0.f};
       sq.add(v);
+      sq.flush();
     }
   });
   const double s = block_sum(sq);
@@ -334,7 +368,7 @@ using Many = std::integral_constant<int, kTensors>;
 
 // CTAs of a kernel: one per kThreads units up to the resident ones, or, where `small` units are enough
 // for a CTA, as many as there are such shares.  The norm, which only reads, runs at the copy's rate with
-// equal shares for the resident CTAs (0.9 GB in 138 us).  The step, with seven streams, wants neighbouring
+// equal shares for the resident CTAs (0.9 GB in 139 us).  The step, with seven streams, wants neighbouring
 // CTAs at neighbouring addresses and a scheduler that hands out work as it is done: 360 million
 // parameters (norm included) take 1.93 ms with resident shares, 1.67 with 1024 units, 1.63 with 512, the
 // two vectors that a thread has in flight.

@@ -65,8 +65,6 @@ struct RopeArgs {
   float eps;
 };
 
-__device__ __forceinline__ float2 neg2(float2 v) { return make_float2(-v.x, -v.y); }
-
 // f / 2 pi in units of 2^-64 turns, modulo a turn (in 64-bit integers the same took as long).
 __device__ __forceinline__ unsigned long long turns_of(float f) {
   double w = (double)f * 0.15915494309189533577;  // 1 / 2 pi
