@@ -597,7 +597,8 @@ poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, const void* x, 
  * multiples of 16), 1 <= axes <= 8.
  * inv_freq [rot_dim / 2] fp32; axis [rot_dim / 2] int32 in 0 .. axes-1 (nullable: all 0; a value outside
  * makes its pair NaN); both device.  Positions are int32, of either sign.  Angles are reduced in
- * 64-bit fixed point, exact to 2^-32 turns at any position for |inv_freq| <= 2 pi. */
+ * 64-bit fixed point, to 2^-32 turns at any position for |inv_freq| <= 2 pi, and rounded to fp32 (2^-26 turns
+ * at most). */
 typedef struct poetx_rope {
   int head_dim, rot_dim;
   int interleaved;

@@ -56,12 +56,49 @@ def _pairs(rot, interleaved):
     return (2 * i, 2 * i + 1) if interleaved else (i, i + rot // 2)
 
 
+# 2^256 / (2 pi), rounded: a turn in integers.  (2 pi by Machin's formula, 320 bits.)
+def _turn_bits(bits=256, more=64):
+    one = 1 << (bits + more)
+
+    def arctan_of_inverse(x):
+        term = total = one // x
+        k, sign = 1, -1
+        while term:
+            term //= x * x
+            k += 2
+            total += sign * (term // k)
+            sign = -sign
+        return total
+
+    two_pi = 8 * (4 * arctan_of_inverse(5) - arctan_of_inverse(239))  # times 2^(bits + more)
+    return ((one << bits) + two_pi // 2) // two_pi
+
+
+_TURN_BITS = 256
+_INVERSE_TURN = _turn_bits(_TURN_BITS)
+
+
+def _angles(pos, freq):
+    """pos * freq (whole numbers by 64-bit numbers, both exact), modulo 2 pi where the product in 64 bits would
+    have lost more than 2^-43 of a radian."""
+    pos, freq = np.broadcast_arrays(pos, freq)
+    angle = pos.astype(np.float64) * freq
+    for i in zip(*np.nonzero(np.abs(angle) > 1024.0)):
+        num, den = float(freq[i]).as_integer_ratio()  # den is a power of two
+        scale = den << _TURN_BITS
+        turns = (int(pos[i]) * num * _INVERSE_TURN) % scale
+        if 2 * turns > scale:
+            turns -= scale
+        angle[i] = turns / scale * (2 * np.pi)
+    return angle
+
+
 def _rotate(x, pos, inv_freq, axis, interleaved, sign):
     """x [N, H, dh]; pos [axes, N]; the pairs turned by sign times their angles."""
     half = len(inv_freq)
     first, second = _pairs(2 * half, interleaved)
     ax = np.zeros(half, int) if axis is None else np.asarray(axis, int)
-    angle = np.asarray(pos, np.float64)[ax].T * np.asarray(inv_freq, np.float64)
+    angle = _angles(np.asarray(pos)[ax].T, np.asarray(inv_freq, np.float64))
     c, s = np.cos(angle)[:, None], sign * np.sin(angle)[:, None]
     y = x.copy()
     y[..., first] = x[..., first] * c - x[..., second] * s

@@ -20,8 +20,9 @@
 // and four heads, 0.55 issued per cycle and quarter of an SM.
 //
 // The angle is reduced in 64-bit fixed point: with f = inv_freq / 2 pi in units of 2^-64 turns (modulo a
-// turn), pos * f modulo 2^64 is the angle modulo a turn, exact to 2^-32 turns at any int32 position (an
-// fp32 product of position and frequency has lost the angle's second decimal at position 100000).
+// turn), pos * f modulo 2^64 is the angle modulo a turn, to 2^-32 turns at any int32 position for |inv_freq| <=
+// 2 pi (an fp32 product of position and frequency has lost the angle's second decimal at position 100000).
+// Its rounding to fp32 is up to 2^-26 turns, 9e-8 radians.
 #include <mutex>
 
 #include "common.cuh"
@@ -65,11 +66,16 @@ struct RopeArgs {
   float eps;
 };
 
-// f / 2 pi in units of 2^-64 turns, modulo a turn (in 64-bit integers the same took as long).
+// f / 2 pi in units of 2^-64 turns, modulo a turn, to one such unit for |f| <= 2 pi: 1 / 2 pi in two doubles,
+// the first's product with its rounding error (one double alone is 2^-53 turns off, which a position of 2^31
+// makes 2^-22).  The magnitude's whole turns leave the first product without rounding; the sign comes last.
 __device__ __forceinline__ unsigned long long turns_of(float f) {
-  double w = (double)f * 0.15915494309189533577;  // 1 / 2 pi
-  w -= floor(w);
-  return w < 1.0 ? (unsigned long long)(w * 18446744073709551616.0) : 0ull;
+  const double a = fabs((double)f), inv_hi = 0x1.45f306dc9c883p-3, inv_lo = -0x1.6b01ec5417056p-57;
+  const double p = a * inv_hi, e = fma(a, inv_lo, fma(a, inv_hi, -p));
+  // (e is below 2^-50 turns for such f; whole turns of a larger one leave it without rounding too)
+  const unsigned long long t = __double2ull_rn((p - floor(p)) * 0x1p64) +
+                               (unsigned long long)__double2ll_rn((e - rint(e)) * 0x1p64);
+  return f < 0.f ? 0ull - t : t;
 }
 
 // A lane's chunk of one head in one array: CH first and CH second elements of its pairs.
@@ -299,7 +305,8 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(CH, NORM && BWD))
         const int p = __shfl_sync(0xffffffffu, pos, k < 0 ? 0 : k);
         if (i >= a.half) break;
         const unsigned long long ang = (unsigned long long)(long long)p * turn[i];
-        const float h = (float)(int)(ang >> 32) * 0x1p-32f;  // turns, in [-1/2, 1/2]
+        // turns, in [-1/2, 1/2]: rounded to 2^-32, then to fp32
+        const float h = (float)(int)((ang + (1ull << 31)) >> 32) * 0x1p-32f;
         float sv, cv;
         // bf16: the hardware's sine and cosine, within 2^-21 on (-pi, pi), far below the result's
         // rounding
