@@ -26,6 +26,7 @@
 
 #include "common.cuh"
 #include "kernels.h"
+#include "pieces.cuh"
 
 namespace poetx {
 
@@ -55,6 +56,8 @@ struct Args {
   int N, D, V;
   int dx, dW;
   const __nv_bfloat16* old;  // dW's contents, added (nullable)
+  const __nv_bfloat16 *z, *x;  // dz's first piece, [N][pitch], and x (for results that are NaN)
+  long long pitch;
   float* dxp;                // [splits][N][D]
   int* err;
   unsigned long long limit_ns;
@@ -285,12 +288,19 @@ __global__ void __launch_bounds__(kThreads, 1)
               v[2 * j + 1] += __uint_as_float(o[j] & 0xffff0000u);
             }
           }
-          *reinterpret_cast<uint4*>(stg + i / 8 * kBoxBytes + lane * 128 + (((i % 8) ^ (lane & 7)) << 4)) =
-              make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                         pack_bf16x2(v[6], v[7]));
+          const uint4 w = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                     pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+          *reinterpret_cast<uint4*>(stg + i / 8 * kBoxBytes + lane * 128 + (((i % 8) ^ (lane & 7)) << 4)) = w;
         }
         fence_async_shared();
         __syncwarp();
+        if (staged_not_finite(stg, kBoxBytes, lane)) {
+          if (row < p.V)
+            first_piece_again(stg, kBoxBytes, lane, p.z + row, p.pitch, p.x, p.N, p.D, col, 1.f,
+                              p.old ? p.old + (long long)row * p.D : nullptr);
+          fence_async_shared();
+          __syncwarp();
+        }
         if (lane == 0) {
           tma_store_2d(&mg, stg, col, row_w);
           if (col + 64 < p.D) tma_store_2d(&mg, stg + kBoxBytes, col + 64, row_w);
@@ -314,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int i = 0; i < 16; ++i)
             if (n + i < p.N && c < p.D)
-              out[(long long)(n + i) * p.D] = __uint_as_float(hi[i]) + __uint_as_float(lo[i]);
+              out[(long long)(n + i) * p.D] = with_rest(__uint_as_float(hi[i]), __uint_as_float(lo[i]));
         }
         tc_fence_before();
         __syncwarp();
@@ -391,6 +401,9 @@ poetx_status few_gradients(const FewGradients& c, cudaStream_t s) {
   a.dx = c.dx != nullptr;
   a.dW = c.dW != nullptr;
   a.old = c.accumulate ? static_cast<const __nv_bfloat16*>(c.dW) : nullptr;
+  a.z = static_cast<const __nv_bfloat16*>(c.dz);
+  a.x = static_cast<const __nv_bfloat16*>(c.x);
+  a.pitch = c.pitch;
   a.dxp = c.dxp;
   a.err = device_error_word();
   a.limit_ns = kWaitLimitNs;

@@ -109,6 +109,9 @@ struct HeadGemm {
   float* unit;           //   largest magnitude goes to unit (head_unit), read back as
   const float* out_scale;  // gradients' products: factor of the sums (nullable: 1), times T
   float T;
+  const __nv_bfloat16 *z, *x;  // dz in two pieces: the first, [rows][z_pitch], and x [rows][N]
+  long long z_pitch;
+  int rows;
   int* err;
   unsigned long long limit_ns;
 };
@@ -582,10 +585,27 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           fill(stg + (BOXES - 1) * kStgBytes, half(64));
           fence_async_shared();
           __syncwarp();
-          if (lane == 0) {
+          auto send = [&]() {
+            if (lane != 0) return;
             tma_store_2d(mc, stg, col0, orow);
             if (col0 + 64 < d.n_store) tma_store_2d(mc, stg + (BOXES - 1) * kStgBytes, col0 + 64, orow);
             bulk_commit();
+          };
+          // (looked at behind the store, where it costs 1 % and not 3, unless the store overwrites what is added)
+          bool bad = d.add_bf16 && staged_not_finite(stg, kStgBytes, lane);
+          if (!bad) {
+            send();
+            bad = !d.add_bf16 && staged_not_finite(stg, kStgBytes, lane);
+            if (bad && lane == 0) bulk_wait_all();
+          }
+          if (bad) {
+            __syncwarp();
+            if (row < d.M)
+              first_piece_again(stg, kStgBytes, lane, p.z + row, p.z_pitch, p.x, p.rows, d.N, col0, out_scale,
+                                d.add_bf16 ? d.add_bf16 + (long long)row * d.N : nullptr);
+            fence_async_shared();
+            __syncwarp();
+            send();
           }
         } else {
 #pragma unroll
@@ -1291,10 +1311,11 @@ __global__ void __launch_bounds__(256) head_split_kernel(const SplitArray a, con
   split_arrays(a, b, (long long)blockIdx.x * blockDim.x + threadIdx.x, (long long)gridDim.x * blockDim.x);
 }
 
-// out = sum over S fp32 partials of `stride` elements each, in order (count a multiple of 4).  The
+// out = sum over S fp32 partials of `stride` elements each, in order (count a multiple of 4).  PAIRS: every
+// second one is of dz's second piece and the one before it of its first (with_rest).  The
 // partials were written just before and are read from L2 (1021 x 1600: 10 us).  Few rows have many partials
 // each: sixteen are in flight per thread (16 rows of 4096 x 14336, the whole backward: 134 -> 120 us).
-template <typename T>
+template <typename T, bool PAIRS>
 __global__ void __launch_bounds__(256)
     head_sum_kernel(const float* __restrict__ part, int S, long long stride, long long quads,
                     T* __restrict__ out) {
@@ -1322,6 +1343,15 @@ __global__ void __launch_bounds__(256)
     };
     if (S <= 5) add(std::integral_constant<int, 4>{});
     else add(std::integral_constant<int, 16>{});
+    if (PAIRS && isnan((a.x + a.y) + (a.z + a.w))) {  // (also where infinities of both signs are beside each other)
+      float v[4] = {};
+#pragma unroll 1
+      for (int k = 0; k < S; k += 2)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          v[j] += with_rest(part[k * stride + 4 * i + j], part[(k + 1) * stride + 4 * i + j]);
+      a = make_float4(v[0], v[1], v[2], v[3]);
+    }
     if (sizeof(T) == 2) {
       *reinterpret_cast<uint2*>(out + 4 * i) = make_uint2(pack_bf16x2(a.x, a.y), pack_bf16x2(a.z, a.w));
     } else {
@@ -1591,6 +1621,12 @@ poetx_status grad_products(const GradProducts& c, cudaStream_t s) {
   set_segs(&h, c.f32, false, rows);
   h.out_scale = c.unit;
   h.T = c.T;
+  if (c.fine) {
+    h.z = reinterpret_cast<const __nv_bfloat16*>(c.z[0]);
+    h.x = reinterpret_cast<const __nv_bfloat16*>(c.x);
+    h.z_pitch = c.pitch;
+    h.rows = rows;
+  }
   int used = 0;
   const int c_rows = (int)align_up((size_t)rows, 256);
   if (c.dx) {
@@ -1652,19 +1688,23 @@ poetx_status grad_products(const GradProducts& c, cudaStream_t s) {
     POETX_TRY((gemm<false, 1>(mp, second, h, s)));
   if (c.dx && sums > 1)
     POETX_TRY(sum_partials(c.f32, c.dxp, sums, (long long)(c.fine ? BM : c_rows) * c.D,
-                           (long long)rows * c.D, c.dx, s));
+                           (long long)rows * c.D, c.dx, s, c.fine));
   return POETX_OK;
 }
 
 poetx_status sum_partials(bool f32, const float* part, int S, long long stride, long long count, void* out,
-                          cudaStream_t s) {
+                          cudaStream_t s, bool pairs) {
   const dim3 grid(grid_for(count / 4, 256)), block(256);
+  __nv_bfloat16* const out16 = static_cast<__nv_bfloat16*>(out);
   if (f32)
-    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float>, grid, block, 0, s, part, S, stride, count / 4,
+    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<float, false>, grid, block, 0, s, part, S, stride, count / 4,
                               static_cast<float*>(out)));
+  else if (pairs)
+    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16, true>, grid, block, 0, s, part, S, stride,
+                              count / 4, out16));
   else
-    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16>, grid, block, 0, s, part, S, stride, count / 4,
-                              static_cast<__nv_bfloat16*>(out)));
+    POETX_CUDA_TRY(launch_pdl(head_sum_kernel<__nv_bfloat16, false>, grid, block, 0, s, part, S, stride,
+                              count / 4, out16));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_HEAD_ROW);
   return POETX_OK;

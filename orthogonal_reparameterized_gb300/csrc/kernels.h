@@ -236,9 +236,10 @@ int grad_splits(long long rows, int D, int V, bool f32);
 poetx_status split_pieces(const float* a, long long na, uint8_t* da, size_t a_step, const float* b,
                           long long nb, uint8_t* db, size_t b_step, cudaStream_t s);
 
-// out = the sum of S partial sums of `count` values (a multiple of 4), `stride` apart.
+// out = the sum of S partial sums of `count` values (a multiple of 4), `stride` apart; pairs: those of dz's two
+// pieces in turn.
 poetx_status sum_partials(bool f32, const float* part, int S, long long stride, long long count, void* out,
-                          cudaStream_t s);
+                          cudaStream_t s, bool pairs = false);
 
 // ---- ffn_rows.cu: the gated feed-forward block of few rows (bf16: the forward of one to four)
 constexpr int kRowsForward = 32;  // at most, or by the size of the block

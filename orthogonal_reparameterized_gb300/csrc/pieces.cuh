@@ -5,6 +5,43 @@
 
 namespace poetx {
 
+// Products of two bf16 pieces of dz with W or x: the second piece holds rests of either sign and zeros, so that
+// where W or x is infinite its product is NaN or of the wrong sign, and the first piece's alone, an infinity or
+// NaN, is the result.  (It is finite only where no factor was infinite.)
+__device__ __forceinline__ float with_rest(float first, float rest) {
+  return isfinite(first) ? first + rest : first;
+}
+// dW's sum is over both pieces.  An infinity of x meets every feature's dz, so that its column of dW is infinite or
+// NaN in every row: a warp looks at one row of its staged 32 rows x 128 columns (two boxes of 64 columns with
+// 128-byte swizzle, `box` bytes apart), each lane at four columns.  (Looking at every result cost the gradients of
+// 33 rows 3 %.)
+__device__ __forceinline__ bool staged_not_finite(const uint8_t* stg, int box, int lane) {
+  const uint2 w =
+      *reinterpret_cast<const uint2*>(stg + lane / 16 * box + ((lane % 16 / 2) << 4) + (lane & 1) * 8);
+  const uint32_t top = __vmaxs2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
+  return __any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || top >> 16 >= 0x7f80u);
+}
+// Then each lane goes through its row of the boxes, columns from col on of D: what is NaN becomes scale * the sum
+// over the tokens of the first piece of dz (z + n pitch) by x (+ old), which ends at a NaN of its own.
+__device__ __forceinline__ void first_piece_again(uint8_t* stg, int box, int lane, const __nv_bfloat16* z,
+                                                  long long pitch, const __nv_bfloat16* x, int N, int D,
+                                                  int col, float scale, const __nv_bfloat16* old) {
+#pragma unroll 1
+  for (int c = 0; c < 128 && col + c < D; ++c) {
+    __nv_bfloat16* const at =
+        reinterpret_cast<__nv_bfloat16*>(stg + c / 64 * box + lane * 128 + (((c % 64 / 8) ^ (lane & 7)) << 4)) +
+        c % 8;
+    if (!isnan(__bfloat162float(*at))) continue;
+    float s = 0.f;
+#pragma unroll 1
+    for (int n = 0; n < N && !isnan(s); ++n)
+      s = fmaf(__bfloat162float(z[n * pitch]), __bfloat162float(x[(long long)n * D + col + c]), s);
+    s *= scale;
+    if (old) s += __bfloat162float(old[col + c]);
+    *at = __float2bfloat16_rn(s);
+  }
+}
+
 // Three bf16 pieces of v, whose sum it is.  An infinity or NaN goes into the third with zeros before it:
 // the products take the third piece with the other operand's first alone, so that it meets each number
 // once, with that number's own sign (inf - inf in the split and inf times a rest of either sign would make
