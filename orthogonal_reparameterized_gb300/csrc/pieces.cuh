@@ -42,17 +42,19 @@ __device__ __forceinline__ void first_piece_again(uint8_t* stg, int box, int lan
   }
 }
 
-// Three bf16 pieces of v, whose sum it is.  An infinity or NaN goes into the third with zeros before it:
-// the products take the third piece with the other operand's first alone, so that it meets each number
-// once, with that number's own sign (inf - inf in the split and inf times a rest of either sign would make
-// NaN of a plain infinity).  A finite value that would round to infinity is cut off at bf16's largest.
+// Three bf16 pieces of v, whose sum it is.  An infinity goes into the third: the products take the third piece
+// with the other operand's first alone, so that it meets each number once, with that number's own sign (inf - inf
+// in the split and inf times a rest of either sign would make NaN of a plain infinity).  Its first piece is its sign
+// as a 1, for an infinity of the other operand: zero would make NaN of inf times inf.  A NaN is the third piece
+// with zeros before it.  A finite value that would round to infinity is cut off at bf16's largest.
 constexpr float kBf16Max = 0x1.fep127f;
 template <bool CHECK = true>
 __device__ __forceinline__ void split3(float v, __nv_bfloat16 (&o)[3]) {
   o[0] = __float2bfloat16_rn(v);
   if (CHECK && !(fabsf(v) <= kBf16Max)) {
     if (!isfinite(v)) {
-      o[0] = o[1] = __float2bfloat16_rn(0.f);
+      o[0] = __float2bfloat16_rn(isnan(v) ? 0.f : copysignf(1.f, v));
+      o[1] = __float2bfloat16_rn(0.f);
       o[2] = __float2bfloat16_rn(v);
       return;
     }

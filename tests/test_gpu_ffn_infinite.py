@@ -91,3 +91,33 @@ def test_nan_among_the_gradients(P, N, dt):
     dx, dW, rdx, rdW = _grads(N, D, F, dt, x, W, z, dh)
     _same_kind(dx, rdx)
     _same_kind(dW, rdW)
+
+
+@pytest.mark.parametrize("N,D,dt", [(1, 264, "bf16"), (40, 264, "bf16"), (300, 264, "bf16"), (3, 264, "f32"),
+                                    (20, 264, "f32"), (300, 264, "f32"), (300, 1544, "f32")])
+def test_infinity_meets_infinity(P, N, D, dt):
+    """x W^T where x and W are infinite in the same place of K, and where one of them alone is."""
+    F = 200
+    x, W, _, _ = _inputs(N, D, F, dt, 7 * N)
+    x[N // 2, 5], W[9, 5], W[F + 12, 5] = INF, INF, -INF
+    W[F + 9, 100] = -INF
+    z = torch.empty(N, 2 * F, dtype=DT[dt], device=DEV)
+    h = torch.empty(N, F, dtype=DT[dt], device=DEV)
+    P.poetx_ffn_fwd(x.to(DEV), W.to(DEV), h, z=z)
+    torch.cuda.synchronize()
+    with np.errstate(invalid="ignore"):
+        ref = host(x) @ host(W).T
+    assert ref[N // 2, 9] == INF and ref[N // 2, F + 12] == -INF
+    _same_kind(host(z), ref)
+
+
+@pytest.mark.parametrize("N,D", [(17, 136), (140, 136), (300, 1544)])
+def test_infinite_gradient_meets_infinity(P, N, D):
+    """fp32 gradients: an infinite dz beside an infinite weight (dx) and an infinite input (dW)."""
+    F = 200
+    x, W, z, dh = _inputs(N, D, F, "f32", N + 3000)
+    dh[N // 2, 40], W[40, 7], W[F + 40, 9], x[N // 2, 30] = INF, INF, -INF, -INF
+    dx, dW, rdx, rdW = _grads(N, D, F, "f32", x, W, z, dh)
+    assert np.isinf(rdW[[40, F + 40], 30]).all()
+    _same_kind(dx, rdx)
+    _same_kind(dW, rdW)
