@@ -521,12 +521,20 @@ def _want(fn: str, what: str, t, shape, dtype):
                          f"got {tuple(t.shape)} of {t.dtype}")
 
 
+def _here(t):
+    """Refuses a tensor that does not live on the current device, whose stream and limits a call takes."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("poetx: tensors must live on a CUDA device")
+    if dev != torch._C._cuda_getDevice():
+        raise ValueError("poetx: tensors must live on the current device")
+
+
 def _addr(t):
     """A tensor's device address as an integer (None: None)."""
     if t is None:
         return None
-    if not t.is_cuda:
-        raise ValueError("poetx: tensors must live on a CUDA device")
+    _here(t)
     if not t.is_contiguous():
         raise ValueError("poetx: tensors must be contiguous")
     return t.data_ptr()
@@ -658,11 +666,7 @@ def poetx_head_distill(x, W, t_index, t_logit, loss, dloss=None, dx=None, dW=Non
 
 # ---------------------------------------------------------------- the gated feed-forward block
 def _dtype(fn: str, t) -> int:
-    """The code of t's type; t must live on the current device."""
-    if not t.is_cuda:
-        raise ValueError("poetx: tensors must live on a CUDA device")
-    if t.get_device() != torch._C._cuda_getDevice():
-        raise ValueError(f"{fn}: tensors must live on the current device")
+    """The code of t's type."""
     dt = _DT.get(t.dtype)
     if dt is None or dt == I8:
         raise ValueError(f"{fn}: bf16 or fp32, got {t.dtype}")
@@ -672,8 +676,7 @@ def _dtype(fn: str, t) -> int:
 def _rows(fn: str, what: str, t, width: int):
     """(address, elements from row to row) of t [N, ...] whose rows of `width` elements are each
     contiguous."""
-    if not t.is_cuda:
-        raise ValueError("poetx: tensors must live on a CUDA device")
+    _here(t)
     if t.is_contiguous():
         return t.data_ptr(), width
     at = width
