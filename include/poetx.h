@@ -660,7 +660,7 @@ poetx_status poetx_grad_clip(void* const* g, const poetx_dtype* dt, const long l
 /* poetx_adam_triu on n sets of tensors (HOST arrays of device pointers; count[i] elements each), with
  * every gradient multiplied by the factor of poetx_grad_clip as it is read (norm NULL: not at all;
  * dq itself is not written).  Without norm, or with the factor 1, bit for bit the result of
- * poetx_adam_triu on each. */
+ * poetx_adam_triu on each.  The tensors of q, m and v do not overlap each other. */
 poetx_status poetx_adam_group(float* const* q, const float* const* dq, float* const* m,
                               float* const* v, const long long* count, int n, const poetx_adam* hp,
                               float max_norm, const float* norm, cudaStream_t stream);

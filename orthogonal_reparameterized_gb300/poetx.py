@@ -863,6 +863,15 @@ def _at(a):
     return a.buffer_info()[0]
 
 
+def _distinct(fn, what, p, counts):
+    """Refuses tensors that are written and named twice: two blocks would do so at once."""
+    if len(set(p)) == len(p):
+        return
+    some = [a for a, n in zip(p, counts) if n]
+    if len(set(some)) != len(some):
+        raise ValueError(f"{fn}: a tensor is among {what} twice")
+
+
 def _gradients(fn, grads):
     if not isinstance(grads, (list, tuple)):
         grads = list(grads)  # (gone through several times)
@@ -895,11 +904,12 @@ def poetx_grad_norm(grads, norm, ws=None, stream=None):
 
 def poetx_grad_clip(grads, norm, max_norm: float, stream=None):
     """Every tensor of the list times min(1, max_norm / (norm + 1e-6)), in place; norm [1] as
-    poetx_grad_norm leaves it."""
+    poetx_grad_norm leaves it.  The tensors must not overlap (one that is listed twice is refused)."""
     fn = "poetx_grad_clip"
     _want(fn, "norm", norm, (1,), torch.float32)
     pn = _addr(norm)
     p, dts, counts = _gradients(fn, grads)
+    _distinct(fn, "the gradients", p, counts)
     st = lib().poetx_grad_clip(_at(p), _at(dts), _at(counts), len(p), max_norm, pn,
                                _raw_stream(stream, norm))
     if st:
@@ -910,7 +920,8 @@ def poetx_adam_group(q, dq, m, v, step: int, lr: float, beta1: float = 0.9, beta
                      eps: float = 1e-8, weight_decay: float = 0.0, norm=None,
                      max_norm: float = float("inf"), stream=None):
     """poetx_adam_triu on lists of fp32 tensors at once; with norm [1] every gradient is multiplied by
-    min(1, max_norm / (norm + 1e-6)) as it is read (dq is not written)."""
+    min(1, max_norm / (norm + 1e-6)) as it is read (dq is not written).  The tensors of q, m and v must not
+    overlap (one that is listed twice is refused)."""
     fn = "poetx_adam_group"
     n = len(q)
     if len(dq) != n or len(m) != n or len(v) != n:
@@ -921,6 +932,8 @@ def poetx_adam_group(q, dq, m, v, step: int, lr: float, beta1: float = 0.9, beta
         if ts is not q and array("q", map(torch.Tensor.numel, ts)) != count:
             raise ValueError(f"{fn}: dq, m and v must have the sizes of q")
         arrays.append(_arrays(fn, what, ts, _FP32)[0])
+        if what != "dq":
+            _distinct(fn, what, arrays[-1], count)
     _want(fn, "norm", norm, (1,), torch.float32)
     hp = AdamDesc(lr, beta1, beta2, eps, weight_decay, step)
     handle = _stream(stream) if n == 0 else _raw_stream(stream, q[0])
