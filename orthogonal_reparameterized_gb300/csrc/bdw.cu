@@ -467,12 +467,8 @@ poetx_status umma_bdw(const void* T, const void* S, long long N, int nblk, int b
   p.trace = trace_buffer(&p.trace_cap);
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [] {
-    attr = cudaFuncSetAttribute(bdw_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, BDW_SMEM);
-  });
-  POETX_CUDA_TRY(attr);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, bdw_kernel, BDW_SMEM));
   const int grid = (int)(units < sm_count() ? units : sm_count());
   POETX_CUDA_TRY(launch_pdl(bdw_kernel, dim3(grid), dim3(BDW_THREADS), BDW_SMEM, s, tT, tS, tY, tD,
                             p));

@@ -20,7 +20,7 @@ static std::atomic<int*> g_err_ptr[64];
 static std::atomic<int> g_sms[64];
 static std::atomic<int> g_last_site{0};
 
-static int current_device() {
+int current_device() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return -1;
   return dev;

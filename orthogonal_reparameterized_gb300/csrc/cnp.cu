@@ -25,7 +25,6 @@
 // (XS + SX) T + S^2 (XP + PX) with S = I + P, T = I + P^2 = I + Q2, S^2 = I - 2Q + Q2;
 // expanding the products gives the expression above.  Work per block: forward 3 b^3 FMA
 // (Q2 half by symmetry, then one full product), backward 5 b^3 FMA.
-#include <mutex>
 
 #include "cnp_umma.h"
 #include "common.cuh"
@@ -376,13 +375,8 @@ poetx_status cnp_backward_sides(const CnpSides& q, const float* Qin, const float
     vec = vec && aligned16(gr.dG[k]);
   }
   if (vec) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [] {
-      attr = cudaFuncSetAttribute(sum_partials_vec_kernel,
-                                  cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSumSmem);
-    });
-    POETX_CUDA_TRY(attr);
+    static PerDevice<cudaError_t> attr;
+    POETX_CUDA_TRY(allow_smem(attr, sum_partials_vec_kernel, (int)kSumSmem));
     dim3 grid(b / kSumC, b / kSumR, nblk);
     size_t tr_cap = 0;
     unsigned long long* tr = trace_buffer(&tr_cap);

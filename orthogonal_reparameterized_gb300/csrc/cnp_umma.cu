@@ -658,12 +658,8 @@ poetx_status launch_t(const CnpMaps& maps, const CnpUParams& p, int nblk, cudaSt
   auto k = cnp_umma_kernel<BN>;
   constexpr int smem = cnp_smem<BN>();
   static_assert(smem <= 227 * 1024, "shared memory per CTA exceeds the sm_103 limit");
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  });
-  POETX_CUDA_TRY(attr);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, k, smem));
   const int MT = p.b / BM, NT = p.b / BN;
   dim3 grid(p.sym ? MT * NT - (BM / BN) * MT * (MT - 1) / 2 : (p.M + BM - 1) / BM,
             p.sym ? 1 : p.b / BN, nblk);

@@ -11,6 +11,7 @@
 #include <utility>
 
 #include "../../include/poetx.h"
+#include "per_device.h"
 
 #define POETX_CUDA_TRY(expr)                                    \
   do {                                                          \
@@ -44,7 +45,8 @@ inline size_t dtype_size(poetx_dtype dt) {
   return dt == POETX_F32 ? 4 : (dt == POETX_BF16 ? 2 : (dt == POETX_I8 ? 1 : 0));
 }
 
-// Number of SMs of the current device (cached per device).
+// The current device (-1: none, or one beyond the 64 that are told apart), and its SMs (cached per device).
+int current_device();
 int sm_count();
 
 // Launch with programmatic dependent launch allowed: the kernel may start (and run its
@@ -85,6 +87,42 @@ inline cudaError_t launch_pdl_cluster(void (*kernel)(KArgs...), dim3 grid, dim3 
   cfg.attrs = attr;
   cfg.numAttrs = 2;
   return cudaLaunchKernelEx(&cfg, kernel, std::forward<Args>(args)...);
+}
+
+// The dynamic shared memory that a kernel asks for, allowed on the current device (`once`: the kernel's own).
+template <typename... KArgs>
+inline cudaError_t allow_smem(PerDevice<cudaError_t>& once, void (*kernel)(KArgs...), int smem) {
+  return once.get(current_device(), [&] {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+}
+// The same, and how many clusters of `cluster` blocks along x, of up to `grid` blocks, the device holds at a time
+// (cluster 1: not asked, 0).
+struct Clusters {
+  cudaError_t err;
+  int resident;
+};
+template <typename... KArgs>
+inline Clusters allow_clusters(PerDevice<Clusters>& once, void (*kernel)(KArgs...), int grid, int threads,
+                               int smem, int cluster) {
+  return once.get(current_device(), [&] {
+    Clusters c{cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, smem), 0};
+    if (c.err != cudaSuccess || cluster == 1) return c;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = cluster;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    c.err = cudaOccupancyMaxActiveClusters(&c.resident, kernel, &cfg);
+    if (c.err == cudaSuccess && c.resident < 1) c.err = cudaErrorInvalidConfiguration;
+    return c;
+  });
 }
 
 // Stages of the hot path, for the launch counter and the optional per-stage event timing.

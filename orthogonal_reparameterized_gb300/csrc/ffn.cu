@@ -27,7 +27,6 @@
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, drains its own
 // copies, frees its TMEM and returns.
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "gated.cuh"
@@ -889,12 +888,8 @@ poetx_status run_glu(const GluCall& c, cudaStream_t s) {
 template <int NT, bool MERGED>
 poetx_status score(const CUtensorMap& mw, const CUtensorMap& mx, FfnScore p, cudaStream_t s) {
   auto k = ffn_score_kernel<NT, MERGED>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, k, kScoreSmem));
   p.stages = score_room(NT, MERGED) / score_stage_bytes(NT, p.height, p.kps);
   if (p.stages > kScoreRing) p.stages = kScoreRing;
   p.err = device_error_word();
@@ -909,30 +904,12 @@ poetx_status score(const CUtensorMap& mw, const CUtensorMap& mx, FfnScore p, cud
 template <int SEGS, bool DZ>
 poetx_status gemm(const FfnMaps& m, FfnGemm& p, cudaStream_t s) {
   auto k = ffn_gemm_kernel<SEGS, DZ>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_pairs = 0;  // co-resident CTA pairs
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-    if (attr_err != cudaSuccess) return;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sm_count() / 2 * 2);
-    cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = kSmem;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    attr_err = cudaOccupancyMaxActiveClusters(&max_pairs, k, &cfg);
-    if (attr_err == cudaSuccess && max_pairs < 1) attr_err = cudaErrorInvalidConfiguration;
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<Clusters> setup;
+  const Clusters c = allow_clusters(setup, k, sm_count() / 2 * 2, kThreads, kSmem, 2);
+  POETX_CUDA_TRY(c.err);
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
-  const int pairs = p.num_tiles < max_pairs ? p.num_tiles : max_pairs;
+  const int pairs = p.num_tiles < c.resident ? p.num_tiles : c.resident;
   POETX_CUDA_TRY(launch_pdl_cluster(k, dim3(2 * pairs), dim3(kThreads), kSmem, s, 2, m, p));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_FFN_GEMM);

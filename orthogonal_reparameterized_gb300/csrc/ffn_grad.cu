@@ -22,7 +22,6 @@
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, waits for its own copies,
 // frees its TMEM and returns.
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -345,12 +344,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 template <int NT>
 poetx_status launch(const CUtensorMap (&m)[5], const Args& a, cudaStream_t s) {
   auto k = few_grad_kernel<NT>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of(NT));
-  });
-  POETX_CUDA_TRY(attr);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, k, smem_of(NT)));
   const int grid = (int)std::min<long long>((long long)a.blocks * a.splits, sm_count());
   POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kThreads), smem_of(NT), s, m[0], m[1], m[2], m[3], m[4], a));
   POETX_CUDA_TRY(cudaGetLastError());

@@ -20,7 +20,6 @@
 // several loads in flight is a wait for all of them).  The warps' sums of dx are joined in shared memory, the
 // CTAs' by the head's kernel for partial sums.  Sixteen rows of 2048 x 5632: 48 us (115 on the tensor cores).
 #include <algorithm>
-#include <mutex>
 
 #include "common.cuh"
 #include "gated.cuh"
@@ -407,13 +406,8 @@ poetx_status launch_fwd1(const FwdArgs& a, cudaStream_t s) {
   auto k = rows_fwd_kernel<T, NT, RING>;
   size_t smem = 0;
   if (RING) {
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] {
-      attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                  (int)(x_room(RING) + ring_bytes(RING)));
-    });
-    POETX_CUDA_TRY(attr);
+    static PerDevice<cudaError_t> attr;
+    POETX_CUDA_TRY(allow_smem(attr, k, (int)(x_room(RING) + ring_bytes(RING))));
     smem = a.x_bytes + ring_bytes(RING);
   }
   const int blocks = ceil_div(a.c.N, kBlock), pairs = a.c.F / 2;
@@ -442,12 +436,8 @@ poetx_status launch_fwd(FwdArgs a, cudaStream_t s) {
 template <int NT, bool ADD>
 poetx_status launch_grad1(const GradArgs& a, cudaStream_t s) {
   auto k = rows_grad_kernel<NT, ADD>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, grad_smem(NT, ADD));
-  });
-  POETX_CUDA_TRY(attr);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, k, grad_smem(NT, ADD)));
   POETX_CUDA_TRY(launch_pdl(k, dim3(a.tiles * a.splits), dim3(32 * kGradWarps), grad_smem(NT, ADD), s, a));
   POETX_CUDA_TRY(cudaGetLastError());
   after_launch(s, ST_FFN_GEMM);

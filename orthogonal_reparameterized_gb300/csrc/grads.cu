@@ -12,7 +12,6 @@
 // 360 M in 448, with the norm before it, 1.63 ms (11.5 GB at 7.0 TB/s).
 //
 #include <algorithm>
-#include <mutex>
 #include <type_traits>
 
 #include "adam.cuh"
@@ -374,13 +373,11 @@ using Many = std::integral_constant<int, kTensors>;
 // two vectors that a thread has in flight.
 template <typename K>
 int grid_of(K kernel, long long units, int small = 0) {
-  static std::once_flag once;  // (per kernel: a type of its own)
-  static int per_sm = 0;
-  std::call_once(once, [&] {
-    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kernel, kThreads, 0) != cudaSuccess ||
-        per_sm < 1)
-      per_sm = 1;
-    if (per_sm > kMaxParts) per_sm = kMaxParts;
+  static PerDevice<int> blocks;  // (per kernel: a type of its own)
+  const int per_sm = blocks.get(current_device(), [&] {
+    int n = 0;
+    if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kernel, kThreads, 0) != cudaSuccess) n = 1;
+    return std::min(std::max(n, 1), kMaxParts);
   });
   const long long even = std::min<long long>((units + kThreads - 1) / kThreads,
                                              (long long)per_sm * sm_count());

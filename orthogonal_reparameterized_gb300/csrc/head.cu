@@ -31,7 +31,6 @@
 //
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, drains its own
 // copies, frees its TMEM and returns.
-#include <mutex>
 #include <type_traits>
 
 #include "common.cuh"
@@ -1371,12 +1370,8 @@ unsigned grid_for(long long items, int threads) {
 template <int NT>
 poetx_status score(const CUtensorMap& mW, const CUtensorMap& mx, HeadScore p, cudaStream_t s) {
   auto k = head_score_kernel<NT>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kScoreSmem);
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, k, kScoreSmem));
   // (16 KB kept behind the last stage: the MMAs read 128 rows from its last K block's first)
   p.stages = (kScoreSmem - 1024 - 512 - score_turn_bytes(NT) - (int)kABytes) /
              score_stage_bytes(NT, p.height, p.kps);
@@ -1390,38 +1385,13 @@ poetx_status score(const CUtensorMap& mW, const CUtensorMap& mx, HeadScore p, cu
   return POETX_OK;
 }
 
-// Co-resident CTA pairs of a GEMM kernel (one CTA per SM).
-template <bool LSE, int SEGS>
-cudaError_t gemm_pairs(int* pairs) {
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_pairs = 0;
-  std::call_once(once, [&] {
-    auto k = head_gemm_kernel<LSE, SEGS>;
-    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, gemm_smem(SEGS));
-    if (attr_err != cudaSuccess) return;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(sm_count() / 2 * 2);
-    cfg.blockDim = dim3(kGemmThreads);
-    cfg.dynamicSmemBytes = gemm_smem(SEGS);
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeClusterDimension;
-    attr[0].val.clusterDim.x = 2;
-    attr[0].val.clusterDim.y = 1;
-    attr[0].val.clusterDim.z = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    attr_err = cudaOccupancyMaxActiveClusters(&max_pairs, k, &cfg);
-    if (attr_err == cudaSuccess && max_pairs < 1) attr_err = cudaErrorInvalidConfiguration;
-  });
-  *pairs = max_pairs;
-  return attr_err;
-}
-
 template <bool LSE, int SEGS>
 poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStream_t s) {
-  int max_pairs = 0;
-  POETX_CUDA_TRY((gemm_pairs<LSE, SEGS>(&max_pairs)));
+  // (one CTA per SM)
+  static PerDevice<Clusters> setup;
+  const Clusters c = allow_clusters(setup, head_gemm_kernel<LSE, SEGS>, sm_count() / 2 * 2, kGemmThreads,
+                                    gemm_smem(SEGS), 2);
+  POETX_CUDA_TRY(c.err);
   long long tiles = 0;
   for (const Product& d : p.prod) {
     if ((long long)d.tiles_m * d.tiles_n > 0x3fffffffLL) return POETX_ERR_SHAPE;
@@ -1431,7 +1401,7 @@ poetx_status gemm(const HeadMaps& m0, const HeadMaps& m1, HeadGemm& p, cudaStrea
   p.num_tiles = (int)tiles;
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
-  const int pairs = (int)(tiles < max_pairs ? tiles : max_pairs);
+  const int pairs = (int)(tiles < c.resident ? tiles : c.resident);
   POETX_CUDA_TRY(launch_pdl_cluster(head_gemm_kernel<LSE, SEGS>, dim3(2 * pairs),
                                     dim3(kGemmThreads),
                                     gemm_smem(SEGS), s, 2, m0, m1, p));
@@ -1747,16 +1717,9 @@ poetx_status run_head(const HeadCall& c, cudaStream_t s) {
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
   const size_t row_smem = align_up((size_t)c.K, 8) * 2 + (pl.grads ? (size_t)pl.groups * 4 : 0) +
                           (size_t)c.K * 12;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [] {
-    attr_err = cudaFuncSetAttribute(head_row_kernel<false>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(head_row_kernel<true>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, 160 * 1024);
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<cudaError_t> attr[2];
+  POETX_CUDA_TRY(pl.f32 ? allow_smem(attr[1], head_row_kernel<true>, 160 * 1024)
+                        : allow_smem(attr[0], head_row_kernel<false>, 160 * 1024));
 
   uint8_t* w = static_cast<uint8_t*>(c.ws);
   const size_t x_step = align_up((size_t)pl.rows * c.D * 2, 1024);

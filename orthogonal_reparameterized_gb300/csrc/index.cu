@@ -6,7 +6,6 @@
 // POET-X summary page ("POET-X: Memory-efficient LLM Training by Scaling Orthogonal
 // Transformation"), "Core method" section 2 (permutations as index remaps; merge of the
 // two permutations into W once per inner loop) and section 4 (upper-triangle storage).
-#include <mutex>
 
 #include "adam.cuh"
 #include "common.cuh"
@@ -573,17 +572,16 @@ static poetx_status launch_perm_rows_t(const void* X, long long N, int D, const 
   if (!(side ? perm_shape_side : perm_shape)(row_bytes, idx_bytes + 16, &G, &S, &smem))
     return POETX_ERR_SHAPE;
   auto k = perm_rows_kernel<E, SCATTER, IdxT, PITCHED>;
-  static std::once_flag once;  // the opt-in limit is set once, to the largest size used
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  static PerDevice<cudaError_t> attr;  // the opt-in limit is set once, to the largest size used
+  POETX_CUDA_TRY(attr.get(current_device(), [&] {
+    const cudaError_t e =
+        cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     // all of the unified L1 as shared memory, as the CNP products take it, so that a
     // co-resident CTA never holds an SM in a smaller split
-    if (attr == cudaSuccess)
-      attr = cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
-                                  (int)cudaSharedmemCarveoutMaxShared);
-  });
-  POETX_CUDA_TRY(attr);
+    return e != cudaSuccess ? e
+                            : cudaFuncSetAttribute(k, cudaFuncAttributePreferredSharedMemoryCarveout,
+                                                   (int)cudaSharedmemCarveoutMaxShared);
+  }));
   const int ngrp = kPermWarps / G;
   size_t tr_cap = 0;
   unsigned long long* tr = trace_buffer(&tr_cap);

@@ -11,7 +11,6 @@
 // Both passes are bound by HBM: 2 (forward) and 3 (backward) activations move, at a few flops per
 // byte.  A row is held in the registers of a group of threads, so that it is read once, and the
 // variance is the mean of the squared deviations from the mean already known (no cancellation).
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -865,10 +864,6 @@ int ring_stages(size_t bytes, int groups) {
   const int n = (int)((size_t)kRingBytes / (groups * bytes));
   return n < kMaxRing ? n : kMaxRing;
 }
-template <typename K>
-cudaError_t ring_attr(K k) {
-  return cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, kRingBytes);
-}
 
 template <typename T>
 cudaError_t fwd_ring(const void* x, int N, int D, const float* gamma, const float* beta, float eps,
@@ -877,10 +872,9 @@ cudaError_t fwd_ring(const void* x, int N, int D, const float* gamma, const floa
   const int threads = ring_shape(D / (16 / (int)sizeof(T))).threads;
   const int stages = ring_stages(stage, 1);
   auto k = layernorm_fwd_ring_kernel<T>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] { attr = ring_attr(k); });
-  if (attr != cudaSuccess) return attr;
+  static PerDevice<cudaError_t> attr;
+  const cudaError_t e = allow_smem(attr, k, kRingBytes);
+  if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(N < sm_count() ? N : sm_count()), dim3(threads), stages * stage, s,
                     static_cast<const T*>(x), N, D, gamma, beta, eps, static_cast<T*>(y), mean, rstd,
                     stages, device_error_word(), kWaitLimitNs);
@@ -894,10 +888,9 @@ cudaError_t bwd_ring_launch(const void* x, const void* dy, int N, int D, const f
   const int threads = ring_shape(D / (16 / (int)sizeof(T))).threads;
   const int stages = ring_stages(stage, GROUPS);
   auto k = layernorm_bwd_ring_kernel<T, NV, GROUPS>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] { attr = ring_attr(k); });
-  if (attr != cudaSuccess) return attr;
+  static PerDevice<cudaError_t> attr;
+  const cudaError_t e = allow_smem(attr, k, kRingBytes);
+  if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(parts), dim3(GROUPS * threads), GROUPS * stages * stage, s,
                     static_cast<const T*>(x), static_cast<const T*>(dy), N, D, gamma, mean, rstd,
                     static_cast<T*>(dx), pg, pb, stages, device_error_word(), kWaitLimitNs);

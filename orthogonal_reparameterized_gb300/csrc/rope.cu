@@ -23,7 +23,6 @@
 // turn), pos * f modulo 2^64 is the angle modulo a turn, to 2^-32 turns at any int32 position for |inv_freq| <=
 // 2 pi (an fp32 product of position and frequency has lost the angle's second decimal at position 100000).
 // Its rounding to fp32 is up to 2^-26 turns, 9e-8 radians.
-#include <mutex>
 
 #include "common.cuh"
 #include "kernels.h"
@@ -515,13 +514,9 @@ int rope_ctas(int esz, int CH, bool both, int half) {
 template <typename T, int CH, bool INTER, bool NORM, bool BWD>
 cudaError_t rope_launch1(const RopeArgs& a, cudaStream_t s) {
   auto k = rope_kernel<T, CH, INTER, NORM, BWD>;
-  static std::once_flag once;
-  static cudaError_t attr = cudaSuccess;
-  std::call_once(once, [&] {
-    attr = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                rope_smem(sizeof(T), CH, BWD && NORM, kMaxHalf));
-  });
-  if (attr != cudaSuccess) return attr;
+  static PerDevice<cudaError_t> attr;
+  const cudaError_t e = allow_smem(attr, k, rope_smem(sizeof(T), CH, BWD && NORM, kMaxHalf));
+  if (e != cudaSuccess) return e;
   return launch_pdl(k, dim3(a.s[0].ctas + a.s[1].ctas), dim3(kThreads),
                     rope_smem(sizeof(T), CH, BWD && NORM, a.half), s, a);
 }

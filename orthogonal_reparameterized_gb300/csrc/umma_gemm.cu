@@ -1251,35 +1251,16 @@ poetx_status launch(const CUtensorMap& ta, const CUtensorMap& tb, UmmaParams p, 
   constexpr int per_sm = by_tmem < by_smem ? by_tmem : by_smem;
   static_assert(smem <= 227 * 1024, "shared memory per CTA exceeds the sm_103 limit");
   static_assert(per_sm >= 1, "configuration exceeds TMEM or shared memory");
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  static int max_clusters = 0;  // CL > 1: co-resident clusters of this configuration
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (attr_err == cudaSuccess && CL > 1) {
-      cudaLaunchConfig_t cfg = {};
-      cfg.gridDim = dim3(CL * sm_count());
-      cfg.blockDim = dim3(kGemmThreads);
-      cfg.dynamicSmemBytes = smem;
-      cudaLaunchAttribute attr[1];
-      attr[0].id = cudaLaunchAttributeClusterDimension;
-      attr[0].val.clusterDim.x = CL;
-      attr[0].val.clusterDim.y = 1;
-      attr[0].val.clusterDim.z = 1;
-      cfg.attrs = attr;
-      cfg.numAttrs = 1;
-      attr_err = cudaOccupancyMaxActiveClusters(&max_clusters, k, &cfg);
-      if (attr_err == cudaSuccess && max_clusters < 1) attr_err = cudaErrorInvalidConfiguration;
-    }
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<Clusters> setup;
+  const Clusters c = allow_clusters(setup, k, CL * sm_count(), kGemmThreads, smem, CL);
+  POETX_CUDA_TRY(c.err);
   const long long tiles = (long long)tiles_m * tiles_n * tiles_z;
   if (tiles == 0) return POETX_OK;
   if (tiles > 0x7fffffffLL) return POETX_ERR_SHAPE;
   p.tiles_m = tiles_m;
   p.tiles_n = tiles_n;
   p.num_tiles = (int)tiles;
-  const long long want = CL > 1 ? max_clusters : (long long)sm_count() * per_sm;
+  const long long want = CL > 1 ? c.resident : (long long)sm_count() * per_sm;
   const int grid = CL * (int)(tiles < want ? tiles : want);
   if (CL > 1)
     POETX_CUDA_TRY(launch_pdl_cluster(k, dim3(grid), dim3(kGemmThreads), smem, s, CL, ta, tb, tcm,
@@ -1590,16 +1571,8 @@ poetx_status umma_wprime_fused(const void* A, long long N, int m, int n, const v
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
   auto k = trans ? umma_fused_kernel<true, false> : umma_fused_kernel<false, true>;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(umma_fused_kernel<false, true>,
-                                    cudaFuncAttributeMaxDynamicSharedMemorySize, FZ_SMEM);
-    if (attr_err == cudaSuccess)
-      attr_err = cudaFuncSetAttribute(umma_fused_kernel<true, false>,
-                                      cudaFuncAttributeMaxDynamicSharedMemorySize, FZ_SMEM);
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<cudaError_t> attr[2];
+  POETX_CUDA_TRY(allow_smem(attr[trans ? 1 : 0], k, FZ_SMEM));
   const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
   POETX_CUDA_TRY(launch_pdl(k, dim3(grid), dim3(kGemmThreads), FZ_SMEM, s, ta, tw, tg, p));
   POETX_CUDA_TRY(cudaGetLastError());
@@ -1636,13 +1609,8 @@ poetx_status umma_wprime_i8(const void* A, long long N, int m, int n, const void
   p.trace = trace_buffer(&p.trace_cap);
   p.err = device_error_word();
   p.limit_ns = kWaitLimitNs;
-  static std::once_flag once;
-  static cudaError_t attr_err = cudaSuccess;
-  std::call_once(once, [&] {
-    attr_err = cudaFuncSetAttribute(umma_i8_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    I8_SMEM);
-  });
-  POETX_CUDA_TRY(attr_err);
+  static PerDevice<cudaError_t> attr;
+  POETX_CUDA_TRY(allow_smem(attr, umma_i8_kernel, I8_SMEM));
   const int grid = (int)(tiles < sm_count() ? tiles : sm_count());
   POETX_CUDA_TRY(launch_pdl(umma_i8_kernel, dim3(grid), dim3(I8_THREADS), I8_SMEM, s, tw, tx, p));
   POETX_CUDA_TRY(cudaGetLastError());
