@@ -1102,10 +1102,11 @@ extern "C" poetx_status poetx_glu_bwd(poetx_dtype dt, poetx_activation act, cons
 
 extern "C" size_t poetx_ffn_fwd_workspace_bytes(poetx_dtype dt, int N, int D, int F) {
   if (!shape_ok(dt, N, D, F) || dt != POETX_F32) return 0;
-  // (Few rows need none of W's pieces, and none of x's: but so an fp32 call without a workspace is refused at
-  // every N.)
-  if (N <= kRowsForward) return 3 * piece_step((size_t)(N > 0 ? N : 1) * D);
-  return 3 * (piece_step((size_t)(N > 0 ? N : 1) * D) + piece_step((size_t)2 * F * D));
+  // What the CUDA cores take needs none of W's pieces, and none of x's: but so an fp32 call without a workspace
+  // is refused at every N.  (Up to a megabyte W's are asked for from 33 rows on, whichever way the call goes.)
+  const size_t x_bytes = 3 * piece_step((size_t)(N > 0 ? N : 1) * D), w_bytes = 3 * piece_step((size_t)2 * F * D);
+  const bool rows = rows_forward_fits(N, D, F) && (N <= kRowsForward || w_bytes > (1u << 20));
+  return rows ? x_bytes : x_bytes + w_bytes;
 }
 
 extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, const void* x, int N, int D,
