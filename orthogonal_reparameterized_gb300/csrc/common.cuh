@@ -49,6 +49,14 @@ inline size_t dtype_size(poetx_dtype dt) {
 int current_device();
 int sm_count();
 
+// Blocks of `threads` for that many items, at most eight per SM.
+inline unsigned grid_for(long long items, int threads) {
+  long long b = (items + threads - 1) / threads;
+  const long long cap = (long long)sm_count() * 8;
+  if (b > cap) b = cap;
+  return (unsigned)(b < 1 ? 1 : b);
+}
+
 // Launch with programmatic dependent launch allowed: the kernel may start (and run its
 // prologue) while the previous kernel on the stream is finishing; every kernel of this
 // library calls pdl_wait() before it touches global memory, so results are unchanged.
@@ -185,6 +193,10 @@ __device__ __forceinline__ float bf16_to_f32(__nv_bfloat16 v) { return __bfloat1
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);  // round-to-nearest-even
   return *reinterpret_cast<uint32_t*>(&h);
+}
+__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
+  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
+                    pack_bf16x2(v[6], v[7]));
 }
 
 template <typename T>
@@ -520,6 +532,20 @@ __device__ __forceinline__ void mbar_arrive_cluster_tmem(uint32_t bar_cluster) {
   asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster)
                : "memory");
 }
+// Position in a ring of n buffers.  (Counted, not divided: the issuing threads have some 500 cycles
+// per K block, and 64-bit remainders by the stage count alone cost the head's products 8 %.)
+template <int n>
+struct Ring {
+  int s = 0;
+  uint32_t ph = 0;
+  __device__ __forceinline__ void next() {
+    if (++s == n) {
+      s = 0;
+      ph ^= 1;
+    }
+  }
+};
+
 // Every thread of every CTA of the cluster (release / acquire: shared-memory writes before it,
 // e.g. mbarrier initialisation, are visible to the other CTAs after it).
 __device__ __forceinline__ void cluster_sync() {

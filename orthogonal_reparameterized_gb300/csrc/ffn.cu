@@ -72,10 +72,6 @@ struct Eight<float> {
     v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
   }
 };
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
 __device__ __forceinline__ void put8(__nv_bfloat16* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) = pack8(v);
 }
@@ -235,18 +231,6 @@ struct FfnGemm {
   Act act;
   int* err;
   unsigned long long limit_ns;
-};
-
-template <int n>
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++s == n) {
-      s = 0;
-      ph ^= 1;
-    }
-  }
 };
 
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
@@ -819,13 +803,6 @@ __global__ void __launch_bounds__(score_threads(NT), 1)
 }
 
 // ---------------------------------------------------------------- host side
-unsigned grid_for(long long items, int threads) {
-  long long b = (items + threads - 1) / threads;
-  const long long cap = (long long)sm_count() * 8;
-  if (b > cap) b = cap;
-  return (unsigned)(b < 1 ? 1 : b);
-}
-
 // Launches an elementwise kernel over N rows of F elements (h, dh: rows of F), at most 2^31 - 1 vectors
 // at a time; rows that follow each other in every array count as one.
 struct GluCall {

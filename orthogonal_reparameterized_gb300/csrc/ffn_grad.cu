@@ -62,19 +62,6 @@ struct Args {
   unsigned long long limit_ns;
 };
 
-// Position in a ring of n buffers.
-template <int n>
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++s == n) {
-      s = 0;
-      ph ^= 1;
-    }
-  }
-};
-
 template <int NT>
 __global__ void __launch_bounds__(kThreads, 1)
     few_grad_kernel(const __grid_constant__ CUtensorMap mw, const __grid_constant__ CUtensorMap mz,

@@ -169,20 +169,6 @@ __device__ __forceinline__ Tile tile_of(const HeadGemm& p, int t) {
   return c;
 }
 
-// Position in a ring of n buffers.  (Counted, not divided: the issuing threads have some 500 cycles
-// per K block, and 64-bit remainders by the stage count alone cost the products 8 %.)
-template <int n>
-struct Ring {
-  int s = 0;
-  uint32_t ph = 0;
-  __device__ __forceinline__ void next() {
-    if (++s == n) {
-      s = 0;
-      ph ^= 1;
-    }
-  }
-};
-
 // Bounded wait that looks at the abort flag only where the barrier is not ready.
 __device__ __forceinline__ bool ring_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
                                           const HeadGemm& p, int site) {
@@ -1062,11 +1048,6 @@ __device__ __forceinline__ void block_reduce2(float& a, float& b, float2* red) {
   }
 }
 
-__device__ __forceinline__ uint4 pack8(const float (&v)[8]) {
-  return make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                    pack_bf16x2(v[6], v[7]));
-}
-
 // One CTA per row: joins the groups, writes loss and lse and turns e into dz.  Bound by HBM: a row of
 // e read and written (4096 x 32000: 524 MB in 85 us, 6.2 TB/s; 8192 x 128256: 0.64 ms, 6.6 TB/s).
 // Where there are few rows, several CTAs share one: each joins the groups again and turns its columns.
@@ -1360,13 +1341,6 @@ __global__ void __launch_bounds__(256)
 }
 
 // ---------------------------------------------------------------- host side
-unsigned grid_for(long long items, int threads) {
-  long long b = (items + threads - 1) / threads;
-  const long long cap = (long long)sm_count() * 8;
-  if (b > cap) b = cap;
-  return (unsigned)(b < 1 ? 1 : b);
-}
-
 template <int NT>
 poetx_status score(const CUtensorMap& mW, const CUtensorMap& mx, HeadScore p, cudaStream_t s) {
   auto k = head_score_kernel<NT>;
