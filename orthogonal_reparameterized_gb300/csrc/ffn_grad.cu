@@ -16,8 +16,8 @@
 // which the head's kernel for partial sums adds up.  A job has at most 4096 rows, after which the tensor
 // core's truncating adds are 1.5e-5 of the sum.
 //
-// 16 x 4096 x 14336: 470 MB in 81 us, dz before it and the sum of 9 partial sums included (5.8 TB/s); 64 rows
-// 91 us; 9 x 1024 x 2816 11.8 us (of which dz and the sum are 5).
+// 16 x 4096 x 14336: 470 MB in 82 us, dz before it and the sum of 9 partial sums included (5.7 TB/s); 64 rows
+// 92 us; 64 x 2048 x 5632 25.4 us.
 //
 // Every mbarrier wait is bounded; on expiry the kernel records POETX_ERR_TIMEOUT, waits for its own copies,
 // frees its TMEM and returns.

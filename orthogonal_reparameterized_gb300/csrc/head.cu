@@ -200,7 +200,7 @@ __device__ __forceinline__ float unit_share(float dloss, int target, int V) {
 // 32 (w % 4).. of the CTA's 128, columns 128 ((w - 4) / 4)..).
 //
 // Bound by the tensor pipe, and in a run of calls by the board's power.  4096 x 32000 x 2048: logits
-// 310-335 us (1.6-1.7 PFLOP/s, tensor pipe 78 % active), dx and dW 600-615 us (1.75-1.8, 86 %);
+// 307-335 us (1.6-1.75 PFLOP/s, tensor pipe 79 % active), dx and dW 592-615 us (1.75-1.81, 86 %);
 // 8192 x 128256 x 4096: 5.0-5.3 ms and 9.6-10.2 ms at 1.4-1.55 GHz.
 template <bool LSE, int SEGS>
 __global__ void __launch_bounds__(kGemmThreads, 1)
@@ -1422,9 +1422,9 @@ constexpr size_t kPieceBytes = (size_t)9 << 28;  // 2.25 GiB
 // Rows up to which dz is kept in two bf16 pieces: over few rows the gradients hang on a few large
 // p - q, whose rounding is not averaged (over many rows one piece stays below 1.45 times).  Error of dx
 // and dW against their own output's rounding, 1 to 128 rows: 1.15-1.54 times it with one piece, 1.0
-// with two.  The second piece costs next to nothing: dx's tile has the room for it, and of a dW of so
-// few rows its stores are the most (whole call, one piece and two: 120 and 126 us at 33 x 32000 x 2048,
-// 140 and 144 us at 128, 683 and 664 us at 33 x 128256 x 4096, 800 and 751 us at 128).
+// with two.  The second piece costs little: dx's tile has the room for it, and of a dW of so
+// few rows its stores are the most (whole call, one piece and two: 98 and 101 us at 33 x 32000 x 2048,
+// 117 and 129 us at 128, 550 and 560 us at 33 x 128256 x 4096, 629 and 683 us at 128).
 constexpr int kFineRows = kScoreRows;
 constexpr int kMaxFactors = 32768;  // groups of a row with gradients (4194304 columns of 128)
 constexpr long long kMaxRows = 1 << 16;  // of a piece (one warp looks through its upstream gradients)
