@@ -74,8 +74,9 @@ __device__ __forceinline__ float2 lost_by(float2 a, float2 b, float2 s) {
   return add2(add2(a, neg2(a0)), add2(b, neg2(b0)));
 }
 
-// A sum in two numbers: what rounding took from the first is in the second, so that its error (2^-45 or so)
-// does not grow with the terms.  (64-bit adds run at two a cycle on an SM.)
+// A sum in two numbers: what rounding took from the first is in the second.  What rounding takes from that is at
+// most n^2 2^-50 of the sum over n adds: 2^-27 for the 2800 of a thread's share of 2^33 elements.  (64-bit adds run
+// at two a cycle on an SM.)
 struct Sum2 {
   float2 top = {0.f, 0.f}, rest = {0.f, 0.f};
   __device__ __forceinline__ void add(float2 v) {
@@ -86,8 +87,8 @@ struct Sum2 {
 };
 
 // A thread's sum of squares.  The kUnroll vectors that it loads at a time give two fp32 sums of eight terms
-// at most, whose sum (off by 9 x 2^-24 at most) a Sum2 takes up: the error is the same for any number of
-// elements.  Where the largest of a vector would lose its square to fp32's range (above 2^50, or below 2^-50
+// at most, whose sum (off by 9 x 2^-24 at most) a Sum2 takes up, so that the error is the same for few elements and
+// for many.  Where the largest of a vector would lose its square to fp32's range (above 2^50, or below 2^-50
 // and not zero), that vector goes into a 64-bit sum.  The others beside a largest of 2^-50 or more are below
 // 2^-13 of it where their square leaves the normal range.
 constexpr int kUnroll = 4;
