@@ -281,9 +281,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         fence_async_shared();
         __syncwarp();
         if (staged_not_finite(stg, kBoxBytes, lane)) {
-          if (row < p.V)
-            first_piece_again(stg, kBoxBytes, lane, p.z + row, p.pitch, p.x, p.N, p.D, col, 1.f,
-                              p.old ? p.old + (long long)row * p.D : nullptr);
+          first_piece_again(stg, kBoxBytes, lane, row < p.V, p.z + row, p.pitch, p.x, p.N, p.D, col, 1.f,
+                            p.old ? p.old + (long long)row * p.D : nullptr);
           fence_async_shared();
           __syncwarp();
         }

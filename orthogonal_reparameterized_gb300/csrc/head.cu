@@ -585,9 +585,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1)
           }
           if (bad) {
             __syncwarp();
-            if (row < d.M)
-              first_piece_again(stg, kStgBytes, lane, p.z + row, p.z_pitch, p.x, p.rows, d.N, col0, out_scale,
-                                d.add_bf16 ? d.add_bf16 + (long long)row * d.N : nullptr);
+            first_piece_again(stg, kStgBytes, lane, row < d.M, p.z + row, p.z_pitch, p.x, p.rows, d.N, col0,
+                              out_scale, d.add_bf16 ? d.add_bf16 + (long long)row * d.N : nullptr);
             fence_async_shared();
             __syncwarp();
             send();

@@ -21,24 +21,41 @@ __device__ __forceinline__ bool staged_not_finite(const uint8_t* stg, int box, i
   const uint32_t top = __vmaxs2(w.x & 0x7fff7fffu, w.y & 0x7fff7fffu);
   return __any_sync(0xffffffffu, (top & 0xffffu) >= 0x7f80u || top >> 16 >= 0x7f80u);
 }
-// Then each lane goes through its row of the boxes, columns from col on of D: what is NaN becomes scale * the sum
-// over the tokens of the first piece of dz (z + n pitch) by x (+ old), which ends at a NaN of its own.
-__device__ __forceinline__ void first_piece_again(uint8_t* stg, int box, int lane, const __nv_bfloat16* z,
-                                                  long long pitch, const __nv_bfloat16* x, int N, int D,
-                                                  int col, float scale, const __nv_bfloat16* old) {
+// Then the warp looks for infinities in those columns of x, `col` on of D, eight at a time (dz's own infinities and
+// NaN are in dW already: a step that has blown up must not end in this).  In a column with one, each lane
+// (`mine`: its row is dW's) takes its result, and where that is NaN puts scale * the sum over the tokens of the
+// first piece of dz (z + n pitch) by x (+ old) in its place.
+__device__ __forceinline__ void first_piece_again(uint8_t* stg, int box, int lane, bool mine,
+                                                  const __nv_bfloat16* z, long long pitch,
+                                                  const __nv_bfloat16* x, int N, int D, int col, float scale,
+                                                  const __nv_bfloat16* old) {
 #pragma unroll 1
-  for (int c = 0; c < 128 && col + c < D; ++c) {
-    __nv_bfloat16* const at =
-        reinterpret_cast<__nv_bfloat16*>(stg + c / 64 * box + lane * 128 + (((c % 64 / 8) ^ (lane & 7)) << 4)) +
-        c % 8;
-    if (!isnan(__bfloat162float(*at))) continue;
-    float s = 0.f;
+  for (int c8 = 0; c8 < 128 && col + c8 < D; c8 += 8) {
+    uint32_t inf = 0;
 #pragma unroll 1
-    for (int n = 0; n < N && !isnan(s); ++n)
-      s = fmaf(__bfloat162float(z[n * pitch]), __bfloat162float(x[(long long)n * D + col + c]), s);
-    s *= scale;
-    if (old) s += __bfloat162float(old[col + c]);
-    *at = __float2bfloat16_rn(s);
+    for (int n = lane; n < N; n += 32) {
+      const uint4 w = *reinterpret_cast<const uint4*>(x + (long long)n * D + col + c8);
+      const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        inf |= ((u[i] & 0x7fffu) == 0x7f80u ? 1u : 0u) << (2 * i) |
+               ((u[i] & 0x7fff0000u) == 0x7f800000u ? 2u : 0u) << (2 * i);
+    }
+#pragma unroll 1
+    for (inf = __reduce_or_sync(0xffffffffu, inf); inf; inf &= inf - 1) {
+      const int c = c8 + __ffs(inf) - 1;
+      __nv_bfloat16* const at =
+          reinterpret_cast<__nv_bfloat16*>(stg + c / 64 * box + lane * 128 + (((c % 64 / 8) ^ (lane & 7)) << 4)) +
+          c % 8;
+      if (!mine || !isnan(__bfloat162float(*at))) continue;
+      float s = 0.f;
+#pragma unroll 8
+      for (int n = 0; n < N; ++n)
+        s = fmaf(__bfloat162float(z[n * pitch]), __bfloat162float(x[(long long)n * D + col + c]), s);
+      s *= scale;
+      if (old) s += __bfloat162float(old[col + c]);
+      *at = __float2bfloat16_rn(s);
+    }
   }
 }
 
