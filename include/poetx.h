@@ -565,7 +565,7 @@ poetx_status poetx_glu_bwd(poetx_dtype dt, poetx_activation act, const void* g, 
  *           8 <= D <= 131072, 8 <= F <= 2097152, N >= 0 (POETX_ERR_SHAPE otherwise)
  *   z       [N, 2 F] output (nullable): the projections, for the backward
  *   ws      scratch of poetx_ffn_fwd_workspace_bytes(dt, N, D, F) bytes (bf16: 0, ws may be NULL)
- * Outputs must not alias inputs. */
+ * Outputs must not overlap inputs or each other (POETX_ERR_ARG where two are the same array). */
 size_t poetx_ffn_fwd_workspace_bytes(poetx_dtype dt, int N, int D, int F);
 poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, const void* x, int N, int D,
                            const void* W, int F, void* h, void* z, void* ws, size_t ws_bytes,
@@ -578,7 +578,8 @@ poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, const void* x, 
  *   ws      scratch of poetx_ffn_bwd_workspace_bytes(dt, N, D, F, z != NULL, dx != NULL, dW != NULL)
  * bf16: dz is rounded to bf16 for the products, to two bf16 pieces where N <= 128: dx and dW are 1.4 times as far
  * from their exact values as their own rounding alone, 1.0 times up to 128 rows.  fp32: about fp32 accuracy
- * throughout. */
+ * throughout.  dx and dW must not overlap x, W or each other (POETX_ERR_ARG where two are the same array; dx alone
+ * may be x's array). */
 size_t poetx_ffn_bwd_workspace_bytes(poetx_dtype dt, int N, int D, int F, int have_z, int want_dx,
                                      int want_dW);
 poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, const void* x, int N, int D,

@@ -1103,6 +1103,7 @@ extern "C" poetx_status poetx_ffn_fwd(poetx_dtype dt, poetx_activation act, cons
   const size_t need = poetx_ffn_fwd_workspace_bytes(dt, N, D, F);
   if (!x || !W || !h || (need && !ws)) return POETX_ERR_ARG;
   if (ws_bytes < need) return POETX_ERR_WORKSPACE;
+  if (h == x || h == W || h == z || (z && (z == x || z == W))) return POETX_ERR_ARG;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
   if (dt == POETX_F32 && rows_forward_fits(N, D, F))
     return rows_forward({true, x, W, N, D, F, h, z, nullptr, nullptr, 2ll * F}, act_of(act), stream);
@@ -1141,6 +1142,7 @@ extern "C" poetx_status poetx_ffn_bwd(poetx_dtype dt, poetx_activation act, cons
   if (!x || !W || !dh || !ws) return POETX_ERR_ARG;
   const Plan pl = plan(dt, N, D, F, z != nullptr, dx != nullptr);
   if (ws_bytes < pl.bytes) return POETX_ERR_WORKSPACE;
+  if ((dW && (dW == x || dW == W || dW == dx || dx == x)) || dx == W) return POETX_ERR_ARG;
   if (!umma_supported()) return POETX_ERR_UNSUPPORTED;
   uint8_t* w = static_cast<uint8_t*>(ws);
   const uint8_t *xp = static_cast<const uint8_t*>(x), *wp = static_cast<const uint8_t*>(W);
