@@ -134,9 +134,15 @@ def test_added_dW(P, N, D, F, dt):
     assert (np.abs(got["dW"] - (dW + base)) <= r * np.abs(dW + base) + 2.0 ** -22 * np.abs(base) + off * dW_off).all()
 
 
-def _needs(gigabytes):
-    if torch.cuda.mem_get_info()[0] < gigabytes << 30:
-        pytest.skip(f"needs {gigabytes} GB")
+@pytest.fixture
+def room():
+    """Skips a test that the GPU has too little memory for; gives back afterwards what it took."""
+    def needs(gigabytes):
+        torch.cuda.empty_cache()
+        if torch.cuda.mem_get_info()[0] < gigabytes << 30:
+            pytest.skip(f"needs {gigabytes} GB")
+    yield needs
+    torch.cuda.empty_cache()
 
 
 def _rows_of(N, some):
@@ -147,12 +153,12 @@ def _rows_of(N, some):
 
 
 @pytest.mark.parametrize("halves", [True, False], ids=["halves", "two_launches"])
-def test_glu_beyond_32_bits(P, halves):
+def test_glu_beyond_32_bits(P, room, halves):
     """More than 2^31 elements with rows apart from each other; more than 2^31 vectors, which take two launches
     (8191 rows in the first)."""
     F = 1 << 21
     N, some = (600, [0, 300, 511, 512, 599]) if halves else (8250, [0, 1023, 1024, 4096, 8190, 8191, 8192, 8249])
-    _needs(20 if halves else 115)
+    room(20 if halves else 115)
     g = torch.Generator(device=DEV).manual_seed(2)
     if halves:
         z = torch.zeros(N, 2 * F, dtype=BF, device=DEV)
@@ -191,10 +197,10 @@ def test_glu_beyond_32_bits(P, halves):
     same(up, want[2])
 
 
-def test_ffn_with_projections_beyond_32_bits(P):
+def test_ffn_with_projections_beyond_32_bits(P, room):
     """z and dz of more than 2^31 elements, through the products of many rows."""
     N, D, F = 600, 8, 1 << 21
-    _needs(40)
+    room(40)
     g = torch.Generator(device=DEV).manual_seed(3)
     x = torch.randn(N, D, generator=g, device=DEV).to(BF)
     W = (torch.randn(2 * F, D, generator=g, device=DEV) / 3).to(BF)
